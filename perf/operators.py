@@ -1,0 +1,410 @@
+"""Timing cases of the 4-bit key/value cache: writing new tokens and reading them back, reading a
+long cache, and attention over it, for prompts and for single tokens.
+
+Each case is a dict of plain values.  ``run`` with ``own`` false computes it with elementary torch
+operations in 32 bits, with ``own`` true through the package's entry points ``kv_write``,
+``kv_read`` and ``kv_attend``.
+
+A batch is described as a serving loop holds it: ``table[b]`` lists the 64-token pages of sequence
+b, ``length[b]`` counts its tokens, and its newest tokens are the rows ``start[b] .. start[b+1]`` of
+the packed inputs.  The cache holds, per (page, kv head), 72 * dim bytes:
+
+    K codes   64 tokens x dim/2 bytes     16 bytes per group of 32 values
+    K scales  64 x dim/32 f16             [token][group]
+    V codes   32 token pairs x dim bytes  16 bytes per 16 values of two tokens
+    V scales  dim/32 x 64 f16             [group][token]
+
+with value = scale * (code - 8), scale of 7 significant bits.
+"""
+import torch
+
+own = False
+
+PAGE = 64
+DTYPES = {"f32": torch.float32, "f16": torch.float16, "bf16": torch.bfloat16}
+
+
+# ------------------------------------------------------------------------------------------- cases
+def _write(name, dtype, batch, new, length, kv_heads, dim):
+    """new and length are (shortest, longest) over the sequences of the batch."""
+    return {"name": name, "op": "write", "dtype": dtype, "batch": batch, "new_lo": new[0], "new_hi": new[1],
+            "len_lo": length[0], "len_hi": length[1], "kv_heads": kv_heads, "dim": dim}
+
+
+def _read(name, dtype, batch, length, kv_heads, dim):
+    return {"name": name, "op": "read", "dtype": dtype, "batch": batch, "new_lo": length[0], "new_hi": length[1],
+            "len_lo": length[0], "len_hi": length[1], "kv_heads": kv_heads, "dim": dim}
+
+
+def _attend(name, dtype, batch, new, length, heads, kv_heads, dim, window=0, sinks=0):
+    return {"name": name, "op": "attend", "dtype": dtype, "batch": batch, "new_lo": new[0], "new_hi": new[1],
+            "len_lo": length[0], "len_hi": length[1], "heads": heads, "kv_heads": kv_heads, "dim": dim,
+            "window": window, "sinks": sinks}
+
+
+def listed():
+    return [
+        # one decoding step of a small batch: the K and V rows of 8 sequences enter the cache
+        _write("write_step", "f32", 8, (1, 1), (130, 3314), 8, 128),
+        # a prompt of the 7B shape (32 heads of 128, 3314 tokens) enters the cache
+        _write("write_prompt", "f32", 1, (3314, 3314), (3314, 3314), 32, 128),
+        # a short cached prefix handed on in 16 bits, small heads
+        _read("read_prefix", "f16", 1, (517, 517), 8, 64),
+        # a long cache read back whole
+        _read("read_long", "bf16", 2, (40001, 65536), 8, 128),
+        # a single token of one short conversation, 7B shape: latency
+        _attend("step_short", "f32", 1, (1, 1), (203, 203), 32, 32, 128),
+        # a single token over one long document: few rows, a long axis
+        _attend("step_long", "f32", 1, (1, 1), (131071, 131071), 32, 8, 128),
+        # a decoding step of a ragged batch with shared heads
+        _attend("step_batch", "bf16", 64, (1, 1), (95, 8192), 32, 8, 128),
+        # a few drafted tokens per sequence checked at once, window and first tokens visible
+        _attend("step_draft", "f16", 12, (3, 6), (1000, 30000), 32, 4, 128, 4096, 4),
+        # the prompt of the 7B shape, in the 32 bits that the linear layers give
+        _attend("prompt", "f32", 1, (3314, 3314), (3314, 3314), 32, 32, 128),
+        # prompts' next chunks on top of what the cache holds
+        _attend("prompt_chunk", "bf16", 2, (1777, 2048), (9001, 16384), 32, 8, 128),
+        # a long prompt with a window and first tokens that stay visible, small heads
+        _attend("prompt_window", "f16", 1, (8191, 8191), (8191, 8191), 16, 2, 64, 1024, 4),
+        # many short prompts in one batch
+        _attend("prompt_ragged", "f16", 16, (5, 700), (5, 900), 16, 4, 128),
+    ]
+
+
+def _log(rng, lo, hi):
+    return int(round(lo * (hi / lo) ** rng.random()))
+
+
+def draw(rng):
+    kind = rng.choice(["write", "read", "step", "step", "prompt", "prompt"])
+    dim = rng.choice([64, 128, 128])
+    kv_heads = rng.choice([1, 2, 4, 8, 8, 16, 32])
+    dtype = rng.choice(sorted(DTYPES))
+    if kind in ("write", "read"):
+        batch = _log(rng, 1, 64)
+        top = max(1, 131072 * 4 // (kv_heads * batch) * 128 // dim)
+        if kind == "write":
+            new = _log(rng, 1, min(top // 2 + 1, 4096))
+            more = _log(rng, 1, min(top, 8192))
+            case = _write("", dtype, batch, (max(1, new // 2), new), (new, new + more), kv_heads, dim)
+        else:
+            length = _log(rng, 1, min(top, 131072))
+            case = _read("", dtype, batch, (max(1, length // 3), length), kv_heads, dim)
+    else:
+        group = rng.choice([g for g in (1, 2, 3, 4, 5, 8, 16) if g * kv_heads <= 64])
+        heads = group * kv_heads
+        batch = _log(rng, 1, 64) if kind == "step" else _log(rng, 1, 8)
+        window = rng.choice([0, 0, _log(rng, 16, 4096)])
+        sinks = rng.choice([0, 1, 4, 65]) if window else 0
+        if kind == "step":
+            new = rng.choice([1, 1, 1, 2, 4, 7])
+            top = min(131072, 131072 * 8 * 128 // (kv_heads * batch * dim), (1 << 29) // (heads * batch * new))
+            length = new + _log(rng, 1, max(2, top))
+        else:
+            length = _log(rng, 33, 16384)
+            room = 3 * (1 << 29) // (heads * batch * length)
+            new = max(1, min(length, room, _log(rng, 17, 4096)))
+        case = _attend("", dtype, batch, (max(1, new // 2), new), (max(new, length // 3), length), heads, kv_heads,
+                       dim, window, sinks)
+    del case["name"]
+    return case
+
+
+def _spread(lo, hi, n):
+    """n whole numbers from lo to hi, uneven, the longest first."""
+    return [hi] + [lo + int((hi - lo) * ((i * 0.6180339887) % 1.0)) for i in range(1, n)]
+
+
+def _batch(case):
+    """(new tokens, length) of each sequence."""
+    new = _spread(case["new_lo"], case["new_hi"], case["batch"])
+    length = _spread(case["len_lo"], case["len_hi"], case["batch"])
+    if case["op"] == "read":
+        return length, length
+    return new, [max(n, m) for n, m in zip(new, length)]
+
+
+def _visible(p, window, sinks):
+    """Keys that a query at position p sees."""
+    return p + 1 if window == 0 else min(p + 1, window + max(0, min(sinks, p + 1 - window)))
+
+
+def work(case):
+    new, length = _batch(case)
+    values = 2 * case["kv_heads"] * case["dim"]
+    wide = 4 if case["dtype"] == "f32" else 2
+    if case["op"] == "write":       # rows in, 4.5 bits a value out and in again, values out
+        n = sum(new) * values
+        return {"bytes": n * (2 * wide + 2 * 0.5625), "flops": 6 * n}
+    if case["op"] == "read":
+        n = sum(length) * values
+        return {"bytes": n * (0.5625 + wide), "flops": 2 * n}
+    pairs = keys = 0
+    for n, m in zip(new, length):
+        first = m - n
+        pairs += sum(_visible(p, case["window"], case["sinks"]) for p in range(first, m))
+        seen = m if case["window"] == 0 else min(m, case["window"] + n - 1 + min(case["sinks"], m))
+        keys += min(m, seen)
+    rows = sum(new) * case["heads"] * case["dim"]
+    return {"bytes": 2 * rows * wide + keys * values * 0.5625, "flops": 4 * case["dim"] * case["heads"] * pairs}
+
+
+# ------------------------------------------------------------------------------------- plain form
+def _maps(dim, device):
+    """Byte and shift of the code, and byte of the scale, of each (token, value) of a piece."""
+    t = torch.arange(PAGE, device=device)[:, None]
+    d = torch.arange(dim, device=device)[None, :]
+    ng, g, r = dim // 32, d // 32, d % 32
+    place = g ^ ((t >> (1 if dim == 128 else 2)) & (ng - 1))
+    maps = {"k_byte": t * (dim // 2) + place * 16 + (r // 8) * 4 + (r % 2) * 2 + (r % 8) // 4,
+            "k_shift": 4 * (((r % 8) // 2) % 2) + 0 * t,
+            "k_scale": 32 * dim + (t * ng + g) * 2}
+    pair, block = t // 2, d // 16
+    place = block ^ ((pair >> 2) & (dim // 16 - 1))
+    maps["v_byte"] = 36 * dim + pair * dim + place * 16 + (d % 16) // 4 * 4 + (t % 2) * 2 + (d % 4) // 2
+    maps["v_shift"] = 4 * (d % 2) + 0 * t
+    maps["v_scale"] = 68 * dim + (g * PAGE + t) * 2
+    for x in ("k", "v"):    # the values of each byte, low one first, and the bytes
+        maps[x + "_order"] = torch.argsort(maps[x + "_byte"] * 8 + maps[x + "_shift"], dim=-1)
+        maps[x + "_bytes"] = maps[x + "_byte"].gather(-1, maps[x + "_order"])[:, ::2]
+    return maps
+
+
+def _quantise(x):
+    """f32 [..., dim] -> codes 0..15 and scales [..., dim/32]."""
+    x = x.float()
+    g = x.reshape(*x.shape[:-1], x.shape[-1] // 32, 32)
+    amax = g.abs().amax(-1)
+    s = amax / torch.full_like(amax, 7.5)
+    s = ((s.view(torch.int32) + 0x1FFFF) & ~0x1FFFF).view(torch.float32).clamp(2.0 ** -14, 896.0)
+    c = (g / s[..., None]).round().clamp(-8, 7) + 8
+    return c.to(torch.uint8).reshape(x.shape), s.half()
+
+
+def _store(pages, page, slot, k, v, maps):
+    """Rows k, v [n, kv heads, dim] into slot[n] of page[n]."""
+    n, heads, dim = k.shape
+    h = torch.arange(heads, device=k.device)[None, :, None]
+    for x, name in ((k, "k"), (v, "v")):
+        codes, scales = _quantise(x)
+        order = maps[name + "_order"][slot][:, None].expand(n, heads, dim)
+        both = codes.gather(-1, order).reshape(n, heads, dim // 2, 2)
+        where = maps[name + "_bytes"][slot][:, None]
+        pages[page[:, None, None], h, where] = both[..., 0] | (both[..., 1] << 4)
+        at = maps[name + "_scale"][slot][:, ::32]
+        raw = scales.contiguous().view(torch.uint8).reshape(n, heads, dim // 32, 2)
+        pages[page[:, None, None], h, at[:, None, :]] = raw[..., 0]
+        pages[page[:, None, None], h, at[:, None, :] + 1] = raw[..., 1]
+
+
+def _load(pieces, name, maps):
+    """uint8 pieces [..., 72 * dim] -> f32 values [..., 64, dim]."""
+    by, sh, at = maps[name + "_byte"], maps[name + "_shift"].to(torch.uint8), maps[name + "_scale"]
+    codes = ((pieces[..., by] >> sh) & 15).float() - 8.0
+    scales = pieces.view(torch.float16)[..., at[:, ::32] // 2].float()
+    return codes * scales.repeat_interleave(32, -1)
+
+
+def _places(s):
+    """(sequence, position, page, slot) of each packed row."""
+    row = torch.arange(s["rows"], device=s["start"].device, dtype=torch.int32)
+    b = torch.searchsorted(s["start"][1:], row, right=True)
+    pos = (s["length"][b] - s["start"][b + 1] + row).long()
+    return b, pos, s["table"][b, pos // PAGE].long(), pos % PAGE
+
+
+def _plain_write(s):
+    _, _, page, slot = _places(s)
+    _store(s["pages"], page, slot, s["k"], s["v"], s["maps"])
+    return _plain_read(s)
+
+
+def _plain_read(s):
+    b, pos, page, slot = _places(s)
+    maps, out = s["maps"], []
+    h = torch.arange(s["kv_heads"], device=page.device)[None, :, None]
+    for name in ("k", "v"):
+        by, sh = maps[name + "_byte"][slot][:, None], maps[name + "_shift"][slot][:, None].to(torch.uint8)
+        at = maps[name + "_scale"][slot][:, None, ::32]
+        p = page[:, None, None]
+        codes = ((s["pages"][p, h, by] >> sh) & 15).float() - 8.0
+        scales = s["pages"].view(torch.float16)[p, h, at // 2].float()
+        out.append((codes * scales.repeat_interleave(32, -1)).to(s["out_dtype"]))
+    return out
+
+
+def _plain_attend(s):
+    q, hk, dim = s["q"], s["kv_heads"], s["dim"]
+    n, heads = q.shape[:2]
+    batch, group, dev = s["table"].shape[0], heads // hk, q.device
+    # the whole cache of the batch in 32 bits: [batch, kv heads, keys, dim]
+    pieces = s["pages"][s["table"].clamp(min=0).long()].transpose(1, 2)
+    keys = s["table"].shape[1] * PAGE
+    j = torch.arange(keys, device=dev)
+    held = (j[None] < s["length"][:, None])[:, None, :, None]
+    k, v = (torch.where(held, _load(pieces, x, s["maps"]).reshape(batch, hk, keys, dim), 0.0) for x in ("k", "v"))
+    # the rows of the batch, padded to the longest: [batch, kv heads, rows * group, dim]
+    b, pos, _, _ = _places(s)
+    i = torch.arange(n, device=dev) - s["start"][b]
+    rows = s["max_q"]
+    wide = torch.zeros(batch, rows, hk, group, dim, device=dev)
+    wide[b, i] = q.reshape(n, hk, group, dim).float()
+    at = torch.full((batch, rows), -1, device=dev, dtype=torch.long)
+    at[b, i] = pos
+    wide = wide.permute(0, 2, 1, 3, 4).reshape(batch, hk, rows * group, dim)
+    x = wide @ k.transpose(-1, -2)
+    x *= s["scale"]
+    seen = j[None, None] <= at[..., None]
+    if s["window"]:
+        seen &= (j[None, None] > at[..., None] - s["window"]) | (j < s["sinks"])
+    seen = seen[:, None, :, None]
+    x = x.reshape(batch, hk, rows, group, keys).masked_fill_(~seen, float("-inf"))
+    m = x.amax(-1, keepdim=True).clamp(min=-3e38)
+    p = x.sub_(m).exp_()
+    total = p.sum(-1, keepdim=True)
+    o = p.reshape(batch, hk, rows * group, keys) @ v
+    o = o.reshape(batch, hk, rows, group, dim) / total.clamp(min=1e-30)
+    return o.permute(0, 2, 1, 3, 4).reshape(batch, rows, heads, dim)[b, i].to(q.dtype)
+
+
+# ------------------------------------------------------------------------------------------ state
+def prepare(case, seed):
+    dev = "cuda"
+    gen = torch.Generator(dev).manual_seed(seed)
+    new, length = _batch(case)
+    batch, hk, dim = case["batch"], case["kv_heads"], case["dim"]
+    dtype = DTYPES[case["dtype"]]
+    maps = _maps(dim, dev)
+    need = [-(-m // PAGE) for m in length]
+    most = max(need)
+    num = sum(need) + 3
+    # pages in no order; entries past a sequence's last page are no pages
+    perm = torch.randperm(num, device=dev, generator=gen).to(torch.int32)
+    first = torch.tensor([0] + need, device=dev).cumsum(0)
+    col = torch.arange(most, device=dev)
+    used = col[None] < torch.tensor(need, device=dev)[:, None]
+    table = torch.where(used, perm[(first[:-1, None] + col[None]).clamp(max=num - 1)], -1).contiguous()
+    start = torch.tensor([0] + new, device=dev).cumsum(0).to(torch.int32)
+    rows = sum(new)
+    s = {"op": case["op"], "maps": maps, "table": table, "start": start, "rows": rows, "kv_heads": hk, "dim": dim,
+         "length": torch.tensor(length, device=dev, dtype=torch.int32), "max_q": max(new), "max_kv": max(length)}
+    # slots that no token has been written to hold whatever the memory held
+    pages = torch.randint(0, 256, (num, hk, 72 * dim), device=dev, dtype=torch.uint8, generator=gen)
+    # keys have a few strong channels, values a few strong tokens
+    loud = 1.0 + 4.0 * (torch.rand(hk, dim, device=dev, generator=gen) < 0.05)
+
+    def kv(n):
+        k = torch.randn(n, hk, dim, device=dev, generator=gen)
+        k *= loud
+        v = torch.randn(n, hk, dim, device=dev, generator=gen)
+        v *= torch.rand(n, 1, 1, device=dev, generator=gen) + 0.5
+        return k, v
+
+    if case["op"] == "write":
+        s["k"], s["v"] = (x.to(dtype) for x in kv(rows))
+        s["out_dtype"] = torch.float32 if case["dtype"] == "f32" else torch.float16
+    else:
+        # every token of every sequence, a page of each sequence at a time
+        tail = torch.tensor(length, device=dev)
+        seq = torch.repeat_interleave(torch.arange(batch, device=dev), tail)
+        pos = torch.arange(sum(length), device=dev) - torch.repeat_interleave(tail.cumsum(0) - tail, tail)
+        for lo in range(0, sum(length), 1 << 16):
+            b, p = seq[lo:lo + (1 << 16)], pos[lo:lo + (1 << 16)]
+            k, v = kv(b.numel())
+            _store(pages, table[b, p // PAGE].long(), p % PAGE, k, v, maps)
+        s["out_dtype"] = dtype
+    s["pages"] = pages
+    if case["op"] == "attend":
+        heads = case["heads"]
+        s["q"] = (1.5 * torch.randn(rows, heads, dim, device=dev, generator=gen)).to(dtype)
+        s["scale"] = dim ** -0.5
+        s["window"], s["sinks"] = case["window"], case["sinks"]
+    return s
+
+
+def run(s):
+    if not own:
+        return {"write": _plain_write, "read": _plain_read, "attend": _plain_attend}[s["op"]](s)
+    import quant_int8_mmq_gb300 as mmq
+    cache = (s["pages"], s["table"], s["start"], s["length"])
+    if s["op"] == "attend":
+        return mmq.kv_attend(s["q"], *cache, max_q=s["max_q"], max_kv=s["max_kv"], scale=s["scale"],
+                             window=s["window"], sinks=s["sinks"])
+    if s["op"] == "write":
+        mmq.kv_write(s["k"], s["v"], *cache)
+    return list(mmq.kv_read(*cache, s["rows"], dtype=s["out_dtype"]))
+
+
+# ------------------------------------------------------------------------------- the definition, 64 bits
+def _values64(x):
+    """What the cache holds for f64 rows: groups of 32, 4-bit codes, a scale of 7 significant bits."""
+    g = x.unflatten(-1, (-1, 32))
+    t = (g.abs().amax(-1, keepdim=True) / 7.5).clamp(min=2.0 ** -14)
+    # the unit in the seventh significant place: t's power of two, 6 places down
+    unit = (((t.view(torch.int64) >> 52) - 6) << 52).view(torch.float64)
+    s = (torch.ceil(t / unit) * unit).clamp(2.0 ** -14, 896.0)
+    return (s * torch.clamp(torch.round(g / s), -8, 7)).flatten(-2)
+
+
+def _decode64(piece, dim):
+    """Pieces [n, kv heads, 72 * dim] -> K and V [kv heads, n * 64, dim] in 64 bits, value by value."""
+    piece = piece.transpose(0, 1).contiguous()
+    n = piece.shape[:2]
+    ng = dim // 32
+    words = piece.view(torch.int32)
+    k = torch.empty(*n, PAGE, dim, dtype=torch.float64, device=piece.device)
+    v = torch.empty_like(k)
+    half = piece.view(torch.float16).double()
+    for t in range(PAGE):
+        for g in range(ng):
+            at = t * (dim // 8) + (g ^ ((t >> (1 if dim == 128 else 2)) & (ng - 1))) * 4
+            for u in range(4):
+                for p in range(4):
+                    for h in range(2):
+                        code = (words[..., at + u] >> (4 * p + 16 * h)) & 15
+                        k[..., t, 32 * g + 8 * u + 2 * p + h] = (code - 8) * half[..., 16 * dim + t * ng + g]
+        for block in range(dim // 16):
+            at = 9 * dim + (t // 2) * (dim // 4) + (block ^ ((t // 8) & (dim // 16 - 1))) * 4
+            for d in range(16):
+                code = (words[..., at + d // 4] >> (4 * (d % 4) + 16 * (t % 2))) & 15
+                v[..., t, 16 * block + d] = (code - 8) * half[..., 34 * dim + (block // 2) * PAGE + t]
+    return k.flatten(1, 2), v.flatten(1, 2)
+
+
+def exact(case, seed):
+    s = prepare(case, seed)
+    if case["op"] == "write":
+        return [_values64(s["k"].double()), _values64(s["v"].double())]
+    table, length, start = s["table"].cpu(), s["length"].tolist(), s["start"].tolist()
+    hk, dim = s["kv_heads"], s["dim"]
+    if case["op"] == "read":
+        out = [torch.empty(s["rows"], hk, dim, dtype=torch.float64, device="cuda") for _ in range(2)]
+    else:
+        out = torch.zeros(s["q"].shape, dtype=torch.float64, device="cuda")
+    # the pages of all sequences, one after another
+    pages = [table[b, :-(-m // PAGE)].long() for b, m in enumerate(length)]
+    k, v = _decode64(s["pages"][torch.cat(pages).cuda()], dim)
+    for h in range(hk):
+        lo = 0
+        for b, m in enumerate(length):
+            kb, vb = k[h, lo:lo + m], v[h, lo:lo + m]
+            lo += pages[b].numel() * PAGE
+            rows = slice(start[b], start[b + 1])
+            if case["op"] == "read":
+                out[0][rows, h], out[1][rows, h] = kb, vb
+                continue
+            group = case["heads"] // hk
+            n = start[b + 1] - start[b]
+            for i in range(0, n, 1024):
+                c = min(1024, n - i)
+                rows = slice(start[b] + i, start[b] + i + c)
+                q = s["q"][rows, h * group:(h + 1) * group].double()
+                x = torch.einsum("igd,jd->igj", q, kb) * s["scale"]
+                p = torch.arange(m - n + i, m - n + i + c, device="cuda")[:, None]
+                j = torch.arange(m, device="cuda")[None]
+                ok = j <= p
+                if s["window"]:
+                    ok &= (p - j < s["window"]) | (j < s["sinks"])
+                w = torch.softmax(torch.where(ok[:, None], x, float("-inf")), -1)
+                out[rows, h * group:(h + 1) * group] = torch.einsum("igj,jd->igd", w, vb)
+    return out
