@@ -12,7 +12,7 @@ the packed inputs.  The cache holds, per (page, kv head), 72 * dim bytes:
     K codes   64 tokens x dim/2 bytes     16 bytes per group of 32 values
     K scales  64 x dim/32 f16             [token][group]
     V codes   32 token pairs x dim bytes  16 bytes per 16 values of two tokens
-    V scales  dim/32 x 64 f16             [group][token]
+    V scales  32 x dim/32 x 2 f16         [token pair][group][token]
 
 with value = scale * (code - 8), scale of 7 significant bits.
 """
@@ -160,10 +160,10 @@ def _maps(dim, device):
             "k_shift": 4 * (((r % 8) // 2) % 2) + 0 * t,
             "k_scale": 32 * dim + (t * ng + g) * 2}
     pair, block = t // 2, d // 16
-    place = block ^ ((pair >> 2) & (dim // 16 - 1))
+    place = block ^ (((pair >> 2) ^ (pair << 1 & 6 if dim == 128 else pair & 2)) & (dim // 16 - 1))
     maps["v_byte"] = 36 * dim + pair * dim + place * 16 + (d % 16) // 4 * 4 + (t % 2) * 2 + (d % 4) // 2
     maps["v_shift"] = 4 * (d % 2) + 0 * t
-    maps["v_scale"] = 68 * dim + (g * PAGE + t) * 2
+    maps["v_scale"] = 68 * dim + ((pair * ng + g) * 2 + t % 2) * 2
     for x in ("k", "v"):    # the values of each byte, low one first, and the bytes
         maps[x + "_order"] = torch.argsort(maps[x + "_byte"] * 8 + maps[x + "_shift"], dim=-1)
         maps[x + "_bytes"] = maps[x + "_byte"].gather(-1, maps[x + "_order"])[:, ::2]
@@ -364,10 +364,11 @@ def _decode64(piece, dim):
                         code = (words[..., at + u] >> (4 * p + 16 * h)) & 15
                         k[..., t, 32 * g + 8 * u + 2 * p + h] = (code - 8) * half[..., 16 * dim + t * ng + g]
         for block in range(dim // 16):
-            at = 9 * dim + (t // 2) * (dim // 4) + (block ^ ((t // 8) & (dim // 16 - 1))) * 4
+            turn = (t // 8) ^ (t // 2 % 4 * 2) if dim == 128 else (t // 8 % 4) ^ (t // 4 % 2 * 2)
+            at = 9 * dim + (t // 2) * (dim // 4) + (block ^ (turn & 7)) * 4
             for d in range(16):
                 code = (words[..., at + d // 4] >> (4 * (d % 4) + 16 * (t % 2))) & 15
-                v[..., t, 16 * block + d] = (code - 8) * half[..., 34 * dim + (block // 2) * PAGE + t]
+                v[..., t, 16 * block + d] = (code - 8) * half[..., 34 * dim + (t // 2 * ng + block // 2) * 2 + t % 2]
     return k.flatten(1, 2), v.flatten(1, 2)
 
 
