@@ -325,9 +325,106 @@ mmq_status mmq_debug_select_large_m_kernel(int which);
  * Process-wide host state; no CUDA call. */
 mmq_status mmq_debug_inject_wait_timeout(int fill, unsigned long long limit_ns);
 
-/* Synchronizes `s`, then reports and clears the sticky device error word:
- * MMQ_ERR_TIMEOUT if a bounded wait expired since the last call, MMQ_ERR_CUDA
- * if the synchronization failed, else MMQ_OK. */
+/* --------------------------------------------------------------------------
+ * A 4-bit key/value cache and attention over it.
+ *
+ * The cache is a pool of pages of MMQ_KV_PAGE tokens.  A page holds one piece of
+ * 72 * head_dim bytes per kv head (mmq_kv_page_bytes for all heads), page p at
+ * pages + p * kv_heads * 72 * head_dim, head h's piece h pieces further on.  Groups of
+ * 32 consecutive values of one head of one token share a scale s of 7 significant
+ * bits in [2^-14, 896], held as f16; code n = 0..15 stands for s * (n - 8) (exact in
+ * f16).  4.5 bits a value in all.  Inside a piece, D = head_dim, NG = D/32 groups:
+ *   K codes   at 0: token t (0..63), group g: the 16-byte chunk at t*(D/2) +
+ *             16*(g ^ ((t >> 1) & 3)) for D = 128, 16*(g ^ ((t >> 2) & 1)) for D = 64;
+ *             the code of value 8u + 2p + h of the group (u, p = 0..3, h = 0, 1) at bit
+ *             4p + 16h of the chunk's 32-bit word u.
+ *   K scales  at 32 D: f16 [t][g].
+ *   V codes   at 36 D: pair p = t/2, block a = value/16: the 16-byte chunk at p*D +
+ *             16*(a ^ turn), turn = ((p >> 2) ^ (2p & 6)) & 7 for D = 128,
+ *             ((p >> 2) ^ (p & 2)) & 3 for D = 64; the code of value 16a + 4u + i
+ *             (u, i = 0..3) of token 2p + e at bit 4i + 16e of the chunk's word u.
+ *   V scales  at 68 D: f16 [p][g][e].
+ * Slots that no token was written to may hold anything.
+ *
+ * A batch of sequences: table[b * max_pages + i] is the page of positions 64 i ..
+ * 64 i + 63 of sequence b, length[b] its token count.  The calls work on packed rows of
+ * new tokens: rows start[b] <= r < start[b + 1] (start has batch + 1 entries,
+ * start[0] = 0 and start[batch] = ntok) are the last tokens of sequence b, row r at
+ * position length[b] - start[b + 1] + r.  table, start and length are read on the
+ * device.  A page id outside [0, num_pages) or a position outside [0, 64 max_pages) is
+ * not followed: such a token is not written and reads as zeros, such keys are not
+ * there for the attention, and mmq_get_device_error then returns MMQ_ERR_ARG.
+ * -------------------------------------------------------------------------- */
+#define MMQ_KV_PAGE 64
+#define MMQ_KV_MAX_HEADS 1024
+#define MMQ_KV_MAX_BATCH (1 << 20)
+#define MMQ_KV_MAX_PAGES (1 << 24)
+
+typedef enum { MMQ_F32 = 0, MMQ_F16 = 1, MMQ_BF16 = 2 } mmq_dtype;
+
+typedef struct {
+    void* pages;              /* device, 16-byte aligned */
+    const int32_t* table;     /* device, batch * max_pages */
+    const int32_t* start;     /* device, batch + 1 */
+    const int32_t* length;    /* device, batch */
+    int num_pages;
+    int kv_heads;             /* 1 .. MMQ_KV_MAX_HEADS */
+    int head_dim;             /* 64 or 128 */
+    int batch;                /* 1 .. MMQ_KV_MAX_BATCH */
+    int max_pages;            /* 1 .. MMQ_KV_MAX_PAGES */
+} mmq_kv_cache;
+
+/* Rows [token][head][head_dim] of a tensor; strides in elements, >= 0, the last
+ * dimension contiguous.  Any alignment of an element; rows aligned to four elements are
+ * moved four at a time.  Rows that a call writes may not overlap (MMQ_ERR_ARG). */
+typedef struct {
+    void* data;
+    int dtype;                /* mmq_dtype */
+    long long token_stride;
+    long long head_stride;
+} mmq_rows;
+
+/* Bytes of one page. */
+mmq_status mmq_kv_page_bytes(int kv_heads, int head_dim, size_t* bytes);
+
+/* Quantise k and v (one dtype, ntok rows of kv_heads heads) into the cache.  Per group:
+ * s = amax / 7.5 (IEEE f32 division) rounded up to 7 significant bits and limited to
+ * [2^-14, 896]; n = rint(x / s) (IEEE f32 division, ties to even) limited to -8..7,
+ * plus 8.  Magnitudes over 6720 saturate; NaN is stored as 0.  Tokens of one call must
+ * have places of their own.  ntok = 0 is a no-op. */
+mmq_status mmq_kv_write(const mmq_kv_cache* c, const mmq_rows* k, const mmq_rows* v, int ntok, mmq_stream_t s);
+
+/* The reverse: rows of k and v get the values that the cache holds for those tokens
+ * (exact in f32 and f16, rounded to nearest in bf16).  With start[b + 1] - start[b] =
+ * length[b] whole sequences are read. */
+mmq_status mmq_kv_read(const mmq_kv_cache* c, const mmq_rows* k, const mmq_rows* v, int ntok, mmq_stream_t s);
+
+/* Attention of the new tokens' queries over the cache (their own keys included: write
+ * them first):
+ *   out[r][h] = sum_j w_j v_j / sum_j w_j,   w_j = exp(scale * q[r][h] . k_j),
+ * j over the keys that a query at position p sees: j <= p, and with window > 0 also
+ * j > p - window or j < sinks (the first tokens that stay visible).  Head h reads kv
+ * head h / (heads / kv_heads).  A row that sees no key is 0.  q and out have one dtype;
+ * sums, the softmax and both products' accumulators are f32.  For f32 rows the queries
+ * and the weights enter the products as pairs of f16 (22 bits).  q must be finite.
+ * scale > 0, a normal number up to 1e38.
+ *   max_q   at least the largest start[b + 1] - start[b] (else rows past it are left out
+ *           and mmq_get_device_error returns MMQ_ERR_ARG)
+ *   max_kv  about the largest length[b]; it guides how the work is cut, any value is right
+ * The work is cut into parts whose sums meet in the workspace (of
+ * mmq_kv_attend_workspace_bytes for the same arguments, 16-byte aligned; may be NULL when
+ * that is 0) in a fixed order, so results do not vary from call to call.  out may not
+ * overlap q, the cache or the workspace. */
+mmq_status mmq_kv_attend_workspace_bytes(const mmq_kv_cache* c, int dtype, int heads, int ntok, int max_q, int max_kv,
+                                         int window, int sinks, size_t* bytes);
+mmq_status mmq_kv_attend(const mmq_kv_cache* c, const mmq_rows* q, const mmq_rows* out, int heads, int ntok, int max_q,
+                         int max_kv, float scale, int window, int sinks, void* workspace, size_t workspace_bytes,
+                         mmq_stream_t s);
+
+/* Synchronizes `s`, then reports and clears the sticky device error words:
+ * MMQ_ERR_TIMEOUT if a bounded wait expired since the last call, else MMQ_ERR_ARG if a
+ * cache call met a page, a position or a row count outside what it was given,
+ * MMQ_ERR_CUDA if the synchronization failed, else MMQ_OK. */
 mmq_status mmq_get_device_error(mmq_stream_t s);
 
 const char* mmq_status_string(mmq_status st);

@@ -26,11 +26,15 @@ __all__ = [
     "mmq_debug_inject_wait_timeout", "mmq_debug_route", "ROUTES",
     "mmq_get_device_error", "mmq_status_string", "mmq_last_path", "mmq_version", "mmq_launch_count",
     "quantize_act", "pack_weights", "pack_weights_fused", "gemm", "gemm_dots", "TYPES",
+    "mmq_kv_page_bytes", "mmq_kv_write", "mmq_kv_read", "mmq_kv_attend_workspace_bytes", "mmq_kv_attend",
+    "KVCache", "Rows", "DTYPES", "KV_PAGE", "kv_pages", "kv_write", "kv_read", "kv_attend",
 ]
 
 MMQ_Q4_K = 12
 MMQ_Q6_K = 14
 TYPES = {"q4_K": MMQ_Q4_K, "q6_K": MMQ_Q6_K}
+DTYPES = {"float32": 0, "float16": 1, "bfloat16": 2}     # mmq_dtype by torch's name
+KV_PAGE = 64                                             # tokens per page of the 4-bit key/value cache
 BLOCK_BYTES = {MMQ_Q4_K: 144, MMQ_Q6_K: 210}
 
 STATUS = {0: "MMQ_OK", 1: "MMQ_ERR_ARG", 2: "MMQ_ERR_SHAPE", 3: "MMQ_ERR_ALIGN", 4: "MMQ_ERR_CUDA",
@@ -38,6 +42,19 @@ STATUS = {0: "MMQ_OK", 1: "MMQ_ERR_ARG", 2: "MMQ_ERR_SHAPE", 3: "MMQ_ERR_ALIGN",
 
 _lib = None
 _lock = threading.Lock()
+
+
+class KVCache(ctypes.Structure):
+    """mmq_kv_cache of the C ABI."""
+    _fields_ = [("pages", ctypes.c_void_p), ("table", ctypes.c_void_p), ("start", ctypes.c_void_p),
+                ("length", ctypes.c_void_p), ("num_pages", ctypes.c_int), ("kv_heads", ctypes.c_int),
+                ("head_dim", ctypes.c_int), ("batch", ctypes.c_int), ("max_pages", ctypes.c_int)]
+
+
+class Rows(ctypes.Structure):
+    """mmq_rows of the C ABI."""
+    _fields_ = [("data", ctypes.c_void_p), ("dtype", ctypes.c_int), ("token_stride", ctypes.c_longlong),
+                ("head_stride", ctypes.c_longlong)]
 
 
 class MMQError(RuntimeError):
@@ -61,6 +78,7 @@ def load():
                                "(or __graft_entry__.build())")
         lib = ctypes.CDLL(LIB_PATH)
         P, I, S = ctypes.c_void_p, ctypes.c_int, ctypes.POINTER(ctypes.c_size_t)
+        C, R = ctypes.POINTER(KVCache), ctypes.POINTER(Rows)
         sig = {
             "mmq_act_plane_bytes": [I, I, S, S],
             "mmq_quantize_act": [P, I, I, I, P, P, P],
@@ -78,6 +96,11 @@ def load():
             "mmq_debug_route": [I, I, I, I, I, I, ctypes.POINTER(ctypes.c_int)],
             "mmq_debug_inject_wait_timeout": [I, ctypes.c_ulonglong],
             "mmq_get_device_error": [P],
+            "mmq_kv_page_bytes": [I, I, S],
+            "mmq_kv_write": [C, R, R, I, P],
+            "mmq_kv_read": [C, R, R, I, P],
+            "mmq_kv_attend_workspace_bytes": [C, I, I, I, I, I, I, I, S],
+            "mmq_kv_attend": [C, R, R, I, I, I, I, ctypes.c_float, I, I, P, ctypes.c_size_t, P],
         }
         for name, args in sig.items():
             fn = getattr(lib, name)
@@ -192,8 +215,35 @@ def mmq_debug_inject_wait_timeout(fill: int, limit_ns: int = 0):
     _check(load().mmq_debug_inject_wait_timeout(fill, limit_ns), "mmq_debug_inject_wait_timeout")
 
 
+def mmq_kv_page_bytes(kv_heads: int, head_dim: int) -> int:
+    b = ctypes.c_size_t()
+    _check(load().mmq_kv_page_bytes(kv_heads, head_dim, ctypes.byref(b)), "mmq_kv_page_bytes")
+    return b.value
+
+
+def mmq_kv_write(cache, k, v, ntok, stream=0):
+    _check(load().mmq_kv_write(cache, k, v, ntok, stream or None), "mmq_kv_write")
+
+
+def mmq_kv_read(cache, k, v, ntok, stream=0):
+    _check(load().mmq_kv_read(cache, k, v, ntok, stream or None), "mmq_kv_read")
+
+
+def mmq_kv_attend_workspace_bytes(cache, dtype, heads, ntok, max_q, max_kv, window=0, sinks=0) -> int:
+    b = ctypes.c_size_t()
+    _check(load().mmq_kv_attend_workspace_bytes(cache, dtype, heads, ntok, max_q, max_kv, window, sinks,
+                                                ctypes.byref(b)), "mmq_kv_attend_workspace_bytes")
+    return b.value
+
+
+def mmq_kv_attend(cache, q, out, heads, ntok, max_q, max_kv, scale, window=0, sinks=0, workspace=0,
+                  workspace_bytes=0, stream=0):
+    _check(load().mmq_kv_attend(cache, q, out, heads, ntok, max_q, max_kv, scale, window, sinks, workspace or None,
+                                workspace_bytes, stream or None), "mmq_kv_attend")
+
+
 def mmq_get_device_error(stream=0) -> int:
-    """Returns the raw status (0 ok, 5 timeout, 4 CUDA error)."""
+    """Returns the raw status (0 ok, 5 timeout, 1 cache index out of range, 4 CUDA error)."""
     return load().mmq_get_device_error(stream or None)
 
 
@@ -343,3 +393,94 @@ def gemm_dots(t, packed, od, id_, qa, scales, M, stream=None):
     mmq_debug_gemm_dots(tid, packed.data_ptr(), od, id_, qa.data_ptr(), scales.data_ptr(), M, dots.data_ptr(),
                         _stream(stream))
     return dots
+
+
+# ----------------------------------------------------------------------------
+# The 4-bit key/value cache.  A batch of sequences is (pages, table, start, length):
+# pages from kv_pages, table int32 [batch, max_pages], start int32 [batch + 1] (the packed
+# rows of each sequence's newest tokens), length int32 [batch]; see include/mmq.h.
+# ----------------------------------------------------------------------------
+def kv_pages(num_pages, kv_heads, head_dim, device="cuda"):
+    """A pool of pages: uint8 [num_pages, kv_heads, 72 * head_dim], its slots not yet written."""
+    torch = _torch()
+    mmq_kv_page_bytes(kv_heads, head_dim)
+    return torch.empty((num_pages, kv_heads, 72 * head_dim), dtype=torch.uint8, device=device)
+
+
+def _kv_cache(pages, table, start, length):
+    torch = _torch()
+    i32, dev = torch.int32, pages.device
+    if pages.dtype != torch.uint8 or pages.dim() != 3 or not pages.is_contiguous() or pages.shape[2] % 72:
+        raise ValueError("pages must be a contiguous uint8 [num_pages, kv_heads, 72 * head_dim] tensor")
+    if table.dtype != i32 or table.dim() != 2 or not table.is_contiguous():
+        raise ValueError("table must be a contiguous int32 [batch, max_pages] tensor")
+    batch, max_pages = table.shape
+    for x, n, name in ((start, batch + 1, "start"), (length, batch, "length")):
+        if x.dtype != i32 or x.shape != (n,) or not x.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous int32 [{n}] tensor")
+    if not pages.is_cuda or not (dev == table.device == start.device == length.device):
+        raise ValueError("pages, table, start and length must be CUDA tensors on one device")
+    return KVCache(pages.data_ptr(), table.data_ptr(), start.data_ptr(), length.data_ptr(), pages.shape[0],
+                   pages.shape[1], pages.shape[2] // 72, batch, max_pages)
+
+
+def _kv_rows(x, shape, cache_device, name):
+    if x.dim() != 3 or tuple(x.shape) != shape or x.stride(2) != 1:
+        raise ValueError(f"{name} must be {list(shape)} with unit stride in its last dimension, got {list(x.shape)}")
+    t = DTYPES.get(str(x.dtype)[6:])
+    if t is None:
+        raise ValueError(f"{name} must be float32, float16 or bfloat16, got {x.dtype}")
+    if x.device != cache_device:
+        raise ValueError(f"{name} must be on the cache's device")
+    return Rows(x.data_ptr(), t, x.stride(0), x.stride(1))
+
+
+def kv_write(k, v, pages, table, start, length, stream=None):
+    """Quantise the new tokens' k and v ([rows, kv_heads, head_dim], any token and head strides)
+    into the cache."""
+    c = _kv_cache(pages, table, start, length)
+    shape = (k.shape[0], c.kv_heads, c.head_dim)
+    mmq_kv_write(c, _kv_rows(k, shape, pages.device, "k"), _kv_rows(v, shape, pages.device, "v"), shape[0],
+                 _stream(stream))
+
+
+def kv_read(pages, table, start, length, rows, dtype=None, k=None, v=None, stream=None):
+    """(k, v) [rows, kv_heads, head_dim] that the cache holds for the packed rows, in dtype
+    (float16 unless given) or into given k and v."""
+    torch = _torch()
+    c = _kv_cache(pages, table, start, length)
+    shape = (rows, c.kv_heads, c.head_dim)
+    with torch.cuda.stream(stream):       # a result belongs to the stream that writes it
+        k = torch.empty(shape, dtype=dtype or torch.float16, device=pages.device) if k is None else k
+        v = torch.empty(shape, dtype=k.dtype, device=pages.device) if v is None else v
+    mmq_kv_read(c, _kv_rows(k, shape, pages.device, "k"), _kv_rows(v, shape, pages.device, "v"), rows,
+                _stream(stream))
+    return k, v
+
+
+def kv_attend(q, pages, table, start, length, max_q, max_kv=None, scale=None, window=0, sinks=0, out=None,
+              workspace=None, stream=None):
+    """Attention of q [rows, heads, head_dim] over the cache.  max_q: at least the most new tokens
+    of a sequence; max_kv: about the longest length (all of the table unless given); scale:
+    head_dim ** -0.5 unless given; window 0: none."""
+    torch = _torch()
+    c = _kv_cache(pages, table, start, length)
+    rows, heads = q.shape[:2]
+    shape = (rows, heads, c.head_dim)
+    if max_kv is None:
+        max_kv = c.max_pages * KV_PAGE
+    if scale is None:
+        scale = c.head_dim ** -0.5
+    rq = _kv_rows(q, shape, pages.device, "q")
+    need = mmq_kv_attend_workspace_bytes(c, rq.dtype, heads, rows, max_q, max_kv, window, sinks)
+    with torch.cuda.stream(stream):
+        if out is None:
+            out = torch.empty(shape, dtype=q.dtype, device=q.device)
+        if need and workspace is None:
+            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    if need and (not workspace.is_cuda or workspace.device != q.device or not workspace.is_contiguous()
+                 or _nbytes(workspace) < need):
+        raise ValueError(f"workspace must be a contiguous CUDA buffer of at least {need} bytes")
+    mmq_kv_attend(c, rq, _kv_rows(out, shape, pages.device, "out"), heads, rows, max_q, max_kv, scale, window, sinks,
+                  workspace.data_ptr() if need else 0, need, _stream(stream))
+    return out

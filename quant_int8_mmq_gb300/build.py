@@ -14,7 +14,8 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(HERE, "_build")
 LIB_NAME = "libmmq_gb300.so"
 LIB_PATH = os.path.join(HERE, LIB_NAME)
-SOURCES = ["api.cu", "prepass.cu", "pack.cu", "ggml.cu", "gemm.cu", "gemm_sb.cu", "gemm_small.cu", "gemm_ft.cu", "route.cu"]
+SOURCES = ["api.cu", "prepass.cu", "pack.cu", "ggml.cu", "gemm.cu", "gemm_sb.cu", "gemm_small.cu", "gemm_ft.cu", "route.cu",
+           "kv_api.cu", "kv_cache.cu", "kv_step.cu"]
 PEAKS_SRC = "peaks.cu"
 PEAKS_EXE = os.path.join(BUILD_DIR, "mmq_peaks")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

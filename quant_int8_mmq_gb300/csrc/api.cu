@@ -7,6 +7,7 @@
 #include <atomic>
 #include <cstdint>
 
+#include "api.h"
 #include "mmq.h"
 #include "mmq_internal.h"
 #include "route.h"
@@ -18,7 +19,7 @@ std::atomic<unsigned long long> g_launches{0};
 // The sticky device error word of the whole library (one per device the library
 // is loaded on).  Kernels receive its address in their arguments; nothing else
 // names it in device code.
-__device__ unsigned int g_device_error_word;
+__device__ unsigned int g_device_error_word[2];   // [0] an expired wait, [1] a cache index out of range
 std::atomic<unsigned int*> g_error_word_addr[64];   // per device ordinal, looked up once
 
 // One-shot wait-timeout injection (verification only): fill index, wait limit.
@@ -51,17 +52,17 @@ cudaError_t device_error_word(unsigned int** word)
     return cudaSuccess;
 }
 
-cudaError_t read_and_clear_device_error(cudaStream_t s, unsigned int* value)
+cudaError_t read_and_clear_device_error(cudaStream_t s, unsigned int (&value)[2])
 {
-    *value = 0;
+    value[0] = value[1] = 0;
     cudaError_t e = cudaStreamSynchronize(s);
     if (e != cudaSuccess)
         return e;
-    e = cudaMemcpyFromSymbol(value, g_device_error_word, sizeof(unsigned int));
+    e = cudaMemcpyFromSymbol(value, g_device_error_word, sizeof(value));
     if (e != cudaSuccess)
         return e;
-    const unsigned int zero = 0;
-    return cudaMemcpyToSymbol(g_device_error_word, &zero, sizeof(unsigned int));
+    const unsigned int zero[2] = {0, 0};
+    return cudaMemcpyToSymbol(g_device_error_word, zero, sizeof(zero));
 }
 
 void arm_wait_injection(int fill, unsigned long long limit_ns)
@@ -87,7 +88,17 @@ namespace {
 
 std::atomic<const char*> g_last_path{"none"};
 
+}  // namespace
+
+namespace mmq {
+
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+
+}  // namespace mmq
+
+namespace {
+
+using mmq::aligned;
 
 bool valid_k(int K) { return K >= mmq::QK_K && K <= MMQ_MAX_ID && (K % mmq::QK_K) == 0; }
 
@@ -95,7 +106,9 @@ bool valid_k(int K) { return K >= mmq::QK_K && K <= MMQ_MAX_ID && (K % mmq::QK_K
 // device's compute capability does not change while the process runs.
 std::atomic<unsigned char> g_dev_ok[64];
 
-mmq_status check_device()
+}  // namespace
+
+mmq_status mmq::check_device()
 {
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) {
@@ -119,7 +132,12 @@ mmq_status check_device()
     return ok ? MMQ_OK : MMQ_ERR_UNSUPPORTED;
 }
 
-mmq_status from_cuda(cudaError_t e) { return e == cudaSuccess ? MMQ_OK : MMQ_ERR_CUDA; }
+mmq_status mmq::from_cuda(cudaError_t e) { return e == cudaSuccess ? MMQ_OK : MMQ_ERR_CUDA; }
+
+namespace {
+
+using mmq::check_device;
+using mmq::from_cuda;
 
 // After a pack: for q6_K, read the fold flag (FLAG word 0) back once, so that GEMM
 // calls on this buffer choose their kernel without a device read.  The read waits for
@@ -432,11 +450,11 @@ mmq_status mmq_get_device_error(mmq_stream_t s)
     const mmq_status st = check_device();
     if (st != MMQ_OK)
         return st;
-    unsigned int word = 0;
-    const cudaError_t e = mmq::read_and_clear_device_error(reinterpret_cast<cudaStream_t>(s), &word);
+    unsigned int word[2];
+    const cudaError_t e = mmq::read_and_clear_device_error(reinterpret_cast<cudaStream_t>(s), word);
     if (e != cudaSuccess)
         return MMQ_ERR_CUDA;
-    return word ? MMQ_ERR_TIMEOUT : MMQ_OK;
+    return word[0] ? MMQ_ERR_TIMEOUT : word[1] ? MMQ_ERR_ARG : MMQ_OK;
 }
 
 const char* mmq_status_string(mmq_status st)

@@ -1,0 +1,189 @@
+// kv.cuh -- the 4-bit key/value cache: layout of a piece (one page of 64 tokens of one
+// kv head), the widening of its codes, and the argument structures of its kernels.
+//
+// A group is 32 consecutive values of one head of one token.  Its scale s has 7
+// significant bits, s in [2^-14, 896], and its codes n = 0..15 stand for s * (n - 8).
+// 7 + 3 significant bits and a lowest bit of at least 2^-20 make every cached value
+// exact in f16, so the attention kernels may feed the tensor cores f16 operands without
+// a rounding on the cache's side.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <cstdint>
+
+#include "mmq.h"
+#include "mmq_internal.h"
+#include "ptx.cuh"
+
+namespace mmq {
+
+constexpr int KV_PAGE = MMQ_KV_PAGE;   // tokens per page
+constexpr int KV_GROUP = 32;           // values per scale
+
+// Byte offsets inside a piece of head size D; the documented layout is in mmq.h.
+template <int D>
+struct Piece {
+    static_assert(D == 64 || D == 128, "head size");
+    static constexpr int NG = D / KV_GROUP;
+    static constexpr int K_CODES = 0;
+    static constexpr int K_SCALES = 32 * D;
+    static constexpr int V_CODES = 36 * D;
+    static constexpr int V_SCALES = 68 * D;
+    static constexpr int BYTES = 72 * D;
+
+    // the 16-byte chunk that holds group g of token t's key
+    __host__ __device__ static constexpr int k_chunk(int t, int g)
+    {
+        return K_CODES + t * (D / 2) + ((g ^ ((t >> (D == 128 ? 1 : 2)) & (NG - 1))) << 4);
+    }
+    __host__ __device__ static constexpr int k_scale(int t, int g) { return K_SCALES + (t * NG + g) * 2; }
+    // the 16-byte chunk that holds values 16 a .. 16 a + 15 of the two tokens of pair p
+    __host__ __device__ static constexpr int v_turn(int p)
+    {
+        return D == 128 ? ((p >> 2) ^ (p << 1 & 6)) & 7 : ((p >> 2) ^ (p & 2)) & 3;
+    }
+    __host__ __device__ static constexpr int v_chunk(int p, int a) { return V_CODES + p * D + ((a ^ v_turn(p)) << 4); }
+    // the two f16 scales (tokens 2p, 2p + 1) of group g
+    __host__ __device__ static constexpr int v_scale(int p, int g) { return V_SCALES + (p * NG + g) * 4; }
+};
+
+constexpr float KV_SCALE_MIN = 6.103515625e-05f;   // 2^-14
+constexpr float KV_SCALE_MAX = 896.0f;             // 72 * 896 < 65504, the widening's addend
+
+// A batch as the entry points describe it (mmq_kv_cache with its pointers typed).
+struct KvView {
+    uint8_t* pages;
+    const int* table;
+    const int* start;
+    const int* length;
+    int num_pages, kv_heads, batch, max_pages;
+    unsigned int* bad;   // set to 1 when a table entry or a length leads outside the cache
+};
+
+struct KvRows {
+    void* data;
+    long long tok, head;   // strides in elements
+};
+
+// ------------------------------------------------------------------ widening
+__device__ __forceinline__ uint32_t kv_h2u(__half2 v) { return *reinterpret_cast<const uint32_t*>(&v); }
+__device__ __forceinline__ __half2 kv_u2h(uint32_t v) { return *reinterpret_cast<const __half2*>(&v); }
+
+// Pair i (0..3) of a code word: the nibbles at bits 4i and 4i + 16, brought to bits 4-7
+// under the exponent of 64, where they read 64 + n; one f16x2 fma with {s, -72 s} leaves
+// s * (n - 8).  Nothing is rounded: 72 s = 9 * 8 s has at most 11 significant bits.
+template <int I>
+__device__ __forceinline__ __half2 kv_widen(uint32_t w, __half2 s, __half2 b)
+{
+    const uint32_t x = I == 0 ? w << 4 : I == 1 ? w : I == 2 ? w >> 4 : w >> 8;
+    return __hfma2(kv_u2h((x & 0x00F000F0u) | 0x54005400u), s, b);
+}
+__device__ __forceinline__ __half2 kv_addend(__half2 s) { return __hmul2(s, __floats2half2_rn(-72.0f, -72.0f)); }
+
+// ------------------------------------------------------------------ rows of any type
+template <typename T>
+struct Elt;
+template <>
+struct Elt<float> {
+    static __device__ __forceinline__ float to(float v) { return v; }
+    static __device__ __forceinline__ float from(float v) { return v; }
+};
+template <>
+struct Elt<__half> {
+    static __device__ __forceinline__ float to(__half v) { return __half2float(v); }
+    static __device__ __forceinline__ __half from(float v) { return __float2half_rn(v); }
+};
+template <>
+struct Elt<__nv_bfloat16> {
+    static __device__ __forceinline__ float to(__nv_bfloat16 v) { return __bfloat162float(v); }
+    static __device__ __forceinline__ __nv_bfloat16 from(float v) { return __float2bfloat16_rn(v); }
+};
+
+// Four consecutive elements; `wide` when their address is aligned to all four.
+template <typename T>
+__device__ __forceinline__ float4 load4(const T* p, bool wide)
+{
+    T e[4];
+    if (wide) {
+        if constexpr (sizeof(T) == 4)
+            *reinterpret_cast<uint4*>(e) = *reinterpret_cast<const uint4*>(p);
+        else
+            *reinterpret_cast<uint2*>(e) = *reinterpret_cast<const uint2*>(p);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            e[i] = p[i];
+    }
+    return make_float4(Elt<T>::to(e[0]), Elt<T>::to(e[1]), Elt<T>::to(e[2]), Elt<T>::to(e[3]));
+}
+template <typename T>
+__device__ __forceinline__ void store4(T* p, float4 v, bool wide)
+{
+    T e[4] = {Elt<T>::from(v.x), Elt<T>::from(v.y), Elt<T>::from(v.z), Elt<T>::from(v.w)};
+    if (wide) {
+        if constexpr (sizeof(T) == 4)
+            *reinterpret_cast<uint4*>(p) = *reinterpret_cast<uint4*>(e);
+        else
+            *reinterpret_cast<uint2*>(p) = *reinterpret_cast<uint2*>(e);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            p[i] = e[i];
+    }
+}
+
+// The sequence of packed row r: the last b with start[b] <= r, found by one warp, 32
+// probes a step (sequences without rows are passed over).  0 <= result < batch whatever
+// start holds.
+__device__ __forceinline__ int kv_sequence_of(const int* start, int batch, int r, int lane)
+{
+    int lo = 0, n = batch;
+    while (n > 1) {
+        const int step = (n + 31) / 32;
+        const int i = lo + lane * step;
+        const bool in = lane * step < n && (lane == 0 || start[i] <= r);
+        const int last = 31 - __clz(__ballot_sync(0xffffffffu, in));   // lane 0 is always in
+        lo += last * step;
+        n = min(step, n - last * step);
+    }
+    return lo;
+}
+
+// ------------------------------------------------------------------ launchers
+enum KvType { KV_F32 = 0, KV_F16 = 1, KV_BF16 = 2 };
+
+cudaError_t launch_kv_write(const KvView& c, int dim, int dtype, const KvRows& k, const KvRows& v, bool wide,
+                            int ntok, cudaStream_t s);
+cudaError_t launch_kv_read(const KvView& c, int dim, int dtype, const KvRows& k, const KvRows& v, bool wide, int ntok,
+                           cudaStream_t s);
+
+// What an attention call computes; positions and lengths are read on the device.
+struct AttendArgs {
+    KvView c;
+    KvRows q, out;
+    int heads, group;      // group = heads / kv_heads
+    int ntok;
+    float scale_log2;      // softmax scale times log2(e)
+    int window, sinks;
+    int row_tiles;         // row tiles per (sequence, kv head)
+    int nsplit;            // parts of the visible pages
+    bool wide;
+    float* part;           // nsplit > 1: [nsplit][ntok * heads][D] unnormalised sums
+    float2* part_ml;       //             [nsplit][ntok * heads] {reference, sum}
+    WaitCtl wc;
+};
+
+struct AttendPlan {
+    int kernel;      // 0: few rows per sequence
+    int row_tiles;
+    int nsplit;
+    size_t part_bytes, ml_bytes;
+};
+AttendPlan plan_attend(int dtype, int heads, int kv_heads, int dim, int batch, int ntok, int max_q, int max_kv,
+                       int window, int sinks);
+cudaError_t launch_kv_step(const AttendArgs& a, int dim, int dtype, cudaStream_t s);
+cudaError_t launch_kv_join(const AttendArgs& a, int dim, int dtype, cudaStream_t s);
+
+}  // namespace mmq

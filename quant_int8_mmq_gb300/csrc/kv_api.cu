@@ -1,0 +1,241 @@
+// kv_api.cu -- entry points of the 4-bit key/value cache and the attention over it.
+//
+// As in api.cu, arguments are checked on the host before any CUDA call; what only the
+// device knows (page ids, lengths) is checked by the kernels.
+#include "api.h"
+#include "kv.cuh"
+
+namespace mmq {
+
+// How an attention call is cut up.  Target CTAs: two of the few-row kernel's fit an SM of
+// the chip's 152, and parts of the pages below one page per warp gain nothing.
+AttendPlan plan_attend(int dtype, int heads, int kv_heads, int dim, int batch, int ntok, int max_q, int max_kv,
+                       int window, int sinks)
+{
+    (void)dtype;
+    AttendPlan p = {};
+    const int group = heads / kv_heads;
+    max_q = max_q < ntok ? max_q : ntok;
+    long long pages = (static_cast<long long>(max_kv) + KV_PAGE - 1) / KV_PAGE;
+    if (window > 0) {
+        const long long seen = (static_cast<long long>(window) + max_q + sinks) / KV_PAGE + 3;
+        pages = pages < seen ? pages : seen;
+    }
+    p.row_tiles = static_cast<int>((static_cast<long long>(max_q) * group + 7) / 8);
+    const long long units = static_cast<long long>(batch) * kv_heads * p.row_tiles;
+    long long nsplit = (2 * 152 + units - 1) / units;
+    const long long most = (pages + 3) / 4;
+    nsplit = nsplit < most ? nsplit : most;
+    p.nsplit = static_cast<int>(nsplit < 1 ? 1 : nsplit);
+    if (p.nsplit > 1) {
+        const size_t rows = static_cast<size_t>(p.nsplit) * ntok * heads;
+        p.part_bytes = rows * dim * sizeof(float);
+        p.ml_bytes = rows * sizeof(float2);
+    }
+    return p;
+}
+
+}  // namespace mmq
+
+namespace {
+
+using mmq::aligned;
+using mmq::AttendPlan;
+using mmq::KvRows;
+using mmq::KvView;
+
+mmq_status check_cache(const mmq_kv_cache* c)
+{
+    if (!c)
+        return MMQ_ERR_ARG;
+    if (c->head_dim != 64 && c->head_dim != 128)
+        return MMQ_ERR_SHAPE;
+    if (c->kv_heads < 1 || c->kv_heads > MMQ_KV_MAX_HEADS || c->num_pages < 1 || c->batch < 1 ||
+        c->batch > MMQ_KV_MAX_BATCH || c->max_pages < 1 || c->max_pages > MMQ_KV_MAX_PAGES)
+        return MMQ_ERR_SHAPE;
+    if (!c->pages || !c->table || !c->start || !c->length)
+        return MMQ_ERR_ARG;
+    if (!aligned(c->pages, 16) || !aligned(c->table, 4) || !aligned(c->start, 4) || !aligned(c->length, 4))
+        return MMQ_ERR_ALIGN;
+    return MMQ_OK;
+}
+
+bool known_type(int t) { return t == MMQ_F32 || t == MMQ_F16 || t == MMQ_BF16; }
+
+// [ntok][heads][dim] rows; those that are written may not overlap.
+mmq_status check_rows(const mmq_rows* r, int ntok, int heads, int dim, bool written)
+{
+    if (!r || !r->data || !known_type(r->dtype) || r->token_stride < 0 || r->head_stride < 0)
+        return MMQ_ERR_ARG;
+    constexpr long long MOST = 1ll << 40;
+    if (r->token_stride > MOST || r->head_stride > MOST)
+        return MMQ_ERR_SHAPE;
+    if (!aligned(r->data, r->dtype == MMQ_F32 ? 4 : 2))
+        return MMQ_ERR_ALIGN;
+    if (written) {
+        const long long t = r->token_stride, h = r->head_stride;
+        const bool by_token = (heads == 1 || h >= dim) && (ntok == 1 || t >= (heads - 1) * h + dim);
+        const bool by_head = (ntok == 1 || t >= dim) && (heads == 1 || h >= (ntok - 1) * t + dim);
+        if (!by_token && !by_head)
+            return MMQ_ERR_ARG;
+    }
+    return MMQ_OK;
+}
+
+// Whether four elements from a multiple of four on may be loaded at once.
+bool wide(const mmq_rows* r)
+{
+    return aligned(r->data, r->dtype == MMQ_F32 ? 16 : 8) && r->token_stride % 4 == 0 && r->head_stride % 4 == 0;
+}
+
+KvRows rows(const mmq_rows* r) { return {r->data, r->token_stride, r->head_stride}; }
+
+mmq_status view(const mmq_kv_cache* c, KvView* v)
+{
+    unsigned int* err = nullptr;
+    const cudaError_t e = mmq::device_error_word(&err);
+    if (e != cudaSuccess)
+        return MMQ_ERR_CUDA;
+    *v = {static_cast<uint8_t*>(c->pages), c->table, c->start, c->length, c->num_pages, c->kv_heads, c->batch,
+          c->max_pages, err + 1};
+    return MMQ_OK;
+}
+
+mmq_status move_rows(bool write, const mmq_kv_cache* c, const mmq_rows* k, const mmq_rows* v, int ntok,
+                     mmq_stream_t s)
+{
+    mmq_status st = check_cache(c);
+    if (st != MMQ_OK)
+        return st;
+    if (ntok < 0 || ntok > MMQ_MAX_M)
+        return MMQ_ERR_SHAPE;
+    for (const mmq_rows* r : {k, v})
+        if ((st = check_rows(r, ntok, c->kv_heads, c->head_dim, !write)) != MMQ_OK)
+            return st;
+    if (k->dtype != v->dtype)
+        return MMQ_ERR_ARG;
+    if (ntok == 0)
+        return MMQ_OK;
+    if ((st = mmq::check_device()) != MMQ_OK)
+        return st;
+    KvView cv;
+    if ((st = view(c, &cv)) != MMQ_OK)
+        return st;
+    const auto launch = write ? mmq::launch_kv_write : mmq::launch_kv_read;
+    return mmq::from_cuda(launch(cv, c->head_dim, k->dtype, rows(k), rows(v), wide(k) && wide(v), ntok,
+                                 reinterpret_cast<cudaStream_t>(s)));
+}
+
+mmq_status check_attend(const mmq_kv_cache* c, int dtype, int heads, int ntok, int max_q, int max_kv, int window,
+                        int sinks)
+{
+    if (!known_type(dtype) || window < 0 || sinks < 0 || max_q < 0 || max_kv < 0)
+        return MMQ_ERR_ARG;
+    if (c->head_dim != 64 && c->head_dim != 128)
+        return MMQ_ERR_SHAPE;
+    if (c->kv_heads < 1 || c->kv_heads > MMQ_KV_MAX_HEADS || c->batch < 1 || c->batch > MMQ_KV_MAX_BATCH ||
+        heads < 1 || heads > MMQ_KV_MAX_HEADS || heads % c->kv_heads != 0 || ntok < 0 || ntok > MMQ_MAX_M)
+        return MMQ_ERR_SHAPE;
+    return MMQ_OK;
+}
+
+AttendPlan plan(const mmq_kv_cache* c, int dtype, int heads, int ntok, int max_q, int max_kv, int window, int sinks)
+{
+    return mmq::plan_attend(dtype, heads, c->kv_heads, c->head_dim, c->batch, ntok, max_q < 1 ? 1 : max_q,
+                            max_kv < 1 ? 1 : max_kv, window, sinks);
+}
+
+}  // namespace
+
+extern "C" {
+
+mmq_status mmq_kv_page_bytes(int kv_heads, int head_dim, size_t* bytes)
+{
+    if (!bytes)
+        return MMQ_ERR_ARG;
+    if (kv_heads < 1 || kv_heads > MMQ_KV_MAX_HEADS || (head_dim != 64 && head_dim != 128))
+        return MMQ_ERR_SHAPE;
+    *bytes = static_cast<size_t>(kv_heads) * head_dim * 72;
+    return MMQ_OK;
+}
+
+mmq_status mmq_kv_write(const mmq_kv_cache* c, const mmq_rows* k, const mmq_rows* v, int ntok, mmq_stream_t s)
+{
+    return move_rows(true, c, k, v, ntok, s);
+}
+
+mmq_status mmq_kv_read(const mmq_kv_cache* c, const mmq_rows* k, const mmq_rows* v, int ntok, mmq_stream_t s)
+{
+    return move_rows(false, c, k, v, ntok, s);
+}
+
+mmq_status mmq_kv_attend_workspace_bytes(const mmq_kv_cache* c, int dtype, int heads, int ntok, int max_q, int max_kv,
+                                         int window, int sinks, size_t* bytes)
+{
+    if (!c || !bytes)
+        return MMQ_ERR_ARG;
+    const mmq_status st = check_attend(c, dtype, heads, ntok, max_q, max_kv, window, sinks);
+    if (st != MMQ_OK)
+        return st;
+    *bytes = 0;
+    if (ntok > 0) {
+        const AttendPlan p = plan(c, dtype, heads, ntok, max_q, max_kv, window, sinks);
+        *bytes = p.part_bytes + p.ml_bytes;
+    }
+    return MMQ_OK;
+}
+
+mmq_status mmq_kv_attend(const mmq_kv_cache* c, const mmq_rows* q, const mmq_rows* out, int heads, int ntok, int max_q,
+                         int max_kv, float scale, int window, int sinks, void* workspace, size_t workspace_bytes,
+                         mmq_stream_t s)
+{
+    mmq_status st = check_cache(c);
+    if (st != MMQ_OK)
+        return st;
+    if (!q || !out)
+        return MMQ_ERR_ARG;
+    if ((st = check_attend(c, q->dtype, heads, ntok, max_q, max_kv, window, sinks)) != MMQ_OK ||
+        (st = check_rows(q, ntok, heads, c->head_dim, false)) != MMQ_OK ||
+        (st = check_rows(out, ntok, heads, c->head_dim, true)) != MMQ_OK)
+        return st;
+    // a positive normal number whose log2(e) multiple is finite
+    if (q->dtype != out->dtype || !(scale >= 1.17549435e-38f && scale <= 1e38f))
+        return MMQ_ERR_ARG;
+    if (ntok == 0)
+        return MMQ_OK;
+    const AttendPlan p = plan(c, q->dtype, heads, ntok, max_q, max_kv, window, sinks);
+    if (p.part_bytes + p.ml_bytes > 0) {
+        if (!workspace || workspace_bytes < p.part_bytes + p.ml_bytes)
+            return MMQ_ERR_ARG;
+        if (!aligned(workspace, 16))
+            return MMQ_ERR_ALIGN;
+    }
+    if (static_cast<long long>(p.nsplit) * p.row_tiles * c->kv_heads * c->batch > 0x7fffffffll ||
+        static_cast<long long>(ntok) * heads > 0x7fffffffll)
+        return MMQ_ERR_SHAPE;
+    if ((st = mmq::check_device()) != MMQ_OK)
+        return st;
+    mmq::AttendArgs a = {};
+    if ((st = view(c, &a.c)) != MMQ_OK)
+        return st;
+    a.q = rows(q);
+    a.out = rows(out);
+    a.heads = heads;
+    a.group = heads / c->kv_heads;
+    a.ntok = ntok;
+    a.scale_log2 = scale * 1.4426950408889634f;
+    a.window = window;
+    a.sinks = window > 0 ? sinks : 0;
+    a.row_tiles = p.row_tiles;
+    a.nsplit = p.nsplit;
+    a.wide = wide(q) && wide(out);
+    a.part = static_cast<float*>(workspace);
+    a.part_ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(workspace) + p.part_bytes);
+    a.wc = {a.c.bad - 1, mmq::WAIT_LIMIT_NS, -1};
+    cudaError_t e = mmq::launch_kv_step(a, c->head_dim, q->dtype, reinterpret_cast<cudaStream_t>(s));
+    if (e == cudaSuccess && p.nsplit > 1)
+        e = mmq::launch_kv_join(a, c->head_dim, q->dtype, reinterpret_cast<cudaStream_t>(s));
+    return mmq::from_cuda(e);
+}
+
+}  // extern "C"

@@ -158,11 +158,13 @@ inline WeightPlanes weight_planes(int type, int od, int id)
 // (mmq_launch_count); count_launch is called once per launch attempt.
 void count_launch();
 
-// The library's sticky device error word (api.cu): its device address on the
-// current device (looked up once per device), and the host-side read-and-clear
-// behind mmq_get_device_error (synchronizes the stream first).
+// The library's sticky device error words (api.cu): the device address of the first on
+// the current device (looked up once per device), and the host-side read-and-clear
+// behind mmq_get_device_error (synchronizes the stream first).  Word 0 is set by a wait
+// that ran out and makes every wait give up; word 1, which no wait looks at, by a cache
+// kernel that met a page or a length outside the cache.
 cudaError_t device_error_word(unsigned int** word);
-cudaError_t read_and_clear_device_error(cudaStream_t s, unsigned int* value);
+cudaError_t read_and_clear_device_error(cudaStream_t s, unsigned int (&value)[2]);
 
 // What a tile-GEMM launch's bounded waits use: the error word, the time limit of
 // each wait, and (verification only) one operand-ring fill that CTA 0's producer

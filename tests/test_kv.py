@@ -1,0 +1,135 @@
+"""Refusals and size queries of the 4-bit key/value cache and its attention (no GPU needed)."""
+import ctypes
+
+import pytest
+
+import quant_int8_mmq_gb300 as mmq
+
+P16 = 0x10000          # an aligned address that the error paths never follow
+OK, ARG, SHAPE, ALIGN, UNSUPPORTED = 0, 1, 2, 3, 6
+
+
+def cache(**kw):
+    f = dict(pages=P16, table=P16, start=P16, length=P16, num_pages=8, kv_heads=2, head_dim=128, batch=1, max_pages=8)
+    f.update(kw)
+    return mmq.KVCache(*(f[n] for n, _ in mmq.KVCache._fields_))
+
+
+def rows(heads=2, dim=128, dtype=0, **kw):
+    f = dict(data=P16, dtype=dtype, token_stride=heads * dim, head_stride=dim)
+    f.update(kw)
+    return mmq.Rows(*(f[n] for n, _ in mmq.Rows._fields_))
+
+
+def write(c=None, k=None, v=None, n=4):
+    return mmq.load().mmq_kv_write(c or cache(), k or rows(), v or rows(), n, None)
+
+
+def read(c=None, k=None, v=None, n=4):
+    return mmq.load().mmq_kv_read(c or cache(), k or rows(), v or rows(), n, None)
+
+
+def attend(c=None, q=None, out=None, heads=2, n=4, max_q=4, max_kv=256, scale=0.1, window=0, sinks=0, ws=P16,
+           size=1 << 40):
+    return mmq.load().mmq_kv_attend(c or cache(), q or rows(), out or rows(), heads, n, max_q, max_kv, scale, window,
+                                    sinks, ws, size, None)
+
+
+def test_page_bytes(mmq_lib):
+    assert mmq.mmq_kv_page_bytes(1, 64) == 4608
+    assert mmq.mmq_kv_page_bytes(8, 128) == 8 * 9216
+    for heads, dim in ((0, 128), (1025, 128), (1, 96), (1, 256), (1, 0)):
+        with pytest.raises(mmq.MMQError) as e:
+            mmq.mmq_kv_page_bytes(heads, dim)
+        assert e.value.status == SHAPE
+    assert mmq.load().mmq_kv_page_bytes(1, 64, None) == ARG
+
+
+@pytest.mark.parametrize("call", [write, read, attend])
+def test_cache_is_checked_by_every_call(mmq_lib, call):
+    for kw, st in ((dict(head_dim=80), SHAPE), (dict(kv_heads=0), SHAPE), (dict(kv_heads=1025), SHAPE),
+                   (dict(num_pages=0), SHAPE), (dict(batch=0), SHAPE), (dict(batch=(1 << 20) + 1), SHAPE),
+                   (dict(max_pages=0), SHAPE), (dict(max_pages=(1 << 24) + 1), SHAPE),
+                   (dict(pages=None), ARG), (dict(table=None), ARG), (dict(start=None), ARG), (dict(length=None), ARG),
+                   (dict(pages=P16 + 8), ALIGN), (dict(table=P16 + 2), ALIGN), (dict(start=P16 + 1), ALIGN),
+                   (dict(length=P16 + 2), ALIGN)):
+        assert call(c=cache(**kw)) == st, kw
+    lib = mmq.load()
+    assert lib.mmq_kv_write(None, rows(), rows(), 4, None) == ARG
+    assert lib.mmq_kv_read(None, rows(), rows(), 4, None) == ARG
+    assert lib.mmq_kv_attend(None, rows(), rows(), 2, 4, 4, 256, 0.1, 0, 0, P16, 0, None) == ARG
+
+
+@pytest.mark.parametrize("call,names", [(write, ("k", "v")), (read, ("k", "v")), (attend, ("q", "out"))])
+def test_rows_are_checked_by_every_call(mmq_lib, call, names):
+    for name in names:
+        for kw, st in ((dict(data=None), ARG), (dict(dtype=3), ARG), (dict(dtype=-1), ARG), (dict(token_stride=-256), ARG),
+                       (dict(head_stride=-128), ARG), (dict(token_stride=1 << 41), SHAPE), (dict(data=P16 + 2), ALIGN)):
+            assert call(**{name: rows(**kw)}) == st, (name, kw)
+        assert call(**{name: rows(dtype=1)}) == ARG          # one type for both
+    both = {name: rows(dtype=2, data=P16 + 1) for name in names}
+    assert call(**both) == ALIGN
+
+
+def test_written_rows_may_not_overlap(mmq_lib):
+    unsupported_or_launched = (OK, UNSUPPORTED)
+    for kw in (dict(token_stride=0), dict(head_stride=0), dict(token_stride=200), dict(token_stride=64, head_stride=64)):
+        assert read(v=rows(**kw)) == ARG, kw
+        assert attend(out=rows(**kw)) == ARG, kw
+    import torch
+    if torch.cuda.is_available():
+        pytest.skip("the addresses below are no memory")
+    # heads outside tokens, gaps, and (for rows that are only read) broadcasts
+    for kw in (dict(token_stride=128, head_stride=512), dict(token_stride=300, head_stride=130)):
+        assert read(v=rows(**kw)) in unsupported_or_launched, kw
+        assert attend(out=rows(**kw)) in unsupported_or_launched, kw
+    assert write(k=rows(token_stride=0), v=rows(head_stride=0)) in unsupported_or_launched
+
+
+def test_counts_scale_window_and_workspace(mmq_lib):
+    assert write(n=-1) == SHAPE and read(n=(1 << 22) + 1) == SHAPE and attend(n=-1) == SHAPE
+    for kw, st in ((dict(heads=3), SHAPE), (dict(heads=0), SHAPE), (dict(heads=2048), SHAPE), (dict(scale=0.0), ARG),
+                   (dict(scale=-1.0), ARG), (dict(scale=float("nan")), ARG), (dict(scale=float("inf")), ARG),
+                   (dict(window=-1), ARG), (dict(sinks=-1), ARG), (dict(max_q=-1), ARG), (dict(max_kv=-1), ARG)):
+        assert attend(**kw) == st, kw
+    # a call that is cut into parts needs its workspace
+    many = dict(c=cache(max_pages=4096), n=1, max_q=1, max_kv=4096 * 64)
+    need = mmq.mmq_kv_attend_workspace_bytes(many["c"], 0, 2, 1, 1, 4096 * 64)
+    assert need > 0 and need % 16 == 0
+    assert attend(**many, ws=None) == ARG
+    assert attend(**many, size=need - 1) == ARG
+    assert attend(**many, ws=P16 + 8) == ALIGN
+    assert mmq.load().mmq_kv_attend_workspace_bytes(many["c"], 0, 2, 1, 1, 64, 0, 0, None) == ARG
+    assert mmq.load().mmq_kv_attend_workspace_bytes(None, 0, 2, 1, 1, 64, 0, 0,
+                                                    ctypes.byref(ctypes.c_size_t())) == ARG
+
+
+def test_no_rows_is_no_work(mmq_lib):
+    before = mmq.mmq_launch_count()
+    assert write(n=0) == OK and read(n=0) == OK and attend(n=0, ws=None, size=0) == OK
+    assert mmq.mmq_kv_attend_workspace_bytes(cache(), 0, 2, 0, 1, 64) == 0
+    assert mmq.mmq_launch_count() == before
+
+
+def test_without_a_gpu_calls_are_unsupported(mmq_lib):
+    import torch
+    if torch.cuda.is_available():
+        pytest.skip("a GPU is present")
+    assert write() == UNSUPPORTED and read() == UNSUPPORTED and attend() == UNSUPPORTED
+
+
+def test_tensor_helpers_refuse(mmq_lib):
+    import torch
+    pages = mmq.kv_pages(4, 2, 64, device="cpu")
+    assert pages.shape == (4, 2, 4608) and pages.dtype == torch.uint8
+    table, start, length = (torch.zeros(s, dtype=torch.int32) for s in ((1, 4), (2,), (1,)))
+    x = torch.zeros(3, 2, 64)
+    with pytest.raises(ValueError, match="CUDA"):
+        mmq.kv_write(x, x, pages, table, start, length)
+    for bad, what in (((pages.float(), table, start, length), "pages"), ((pages[..., :-1], table, start, length), "pages"),
+                      ((pages, table.long(), start, length), "table"), ((pages, table[0], start, length), "table"),
+                      ((pages, table, start[:1], length), "start"), ((pages, table, start, length.long()), "length"),
+                      ((pages, table, start, start), "length")):
+        for call in (lambda c: mmq.kv_write(x, x, *c), lambda c: mmq.kv_read(*c, 3), lambda c: mmq.kv_attend(x, *c, 3)):
+            with pytest.raises(ValueError, match=what):
+                call(bad)

@@ -1,0 +1,394 @@
+"""The 4-bit key/value cache and the attention over it, on the GPU, against the definitions of
+tests/kv_reference.py in 64 bits.
+
+Written bytes and values read back are exact.  Attention: a score's error is at most
+2^-20 (S + 1) with S = scale * sum |q| |k| (operands of 22 bits, f32 sums of up to 2 * 128 terms, the
+exponential's 2^-22), and moves the result by at most twice that times the largest |v|; weights
+that enter the products in 16 bits (16-bit rows only) add 2^-11 of it, and the result's own
+rounding half a unit of its last place.
+"""
+import numpy as np
+import pytest
+import torch
+
+import quant_int8_mmq_gb300 as mmq
+from tests import kv_reference as ref
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+F32, F16, BF16 = torch.float32, torch.float16, torch.bfloat16
+HALF_ULP = {F32: 2.0 ** -24, F16: 2.0 ** -11, BF16: 2.0 ** -8}
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib(mmq_lib):
+    assert torch.cuda.is_available(), "GPU tests need a CUDA device"
+    torch.cuda.synchronize()
+    mmq.mmq_get_device_error()
+    yield
+
+
+def status():
+    return mmq.mmq_get_device_error()
+
+
+class Batch:
+    """Sequences of the given lengths whose last new[b] tokens are the packed rows, in pages in no
+    order; unwritten slots hold 0xFF (their scales are no numbers)."""
+
+    def __init__(self, new, length, kv_heads, dim, dtype=F32, seed=0, max_pages=None, spare=2, fill=True):
+        g = torch.Generator().manual_seed(seed)
+        self.new, self.len, self.hk, self.dim, self.dtype = new, length, kv_heads, dim, dtype
+        need = [-(-max(m, 0) // 64) for m in length]
+        self.max_pages = max_pages or max(max(need), 1)
+        num = sum(need) + spare
+        perm = torch.randperm(num, generator=g).to(torch.int32)
+        table = torch.full((len(new), self.max_pages), -1, dtype=torch.int32)
+        at = 0
+        for b, n in enumerate(need):
+            table[b, :n] = perm[at:at + n]
+            at += n
+        self.table = table.to(DEV)
+        self.start = torch.tensor([0] + list(np.cumsum(new)), dtype=torch.int32, device=DEV)
+        self.length = torch.tensor(length, dtype=torch.int32, device=DEV)
+        self.rows = sum(new)
+        self.pages = torch.full((num, kv_heads, 72 * dim), 0xFF, dtype=torch.uint8, device=DEV)
+        self.k, self.v = [], []
+        if fill:   # every token of every sequence, written by the package (checked bit for bit elsewhere)
+            self.k = [torch.randn(max(m, 0), kv_heads, dim, generator=g).to(dtype).to(DEV) for m in length]
+            self.v = [torch.randn(max(m, 0), kv_heads, dim, generator=g).to(dtype).to(DEV) for m in length]
+            whole = torch.tensor([0] + list(np.cumsum([max(m, 0) for m in length])), dtype=torch.int32, device=DEV)
+            if sum(max(m, 0) for m in length):
+                mmq.kv_write(torch.cat(self.k), torch.cat(self.v), self.pages, self.table, whole,
+                             self.length.clamp(min=0))
+
+    @property
+    def cache(self):
+        return self.pages, self.table, self.start, self.length
+
+    def q(self, heads, seed=1, factor=1.5):
+        g = torch.Generator().manual_seed(seed)
+        return (factor * torch.randn(self.rows, heads, self.dim, generator=g)).to(self.dtype).to(DEV)
+
+    def held(self, b):
+        """What the cache holds of sequence b, f64."""
+        return tuple(torch.from_numpy(ref.values(x[b].double().cpu().numpy())).to(DEV) for x in (self.k, self.v))
+
+    def check(self, q, out, scale=None, window=0, sinks=0):
+        scale = self.dim ** -0.5 if scale is None else scale
+        assert out.dtype == self.dtype
+        lo = 0
+        for b, (n, m) in enumerate(zip(self.new, self.len)):
+            k, v = self.held(b)
+            for i in range(0, n, 512):
+                c = min(512, n - i)
+                rows = slice(lo + i, lo + i + c)
+                pos = torch.arange(m - n + i, m - n + i + c, device=DEV)
+                want, S = ref.attend(q[rows].double(), k, v, pos, scale, window, sinks)
+                big = v.abs().max() if v.numel() else 0.0
+                # f32 rounding of the scale itself moves every score by a factor within 2^-23
+                tol = (2 ** -19 * (S + 1) + (2 ** -11 if self.dtype != F32 else 0))[..., None] * big \
+                    + HALF_ULP[self.dtype] * want.abs() + 2.0 ** -25
+                err = (out[rows].double() - want).abs()
+                assert torch.isfinite(out[rows]).all()
+                assert (err <= tol).all(), (b, i, err.max().item(), (err / tol).max().item())
+            lo += n
+        assert status() == 0
+
+
+# ------------------------------------------------------------------------------------ write, read
+def hard_rows(n, heads, dim, dtype, seed):
+    """Rows with what quantising can get wrong: ties, zeros, huge, tiny, no numbers."""
+    g = torch.Generator().manual_seed(seed)
+    x = torch.randn(n, heads, dim, generator=g)
+    x[0::5] *= 10.0 ** torch.randint(-9, 6, (len(x[0::5]), heads, 1), generator=g)
+    x[1::5] = torch.randint(-15, 16, (len(x[1::5]), heads, dim), generator=g).float() / 2     # exact ties
+    x[2, :, :32] = 0.0
+    x[2, :, 32:64] = -0.0
+    x[3, :, 5] = float("nan")
+    x[3, :, 40] = float("inf")
+    x[4, :, 7] = float("-inf")
+    x[4, :, 33:] = 7000.0
+    return x.to(dtype)
+
+
+@pytest.mark.parametrize("dtype", [F32, F16, BF16])
+@pytest.mark.parametrize("dim,heads", [(64, 3), (128, 2), (128, 1)])
+def test_written_bytes_are_the_definition(dtype, dim, heads):
+    new, length = [1, 7, 0, 70], [1, 70, 5, 131]
+    b = Batch(new, length, heads, dim, dtype, fill=False)
+    k, v = (hard_rows(b.rows, heads, dim, dtype, s) for s in (1, 2))
+    want = b.pages.cpu().numpy()
+    r = 0
+    for s, (n, m) in enumerate(zip(new, length)):
+        for p in range(m - n, m):
+            ref.put(want, int(b.table[s, p // 64]), p % 64, k[r].double().numpy(), v[r].double().numpy())
+            r += 1
+    mmq.kv_write(k.to(DEV), v.to(DEV), *b.cache)
+    assert status() == 0
+    got = b.pages.cpu().numpy()
+    assert np.array_equal(got, want)          # slots of no new token are untouched too
+    for out, x in zip(mmq.kv_read(*b.cache, b.rows, dtype=F32), (k, v)):
+        assert np.array_equal(out.double().cpu().numpy(), ref.values(x.double().numpy()))
+    for t in (F16, BF16):
+        for out, x in zip(mmq.kv_read(*b.cache, b.rows, dtype=t), (k, v)):
+            assert torch.equal(out.cpu(), torch.from_numpy(ref.values(x.double().numpy())).to(t))
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("shift", [0, 1, 4])
+def test_rows_of_any_stride_and_alignment(dtype, shift):
+    """k and v as parts of one wide row, shifted by single elements; heads outside tokens; broadcasts."""
+    heads, dim, n = 2, 128, 67
+    b = Batch([n], [n], heads, dim, dtype, fill=False)
+    wide = torch.randn(n, 1000 + shift, device=DEV).to(dtype)
+    k = wide[:, shift:shift + 256].view(n, heads, dim)
+    v = wide[:, shift + 300:shift + 300 + 256].view(n, heads, dim)
+    mmq.kv_write(k, v, *b.cache)
+    out = [x.double().cpu().numpy() for x in mmq.kv_read(*b.cache, n, dtype=F32)]
+    for o, x in zip(out, (k, v)):
+        assert np.array_equal(o, ref.values(x.double().cpu().numpy()))
+    outer = torch.full((heads, n, dim + shift), 9.0, device=DEV, dtype=dtype)
+    both = [x[..., :dim].transpose(0, 1) for x in (outer.clone(), outer.clone())]
+    mmq.kv_read(*b.cache, n, k=both[0], v=both[1])
+    for o, x in zip(both, out):
+        assert torch.equal(o.cpu(), torch.from_numpy(x).to(dtype))
+    assert all((o.transpose(0, 1)._base[..., dim:] == 9.0).all() for o in both)
+    one = torch.randn(1, 1, dim, device=DEV).to(dtype).expand(n, heads, dim)
+    mmq.kv_write(one, one, *b.cache)
+    got = mmq.kv_read(*b.cache, n, dtype=F32)
+    want = torch.from_numpy(ref.values(one[:1, :1].double().cpu().numpy())).float().to(DEV)
+    assert all(torch.equal(g, want.expand(n, heads, dim)) for g in got)
+    assert status() == 0
+
+
+def test_tokens_without_a_place_are_reported_and_read_as_zero():
+    b = Batch([3, 70], [2, 70], 2, 64, max_pages=2)         # the first row of sequence 0 is before it
+    before = b.pages.clone()
+    bad = b.table.clone()
+    bad[1, 1] = b.pages.shape[0]                            # a page past the pool
+    x = torch.randn(73, 2, 64, device=DEV)
+    mmq.kv_write(x, x, b.pages, bad, b.start, b.length)
+    assert status() == 1 and status() == 0
+    touched = (b.pages != before).flatten(1).any(1)
+    assert touched.sum() == 2
+    k, v = mmq.kv_read(b.pages, bad, b.start, b.length, 73, dtype=F32)
+    assert status() == 1
+    want = torch.from_numpy(ref.values(x.double().cpu().numpy())).float().to(DEV)
+    want[0] = 0
+    want[3 + 64:] = 0
+    assert torch.equal(k, want) and torch.equal(v, want)
+    bad[1, 1] = -7
+    mmq.kv_read(b.pages, bad, b.start, torch.tensor([3, 200], dtype=torch.int32, device=DEV), 73)
+    assert status() == 1
+
+
+def test_many_sequences_find_their_rows():
+    """Row to sequence over more sequences than a warp probes at once, some without rows."""
+    new = [(i * 7) % 4 for i in range(1500)]
+    length = [n + (i * 13) % 50 for i, n in enumerate(new)]
+    b = Batch(new, length, 1, 64, fill=False)
+    x = torch.randn(b.rows, 1, 64, device=DEV)
+    mmq.kv_write(x, 2 * x, *b.cache)
+    k, v = mmq.kv_read(*b.cache, b.rows, dtype=F32)
+    want = torch.from_numpy(ref.values(x.double().cpu().numpy())).float().to(DEV)
+    assert torch.equal(k, want) and torch.equal(v, 2 * want) and status() == 0
+
+
+def test_pool_past_32_bits():
+    heads, dim, num = 8, 128, 60000                          # 4.4 GB of pages
+    pages = mmq.kv_pages(num, heads, dim)
+    assert pages.numel() > 1 << 32
+    table = torch.tensor([[num - 1, 3, num - 2]], dtype=torch.int32, device=DEV)
+    start = torch.tensor([0, 150], dtype=torch.int32, device=DEV)
+    length = torch.tensor([150], dtype=torch.int32, device=DEV)
+    x = torch.randn(150, heads, dim, device=DEV)
+    mmq.kv_write(x, -x, pages, table, start, length)
+    k, v = mmq.kv_read(pages, table, start, length, 150, dtype=F32)
+    want = torch.from_numpy(ref.values(x.double().cpu().numpy())).to(DEV)
+    assert torch.equal(k.double(), want)
+    assert torch.equal(v.double(), torch.from_numpy(ref.values(-x.double().cpu().numpy())).to(DEV))
+    q = torch.randn(150, heads, dim, device=DEV)
+    out = mmq.kv_attend(q, pages, table, start, length, 150)
+    want, S = ref.attend(q.double(), want, v.double(), torch.arange(150, device=DEV), dim ** -0.5)
+    assert ((out.double() - want).abs() <= 2 ** -19 * (S + 1)[..., None] * v.abs().max() + 2.0 ** -25).all()
+    assert status() == 0
+
+
+# ----------------------------------------------------------------------------------------- attention
+STEP = [  # new, length, heads, kv heads, dim
+    ([1], [1], 1, 1, 128),
+    ([1], [64], 4, 4, 64),
+    ([1], [65], 8, 1, 128),
+    ([1, 1, 1], [63, 200, 1], 6, 2, 128),
+    ([1], [5000], 32, 8, 128),
+    ([3, 0, 5, 1], [3, 7, 700, 130], 10, 2, 64),
+    ([2], [4097], 48, 3, 128),
+    ([1] * 40, [1 + 97 * i for i in range(40)], 8, 8, 64),
+]
+PROMPT = [
+    ([65], [65], 2, 2, 128),
+    ([129, 1, 0, 300], [129, 64, 9, 1000], 6, 2, 128),
+    ([500], [511], 5, 1, 64),
+    ([1000], [1300], 4, 2, 128),
+    ([33, 257], [2000, 257], 16, 2, 64),
+]
+
+
+@pytest.mark.parametrize("dtype", [F32, F16, BF16])
+@pytest.mark.parametrize("new,length,heads,kv_heads,dim", STEP + PROMPT)
+def test_attention(new, length, heads, kv_heads, dim, dtype):
+    b = Batch(new, length, kv_heads, dim, dtype, seed=len(new) + heads)
+    q = b.q(heads)
+    b.check(q, mmq.kv_attend(q, *b.cache, max_q=max(new)))
+
+
+@pytest.mark.parametrize("dtype", [F32, F16])
+@pytest.mark.parametrize("window,sinks", [(1, 0), (1, 1), (64, 4), (65, 0), (100, 64), (100, 65), (700, 4),
+                                          (333, 200), (1 << 30, 3), (50, 1 << 30)])
+@pytest.mark.parametrize("new,length,heads,kv_heads,dim", [([1, 2], [1000, 64], 4, 1, 128), ([1], [3001], 4, 4, 64),
+                                                           ([400, 3], [900, 400], 4, 2, 128),
+                                                           ([300], [300], 8, 1, 64)])
+def test_window_and_first_tokens(new, length, heads, kv_heads, dim, window, sinks, dtype):
+    b = Batch(new, length, kv_heads, dim, dtype, seed=window % 97)
+    q = b.q(heads)
+    out = mmq.kv_attend(q, *b.cache, max_q=max(new), window=window, sinks=sinks)
+    b.check(q, out, window=window, sinks=sinks)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("new,length", [([5, 2], [3, 0]), ([200, 1], [100, 0]), ([1], [0])])
+def test_rows_that_see_no_key_are_zero(new, length, dtype):
+    b = Batch(new, length, 2, 64, dtype)
+    q = b.q(4)
+    out = mmq.kv_attend(q, *b.cache, max_q=max(new))
+    b.check(q, out)
+    assert (out[:new[0] - length[0]] == 0).all()
+
+
+@pytest.mark.parametrize("hint", [0, 1, 64, 5000, 1 << 30])
+def test_any_length_hint_is_right(hint):
+    b = Batch([1, 2], [5000, 100], 2, 128)
+    q = b.q(4)
+    b.check(q, mmq.kv_attend(q, *b.cache, max_q=2, max_kv=hint))
+
+
+@pytest.mark.parametrize("factor,scale", [(1e-30, 1e28), (1e25, 3e-26), (40.0, None), (0.0, None), (1.0, 1e-20)])
+@pytest.mark.parametrize("new,length", [([2], [300]), ([150], [300])])
+def test_queries_and_scales_of_any_size(new, length, factor, scale):
+    """Large logits (one key takes all the weight), zero queries, magnitudes far from 1."""
+    b = Batch(new, length, 1, 128)
+    q = b.q(4, factor=factor)
+    b.check(q, mmq.kv_attend(q, *b.cache, max_q=max(new), scale=scale), scale=scale)
+
+
+@pytest.mark.parametrize("new,length", [([2, 3], [300, 90]), ([150, 140], [300, 140])])
+def test_a_row_that_is_no_number_stays_alone(new, length):
+    b = Batch(new, length, 1, 64)
+    q = b.q(2)
+    clean = mmq.kv_attend(q, *b.cache, max_q=max(new))
+    q[1, 1, 7] = float("nan")
+    out = mmq.kv_attend(q, *b.cache, max_q=max(new))
+    assert torch.isnan(out[1, 1]).all()
+    out[1, 1] = clean[1, 1]
+    assert torch.equal(out, clean) and status() == 0
+
+
+@pytest.mark.parametrize("new,length", [([1], [700]), ([200], [700])])
+def test_keys_of_a_page_outside_the_pool_are_not_there(new, length):
+    b = Batch(new, length, 2, 128)
+    q = b.q(2)
+    table = b.table.clone()
+    table[0, 3] = 1 << 20
+    out = mmq.kv_attend(q, b.pages, table, b.start, b.length, max_q=max(new))
+    assert status() == 1 and status() == 0
+    k, v = b.held(0)
+    keep = torch.cat([torch.arange(0, 192), torch.arange(256, length[0])]).to(DEV)
+    # without page 3 later keys move up by 64, so do the positions that look at them
+    pos = torch.arange(length[0] - new[0], length[0], device=DEV) - 64
+    want, S = ref.attend(q.double(), k[keep], v[keep], pos, 128 ** -0.5)
+    assert ((out.double() - want).abs() <= 2 ** -19 * (S + 1)[..., None] * v.abs().max() + 2.0 ** -25).all()
+
+
+def test_length_past_the_table_is_reported():
+    b = Batch([1], [128], 1, 64)
+    q = b.q(1)
+    mmq.kv_attend(q, b.pages, b.table, b.start, b.length + 64, max_q=1)
+    assert status() == 1
+    b2 = Batch([40], [128], 1, 64)
+    mmq.kv_attend(b2.q(1), *b2.cache, max_q=1)               # more rows than the caller said
+    assert status() == 1
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("new,length", [([1, 1], [900, 65]), ([200, 30], [300, 64])])
+def test_strided_queries_and_results(new, length, dtype):
+    heads, dim = 6, 128
+    b = Batch(new, length, 2, dim, dtype)
+    q = b.q(heads)
+    plain = mmq.kv_attend(q, *b.cache, max_q=max(new))
+    for shift in (0, 1):
+        wide = torch.zeros(b.rows, 1200 + shift, device=DEV, dtype=dtype)
+        part = wide[:, 7 * 4 + shift:7 * 4 + shift + heads * dim].view(b.rows, heads, dim)
+        part.copy_(q)
+        out = torch.full((heads, b.rows, dim + shift), 5.0, device=DEV, dtype=dtype)
+        mmq.kv_attend(part, *b.cache, max_q=max(new), out=out[..., :dim].transpose(0, 1))
+        assert torch.equal(out[..., :dim].transpose(0, 1), plain)
+        assert (out[..., dim:] == 5.0).all()
+
+
+@pytest.mark.parametrize("new,length,heads", [([1], [20000], 8), ([1] * 9, [777] * 9, 4), ([300], [1500], 4)])
+def test_results_do_not_vary(new, length, heads):
+    b = Batch(new, length, 2, 128)
+    q = b.q(heads)
+    first = mmq.kv_attend(q, *b.cache, max_q=max(new))
+    for _ in range(5):
+        assert torch.equal(mmq.kv_attend(q, *b.cache, max_q=max(new)), first)
+    b.check(q, first)
+
+
+def test_other_streams_and_graphs():
+    """Work on a stream that is not the current one; a captured step replayed over new tokens."""
+    b = Batch([1, 1], [600, 90], 2, 128, spare=4)
+    q = b.q(4)
+    want = mmq.kv_attend(q, *b.cache, max_q=1)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    out = mmq.kv_attend(q, *b.cache, max_q=1, stream=side)
+    side.synchronize()
+    assert torch.equal(out, want)
+
+    k, v = (torch.randn(2, 2, 128, device=DEV) for _ in range(2))
+    warm = mmq.kv_attend(q, *b.cache, max_q=1)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        mmq.kv_write(k, v, *b.cache)
+        got = mmq.kv_attend(q, *b.cache, max_q=1)
+    del warm
+    for step in range(3):
+        b.length += 1
+        b.len = [m + 1 for m in b.len]
+        k.normal_()
+        v.normal_()
+        q.normal_()
+        for s in range(2):
+            b.k[s] = torch.cat([b.k[s], k[s:s + 1]])
+            b.v[s] = torch.cat([b.v[s], v[s:s + 1]])
+        graph.replay()
+        b.check(q, got)
+
+
+def test_a_prompt_and_its_tokens_one_by_one_agree():
+    """The same rows as one prompt, as chunks and as single tokens."""
+    n, heads = 260, 4
+    b = Batch([n], [n], 2, 64)
+    q = b.q(heads)
+    whole = mmq.kv_attend(q, *b.cache, max_q=n)
+    b.check(q, whole)
+    parts = []
+    for lo, hi in ((0, 1), (1, 2), (2, 9), (9, 140), (140, 259), (259, 260)):
+        start = torch.tensor([0, hi - lo], dtype=torch.int32, device=DEV)
+        length = torch.tensor([hi], dtype=torch.int32, device=DEV)
+        parts.append(mmq.kv_attend(q[lo:hi], b.pages, b.table, start, length, max_q=hi - lo))
+    b.check(q, torch.cat(parts))
