@@ -70,6 +70,8 @@ def lib_path() -> str:
 def load():
     """Load libmmq_gb300.so (raises if it has not been built)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -269,9 +271,17 @@ def mmq_version() -> str:
 # ----------------------------------------------------------------------------
 # Tensor helpers: PyTorch provides device memory and the current stream only.
 # ----------------------------------------------------------------------------
+_torch_module = None
+_ROW_TYPES = {}      # torch dtype -> mmq_dtype
+
+
 def _torch():
-    import torch
-    return torch
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _ROW_TYPES.update({getattr(torch, name): t for name, t in DTYPES.items()})
+        _torch_module = torch
+    return _torch_module
 
 
 def _stream(stream):
@@ -408,53 +418,81 @@ def kv_pages(num_pages, kv_heads, head_dim, device="cuda"):
 
 
 def _kv_cache(pages, table, start, length):
+    """The batch as a KVCache structure.  One chain of cheap checks for a right call (a decoding
+    step's time is the host's); a wrong one is told what is wrong."""
     torch = _torch()
-    i32, dev = torch.int32, pages.device
+    i32, dev = torch.int32, pages.get_device()
+    if (pages.dtype is torch.uint8 and pages.dim() == 3 and table.dtype is i32 and table.dim() == 2
+            and start.dtype is i32 and start.dim() == 1 and length.dtype is i32 and length.dim() == 1
+            and pages.is_contiguous() and table.is_contiguous() and start.is_contiguous() and length.is_contiguous()):
+        num_pages, kv_heads, piece = pages.shape
+        batch, max_pages = table.shape
+        if (piece % 72 == 0 and start.shape[0] == batch + 1 and length.shape[0] == batch
+                and dev >= 0 and dev == table.get_device() == start.get_device() == length.get_device()):
+            return KVCache(pages.data_ptr(), table.data_ptr(), start.data_ptr(), length.data_ptr(), num_pages,
+                           kv_heads, piece // 72, batch, max_pages), dev
     if pages.dtype != torch.uint8 or pages.dim() != 3 or not pages.is_contiguous() or pages.shape[2] % 72:
         raise ValueError("pages must be a contiguous uint8 [num_pages, kv_heads, 72 * head_dim] tensor")
     if table.dtype != i32 or table.dim() != 2 or not table.is_contiguous():
         raise ValueError("table must be a contiguous int32 [batch, max_pages] tensor")
-    batch, max_pages = table.shape
-    for x, n, name in ((start, batch + 1, "start"), (length, batch, "length")):
+    for x, n, name in ((start, table.shape[0] + 1, "start"), (length, table.shape[0], "length")):
         if x.dtype != i32 or x.shape != (n,) or not x.is_contiguous():
             raise ValueError(f"{name} must be a contiguous int32 [{n}] tensor")
-    if not pages.is_cuda or not (dev == table.device == start.device == length.device):
-        raise ValueError("pages, table, start and length must be CUDA tensors on one device")
-    return KVCache(pages.data_ptr(), table.data_ptr(), start.data_ptr(), length.data_ptr(), pages.shape[0],
-                   pages.shape[1], pages.shape[2] // 72, batch, max_pages)
+    raise ValueError("pages, table, start and length must be CUDA tensors on one device")
 
 
-def _kv_rows(x, shape, cache_device, name):
-    if x.dim() != 3 or tuple(x.shape) != shape or x.stride(2) != 1:
-        raise ValueError(f"{name} must be {list(shape)} with unit stride in its last dimension, got {list(x.shape)}")
-    t = DTYPES.get(str(x.dtype)[6:])
+def _kv_rows(x, rows, heads, dim, dev, name):
+    t = _ROW_TYPES.get(x.dtype)
+    if t is not None and x.shape == (rows, heads, dim) and x.get_device() == dev:
+        st, sh, sd = x.stride()
+        if sd == 1:
+            return Rows(x.data_ptr(), t, st, sh)
     if t is None:
         raise ValueError(f"{name} must be float32, float16 or bfloat16, got {x.dtype}")
-    if x.device != cache_device:
+    if x.get_device() != dev:
         raise ValueError(f"{name} must be on the cache's device")
-    return Rows(x.data_ptr(), t, x.stride(0), x.stride(1))
+    raise ValueError(f"{name} must be {[rows, heads, dim]} with unit stride in its last dimension, got {list(x.shape)} "
+                     f"with strides {list(x.stride())}")
+
+
+def _kv_stream(stream, dev):
+    """Handle of the given or the device's current stream."""
+    return _torch()._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+
+
+def _kv_empty(shape, dtype, device, stream):
+    """Memory that belongs to the stream that uses it."""
+    torch = _torch()
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
 
 
 def kv_write(k, v, pages, table, start, length, stream=None):
     """Quantise the new tokens' k and v ([rows, kv_heads, head_dim], any token and head strides)
     into the cache."""
-    c = _kv_cache(pages, table, start, length)
-    shape = (k.shape[0], c.kv_heads, c.head_dim)
-    mmq_kv_write(c, _kv_rows(k, shape, pages.device, "k"), _kv_rows(v, shape, pages.device, "v"), shape[0],
-                 _stream(stream))
+    c, dev = _kv_cache(pages, table, start, length)
+    rows, hk, dim = k.shape[0], c.kv_heads, c.head_dim
+    st = load().mmq_kv_write(c, _kv_rows(k, rows, hk, dim, dev, "k"), _kv_rows(v, rows, hk, dim, dev, "v"), rows,
+                             _kv_stream(stream, dev) or None)
+    if st:
+        raise MMQError(st, "kv_write")
 
 
 def kv_read(pages, table, start, length, rows, dtype=None, k=None, v=None, stream=None):
     """(k, v) [rows, kv_heads, head_dim] that the cache holds for the packed rows, in dtype
     (float16 unless given) or into given k and v."""
-    torch = _torch()
-    c = _kv_cache(pages, table, start, length)
-    shape = (rows, c.kv_heads, c.head_dim)
-    with torch.cuda.stream(stream):       # a result belongs to the stream that writes it
-        k = torch.empty(shape, dtype=dtype or torch.float16, device=pages.device) if k is None else k
-        v = torch.empty(shape, dtype=k.dtype, device=pages.device) if v is None else v
-    mmq_kv_read(c, _kv_rows(k, shape, pages.device, "k"), _kv_rows(v, shape, pages.device, "v"), rows,
-                _stream(stream))
+    c, dev = _kv_cache(pages, table, start, length)
+    hk, dim = c.kv_heads, c.head_dim
+    if k is None:
+        k = _kv_empty((rows, hk, dim), dtype or _torch().float16, pages.device, stream)
+    if v is None:
+        v = _kv_empty((rows, hk, dim), k.dtype, pages.device, stream)
+    st = load().mmq_kv_read(c, _kv_rows(k, rows, hk, dim, dev, "k"), _kv_rows(v, rows, hk, dim, dev, "v"), rows,
+                            _kv_stream(stream, dev) or None)
+    if st:
+        raise MMQError(st, "kv_read")
     return k, v
 
 
@@ -463,24 +501,30 @@ def kv_attend(q, pages, table, start, length, max_q, max_kv=None, scale=None, wi
     """Attention of q [rows, heads, head_dim] over the cache.  max_q: at least the most new tokens
     of a sequence; max_kv: about the longest length (all of the table unless given); scale:
     head_dim ** -0.5 unless given; window 0: none."""
-    torch = _torch()
-    c = _kv_cache(pages, table, start, length)
+    c, dev = _kv_cache(pages, table, start, length)
     rows, heads = q.shape[:2]
-    shape = (rows, heads, c.head_dim)
+    dim = c.head_dim
     if max_kv is None:
         max_kv = c.max_pages * KV_PAGE
     if scale is None:
-        scale = c.head_dim ** -0.5
-    rq = _kv_rows(q, shape, pages.device, "q")
-    need = mmq_kv_attend_workspace_bytes(c, rq.dtype, heads, rows, max_q, max_kv, window, sinks)
-    with torch.cuda.stream(stream):
-        if out is None:
-            out = torch.empty(shape, dtype=q.dtype, device=q.device)
-        if need and workspace is None:
-            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-    if need and (not workspace.is_cuda or workspace.device != q.device or not workspace.is_contiguous()
-                 or _nbytes(workspace) < need):
-        raise ValueError(f"workspace must be a contiguous CUDA buffer of at least {need} bytes")
-    mmq_kv_attend(c, rq, _kv_rows(out, shape, pages.device, "out"), heads, rows, max_q, max_kv, scale, window, sinks,
-                  workspace.data_ptr() if need else 0, need, _stream(stream))
+        scale = dim ** -0.5
+    rq = _kv_rows(q, rows, heads, dim, dev, "q")
+    lib, size = load(), ctypes.c_size_t()
+    st = lib.mmq_kv_attend_workspace_bytes(c, rq.dtype, heads, rows, max_q, max_kv, window, sinks, size)
+    if st:
+        raise MMQError(st, "kv_attend")
+    need, at = size.value, None
+    if out is None:
+        out = _torch().empty_like(q) if stream is None and q.is_contiguous() else _kv_empty(
+            (rows, heads, dim), q.dtype, q.device, stream)
+    if need:
+        if workspace is None:
+            workspace = _kv_empty((need,), _torch().uint8, q.device, stream)
+        elif workspace.get_device() != dev or not workspace.is_contiguous() or _nbytes(workspace) < need:
+            raise ValueError(f"workspace must be a contiguous CUDA buffer of at least {need} bytes")
+        at = workspace.data_ptr()
+    st = lib.mmq_kv_attend(c, rq, _kv_rows(out, rows, heads, dim, dev, "out"), heads, rows, max_q, max_kv, scale,
+                           window, sinks, at, need, _kv_stream(stream, dev) or None)
+    if st:
+        raise MMQError(st, "kv_attend")
     return out

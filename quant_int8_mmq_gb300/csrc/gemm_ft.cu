@@ -343,21 +343,6 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint4 (&v)[4])
         "r"(v[2].x), "r"(v[2].y), "r"(v[2].z), "r"(v[2].w), "r"(v[3].x), "r"(v[3].y), "r"(v[3].z), "r"(v[3].w)
         : "memory");
 }
-__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-
-// D[tmem] (+)= A[tmem] * B[smem]^T, one 128 x N x 16 kind::f16 step (A: 128 lanes x 8
-// columns, each 32-bit column two consecutive K values), issued by one thread.
-__device__ __forceinline__ void umma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
-                                            uint32_t accumulate)
-{
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d_tmem),
-        "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
-        : "memory");
-}
-
 // Work unit u: weight tile n and its super-block range; stage st of the unit covers
 // k-blocks [4*sb0 + st*KPS, +KPS).  Stages are numbered across the CTA's units (g);
 // stage g goes to issuer g % 2 and accumulator item g % ITEMS, its super-block's

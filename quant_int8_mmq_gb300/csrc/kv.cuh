@@ -11,6 +11,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <atomic>
 #include <cstdint>
 
 #include "mmq.h"
@@ -21,6 +22,8 @@ namespace mmq {
 
 constexpr int KV_PAGE = MMQ_KV_PAGE;   // tokens per page
 constexpr int KV_GROUP = 32;           // values per scale
+constexpr int KV_STEP_ROWS = 8;        // rows of a kv_step.cu tile
+constexpr int KV_PROMPT_ROWS = 256;    // rows of a kv_prompt.cu CTA
 
 // Byte offsets inside a piece of head size D; the documented layout is in mmq.h.
 template <int D>
@@ -134,6 +137,28 @@ __device__ __forceinline__ void store4(T* p, float4 v, bool wide)
     }
 }
 
+__device__ __forceinline__ float kv_ex2(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// x = hi + lo in f16 (22 bits) for two values
+__device__ __forceinline__ void kv_split2(float x, float y, uint32_t& hi, uint32_t& lo)
+{
+    const __half2 h = __floats2half2_rn(x, y);
+    const float2 f = __half22float2(h);
+    hi = kv_h2u(h);
+    lo = kv_h2u(__floats2half2_rn(x - f.x, y - f.y));
+}
+
+// Softmax weights p = 2^(x - ref) are kept in f16 halves.  A fresh reference is 7 below the
+// row's largest x and stands until some x is 15 above it, so p is at most 2^15, rows are
+// rescaled rarely, and what 2^7 is to the largest p, f16's least step 2^-24 is to the least.
+constexpr float KV_REF_BELOW = 7.0f;
+constexpr float KV_REF_LIMIT = 15.0f;
+
 // The sequence of packed row r: the last b with start[b] <= r, found by one warp, 32
 // probes a step (sequences without rows are passed over).  0 <= result < batch whatever
 // start holds.
@@ -152,6 +177,23 @@ __device__ __forceinline__ int kv_sequence_of(const int* start, int batch, int r
 }
 
 // ------------------------------------------------------------------ launchers
+// Lets `kernel` use `bytes` of dynamic shared memory, once per device (a bit of `done` each).
+template <typename K>
+cudaError_t kv_allow_smem(K* kernel, int bytes, std::atomic<uint64_t>* done)
+{
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess)
+        return e;
+    const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+    if (done->load(std::memory_order_acquire) & bit)
+        return cudaSuccess;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess)
+        done->fetch_or(bit, std::memory_order_release);
+    return e;
+}
+
 enum KvType { KV_F32 = 0, KV_F16 = 1, KV_BF16 = 2 };
 
 cudaError_t launch_kv_write(const KvView& c, int dim, int dtype, const KvRows& k, const KvRows& v, bool wide,
@@ -167,7 +209,7 @@ struct AttendArgs {
     int ntok;
     float scale_log2;      // softmax scale times log2(e)
     int window, sinks;
-    int row_tiles;         // row tiles per (sequence, kv head)
+    int row_tiles;         // kv_step.cu: row tiles per (sequence, kv head); kv_prompt.cu: of the whole batch
     int nsplit;            // parts of the visible pages
     bool wide;
     float* part;           // nsplit > 1: [nsplit][ntok * heads][D] unnormalised sums
@@ -176,7 +218,7 @@ struct AttendArgs {
 };
 
 struct AttendPlan {
-    int kernel;      // 0: few rows per sequence
+    int kernel;      // 0: kv_step.cu, 1: kv_prompt.cu
     int row_tiles;
     int nsplit;
     size_t part_bytes, ml_bytes;
@@ -184,6 +226,7 @@ struct AttendPlan {
 AttendPlan plan_attend(int dtype, int heads, int kv_heads, int dim, int batch, int ntok, int max_q, int max_kv,
                        int window, int sinks);
 cudaError_t launch_kv_step(const AttendArgs& a, int dim, int dtype, cudaStream_t s);
+cudaError_t launch_kv_prompt(const AttendArgs& a, int dim, int dtype, cudaStream_t s);
 cudaError_t launch_kv_join(const AttendArgs& a, int dim, int dtype, cudaStream_t s);
 
 }  // namespace mmq

@@ -7,12 +7,13 @@
 
 namespace mmq {
 
-// How an attention call is cut up.  Target CTAs: two of the few-row kernel's fit an SM of
-// the chip's 152, and parts of the pages below one page per warp gain nothing.
+// How an attention call is cut up: rows to row tiles and, where those are few, the visible
+// pages to parts.  Depends on the arguments alone (the chip has 152 SMs).
 AttendPlan plan_attend(int dtype, int heads, int kv_heads, int dim, int batch, int ntok, int max_q, int max_kv,
                        int window, int sinks)
 {
     (void)dtype;
+    constexpr int SMS = 152;
     AttendPlan p = {};
     const int group = heads / kv_heads;
     max_q = max_q < ntok ? max_q : ntok;
@@ -21,16 +22,30 @@ AttendPlan plan_attend(int dtype, int heads, int kv_heads, int dim, int batch, i
         const long long seen = (static_cast<long long>(window) + max_q + sinks) / KV_PAGE + 3;
         pages = pages < seen ? pages : seen;
     }
-    p.row_tiles = static_cast<int>((static_cast<long long>(max_q) * group + 7) / 8);
-    const long long units = static_cast<long long>(batch) * kv_heads * p.row_tiles;
-    long long nsplit = (2 * 152 + units - 1) / units;
-    const long long most = (pages + 3) / 4;
+    const long long rows = static_cast<long long>(max_q) * group;
+    p.kernel = rows > 64 ? 1 : 0;
+    long long units, most, slots;
+    if (p.kernel == 0) {
+        p.row_tiles = static_cast<int>((rows + KV_STEP_ROWS - 1) / KV_STEP_ROWS);
+        units = static_cast<long long>(batch) * kv_heads * p.row_tiles;
+        slots = 2 * SMS;            // two CTAs an SM
+        most = (pages + 3) / 4;     // a page per warp at least
+    } else {
+        // sum over the sequences of ceil(rows / KV_PROMPT_ROWS), or more
+        const long long tiles =
+            static_cast<long long>(ntok) * group / KV_PROMPT_ROWS + (batch < ntok ? batch : ntok);
+        p.row_tiles = static_cast<int>(tiles < 0x7fffffffll ? tiles : 0x7fffffffll);
+        units = tiles * kv_heads;
+        slots = SMS;
+        most = (pages + 7) / 8;
+    }
+    long long nsplit = slots / units;
     nsplit = nsplit < most ? nsplit : most;
     p.nsplit = static_cast<int>(nsplit < 1 ? 1 : nsplit);
     if (p.nsplit > 1) {
-        const size_t rows = static_cast<size_t>(p.nsplit) * ntok * heads;
-        p.part_bytes = rows * dim * sizeof(float);
-        p.ml_bytes = rows * sizeof(float2);
+        const size_t flat = static_cast<size_t>(p.nsplit) * ntok * heads;
+        p.part_bytes = flat * dim * sizeof(float);
+        p.ml_bytes = (flat * sizeof(float2) + 15) / 16 * 16;
     }
     return p;
 }
@@ -210,7 +225,7 @@ mmq_status mmq_kv_attend(const mmq_kv_cache* c, const mmq_rows* q, const mmq_row
         if (!aligned(workspace, 16))
             return MMQ_ERR_ALIGN;
     }
-    if (static_cast<long long>(p.nsplit) * p.row_tiles * c->kv_heads * c->batch > 0x7fffffffll ||
+    if (static_cast<long long>(p.nsplit) * p.row_tiles * c->kv_heads * (p.kernel == 0 ? c->batch : 1) > 0x7fffffffll ||
         static_cast<long long>(ntok) * heads > 0x7fffffffll)
         return MMQ_ERR_SHAPE;
     if ((st = mmq::check_device()) != MMQ_OK)
@@ -232,7 +247,8 @@ mmq_status mmq_kv_attend(const mmq_kv_cache* c, const mmq_rows* q, const mmq_row
     a.part = static_cast<float*>(workspace);
     a.part_ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(workspace) + p.part_bytes);
     a.wc = {a.c.bad - 1, mmq::WAIT_LIMIT_NS, -1};
-    cudaError_t e = mmq::launch_kv_step(a, c->head_dim, q->dtype, reinterpret_cast<cudaStream_t>(s));
+    const auto launch = p.kernel == 0 ? mmq::launch_kv_step : mmq::launch_kv_prompt;
+    cudaError_t e = launch(a, c->head_dim, q->dtype, reinterpret_cast<cudaStream_t>(s));
     if (e == cudaSuccess && p.nsplit > 1)
         e = mmq::launch_kv_join(a, c->head_dim, q->dtype, reinterpret_cast<cudaStream_t>(s));
     return mmq::from_cuda(e);

@@ -1,0 +1,632 @@
+// kv_prompt.cu -- attention over the 4-bit cache for many rows per sequence: prompts and
+// their chunks, on the tensor cores.
+//
+//   S = Q K^T,  P = 2^(scale log2(e) S - ref),  O += P V,  o = O / sum P
+//
+// A CTA takes 256 rows (a row is a query token and one of the heads that share the kv
+// head) as two tiles of 128 TMEM lanes, and walks the visible pages 128 keys at a time.
+// The cached values are widened to f16, exactly, by one warpgroup for both tiles: K as
+// [key][value] and V transposed as [value][key], the K-major operand tiles of the two
+// products.  Q is scaled per row by a power of two and split q = hi + lo in f16, P
+// likewise: f32 rows use both parts (four products a tile, 22-bit operands), 16-bit rows
+// are exact in hi (bf16 to 2^-24 of the row's largest) and round P to f16.
+//
+// TMEM: S of each tile in 128 columns, its P (hi, lo) over the S that it came from, O in
+// D columns.  The tiles alternate on the tensor pipe, P V and the next Q K^T of one
+// while the other's softmax runs: a thread per row reads S, keeps the row's reference and
+// sum, and writes P.  A row's O is rescaled only when its reference moves, which the
+// lag of kv.cuh makes rare, by the softmax thread itself: its S arrived behind the last
+// P V of the tile, so O is at rest.
+//
+// 16 warps: warp 0 issues the MMAs, warp 1 copies the pages' bytes into a ring, warps 4-7
+// widen, warps 8-11 and 12-15 are the softmax of tiles 0 and 1.  Every wait is bounded; on
+// expiry the roles leave their loops, copies and MMAs in flight are waited for, TMEM is
+// freed and the CTA ends.
+#include "kv.cuh"
+
+namespace mmq {
+namespace {
+
+constexpr int THREADS = 512;
+constexpr int TILE = 128;                    // rows of a tile, keys of a step
+constexpr int ROWS = KV_PROMPT_ROWS;
+static_assert(ROWS == 2 * TILE, "two tiles");
+constexpr int WIDEN_WARP = 4, SOFT_WARP = 8;
+// The launch's 128 registers a thread, shared out by warpgroup.
+constexpr int LAUNCH_REGS = 128, CTRL_REGS = 48, WIDEN_REGS = 96, SOFT_REGS = 184;
+static_assert(CTRL_REGS + WIDEN_REGS + 2 * SOFT_REGS == 4 * LAUNCH_REGS, "register split");
+constexpr int META = 8;   // steps whose page descriptions are kept: more than any role runs ahead
+
+// HL: hi and lo parts of Q and P.
+template <int D, bool HL>
+struct Cfg {
+    static constexpr int KB = D / 64;                            // 64-value blocks of a row
+    static constexpr int PARTS = HL ? 2 : 1;
+    static constexpr int BLOCK = TILE * 128;                     // 128 rows x 64 f16
+    static constexpr int Q_BYTES = 2 * PARTS * KB * BLOCK;       // [tile][part][kb]
+    static constexpr int K_BYTES = KB * BLOCK;                   // [kb][key]
+    static constexpr int V_BYTES = 2 * D * 128;                  // [64 keys][value]
+    static constexpr int BUFS = HL && D == 128 ? 1 : 2;          // buffers of each
+    static constexpr int HALF = 36 * D;                          // bytes of a piece's K or V
+    static constexpr int STAGE = 2 * HALF;                       // K or V of two pages
+    static constexpr int STAGES = D == 128 ? 3 : 4;
+    static constexpr int Q = 0;
+    static constexpr int K = Q + Q_BYTES;
+    static constexpr int V = K + BUFS * K_BYTES;
+    static constexpr int RING = V + BUFS * V_BYTES;
+    static constexpr int META_AT = RING + STAGES * STAGE;        // int2 [META]: tokens held of each page, -1 no page
+    static constexpr int BAR = META_AT + META * 8;
+    enum { QFULL, RFULL, REMPTY = RFULL + STAGES, KFULL = REMPTY + STAGES, KEMPTY = KFULL + BUFS,
+           VFULL = KEMPTY + BUFS, VEMPTY = VFULL + BUFS, SFULL = VEMPTY + BUFS, PFULL = SFULL + 2,
+           OFULL = PFULL + 2, DRAIN = OFULL + 2, NBAR };
+    static constexpr int TMEM_AT = BAR + NBAR * 8;
+    static constexpr int UNIT_AT = TMEM_AT + 4;                  // int: sequence, tile
+    static constexpr int BYTES = UNIT_AT + 12 + 1024;            // and the alignment to 1024
+    static_assert(BYTES <= 227 * 1024, "shared memory");
+    static_assert(K % 1024 == 0 && V % 1024 == 0 && RING % 16 == 0 && META_AT % 8 == 0, "alignment");
+};
+
+constexpr uint32_t S_COL = 0, O_COL = 256;   // tile w: S at 128 w, O at 256 + D w
+
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&v)[32])
+{
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+        "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,"
+        "%30,%31,%32};\n" ::"r"(taddr),
+        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+        "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(v[16]), "r"(v[17]), "r"(v[18]),
+        "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]),
+        "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
+        : "memory");
+}
+
+// What a CTA works on; the same in every thread.
+struct Unit {
+    int b, head, split, first, row0, nrow;   // rows row0 .. row0 + nrow - 1 of sequence b's
+    long long pos0;                          // position of the sequence's first new token
+    int kend, nsink, page_lo, npage;         // keys [0, kend); pages 0 .. nsink - 1, page_lo ..
+    int i0, steps;                           // first page of this split's and its 128-key steps
+};
+__device__ __forceinline__ int page_of(const Unit& u, int i) { return i < u.nsink ? i : u.page_lo + i - u.nsink; }
+
+__device__ __forceinline__ bool wait(const AttendArgs& g, uint32_t bar, uint32_t parity)
+{
+    return mbar_wait(bar, parity, g.wc.limit_ns, g.wc.err);
+}
+__device__ __forceinline__ bool warp_wait(const AttendArgs& g, uint32_t bar, uint32_t parity)
+{
+    return __all_sync(0xffffffffu, wait(g, bar, parity));
+}
+
+// Which keys of a page (64 from kbase on) a row at position pos sees, one bit each.
+__device__ __forceinline__ uint64_t seen_bits(long long pos, long long kbase, int window, int sinks)
+{
+    const int to = static_cast<int>(min(max(pos - kbase, -1ll), 63ll));
+    uint64_t m = to < 0 ? 0 : ~0ull >> (63 - to);
+    if (window > 0) {
+        const int from = static_cast<int>(min(max(pos - window + 1 - kbase, 0ll), 64ll));
+        const int sink = static_cast<int>(min(max(sinks - kbase, 0ll), 64ll));
+        m &= (from < 64 ? ~0ull << from : 0) | (sink > 0 ? ~0ull >> (64 - sink) : 0);
+    }
+    return m;
+}
+
+template <int D, typename T>
+__global__ void __launch_bounds__(THREADS, 1) kv_prompt_kernel(const AttendArgs g)
+{
+    constexpr bool HL = sizeof(T) == 4;
+    using C = Cfg<D, HL>;
+    using P = Piece<D>;
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw = smem_u32(smem_raw), pad = (1024u - (raw & 1023u)) & 1023u;
+    uint8_t* smem = smem_raw + pad;
+    const uint32_t sbase = raw + pad;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    auto bar = [&](int i) -> uint32_t { return sbase + C::BAR + 8u * static_cast<uint32_t>(i); };
+
+    grid_dep_wait();
+    // ---------------------------------------------------------------- the unit
+    // blocks run from the last row tile of the batch to the first (a sequence's later tiles
+    // see more keys), all heads and splits of a tile together
+    Unit u;
+    int id = blockIdx.x;
+    u.split = id % g.nsplit;
+    id /= g.nsplit;
+    u.head = id % g.c.kv_heads;
+    id /= g.c.kv_heads;
+    {
+        // sequence b has ceil(rows / 256) tiles; the warp sums 32 sequences at a time
+        const int want = g.row_tiles - 1 - id;
+        int before = 0;
+        u.b = -1;
+        u.row0 = 0;
+        for (int b0 = 0; b0 < g.c.batch; b0 += 32) {
+            int tiles = 0;
+            if (b0 + lane < g.c.batch) {
+                const int s = g.c.start[b0 + lane], e = g.c.start[b0 + lane + 1];
+                if (s >= 0 && e > s && e <= g.ntok)
+                    tiles = static_cast<int>((static_cast<long long>(e - s) * g.group + ROWS - 1) / ROWS);
+            }
+            int sum = tiles;
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const int v = __shfl_up_sync(0xffffffffu, sum, d);
+                sum += lane >= d ? v : 0;
+            }
+            const uint32_t here = __ballot_sync(0xffffffffu, want < before + sum);
+            if (here) {
+                const int l = __ffs(here) - 1;
+                u.b = b0 + l;
+                u.row0 = (want - before - __shfl_sync(0xffffffffu, sum - tiles, l)) * ROWS;
+                break;
+            }
+            before += __shfl_sync(0xffffffffu, sum, 31);
+        }
+    }
+    if (u.b < 0)
+        return;   // fewer tiles than the host's bound
+    u.first = g.c.start[u.b];
+    const int ntok = g.c.start[u.b + 1] - u.first;
+    u.nrow = min(ROWS, ntok * g.group - u.row0);
+    u.pos0 = static_cast<long long>(g.c.length[u.b]) - ntok;
+    {
+        const long long room = static_cast<long long>(g.c.max_pages) * KV_PAGE;
+        const long long plo = u.pos0 + u.row0 / g.group, phi = u.pos0 + (u.row0 + u.nrow - 1) / g.group;
+        u.kend = static_cast<int>(min(max(phi + 1, 0ll), room));
+        if (threadIdx.x == 0 && phi + 1 > room)
+            *g.c.bad = 1u;
+        const int klo =
+            g.window > 0 ? static_cast<int>(min(max(plo - g.window + 1, 0ll), static_cast<long long>(u.kend))) : 0;
+        u.page_lo = klo / KV_PAGE;
+        u.nsink = min((min(g.sinks, u.kend) + KV_PAGE - 1) / KV_PAGE, u.page_lo);
+        u.npage = u.nsink + (u.kend + KV_PAGE - 1) / KV_PAGE - u.page_lo;
+        const int per = ((u.npage + 1) / 2 + g.nsplit - 1) / g.nsplit;   // steps of a split
+        u.i0 = 2 * per * u.split;
+        u.steps = max(0, min(per, (u.npage - u.i0 + 1) / 2));
+    }
+    const bool two = u.nrow > TILE;
+
+    // ---------------------------------------------------------------- setup
+    if (threadIdx.x == 0) {
+        mbar_init(bar(C::QFULL), 8);
+        for (int i = 0; i < C::STAGES; ++i) {
+            mbar_init(bar(C::RFULL + i), 1);
+            mbar_init(bar(C::REMPTY + i), 4);
+        }
+        for (int i = 0; i < C::BUFS; ++i) {
+            mbar_init(bar(C::KFULL + i), 4);
+            mbar_init(bar(C::KEMPTY + i), 1);
+            mbar_init(bar(C::VFULL + i), 4);
+            mbar_init(bar(C::VEMPTY + i), 1);
+        }
+        for (int w = 0; w < 2; ++w) {
+            mbar_init(bar(C::SFULL + w), 1);
+            mbar_init(bar(C::PFULL + w), 4);
+            mbar_init(bar(C::OFULL + w), 1);
+        }
+        mbar_init(bar(C::DRAIN), 1);
+        fence_barrier_init();
+    }
+    if (warp == 0) {
+        tmem_alloc(sbase + C::TMEM_AT, 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *reinterpret_cast<const uint32_t*>(smem + C::TMEM_AT);
+
+    if (warp < WIDEN_WARP) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(CTRL_REGS));
+        if (warp == 0 && lane == 0) {
+            // -------------------------------------------------------- MMA issue
+            constexpr uint32_t qk = idesc_f16_f32(TILE, TILE), pv = idesc_f16_f32(TILE, D);
+            auto product_qk = [&](int w, int buf) {
+#pragma unroll
+                for (int part = 0; part < C::PARTS; ++part)
+#pragma unroll
+                    for (int kb = 0; kb < C::KB; ++kb) {
+                        const uint64_t a =
+                            sdesc_k_sw128(sbase + C::Q + ((w * C::PARTS + part) * C::KB + kb) * C::BLOCK);
+                        const uint64_t b = sdesc_k_sw128(sbase + C::K + buf * C::K_BYTES + kb * C::BLOCK);
+#pragma unroll
+                        for (int kk = 0; kk < 4; ++kk)
+                            umma_f16(tmem + S_COL + TILE * w, a + 2u * kk, b + 2u * kk, qk, (part | kb | kk) ? 1u : 0u);
+                    }
+                umma_commit(bar(C::SFULL + w));
+            };
+            auto product_pv = [&](int w, int buf, bool add) {
+#pragma unroll
+                for (int part = 0; part < C::PARTS; ++part)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const uint64_t b = sdesc_k_sw128(sbase + C::V + buf * C::V_BYTES + h * D * 128);
+#pragma unroll
+                        for (int kk = 0; kk < 4; ++kk)
+                            umma_f16_ts(tmem + O_COL + D * w, tmem + S_COL + TILE * w + 64 * part + 32 * h + 8 * kk,
+                                        b + 2u * kk, pv, (part | h | kk || add) ? 1u : 0u);
+                    }
+            };
+            const int tiles = two ? 2 : 1;
+            bool ok = u.steps == 0 || (wait(g, bar(C::QFULL), 0) && wait(g, bar(C::KFULL), 0));
+            if (ok && u.steps > 0) {
+                tc_fence_after();
+                for (int w = 0; w < tiles; ++w)
+                    product_qk(w, 0);
+                umma_commit(bar(C::KEMPTY));
+            }
+            for (int j = 0; ok && j < u.steps; ++j) {
+                const int buf = j % C::BUFS, next = (j + 1) % C::BUFS;
+                for (int w = 0; ok && w < tiles; ++w) {
+                    ok = wait(g, bar(C::PFULL + w), j & 1) && (w > 0 || wait(g, bar(C::VFULL + buf), j / C::BUFS & 1));
+                    if (!ok)
+                        break;
+                    tc_fence_after();
+                    product_pv(w, buf, j > 0);
+                    if (w == tiles - 1)
+                        umma_commit(bar(C::VEMPTY + buf));
+                    if (j + 1 == u.steps) {
+                        umma_commit(bar(C::OFULL + w));
+                        continue;
+                    }
+                    ok = w > 0 || wait(g, bar(C::KFULL + next), (j + 1) / C::BUFS & 1);
+                    if (!ok)
+                        break;
+                    tc_fence_after();
+                    product_qk(w, next);
+                    if (w == tiles - 1)
+                        umma_commit(bar(C::KEMPTY + next));
+                }
+            }
+            umma_commit(bar(C::DRAIN));   // nothing of this CTA's is left on the tensor pipe
+            mbar_drain_wait(bar(C::DRAIN), 0, WAIT_LIMIT_NS, g.wc.err);
+        } else if (warp == 1) {
+            // -------------------------------------------------------- page bytes: K, V of each step
+            const int* table = g.c.table + static_cast<size_t>(u.b) * g.c.max_pages;
+            int ids = -1, count = 0;
+            for (int j = 0; j < u.steps; ++j) {
+                if (j % 16 == 0) {   // 32 page ids at a time, one per lane
+                    const int i = u.i0 + 2 * j + lane;
+                    ids = -1;
+                    if (i < u.npage) {
+                        ids = table[page_of(u, i)];
+                        if (ids < 0 || ids >= g.c.num_pages) {
+                            *g.c.bad = 1u;
+                            ids = -1;
+                        }
+                    }
+                }
+                const int p0 = __shfl_sync(0xffffffffu, ids, j % 16 * 2);
+                const int p1 = __shfl_sync(0xffffffffu, ids, j % 16 * 2 + 1);
+                bool ok = true;
+#pragma unroll
+                for (int kv = 0; kv < 2; ++kv, ++count) {
+                    const int stage = count % C::STAGES;
+                    ok = warp_wait(g, bar(C::REMPTY + stage), (count / C::STAGES & 1) ^ 1);
+                    if (!ok)
+                        break;
+                    if (lane == 0) {
+                        int2* meta = reinterpret_cast<int2*>(smem + C::META_AT) + j % META;
+                        if (kv == 0) {
+                            const int i = u.i0 + 2 * j;
+                            const int h0 = u.kend - page_of(u, i) * KV_PAGE, h1 = u.kend - page_of(u, i + 1) * KV_PAGE;
+                            *meta = make_int2(p0 < 0 ? -1 : min(h0, KV_PAGE), p1 < 0 ? -1 : min(h1, KV_PAGE));
+                        }
+                        fence_proxy_async_smem();   // the stage was read with ordinary loads
+                        mbar_arrive_expect_tx(bar(C::RFULL + stage), ((p0 >= 0) + (p1 >= 0)) * C::HALF);
+                        const uint32_t dst = sbase + C::RING + stage * C::STAGE;
+                        const size_t piece = static_cast<size_t>(g.c.kv_heads) * P::BYTES;
+                        const uint8_t* src = g.c.pages + static_cast<size_t>(u.head) * P::BYTES + kv * C::HALF;
+                        if (p0 >= 0)
+                            bulk_g2s(dst, src + p0 * piece, C::HALF, bar(C::RFULL + stage));
+                        if (p1 >= 0)
+                            bulk_g2s(dst + C::HALF, src + p1 * piece, C::HALF, bar(C::RFULL + stage));
+                    }
+                }
+                if (!ok)
+                    break;
+            }
+            if (lane == 0)   // the last fill of each stage lands before the CTA ends
+                for (int i = max(0, count - C::STAGES); i < count; ++i)
+                    mbar_drain_wait(bar(C::RFULL + i % C::STAGES), i / C::STAGES & 1, WAIT_LIMIT_NS, g.wc.err);
+        }
+        __syncwarp();
+    } else if (warp < SOFT_WARP) {
+        // ------------------------------------------------------------ widening
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(WIDEN_REGS));
+        const int t = threadIdx.x - WIDEN_WARP * 32;
+        int count = 0;
+        bool ok = true;
+        for (int j = 0; ok && j < u.steps; ++j) {
+            const int buf = j % C::BUFS;
+            const uint32_t empty = (j / C::BUFS & 1) ^ 1;
+            {   // K: a thread per key
+                const int stage = count % C::STAGES;
+                ok = warp_wait(g, bar(C::RFULL + stage), count / C::STAGES & 1) &&
+                     warp_wait(g, bar(C::KEMPTY + buf), empty);
+                if (!ok)
+                    break;
+                const int2 held = reinterpret_cast<const int2*>(smem + C::META_AT)[j % META];
+                const bool there = (t < KV_PAGE ? held.x : held.y) >= 0;
+                const uint8_t* src = smem + C::RING + stage * C::STAGE + t / KV_PAGE * C::HALF;
+                uint8_t* dst = smem + C::K + buf * C::K_BYTES + t * 128;
+#pragma unroll
+                for (int gr = 0; gr < P::NG; ++gr) {
+                    const uint4 v = *reinterpret_cast<const uint4*>(src + P::k_chunk(t % KV_PAGE, gr));
+                    const __half2 s = __half2half2(
+                        *reinterpret_cast<const __half*>(src + P::k_scale(t % KV_PAGE, gr)));
+                    const __half2 sb = kv_addend(s);
+                    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        uint4 o = make_uint4(kv_h2u(kv_widen<0>(w[i], s, sb)), kv_h2u(kv_widen<1>(w[i], s, sb)),
+                                             kv_h2u(kv_widen<2>(w[i], s, sb)), kv_h2u(kv_widen<3>(w[i], s, sb)));
+                        if (!there)
+                            o = make_uint4(0, 0, 0, 0);
+                        *reinterpret_cast<uint4*>(dst + gr / 2 * C::BLOCK + ((gr % 2 * 4 + i) ^ (t & 7)) * 16) = o;
+                    }
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(bar(C::KFULL + buf));
+                    mbar_arrive(bar(C::REMPTY + stage));
+                }
+                ++count;
+            }
+            {   // V: a thread per 8 keys (chunk c of a page's row) and 16 values
+                const int stage = count % C::STAGES;
+                ok = warp_wait(g, bar(C::RFULL + stage), count / C::STAGES & 1) &&
+                     warp_wait(g, bar(C::VEMPTY + buf), empty);
+                if (!ok)
+                    break;
+                const int2 meta = reinterpret_cast<const int2*>(smem + C::META_AT)[j % META];
+                for (int item = t; item < 2 * 8 * (D / 16); item += 128) {
+                    const int c = item % 8, a = item / 8 % (D / 16), h = item / 8 / (D / 16);
+                    const int held = h ? meta.y : meta.x;
+                    const uint8_t* src = smem + C::RING + stage * C::STAGE + h * C::HALF - P::V_CODES;
+                    uint32_t w[4][4];
+                    __half2 s[4], sb[4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const int pair = 4 * c + k;
+                        const uint4 v = *reinterpret_cast<const uint4*>(src + P::v_chunk(pair, a));
+                        w[k][0] = v.x, w[k][1] = v.y, w[k][2] = v.z, w[k][3] = v.w;
+                        // slots without a token hold anything, and 0 times no number is none
+                        uint32_t sc = *reinterpret_cast<const uint32_t*>(src + P::v_scale(pair, a / 2));
+                        sc = 2 * pair + 1 < held ? sc : 2 * pair < held ? sc & 0xffffu : 0u;
+                        s[k] = kv_u2h(sc);
+                        sb[k] = kv_addend(s[k]);
+                    }
+                    uint8_t* dst = smem + C::V + buf * C::V_BYTES + h * D * 128 + 16 * a * 128;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        auto put = [&](int n, uint4 o) {
+                            *reinterpret_cast<uint4*>(dst + (4 * i + n) * 128 + ((c ^ (4 * i + n) & 7) << 4)) = o;
+                        };
+                        put(0, make_uint4(kv_h2u(kv_widen<0>(w[0][i], s[0], sb[0])), kv_h2u(kv_widen<0>(w[1][i], s[1], sb[1])),
+                                          kv_h2u(kv_widen<0>(w[2][i], s[2], sb[2])), kv_h2u(kv_widen<0>(w[3][i], s[3], sb[3]))));
+                        put(1, make_uint4(kv_h2u(kv_widen<1>(w[0][i], s[0], sb[0])), kv_h2u(kv_widen<1>(w[1][i], s[1], sb[1])),
+                                          kv_h2u(kv_widen<1>(w[2][i], s[2], sb[2])), kv_h2u(kv_widen<1>(w[3][i], s[3], sb[3]))));
+                        put(2, make_uint4(kv_h2u(kv_widen<2>(w[0][i], s[0], sb[0])), kv_h2u(kv_widen<2>(w[1][i], s[1], sb[1])),
+                                          kv_h2u(kv_widen<2>(w[2][i], s[2], sb[2])), kv_h2u(kv_widen<2>(w[3][i], s[3], sb[3]))));
+                        put(3, make_uint4(kv_h2u(kv_widen<3>(w[0][i], s[0], sb[0])), kv_h2u(kv_widen<3>(w[1][i], s[1], sb[1])),
+                                          kv_h2u(kv_widen<3>(w[2][i], s[2], sb[2])), kv_h2u(kv_widen<3>(w[3][i], s[3], sb[3]))));
+                    }
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(bar(C::VFULL + buf));
+                    mbar_arrive(bar(C::REMPTY + stage));
+                }
+                ++count;
+            }
+        }
+    } else {
+        // ------------------------------------------------------------ softmax: a thread per row
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(SOFT_REGS));
+        const int w = (warp - SOFT_WARP) / 4;                           // tile
+        const int l = threadIdx.x - (SOFT_WARP + 4 * w) * 32;           // TMEM lane
+        const int r = TILE * w + l, row = u.row0 + r;
+        const bool mine = r < u.nrow;
+        const long long token = u.first + row / g.group;
+        const int head = u.head * g.group + row % g.group;
+        float coef = g.scale_log2;
+        if (u.steps > 0) {
+            // 2^-e q into the operand tiles, e the exponent of the row's largest magnitude
+            const T* q = static_cast<const T*>(g.q.data) + token * g.q.tok + head * g.q.head;
+            float a = 0.0f;
+            if (mine)
+                for (int d = 0; d < D; d += 4) {
+                    const float4 x = load4(q + d, g.wide);
+                    a = fmaxf(fmaxf(a, fmaxf(fabsf(x.x), fabsf(x.y))), fmaxf(fabsf(x.z), fabsf(x.w)));
+                }
+            const int e = a > 0.0f && a < INFINITY ? ilogbf(a) : 0;
+            coef = scalbnf(g.scale_log2, e);
+            uint8_t* dst = smem + C::Q + w * C::PARTS * C::KB * C::BLOCK + l * 128;
+            for (int d = 0; d < D; d += 8) {
+                float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f), y = x;
+                if (mine) {
+                    x = load4(q + d, g.wide);
+                    y = load4(q + d + 4, g.wide);
+                }
+                uint4 hi, lo;
+                kv_split2(scalbnf(x.x, -e), scalbnf(x.y, -e), hi.x, lo.x);
+                kv_split2(scalbnf(x.z, -e), scalbnf(x.w, -e), hi.y, lo.y);
+                kv_split2(scalbnf(y.x, -e), scalbnf(y.y, -e), hi.z, lo.z);
+                kv_split2(scalbnf(y.z, -e), scalbnf(y.w, -e), hi.w, lo.w);
+                uint8_t* at = dst + d / 64 * C::BLOCK + ((d / 8 % 8 ^ (l & 7)) << 4);
+                *reinterpret_cast<uint4*>(at) = hi;
+                if (HL)
+                    *reinterpret_cast<uint4*>(at + C::KB * C::BLOCK) = lo;
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(bar(C::QFULL));
+        }
+
+        const uint32_t lanes = static_cast<uint32_t>(l & ~31) << 16;
+        const uint32_t s_at = tmem + lanes + S_COL + TILE * w, o_at = tmem + lanes + O_COL + D * w;
+        const long long pos = mine ? u.pos0 + row / g.group : -1;
+        // positions of the tile's rows, for steps that no mask touches
+        const long long plo = u.pos0 + (u.row0 + TILE * w) / g.group;
+        const long long phi = u.pos0 + (u.row0 + min(u.nrow, TILE * (w + 1)) - 1) / g.group;
+        float ref = -INFINITY, sum = 0.0f;
+        bool ok = true;
+        if (w == 0 || two) {
+            for (int j = 0; j < u.steps; ++j) {
+                ok = warp_wait(g, bar(C::SFULL + w), j & 1);
+                if (!ok)
+                    break;
+                tc_fence_after();
+                float x[2][64];
+                tmem_ld64_wait(s_at, x[0]);
+                tmem_ld64_wait(s_at + 64, x[1]);
+                const int2 held = reinterpret_cast<const int2*>(smem + C::META_AT)[j % META];
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const long long kbase = static_cast<long long>(page_of(u, u.i0 + 2 * j + h)) * KV_PAGE;
+                    const bool there = (h ? held.y : held.x) >= 0;
+                    const bool whole = there && kbase + KV_PAGE - 1 <= plo &&
+                                       (g.window == 0 || kbase > phi - g.window || kbase + KV_PAGE <= g.sinks);
+                    if (!whole) {
+                        const uint64_t m = there ? seen_bits(pos, kbase, g.window, g.sinks) : 0;
+                        const uint32_t lo = static_cast<uint32_t>(m), hi = static_cast<uint32_t>(m >> 32);
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) {
+                            x[h][i] = lo >> i & 1u ? x[h][i] : -INFINITY;
+                            x[h][32 + i] = hi >> i & 1u ? x[h][32 + i] : -INFINITY;
+                        }
+                    }
+                }
+                float top = -INFINITY;
+#pragma unroll
+                for (int i = 0; i < 64; ++i)
+                    top = fmaxf(top, fmaxf(x[0][i], x[1][i]));
+                top *= coef;
+                const bool raise = top > ref + KV_REF_LIMIT;   // also the first visible key
+                if (__any_sync(0xffffffffu, raise)) {
+                    const float next = raise ? top - KV_REF_BELOW : ref;
+                    const float f = raise ? kv_ex2(ref - next) : 1.0f;
+                    ref = next;
+                    sum *= f;
+                    if (j > 0) {
+#pragma unroll 1
+                        for (int d = 0; d < D; d += 32) {
+                            float o[32];
+                            uint32_t v[32];
+                            tmem_ld32_wait(o_at + d, o);
+#pragma unroll
+                            for (int i = 0; i < 32; ++i)
+                                v[i] = __float_as_uint(o[i] * f);
+                            tmem_st32(o_at + d, v);
+                        }
+                    }
+                }
+                const float base = ref == -INFINITY ? 0.0f : ref;
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    uint32_t hi[32], lo[32];
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) {
+                        const float p0 = kv_ex2(fmaf(x[h][2 * i], coef, -base));
+                        const float p1 = kv_ex2(fmaf(x[h][2 * i + 1], coef, -base));
+                        sum += p0 + p1;
+                        if (HL)
+                            kv_split2(p0, p1, hi[i], lo[i]);
+                        else
+                            hi[i] = kv_h2u(__floats2half2_rn(p0, p1));
+                    }
+                    tmem_st32(s_at + 32 * h, hi);
+                    if (HL)
+                        tmem_st32(s_at + 64 + 32 * h, lo);
+                }
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(bar(C::PFULL + w));
+            }
+            if (ok && u.steps > 0) {
+                ok = warp_wait(g, bar(C::OFULL + w), 0);
+                tc_fence_after();
+            }
+            const float inv = g.nsplit > 1 ? 1.0f : sum == 0.0f ? 0.0f : 1.0f / sum;
+            const size_t flat = static_cast<size_t>(token) * g.heads + head;
+            const size_t at = static_cast<size_t>(u.split) * g.ntok * g.heads + flat;
+            T* out = static_cast<T*>(g.out.data) + token * g.out.tok + head * g.out.head;
+            if (g.nsplit > 1 && mine)
+                g.part_ml[at] = make_float2(ref, sum);
+#pragma unroll 1
+            for (int d = 0; d < D; d += 32) {
+                float o[32];
+                if (u.steps > 0) {
+                    tmem_ld32_wait(o_at + d, o);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        o[i] = 0.0f;
+                }
+                if (mine) {
+#pragma unroll
+                    for (int i = 0; i < 32; i += 4) {
+                        const float4 v = make_float4(o[i] * inv, o[i + 1] * inv, o[i + 2] * inv, o[i + 3] * inv);
+                        if (g.nsplit > 1)
+                            *reinterpret_cast<float4*>(g.part + at * D + d + i) = v;
+                        else
+                            store4(out + d + i, v, g.wide);
+                    }
+                }
+            }
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 0)
+        tmem_dealloc(tmem, 512);
+}
+
+template <int D, typename T>
+cudaError_t launch_prompt(const AttendArgs& a, cudaStream_t s)
+{
+    using C = Cfg<D, sizeof(T) == 4>;
+    static std::atomic<uint64_t> done{0};
+    cudaError_t e = kv_allow_smem(kv_prompt_kernel<D, T>, C::BYTES, &done);
+    if (e != cudaSuccess)
+        return e;
+    // the register split draws on what the launch reserves: with fewer the softmax would
+    // wait for registers that never come
+    static std::atomic<int> regs{0};
+    if (regs.load() == 0) {
+        cudaFuncAttributes fa;
+        if ((e = cudaFuncGetAttributes(&fa, kv_prompt_kernel<D, T>)) != cudaSuccess)
+            return e;
+        regs.store(fa.numRegs);
+    }
+    if (regs.load() != LAUNCH_REGS)
+        return cudaErrorInvalidConfiguration;
+    const unsigned int grid =
+        static_cast<unsigned int>(static_cast<long long>(a.nsplit) * a.c.kv_heads * a.row_tiles);
+    count_launch();
+    return launch_dependent_smem(kv_prompt_kernel<D, T>, dim3(grid), dim3(THREADS), C::BYTES, s, a);
+}
+
+}  // namespace
+
+cudaError_t launch_kv_prompt(const AttendArgs& a, int dim, int dtype, cudaStream_t s)
+{
+    if (dim == 128)
+        return dtype == KV_F32   ? launch_prompt<128, float>(a, s)
+               : dtype == KV_F16 ? launch_prompt<128, __half>(a, s)
+                                 : launch_prompt<128, __nv_bfloat16>(a, s);
+    return dtype == KV_F32   ? launch_prompt<64, float>(a, s)
+           : dtype == KV_F16 ? launch_prompt<64, __half>(a, s)
+                             : launch_prompt<64, __nv_bfloat16>(a, s);
+}
+
+}  // namespace mmq

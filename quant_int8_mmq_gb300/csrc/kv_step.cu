@@ -29,13 +29,7 @@ namespace {
 
 constexpr int WARPS = 4;
 constexpr int STAGES = 2;
-constexpr int ROWS = 8;
-
-// p = 2^(x - ref) is kept in f16 halves.  A fresh reference is 7 below the row's largest x
-// and stands until some x is 15 above it, so p is at most 2^15 and rows are rescaled
-// rarely; what 2^7 is to the largest p, f16's least step 2^-24 is to the least.
-constexpr float REF_BELOW = 7.0f;
-constexpr float REF_LIMIT = 15.0f;
+constexpr int ROWS = KV_STEP_ROWS;
 
 template <int D>
 struct StepSmem {
@@ -58,22 +52,6 @@ __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1
         "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-
-__device__ __forceinline__ float ex2(float x)
-{
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
-// hi and lo halves of two values, hi in the first result
-__device__ __forceinline__ void split2(float x, float y, uint32_t& hi, uint32_t& lo)
-{
-    const __half2 h = __floats2half2_rn(x, y);
-    const float2 f = __half22float2(h);
-    hi = kv_h2u(h);
-    lo = kv_h2u(__floats2half2_rn(x - f.x, y - f.y));
 }
 
 template <int D, typename T>
@@ -178,8 +156,8 @@ __global__ void __launch_bounds__(WARPS * 32) kv_step_kernel(const AttendArgs g)
         const int e = a > 0.0f && a < INFINITY ? ilogbf(a) : 0;
         if (lane < D / 4) {
             uint2 hi, lo;
-            split2(scalbnf(x.x, -e), scalbnf(x.y, -e), hi.x, lo.x);
-            split2(scalbnf(x.z, -e), scalbnf(x.w, -e), hi.y, lo.y);
+            kv_split2(scalbnf(x.x, -e), scalbnf(x.y, -e), hi.x, lo.x);
+            kv_split2(scalbnf(x.z, -e), scalbnf(x.w, -e), hi.y, lo.y);
             *reinterpret_cast<uint2*>(smem + S::Q + r * S::QROW + lane * 8) = hi;
             *reinterpret_cast<uint2*>(smem + S::Q + (ROWS + r) * S::QROW + lane * 8) = lo;
         }
@@ -276,10 +254,10 @@ __global__ void __launch_bounds__(WARPS * 32) kv_step_kernel(const AttendArgs g)
             top = fmaxf(top, fmaxf(x[oct][0], x[oct][1]));
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        const bool raise = top > ref + REF_LIMIT;   // also the first visible key: ref is -inf until then
+        const bool raise = top > ref + KV_REF_LIMIT;   // also the first visible key: ref is -inf until then
         if (__any_sync(0xffffffffu, raise)) {
-            const float next = raise ? top - REF_BELOW : ref;
-            const float f = raise ? ex2(ref - next) : 1.0f;
+            const float next = raise ? top - KV_REF_BELOW : ref;
+            const float f = raise ? kv_ex2(ref - next) : 1.0f;
             ref = next;
             sum *= f;
 #pragma unroll
@@ -296,9 +274,9 @@ __global__ void __launch_bounds__(WARPS * 32) kv_step_kernel(const AttendArgs g)
             uint32_t a[4];
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                const float p0 = ex2(x[2 * kk + h][0] - base), p1 = ex2(x[2 * kk + h][1] - base);
+                const float p0 = kv_ex2(x[2 * kk + h][0] - base), p1 = kv_ex2(x[2 * kk + h][1] - base);
                 sum += p0 + p1;
-                split2(p0, p1, a[2 * h], a[2 * h + 1]);
+                kv_split2(p0, p1, a[2 * h], a[2 * h + 1]);
             }
             uint32_t w[2][D / 32];
             __half2 s[2], sb[2];
@@ -370,7 +348,7 @@ __global__ void __launch_bounds__(WARPS * 32) kv_step_kernel(const AttendArgs g)
 #pragma unroll
     for (int w = 0; w < WARPS; ++w) {
         const float2 v = ml[w * ROWS + r];
-        f[w] = v.x == -INFINITY ? 0.0f : ex2(v.x - top);
+        f[w] = v.x == -INFINITY ? 0.0f : kv_ex2(v.x - top);
         total += f[w] * v.y;
     }
     const int row = row0 + r;
@@ -430,7 +408,7 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) kv_join_kernel(const AttendAr
         const size_t at = s * rows + flat;
         const float2 ml = g.part_ml[at];
         const float4 p = *reinterpret_cast<const float4*>(g.part + at * D + d);
-        const float f = ml.x == -INFINITY ? 0.0f : ex2(ml.x - top);
+        const float f = ml.x == -INFINITY ? 0.0f : kv_ex2(ml.x - top);
         total += f * ml.y;
         v.x += f * p.x;
         v.y += f * p.y;
@@ -469,14 +447,10 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) kv_join_kernel(const AttendAr
 template <int D, typename T>
 cudaError_t launch_step(const AttendArgs& a, cudaStream_t s)
 {
-    static std::atomic<bool> set{false};
-    if (!set.load(std::memory_order_acquire)) {
-        const cudaError_t e = cudaFuncSetAttribute(kv_step_kernel<D, T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                   StepSmem<D>::BYTES);
-        if (e != cudaSuccess)
-            return e;
-        set.store(true, std::memory_order_release);
-    }
+    static std::atomic<uint64_t> done{0};
+    const cudaError_t e = kv_allow_smem(kv_step_kernel<D, T>, StepSmem<D>::BYTES, &done);
+    if (e != cudaSuccess)
+        return e;
     const unsigned int grid = static_cast<unsigned int>(static_cast<long long>(a.nsplit) * a.c.kv_heads * a.row_tiles *
                                                         a.c.batch);
     count_launch();
