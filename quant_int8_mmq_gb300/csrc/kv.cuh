@@ -74,14 +74,27 @@ struct KvRows {
 __device__ __forceinline__ uint32_t kv_h2u(__half2 v) { return *reinterpret_cast<const uint32_t*>(&v); }
 __device__ __forceinline__ __half2 kv_u2h(uint32_t v) { return *reinterpret_cast<const __half2*>(&v); }
 
-// Pair i (0..3) of a code word: the nibbles at bits 4i and 4i + 16, brought to bits 4-7
-// under the exponent of 64, where they read 64 + n; one f16x2 fma with {s, -72 s} leaves
-// s * (n - 8).  Nothing is rounded: 72 s = 9 * 8 s has at most 11 significant bits.
+// Pair I (0..3) of a code word w (the nibbles at bits 4 I and 4 I + 16), times the scale.
+// A nibble at bits 0-3 under the exponent of 1024 reads 1024 + n, at bits 4-7 under that
+// of 64 reads 64 + n.  The latter becomes s (n - 8) in one f16x2 fma with b = -72 s, of
+// at most 11 significant bits; the former takes an add and a multiply, as 1032 s would
+// be rounded.  Nothing is inexact.  Each mask and exponent is one three-input logic
+// operation (written as such: as an expression it compiled to two, and the step kernel
+// executed 1571 instructions a page for 1315), and only pairs 2 and 3 share a shift, which
+// keeps half of the work off the integer pipe.
+__device__ __forceinline__ uint32_t kv_field(uint32_t x, uint32_t mask, uint32_t exponent)
+{
+    uint32_t y;
+    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(y) : "r"(x), "r"(mask), "r"(exponent));   // (x & mask) | exponent
+    return y;
+}
 template <int I>
 __device__ __forceinline__ __half2 kv_widen(uint32_t w, __half2 s, __half2 b)
 {
-    const uint32_t x = I == 0 ? w << 4 : I == 1 ? w : I == 2 ? w >> 4 : w >> 8;
-    return __hfma2(kv_u2h((x & 0x00F000F0u) | 0x54005400u), s, b);
+    const uint32_t x = I < 2 ? w : w >> 8;
+    if constexpr (I % 2 == 0)
+        return __hmul2(__hadd2(kv_u2h(kv_field(x, 0x000F000Fu, 0x64006400u)), __floats2half2_rn(-1032.0f, -1032.0f)), s);
+    return __hfma2(kv_u2h(kv_field(x, 0x00F000F0u, 0x54005400u)), s, b);
 }
 __device__ __forceinline__ __half2 kv_addend(__half2 s) { return __hmul2(s, __floats2half2_rn(-72.0f, -72.0f)); }
 
@@ -210,7 +223,8 @@ struct AttendArgs {
     float scale_log2;      // softmax scale times log2(e)
     int window, sinks;
     int row_tiles;         // kv_step.cu: row tiles per (sequence, kv head); kv_prompt.cu: of the whole batch
-    int nsplit;            // parts of the visible pages
+    int nsplit;            // parts of the visible pages,
+    int part_pages;        // each of so many
     bool wide;
     float* part;           // nsplit > 1: [nsplit][ntok * heads][D] unnormalised sums
     float2* part_ml;       //             [nsplit][ntok * heads] {reference, sum}
@@ -220,7 +234,7 @@ struct AttendArgs {
 struct AttendPlan {
     int kernel;      // 0: kv_step.cu, 1: kv_prompt.cu
     int row_tiles;
-    int nsplit;
+    int nsplit, part_pages;
     size_t part_bytes, ml_bytes;
 };
 AttendPlan plan_attend(int dtype, int heads, int kv_heads, int dim, int batch, int ntok, int max_q, int max_kv,

@@ -24,12 +24,15 @@ AttendPlan plan_attend(int dtype, int heads, int kv_heads, int dim, int batch, i
     }
     const long long rows = static_cast<long long>(max_q) * group;
     p.kernel = rows > 64 ? 1 : 0;
-    long long units, most, slots;
+    // units: independent CTAs without parts; slots: CTAs that the chip holds at once; least,
+    // most: pages of a part
+    long long units, slots, least, most;
     if (p.kernel == 0) {
         p.row_tiles = static_cast<int>((rows + KV_STEP_ROWS - 1) / KV_STEP_ROWS);
         units = static_cast<long long>(batch) * kv_heads * p.row_tiles;
-        slots = 2 * SMS;            // two CTAs an SM
-        most = (pages + 3) / 4;     // a page per warp at least
+        slots = 3 * SMS;
+        least = 4;      // a page a warp
+        most = 64;      // sequences of uneven length: parts even the load out
     } else {
         // sum over the sequences of ceil(rows / KV_PROMPT_ROWS), or more
         const long long tiles =
@@ -37,11 +40,16 @@ AttendPlan plan_attend(int dtype, int heads, int kv_heads, int dim, int batch, i
         p.row_tiles = static_cast<int>(tiles < 0x7fffffffll ? tiles : 0x7fffffffll);
         units = tiles * kv_heads;
         slots = SMS;
-        most = (pages + 7) / 8;
+        least = 8;
+        most = 1ll << 30;
     }
-    long long nsplit = slots / units;
-    nsplit = nsplit < most ? nsplit : most;
-    p.nsplit = static_cast<int>(nsplit < 1 ? 1 : nsplit);
+    long long parts = slots / units;
+    parts = parts < 1 ? 1 : parts;
+    long long part = (pages + parts - 1) / parts;
+    part = part < least ? least : part > most ? most : part;
+    part = (part + 3) / 4 * 4;
+    p.part_pages = static_cast<int>(part);
+    p.nsplit = static_cast<int>((pages + part - 1) / part);
     if (p.nsplit > 1) {
         const size_t flat = static_cast<size_t>(p.nsplit) * ntok * heads;
         p.part_bytes = flat * dim * sizeof(float);
@@ -243,6 +251,7 @@ mmq_status mmq_kv_attend(const mmq_kv_cache* c, const mmq_rows* q, const mmq_row
     a.sinks = window > 0 ? sinks : 0;
     a.row_tiles = p.row_tiles;
     a.nsplit = p.nsplit;
+    a.part_pages = p.part_pages;
     a.wide = wide(q) && wide(out);
     a.part = static_cast<float*>(workspace);
     a.part_ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(workspace) + p.part_bytes);

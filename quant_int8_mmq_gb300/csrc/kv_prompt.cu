@@ -181,9 +181,10 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prompt_kernel(const AttendArgs 
         u.page_lo = klo / KV_PAGE;
         u.nsink = min((min(g.sinks, u.kend) + KV_PAGE - 1) / KV_PAGE, u.page_lo);
         u.npage = u.nsink + (u.kend + KV_PAGE - 1) / KV_PAGE - u.page_lo;
-        const int per = ((u.npage + 1) / 2 + g.nsplit - 1) / g.nsplit;   // steps of a split
-        u.i0 = 2 * per * u.split;
-        u.steps = max(0, min(per, (u.npage - u.i0 + 1) / 2));
+        // a part is an even number of pages; the last takes what max_kv did not foresee
+        const long long part0 = static_cast<long long>(u.split) * g.part_pages;
+        u.i0 = static_cast<int>(min(part0, static_cast<long long>(u.npage)));
+        u.steps = ((u.split == g.nsplit - 1 ? u.npage - u.i0 : min(g.part_pages, u.npage - u.i0)) + 1) / 2;
     }
     const bool two = u.nrow > TILE;
 

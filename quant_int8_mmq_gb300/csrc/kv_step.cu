@@ -28,14 +28,15 @@ namespace mmq {
 namespace {
 
 constexpr int WARPS = 4;
-constexpr int STAGES = 2;
+constexpr int STAGES = 3;   // half pieces (K or V) a warp's ring holds
 constexpr int ROWS = KV_STEP_ROWS;
 
 template <int D>
 struct StepSmem {
     static constexpr int QROW = D * 2 + 16;                         // padded row of f16
-    static constexpr int RING = 0;                                  // [WARPS][STAGES] pieces
-    static constexpr int Q = RING + WARPS * STAGES * Piece<D>::BYTES;
+    static constexpr int HALF = Piece<D>::V_CODES;                  // bytes of a piece's K or V
+    static constexpr int RING = 0;                                  // [WARPS][STAGES] halves
+    static constexpr int Q = RING + WARPS * STAGES * HALF;
     static constexpr int COEF = Q + 2 * ROWS * QROW;                // f32 per row
     static constexpr int ML = COEF + ROWS * 4;                      // float2 [WARPS][ROWS]
     static constexpr int BAR = ML + WARPS * ROWS * 8;
@@ -55,7 +56,7 @@ __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1
 }
 
 template <int D, typename T>
-__global__ void __launch_bounds__(WARPS * 32) kv_step_kernel(const AttendArgs g)
+__global__ void __launch_bounds__(WARPS * 32, D == 128 ? 3 : 4) kv_step_kernel(const AttendArgs g)
 {
     using P = Piece<D>;
     using S = StepSmem<D>;
@@ -92,12 +93,22 @@ __global__ void __launch_bounds__(WARPS * 32) kv_step_kernel(const AttendArgs g)
     const int page_lo = klo / KV_PAGE;
     const int nsink = min((min(g.sinks, kend) + KV_PAGE - 1) / KV_PAGE, page_lo);
     const int npage = nsink + (kend + KV_PAGE - 1) / KV_PAGE - page_lo;
-    const int per = (npage + g.nsplit - 1) / g.nsplit;
-    const int i_end = min(npage, (split + 1) * per);
-    const int i0 = split * per + warp;
+    // the last part takes what the caller's max_kv did not foresee
+    const long long part0 = static_cast<long long>(split) * g.part_pages;
+    const int i_end = split == g.nsplit - 1 ? npage : static_cast<int>(min(part0 + g.part_pages, static_cast<long long>(npage)));
+    const int flat_rows = g.ntok * g.heads;
+    if (g.nsplit > 1 && part0 >= npage) {   // nothing here: say so and leave
+        if (threadIdx.x < nrow) {
+            const int row = row0 + threadIdx.x;
+            g.part_ml[static_cast<size_t>(split) * flat_rows + static_cast<size_t>(first + row / g.group) * g.heads +
+                      head * g.group + row % g.group] = make_float2(-INFINITY, 0.0f);
+        }
+        return;
+    }
 
+    const int i0 = static_cast<int>(part0) + warp;
     const uint32_t sbase = smem_u32(smem);
-    const uint32_t ring = sbase + S::RING + warp * STAGES * P::BYTES;
+    const uint32_t ring = sbase + S::RING + warp * STAGES * S::HALF;
     const uint32_t bar = sbase + S::BAR + warp * STAGES * 8;
     if (lane == 0) {
 #pragma unroll
@@ -109,11 +120,12 @@ __global__ void __launch_bounds__(WARPS * 32) kv_step_kernel(const AttendArgs g)
 
     // the warp's pages are i0, i0 + WARPS, ...; ids of 32 of them at a time, one per lane
     const int* table = g.c.table + static_cast<size_t>(b) * g.c.max_pages;
-    int ids = -1;
-    uint32_t flying = 0;   // bit s: stage s holds or awaits a page
-    // page number k of this warp into stage k % STAGES
-    auto fetch = [&](int k) {
-        if (k % 32 == 0) {
+    int ids = -1, ahead = 0;   // halves asked for so far: K, V of the first page, K, ...
+    int fill = 0;              // their next stage
+    uint32_t flying = 0;       // bit s: stage s holds or awaits a half
+    auto fetch = [&] {
+        const int k = ahead / 2;
+        if (ahead % 64 == 0) {
             const int j = i0 + (k + lane) * WARPS;
             ids = -1;
             if (j < i_end) {
@@ -125,20 +137,22 @@ __global__ void __launch_bounds__(WARPS * 32) kv_step_kernel(const AttendArgs g)
             }
         }
         const int pid = __shfl_sync(0xffffffffu, ids, k % 32);
-        const uint32_t stage = k % STAGES;
-        if (pid < 0)
-            return;
-        flying |= 1u << stage;
-        if (lane == 0) {
-            fence_proxy_async_smem();   // the stage's last page was read with ordinary loads
-            mbar_arrive_expect_tx(bar + 8 * stage, P::BYTES);
-            bulk_g2s(ring + stage * P::BYTES,
-                     g.c.pages + (static_cast<size_t>(pid) * g.c.kv_heads + head) * P::BYTES, P::BYTES, bar + 8 * stage);
+        if (pid >= 0) {
+            flying |= 1u << fill;
+            if (lane == 0) {
+                fence_proxy_async_smem();   // the stage's last half was read with ordinary loads
+                mbar_arrive_expect_tx(bar + 8 * fill, S::HALF);
+                bulk_g2s(ring + fill * S::HALF,
+                         g.c.pages + (static_cast<size_t>(pid) * g.c.kv_heads + head) * P::BYTES + ahead % 2 * S::HALF,
+                         S::HALF, bar + 8 * fill);
+            }
         }
+        ++ahead;
+        fill = fill + 1 == STAGES ? 0 : fill + 1;
     };
 #pragma unroll
-    for (int k = 0; k < STAGES - 1; ++k)
-        fetch(k);
+    for (int i = 0; i < STAGES - 1; ++i)
+        fetch();
 
     // query rows: 2^-e q as hi and lo f16, coefficient 2^e scale log2(e)
     for (int r = warp; r < ROWS; r += WARPS) {
@@ -188,19 +202,31 @@ __global__ void __launch_bounds__(WARPS * 32) kv_step_kernel(const AttendArgs g)
     float ref = -INFINITY, sum = 0.0f;
 
     uint32_t parity = 0;   // bit s: parity of stage s's next arrival
+    int take = 0;          // stage of the next half
     bool ok = true;
-    for (int i = i0, k = 0; i < i_end; i += WARPS, ++k) {
+    // the next half, once it is there: its bytes, or null for a page that is not in the pool
+    auto next_half = [&]() -> const uint8_t* {
         __syncwarp();
-        fetch(k + STAGES - 1);
-        const uint32_t stage = k % STAGES;
+        fetch();
+        const int stage = take;
+        take = take + 1 == STAGES ? 0 : take + 1;
         if ((flying >> stage & 1u) == 0)
-            continue;   // no such page: its keys are not there
+            return nullptr;
         ok = __all_sync(0xffffffffu, mbar_wait(bar + 8 * stage, parity >> stage & 1u, g.wc.limit_ns, g.wc.err));
         if (!ok)
-            break;
+            return nullptr;
         parity ^= 1u << stage;
         flying &= ~(1u << stage);
-        const uint8_t* page = smem + S::RING + (warp * STAGES + stage) * P::BYTES;
+        return smem + S::RING + (warp * STAGES + stage) * S::HALF;
+    };
+    for (int i = i0; i < i_end; i += WARPS) {
+        const uint8_t* page = next_half();
+        if (page == nullptr) {
+            if (!ok)
+                break;
+            next_half();   // its other half is not there either
+            continue;
+        }
         const long long kbase = static_cast<long long>(i < nsink ? i : page_lo + i - nsink) * KV_PAGE;
 
         // x[o]: keys 8o + 2t and 8o + 2t + 1 of row n
@@ -268,6 +294,10 @@ __global__ void __launch_bounds__(WARPS * 32) kv_step_kernel(const AttendArgs g)
         }
         const float base = ref == -INFINITY ? 0.0f : ref;
 
+        page = next_half();
+        if (!ok)
+            break;
+        page -= P::V_CODES;
         const int held = static_cast<int>(min(kend - kbase, static_cast<long long>(KV_PAGE)));
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk) {   // keys 16 kk .. 16 kk + 15
@@ -372,7 +402,7 @@ __global__ void __launch_bounds__(WARPS * 32) kv_step_kernel(const AttendArgs g)
             v = make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv);
             store4(static_cast<T*>(g.out.data) + token * g.out.tok + h * g.out.head + d, v, g.wide);
         } else {
-            const size_t at = static_cast<size_t>(split) * g.ntok * g.heads + flat;
+            const size_t at = static_cast<size_t>(split) * flat_rows + flat;
             *reinterpret_cast<float4*>(g.part + at * D + d) = v;
             if (l == 0 && j == 0)
                 g.part_ml[at] = make_float2(top, total);
@@ -407,8 +437,10 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) kv_join_kernel(const AttendAr
     for (int s = warp * SETS + set; s < g.nsplit; s += JOIN_WARPS * SETS) {
         const size_t at = s * rows + flat;
         const float2 ml = g.part_ml[at];
+        if (ml.x == -INFINITY && ml.y == 0.0f)
+            continue;   // saw no key; its sums may not have been written
         const float4 p = *reinterpret_cast<const float4*>(g.part + at * D + d);
-        const float f = ml.x == -INFINITY ? 0.0f : kv_ex2(ml.x - top);
+        const float f = kv_ex2(ml.x - top);
         total += f * ml.y;
         v.x += f * p.x;
         v.y += f * p.y;
