@@ -22,7 +22,6 @@ namespace mmq {
 
 constexpr int KV_PAGE = MMQ_KV_PAGE;   // tokens per page
 constexpr int KV_GROUP = 32;           // values per scale
-constexpr int KV_STEP_ROWS = 8;        // rows of a kv_step.cu tile
 constexpr int KV_PROMPT_ROWS = 256;    // rows of a kv_prompt.cu CTA
 
 // Byte offsets inside a piece of head size D; the documented layout is in mmq.h.
@@ -172,6 +171,19 @@ __device__ __forceinline__ void kv_split2(float x, float y, uint32_t& hi, uint32
 constexpr float KV_REF_BELOW = 7.0f;
 constexpr float KV_REF_LIMIT = 15.0f;
 
+// Which keys of a page (64 from kbase on) a row at position pos sees, one bit each.
+__device__ __forceinline__ uint64_t kv_seen_bits(long long pos, long long kbase, int window, int sinks)
+{
+    const int to = static_cast<int>(min(max(pos - kbase, -1ll), 63ll));
+    uint64_t m = to < 0 ? 0 : ~0ull >> (63 - to);
+    if (window > 0) {
+        const int from = static_cast<int>(min(max(pos - window + 1 - kbase, 0ll), 64ll));
+        const int sink = static_cast<int>(min(max(sinks - kbase, 0ll), 64ll));
+        m &= (from < 64 ? ~0ull << from : 0) | (sink > 0 ? ~0ull >> (64 - sink) : 0);
+    }
+    return m;
+}
+
 // The sequence of packed row r: the last b with start[b] <= r, found by one warp, 32
 // probes a step (sequences without rows are passed over).  0 <= result < batch whatever
 // start holds.
@@ -222,6 +234,7 @@ struct AttendArgs {
     int ntok;
     float scale_log2;      // softmax scale times log2(e)
     int window, sinks;
+    int tile_rows;         // kv_step.cu: rows of a tile, 8 or (16-bit rows) 16
     int row_tiles;         // kv_step.cu: row tiles per (sequence, kv head); kv_prompt.cu: of the whole batch
     int nsplit;            // parts of the visible pages,
     int part_pages;        // each of so many
@@ -233,7 +246,7 @@ struct AttendArgs {
 
 struct AttendPlan {
     int kernel;      // 0: kv_step.cu, 1: kv_prompt.cu
-    int row_tiles;
+    int tile_rows, row_tiles;
     int nsplit, part_pages;
     size_t part_bytes, ml_bytes;
 };

@@ -12,7 +12,6 @@ namespace mmq {
 AttendPlan plan_attend(int dtype, int heads, int kv_heads, int dim, int batch, int ntok, int max_q, int max_kv,
                        int window, int sinks)
 {
-    (void)dtype;
     constexpr int SMS = 152;
     AttendPlan p = {};
     const int group = heads / kv_heads;
@@ -28,9 +27,10 @@ AttendPlan plan_attend(int dtype, int heads, int kv_heads, int dim, int batch, i
     // most: pages of a part
     long long units, slots, least, most;
     if (p.kernel == 0) {
-        p.row_tiles = static_cast<int>((rows + KV_STEP_ROWS - 1) / KV_STEP_ROWS);
+        p.tile_rows = dtype == KV_F32 || rows <= 8 ? 8 : 16;
+        p.row_tiles = static_cast<int>((rows + p.tile_rows - 1) / p.tile_rows);
         units = static_cast<long long>(batch) * kv_heads * p.row_tiles;
-        slots = 3 * SMS;
+        slots = (p.tile_rows == 16 ? 3 : 4) * SMS;
         least = 4;      // a page a warp
         most = 64;      // sequences of uneven length: parts even the load out
     } else {
@@ -249,6 +249,7 @@ mmq_status mmq_kv_attend(const mmq_kv_cache* c, const mmq_rows* q, const mmq_row
     a.scale_log2 = scale * 1.4426950408889634f;
     a.window = window;
     a.sinks = window > 0 ? sinks : 0;
+    a.tile_rows = p.tile_rows;
     a.row_tiles = p.row_tiles;
     a.nsplit = p.nsplit;
     a.part_pages = p.part_pages;

@@ -99,19 +99,6 @@ __device__ __forceinline__ bool warp_wait(const AttendArgs& g, uint32_t bar, uin
     return __all_sync(0xffffffffu, wait(g, bar, parity));
 }
 
-// Which keys of a page (64 from kbase on) a row at position pos sees, one bit each.
-__device__ __forceinline__ uint64_t seen_bits(long long pos, long long kbase, int window, int sinks)
-{
-    const int to = static_cast<int>(min(max(pos - kbase, -1ll), 63ll));
-    uint64_t m = to < 0 ? 0 : ~0ull >> (63 - to);
-    if (window > 0) {
-        const int from = static_cast<int>(min(max(pos - window + 1 - kbase, 0ll), 64ll));
-        const int sink = static_cast<int>(min(max(sinks - kbase, 0ll), 64ll));
-        m &= (from < 64 ? ~0ull << from : 0) | (sink > 0 ? ~0ull >> (64 - sink) : 0);
-    }
-    return m;
-}
-
 template <int D, typename T>
 __global__ void __launch_bounds__(THREADS, 1) kv_prompt_kernel(const AttendArgs g)
 {
@@ -445,7 +432,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prompt_kernel(const AttendArgs 
                     a = fmaxf(fmaxf(a, fmaxf(fabsf(x.x), fabsf(x.y))), fmaxf(fabsf(x.z), fabsf(x.w)));
                 }
             const int e = a > 0.0f && a < INFINITY ? ilogbf(a) : 0;
-            coef = scalbnf(g.scale_log2, e);
+            coef = fminf(fmaxf(scalbnf(g.scale_log2, e), 1e-38f), 1e38f);
             uint8_t* dst = smem + C::Q + w * C::PARTS * C::KB * C::BLOCK + l * 128;
             for (int d = 0; d < D; d += 8) {
                 float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f), y = x;
@@ -494,7 +481,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prompt_kernel(const AttendArgs 
                     const bool whole = there && kbase + KV_PAGE - 1 <= plo &&
                                        (g.window == 0 || kbase > phi - g.window || kbase + KV_PAGE <= g.sinks);
                     if (!whole) {
-                        const uint64_t m = there ? seen_bits(pos, kbase, g.window, g.sinks) : 0;
+                        const uint64_t m = there ? kv_seen_bits(pos, kbase, g.window, g.sinks) : 0;
                         const uint32_t lo = static_cast<uint32_t>(m), hi = static_cast<uint32_t>(m >> 32);
 #pragma unroll
                         for (int i = 0; i < 32; ++i) {

@@ -5,21 +5,27 @@
 //
 // The cache is read once and its bytes bound the work: a 128-value head costs 144 bytes a
 // key.  What has to keep up with them is the widening of the codes, so the layout is made
-// for registers: a lane's 16-byte load is exactly its part of the tensor-core operand
-// (mma m16n8k16: keys are the 8 columns of Q K^T, each lane supplying a quarter of its
-// key's values; 16 keys are the depth of P V, each lane supplying two pairs of keys for
-// D/8 values), and widening a pair of codes takes a mask, mostly a shift, and one fma
-// that also applies the scale.
+// for registers: a lane's 16-byte load is exactly its part of an operand of mma m16n8k16,
+// and widening a pair of codes takes one logic operation, a quarter of a shift and one or
+// two f16x2 operations that also apply the scale.
+//   S = Q K^T   Q is the 16-row operand, 8 keys the columns; lane (n, t) supplies a quarter
+//               t of key n's values.
+//   O^T = V^T P^T   V is the 16-row operand (lane (n, t): two of its D/8 values by two pairs
+//               of keys), and the accumulators of S are, in place, the operand P^T.
+// Transposed, O needs D/4 accumulators a lane for 8 rows whether P has one or two parts;
+// as P V they were twice that, and 12 warps an SM instead of 16.
 //
-// A tile is 8 rows (a row is a query token and one of the heads that share the kv head).
-// They fill the 16 operand rows as 8 high parts and 8 low parts of f16 each, q = 2^e
-// (hi + lo) and p = hi + lo with 22 bits, while the cached values are exact in f16, so
-// the products carry f32 precision at the price of the 16-bit instruction.
+// A row is a query token and one of the heads that share the kv head.  Tiles:
+//   f32 rows: 8, the operand's 16 rows holding the f16 parts of q = 2^e (hi + lo), and
+//     P = hi + lo as two products into the same accumulators: 22 bits at each operand;
+//   16-bit rows: 8 in the same way with P rounded to f16, or, where there are more, 16
+//     (q has no low part worth having: 2^-e q is exact in f16 down to 2^-24).
 //
 // A CTA is 4 warps; each takes every fourth of the CTA's pages through its own ring of
 // bulk copies, with its own running reference and sums, and the four are joined in shared
-// memory.  When there are few tiles the visible pages are split over nsplit CTAs, whose
-// sums go to the workspace and are joined by a second kernel.
+// memory.  When there are few tiles, or sequences of uneven length, the visible pages are
+// cut into parts of bounded length, whose sums go to the workspace and are joined by a
+// second kernel.
 #include <atomic>
 
 #include "kv.cuh"
@@ -28,16 +34,19 @@ namespace mmq {
 namespace {
 
 constexpr int WARPS = 4;
-constexpr int STAGES = 3;   // half pieces (K or V) a warp's ring holds
-constexpr int ROWS = KV_STEP_ROWS;
+constexpr int STAGES = 2;   // half pieces (K or V) a warp's ring holds
 
-template <int D>
+// Row tiles (see above).
+enum Mode { HI_LO = 0, ONE_PART = 1, WIDE = 2 };
+
+template <int D, int MODE>
 struct StepSmem {
+    static constexpr int ROWS = MODE == WIDE ? 16 : 8;
     static constexpr int QROW = D * 2 + 16;                         // padded row of f16
     static constexpr int HALF = Piece<D>::V_CODES;                  // bytes of a piece's K or V
     static constexpr int RING = 0;                                  // [WARPS][STAGES] halves
     static constexpr int Q = RING + WARPS * STAGES * HALF;
-    static constexpr int COEF = Q + 2 * ROWS * QROW;                // f32 per row
+    static constexpr int COEF = Q + 16 * QROW;                      // f32 per row
     static constexpr int ML = COEF + ROWS * 4;                      // float2 [WARPS][ROWS]
     static constexpr int BAR = ML + WARPS * ROWS * 8;
     static constexpr int BYTES = BAR + WARPS * STAGES * 8;
@@ -46,20 +55,28 @@ struct StepSmem {
     static_assert(Q % 16 == 0 && ML % 8 == 0 && BAR % 8 == 0, "alignment");
 };
 
+__device__ __forceinline__ void mma16816_first(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                               uint32_t b0, uint32_t b1)
+{
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+        : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
+}
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                          uint32_t b0, uint32_t b1)
 {
-    asm volatile(
+    asm(
         "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-template <int D, typename T>
-__global__ void __launch_bounds__(WARPS * 32, D == 128 ? 3 : 4) kv_step_kernel(const AttendArgs g)
+template <int D, typename T, int MODE>
+__global__ void __launch_bounds__(WARPS * 32, MODE == WIDE ? 3 : D == 128 ? 4 : 5) kv_step_kernel(const AttendArgs g)
 {
     using P = Piece<D>;
-    using S = StepSmem<D>;
+    using S = StepSmem<D, MODE>;
+    constexpr int ROWS = S::ROWS, SETS = ROWS / 8;   // rows n and, of a wide tile, n + 8
     extern __shared__ __align__(128) uint8_t smem[];
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const int n = lane / 4, t = lane % 4;
@@ -173,33 +190,41 @@ __global__ void __launch_bounds__(WARPS * 32, D == 128 ? 3 : 4) kv_step_kernel(c
             kv_split2(scalbnf(x.x, -e), scalbnf(x.y, -e), hi.x, lo.x);
             kv_split2(scalbnf(x.z, -e), scalbnf(x.w, -e), hi.y, lo.y);
             *reinterpret_cast<uint2*>(smem + S::Q + r * S::QROW + lane * 8) = hi;
-            *reinterpret_cast<uint2*>(smem + S::Q + (ROWS + r) * S::QROW + lane * 8) = lo;
+            if (MODE != WIDE)
+                *reinterpret_cast<uint2*>(smem + S::Q + (8 + r) * S::QROW + lane * 8) = lo;
         }
         if (lane == 0)
-            *reinterpret_cast<float*>(smem + S::COEF + 4 * r) = scalbnf(g.scale_log2, e);
+            *reinterpret_cast<float*>(smem + S::COEF + 4 * r) = fminf(fmaxf(scalbnf(g.scale_log2, e), 1e-38f), 1e38f);
     }
     __syncthreads();
 
-    // operand rows n (hi) and n + 8 (lo): lane t holds values D/4 t .. D/4 t + D/4 - 1
+    // operand rows n and n + 8: lane t holds values D/4 t .. D/4 t + D/4 - 1
     uint32_t qf[D / 16][4];
 #pragma unroll
     for (int j = 0; j < D / 16; ++j) {
-        const uint2 hi = *reinterpret_cast<const uint2*>(smem + S::Q + n * S::QROW + (D / 4 * t + 4 * j) * 2);
-        const uint2 lo = *reinterpret_cast<const uint2*>(smem + S::Q + (ROWS + n) * S::QROW + (D / 4 * t + 4 * j) * 2);
-        qf[j][0] = hi.x;
-        qf[j][1] = lo.x;
-        qf[j][2] = hi.y;
-        qf[j][3] = lo.y;
+        const uint2 up = *reinterpret_cast<const uint2*>(smem + S::Q + n * S::QROW + (D / 4 * t + 4 * j) * 2);
+        const uint2 low = *reinterpret_cast<const uint2*>(smem + S::Q + (8 + n) * S::QROW + (D / 4 * t + 4 * j) * 2);
+        qf[j][0] = up.x;
+        qf[j][1] = low.x;
+        qf[j][2] = up.y;
+        qf[j][3] = low.y;
     }
-    const float coef = *reinterpret_cast<const float*>(smem + S::COEF + 4 * n);
-    const long long pos = n < nrow ? pos0 + (row0 + n) / g.group : -1;   // row n sees keys up to here
-    const long long low = g.window > 0 ? pos - g.window + 1 : 0;         // and from here, or below g.sinks
-
-    float o[D / 8][4];
+    float coef[SETS], ref[SETS], sum[SETS];
+    long long pos[SETS];   // the row sees keys up to here, -1: no row
 #pragma unroll
-    for (int i = 0; i < D / 8; ++i)
-        o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.0f;
-    float ref = -INFINITY, sum = 0.0f;
+    for (int i = 0; i < SETS; ++i) {
+        coef[i] = *reinterpret_cast<const float*>(smem + S::COEF + 4 * (n + 8 * i));
+        pos[i] = n + 8 * i < nrow ? pos0 + (row0 + n + 8 * i) / g.group : -1;
+        ref[i] = -INFINITY;
+        sum[i] = 0.0f;
+    }
+    // values D/8 n + 2 j (elements 0, 1) and D/8 n + 2 j + 1 (2, 3) of rows 2t, 2t + 1 (and + 8)
+    float o[SETS][D / 16][4];
+#pragma unroll
+    for (int i = 0; i < SETS; ++i)
+#pragma unroll
+        for (int j = 0; j < D / 16; ++j)
+            o[i][j][0] = o[i][j][1] = o[i][j][2] = o[i][j][3] = 0.0f;
 
     uint32_t parity = 0;   // bit s: parity of stage s's next arrival
     int take = 0;          // stage of the next half
@@ -229,70 +254,105 @@ __global__ void __launch_bounds__(WARPS * 32, D == 128 ? 3 : 4) kv_step_kernel(c
         }
         const long long kbase = static_cast<long long>(i < nsink ? i : page_lo + i - nsink) * KV_PAGE;
 
-        // x[o]: keys 8o + 2t and 8o + 2t + 1 of row n
-        float x[8][2];
+        // x[o]: keys 8o + 2t and 8o + 2t + 1 of row n (and n + 8); two octets of keys at a time
+        float x[8][SETS][2];
 #pragma unroll
-        for (int oct = 0; oct < 8; ++oct) {
-            const int token = 8 * oct + n;
-            uint32_t w[D / 32];
-            if constexpr (D == 128) {
-                const uint4 v = *reinterpret_cast<const uint4*>(page + P::k_chunk(token, t));
-                w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
-            } else {
-                const uint2 v = *reinterpret_cast<const uint2*>(page + P::k_chunk(token, t / 2) + t % 2 * 8);
-                w[0] = v.x, w[1] = v.y;
+        for (int oct = 0; oct < 8; oct += 2) {
+            uint32_t w[2][D / 32];
+            __half2 s[2], sb[2];
+            float c[2][4];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int token = 8 * (oct + h) + n;
+                if constexpr (D == 128) {
+                    const uint4 v = *reinterpret_cast<const uint4*>(page + P::k_chunk(token, t));
+                    w[h][0] = v.x, w[h][1] = v.y, w[h][2] = v.z, w[h][3] = v.w;
+                } else {
+                    const uint2 v = *reinterpret_cast<const uint2*>(page + P::k_chunk(token, t / 2) + t % 2 * 8);
+                    w[h][0] = v.x, w[h][1] = v.y;
+                }
+                s[h] = __half2half2(*reinterpret_cast<const __half*>(page + P::k_scale(token, D == 128 ? t : t / 2)));
+                sb[h] = kv_addend(s[h]);
             }
-            const __half2 s = __half2half2(
-                *reinterpret_cast<const __half*>(page + P::k_scale(token, D == 128 ? t : t / 2)));
-            const __half2 sb = kv_addend(s);
-            float c[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
             for (int j = 0; j < D / 32; ++j) {
-                mma16816(c, qf[2 * j][0], qf[2 * j][1], qf[2 * j][2], qf[2 * j][3], kv_h2u(kv_widen<0>(w[j], s, sb)),
-                         kv_h2u(kv_widen<1>(w[j], s, sb)));
-                mma16816(c, qf[2 * j + 1][0], qf[2 * j + 1][1], qf[2 * j + 1][2], qf[2 * j + 1][3],
-                         kv_h2u(kv_widen<2>(w[j], s, sb)), kv_h2u(kv_widen<3>(w[j], s, sb)));
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const uint32_t b0 = kv_h2u(kv_widen<0>(w[h][j], s[h], sb[h]));
+                    const uint32_t b1 = kv_h2u(kv_widen<1>(w[h][j], s[h], sb[h]));
+                    if (j == 0)
+                        mma16816_first(c[h], qf[0][0], qf[0][1], qf[0][2], qf[0][3], b0, b1);
+                    else
+                        mma16816(c[h], qf[2 * j][0], qf[2 * j][1], qf[2 * j][2], qf[2 * j][3], b0, b1);
+                }
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    mma16816(c[h], qf[2 * j + 1][0], qf[2 * j + 1][1], qf[2 * j + 1][2], qf[2 * j + 1][3],
+                             kv_h2u(kv_widen<2>(w[h][j], s[h], sb[h])), kv_h2u(kv_widen<3>(w[h][j], s[h], sb[h])));
             }
-            x[oct][0] = (c[0] + c[2]) * coef;
-            x[oct][1] = (c[1] + c[3]) * coef;
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    if constexpr (MODE == WIDE) {
+                        x[oct + h][0][e] = c[h][e];
+                        x[oct + h][1][e] = c[h][e + 2];
+                    } else {
+                        x[oct + h][0][e] = c[h][e] + c[h][e + 2];
+                    }
+                }
         }
 
         // keys past the row's own, before its window (and not among the sinks)
         const bool whole = kbase + KV_PAGE - 1 <= plo &&
                            (g.window == 0 || kbase > phi - g.window || kbase + KV_PAGE <= g.sinks);
         if (!whole) {
-            const int to = static_cast<int>(min(max(pos - kbase, -1ll), static_cast<long long>(KV_PAGE)));
-            const int from = static_cast<int>(min(max(low - kbase, 0ll), static_cast<long long>(KV_PAGE)));
-            const int sink = static_cast<int>(min(max(g.sinks - kbase, 0ll), static_cast<long long>(KV_PAGE)));
 #pragma unroll
-            for (int oct = 0; oct < 8; ++oct)
+            for (int i = 0; i < SETS; ++i) {
+                const uint64_t m = kv_seen_bits(pos[i], kbase, g.window, g.sinks) >> (2 * t);
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const int j = 8 * oct + 2 * t + e;
-                    if (j > to || (j < from && j >= sink))
-                        x[oct][e] = -INFINITY;
-                }
+                for (int oct = 0; oct < 8; ++oct)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e)
+                        if ((m >> (8 * oct + e) & 1u) == 0)
+                            x[oct][i][e] = -INFINITY;
+            }
         }
 
-        float top = x[0][0];
+        float base[SETS];
+        bool raise = false;
+        float next[SETS];
 #pragma unroll
-        for (int oct = 0; oct < 8; ++oct)
-            top = fmaxf(top, fmaxf(x[oct][0], x[oct][1]));
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        const bool raise = top > ref + KV_REF_LIMIT;   // also the first visible key: ref is -inf until then
-        if (__any_sync(0xffffffffu, raise)) {
-            const float next = raise ? top - KV_REF_BELOW : ref;
-            const float f = raise ? kv_ex2(ref - next) : 1.0f;
-            ref = next;
-            sum *= f;
+        for (int i = 0; i < SETS; ++i) {
+            float top = x[0][i][0];
 #pragma unroll
-            for (int j = 0; j < D / 8; ++j)
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    o[j][e] *= f;
+            for (int oct = 0; oct < 8; ++oct)
+                top = fmaxf(top, fmaxf(x[oct][i][0], x[oct][i][1]));
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2)) * coef[i];
+            const bool up = top > ref[i] + KV_REF_LIMIT;   // also the first visible key: ref is -inf until then
+            next[i] = up ? top - KV_REF_BELOW : ref[i];
+            raise |= up;
         }
-        const float base = ref == -INFINITY ? 0.0f : ref;
+        if (__any_sync(0xffffffffu, raise)) {
+#pragma unroll
+            for (int i = 0; i < SETS; ++i) {
+                const float f = next[i] == ref[i] ? 1.0f : kv_ex2(ref[i] - next[i]);
+                ref[i] = next[i];
+                sum[i] *= f;
+                const float f0 = __shfl_sync(0xffffffffu, f, 8 * t), f1 = __shfl_sync(0xffffffffu, f, 8 * t + 4);
+#pragma unroll
+                for (int j = 0; j < D / 16; ++j) {
+                    o[i][j][0] *= f0;
+                    o[i][j][1] *= f1;
+                    o[i][j][2] *= f0;
+                    o[i][j][3] *= f1;
+                }
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < SETS; ++i)
+            base[i] = ref[i] == -INFINITY ? 0.0f : ref[i];
 
         page = next_half();
         if (!ok)
@@ -301,13 +361,19 @@ __global__ void __launch_bounds__(WARPS * 32, D == 128 ? 3 : 4) kv_step_kernel(c
         const int held = static_cast<int>(min(kend - kbase, static_cast<long long>(KV_PAGE)));
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk) {   // keys 16 kk .. 16 kk + 15
-            uint32_t a[4];
+            uint32_t hi[SETS][2], lo[2];
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const float p0 = kv_ex2(x[2 * kk + h][0] - base), p1 = kv_ex2(x[2 * kk + h][1] - base);
-                sum += p0 + p1;
-                kv_split2(p0, p1, a[2 * h], a[2 * h + 1]);
-            }
+            for (int i = 0; i < SETS; ++i)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const float p0 = kv_ex2(fmaf(x[2 * kk + h][i][0], coef[i], -base[i]));
+                    const float p1 = kv_ex2(fmaf(x[2 * kk + h][i][1], coef[i], -base[i]));
+                    sum[i] += p0 + p1;
+                    if constexpr (MODE == HI_LO)
+                        kv_split2(p0, p1, hi[i][h], lo[h]);
+                    else
+                        hi[i][h] = kv_h2u(__floats2half2_rn(p0, p1));
+                }
             uint32_t w[2][D / 32];
             __half2 s[2], sb[2];
 #pragma unroll
@@ -327,16 +393,22 @@ __global__ void __launch_bounds__(WARPS * 32, D == 128 ? 3 : 4) kv_step_kernel(c
                 s[h] = kv_u2h(sc);
                 sb[h] = kv_addend(s[h]);
             }
+            auto step = [&](float (&c0)[4], float (&c1)[4], const uint32_t (&a)[4], const uint32_t (&b)[4], uint32_t p0,
+                            uint32_t p1) {
+                mma16816(c0, a[0], a[1], a[2], a[3], p0, p1);
+                mma16816(c1, b[0], b[1], b[2], b[3], p0, p1);
+            };
 #pragma unroll
-            for (int j = 0; j < D / 32; ++j) {
-                mma16816(o[4 * j], a[0], a[1], a[2], a[3], kv_h2u(kv_widen<0>(w[0][j], s[0], sb[0])),
-                         kv_h2u(kv_widen<0>(w[1][j], s[1], sb[1])));
-                mma16816(o[4 * j + 1], a[0], a[1], a[2], a[3], kv_h2u(kv_widen<1>(w[0][j], s[0], sb[0])),
-                         kv_h2u(kv_widen<1>(w[1][j], s[1], sb[1])));
-                mma16816(o[4 * j + 2], a[0], a[1], a[2], a[3], kv_h2u(kv_widen<2>(w[0][j], s[0], sb[0])),
-                         kv_h2u(kv_widen<2>(w[1][j], s[1], sb[1])));
-                mma16816(o[4 * j + 3], a[0], a[1], a[2], a[3], kv_h2u(kv_widen<3>(w[0][j], s[0], sb[0])),
-                         kv_h2u(kv_widen<3>(w[1][j], s[1], sb[1])));
+            for (int j = 0; j < D / 32; ++j) {   // values 4 j .. 4 j + 3 of the lane's
+                const uint32_t a[4] = {kv_h2u(kv_widen<0>(w[0][j], s[0], sb[0])), kv_h2u(kv_widen<1>(w[0][j], s[0], sb[0])),
+                                       kv_h2u(kv_widen<0>(w[1][j], s[1], sb[1])), kv_h2u(kv_widen<1>(w[1][j], s[1], sb[1]))};
+                const uint32_t b[4] = {kv_h2u(kv_widen<2>(w[0][j], s[0], sb[0])), kv_h2u(kv_widen<3>(w[0][j], s[0], sb[0])),
+                                       kv_h2u(kv_widen<2>(w[1][j], s[1], sb[1])), kv_h2u(kv_widen<3>(w[1][j], s[1], sb[1]))};
+#pragma unroll
+                for (int i = 0; i < SETS; ++i)
+                    step(o[i][2 * j], o[i][2 * j + 1], a, b, hi[i][0], hi[i][1]);
+                if constexpr (MODE == HI_LO)
+                    step(o[0][2 * j], o[0][2 * j + 1], a, b, lo[0], lo[1]);
             }
         }
     }
@@ -347,28 +419,28 @@ __global__ void __launch_bounds__(WARPS * 32, D == 128 ? 3 : 4) kv_step_kernel(c
                 mbar_drain_wait(bar + 8 * s, parity >> s & 1u, WAIT_LIMIT_NS, g.wc.err);
     }
 
-    // join the warps: column c of the output operand holds values D/8 c .. D/8 c + D/8 - 1
-    sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-    sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+    grid_dep_launch();
+    // join the warps
     __syncthreads();
     float2* ml = reinterpret_cast<float2*>(smem + S::ML);
-    if (t == 0)
-        ml[warp * ROWS + n] = make_float2(ref, sum);
     float* os = reinterpret_cast<float*>(smem + S::RING);
 #pragma unroll
-    for (int c = 0; c < 2; ++c)
+    for (int i = 0; i < SETS; ++i) {
+        sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], 1);
+        sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], 2);
+        if (t == 0)
+            ml[warp * ROWS + n + 8 * i] = make_float2(ref[i], sum[i]);
 #pragma unroll
-        for (int j = 0; j < D / 32; ++j) {
-            float4 v;
-            v.x = o[4 * j][c] + o[4 * j][c + 2];
-            v.y = o[4 * j + 1][c] + o[4 * j + 1][c + 2];
-            v.z = o[4 * j + 2][c] + o[4 * j + 2][c + 2];
-            v.w = o[4 * j + 3][c] + o[4 * j + 3][c + 2];
-            *reinterpret_cast<float4*>(os + (warp * ROWS + n) * S::OROW + (2 * t + c) * (D / 8) + 4 * j) = v;
-        }
+        for (int e = 0; e < 2; ++e)
+#pragma unroll
+            for (int j = 0; j < D / 32; ++j)
+                *reinterpret_cast<float4*>(os + (warp * ROWS + 2 * t + e + 8 * i) * S::OROW + n * (D / 8) + 4 * j) =
+                    make_float4(o[i][2 * j][e], o[i][2 * j][e + 2], o[i][2 * j + 1][e], o[i][2 * j + 1][e + 2]);
+    }
     __syncthreads();
 
-    const int r = threadIdx.x / 16, l = threadIdx.x % 16;   // 16 threads a row
+    constexpr int LANES = WARPS * 32 / ROWS;   // threads a row
+    const int r = threadIdx.x / LANES, l = threadIdx.x % LANES;
     if (r >= nrow)
         return;
     float top = -INFINITY, total = 0.0f, f[WARPS];
@@ -385,8 +457,8 @@ __global__ void __launch_bounds__(WARPS * 32, D == 128 ? 3 : 4) kv_step_kernel(c
     const long long token = first + row / g.group;
     const int h = head * g.group + row % g.group;
 #pragma unroll
-    for (int j = 0; j < D / 64; ++j) {
-        const int d = 64 * j + 4 * l;
+    for (int j = 0; j < D / (4 * LANES); ++j) {
+        const int d = 4 * (LANES * j + l);
         float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
         for (int w = 0; w < WARPS; ++w) {
@@ -476,17 +548,28 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) kv_join_kernel(const AttendAr
            v, g.wide);
 }
 
-template <int D, typename T>
+template <int D, typename T, int MODE>
 cudaError_t launch_step(const AttendArgs& a, cudaStream_t s)
 {
+    constexpr int BYTES = StepSmem<D, MODE>::BYTES;
     static std::atomic<uint64_t> done{0};
-    const cudaError_t e = kv_allow_smem(kv_step_kernel<D, T>, StepSmem<D>::BYTES, &done);
+    const cudaError_t e = kv_allow_smem(kv_step_kernel<D, T, MODE>, BYTES, &done);
     if (e != cudaSuccess)
         return e;
     const unsigned int grid = static_cast<unsigned int>(static_cast<long long>(a.nsplit) * a.c.kv_heads * a.row_tiles *
                                                         a.c.batch);
     count_launch();
-    return launch_dependent_smem(kv_step_kernel<D, T>, dim3(grid), dim3(WARPS * 32), StepSmem<D>::BYTES, s, a);
+    return launch_dependent_smem(kv_step_kernel<D, T, MODE>, dim3(grid), dim3(WARPS * 32), BYTES, s, a);
+}
+
+template <int D>
+cudaError_t launch_step(const AttendArgs& a, int dtype, cudaStream_t s)
+{
+    if (dtype == KV_F32)
+        return launch_step<D, float, HI_LO>(a, s);
+    if (a.tile_rows == 8)
+        return dtype == KV_F16 ? launch_step<D, __half, ONE_PART>(a, s) : launch_step<D, __nv_bfloat16, ONE_PART>(a, s);
+    return dtype == KV_F16 ? launch_step<D, __half, WIDE>(a, s) : launch_step<D, __nv_bfloat16, WIDE>(a, s);
 }
 
 template <int D, typename T>
@@ -501,13 +584,7 @@ cudaError_t launch_join(const AttendArgs& a, cudaStream_t s)
 
 cudaError_t launch_kv_step(const AttendArgs& a, int dim, int dtype, cudaStream_t s)
 {
-    if (dim == 128)
-        return dtype == KV_F32   ? launch_step<128, float>(a, s)
-               : dtype == KV_F16 ? launch_step<128, __half>(a, s)
-                                 : launch_step<128, __nv_bfloat16>(a, s);
-    return dtype == KV_F32   ? launch_step<64, float>(a, s)
-           : dtype == KV_F16 ? launch_step<64, __half>(a, s)
-                             : launch_step<64, __nv_bfloat16>(a, s);
+    return dim == 128 ? launch_step<128>(a, dtype, s) : launch_step<64>(a, dtype, s);
 }
 
 cudaError_t launch_kv_join(const AttendArgs& a, int dim, int dtype, cudaStream_t s)
