@@ -105,10 +105,11 @@ mmq_status check_rows(const mmq_rows* r, int ntok, int heads, int dim, bool writ
     return MMQ_OK;
 }
 
-// Whether four elements from a multiple of four on may be loaded at once.
-bool wide(const mmq_rows* r)
+// Whether accesses of `bytes` from multiples of so many on are aligned in every row.
+bool wide(const mmq_rows* r, int bytes)
 {
-    return aligned(r->data, r->dtype == MMQ_F32 ? 16 : 8) && r->token_stride % 4 == 0 && r->head_stride % 4 == 0;
+    const int n = bytes / (r->dtype == MMQ_F32 ? 4 : 2);
+    return aligned(r->data, static_cast<uintptr_t>(bytes)) && r->token_stride % n == 0 && r->head_stride % n == 0;
 }
 
 KvRows rows(const mmq_rows* r) { return {r->data, r->token_stride, r->head_stride}; }
@@ -145,7 +146,7 @@ mmq_status move_rows(bool write, const mmq_kv_cache* c, const mmq_rows* k, const
     if ((st = view(c, &cv)) != MMQ_OK)
         return st;
     const auto launch = write ? mmq::launch_kv_write : mmq::launch_kv_read;
-    return mmq::from_cuda(launch(cv, c->head_dim, k->dtype, rows(k), rows(v), wide(k) && wide(v), ntok,
+    return mmq::from_cuda(launch(cv, c->head_dim, k->dtype, rows(k), rows(v), wide(k, 16) && wide(v, 16), ntok,
                                  reinterpret_cast<cudaStream_t>(s)));
 }
 
@@ -253,7 +254,8 @@ mmq_status mmq_kv_attend(const mmq_kv_cache* c, const mmq_rows* q, const mmq_row
     a.row_tiles = p.row_tiles;
     a.nsplit = p.nsplit;
     a.part_pages = p.part_pages;
-    a.wide = wide(q) && wide(out);
+    const int four = q->dtype == MMQ_F32 ? 16 : 8;   // bytes of four elements
+    a.wide = wide(q, four) && wide(out, four);
     a.part = static_cast<float*>(workspace);
     a.part_ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(workspace) + p.part_bytes);
     a.wc = {a.c.bad - 1, mmq::WAIT_LIMIT_NS, -1};

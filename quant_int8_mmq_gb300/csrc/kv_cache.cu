@@ -7,9 +7,12 @@
 // to k + 1/2 only if x equals it, so the codes are the nearest ones, ties to even, and do
 // not depend on how the work is laid out.
 //
-// Both kernels move bytes: a warp takes one (token, head), each lane four values, so
-// that rows are read and written in whole 128-byte lines.  Writing, a group's largest
-// magnitude is three shuffles within its 8 lanes.
+// Both kernels move bytes.  A lane holds 8 consecutive values of a key or a value row
+// (one code word of a key), a warp the key and the value of one head (two heads of 64),
+// so rows move as 16-byte accesses in whole lines and a group's largest magnitude is two
+// shuffles among its 4 lanes; a warp keeps its token and walks over heads, which shares
+// the search for the token's place.  The 8 warps of a CTA hold consecutive tokens, whose
+// value codes share their sectors.
 #include "kv.cuh"
 
 namespace mmq {
@@ -17,10 +20,9 @@ namespace {
 
 constexpr int WARPS = 8;
 
-// The piece and slot of packed row r and one head; piece null (and the cache's error word
-// set) when the row has no place in the cache.
-template <int D>
-__device__ __forceinline__ uint8_t* piece_of(const KvView& c, int r, int head, int lane, int* slot)
+// Offset of the page of packed row r in the pool, and its slot there; -1 (and the cache's
+// error word set) when the row has no place in the cache.
+__device__ __forceinline__ long long page_of(const KvView& c, int r, long long page_bytes, int lane, int* slot)
 {
     const int b = kv_sequence_of(c.start, c.batch, r, lane);
     const int first = c.start[b], end = c.start[b + 1];
@@ -29,137 +31,188 @@ __device__ __forceinline__ uint8_t* piece_of(const KvView& c, int r, int head, i
         const int page = c.table[static_cast<size_t>(b) * c.max_pages + static_cast<size_t>(pos / KV_PAGE)];
         if (page >= 0 && page < c.num_pages) {
             *slot = static_cast<int>(pos % KV_PAGE);
-            return c.pages + (static_cast<size_t>(page) * c.kv_heads + head) * Piece<D>::BYTES;
+            return page * page_bytes;
         }
     }
     if (lane == 0)
         *c.bad = 1u;
     *slot = 0;
-    return nullptr;
+    return -1;
 }
 
-__device__ __forceinline__ uint32_t code_of(float x, float s)
-{
-    const float y = x == x ? rintf(__fdiv_rn(x, s)) : 0.0f;
-    return static_cast<uint32_t>(static_cast<int>(fminf(fmaxf(y, -8.0f), 7.0f)) + 8);
-}
+// How a warp's lanes share the rows of a head: LANES lanes a row, keys then values.
+template <int D>
+struct Share {
+    static constexpr int LANES = D / 8;
+    static constexpr int HEADS = 32 / (2 * LANES);   // heads at once
+};
 
-// Codes and scale of this lane's four values; every 8 lanes hold one group.
-__device__ __forceinline__ void quantise(float4 x, uint32_t (&n)[4], __half* scale)
+// Eight elements from p on; `wide` when p is aligned to 16 bytes.
+template <typename T>
+__device__ __forceinline__ void load8(const T* p, bool wide, float (&x)[8])
 {
-    float a = fmaxf(fmaxf(fabsf(x.x), fabsf(x.y)), fmaxf(fabsf(x.z), fabsf(x.w)));
+    T e[8];
+    if (wide) {
 #pragma unroll
-    for (int d = 1; d < 8; d <<= 1)
-        a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, d));
-    const uint32_t up = (__float_as_uint(__fdiv_rn(a, 7.5f)) + 0x1FFFFu) & ~0x1FFFFu;
-    const float s = fminf(fmaxf(__uint_as_float(up), KV_SCALE_MIN), KV_SCALE_MAX);
-    n[0] = code_of(x.x, s);
-    n[1] = code_of(x.y, s);
-    n[2] = code_of(x.z, s);
-    n[3] = code_of(x.w, s);
-    *scale = __float2half_rn(s);   // exact
+        for (int i = 0; i < static_cast<int>(sizeof(T)) / 2; ++i)
+            reinterpret_cast<uint4*>(e)[i] = __ldg(reinterpret_cast<const uint4*>(p) + i);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            e[i] = p[i];
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        x[i] = Elt<T>::to(e[i]);
 }
 
-// Lane l of a head holds values 4l .. 4l + 3.  (u, p, h) of value 8u + 2p + h: an even lane
-// has p = 0, 1 of its word, the odd lane after it p = 2, 3.
-template <int D>
-__device__ __forceinline__ void put_key(uint8_t* piece, int slot, int l, float4 x)
+// x / y rounded to nearest, r being 1 / y rounded to nearest: the quotient's error, exact in
+// an fma, corrects it (P. Markstein, IBM J. Res. Dev. 34, 1990).  Where the error underflows
+// the quotient is far below every rounding boundary used here.
+__device__ __forceinline__ float quotient(float x, float y, float r)
 {
-    uint32_t n[4];
-    __half s;
-    quantise(x, n, &s);
-    const uint32_t part = n[0] | n[1] << 16 | n[2] << 4 | n[3] << 20;
-    const uint32_t odd = __shfl_down_sync(0xffffffffu, part, 1);
-    if (piece == nullptr)
-        return;
-    if (l % 2 == 0)
-        *reinterpret_cast<uint32_t*>(piece + Piece<D>::k_chunk(slot, l / 8) + (l % 8) * 2) = part | odd << 8;
-    if (l % 8 == 0)
-        *reinterpret_cast<__half*>(piece + Piece<D>::k_scale(slot, l / 8)) = s;
-}
-
-template <int D>
-__device__ __forceinline__ void put_value(uint8_t* piece, int slot, int l, float4 x)
-{
-    uint32_t n[4];
-    __half s;
-    quantise(x, n, &s);
-    if (piece == nullptr)
-        return;
-    const int pair = slot / 2, e = slot % 2;
-    *reinterpret_cast<uint16_t*>(piece + Piece<D>::v_chunk(pair, l / 4) + (l % 4) * 4 + e * 2) =
-        static_cast<uint16_t>(n[0] | n[1] << 4 | n[2] << 8 | n[3] << 12);
-    if (l % 8 == 0)
-        *reinterpret_cast<__half*>(piece + Piece<D>::v_scale(pair, l / 8) + e * 2) = s;
+    const float q = x * r;
+    return fmaf(fmaf(-q, y, x), r, q);
 }
 
 template <int D, typename T>
 __global__ void __launch_bounds__(WARPS * 32) kv_write_kernel(const KvView c, const KvRows k, const KvRows v, bool wide,
-                                                              long long units)
+                                                              int ntok, int heads_a_warp)
 {
-    const long long u = static_cast<long long>(blockIdx.x) * WARPS + threadIdx.x / 32;
-    if (u >= units)
+    using P = Piece<D>;
+    constexpr int LANES = Share<D>::LANES;
+    const int r = blockIdx.x * WARPS + threadIdx.x / 32, lane = threadIdx.x % 32;
+    if (r >= ntok)
         return;
-    const int lane = threadIdx.x % 32;
-    const int r = static_cast<int>(u / c.kv_heads), head = static_cast<int>(u % c.kv_heads);
-    const T* kr = static_cast<const T*>(k.data) + r * k.tok + head * k.head;
-    const T* vr = static_cast<const T*>(v.data) + r * v.tok + head * v.head;
+    const long long page_bytes = static_cast<long long>(c.kv_heads) * P::BYTES;
     int slot;
-    if constexpr (D == 128) {
-        const float4 x = load4(kr + 4 * lane, wide), y = load4(vr + 4 * lane, wide);
-        uint8_t* piece = piece_of<D>(c, r, head, lane, &slot);
-        put_key<D>(piece, slot, lane, x);
-        put_value<D>(piece, slot, lane, y);
-    } else {   // the lower half of the warp takes the key, the upper half the value
-        const float4 x = load4((lane < 16 ? kr : vr) + 4 * (lane % 16), wide);
-        uint8_t* piece = piece_of<D>(c, r, head, lane, &slot);
-        put_key<D>(lane < 16 ? piece : nullptr, slot, lane % 16, x);
-        put_value<D>(lane < 16 ? nullptr : piece, slot, lane % 16, x);
+    const long long page = page_of(c, r, page_bytes, lane, &slot);
+    const int l = lane % LANES;
+    const bool key = lane / LANES % 2 == 0;
+    const int h0 = blockIdx.y * heads_a_warp, h1 = min(c.kv_heads, h0 + heads_a_warp);
+    const KvRows& in = key ? k : v;
+    const T* row = static_cast<const T*>(in.data) + r * in.tok + 8 * l;
+    // this lane's codes and its group's scale in a piece
+    const int codes = key ? P::k_chunk(slot, l / 4) + l % 4 * 4 : P::v_chunk(slot / 2, l / 2) + l % 2 * 8 + slot % 2 * 2;
+    const int scale = key ? P::k_scale(slot, l / 4) : P::v_scale(slot / 2, l / 4) + slot % 2 * 2;
+    uint8_t* pages = c.pages + page;
+#pragma unroll 2
+    for (int h = h0; h < h1; h += Share<D>::HEADS) {
+        const int head = h + lane / (2 * LANES);
+        const bool mine = head < h1;
+        float x[8];
+        load8(row + (mine ? head : h) * in.head, wide, x);
+        float a = 0.0f;
+        bool odd = false;   // some x is no number
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            a = fmaxf(a, fabsf(x[i]));
+            odd |= x[i] != x[i];
+        }
+        if (odd) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                x[i] = x[i] == x[i] ? x[i] : 0.0f;
+        }
+        a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 1));
+        a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 2));
+        const float amax = fminf(a, 1e30f);   // the scale's limit is far below
+        const uint32_t up = (__float_as_uint(quotient(amax, 7.5f, 1.0f / 7.5f)) + 0x1FFFFu) & ~0x1FFFFu;
+        const float s = fminf(fmaxf(__uint_as_float(up), KV_SCALE_MIN), KV_SCALE_MAX);
+        const float inv = __frcp_rn(s);
+        // code = rint(x / s) + 8 in the low bits of 1.5 * 2^23 + 8 + x / s; limiting x to [-8 s, 7 s]
+        // limits the rounded quotient to [-8, 7]
+        uint32_t n[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            n[i] = __float_as_uint(quotient(fminf(fmaxf(x[i], -8.0f * s), 7.0f * s), s, inv) + 12582920.0f);
+        // 16-bit halves of four codes: key values 0 2 4 6 | 1 3 5 7, value values 0 1 2 3 | 4 5 6 7
+        const uint32_t lo = n[0] + ((key ? n[2] : n[1]) << 4) + ((key ? n[4] : n[2]) << 8) + ((key ? n[6] : n[3]) << 12);
+        const uint32_t hi = (key ? n[1] : n[4]) + ((key ? n[3] : n[5]) << 4) + ((key ? n[5] : n[6]) << 8) + (n[7] << 12);
+        if (!mine || page < 0)
+            continue;
+        uint8_t* piece = pages + head * P::BYTES;
+        if (key) {
+            *reinterpret_cast<uint32_t*>(piece + codes) = __byte_perm(lo, hi, 0x5410);
+        } else {
+            *reinterpret_cast<uint16_t*>(piece + codes) = static_cast<uint16_t>(lo);
+            *reinterpret_cast<uint16_t*>(piece + codes + 4) = static_cast<uint16_t>(hi);
+        }
+        if (l % 4 == 0)
+            *reinterpret_cast<__half*>(piece + scale) = __float2half_rn(s);   // exact
     }
 }
 
-// Code n of scale s; the difference and the product are exact.
-__device__ __forceinline__ float value_of(uint32_t n, float s) { return s * (static_cast<float>(n & 15u) - 8.0f); }
-
-template <int D>
-__device__ __forceinline__ float4 get_key(const uint8_t* piece, int slot, int l)
+template <typename T>
+__device__ __forceinline__ void store8(T* p, bool wide, const __half2 (&x)[4])
 {
-    const uint32_t w = *reinterpret_cast<const uint32_t*>(piece + Piece<D>::k_chunk(slot, l / 8) + (l % 8 / 2) * 4) >>
-                       (l % 2 * 8);
-    const float s = __half2float(*reinterpret_cast<const __half*>(piece + Piece<D>::k_scale(slot, l / 8)));
-    return make_float4(value_of(w, s), value_of(w >> 16, s), value_of(w >> 4, s), value_of(w >> 20, s));
-}
-template <int D>
-__device__ __forceinline__ float4 get_value(const uint8_t* piece, int slot, int l)
-{
-    const int pair = slot / 2, e = slot % 2;
-    const uint32_t w =
-        *reinterpret_cast<const uint16_t*>(piece + Piece<D>::v_chunk(pair, l / 4) + (l % 4) * 4 + e * 2);
-    const float s = __half2float(*reinterpret_cast<const __half*>(piece + Piece<D>::v_scale(pair, l / 8) + e * 2));
-    return make_float4(value_of(w, s), value_of(w >> 4, s), value_of(w >> 8, s), value_of(w >> 12, s));
+    T e[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 f = __half22float2(x[i]);
+        e[2 * i] = Elt<T>::from(f.x);
+        e[2 * i + 1] = Elt<T>::from(f.y);
+    }
+    if (wide) {
+#pragma unroll
+        for (int i = 0; i < static_cast<int>(sizeof(T)) / 2; ++i)
+            reinterpret_cast<uint4*>(p)[i] = reinterpret_cast<uint4*>(e)[i];
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            p[i] = e[i];
+    }
 }
 
 template <int D, typename T>
 __global__ void __launch_bounds__(WARPS * 32) kv_read_kernel(const KvView c, const KvRows k, const KvRows v, bool wide,
-                                                             long long units)
+                                                             int ntok, int heads_a_warp)
 {
-    const long long u = static_cast<long long>(blockIdx.x) * WARPS + threadIdx.x / 32;
-    if (u >= units)
+    using P = Piece<D>;
+    constexpr int LANES = Share<D>::LANES;
+    const int r = blockIdx.x * WARPS + threadIdx.x / 32, lane = threadIdx.x % 32;
+    if (r >= ntok)
         return;
-    const int lane = threadIdx.x % 32;
-    const int r = static_cast<int>(u / c.kv_heads), head = static_cast<int>(u % c.kv_heads);
-    T* kr = static_cast<T*>(k.data) + r * k.tok + head * k.head;
-    T* vr = static_cast<T*>(v.data) + r * v.tok + head * v.head;
+    const long long page_bytes = static_cast<long long>(c.kv_heads) * P::BYTES;
     int slot;
-    const uint8_t* piece = piece_of<D>(c, r, head, lane, &slot);
-    const float4 none = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    if constexpr (D == 128) {
-        store4(kr + 4 * lane, piece ? get_key<D>(piece, slot, lane) : none, wide);
-        store4(vr + 4 * lane, piece ? get_value<D>(piece, slot, lane) : none, wide);
-    } else {
-        const int l = lane % 16;
-        const float4 x = piece == nullptr ? none : lane < 16 ? get_key<D>(piece, slot, l) : get_value<D>(piece, slot, l);
-        store4((lane < 16 ? kr : vr) + 4 * l, x, wide);
+    const long long page = page_of(c, r, page_bytes, lane, &slot);
+    const int l = lane % LANES;
+    const bool key = lane / LANES % 2 == 0;
+    const int h0 = blockIdx.y * heads_a_warp, h1 = min(c.kv_heads, h0 + heads_a_warp);
+    const KvRows& out = key ? k : v;
+    T* row = static_cast<T*>(out.data) + r * out.tok + 8 * l;
+    const int codes = key ? P::k_chunk(slot, l / 4) + l % 4 * 4 : P::v_chunk(slot / 2, l / 2) + l % 2 * 8;
+    const int scale = key ? P::k_scale(slot, l / 4) : P::v_scale(slot / 2, l / 4) + slot % 2 * 2;
+    const uint32_t half = slot % 2 ? 0x7632 : 0x5410;   // this token's 16 bits of each word
+    const uint8_t* pages = c.pages + max(page, 0ll);
+#pragma unroll 2
+    for (int h = h0 + lane / (2 * LANES); h < h1; h += Share<D>::HEADS) {
+        __half2 x[4];
+        if (page >= 0) {
+            const uint8_t* piece = pages + h * P::BYTES;
+            // pairs 0 and 1 at nibble 0 and the next (key) or the one after (value) of z0, 2 and 3 of z1
+            uint32_t z0, z1;
+            if (key) {
+                z0 = __ldg(reinterpret_cast<const unsigned int*>(piece + codes));
+                z1 = z0 >> 8;
+            } else {   // both tokens' words; this token's half of each, beside itself moved by a value
+                const uint2 w = __ldg(reinterpret_cast<const uint2*>(piece + codes));
+                const uint32_t m = __byte_perm(w.x, w.y, half);
+                z0 = __byte_perm(m, m >> 4, 0x5410);
+                z1 = __byte_perm(m, m >> 4, 0x7632);
+            }
+            const __half2 s = __half2half2(__ushort_as_half(__ldg(reinterpret_cast<const unsigned short*>(piece + scale))));
+            const int next = key ? 4 : 8;
+            x[0] = kv_widen<0>(z0, s, s);
+            x[1] = kv_widen<0>(z0 >> next, s, s);
+            x[2] = kv_widen<0>(z1, s, s);
+            x[3] = kv_widen<0>(z1 >> next, s, s);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                x[i] = __floats2half2_rn(0.0f, 0.0f);
+        }
+        store8(row + h * out.head, wide, x);
     }
 }
 
@@ -167,13 +220,16 @@ template <int D, typename T>
 cudaError_t launch_rows(bool write, const KvView& c, const KvRows& k, const KvRows& v, bool wide, int ntok,
                         cudaStream_t s)
 {
-    const long long units = static_cast<long long>(ntok) * c.kv_heads;
-    const unsigned int blocks = static_cast<unsigned int>((units + WARPS - 1) / WARPS);
+    // a warp takes more heads of its token once every SM has its 64 warps
+    const long long spread = static_cast<long long>(ntok) * c.kv_heads / (152 * 64);
+    int heads = static_cast<int>(spread < 1 ? 1 : spread > 8 ? 8 : spread);
+    heads = (heads + Share<D>::HEADS - 1) / Share<D>::HEADS * Share<D>::HEADS;
+    const dim3 grid((ntok + WARPS - 1) / WARPS, (c.kv_heads + heads - 1) / heads);
     count_launch();
     if (write)
-        kv_write_kernel<D, T><<<blocks, WARPS * 32, 0, s>>>(c, k, v, wide, units);
+        kv_write_kernel<D, T><<<grid, WARPS * 32, 0, s>>>(c, k, v, wide, ntok, heads);
     else
-        kv_read_kernel<D, T><<<blocks, WARPS * 32, 0, s>>>(c, k, v, wide, units);
+        kv_read_kernel<D, T><<<grid, WARPS * 32, 0, s>>>(c, k, v, wide, ntok, heads);
     return cudaGetLastError();
 }
 
