@@ -84,6 +84,8 @@ __global__ void __launch_bounds__(WARPS * 32) kv_write_kernel(const KvView c, co
     const int r = blockIdx.x * WARPS + threadIdx.x / 32, lane = threadIdx.x % 32;
     if (r >= ntok)
         return;
+    grid_dep_wait();
+    grid_dep_launch();
     const long long page_bytes = static_cast<long long>(c.kv_heads) * P::BYTES;
     int slot;
     const long long page = page_of(c, r, page_bytes, lane, &slot);
@@ -96,12 +98,17 @@ __global__ void __launch_bounds__(WARPS * 32) kv_write_kernel(const KvView c, co
     const int codes = key ? P::k_chunk(slot, l / 4) + l % 4 * 4 : P::v_chunk(slot / 2, l / 2) + l % 2 * 8 + slot % 2 * 2;
     const int scale = key ? P::k_scale(slot, l / 4) : P::v_scale(slot / 2, l / 4) + slot % 2 * 2;
     uint8_t* pages = c.pages + page;
-#pragma unroll 2
+    float ahead[8];   // the next head's values, on their way
+    load8(row + min(h0 + lane / (2 * LANES), h1 - 1) * in.head, wide, ahead);
     for (int h = h0; h < h1; h += Share<D>::HEADS) {
         const int head = h + lane / (2 * LANES);
         const bool mine = head < h1;
         float x[8];
-        load8(row + (mine ? head : h) * in.head, wide, x);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            x[i] = ahead[i];
+        if (h + Share<D>::HEADS < h1)
+            load8(row + min(head + Share<D>::HEADS, h1 - 1) * in.head, wide, ahead);
         float a = 0.0f;
         bool odd = false;   // some x is no number
 #pragma unroll
@@ -173,6 +180,8 @@ __global__ void __launch_bounds__(WARPS * 32) kv_read_kernel(const KvView c, con
     const int r = blockIdx.x * WARPS + threadIdx.x / 32, lane = threadIdx.x % 32;
     if (r >= ntok)
         return;
+    grid_dep_wait();
+    grid_dep_launch();
     const long long page_bytes = static_cast<long long>(c.kv_heads) * P::BYTES;
     int slot;
     const long long page = page_of(c, r, page_bytes, lane, &slot);
@@ -185,34 +194,51 @@ __global__ void __launch_bounds__(WARPS * 32) kv_read_kernel(const KvView c, con
     const int scale = key ? P::k_scale(slot, l / 4) : P::v_scale(slot / 2, l / 4) + slot % 2 * 2;
     const uint32_t half = slot % 2 ? 0x7632 : 0x5410;   // this token's 16 bits of each word
     const uint8_t* pages = c.pages + max(page, 0ll);
-#pragma unroll 2
-    for (int h = h0 + lane / (2 * LANES); h < h1; h += Share<D>::HEADS) {
-        __half2 x[4];
-        if (page >= 0) {
-            const uint8_t* piece = pages + h * P::BYTES;
-            // pairs 0 and 1 at nibble 0 and the next (key) or the one after (value) of z0, 2 and 3 of z1
-            uint32_t z0, z1;
-            if (key) {
-                z0 = __ldg(reinterpret_cast<const unsigned int*>(piece + codes));
-                z1 = z0 >> 8;
-            } else {   // both tokens' words; this token's half of each, beside itself moved by a value
-                const uint2 w = __ldg(reinterpret_cast<const uint2*>(piece + codes));
-                const uint32_t m = __byte_perm(w.x, w.y, half);
-                z0 = __byte_perm(m, m >> 4, 0x5410);
-                z1 = __byte_perm(m, m >> 4, 0x7632);
-            }
-            const __half2 s = __half2half2(__ushort_as_half(__ldg(reinterpret_cast<const unsigned short*>(piece + scale))));
-            const int next = key ? 4 : 8;
-            x[0] = kv_widen<0>(z0, s, s);
-            x[1] = kv_widen<0>(z0 >> next, s, s);
-            x[2] = kv_widen<0>(z1, s, s);
-            x[3] = kv_widen<0>(z1 >> next, s, s);
-        } else {
+    // a batch's loads are all in flight before its first store
+    constexpr int BATCH = 4;
+    const int step = Share<D>::HEADS, next = key ? 4 : 8;
+    for (int h = h0 + lane / (2 * LANES); h < h1; h += BATCH * step) {
+        uint32_t z0[BATCH], z1[BATCH];
+        __half2 s[BATCH];
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                x[i] = __floats2half2_rn(0.0f, 0.0f);
+        for (int i = 0; i < BATCH; ++i) {
+            if (page < 0 || h + i * step >= h1)
+                continue;
+            const uint8_t* piece = pages + (h + i * step) * P::BYTES;
+            if (key) {
+                z0[i] = __ldg(reinterpret_cast<const unsigned int*>(piece + codes));
+            } else {
+                const uint2 w = __ldg(reinterpret_cast<const uint2*>(piece + codes));   // both tokens'
+                z0[i] = w.x;
+                z1[i] = w.y;
+            }
+            s[i] = __half2half2(__ushort_as_half(__ldg(reinterpret_cast<const unsigned short*>(piece + scale))));
         }
-        store8(row + h * out.head, wide, x);
+#pragma unroll
+        for (int i = 0; i < BATCH; ++i) {
+            if (h + i * step >= h1)
+                break;
+            __half2 x[4];
+            if (page >= 0) {
+                // pairs 0 and 1 at nibble 0 and the next (key) or the one after (value) of z0, 2 and 3 of z1
+                if (key) {
+                    z1[i] = z0[i] >> 8;
+                } else {   // this token's half of each word, beside itself moved by a value
+                    const uint32_t m = __byte_perm(z0[i], z1[i], half);
+                    z0[i] = __byte_perm(m, m >> 4, 0x5410);
+                    z1[i] = __byte_perm(m, m >> 4, 0x7632);
+                }
+                x[0] = kv_widen<0>(z0[i], s[i], s[i]);
+                x[1] = kv_widen<0>(z0[i] >> next, s[i], s[i]);
+                x[2] = kv_widen<0>(z1[i], s[i], s[i]);
+                x[3] = kv_widen<0>(z1[i] >> next, s[i], s[i]);
+            } else {
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    x[j] = __floats2half2_rn(0.0f, 0.0f);
+            }
+            store8(row + (h + i * step) * out.head, wide, x);
+        }
     }
 }
 
@@ -227,10 +253,8 @@ cudaError_t launch_rows(bool write, const KvView& c, const KvRows& k, const KvRo
     const dim3 grid((ntok + WARPS - 1) / WARPS, (c.kv_heads + heads - 1) / heads);
     count_launch();
     if (write)
-        kv_write_kernel<D, T><<<grid, WARPS * 32, 0, s>>>(c, k, v, wide, ntok, heads);
-    else
-        kv_read_kernel<D, T><<<grid, WARPS * 32, 0, s>>>(c, k, v, wide, ntok, heads);
-    return cudaGetLastError();
+        return launch_dependent(kv_write_kernel<D, T>, grid, dim3(WARPS * 32), s, c, k, v, wide, ntok, heads);
+    return launch_dependent(kv_read_kernel<D, T>, grid, dim3(WARPS * 32), s, c, k, v, wide, ntok, heads);
 }
 
 template <int D>
