@@ -11,8 +11,8 @@
 // likewise: f32 rows use both parts (four products a tile, 22-bit operands), 16-bit rows
 // are exact in hi (bf16 to 2^-24 of the row's largest) and round P to f16.
 //
-// TMEM: S of each tile in 128 columns, its P (hi, lo) over the S that it came from, O in
-// D columns.  The tiles alternate on the tensor pipe, P V and the next Q K^T of one
+// TMEM: S of each tile in 128 columns, its P over the S that it came from (per 32 keys 16
+// columns of hi and 16 of lo), O in D columns.  The tiles alternate on the tensor pipe, P V and the next Q K^T of one
 // while the other's softmax runs: a thread per row reads S, keeps the row's reference and
 // sum, and writes P.  A row's O is rescaled only when its reference moves, which the
 // lag of kv.cuh makes rare, by the softmax thread itself: its S arrived behind the last
@@ -68,17 +68,48 @@ struct Cfg {
 
 constexpr uint32_t S_COL = 0, O_COL = 256;   // tile w: S at 128 w, O at 256 + D w
 
-__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&v)[32])
+// Starts the load of 32 columns of this thread's TMEM lane; the values are there after
+// tmem_arrived on the same array.
+__device__ __forceinline__ void tmem_load32(uint32_t taddr, uint32_t (&r)[32])
+{
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(taddr)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_arrived(uint32_t (&r)[32])
+{
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
+                 :
+                 : "memory");
+}
+__device__ __forceinline__ void tmem_store16(uint32_t taddr, const uint32_t (&v)[16])
+{
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+        "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+        : "memory");
+}
+__device__ __forceinline__ void tmem_store32(uint32_t taddr, const uint32_t (&v)[32])
 {
     asm volatile(
         "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
-        "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,"
-        "%30,%31,%32};\n" ::"r"(taddr),
-        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
-        "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(v[16]), "r"(v[17]), "r"(v[18]),
-        "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]),
-        "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
+        "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(v[16]), "r"(v[17]), "r"(v[18]), "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]), "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
         : "memory");
+}
+
+__device__ __forceinline__ float2 fadd2(float2 a, float2 b)
+{
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;"
+        : "=l"(d)
+        : "l"(*reinterpret_cast<uint64_t*>(&a)), "l"(*reinterpret_cast<uint64_t*>(&b)));
+    return *reinterpret_cast<float2*>(&d);
 }
 
 // What a CTA works on; the same in every thread.
@@ -92,7 +123,7 @@ __device__ __forceinline__ int page_of(const Unit& u, int i) { return i < u.nsin
 
 __device__ __forceinline__ bool wait(const AttendArgs& g, uint32_t bar, uint32_t parity)
 {
-    return mbar_wait(bar, parity, g.wc.limit_ns, g.wc.err);
+    return mbar_wait_asleep(bar, parity, g.wc.limit_ns, g.wc.err);
 }
 __device__ __forceinline__ bool warp_wait(const AttendArgs& g, uint32_t bar, uint32_t parity)
 {
@@ -228,12 +259,12 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prompt_kernel(const AttendArgs 
 #pragma unroll
                 for (int part = 0; part < C::PARTS; ++part)
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const uint64_t b = sdesc_k_sw128(sbase + C::V + buf * C::V_BYTES + h * D * 128);
+                    for (int c = 0; c < 4; ++c) {   // 32 keys
+                        const uint64_t b = sdesc_k_sw128(sbase + C::V + buf * C::V_BYTES + c / 2 * D * 128);
 #pragma unroll
-                        for (int kk = 0; kk < 4; ++kk)
-                            umma_f16_ts(tmem + O_COL + D * w, tmem + S_COL + TILE * w + 64 * part + 32 * h + 8 * kk,
-                                        b + 2u * kk, pv, (part | h | kk || add) ? 1u : 0u);
+                        for (int kk = 0; kk < 2; ++kk)
+                            umma_f16_ts(tmem + O_COL + D * w, tmem + S_COL + TILE * w + 32 * c + 16 * part + 8 * kk,
+                                        b + 4u * (c % 2) + 2u * kk, pv, (part | c | kk || add) ? 1u : 0u);
                     }
             };
             const int tiles = two ? 2 : 1;
@@ -470,30 +501,50 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prompt_kernel(const AttendArgs 
                 if (!ok)
                     break;
                 tc_fence_after();
-                float x[2][64];
-                tmem_ld64_wait(s_at, x[0]);
-                tmem_ld64_wait(s_at + 64, x[1]);
                 const int2 held = reinterpret_cast<const int2*>(smem + C::META_AT)[j % META];
+                uint32_t seen[4];   // bit i of seen[c]: key 32 c + i
+                bool plain = true;
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     const long long kbase = static_cast<long long>(page_of(u, u.i0 + 2 * j + h)) * KV_PAGE;
                     const bool there = (h ? held.y : held.x) >= 0;
                     const bool whole = there && kbase + KV_PAGE - 1 <= plo &&
                                        (g.window == 0 || kbase > phi - g.window || kbase + KV_PAGE <= g.sinks);
+                    uint64_t m = ~0ull;
                     if (!whole) {
-                        const uint64_t m = there ? kv_seen_bits(pos, kbase, g.window, g.sinks) : 0;
-                        const uint32_t lo = static_cast<uint32_t>(m), hi = static_cast<uint32_t>(m >> 32);
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) {
-                            x[h][i] = lo >> i & 1u ? x[h][i] : -INFINITY;
-                            x[h][32 + i] = hi >> i & 1u ? x[h][32 + i] : -INFINITY;
-                        }
+                        plain = false;
+                        m = there ? kv_seen_bits(pos, kbase, g.window, g.sinks) : 0;
                     }
+                    seen[2 * h] = static_cast<uint32_t>(m);
+                    seen[2 * h + 1] = static_cast<uint32_t>(m >> 32);
                 }
-                float top = -INFINITY;
+                auto mask = [&](uint32_t (&x)[32], uint32_t m) {
 #pragma unroll
-                for (int i = 0; i < 64; ++i)
-                    top = fmaxf(top, fmaxf(x[0][i], x[1][i]));
+                    for (int i = 0; i < 32; ++i)
+                        x[i] = m >> i & 1u ? x[i] : 0xff800000u;   // -inf
+                };
+
+                // all of S on its way at once: a load's latency, some 250 cycles beside the tensor
+                // cores' own traffic, is paid once
+                uint32_t x[4][32];
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+                    tmem_load32(s_at + 32 * c, x[c]);
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    tmem_arrived(x[c]);
+                    if (!plain)
+                        mask(x[c], seen[c]);
+                }
+                float tops[4];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    tops[c] = __uint_as_float(x[c][0]);
+#pragma unroll
+                    for (int i = 0; i < 32; i += 2)
+                        tops[c] = fmaxf(tops[c], fmaxf(__uint_as_float(x[c][i]), __uint_as_float(x[c][i + 1])));
+                }
+                float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
                 top *= coef;
                 const bool raise = top > ref + KV_REF_LIMIT;   // also the first visible key
                 if (__any_sync(0xffffffffu, raise)) {
@@ -504,34 +555,40 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prompt_kernel(const AttendArgs 
                     if (j > 0) {
 #pragma unroll 1
                         for (int d = 0; d < D; d += 32) {
-                            float o[32];
-                            uint32_t v[32];
-                            tmem_ld32_wait(o_at + d, o);
+                            uint32_t o[32];
+                            tmem_load32(o_at + d, o);
+                            tmem_arrived(o);
 #pragma unroll
                             for (int i = 0; i < 32; ++i)
-                                v[i] = __float_as_uint(o[i] * f);
-                            tmem_st32(o_at + d, v);
+                                o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                            tmem_store32(o_at + d, o);
                         }
                     }
                 }
                 const float base = ref == -INFINITY ? 0.0f : ref;
+                float2 part = make_float2(0.0f, 0.0f);
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    uint32_t hi[32], lo[32];
+                for (int c = 0; c < 4; ++c) {
+                    const uint32_t (&y)[32] = x[c];
+                    uint32_t hi[16], lo[16];
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) {
-                        const float p0 = kv_ex2(fmaf(x[h][2 * i], coef, -base));
-                        const float p1 = kv_ex2(fmaf(x[h][2 * i + 1], coef, -base));
-                        sum += p0 + p1;
+                    for (int i = 0; i < 16; ++i) {
+                        const float2 e =
+                            ffma2(make_float2(__uint_as_float(y[2 * i]), __uint_as_float(y[2 * i + 1])),
+                                  make_float2(coef, coef), make_float2(-base, -base));
+                        const float2 q = make_float2(kv_ex2(e.x), kv_ex2(e.y));
+                        part = fadd2(part, q);
                         if (HL)
-                            kv_split2(p0, p1, hi[i], lo[i]);
+                            kv_split2(q.x, q.y, hi[i], lo[i]);
                         else
-                            hi[i] = kv_h2u(__floats2half2_rn(p0, p1));
+                            hi[i] = kv_h2u(__floats2half2_rn(q.x, q.y));
                     }
-                    tmem_st32(s_at + 32 * h, hi);
+                    // P's keys 32 c .. 32 c + 31 go over columns of S that this thread has read
+                    tmem_store16(s_at + 32 * c, hi);
                     if (HL)
-                        tmem_st32(s_at + 64 + 32 * h, lo);
+                        tmem_store16(s_at + 32 * c + 16, lo);
                 }
+                sum += part.x + part.y;
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
@@ -550,14 +607,15 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prompt_kernel(const AttendArgs 
                 g.part_ml[at] = make_float2(ref, sum);
 #pragma unroll 1
             for (int d = 0; d < D; d += 32) {
+                uint32_t bits[32];
                 float o[32];
                 if (u.steps > 0) {
-                    tmem_ld32_wait(o_at + d, o);
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        o[i] = 0.0f;
+                    tmem_load32(o_at + d, bits);
+                    tmem_arrived(bits);
                 }
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                    o[i] = u.steps > 0 ? __uint_as_float(bits[i]) : 0.0f;
                 if (mine) {
 #pragma unroll
                     for (int i = 0; i < 32; i += 4) {

@@ -109,6 +109,24 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, uint64_
     }
 }
 
+// mbar_wait for roles that wait long: the thread sleeps between polls, so that it leaves
+// the issue slots to the warps that share its scheduler.
+__device__ __forceinline__ bool mbar_wait_asleep(uint32_t bar, uint32_t parity, uint64_t limit_ns, unsigned int* err)
+{
+    if (mbar_try_wait(bar, parity))
+        return true;
+    const uint64_t t0 = globaltimer_ns();
+    while (!mbar_try_wait_sleep(bar, parity, 20000u)) {
+        if (*reinterpret_cast<volatile unsigned int*>(err) != 0u)
+            return false;
+        if (globaltimer_ns() - t0 > limit_ns) {
+            atomicOr(err, ERR_WAIT_EXPIRED);
+            return false;
+        }
+    }
+    return true;
+}
+
 // Bounded wait that ignores the error word, used only to drain a CTA's own copies
 // and MMAs in flight before it exits (those always complete): sleeps between polls
 // and gives up after limit_ns, setting ERR_WAIT_EXPIRED.
