@@ -140,7 +140,8 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prompt_kernel(const AttendArgs 
     const uint32_t raw = smem_u32(smem_raw), pad = (1024u - (raw & 1023u)) & 1023u;
     uint8_t* smem = smem_raw + pad;
     const uint32_t sbase = raw + pad;
-    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    // the shuffle tells the compiler that a warp's role is one for all its lanes
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x / 32, 0), lane = threadIdx.x % 32;
     auto bar = [&](int i) -> uint32_t { return sbase + C::BAR + 8u * static_cast<uint32_t>(i); };
 
     grid_dep_wait();
@@ -238,8 +239,11 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prompt_kernel(const AttendArgs 
 
     if (warp < WIDEN_WARP) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(CTRL_REGS));
-        if (warp == 0 && lane == 0) {
+        if (warp == 0) {
             // -------------------------------------------------------- MMA issue
+            // the whole warp walks the loop, one lane's instructions take effect: descriptors
+            // and addresses then stay in uniform registers
+            const uint32_t lead = elect_one();
             constexpr uint32_t qk = idesc_f16_f32(TILE, TILE), pv = idesc_f16_f32(TILE, D);
             auto product_qk = [&](int w, int buf) {
 #pragma unroll
@@ -251,9 +255,10 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prompt_kernel(const AttendArgs 
                         const uint64_t b = sdesc_k_sw128(sbase + C::K + buf * C::K_BYTES + kb * C::BLOCK);
 #pragma unroll
                         for (int kk = 0; kk < 4; ++kk)
-                            umma_f16(tmem + S_COL + TILE * w, a + 2u * kk, b + 2u * kk, qk, (part | kb | kk) ? 1u : 0u);
+                            umma_f16_by(lead, tmem + S_COL + TILE * w, a + 2u * kk, b + 2u * kk, qk,
+                                        (part | kb | kk) ? 1u : 0u);
                     }
-                umma_commit(bar(C::SFULL + w));
+                umma_commit_by(lead, bar(C::SFULL + w));
             };
             auto product_pv = [&](int w, int buf, bool add) {
 #pragma unroll
@@ -263,43 +268,45 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prompt_kernel(const AttendArgs 
                         const uint64_t b = sdesc_k_sw128(sbase + C::V + buf * C::V_BYTES + c / 2 * D * 128);
 #pragma unroll
                         for (int kk = 0; kk < 2; ++kk)
-                            umma_f16_ts(tmem + O_COL + D * w, tmem + S_COL + TILE * w + 32 * c + 16 * part + 8 * kk,
-                                        b + 4u * (c % 2) + 2u * kk, pv, (part | c | kk || add) ? 1u : 0u);
+                            umma_f16_ts_by(lead, tmem + O_COL + D * w,
+                                           tmem + S_COL + TILE * w + 32 * c + 16 * part + 8 * kk,
+                                           b + 4u * (c % 2) + 2u * kk, pv, (part | c | kk || add) ? 1u : 0u);
                     }
             };
             const int tiles = two ? 2 : 1;
-            bool ok = u.steps == 0 || (wait(g, bar(C::QFULL), 0) && wait(g, bar(C::KFULL), 0));
+            bool ok = u.steps == 0 || (warp_wait(g, bar(C::QFULL), 0) && warp_wait(g, bar(C::KFULL), 0));
             if (ok && u.steps > 0) {
                 tc_fence_after();
                 for (int w = 0; w < tiles; ++w)
                     product_qk(w, 0);
-                umma_commit(bar(C::KEMPTY));
+                umma_commit_by(lead, bar(C::KEMPTY));
             }
             for (int j = 0; ok && j < u.steps; ++j) {
                 const int buf = j % C::BUFS, next = (j + 1) % C::BUFS;
                 for (int w = 0; ok && w < tiles; ++w) {
-                    ok = wait(g, bar(C::PFULL + w), j & 1) && (w > 0 || wait(g, bar(C::VFULL + buf), j / C::BUFS & 1));
+                    ok = warp_wait(g, bar(C::PFULL + w), j & 1) && (w > 0 || warp_wait(g, bar(C::VFULL + buf), j / C::BUFS & 1));
                     if (!ok)
                         break;
                     tc_fence_after();
                     product_pv(w, buf, j > 0);
                     if (w == tiles - 1)
-                        umma_commit(bar(C::VEMPTY + buf));
+                        umma_commit_by(lead, bar(C::VEMPTY + buf));
                     if (j + 1 == u.steps) {
-                        umma_commit(bar(C::OFULL + w));
+                        umma_commit_by(lead, bar(C::OFULL + w));
                         continue;
                     }
-                    ok = w > 0 || wait(g, bar(C::KFULL + next), (j + 1) / C::BUFS & 1);
+                    ok = w > 0 || warp_wait(g, bar(C::KFULL + next), (j + 1) / C::BUFS & 1);
                     if (!ok)
                         break;
                     tc_fence_after();
                     product_qk(w, next);
                     if (w == tiles - 1)
-                        umma_commit(bar(C::KEMPTY + next));
+                        umma_commit_by(lead, bar(C::KEMPTY + next));
                 }
             }
-            umma_commit(bar(C::DRAIN));   // nothing of this CTA's is left on the tensor pipe
-            mbar_drain_wait(bar(C::DRAIN), 0, WAIT_LIMIT_NS, g.wc.err);
+            umma_commit_by(lead, bar(C::DRAIN));   // nothing of this CTA's is left on the tensor pipe
+            if (lead)
+                mbar_drain_wait(bar(C::DRAIN), 0, WAIT_LIMIT_NS, g.wc.err);
         } else if (warp == 1) {
             // -------------------------------------------------------- page bytes: K, V of each step
             const int* table = g.c.table + static_cast<size_t>(u.b) * g.c.max_pages;
