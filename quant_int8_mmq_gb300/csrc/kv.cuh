@@ -156,6 +156,14 @@ __device__ __forceinline__ float kv_ex2(float x)
     return y;
 }
 
+// floor(log2 a) within [-126, 126], and 2^e there: scaling by them is exact, and a row
+// whose largest magnitude is a comes to [1, 2), or to (0, 4) at the ends of the range.
+__device__ __forceinline__ int kv_exponent(float a)
+{
+    return min(max(static_cast<int>(__float_as_uint(a) >> 23) - 127, -126), 126);
+}
+__device__ __forceinline__ float kv_pow2(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }
+
 // x = hi + lo in f16 (22 bits) for two values
 __device__ __forceinline__ void kv_split2(float x, float y, uint32_t& hi, uint32_t& lo)
 {

@@ -283,8 +283,12 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prompt_kernel(const AttendArgs 
             }
             for (int j = 0; ok && j < u.steps; ++j) {
                 const int buf = j % C::BUFS, next = (j + 1) % C::BUFS;
+                // with two buffers the next K is there before P is; with one it is widened after
+                // this step's last Q K^T
+                ok = warp_wait(g, bar(C::VFULL + buf), j / C::BUFS & 1) &&
+                     (C::BUFS == 1 || j + 1 == u.steps || warp_wait(g, bar(C::KFULL + next), (j + 1) / C::BUFS & 1));
                 for (int w = 0; ok && w < tiles; ++w) {
-                    ok = warp_wait(g, bar(C::PFULL + w), j & 1) && (w > 0 || warp_wait(g, bar(C::VFULL + buf), j / C::BUFS & 1));
+                    ok = warp_wait(g, bar(C::PFULL + w), j & 1);
                     if (!ok)
                         break;
                     tc_fence_after();
@@ -295,10 +299,12 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prompt_kernel(const AttendArgs 
                         umma_commit_by(lead, bar(C::OFULL + w));
                         continue;
                     }
-                    ok = w > 0 || warp_wait(g, bar(C::KFULL + next), (j + 1) / C::BUFS & 1);
-                    if (!ok)
-                        break;
-                    tc_fence_after();
+                    if (C::BUFS == 1 && w == 0) {
+                        ok = warp_wait(g, bar(C::KFULL + next), (j + 1) / C::BUFS & 1);
+                        if (!ok)
+                            break;
+                        tc_fence_after();
+                    }
                     product_qk(w, next);
                     if (w == tiles - 1)
                         umma_commit_by(lead, bar(C::KEMPTY + next));
@@ -459,34 +465,46 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prompt_kernel(const AttendArgs 
         const bool mine = r < u.nrow;
         const long long token = u.first + row / g.group;
         const int head = u.head * g.group + row % g.group;
-        float coef = g.scale_log2;
+        const long long q_at = token * g.q.tok + head * g.q.head;
+        float coef = 1.0f;
         if (u.steps > 0) {
-            // 2^-e q into the operand tiles, e the exponent of the row's largest magnitude
-            const T* q = static_cast<const T*>(g.q.data) + token * g.q.tok + head * g.q.head;
-            float a = 0.0f;
-            if (mine)
-                for (int d = 0; d < D; d += 4) {
-                    const float4 x = load4(q + d, g.wide);
-                    a = fmaxf(fmaxf(a, fmaxf(fabsf(x.x), fabsf(x.y))), fmaxf(fabsf(x.z), fabsf(x.w)));
+            // 2^-e q into the operand tiles, e the exponent of the row's largest magnitude.  The
+            // warp loads its 32 rows one (or two) at a time, D/4 lanes a row, eight on their way
+            constexpr int LPR = D / 4, RPI = 32 / LPR, BATCH = 8;
+            const int sub = lane / LPR, d = lane % LPR * 4;
+            uint8_t* dst = smem + C::Q + (w * C::PARTS * C::KB + d / 64) * C::BLOCK + d % 8 * 2;
+#pragma unroll 1
+            for (int i0 = 0; i0 < 32; i0 += BATCH * RPI) {
+                float4 x[BATCH];
+#pragma unroll
+                for (int k = 0; k < BATCH; ++k) {
+                    const int i = i0 + k * RPI + sub;
+                    const long long at = __shfl_sync(0xffffffffu, q_at, i);
+                    x[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                    if (__shfl_sync(0xffffffffu, mine, i))
+                        x[k] = load4(static_cast<const T*>(g.q.data) + at + d, g.wide);
                 }
-            const int e = a > 0.0f && a < INFINITY ? ilogbf(a) : 0;
-            coef = fminf(fmaxf(scalbnf(g.scale_log2, e), 1e-38f), 1e38f);
-            uint8_t* dst = smem + C::Q + w * C::PARTS * C::KB * C::BLOCK + l * 128;
-            for (int d = 0; d < D; d += 8) {
-                float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f), y = x;
-                if (mine) {
-                    x = load4(q + d, g.wide);
-                    y = load4(q + d + 4, g.wide);
+#pragma unroll
+                for (int k = 0; k < BATCH; ++k) {
+                    const int i = i0 + k * RPI + sub, r32 = (l & ~31) + i;
+                    float a = fmaxf(fmaxf(fabsf(x[k].x), fabsf(x[k].y)), fmaxf(fabsf(x[k].z), fabsf(x[k].w)));
+#pragma unroll
+                    for (int s = 1; s < LPR; s <<= 1)
+                        a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, s));
+                    const int e = kv_exponent(a);
+                    const float f = kv_pow2(-e);
+                    uint2 hi, lo;
+                    kv_split2(x[k].x * f, x[k].y * f, hi.x, lo.x);
+                    kv_split2(x[k].z * f, x[k].w * f, hi.y, lo.y);
+                    uint8_t* at = dst + r32 * 128 + ((d / 8 % 8 ^ (r32 & 7)) << 4);
+                    *reinterpret_cast<uint2*>(at) = hi;
+                    if (HL)
+                        *reinterpret_cast<uint2*>(at + C::KB * C::BLOCK) = lo;
+                    const int own = lane - (i0 + k * RPI);   // the lane's row is one of these
+                    const int its = __shfl_sync(0xffffffffu, e, (own & (RPI - 1)) * LPR);
+                    if (own >= 0 && own < RPI)
+                        coef = fminf(fmaxf(g.scale_log2 * kv_pow2(its), 1e-38f), 1e38f);
                 }
-                uint4 hi, lo;
-                kv_split2(scalbnf(x.x, -e), scalbnf(x.y, -e), hi.x, lo.x);
-                kv_split2(scalbnf(x.z, -e), scalbnf(x.w, -e), hi.y, lo.y);
-                kv_split2(scalbnf(y.x, -e), scalbnf(y.y, -e), hi.z, lo.z);
-                kv_split2(scalbnf(y.z, -e), scalbnf(y.w, -e), hi.w, lo.w);
-                uint8_t* at = dst + d / 64 * C::BLOCK + ((d / 8 % 8 ^ (l & 7)) << 4);
-                *reinterpret_cast<uint4*>(at) = hi;
-                if (HL)
-                    *reinterpret_cast<uint4*>(at + C::KB * C::BLOCK) = lo;
             }
             fence_proxy_async_smem();
             __syncwarp();
@@ -573,29 +591,33 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prompt_kernel(const AttendArgs 
                     }
                 }
                 const float base = ref == -INFINITY ? 0.0f : ref;
-                float2 part = make_float2(0.0f, 0.0f);
+                float2 part[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
-                    const uint32_t (&y)[32] = x[c];
+                    // in rounds over the 32 values, so that no instruction waits for the one before it
+                    float2 e[16];
                     uint32_t hi[16], lo[16];
 #pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        e[i] = ffma2(make_float2(__uint_as_float(x[c][2 * i]), __uint_as_float(x[c][2 * i + 1])),
+                                     make_float2(coef, coef), make_float2(-base, -base));
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        e[i] = make_float2(kv_ex2(e[i].x), kv_ex2(e[i].y));
+#pragma unroll
                     for (int i = 0; i < 16; ++i) {
-                        const float2 e =
-                            ffma2(make_float2(__uint_as_float(y[2 * i]), __uint_as_float(y[2 * i + 1])),
-                                  make_float2(coef, coef), make_float2(-base, -base));
-                        const float2 q = make_float2(kv_ex2(e.x), kv_ex2(e.y));
-                        part = fadd2(part, q);
+                        part[i % 2] = fadd2(part[i % 2], e[i]);
                         if (HL)
-                            kv_split2(q.x, q.y, hi[i], lo[i]);
+                            kv_split2(e[i].x, e[i].y, hi[i], lo[i]);
                         else
-                            hi[i] = kv_h2u(__floats2half2_rn(q.x, q.y));
+                            hi[i] = kv_h2u(__floats2half2_rn(e[i].x, e[i].y));
                     }
                     // P's keys 32 c .. 32 c + 31 go over columns of S that this thread has read
                     tmem_store16(s_at + 32 * c, hi);
                     if (HL)
                         tmem_store16(s_at + 32 * c + 16, lo);
                 }
-                sum += part.x + part.y;
+                sum += (part[0].x + part[0].y) + (part[1].x + part[1].y);
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
@@ -606,31 +628,45 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prompt_kernel(const AttendArgs 
                 ok = warp_wait(g, bar(C::OFULL + w), 0);
                 tc_fence_after();
             }
+            // a row's share of the result, by way of shared memory (the tile's Q is done with): the
+            // warp writes four rows' 32 values at a time, whole lines for the strided 16 bytes a
+            // thread that its own row would take
             const float inv = g.nsplit > 1 ? 1.0f : sum == 0.0f ? 0.0f : 1.0f / sum;
-            const size_t flat = static_cast<size_t>(token) * g.heads + head;
-            const size_t at = static_cast<size_t>(u.split) * g.ntok * g.heads + flat;
-            T* out = static_cast<T*>(g.out.data) + token * g.out.tok + head * g.out.head;
+            const long long flat = token * g.heads + head;
+            const long long part_at = static_cast<long long>(u.split) * g.ntok * g.heads + flat;
+            const long long out_at = g.nsplit > 1 ? part_at * D : token * g.out.tok + head * g.out.head;
             if (g.nsplit > 1 && mine)
-                g.part_ml[at] = make_float2(ref, sum);
+                g.part_ml[part_at] = make_float2(ref, sum);
+            constexpr int ROW = 32 * 4 + 16;
+            uint8_t* stage = smem + C::Q + (threadIdx.x / 32 - SOFT_WARP) * 32 * ROW;
+            static_assert(8 * 32 * ROW <= C::Q_BYTES + C::K_BYTES, "staged rows");
 #pragma unroll 1
             for (int d = 0; d < D; d += 32) {
-                uint32_t bits[32];
-                float o[32];
+                uint32_t o[32];
                 if (u.steps > 0) {
-                    tmem_load32(o_at + d, bits);
-                    tmem_arrived(bits);
+                    tmem_load32(o_at + d, o);
+                    tmem_arrived(o);
                 }
+                __syncwarp();
 #pragma unroll
-                for (int i = 0; i < 32; ++i)
-                    o[i] = u.steps > 0 ? __uint_as_float(bits[i]) : 0.0f;
-                if (mine) {
+                for (int i = 0; i < 32; i += 4) {
+                    float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                    if (u.steps > 0)
+                        v = make_float4(__uint_as_float(o[i]) * inv, __uint_as_float(o[i + 1]) * inv,
+                                        __uint_as_float(o[i + 2]) * inv, __uint_as_float(o[i + 3]) * inv);
+                    *reinterpret_cast<float4*>(stage + lane * ROW + i * 4) = v;
+                }
+                __syncwarp();
 #pragma unroll
-                    for (int i = 0; i < 32; i += 4) {
-                        const float4 v = make_float4(o[i] * inv, o[i + 1] * inv, o[i + 2] * inv, o[i + 3] * inv);
+                for (int i = 0; i < 8; ++i) {
+                    const int src = 4 * i + lane / 8, c = lane % 8 * 4;
+                    const long long at = __shfl_sync(0xffffffffu, out_at, src) + d + c;
+                    const float4 v = *reinterpret_cast<const float4*>(stage + src * ROW + c * 4);
+                    if (__shfl_sync(0xffffffffu, mine, src)) {
                         if (g.nsplit > 1)
-                            *reinterpret_cast<float4*>(g.part + at * D + d + i) = v;
+                            *reinterpret_cast<float4*>(g.part + at) = v;
                         else
-                            store4(out + d + i, v, g.wide);
+                            store4(static_cast<T*>(g.out.data) + at, v, g.wide);
                     }
                 }
             }

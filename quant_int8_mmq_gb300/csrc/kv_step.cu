@@ -184,17 +184,18 @@ __global__ void __launch_bounds__(WARPS * 32, MODE == WIDE ? 3 : D == 128 ? 4 : 
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1)
             a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, d));
-        const int e = a > 0.0f && a < INFINITY ? ilogbf(a) : 0;
+        const int e = kv_exponent(a);
+        const float f = kv_pow2(-e);
         if (lane < D / 4) {
             uint2 hi, lo;
-            kv_split2(scalbnf(x.x, -e), scalbnf(x.y, -e), hi.x, lo.x);
-            kv_split2(scalbnf(x.z, -e), scalbnf(x.w, -e), hi.y, lo.y);
+            kv_split2(x.x * f, x.y * f, hi.x, lo.x);
+            kv_split2(x.z * f, x.w * f, hi.y, lo.y);
             *reinterpret_cast<uint2*>(smem + S::Q + r * S::QROW + lane * 8) = hi;
             if (MODE != WIDE)
                 *reinterpret_cast<uint2*>(smem + S::Q + (8 + r) * S::QROW + lane * 8) = lo;
         }
         if (lane == 0)
-            *reinterpret_cast<float*>(smem + S::COEF + 4 * r) = fminf(fmaxf(scalbnf(g.scale_log2, e), 1e-38f), 1e38f);
+            *reinterpret_cast<float*>(smem + S::COEF + 4 * r) = fminf(fmaxf(g.scale_log2 * kv_pow2(e), 1e-38f), 1e38f);
     }
     __syncthreads();
 
