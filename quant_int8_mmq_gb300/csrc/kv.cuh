@@ -133,6 +133,28 @@ __device__ __forceinline__ float4 load4(const T* p, bool wide)
     }
     return make_float4(Elt<T>::to(e[0]), Elt<T>::to(e[1]), Elt<T>::to(e[2]), Elt<T>::to(e[3]));
 }
+// The same in two halves: the load, and the values once they are used.
+template <typename T>
+struct Raw4 {
+    T e[4];
+    __device__ __forceinline__ void load(const T* p, bool wide)
+    {
+        if (wide) {
+            if constexpr (sizeof(T) == 4)
+                *reinterpret_cast<uint4*>(e) = *reinterpret_cast<const uint4*>(p);
+            else
+                *reinterpret_cast<uint2*>(e) = *reinterpret_cast<const uint2*>(p);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                e[i] = p[i];
+        }
+    }
+    __device__ __forceinline__ float4 get() const
+    {
+        return make_float4(Elt<T>::to(e[0]), Elt<T>::to(e[1]), Elt<T>::to(e[2]), Elt<T>::to(e[3]));
+    }
+};
 template <typename T>
 __device__ __forceinline__ void store4(T* p, float4 v, bool wide)
 {

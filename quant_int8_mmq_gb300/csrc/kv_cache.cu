@@ -55,7 +55,7 @@ __device__ __forceinline__ void load8(const T* p, bool wide, float (&x)[8])
     if (wide) {
 #pragma unroll
         for (int i = 0; i < static_cast<int>(sizeof(T)) / 2; ++i)
-            reinterpret_cast<uint4*>(e)[i] = __ldg(reinterpret_cast<const uint4*>(p) + i);
+            reinterpret_cast<uint4*>(e)[i] = reinterpret_cast<const uint4*>(p)[i];
     } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
@@ -206,13 +206,13 @@ __global__ void __launch_bounds__(WARPS * 32) kv_read_kernel(const KvView c, con
                 continue;
             const uint8_t* piece = pages + (h + i * step) * P::BYTES;
             if (key) {
-                z0[i] = __ldg(reinterpret_cast<const unsigned int*>(piece + codes));
+                z0[i] = *reinterpret_cast<const unsigned int*>(piece + codes);
             } else {
-                const uint2 w = __ldg(reinterpret_cast<const uint2*>(piece + codes));   // both tokens'
+                const uint2 w = *reinterpret_cast<const uint2*>(piece + codes);   // both tokens'
                 z0[i] = w.x;
                 z1[i] = w.y;
             }
-            s[i] = __half2half2(__ushort_as_half(__ldg(reinterpret_cast<const unsigned short*>(piece + scale))));
+            s[i] = __half2half2(__ushort_as_half(*reinterpret_cast<const unsigned short*>(piece + scale)));
         }
 #pragma unroll
         for (int i = 0; i < BATCH; ++i) {

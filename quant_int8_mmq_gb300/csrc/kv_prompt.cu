@@ -22,6 +22,8 @@
 // widen, warps 8-11 and 12-15 are the softmax of tiles 0 and 1.  Every wait is bounded; on
 // expiry the roles leave their loops, copies and MMAs in flight are waited for, TMEM is
 // freed and the CTA ends.
+#include <type_traits>
+
 #include "kv.cuh"
 
 namespace mmq {
@@ -114,7 +116,9 @@ __device__ __forceinline__ float2 fadd2(float2 a, float2 b)
 
 // What a CTA works on; the same in every thread.
 struct Unit {
-    int b, head, split, first, row0, nrow;   // rows row0 .. row0 + nrow - 1 of sequence b's
+    int b, head, split;
+    int first, ntok, length;                 // the sequence's rows and tokens
+    int row0, nrow;                          // rows row0 .. row0 + nrow - 1 of it
     long long pos0;                          // position of the sequence's first new token
     int kend, nsink, page_lo, npage;         // keys [0, kend); pages 0 .. nsink - 1, page_lo ..
     int i0, steps;                           // first page of this split's and its 128-key steps
@@ -158,12 +162,15 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prompt_kernel(const AttendArgs 
         // sequence b has ceil(rows / 256) tiles; the warp sums 32 sequences at a time
         const int want = g.row_tiles - 1 - id;
         int before = 0;
+        u.first = u.ntok = u.length = 0;
         u.b = -1;
         u.row0 = 0;
         for (int b0 = 0; b0 < g.c.batch; b0 += 32) {
-            int tiles = 0;
+            int tiles = 0, s = 0, e = 0, len = 0;
             if (b0 + lane < g.c.batch) {
-                const int s = g.c.start[b0 + lane], e = g.c.start[b0 + lane + 1];
+                s = g.c.start[b0 + lane];
+                e = g.c.start[b0 + lane + 1];
+                len = g.c.length[b0 + lane];
                 if (s >= 0 && e > s && e <= g.ntok)
                     tiles = static_cast<int>((static_cast<long long>(e - s) * g.group + ROWS - 1) / ROWS);
             }
@@ -178,6 +185,9 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prompt_kernel(const AttendArgs 
                 const int l = __ffs(here) - 1;
                 u.b = b0 + l;
                 u.row0 = (want - before - __shfl_sync(0xffffffffu, sum - tiles, l)) * ROWS;
+                u.first = __shfl_sync(0xffffffffu, s, l);
+                u.ntok = __shfl_sync(0xffffffffu, e, l) - u.first;
+                u.length = __shfl_sync(0xffffffffu, len, l);
                 break;
             }
             before += __shfl_sync(0xffffffffu, sum, 31);
@@ -185,10 +195,8 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prompt_kernel(const AttendArgs 
     }
     if (u.b < 0)
         return;   // fewer tiles than the host's bound
-    u.first = g.c.start[u.b];
-    const int ntok = g.c.start[u.b + 1] - u.first;
-    u.nrow = min(ROWS, ntok * g.group - u.row0);
-    u.pos0 = static_cast<long long>(g.c.length[u.b]) - ntok;
+    u.nrow = min(ROWS, u.ntok * g.group - u.row0);
+    u.pos0 = static_cast<long long>(u.length) - u.ntok;
     {
         const long long room = static_cast<long long>(g.c.max_pages) * KV_PAGE;
         const long long plo = u.pos0 + u.row0 / g.group, phi = u.pos0 + (u.row0 + u.nrow - 1) / g.group;
@@ -461,48 +469,58 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prompt_kernel(const AttendArgs 
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(SOFT_REGS));
         const int w = (warp - SOFT_WARP) / 4;                           // tile
         const int l = threadIdx.x - (SOFT_WARP + 4 * w) * 32;           // TMEM lane
-        const int r = TILE * w + l, row = u.row0 + r;
-        const bool mine = r < u.nrow;
+        const bool mine = TILE * w + l < u.nrow;
+        const int row = u.row0 + min(TILE * w + l, u.nrow - 1);
         const long long token = u.first + row / g.group;
         const int head = u.head * g.group + row % g.group;
         const long long q_at = token * g.q.tok + head * g.q.head;
         float coef = 1.0f;
         if (u.steps > 0) {
             // 2^-e q into the operand tiles, e the exponent of the row's largest magnitude.  The
-            // warp loads its 32 rows one (or two) at a time, D/4 lanes a row, eight on their way
-            constexpr int LPR = D / 4, RPI = 32 / LPR, BATCH = 8;
-            const int sub = lane / LPR, d = lane % LPR * 4;
-            uint8_t* dst = smem + C::Q + (w * C::PARTS * C::KB + d / 64) * C::BLOCK + d % 8 * 2;
+            // warp loads its 32 rows, eight lanes a row, in two batches of loads (lanes past the
+            // last row load that one again: their rows go nowhere)
+            constexpr int LOADS = D / 32, BATCH = 32 / LOADS / 2;   // of four values a lane; four rows at once
+            const int sub = lane / 8, c = lane % 8 * 4;
+            uint8_t* dst = smem + C::Q + w * C::PARTS * C::KB * C::BLOCK;
 #pragma unroll 1
-            for (int i0 = 0; i0 < 32; i0 += BATCH * RPI) {
-                float4 x[BATCH];
+            for (int i0 = 0; i0 < 32; i0 += 4 * BATCH) {
+                Raw4<T> x[BATCH][LOADS];
 #pragma unroll
                 for (int k = 0; k < BATCH; ++k) {
-                    const int i = i0 + k * RPI + sub;
-                    const long long at = __shfl_sync(0xffffffffu, q_at, i);
-                    x[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                    if (__shfl_sync(0xffffffffu, mine, i))
-                        x[k] = load4(static_cast<const T*>(g.q.data) + at + d, g.wide);
+                    const T* q = static_cast<const T*>(g.q.data) + __shfl_sync(0xffffffffu, q_at, i0 + 4 * k + sub) + c;
+#pragma unroll
+                    for (int i = 0; i < LOADS; ++i)
+                        x[k][i].load(q + 32 * i, g.wide);
                 }
 #pragma unroll
                 for (int k = 0; k < BATCH; ++k) {
-                    const int i = i0 + k * RPI + sub, r32 = (l & ~31) + i;
-                    float a = fmaxf(fmaxf(fabsf(x[k].x), fabsf(x[k].y)), fmaxf(fabsf(x[k].z), fabsf(x[k].w)));
+                    const int r32 = (l & ~31) + i0 + 4 * k + sub;
+                    float4 v[LOADS];
+                    float a = 0.0f;
 #pragma unroll
-                    for (int s = 1; s < LPR; s <<= 1)
+                    for (int i = 0; i < LOADS; ++i) {
+                        v[i] = x[k][i].get();
+                        a = fmaxf(a, fmaxf(fmaxf(fabsf(v[i].x), fabsf(v[i].y)), fmaxf(fabsf(v[i].z), fabsf(v[i].w))));
+                    }
+#pragma unroll
+                    for (int s = 1; s < 8; s <<= 1)
                         a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, s));
                     const int e = kv_exponent(a);
                     const float f = kv_pow2(-e);
-                    uint2 hi, lo;
-                    kv_split2(x[k].x * f, x[k].y * f, hi.x, lo.x);
-                    kv_split2(x[k].z * f, x[k].w * f, hi.y, lo.y);
-                    uint8_t* at = dst + r32 * 128 + ((d / 8 % 8 ^ (r32 & 7)) << 4);
-                    *reinterpret_cast<uint2*>(at) = hi;
-                    if (HL)
-                        *reinterpret_cast<uint2*>(at + C::KB * C::BLOCK) = lo;
-                    const int own = lane - (i0 + k * RPI);   // the lane's row is one of these
-                    const int its = __shfl_sync(0xffffffffu, e, (own & (RPI - 1)) * LPR);
-                    if (own >= 0 && own < RPI)
+#pragma unroll
+                    for (int i = 0; i < LOADS; ++i) {
+                        const int d = 32 * i + c;
+                        uint2 hi, lo;
+                        kv_split2(v[i].x * f, v[i].y * f, hi.x, lo.x);
+                        kv_split2(v[i].z * f, v[i].w * f, hi.y, lo.y);
+                        uint8_t* at = dst + d / 64 * C::BLOCK + r32 * 128 + ((d / 8 % 8 ^ (r32 & 7)) << 4) + d % 8 * 2;
+                        *reinterpret_cast<uint2*>(at) = hi;
+                        if (HL)
+                            *reinterpret_cast<uint2*>(at + C::KB * C::BLOCK) = lo;
+                    }
+                    const int own = lane - (i0 + 4 * k);   // the lane's row is one of these four
+                    const int its = __shfl_sync(0xffffffffu, e, (own & 3) * 8);
+                    if (own >= 0 && own < 4)
                         coef = fminf(fmaxf(g.scale_log2 * kv_pow2(its), 1e-38f), 1e38f);
                 }
             }
@@ -549,6 +567,8 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prompt_kernel(const AttendArgs 
                         x[i] = m >> i & 1u ? x[i] : 0xff800000u;   // -inf
                 };
 
+                auto softmax = [&](auto with_mask) {
+                constexpr bool masked = decltype(with_mask)::value;
                 // all of S on its way at once: a load's latency, some 250 cycles beside the tensor
                 // cores' own traffic, is paid once
                 uint32_t x[4][32];
@@ -558,7 +578,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prompt_kernel(const AttendArgs 
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
                     tmem_arrived(x[c]);
-                    if (!plain)
+                    if constexpr (masked)
                         mask(x[c], seen[c]);
                 }
                 float tops[4];
@@ -618,6 +638,12 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prompt_kernel(const AttendArgs 
                         tmem_store16(s_at + 32 * c + 16, lo);
                 }
                 sum += (part[0].x + part[0].y) + (part[1].x + part[1].y);
+                };
+                // two builds, so that steps without a mask carry no selects or copies for it
+                if (plain)
+                    softmax(std::false_type{});
+                else
+                    softmax(std::true_type{});
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
