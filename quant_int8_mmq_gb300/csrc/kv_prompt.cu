@@ -477,9 +477,10 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prompt_kernel(const AttendArgs 
         float coef = 1.0f;
         if (u.steps > 0) {
             // 2^-e q into the operand tiles, e the exponent of the row's largest magnitude.  The
-            // warp loads its 32 rows, eight lanes a row, in two batches of loads (lanes past the
-            // last row load that one again: their rows go nowhere)
-            constexpr int LOADS = D / 32, BATCH = 32 / LOADS / 2;   // of four values a lane; four rows at once
+            // warp loads its 32 rows, eight lanes a row (lanes past the last row load that
+            // one again: their rows go nowhere)
+            constexpr int LOADS = D / 32;                                   // of four values a lane, four rows at once
+            constexpr int BATCH = sizeof(T) == 4 && D == 128 ? 4 : 8;       // 64 registers of loads on their way
             const int sub = lane / 8, c = lane % 8 * 4;
             uint8_t* dst = smem + C::Q + w * C::PARTS * C::KB * C::BLOCK;
 #pragma unroll 1
@@ -664,16 +665,23 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prompt_kernel(const AttendArgs 
             if (g.nsplit > 1 && mine)
                 g.part_ml[part_at] = make_float2(ref, sum);
             constexpr int ROW = 32 * 4 + 16;
-            uint8_t* stage = smem + C::Q + (threadIdx.x / 32 - SOFT_WARP) * 32 * ROW;
             static_assert(8 * 32 * ROW <= C::Q_BYTES + C::K_BYTES, "staged rows");
-#pragma unroll 1
+            uint8_t* stage = smem + C::Q + (warp - SOFT_WARP) * 32 * ROW;
+            const int sub = lane / 8, c = lane % 8 * 4;
+            long long at[8];   // of the eight rows whose values c .. c + 3 this lane writes
+            uint32_t there = 0;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                at[i] = __shfl_sync(0xffffffffu, out_at, 4 * i + sub) + c;
+                there |= (__shfl_sync(0xffffffffu, mine, 4 * i + sub) ? 1u : 0u) << i;
+            }
+#pragma unroll
             for (int d = 0; d < D; d += 32) {
                 uint32_t o[32];
                 if (u.steps > 0) {
                     tmem_load32(o_at + d, o);
                     tmem_arrived(o);
                 }
-                __syncwarp();
 #pragma unroll
                 for (int i = 0; i < 32; i += 4) {
                     float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
@@ -683,18 +691,19 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prompt_kernel(const AttendArgs 
                     *reinterpret_cast<float4*>(stage + lane * ROW + i * 4) = v;
                 }
                 __syncwarp();
+                float4 v[8];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const int src = 4 * i + lane / 8, c = lane % 8 * 4;
-                    const long long at = __shfl_sync(0xffffffffu, out_at, src) + d + c;
-                    const float4 v = *reinterpret_cast<const float4*>(stage + src * ROW + c * 4);
-                    if (__shfl_sync(0xffffffffu, mine, src)) {
+                for (int i = 0; i < 8; ++i)
+                    v[i] = *reinterpret_cast<const float4*>(stage + (4 * i + sub) * ROW + c * 4);
+                __syncwarp();
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    if (there >> i & 1u) {
                         if (g.nsplit > 1)
-                            *reinterpret_cast<float4*>(g.part + at) = v;
+                            *reinterpret_cast<float4*>(g.part + at[i] + d) = v[i];
                         else
-                            store4(static_cast<T*>(g.out.data) + at, v, g.wide);
+                            store4(static_cast<T*>(g.out.data) + at[i] + d, v[i], g.wide);
                     }
-                }
             }
         }
     }
