@@ -88,6 +88,20 @@ __device__ __forceinline__ void tmem_arrived(uint32_t (&r)[32])
                  :
                  : "memory");
 }
+// 128 columns, all on their way at once: a load's latency, some 250 cycles beside the tensor
+// cores' own traffic, is paid once.
+__device__ __forceinline__ void tmem_load128(uint32_t taddr, uint32_t (&r)[4][32])
+{
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%128];\n\t"
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, [%129];\n\t"
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%64,%65,%66,%67,%68,%69,%70,%71,%72,%73,%74,%75,%76,%77,%78,%79,%80,%81,%82,%83,%84,%85,%86,%87,%88,%89,%90,%91,%92,%93,%94,%95}, [%130];\n\t"
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%96,%97,%98,%99,%100,%101,%102,%103,%104,%105,%106,%107,%108,%109,%110,%111,%112,%113,%114,%115,%116,%117,%118,%119,%120,%121,%122,%123,%124,%125,%126,%127}, [%131];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0][0]), "=r"(r[0][1]), "=r"(r[0][2]), "=r"(r[0][3]), "=r"(r[0][4]), "=r"(r[0][5]), "=r"(r[0][6]), "=r"(r[0][7]), "=r"(r[0][8]), "=r"(r[0][9]), "=r"(r[0][10]), "=r"(r[0][11]), "=r"(r[0][12]), "=r"(r[0][13]), "=r"(r[0][14]), "=r"(r[0][15]), "=r"(r[0][16]), "=r"(r[0][17]), "=r"(r[0][18]), "=r"(r[0][19]), "=r"(r[0][20]), "=r"(r[0][21]), "=r"(r[0][22]), "=r"(r[0][23]), "=r"(r[0][24]), "=r"(r[0][25]), "=r"(r[0][26]), "=r"(r[0][27]), "=r"(r[0][28]), "=r"(r[0][29]), "=r"(r[0][30]), "=r"(r[0][31]), "=r"(r[1][0]), "=r"(r[1][1]), "=r"(r[1][2]), "=r"(r[1][3]), "=r"(r[1][4]), "=r"(r[1][5]), "=r"(r[1][6]), "=r"(r[1][7]), "=r"(r[1][8]), "=r"(r[1][9]), "=r"(r[1][10]), "=r"(r[1][11]), "=r"(r[1][12]), "=r"(r[1][13]), "=r"(r[1][14]), "=r"(r[1][15]), "=r"(r[1][16]), "=r"(r[1][17]), "=r"(r[1][18]), "=r"(r[1][19]), "=r"(r[1][20]), "=r"(r[1][21]), "=r"(r[1][22]), "=r"(r[1][23]), "=r"(r[1][24]), "=r"(r[1][25]), "=r"(r[1][26]), "=r"(r[1][27]), "=r"(r[1][28]), "=r"(r[1][29]), "=r"(r[1][30]), "=r"(r[1][31]), "=r"(r[2][0]), "=r"(r[2][1]), "=r"(r[2][2]), "=r"(r[2][3]), "=r"(r[2][4]), "=r"(r[2][5]), "=r"(r[2][6]), "=r"(r[2][7]), "=r"(r[2][8]), "=r"(r[2][9]), "=r"(r[2][10]), "=r"(r[2][11]), "=r"(r[2][12]), "=r"(r[2][13]), "=r"(r[2][14]), "=r"(r[2][15]), "=r"(r[2][16]), "=r"(r[2][17]), "=r"(r[2][18]), "=r"(r[2][19]), "=r"(r[2][20]), "=r"(r[2][21]), "=r"(r[2][22]), "=r"(r[2][23]), "=r"(r[2][24]), "=r"(r[2][25]), "=r"(r[2][26]), "=r"(r[2][27]), "=r"(r[2][28]), "=r"(r[2][29]), "=r"(r[2][30]), "=r"(r[2][31]), "=r"(r[3][0]), "=r"(r[3][1]), "=r"(r[3][2]), "=r"(r[3][3]), "=r"(r[3][4]), "=r"(r[3][5]), "=r"(r[3][6]), "=r"(r[3][7]), "=r"(r[3][8]), "=r"(r[3][9]), "=r"(r[3][10]), "=r"(r[3][11]), "=r"(r[3][12]), "=r"(r[3][13]), "=r"(r[3][14]), "=r"(r[3][15]), "=r"(r[3][16]), "=r"(r[3][17]), "=r"(r[3][18]), "=r"(r[3][19]), "=r"(r[3][20]), "=r"(r[3][21]), "=r"(r[3][22]), "=r"(r[3][23]), "=r"(r[3][24]), "=r"(r[3][25]), "=r"(r[3][26]), "=r"(r[3][27]), "=r"(r[3][28]), "=r"(r[3][29]), "=r"(r[3][30]), "=r"(r[3][31])
+        : "r"(taddr), "r"(taddr + 32), "r"(taddr + 64), "r"(taddr + 96)
+        : "memory");
+}
 __device__ __forceinline__ void tmem_store16(uint32_t taddr, const uint32_t (&v)[16])
 {
     asm volatile(
@@ -394,16 +408,15 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prompt_kernel(const AttendArgs 
 #pragma unroll
                 for (int gr = 0; gr < P::NG; ++gr) {
                     const uint4 v = *reinterpret_cast<const uint4*>(src + P::k_chunk(t % KV_PAGE, gr));
-                    const __half2 s = __half2half2(
-                        *reinterpret_cast<const __half*>(src + P::k_scale(t % KV_PAGE, gr)));
+                    // a page that is not there gives zeros: any code times the scale 0
+                    const uint16_t sc = *reinterpret_cast<const uint16_t*>(src + P::k_scale(t % KV_PAGE, gr));
+                    const __half2 s = __half2half2(__ushort_as_half(there ? sc : 0));
                     const __half2 sb = kv_addend(s);
                     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        uint4 o = make_uint4(kv_h2u(kv_widen<0>(w[i], s, sb)), kv_h2u(kv_widen<1>(w[i], s, sb)),
+                        const uint4 o = make_uint4(kv_h2u(kv_widen<0>(w[i], s, sb)), kv_h2u(kv_widen<1>(w[i], s, sb)),
                                              kv_h2u(kv_widen<2>(w[i], s, sb)), kv_h2u(kv_widen<3>(w[i], s, sb)));
-                        if (!there)
-                            o = make_uint4(0, 0, 0, 0);
                         *reinterpret_cast<uint4*>(dst + gr / 2 * C::BLOCK + ((gr % 2 * 4 + i) ^ (t & 7)) * 16) = o;
                     }
                 }
@@ -570,16 +583,11 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prompt_kernel(const AttendArgs 
 
                 auto softmax = [&](auto with_mask) {
                 constexpr bool masked = decltype(with_mask)::value;
-                // all of S on its way at once: a load's latency, some 250 cycles beside the tensor
-                // cores' own traffic, is paid once
                 uint32_t x[4][32];
+                tmem_load128(s_at, x);
+                if constexpr (masked) {
 #pragma unroll
-                for (int c = 0; c < 4; ++c)
-                    tmem_load32(s_at + 32 * c, x[c]);
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    tmem_arrived(x[c]);
-                    if constexpr (masked)
+                    for (int c = 0; c < 4; ++c)
                         mask(x[c], seen[c]);
                 }
                 float tops[4];
