@@ -202,13 +202,14 @@ constexpr float KV_REF_BELOW = 7.0f;
 constexpr float KV_REF_LIMIT = 15.0f;
 
 // Which keys of a page (64 from kbase on) a row at position pos sees, one bit each.
-__device__ __forceinline__ uint64_t kv_seen_bits(long long pos, long long kbase, int window, int sinks)
+// Positions, windows and sinks stay below 2^30 (the entry point limits the latter two).
+__device__ __forceinline__ uint64_t kv_seen_bits(int pos, int kbase, int window, int sinks)
 {
-    const int to = static_cast<int>(min(max(pos - kbase, -1ll), 63ll));
+    const int to = min(max(pos - kbase, -1), 63);
     uint64_t m = to < 0 ? 0 : ~0ull >> (63 - to);
     if (window > 0) {
-        const int from = static_cast<int>(min(max(pos - window + 1 - kbase, 0ll), 64ll));
-        const int sink = static_cast<int>(min(max(sinks - kbase, 0ll), 64ll));
+        const int from = min(max(pos - window + 1 - kbase, 0), 64);
+        const int sink = min(max(sinks - kbase, 0), 64);
         m &= (from < 64 ? ~0ull << from : 0) | (sink > 0 ? ~0ull >> (64 - sink) : 0);
     }
     return m;

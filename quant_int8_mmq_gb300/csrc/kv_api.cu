@@ -248,8 +248,10 @@ mmq_status mmq_kv_attend(const mmq_kv_cache* c, const mmq_rows* q, const mmq_row
     a.group = heads / c->kv_heads;
     a.ntok = ntok;
     a.scale_log2 = scale * 1.4426950408889634f;
-    a.window = window;
-    a.sinks = window > 0 ? sinks : 0;
+    // positions are below 64 MMQ_KV_MAX_PAGES = 2^30, where larger windows and sinks change nothing
+    constexpr int FAR = 1 << 30;
+    a.window = window < FAR ? window : FAR;
+    a.sinks = window == 0 ? 0 : sinks < FAR ? sinks : FAR;
     a.tile_rows = p.tile_rows;
     a.row_tiles = p.row_tiles;
     a.nsplit = p.nsplit;

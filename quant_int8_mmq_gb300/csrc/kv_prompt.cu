@@ -88,20 +88,6 @@ __device__ __forceinline__ void tmem_arrived(uint32_t (&r)[32])
                  :
                  : "memory");
 }
-// 128 columns, all on their way at once: a load's latency, some 250 cycles beside the tensor
-// cores' own traffic, is paid once.
-__device__ __forceinline__ void tmem_load128(uint32_t taddr, uint32_t (&r)[4][32])
-{
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%128];\n\t"
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, [%129];\n\t"
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%64,%65,%66,%67,%68,%69,%70,%71,%72,%73,%74,%75,%76,%77,%78,%79,%80,%81,%82,%83,%84,%85,%86,%87,%88,%89,%90,%91,%92,%93,%94,%95}, [%130];\n\t"
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%96,%97,%98,%99,%100,%101,%102,%103,%104,%105,%106,%107,%108,%109,%110,%111,%112,%113,%114,%115,%116,%117,%118,%119,%120,%121,%122,%123,%124,%125,%126,%127}, [%131];\n\t"
-        "tcgen05.wait::ld.sync.aligned;"
-        : "=r"(r[0][0]), "=r"(r[0][1]), "=r"(r[0][2]), "=r"(r[0][3]), "=r"(r[0][4]), "=r"(r[0][5]), "=r"(r[0][6]), "=r"(r[0][7]), "=r"(r[0][8]), "=r"(r[0][9]), "=r"(r[0][10]), "=r"(r[0][11]), "=r"(r[0][12]), "=r"(r[0][13]), "=r"(r[0][14]), "=r"(r[0][15]), "=r"(r[0][16]), "=r"(r[0][17]), "=r"(r[0][18]), "=r"(r[0][19]), "=r"(r[0][20]), "=r"(r[0][21]), "=r"(r[0][22]), "=r"(r[0][23]), "=r"(r[0][24]), "=r"(r[0][25]), "=r"(r[0][26]), "=r"(r[0][27]), "=r"(r[0][28]), "=r"(r[0][29]), "=r"(r[0][30]), "=r"(r[0][31]), "=r"(r[1][0]), "=r"(r[1][1]), "=r"(r[1][2]), "=r"(r[1][3]), "=r"(r[1][4]), "=r"(r[1][5]), "=r"(r[1][6]), "=r"(r[1][7]), "=r"(r[1][8]), "=r"(r[1][9]), "=r"(r[1][10]), "=r"(r[1][11]), "=r"(r[1][12]), "=r"(r[1][13]), "=r"(r[1][14]), "=r"(r[1][15]), "=r"(r[1][16]), "=r"(r[1][17]), "=r"(r[1][18]), "=r"(r[1][19]), "=r"(r[1][20]), "=r"(r[1][21]), "=r"(r[1][22]), "=r"(r[1][23]), "=r"(r[1][24]), "=r"(r[1][25]), "=r"(r[1][26]), "=r"(r[1][27]), "=r"(r[1][28]), "=r"(r[1][29]), "=r"(r[1][30]), "=r"(r[1][31]), "=r"(r[2][0]), "=r"(r[2][1]), "=r"(r[2][2]), "=r"(r[2][3]), "=r"(r[2][4]), "=r"(r[2][5]), "=r"(r[2][6]), "=r"(r[2][7]), "=r"(r[2][8]), "=r"(r[2][9]), "=r"(r[2][10]), "=r"(r[2][11]), "=r"(r[2][12]), "=r"(r[2][13]), "=r"(r[2][14]), "=r"(r[2][15]), "=r"(r[2][16]), "=r"(r[2][17]), "=r"(r[2][18]), "=r"(r[2][19]), "=r"(r[2][20]), "=r"(r[2][21]), "=r"(r[2][22]), "=r"(r[2][23]), "=r"(r[2][24]), "=r"(r[2][25]), "=r"(r[2][26]), "=r"(r[2][27]), "=r"(r[2][28]), "=r"(r[2][29]), "=r"(r[2][30]), "=r"(r[2][31]), "=r"(r[3][0]), "=r"(r[3][1]), "=r"(r[3][2]), "=r"(r[3][3]), "=r"(r[3][4]), "=r"(r[3][5]), "=r"(r[3][6]), "=r"(r[3][7]), "=r"(r[3][8]), "=r"(r[3][9]), "=r"(r[3][10]), "=r"(r[3][11]), "=r"(r[3][12]), "=r"(r[3][13]), "=r"(r[3][14]), "=r"(r[3][15]), "=r"(r[3][16]), "=r"(r[3][17]), "=r"(r[3][18]), "=r"(r[3][19]), "=r"(r[3][20]), "=r"(r[3][21]), "=r"(r[3][22]), "=r"(r[3][23]), "=r"(r[3][24]), "=r"(r[3][25]), "=r"(r[3][26]), "=r"(r[3][27]), "=r"(r[3][28]), "=r"(r[3][29]), "=r"(r[3][30]), "=r"(r[3][31])
-        : "r"(taddr), "r"(taddr + 32), "r"(taddr + 64), "r"(taddr + 96)
-        : "memory");
-}
 __device__ __forceinline__ void tmem_store16(uint32_t taddr, const uint32_t (&v)[16])
 {
     asm volatile(
@@ -128,12 +114,21 @@ __device__ __forceinline__ float2 fadd2(float2 a, float2 b)
     return *reinterpret_cast<float2*>(&d);
 }
 
+__device__ __forceinline__ float largest(const uint32_t (&x)[32])
+{
+    float top = __uint_as_float(x[0]);
+#pragma unroll
+    for (int i = 0; i < 32; i += 2)
+        top = fmaxf(top, fmaxf(__uint_as_float(x[i]), __uint_as_float(x[i + 1])));
+    return top;
+}
+
 // What a CTA works on; the same in every thread.
 struct Unit {
     int b, head, split;
     int first, ntok, length;                 // the sequence's rows and tokens
     int row0, nrow;                          // rows row0 .. row0 + nrow - 1 of it
-    long long pos0;                          // position of the sequence's first new token
+    int pos0;                                // position of the sequence's first new token
     int kend, nsink, page_lo, npage;         // keys [0, kend); pages 0 .. nsink - 1, page_lo ..
     int i0, steps;                           // first page of this split's and its 128-key steps
 };
@@ -210,15 +205,14 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prompt_kernel(const AttendArgs 
     if (u.b < 0)
         return;   // fewer tiles than the host's bound
     u.nrow = min(ROWS, u.ntok * g.group - u.row0);
-    u.pos0 = static_cast<long long>(u.length) - u.ntok;
+    u.pos0 = max(u.length, 0) - u.ntok;
     {
-        const long long room = static_cast<long long>(g.c.max_pages) * KV_PAGE;
-        const long long plo = u.pos0 + u.row0 / g.group, phi = u.pos0 + (u.row0 + u.nrow - 1) / g.group;
-        u.kend = static_cast<int>(min(max(phi + 1, 0ll), room));
+        const int room = g.c.max_pages * KV_PAGE;
+        const int plo = u.pos0 + u.row0 / g.group, phi = u.pos0 + (u.row0 + u.nrow - 1) / g.group;
+        u.kend = min(max(phi + 1, 0), room);
         if (threadIdx.x == 0 && phi + 1 > room)
             *g.c.bad = 1u;
-        const int klo =
-            g.window > 0 ? static_cast<int>(min(max(plo - g.window + 1, 0ll), static_cast<long long>(u.kend))) : 0;
+        const int klo = g.window > 0 ? min(max(plo - g.window + 1, 0), u.kend) : 0;
         u.page_lo = klo / KV_PAGE;
         u.nsink = min((min(g.sinks, u.kend) + KV_PAGE - 1) / KV_PAGE, u.page_lo);
         u.npage = u.nsink + (u.kend + KV_PAGE - 1) / KV_PAGE - u.page_lo;
@@ -546,10 +540,10 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prompt_kernel(const AttendArgs 
 
         const uint32_t lanes = static_cast<uint32_t>(l & ~31) << 16;
         const uint32_t s_at = tmem + lanes + S_COL + TILE * w, o_at = tmem + lanes + O_COL + D * w;
-        const long long pos = mine ? u.pos0 + row / g.group : -1;
+        const int pos = mine ? u.pos0 + row / g.group : -1;
         // positions of the tile's rows, for steps that no mask touches
-        const long long plo = u.pos0 + (u.row0 + TILE * w) / g.group;
-        const long long phi = u.pos0 + (u.row0 + min(u.nrow, TILE * (w + 1)) - 1) / g.group;
+        const int plo = u.pos0 + (u.row0 + TILE * w) / g.group;
+        const int phi = u.pos0 + (u.row0 + min(u.nrow, TILE * (w + 1)) - 1) / g.group;
         float ref = -INFINITY, sum = 0.0f;
         bool ok = true;
         if (w == 0 || two) {
@@ -563,7 +557,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prompt_kernel(const AttendArgs 
                 bool plain = true;
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    const long long kbase = static_cast<long long>(page_of(u, u.i0 + 2 * j + h)) * KV_PAGE;
+                    const int kbase = page_of(u, u.i0 + 2 * j + h) * KV_PAGE;
                     const bool there = (h ? held.y : held.x) >= 0;
                     const bool whole = there && kbase + KV_PAGE - 1 <= plo &&
                                        (g.window == 0 || kbase > phi - g.window || kbase + KV_PAGE <= g.sinks);
@@ -582,71 +576,92 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prompt_kernel(const AttendArgs 
                 };
 
                 auto softmax = [&](auto with_mask) {
-                constexpr bool masked = decltype(with_mask)::value;
-                uint32_t x[4][32];
-                tmem_load128(s_at, x);
-                if constexpr (masked) {
-#pragma unroll
-                    for (int c = 0; c < 4; ++c)
-                        mask(x[c], seen[c]);
-                }
-                float tops[4];
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    tops[c] = __uint_as_float(x[c][0]);
-#pragma unroll
-                    for (int i = 0; i < 32; i += 2)
-                        tops[c] = fmaxf(tops[c], fmaxf(__uint_as_float(x[c][i]), __uint_as_float(x[c][i + 1])));
-                }
-                float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
-                top *= coef;
-                const bool raise = top > ref + KV_REF_LIMIT;   // also the first visible key
-                if (__any_sync(0xffffffffu, raise)) {
-                    const float next = raise ? top - KV_REF_BELOW : ref;
-                    const float f = raise ? kv_ex2(ref - next) : 1.0f;
-                    ref = next;
-                    sum *= f;
-                    if (j > 0) {
+                    constexpr bool masked = decltype(with_mask)::value;
+                    // the largest x, from all 128 columns at once
+                    uint32_t x[2][32];
+                    float tops[4];
+                    {
+                        uint32_t y[2][32];
+                        tmem_load32(s_at, x[0]);
+                        tmem_load32(s_at + 32, x[1]);
+                        tmem_load32(s_at + 64, y[0]);
+                        tmem_load32(s_at + 96, y[1]);
+                        tmem_arrived(x[0]);
+                        tmem_arrived(x[1]);
+                        tmem_arrived(y[0]);
+                        tmem_arrived(y[1]);
+                        if constexpr (masked) {
+                            mask(x[0], seen[0]);
+                            mask(x[1], seen[1]);
+                            mask(y[0], seen[2]);
+                            mask(y[1], seen[3]);
+                        }
+                        tops[0] = largest(x[0]);
+                        tops[1] = largest(x[1]);
+                        tops[2] = largest(y[0]);
+                        tops[3] = largest(y[1]);
+                    }
+                    const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])) * coef;
+                    const bool raise = top > ref + KV_REF_LIMIT;   // also the first visible key
+                    if (__any_sync(0xffffffffu, raise)) {
+                        const float next = raise ? top - KV_REF_BELOW : ref;
+                        const float f = raise ? kv_ex2(ref - next) : 1.0f;
+                        ref = next;
+                        sum *= f;
+                        if (j > 0) {
 #pragma unroll 1
-                        for (int d = 0; d < D; d += 32) {
-                            uint32_t o[32];
-                            tmem_load32(o_at + d, o);
-                            tmem_arrived(o);
+                            for (int d = 0; d < D; d += 32) {
+                                uint32_t o[32];
+                                tmem_load32(o_at + d, o);
+                                tmem_arrived(o);
 #pragma unroll
-                            for (int i = 0; i < 32; ++i)
-                                o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-                            tmem_store32(o_at + d, o);
+                                for (int i = 0; i < 32; ++i)
+                                    o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                                tmem_store32(o_at + d, o);
+                            }
                         }
                     }
-                }
-                const float base = ref == -INFINITY ? 0.0f : ref;
-                float2 part[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+                    // the weights, 32 columns at a time.  Rolled to two turns that read S again (the next
+                    // columns on their way) where the registers held it: as straight code the 128 values
+                    // took 1440 cycles for 560, the instructions coming too slowly
+                    const float base = ref == -INFINITY ? 0.0f : ref;
+                    float2 part[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+                    auto weigh = [&](const uint32_t (&y)[32], uint32_t at) {
+                        uint32_t hi[16], lo[16];
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    // in rounds over the 32 values, so that no instruction waits for the one before it
-                    float2 e[16];
-                    uint32_t hi[16], lo[16];
-#pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        e[i] = ffma2(make_float2(__uint_as_float(x[c][2 * i]), __uint_as_float(x[c][2 * i + 1])),
-                                     make_float2(coef, coef), make_float2(-base, -base));
-#pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        e[i] = make_float2(kv_ex2(e[i].x), kv_ex2(e[i].y));
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        part[i % 2] = fadd2(part[i % 2], e[i]);
+                        for (int i = 0; i < 16; ++i) {
+                            float2 e = ffma2(make_float2(__uint_as_float(y[2 * i]), __uint_as_float(y[2 * i + 1])),
+                                             make_float2(coef, coef), make_float2(-base, -base));
+                            e = make_float2(kv_ex2(e.x), kv_ex2(e.y));
+                            part[i % 2] = fadd2(part[i % 2], e);
+                            if (HL)
+                                kv_split2(e.x, e.y, hi[i], lo[i]);
+                            else
+                                hi[i] = kv_h2u(__floats2half2_rn(e.x, e.y));
+                        }
+                        // P's 32 keys go over columns of S that this thread is done with
+                        tmem_store16(at, hi);
                         if (HL)
-                            kv_split2(e[i].x, e[i].y, hi[i], lo[i]);
-                        else
-                            hi[i] = kv_h2u(__floats2half2_rn(e[i].x, e[i].y));
+                            tmem_store16(at + 16, lo);
+                    };
+#pragma unroll 1
+                    for (int c = 0; c < 2; ++c) {
+                        const uint32_t at = s_at + 64 * c;
+                        tmem_load32(at + 32, x[1]);
+                        weigh(x[0], at);
+                        tmem_arrived(x[1]);
+                        if constexpr (masked)
+                            mask(x[1], c == 0 ? seen[1] : seen[3]);
+                        if (c == 0)
+                            tmem_load32(at + 64, x[0]);
+                        weigh(x[1], at + 32);
+                        if (c == 0) {
+                            tmem_arrived(x[0]);
+                            if constexpr (masked)
+                                mask(x[0], seen[2]);
+                        }
                     }
-                    // P's keys 32 c .. 32 c + 31 go over columns of S that this thread has read
-                    tmem_store16(s_at + 32 * c, hi);
-                    if (HL)
-                        tmem_store16(s_at + 32 * c + 16, lo);
-                }
-                sum += (part[0].x + part[0].y) + (part[1].x + part[1].y);
+                    sum += (part[0].x + part[0].y) + (part[1].x + part[1].y);
                 };
                 // two builds, so that steps without a mask carry no selects or copies for it
                 if (plain)

@@ -98,15 +98,15 @@ __global__ void __launch_bounds__(WARPS * 32, MODE == WIDE ? 3 : D == 128 ? 4 : 
     if (threadIdx.x == 0 && tile == 0 && (rows_b + ROWS - 1) / ROWS > g.row_tiles)
         *g.c.bad = 1u;   // more new tokens than the caller's max_q: rows past it are not computed
     const int nrow = min(ROWS, rows_b - row0);
-    const long long pos0 = static_cast<long long>(g.c.length[b]) - rows_b / g.group;
-    const long long room = static_cast<long long>(g.c.max_pages) * KV_PAGE;
+    const int pos0 = max(g.c.length[b], 0) - rows_b / g.group;
+    const int room = g.c.max_pages * KV_PAGE;
     // positions of the tile's first and last row; keys [0, kend) are looked at
-    const long long plo = pos0 + row0 / g.group, phi = pos0 + (row0 + nrow - 1) / g.group;
-    const int kend = static_cast<int>(min(max(phi + 1, 0ll), room));
+    const int plo = pos0 + row0 / g.group, phi = pos0 + (row0 + nrow - 1) / g.group;
+    const int kend = min(max(phi + 1, 0), room);
     if (threadIdx.x == 0 && phi + 1 > room)
         *g.c.bad = 1u;
     // pages: the sinks' that lie wholly before the window's first, then the window's
-    const int klo = g.window > 0 ? static_cast<int>(min(max(plo - g.window + 1, 0ll), static_cast<long long>(kend))) : 0;
+    const int klo = g.window > 0 ? min(max(plo - g.window + 1, 0), kend) : 0;
     const int page_lo = klo / KV_PAGE;
     const int nsink = min((min(g.sinks, kend) + KV_PAGE - 1) / KV_PAGE, page_lo);
     const int npage = nsink + (kend + KV_PAGE - 1) / KV_PAGE - page_lo;
@@ -211,7 +211,7 @@ __global__ void __launch_bounds__(WARPS * 32, MODE == WIDE ? 3 : D == 128 ? 4 : 
         qf[j][3] = low.y;
     }
     float coef[SETS], ref[SETS], sum[SETS];
-    long long pos[SETS];   // the row sees keys up to here, -1: no row
+    int pos[SETS];   // the row sees keys up to here, -1: no row
 #pragma unroll
     for (int i = 0; i < SETS; ++i) {
         coef[i] = *reinterpret_cast<const float*>(smem + S::COEF + 4 * (n + 8 * i));
@@ -253,7 +253,7 @@ __global__ void __launch_bounds__(WARPS * 32, MODE == WIDE ? 3 : D == 128 ? 4 : 
             next_half();   // its other half is not there either
             continue;
         }
-        const long long kbase = static_cast<long long>(i < nsink ? i : page_lo + i - nsink) * KV_PAGE;
+        const int kbase = (i < nsink ? i : page_lo + i - nsink) * KV_PAGE;
 
         // x[o]: keys 8o + 2t and 8o + 2t + 1 of row n (and n + 8); two octets of keys at a time
         float x[8][SETS][2];
@@ -359,7 +359,7 @@ __global__ void __launch_bounds__(WARPS * 32, MODE == WIDE ? 3 : D == 128 ? 4 : 
         if (!ok)
             break;
         page -= P::V_CODES;
-        const int held = static_cast<int>(min(kend - kbase, static_cast<long long>(KV_PAGE)));
+        const int held = min(kend - kbase, KV_PAGE);
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk) {   // keys 16 kk .. 16 kk + 15
             uint32_t hi[SETS][2], lo[2];

@@ -115,16 +115,22 @@ __device__ __forceinline__ bool mbar_wait_asleep(uint32_t bar, uint32_t parity, 
 {
     if (mbar_try_wait(bar, parity))
         return true;
-    const uint64_t t0 = globaltimer_ns();
-    while (!mbar_try_wait_sleep(bar, parity, 20000u)) {
-        if (*reinterpret_cast<volatile unsigned int*>(err) != 0u)
-            return false;
-        if (globaltimer_ns() - t0 > limit_ns) {
-            atomicOr(err, ERR_WAIT_EXPIRED);
-            return false;
+    uint64_t t0 = 0;
+    for (uint32_t i = 1;; ++i) {
+        if (mbar_try_wait_sleep(bar, parity, 20000u))
+            return true;
+        if ((i & 31u) == 0) {   // a poll returns long before its hint; the check costs a global load
+            if (*reinterpret_cast<volatile unsigned int*>(err) != 0u)
+                return false;
+            const uint64_t now = globaltimer_ns();
+            if (i == 32u)
+                t0 = now;
+            else if (now - t0 > limit_ns) {
+                atomicOr(err, ERR_WAIT_EXPIRED);
+                return false;
+            }
         }
     }
-    return true;
 }
 
 // Bounded wait that ignores the error word, used only to drain a CTA's own copies
