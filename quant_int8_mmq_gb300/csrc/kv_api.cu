@@ -22,15 +22,20 @@ AttendPlan plan_attend(int dtype, int heads, int kv_heads, int dim, int batch, i
         pages = pages < seen ? pages : seen;
     }
     const long long rows = static_cast<long long>(max_q) * group;
-    p.kernel = rows > 64 ? 1 : 0;
-    // units: independent CTAs without parts; slots: CTAs that the chip holds at once; least,
-    // most: pages of a part
-    long long units, slots, least, most;
+    // The step kernel reads and widens the cache once per tile of 8 or 16 rows, the prompt kernel
+    // once per 256, whose products take the same time for any number of rows.  Measured, us, 16
+    // sequences of 8192 keys, 4 kv heads: f32 rows of 128 values, 24 rows 63 / 83, 48 rows
+    // 131 / 85; 16-bit ones 32 rows 54 / 59, 48 rows 74 / 60; 16-bit rows of 64, 64 rows
+    // 69 / 70, 96 rows 86 / 72.
+    p.kernel = rows > (dim == 64 && dtype != KV_F32 ? 64 : 32) ? 1 : 0;
+    // units: independent CTAs without parts; least, most: pages of a part
+    long long units, parts, least, most;
     if (p.kernel == 0) {
         p.tile_rows = dtype == KV_F32 || rows <= 8 ? 8 : 16;
         p.row_tiles = static_cast<int>((rows + p.tile_rows - 1) / p.tile_rows);
         units = static_cast<long long>(batch) * kv_heads * p.row_tiles;
-        slots = (p.tile_rows == 16 ? 3 : 4) * SMS;
+        parts = (p.tile_rows == 16 ? 3 : 4) * SMS / units;   // CTAs that the chip holds at once
+        parts = parts < 1 ? 1 : parts;
         least = 4;      // a page a warp
         most = 64;      // sequences of uneven length: parts even the load out
     } else {
@@ -39,12 +44,28 @@ AttendPlan plan_attend(int dtype, int heads, int kv_heads, int dim, int batch, i
             static_cast<long long>(ntok) * group / KV_PROMPT_ROWS + (batch < ntok ? batch : ntok);
         p.row_tiles = static_cast<int>(tiles < 0x7fffffffll ? tiles : 0x7fffffffll);
         units = tiles * kv_heads;
-        slots = SMS;
+        // Where the tiles do not fill the chip, parts do, and cost the trip of their sums through
+        // memory: the least of the expected times in us (GB300: a CTA's start and end 8; 128 keys
+        // of 256 rows 3.0 for f32 rows of 128 values, 1.8 for 16-bit ones, half of it for 64
+        // values; the join 3 and its bytes at 6 TB/s).  More tiles than SMs are left whole: two
+        // parts against the uneven last round took 821 us for 747 (2048 and 1944 tokens on 16384
+        // and 13563, 32 heads on 8).
+        const double step = (dtype == KV_F32 ? 3.0 : 1.8) * dim / 128;
+        const double bytes = 8.0 * ntok * heads * dim;
+        long long best = 1;
+        double least_us = 0;
+        for (long long n = 1; n == 1 || (units < SMS && n <= 64 && pages >= 8 * n); ++n) {
+            const double us = static_cast<double>((units * n + SMS - 1) / SMS) * (8 + step * pages / 2 / n) +
+                              (n == 1 ? 0 : 3 + n * bytes / 6e6);
+            if (n == 1 || us < least_us) {
+                best = n;
+                least_us = us;
+            }
+        }
+        parts = best;
         least = 8;
         most = 1ll << 30;
     }
-    long long parts = slots / units;
-    parts = parts < 1 ? 1 : parts;
     long long part = (pages + parts - 1) / parts;
     part = part < least ? least : part > most ? most : part;
     part = (part + 3) / 4 * 4;

@@ -13,13 +13,15 @@
 //
 // TMEM: S of each tile in 128 columns, its P over the S that it came from (per 32 keys 16
 // columns of hi and 16 of lo), O in D columns.  The tiles alternate on the tensor pipe, P V and the next Q K^T of one
-// while the other's softmax runs: a thread per row reads S, keeps the row's reference and
-// sum, and writes P.  A row's O is rescaled only when its reference moves, which the
+// while the other's softmax runs: two threads a row read S, keep the row's reference and
+// sums, and write P.  A row's O is rescaled only when its reference moves, which the
 // lag of kv.cuh makes rare, by the softmax thread itself: its S arrived behind the last
 // P V of the tile, so O is at rest.
 //
-// 16 warps: warp 0 issues the MMAs, warp 1 copies the pages' bytes into a ring, warps 4-7
-// widen, warps 8-11 and 12-15 are the softmax of tiles 0 and 1.  Every wait is bounded; on
+// 24 warps: warp 0 issues the MMAs, warp 1 copies the pages' bytes into a ring, warps 4-7
+// widen, warps 8-15 and 16-23 are the softmax of tiles 0 and 1: two threads a row, one for
+// each page of the step, which tell each other their largest x (with one thread a row the
+// softmax took 2000 of a step's 3500 cycles, the products waiting for it).  Every wait is bounded; on
 // expiry the roles leave their loops, copies and MMAs in flight are waited for, TMEM is
 // freed and the CTA ends.
 #include <type_traits>
@@ -29,14 +31,17 @@
 namespace mmq {
 namespace {
 
-constexpr int THREADS = 512;
+constexpr int THREADS = 768;
 constexpr int TILE = 128;                    // rows of a tile, keys of a step
 constexpr int ROWS = KV_PROMPT_ROWS;
 static_assert(ROWS == 2 * TILE, "two tiles");
 constexpr int WIDEN_WARP = 4, SOFT_WARP = 8;
-// The launch's 128 registers a thread, shared out by warpgroup.
-constexpr int LAUNCH_REGS = 128, CTRL_REGS = 48, WIDEN_REGS = 96, SOFT_REGS = 184;
-static_assert(CTRL_REGS + WIDEN_REGS + 2 * SOFT_REGS == 4 * LAUNCH_REGS, "register split");
+constexpr int SOFT_WARPS = 16;
+// The launch's 80 registers a thread, shared out by warpgroup.
+constexpr int LAUNCH_REGS = 80, CTRL_REGS = 24, WIDEN_REGS = 72, SOFT_REGS = 96;
+static_assert(CTRL_REGS + WIDEN_REGS + 4 * SOFT_REGS == 6 * LAUNCH_REGS, "register split");
+// .dec may only lower a warp's count and .inc only raise it (the other way is no instruction)
+static_assert(CTRL_REGS < LAUNCH_REGS && WIDEN_REGS < LAUNCH_REGS && SOFT_REGS > LAUNCH_REGS, "register split");
 constexpr int META = 8;   // steps whose page descriptions are kept: more than any role runs ahead
 
 // HL: hi and lo parts of Q and P.
@@ -57,7 +62,8 @@ struct Cfg {
     static constexpr int V = K + BUFS * K_BYTES;
     static constexpr int RING = V + BUFS * V_BYTES;
     static constexpr int META_AT = RING + STAGES * STAGE;        // int2 [META]: tokens held of each page, -1 no page
-    static constexpr int BAR = META_AT + META * 8;
+    static constexpr int RED = META_AT + META * 8;               // f32 [2][page][row]: what a row's threads tell
+    static constexpr int BAR = RED + 2 * 2 * ROWS * 4;           // each other
     enum { QFULL, RFULL, REMPTY = RFULL + STAGES, KFULL = REMPTY + STAGES, KEMPTY = KFULL + BUFS,
            VFULL = KEMPTY + BUFS, VEMPTY = VFULL + BUFS, SFULL = VEMPTY + BUFS, PFULL = SFULL + 2,
            OFULL = PFULL + 2, DRAIN = OFULL + 2, NBAR };
@@ -70,23 +76,17 @@ struct Cfg {
 
 constexpr uint32_t S_COL = 0, O_COL = 256;   // tile w: S at 128 w, O at 256 + D w
 
-// Starts the load of 32 columns of this thread's TMEM lane; the values are there after
-// tmem_arrived on the same array.
-__device__ __forceinline__ void tmem_load32(uint32_t taddr, uint32_t (&r)[32])
+// 64 columns, both halves on their way at once: a load's latency, some 250 cycles beside the
+// tensor cores' own traffic, is paid once.
+__device__ __forceinline__ void tmem_load64(uint32_t taddr, uint32_t (&r)[2][32])
 {
     asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
-        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-        : "r"(taddr)
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%64];\n\t"
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, [%65];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0][0]), "=r"(r[0][1]), "=r"(r[0][2]), "=r"(r[0][3]), "=r"(r[0][4]), "=r"(r[0][5]), "=r"(r[0][6]), "=r"(r[0][7]), "=r"(r[0][8]), "=r"(r[0][9]), "=r"(r[0][10]), "=r"(r[0][11]), "=r"(r[0][12]), "=r"(r[0][13]), "=r"(r[0][14]), "=r"(r[0][15]), "=r"(r[0][16]), "=r"(r[0][17]), "=r"(r[0][18]), "=r"(r[0][19]), "=r"(r[0][20]), "=r"(r[0][21]), "=r"(r[0][22]), "=r"(r[0][23]), "=r"(r[0][24]), "=r"(r[0][25]), "=r"(r[0][26]), "=r"(r[0][27]), "=r"(r[0][28]), "=r"(r[0][29]), "=r"(r[0][30]), "=r"(r[0][31]), "=r"(r[1][0]), "=r"(r[1][1]), "=r"(r[1][2]), "=r"(r[1][3]), "=r"(r[1][4]), "=r"(r[1][5]), "=r"(r[1][6]), "=r"(r[1][7]), "=r"(r[1][8]), "=r"(r[1][9]), "=r"(r[1][10]), "=r"(r[1][11]), "=r"(r[1][12]), "=r"(r[1][13]), "=r"(r[1][14]), "=r"(r[1][15]), "=r"(r[1][16]), "=r"(r[1][17]), "=r"(r[1][18]), "=r"(r[1][19]), "=r"(r[1][20]), "=r"(r[1][21]), "=r"(r[1][22]), "=r"(r[1][23]), "=r"(r[1][24]), "=r"(r[1][25]), "=r"(r[1][26]), "=r"(r[1][27]), "=r"(r[1][28]), "=r"(r[1][29]), "=r"(r[1][30]), "=r"(r[1][31])
+        : "r"(taddr), "r"(taddr + 32)
         : "memory");
-}
-__device__ __forceinline__ void tmem_arrived(uint32_t (&r)[32])
-{
-    asm volatile("tcgen05.wait::ld.sync.aligned;"
-                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
-                 :
-                 : "memory");
 }
 __device__ __forceinline__ void tmem_store16(uint32_t taddr, const uint32_t (&v)[16])
 {
@@ -96,15 +96,6 @@ __device__ __forceinline__ void tmem_store16(uint32_t taddr, const uint32_t (&v)
         "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
         : "memory");
 }
-__device__ __forceinline__ void tmem_store32(uint32_t taddr, const uint32_t (&v)[32])
-{
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
-        "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
-        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(v[16]), "r"(v[17]), "r"(v[18]), "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]), "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
-        : "memory");
-}
-
 __device__ __forceinline__ float2 fadd2(float2 a, float2 b)
 {
     uint64_t d;
@@ -112,15 +103,6 @@ __device__ __forceinline__ float2 fadd2(float2 a, float2 b)
         : "=l"(d)
         : "l"(*reinterpret_cast<uint64_t*>(&a)), "l"(*reinterpret_cast<uint64_t*>(&b)));
     return *reinterpret_cast<float2*>(&d);
-}
-
-__device__ __forceinline__ float largest(const uint32_t (&x)[32])
-{
-    float top = __uint_as_float(x[0]);
-#pragma unroll
-    for (int i = 0; i < 32; i += 2)
-        top = fmaxf(top, fmaxf(__uint_as_float(x[i]), __uint_as_float(x[i + 1])));
-    return top;
 }
 
 // What a CTA works on; the same in every thread.
@@ -225,7 +207,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prompt_kernel(const AttendArgs 
 
     // ---------------------------------------------------------------- setup
     if (threadIdx.x == 0) {
-        mbar_init(bar(C::QFULL), 8);
+        mbar_init(bar(C::QFULL), SOFT_WARPS);
         for (int i = 0; i < C::STAGES; ++i) {
             mbar_init(bar(C::RFULL + i), 1);
             mbar_init(bar(C::REMPTY + i), 4);
@@ -238,7 +220,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prompt_kernel(const AttendArgs 
         }
         for (int w = 0; w < 2; ++w) {
             mbar_init(bar(C::SFULL + w), 1);
-            mbar_init(bar(C::PFULL + w), 4);
+            mbar_init(bar(C::PFULL + w), 8);
             mbar_init(bar(C::OFULL + w), 1);
         }
         mbar_init(bar(C::DRAIN), 1);
@@ -474,8 +456,10 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prompt_kernel(const AttendArgs 
     } else {
         // ------------------------------------------------------------ softmax: a thread per row
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(SOFT_REGS));
-        const int w = (warp - SOFT_WARP) / 4;                           // tile
-        const int l = threadIdx.x - (SOFT_WARP + 4 * w) * 32;           // TMEM lane
+        const int w = (warp - SOFT_WARP) / 8, h = (warp - SOFT_WARP) / 4 % 2;   // tile, page of a step
+        const int l = warp % 4 * 32 + lane;                                      // TMEM lane
+        const int pair = 1 + 4 * w + warp % 4;   // named barrier of the two warps that share 32 rows
+        float* red = reinterpret_cast<float*>(smem + C::RED) + TILE * w + l;     // [2][page]: ROWS apart
         const bool mine = TILE * w + l < u.nrow;
         const int row = u.row0 + min(TILE * w + l, u.nrow - 1);
         const long long token = u.first + row / g.group;
@@ -484,14 +468,14 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prompt_kernel(const AttendArgs 
         float coef = 1.0f;
         if (u.steps > 0) {
             // 2^-e q into the operand tiles, e the exponent of the row's largest magnitude.  The
-            // warp loads its 32 rows, eight lanes a row (lanes past the last row load that
+            // warp loads 16 of its 32 rows, eight lanes a row (lanes past the last row load that
             // one again: their rows go nowhere)
-            constexpr int LOADS = D / 32;                                   // of four values a lane, four rows at once
-            constexpr int BATCH = sizeof(T) == 4 && D == 128 ? 4 : 8;       // 64 registers of loads on their way
+            constexpr int LOADS = D / 32;                              // of four values a lane, four rows at once
+            constexpr int BATCH = sizeof(T) == 4 && D == 128 ? 2 : 4;  // 32 registers of loads on their way
             const int sub = lane / 8, c = lane % 8 * 4;
             uint8_t* dst = smem + C::Q + w * C::PARTS * C::KB * C::BLOCK;
 #pragma unroll 1
-            for (int i0 = 0; i0 < 32; i0 += 4 * BATCH) {
+            for (int i0 = 16 * h; i0 < 16 * h + 16; i0 += 4 * BATCH) {
                 Raw4<T> x[BATCH][LOADS];
 #pragma unroll
                 for (int k = 0; k < BATCH; ++k) {
@@ -502,13 +486,12 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prompt_kernel(const AttendArgs 
                 }
 #pragma unroll
                 for (int k = 0; k < BATCH; ++k) {
-                    const int r32 = (l & ~31) + i0 + 4 * k + sub;
-                    float4 v[LOADS];
+                    const int r32 = warp % 4 * 32 + i0 + 4 * k + sub;
                     float a = 0.0f;
 #pragma unroll
                     for (int i = 0; i < LOADS; ++i) {
-                        v[i] = x[k][i].get();
-                        a = fmaxf(a, fmaxf(fmaxf(fabsf(v[i].x), fabsf(v[i].y)), fmaxf(fabsf(v[i].z), fabsf(v[i].w))));
+                        const float4 v = x[k][i].get();
+                        a = fmaxf(a, fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w))));
                     }
 #pragma unroll
                     for (int s = 1; s < 8; s <<= 1)
@@ -518,18 +501,17 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prompt_kernel(const AttendArgs 
 #pragma unroll
                     for (int i = 0; i < LOADS; ++i) {
                         const int d = 32 * i + c;
+                        const float4 v = x[k][i].get();
                         uint2 hi, lo;
-                        kv_split2(v[i].x * f, v[i].y * f, hi.x, lo.x);
-                        kv_split2(v[i].z * f, v[i].w * f, hi.y, lo.y);
+                        kv_split2(v.x * f, v.y * f, hi.x, lo.x);
+                        kv_split2(v.z * f, v.w * f, hi.y, lo.y);
                         uint8_t* at = dst + d / 64 * C::BLOCK + r32 * 128 + ((d / 8 % 8 ^ (r32 & 7)) << 4) + d % 8 * 2;
                         *reinterpret_cast<uint2*>(at) = hi;
                         if (HL)
                             *reinterpret_cast<uint2*>(at + C::KB * C::BLOCK) = lo;
                     }
-                    const int own = lane - (i0 + 4 * k);   // the lane's row is one of these four
-                    const int its = __shfl_sync(0xffffffffu, e, (own & 3) * 8);
-                    if (own >= 0 && own < 4)
-                        coef = fminf(fmaxf(g.scale_log2 * kv_pow2(its), 1e-38f), 1e38f);
+                    if (c == 0)
+                        red[r32 - l] = fminf(fmaxf(g.scale_log2 * kv_pow2(e), 1e-38f), 1e38f);
                 }
             }
             fence_proxy_async_smem();
@@ -537,9 +519,14 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prompt_kernel(const AttendArgs 
             if (lane == 0)
                 mbar_arrive(bar(C::QFULL));
         }
+        named_bar_sync(pair, 64);
+        if (u.steps > 0)
+            coef = red[0];
+        named_bar_sync(pair, 64);   // both have read theirs
 
         const uint32_t lanes = static_cast<uint32_t>(l & ~31) << 16;
-        const uint32_t s_at = tmem + lanes + S_COL + TILE * w, o_at = tmem + lanes + O_COL + D * w;
+        const uint32_t s_at = tmem + lanes + S_COL + TILE * w + 64 * h;
+        const uint32_t o_at = tmem + lanes + O_COL + D * w + D / 2 * h;   // each thread has half of the row's O
         const int pos = mine ? u.pos0 + row / g.group : -1;
         // positions of the tile's rows, for steps that no mask touches
         const int plo = u.pos0 + (u.row0 + TILE * w) / g.group;
@@ -549,59 +536,37 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prompt_kernel(const AttendArgs 
         if (w == 0 || two) {
             for (int j = 0; j < u.steps; ++j) {
                 ok = warp_wait(g, bar(C::SFULL + w), j & 1);
-                if (!ok)
-                    break;
                 tc_fence_after();
                 const int2 held = reinterpret_cast<const int2*>(smem + C::META_AT)[j % META];
-                uint32_t seen[4];   // bit i of seen[c]: key 32 c + i
-                bool plain = true;
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int kbase = page_of(u, u.i0 + 2 * j + h) * KV_PAGE;
-                    const bool there = (h ? held.y : held.x) >= 0;
-                    const bool whole = there && kbase + KV_PAGE - 1 <= plo &&
-                                       (g.window == 0 || kbase > phi - g.window || kbase + KV_PAGE <= g.sinks);
-                    uint64_t m = ~0ull;
-                    if (!whole) {
-                        plain = false;
-                        m = there ? kv_seen_bits(pos, kbase, g.window, g.sinks) : 0;
-                    }
-                    seen[2 * h] = static_cast<uint32_t>(m);
-                    seen[2 * h + 1] = static_cast<uint32_t>(m >> 32);
-                }
-                auto mask = [&](uint32_t (&x)[32], uint32_t m) {
-#pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        x[i] = m >> i & 1u ? x[i] : 0xff800000u;   // -inf
-                };
+                const int kbase = page_of(u, u.i0 + 2 * j + h) * KV_PAGE;
+                const bool there = (h ? held.y : held.x) >= 0;
+                const bool plain = there && kbase + KV_PAGE - 1 <= plo &&
+                                   (g.window == 0 || kbase > phi - g.window || kbase + KV_PAGE <= g.sinks);
 
+                // false: one of the two warps has given up
                 auto softmax = [&](auto with_mask) {
-                    constexpr bool masked = decltype(with_mask)::value;
-                    // the largest x, from all 128 columns at once
                     uint32_t x[2][32];
-                    float tops[4];
-                    {
-                        uint32_t y[2][32];
-                        tmem_load32(s_at, x[0]);
-                        tmem_load32(s_at + 32, x[1]);
-                        tmem_load32(s_at + 64, y[0]);
-                        tmem_load32(s_at + 96, y[1]);
-                        tmem_arrived(x[0]);
-                        tmem_arrived(x[1]);
-                        tmem_arrived(y[0]);
-                        tmem_arrived(y[1]);
-                        if constexpr (masked) {
-                            mask(x[0], seen[0]);
-                            mask(x[1], seen[1]);
-                            mask(y[0], seen[2]);
-                            mask(y[1], seen[3]);
-                        }
-                        tops[0] = largest(x[0]);
-                        tops[1] = largest(x[1]);
-                        tops[2] = largest(y[0]);
-                        tops[3] = largest(y[1]);
+                    tmem_load64(s_at, x);
+                    if constexpr (decltype(with_mask)::value) {
+                        const uint64_t seen = there ? kv_seen_bits(pos, kbase, g.window, g.sinks) : 0;
+#pragma unroll
+                        for (int i = 0; i < 64; ++i)
+                            x[i / 32][i % 32] = seen >> i & 1u ? x[i / 32][i % 32] : 0xff800000u;   // -inf
                     }
-                    const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])) * coef;
+                    float tops[4];
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        tops[c] = __uint_as_float(x[c / 2][c % 2 * 16]);
+#pragma unroll
+                        for (int i = 0; i < 16; i += 2)
+                            tops[c] = fmaxf(tops[c], fmaxf(__uint_as_float(x[c / 2][c % 2 * 16 + i]),
+                                                           __uint_as_float(x[c / 2][c % 2 * 16 + i + 1])));
+                    }
+                    float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
+                    red[(2 * (j & 1) + h) * ROWS] = top;
+                    if (!named_bar_and(pair, 64, ok))
+                        return false;
+                    top = fmaxf(top, red[(2 * (j & 1) + 1 - h) * ROWS]) * coef;
                     const bool raise = top > ref + KV_REF_LIMIT;   // also the first visible key
                     if (__any_sync(0xffffffffu, raise)) {
                         const float next = raise ? top - KV_REF_BELOW : ref;
@@ -610,27 +575,25 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prompt_kernel(const AttendArgs 
                         sum *= f;
                         if (j > 0) {
 #pragma unroll 1
-                            for (int d = 0; d < D; d += 32) {
-                                uint32_t o[32];
-                                tmem_load32(o_at + d, o);
-                                tmem_arrived(o);
+                            for (int d = 0; d < D / 2; d += 16) {
+                                float o[16];
+                                uint32_t v[16];
+                                tmem_ld16_wait(o_at + d, o);
 #pragma unroll
-                                for (int i = 0; i < 32; ++i)
-                                    o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-                                tmem_store32(o_at + d, o);
+                                for (int i = 0; i < 16; ++i)
+                                    v[i] = __float_as_uint(o[i] * f);
+                                tmem_store16(o_at + d, v);
                             }
                         }
                     }
-                    // the weights, 32 columns at a time.  Rolled to two turns that read S again (the next
-                    // columns on their way) where the registers held it: as straight code the 128 values
-                    // took 1440 cycles for 560, the instructions coming too slowly
                     const float base = ref == -INFINITY ? 0.0f : ref;
                     float2 part[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
-                    auto weigh = [&](const uint32_t (&y)[32], uint32_t at) {
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
                         uint32_t hi[16], lo[16];
 #pragma unroll
                         for (int i = 0; i < 16; ++i) {
-                            float2 e = ffma2(make_float2(__uint_as_float(y[2 * i]), __uint_as_float(y[2 * i + 1])),
+                            float2 e = ffma2(make_float2(__uint_as_float(x[c][2 * i]), __uint_as_float(x[c][2 * i + 1])),
                                              make_float2(coef, coef), make_float2(-base, -base));
                             e = make_float2(kv_ex2(e.x), kv_ex2(e.y));
                             part[i % 2] = fadd2(part[i % 2], e);
@@ -639,35 +602,18 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prompt_kernel(const AttendArgs 
                             else
                                 hi[i] = kv_h2u(__floats2half2_rn(e.x, e.y));
                         }
-                        // P's 32 keys go over columns of S that this thread is done with
-                        tmem_store16(at, hi);
+                        // P's keys go over columns of S that this thread has read
+                        tmem_store16(s_at + 32 * c, hi);
                         if (HL)
-                            tmem_store16(at + 16, lo);
-                    };
-#pragma unroll 1
-                    for (int c = 0; c < 2; ++c) {
-                        const uint32_t at = s_at + 64 * c;
-                        tmem_load32(at + 32, x[1]);
-                        weigh(x[0], at);
-                        tmem_arrived(x[1]);
-                        if constexpr (masked)
-                            mask(x[1], c == 0 ? seen[1] : seen[3]);
-                        if (c == 0)
-                            tmem_load32(at + 64, x[0]);
-                        weigh(x[1], at + 32);
-                        if (c == 0) {
-                            tmem_arrived(x[0]);
-                            if constexpr (masked)
-                                mask(x[0], seen[2]);
-                        }
+                            tmem_store16(s_at + 32 * c + 16, lo);
                     }
                     sum += (part[0].x + part[0].y) + (part[1].x + part[1].y);
+                    return true;
                 };
-                // two builds, so that steps without a mask carry no selects or copies for it
-                if (plain)
-                    softmax(std::false_type{});
-                else
-                    softmax(std::true_type{});
+                // two builds, so that steps without a mask carry no selects for it
+                ok = plain ? softmax(std::false_type{}) : softmax(std::true_type{});
+                if (!ok)
+                    break;
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
@@ -675,58 +621,55 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prompt_kernel(const AttendArgs 
                     mbar_arrive(bar(C::PFULL + w));
             }
             if (ok && u.steps > 0) {
-                ok = warp_wait(g, bar(C::OFULL + w), 0);
+                warp_wait(g, bar(C::OFULL + w), 0);
                 tc_fence_after();
             }
-            // a row's share of the result, by way of shared memory (the tile's Q is done with): the
-            // warp writes four rows' 32 values at a time, whole lines for the strided 16 bytes a
-            // thread that its own row would take
+        }
+        red[2 * ROWS * (u.steps & 1) + h * ROWS] = sum;
+        named_bar_sync(pair, 64);
+        sum += red[2 * ROWS * (u.steps & 1) + (1 - h) * ROWS];
+        if (w == 0 || two) {
+            // half of a row's share of the result, by way of shared memory (the tile's Q is done
+            // with): the warp writes four rows' 32 values at a time, whole lines for the strided 16
+            // bytes a thread that its own row would take
             const float inv = g.nsplit > 1 ? 1.0f : sum == 0.0f ? 0.0f : 1.0f / sum;
             const long long flat = token * g.heads + head;
             const long long part_at = static_cast<long long>(u.split) * g.ntok * g.heads + flat;
             const long long out_at = g.nsplit > 1 ? part_at * D : token * g.out.tok + head * g.out.head;
-            if (g.nsplit > 1 && mine)
+            if (g.nsplit > 1 && mine && h == 0)
                 g.part_ml[part_at] = make_float2(ref, sum);
-            constexpr int ROW = 32 * 4 + 16;
-            static_assert(8 * 32 * ROW <= C::Q_BYTES + C::K_BYTES, "staged rows");
+            constexpr int COLS = D == 64 && !HL ? 16 : 32;   // values staged at a time
+            constexpr int ROW = COLS * 4 + 16, LPR = COLS / 4;
+            static_assert(SOFT_WARPS * 32 * ROW <= C::Q_BYTES + C::K_BYTES, "staged rows");
             uint8_t* stage = smem + C::Q + (warp - SOFT_WARP) * 32 * ROW;
-            const int sub = lane / 8, c = lane % 8 * 4;
-            long long at[8];   // of the eight rows whose values c .. c + 3 this lane writes
-            uint32_t there = 0;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                at[i] = __shfl_sync(0xffffffffu, out_at, 4 * i + sub) + c;
-                there |= (__shfl_sync(0xffffffffu, mine, 4 * i + sub) ? 1u : 0u) << i;
-            }
-#pragma unroll
-            for (int d = 0; d < D; d += 32) {
-                uint32_t o[32];
+            const int sub = lane / LPR, c = lane % LPR * 4;
+#pragma unroll 1
+            for (int d = 0; d < D / 2; d += COLS) {
+                float o[COLS];
                 if (u.steps > 0) {
-                    tmem_load32(o_at + d, o);
-                    tmem_arrived(o);
+#pragma unroll
+                    for (int i = 0; i < COLS; i += 16)
+                        tmem_ld16_wait(o_at + d + i, *reinterpret_cast<float(*)[16]>(o + i));
                 }
 #pragma unroll
-                for (int i = 0; i < 32; i += 4) {
-                    float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                    if (u.steps > 0)
-                        v = make_float4(__uint_as_float(o[i]) * inv, __uint_as_float(o[i + 1]) * inv,
-                                        __uint_as_float(o[i + 2]) * inv, __uint_as_float(o[i + 3]) * inv);
-                    *reinterpret_cast<float4*>(stage + lane * ROW + i * 4) = v;
-                }
-                __syncwarp();
-                float4 v[8];
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    v[i] = *reinterpret_cast<const float4*>(stage + (4 * i + sub) * ROW + c * 4);
+                for (int i = 0; i < COLS; i += 4)
+                    *reinterpret_cast<float4*>(stage + lane * ROW + i * 4) =
+                        u.steps > 0 ? make_float4(o[i] * inv, o[i + 1] * inv, o[i + 2] * inv, o[i + 3] * inv)
+                                    : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
                 __syncwarp();
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    if (there >> i & 1u) {
+                for (int i = 0; i < LPR; ++i) {
+                    const int src = 32 / LPR * i + sub;
+                    const long long at = __shfl_sync(0xffffffffu, out_at, src) + c + D / 2 * h + d;
+                    const float4 v = *reinterpret_cast<const float4*>(stage + src * ROW + c * 4);
+                    if (__shfl_sync(0xffffffffu, mine, src)) {
                         if (g.nsplit > 1)
-                            *reinterpret_cast<float4*>(g.part + at[i] + d) = v[i];
+                            *reinterpret_cast<float4*>(g.part + at) = v;
                         else
-                            store4(static_cast<T*>(g.out.data) + at[i] + d, v[i], g.wide);
+                            store4(static_cast<T*>(g.out.data) + at, v, g.wide);
                     }
+                }
+                __syncwarp();
             }
         }
     }
