@@ -245,8 +245,8 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prompt_kernel(const AttendArgs 
             constexpr uint32_t qk = idesc_f16_f32(TILE, TILE), pv = idesc_f16_f32(TILE, D);
             auto product_qk = [&](int w, int buf) {
 #pragma unroll
-                for (int part = 0; part < C::PARTS; ++part)
-#pragma unroll
+                for (int part = C::PARTS - 1; part >= 0; --part)   // lo first: the sums are cut toward zero,
+#pragma unroll                                                 // by less while they are small
                     for (int kb = 0; kb < C::KB; ++kb) {
                         const uint64_t a =
                             sdesc_k_sw128(sbase + C::Q + ((w * C::PARTS + part) * C::KB + kb) * C::BLOCK);
@@ -254,7 +254,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prompt_kernel(const AttendArgs 
 #pragma unroll
                         for (int kk = 0; kk < 4; ++kk)
                             umma_f16_by(lead, tmem + S_COL + TILE * w, a + 2u * kk, b + 2u * kk, qk,
-                                        (part | kb | kk) ? 1u : 0u);
+                                        (part < C::PARTS - 1 || kb || kk) ? 1u : 0u);
                     }
                 umma_commit_by(lead, bar(C::SFULL + w));
             };

@@ -261,7 +261,9 @@ __global__ void __launch_bounds__(WARPS * 32, MODE == WIDE ? 3 : D == 128 ? 4 : 
         for (int oct = 0; oct < 8; oct += 2) {
             uint32_t w[2][D / 32];
             __half2 s[2], sb[2];
-            float c[2][4];
+            // f32 rows: two sums a key, as the tensor cores cut sums toward zero at every step
+            constexpr int SUMS = MODE == HI_LO ? 2 : 1;
+            float c[2][SUMS][4];
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 const int token = 8 * (oct + h) + n;
@@ -276,30 +278,28 @@ __global__ void __launch_bounds__(WARPS * 32, MODE == WIDE ? 3 : D == 128 ? 4 : 
                 sb[h] = kv_addend(s[h]);
             }
 #pragma unroll
-            for (int j = 0; j < D / 32; ++j) {
+            for (int j = 0; j < D / 16; ++j)
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    const uint32_t b0 = kv_h2u(kv_widen<0>(w[h][j], s[h], sb[h]));
-                    const uint32_t b1 = kv_h2u(kv_widen<1>(w[h][j], s[h], sb[h]));
-                    if (j == 0)
-                        mma16816_first(c[h], qf[0][0], qf[0][1], qf[0][2], qf[0][3], b0, b1);
+                    const uint32_t v = w[h][j / 2];
+                    const uint32_t b0 = kv_h2u(j % 2 ? kv_widen<2>(v, s[h], sb[h]) : kv_widen<0>(v, s[h], sb[h]));
+                    const uint32_t b1 = kv_h2u(j % 2 ? kv_widen<3>(v, s[h], sb[h]) : kv_widen<1>(v, s[h], sb[h]));
+                    if (j < SUMS)
+                        mma16816_first(c[h][j % SUMS], qf[j][0], qf[j][1], qf[j][2], qf[j][3], b0, b1);
                     else
-                        mma16816(c[h], qf[2 * j][0], qf[2 * j][1], qf[2 * j][2], qf[2 * j][3], b0, b1);
+                        mma16816(c[h][j % SUMS], qf[j][0], qf[j][1], qf[j][2], qf[j][3], b0, b1);
                 }
-#pragma unroll
-                for (int h = 0; h < 2; ++h)
-                    mma16816(c[h], qf[2 * j + 1][0], qf[2 * j + 1][1], qf[2 * j + 1][2], qf[2 * j + 1][3],
-                             kv_h2u(kv_widen<2>(w[h][j], s[h], sb[h])), kv_h2u(kv_widen<3>(w[h][j], s[h], sb[h])));
-            }
 #pragma unroll
             for (int h = 0; h < 2; ++h)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     if constexpr (MODE == WIDE) {
-                        x[oct + h][0][e] = c[h][e];
-                        x[oct + h][1][e] = c[h][e + 2];
+                        x[oct + h][0][e] = c[h][0][e];
+                        x[oct + h][1][e] = c[h][0][e + 2];
+                    } else if constexpr (MODE == HI_LO) {
+                        x[oct + h][0][e] = (c[h][0][e + 2] + c[h][1][e + 2]) + (c[h][0][e] + c[h][1][e]);
                     } else {
-                        x[oct + h][0][e] = c[h][e] + c[h][e + 2];
+                        x[oct + h][0][e] = c[h][0][e] + c[h][0][e + 2];
                     }
                 }
         }
