@@ -32,6 +32,7 @@ __all__ = [
 
 MMQ_Q4_K = 12
 MMQ_Q6_K = 14
+MMQ_ERR_ARG = 1
 TYPES = {"q4_K": MMQ_Q4_K, "q6_K": MMQ_Q6_K}
 DTYPES = {"float32": 0, "float16": 1, "bfloat16": 2}     # mmq_dtype by torch's name
 KV_PAGE = 64                                             # tokens per page of the 4-bit key/value cache
@@ -420,15 +421,17 @@ def kv_pages(num_pages, kv_heads, head_dim, device="cuda"):
 def _kv_cache(pages, table, start, length):
     """The batch as a KVCache structure.  One chain of cheap checks for a right call (a decoding
     step's time is the host's); a wrong one is told what is wrong."""
-    torch = _torch()
+    torch = _torch_module or _torch()
     i32, dev = torch.int32, pages.get_device()
-    if (pages.dtype is torch.uint8 and pages.dim() == 3 and table.dtype is i32 and table.dim() == 2
-            and start.dtype is i32 and start.dim() == 1 and length.dtype is i32 and length.dim() == 1
-            and pages.is_contiguous() and table.is_contiguous() and start.is_contiguous() and length.is_contiguous()):
-        num_pages, kv_heads, piece = pages.shape
-        batch, max_pages = table.shape
-        if (piece % 72 == 0 and start.shape[0] == batch + 1 and length.shape[0] == batch
-                and dev >= 0 and dev == table.get_device() == start.get_device() == length.get_device()):
+    if (pages.dtype is torch.uint8 and table.dtype is i32 and start.dtype is i32 and length.dtype is i32
+            and pages.is_contiguous() and table.is_contiguous() and start.is_contiguous() and length.is_contiguous()
+            and dev >= 0 and dev == table.get_device() == start.get_device() == length.get_device()):
+        try:
+            (num_pages, kv_heads, piece), (batch, max_pages) = pages.shape, table.shape
+            (nstart,), (nlength,) = start.shape, length.shape
+        except ValueError:
+            piece = 1
+        if piece % 72 == 0 and nstart == batch + 1 and nlength == batch:
             return KVCache(pages.data_ptr(), table.data_ptr(), start.data_ptr(), length.data_ptr(), num_pages,
                            kv_heads, piece // 72, batch, max_pages), dev
     if pages.dtype != torch.uint8 or pages.dim() != 3 or not pages.is_contiguous() or pages.shape[2] % 72:
@@ -457,12 +460,12 @@ def _kv_rows(x, rows, heads, dim, dev, name):
 
 def _kv_stream(stream, dev):
     """Handle of the given or the device's current stream."""
-    return _torch()._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+    return _torch_module._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
 
 
 def _kv_empty(shape, dtype, device, stream):
     """Memory that belongs to the stream that uses it."""
-    torch = _torch()
+    torch = _torch_module
     if stream is None:
         return torch.empty(shape, dtype=dtype, device=device)
     with torch.cuda.stream(stream):
@@ -474,8 +477,8 @@ def kv_write(k, v, pages, table, start, length, stream=None):
     into the cache."""
     c, dev = _kv_cache(pages, table, start, length)
     rows, hk, dim = k.shape[0], c.kv_heads, c.head_dim
-    st = load().mmq_kv_write(c, _kv_rows(k, rows, hk, dim, dev, "k"), _kv_rows(v, rows, hk, dim, dev, "v"), rows,
-                             _kv_stream(stream, dev) or None)
+    st = (_lib or load()).mmq_kv_write(c, _kv_rows(k, rows, hk, dim, dev, "k"), _kv_rows(v, rows, hk, dim, dev, "v"), rows,
+                                       _kv_stream(stream, dev) or None)
     if st:
         raise MMQError(st, "kv_write")
 
@@ -489,8 +492,8 @@ def kv_read(pages, table, start, length, rows, dtype=None, k=None, v=None, strea
         k = _kv_empty((rows, hk, dim), dtype or _torch().float16, pages.device, stream)
     if v is None:
         v = _kv_empty((rows, hk, dim), k.dtype, pages.device, stream)
-    st = load().mmq_kv_read(c, _kv_rows(k, rows, hk, dim, dev, "k"), _kv_rows(v, rows, hk, dim, dev, "v"), rows,
-                            _kv_stream(stream, dev) or None)
+    st = (_lib or load()).mmq_kv_read(c, _kv_rows(k, rows, hk, dim, dev, "k"), _kv_rows(v, rows, hk, dim, dev, "v"), rows,
+                                      _kv_stream(stream, dev) or None)
     if st:
         raise MMQError(st, "kv_read")
     return k, v
@@ -509,22 +512,22 @@ def kv_attend(q, pages, table, start, length, max_q, max_kv=None, scale=None, wi
     if scale is None:
         scale = dim ** -0.5
     rq = _kv_rows(q, rows, heads, dim, dev, "q")
-    lib, size = load(), ctypes.c_size_t()
-    st = lib.mmq_kv_attend_workspace_bytes(c, rq.dtype, heads, rows, max_q, max_kv, window, sinks, size)
-    if st:
-        raise MMQError(st, "kv_attend")
-    need, at = size.value, None
     if out is None:
-        out = _torch().empty_like(q) if stream is None and q.is_contiguous() else _kv_empty(
+        out = _torch_module.empty_like(q) if stream is None and q.is_contiguous() else _kv_empty(
             (rows, heads, dim), q.dtype, q.device, stream)
-    if need:
+    ro = _kv_rows(out, rows, heads, dim, dev, "out")
+    call, handle = (_lib or load()).mmq_kv_attend, _kv_stream(stream, dev) or None
+    # most calls of few tokens need no workspace, and asking costs as much as a call that does
+    st = MMQ_ERR_ARG
+    if workspace is None:
+        st = call(c, rq, ro, heads, rows, max_q, max_kv, scale, window, sinks, None, 0, handle)
+    if st == MMQ_ERR_ARG:
+        need = mmq_kv_attend_workspace_bytes(c, rq.dtype, heads, rows, max_q, max_kv, window, sinks)
         if workspace is None:
-            workspace = _kv_empty((need,), _torch().uint8, q.device, stream)
+            workspace = _kv_empty((need,), _torch_module.uint8, q.device, stream)
         elif workspace.get_device() != dev or not workspace.is_contiguous() or _nbytes(workspace) < need:
             raise ValueError(f"workspace must be a contiguous CUDA buffer of at least {need} bytes")
-        at = workspace.data_ptr()
-    st = lib.mmq_kv_attend(c, rq, _kv_rows(out, rows, heads, dim, dev, "out"), heads, rows, max_q, max_kv, scale,
-                           window, sinks, at, need, _kv_stream(stream, dev) or None)
+        st = call(c, rq, ro, heads, rows, max_q, max_kv, scale, window, sinks, workspace.data_ptr(), need, handle)
     if st:
         raise MMQError(st, "kv_attend")
     return out

@@ -392,3 +392,13 @@ def test_a_prompt_and_its_tokens_one_by_one_agree():
         length = torch.tensor([hi], dtype=torch.int32, device=DEV)
         parts.append(mmq.kv_attend(q[lo:hi], b.pages, b.table, start, length, max_q=hi - lo))
     b.check(q, torch.cat(parts))
+
+
+@pytest.mark.parametrize("kv_heads,dim,hidden", [(2, 128, 512), (1, 64, 256)])
+def test_example_block(kv_heads, dim, hidden):
+    """The example's prompt and steps agree up to what the products before the attention differ by
+    (their kernels for few and many tokens, 1e-5 of a row, which may move a 4-bit code)."""
+    from examples import attention_block
+    worst = attention_block.main(["--hidden", str(hidden), "--heads", str(hidden // dim), "--kv-heads", str(kv_heads),
+                                  "--dim", str(dim), "--prompt", "150", "--steps", "3"])
+    assert worst < 1e-3
