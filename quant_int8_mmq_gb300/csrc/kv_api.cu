@@ -23,11 +23,12 @@ AttendPlan plan_attend(int dtype, int heads, int kv_heads, int dim, int batch, i
     }
     const long long rows = static_cast<long long>(max_q) * group;
     // The step kernel reads and widens the cache once per tile of 8 or 16 rows, the prompt kernel
-    // once per 256, whose products take the same time for any number of rows.  Measured, us, 16
-    // sequences of 8192 keys, 4 kv heads: f32 rows of 128 values, 24 rows 63 / 83, 48 rows
-    // 131 / 85; 16-bit ones 32 rows 54 / 59, 48 rows 74 / 60; 16-bit rows of 64, 64 rows
-    // 69 / 70, 96 rows 86 / 72.
-    p.kernel = rows > (dim == 64 && dtype != KV_F32 ? 64 : 32) ? 1 : 0;
+    // once per 256, at a cost that hardly depends on how many there are.  Measured, us, step /
+    // prompt kernel, 16 sequences of 8192 keys and 4 kv heads: f32 rows of 128 values, 32 rows
+    // 91 / 90, 48 rows 134 / 92; 16-bit ones 16 rows 30 / 50, 24 rows 54 / 50; f32 rows of 64,
+    // 24 rows 42 / 48, 32 rows 58 / 49; 16-bit ones 32 rows 34 / 45, 48 rows 45 / 45.
+    const int few = dtype == KV_F32 ? (dim == 128 ? 32 : 24) : (dim == 128 ? 16 : 48);
+    p.kernel = rows > few ? 1 : 0;
     // units: independent CTAs without parts; least, most: pages of a part
     long long units, parts, least, most;
     if (p.kernel == 0) {

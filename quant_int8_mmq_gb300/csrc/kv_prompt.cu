@@ -18,6 +18,9 @@
 // lag of kv.cuh makes rare, by the softmax thread itself: its S arrived behind the last
 // P V of the tile, so O is at rest.
 //
+// Where a CTA has 128 rows or fewer, both tiles hold them and take every other step, and
+// their sums are joined at the end.
+//
 // 24 warps: warp 0 issues the MMAs, warp 1 copies the pages' bytes into a ring, warps 4-7
 // widen, warps 8-15 and 16-23 are the softmax of tiles 0 and 1: two threads a row, one for
 // each page of the step, which tell each other their largest x (with one thread a row the
@@ -42,6 +45,7 @@ constexpr int LAUNCH_REGS = 80, CTRL_REGS = 24, WIDEN_REGS = 72, SOFT_REGS = 96;
 static_assert(CTRL_REGS + WIDEN_REGS + 4 * SOFT_REGS == 6 * LAUNCH_REGS, "register split");
 // .dec may only lower a warp's count and .inc only raise it (the other way is no instruction)
 static_assert(CTRL_REGS < LAUNCH_REGS && WIDEN_REGS < LAUNCH_REGS && SOFT_REGS > LAUNCH_REGS, "register split");
+constexpr int JOIN_BAR = 9;   // named barrier of all softmax warps (1-8: pairs)
 constexpr int META = 8;   // steps whose page descriptions are kept: more than any role runs ahead
 
 // HL: hi and lo parts of Q and P.
@@ -57,13 +61,18 @@ struct Cfg {
     static constexpr int HALF = 36 * D;                          // bytes of a piece's K or V
     static constexpr int STAGE = 2 * HALF;                       // K or V of two pages
     static constexpr int STAGES = D == 128 ? 3 : 4;
+    static constexpr int COLS = D == 64 && !HL ? 16 : 32;        // values of a row that a warp stages at a time
+    static constexpr int STAGED = COLS * 4 + 16;                 // bytes of a staged row
+    static_assert(16 * 32 * STAGED <= Q_BYTES + BUFS * K_BYTES, "staged rows of both tiles");
+    static_assert(8 * 32 * STAGED + TILE * D * 4 <= Q_BYTES + BUFS * K_BYTES, "staged rows beside tile 1's sums");
     static constexpr int Q = 0;
     static constexpr int K = Q + Q_BYTES;
     static constexpr int V = K + BUFS * K_BYTES;
     static constexpr int RING = V + BUFS * V_BYTES;
     static constexpr int META_AT = RING + STAGES * STAGE;        // int2 [META]: tokens held of each page, -1 no page
     static constexpr int RED = META_AT + META * 8;               // f32 [2][page][row]: what a row's threads tell
-    static constexpr int BAR = RED + 2 * 2 * ROWS * 4;           // each other
+    static constexpr int JOIN = RED + 2 * 2 * ROWS * 4;          // each other; float2 [row]: tile 1's {reference, sum}
+    static constexpr int BAR = JOIN + TILE * 8;
     enum { QFULL, RFULL, REMPTY = RFULL + STAGES, KFULL = REMPTY + STAGES, KEMPTY = KFULL + BUFS,
            VFULL = KEMPTY + BUFS, VEMPTY = VFULL + BUFS, SFULL = VEMPTY + BUFS, PFULL = SFULL + 2,
            OFULL = PFULL + 2, DRAIN = OFULL + 2, NBAR };
@@ -203,7 +212,8 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prompt_kernel(const AttendArgs 
         u.i0 = static_cast<int>(min(part0, static_cast<long long>(u.npage)));
         u.steps = ((u.split == g.nsplit - 1 ? u.npage - u.i0 : min(g.part_pages, u.npage - u.i0)) + 1) / 2;
     }
-    const bool two = u.nrow > TILE;
+    const bool two = u.nrow > TILE;        // else both tiles hold the same rows
+    const int stride = two ? 1 : 2;        // and take every other step
 
     // ---------------------------------------------------------------- setup
     if (threadIdx.x == 0) {
@@ -271,40 +281,49 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prompt_kernel(const AttendArgs 
                                            b + 4u * (c % 2) + 2u * kk, pv, (part | c | kk || add) ? 1u : 0u);
                     }
             };
-            const int tiles = two ? 2 : 1;
-            bool ok = u.steps == 0 || (warp_wait(g, bar(C::QFULL), 0) && warp_wait(g, bar(C::KFULL), 0));
-            if (ok && u.steps > 0) {
+            // a tile's steps are stride apart; K and V are free once the last tile that reads them has
+            bool ok = u.steps == 0 || warp_wait(g, bar(C::QFULL), 0);
+            auto ready_k = [&](int j) {
+                ok = ok && warp_wait(g, bar(C::KFULL + j % C::BUFS), j / C::BUFS & 1);
                 tc_fence_after();
-                for (int w = 0; w < tiles; ++w)
-                    product_qk(w, 0);
-                umma_commit_by(lead, bar(C::KEMPTY));
+            };
+            for (int w = 0; w < 2; ++w) {
+                const int j = two ? 0 : w;
+                if (ok && j < u.steps) {
+                    if (w == 0 || !two)
+                        ready_k(j);
+                    if (ok)
+                        product_qk(w, j % C::BUFS);
+                    if (w == 1 || !two)
+                        umma_commit_by(lead, bar(C::KEMPTY + j % C::BUFS));
+                }
             }
             for (int j = 0; ok && j < u.steps; ++j) {
-                const int buf = j % C::BUFS, next = (j + 1) % C::BUFS;
-                // with two buffers the next K is there before P is; with one it is widened after
-                // this step's last Q K^T
-                ok = warp_wait(g, bar(C::VFULL + buf), j / C::BUFS & 1) &&
-                     (C::BUFS == 1 || j + 1 == u.steps || warp_wait(g, bar(C::KFULL + next), (j + 1) / C::BUFS & 1));
-                for (int w = 0; ok && w < tiles; ++w) {
-                    ok = warp_wait(g, bar(C::PFULL + w), j & 1);
+                const int buf = j % C::BUFS, jn = j + stride, next = jn % C::BUFS;
+                // with two buffers and both tiles at a step the next K is there before P is; else it
+                // may be widened only after this step's products
+                const bool early = C::BUFS == 2 && two;
+                ok = warp_wait(g, bar(C::VFULL + buf), j / C::BUFS & 1);
+                if (early && jn < u.steps)
+                    ready_k(jn);
+                for (int w = two ? 0 : j % 2; ok && w < (two ? 2 : j % 2 + 1); ++w) {
+                    ok = warp_wait(g, bar(C::PFULL + w), j / stride & 1);
                     if (!ok)
                         break;
                     tc_fence_after();
-                    product_pv(w, buf, j > 0);
-                    if (w == tiles - 1)
+                    product_pv(w, buf, j >= stride);
+                    if (w == 1 || !two)
                         umma_commit_by(lead, bar(C::VEMPTY + buf));
-                    if (j + 1 == u.steps) {
+                    if (jn >= u.steps) {
                         umma_commit_by(lead, bar(C::OFULL + w));
                         continue;
                     }
-                    if (C::BUFS == 1 && w == 0) {
-                        ok = warp_wait(g, bar(C::KFULL + next), (j + 1) / C::BUFS & 1);
-                        if (!ok)
-                            break;
-                        tc_fence_after();
-                    }
+                    if (!early && (w == 0 || !two))
+                        ready_k(jn);
+                    if (!ok)
+                        break;
                     product_qk(w, next);
-                    if (w == tiles - 1)
+                    if (w == 1 || !two)
                         umma_commit_by(lead, bar(C::KEMPTY + next));
                 }
             }
@@ -460,8 +479,9 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prompt_kernel(const AttendArgs 
         const int l = warp % 4 * 32 + lane;                                      // TMEM lane
         const int pair = 1 + 4 * w + warp % 4;   // named barrier of the two warps that share 32 rows
         float* red = reinterpret_cast<float*>(smem + C::RED) + TILE * w + l;     // [2][page]: ROWS apart
-        const bool mine = TILE * w + l < u.nrow;
-        const int row = u.row0 + min(TILE * w + l, u.nrow - 1);
+        const int tile0 = two ? TILE * w : 0;    // the tile's first row
+        const bool mine = tile0 + l < u.nrow;
+        const int row = u.row0 + min(tile0 + l, u.nrow - 1);
         const long long token = u.first + row / g.group;
         const int head = u.head * g.group + row % g.group;
         const long long q_at = token * g.q.tok + head * g.q.head;
@@ -529,13 +549,14 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prompt_kernel(const AttendArgs 
         const uint32_t o_at = tmem + lanes + O_COL + D * w + D / 2 * h;   // each thread has half of the row's O
         const int pos = mine ? u.pos0 + row / g.group : -1;
         // positions of the tile's rows, for steps that no mask touches
-        const int plo = u.pos0 + (u.row0 + TILE * w) / g.group;
-        const int phi = u.pos0 + (u.row0 + min(u.nrow, TILE * (w + 1)) - 1) / g.group;
+        const int plo = u.pos0 + (u.row0 + tile0) / g.group;
+        const int phi = u.pos0 + (u.row0 + min(u.nrow, tile0 + TILE) - 1) / g.group;
         float ref = -INFINITY, sum = 0.0f;
         bool ok = true;
-        if (w == 0 || two) {
-            for (int j = 0; j < u.steps; ++j) {
-                ok = warp_wait(g, bar(C::SFULL + w), j & 1);
+        int k = 0;   // steps of this tile so far
+        {
+            for (int j = two ? 0 : w; j < u.steps; j += stride, ++k) {
+                ok = warp_wait(g, bar(C::SFULL + w), k & 1);
                 tc_fence_after();
                 const int2 held = reinterpret_cast<const int2*>(smem + C::META_AT)[j % META];
                 const int kbase = page_of(u, u.i0 + 2 * j + h) * KV_PAGE;
@@ -563,17 +584,17 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prompt_kernel(const AttendArgs 
                                                            __uint_as_float(x[c / 2][c % 2 * 16 + i + 1])));
                     }
                     float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
-                    red[(2 * (j & 1) + h) * ROWS] = top;
+                    red[(2 * (k & 1) + h) * ROWS] = top;
                     if (!named_bar_and(pair, 64, ok))
                         return false;
-                    top = fmaxf(top, red[(2 * (j & 1) + 1 - h) * ROWS]) * coef;
+                    top = fmaxf(top, red[(2 * (k & 1) + 1 - h) * ROWS]) * coef;
                     const bool raise = top > ref + KV_REF_LIMIT;   // also the first visible key
                     if (__any_sync(0xffffffffu, raise)) {
                         const float next = raise ? top - KV_REF_BELOW : ref;
                         const float f = raise ? kv_ex2(ref - next) : 1.0f;
                         ref = next;
                         sum *= f;
-                        if (j > 0) {
+                        if (k > 0) {
 #pragma unroll 1
                             for (int d = 0; d < D / 2; d += 16) {
                                 float o[16];
@@ -620,14 +641,41 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prompt_kernel(const AttendArgs 
                 if (lane == 0)
                     mbar_arrive(bar(C::PFULL + w));
             }
-            if (ok && u.steps > 0) {
+            if (ok && k > 0) {
                 warp_wait(g, bar(C::OFULL + w), 0);
                 tc_fence_after();
             }
         }
-        red[2 * ROWS * (u.steps & 1) + h * ROWS] = sum;
+        red[2 * ROWS * (k & 1) + h * ROWS] = sum;
         named_bar_sync(pair, 64);
-        sum += red[2 * ROWS * (u.steps & 1) + (1 - h) * ROWS];
+        sum += red[2 * ROWS * (k & 1) + (1 - h) * ROWS];
+
+        // with the same rows in both tiles, tile 0 takes over what tile 1 has: O by way of the shared
+        // memory of Q and K, which no product reads any more
+        float4* joined = reinterpret_cast<float4*>(smem + C::Q + 8 * 32 * C::STAGED) + h * TILE + l;   // [value / 4][page][row]
+        float f_own = 1.0f, f_other = 0.0f;
+        if (!two && u.steps > 1) {
+            float2* other = reinterpret_cast<float2*>(smem + C::JOIN) + l;
+            if (w == 1) {
+#pragma unroll 1
+                for (int d = 0; d < D / 2; d += 16) {
+                    float o[16];
+                    tmem_ld16_wait(o_at + d, o);
+#pragma unroll
+                    for (int i = 0; i < 16; i += 4)
+                        joined[(d + i) / 4 * 2 * TILE] = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+                }
+                if (h == 0)
+                    *other = make_float2(ref, sum);
+            }
+            named_bar_sync(JOIN_BAR, SOFT_WARPS * 32);
+            const float2 v = *other;
+            const float top = fmaxf(ref, v.x);
+            f_own = ref == -INFINITY ? 0.0f : kv_ex2(ref - top);
+            f_other = v.x == -INFINITY ? 0.0f : kv_ex2(v.x - top);
+            sum = f_own * sum + f_other * v.y;
+            ref = top;
+        }
         if (w == 0 || two) {
             // half of a row's share of the result, by way of shared memory (the tile's Q is done
             // with): the warp writes four rows' 32 values at a time, whole lines for the strided 16
@@ -638,9 +686,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prompt_kernel(const AttendArgs 
             const long long out_at = g.nsplit > 1 ? part_at * D : token * g.out.tok + head * g.out.head;
             if (g.nsplit > 1 && mine && h == 0)
                 g.part_ml[part_at] = make_float2(ref, sum);
-            constexpr int COLS = D == 64 && !HL ? 16 : 32;   // values staged at a time
-            constexpr int ROW = COLS * 4 + 16, LPR = COLS / 4;
-            static_assert(SOFT_WARPS * 32 * ROW <= C::Q_BYTES + C::K_BYTES, "staged rows");
+            constexpr int COLS = C::COLS, ROW = C::STAGED, LPR = COLS / 4;
             uint8_t* stage = smem + C::Q + (warp - SOFT_WARP) * 32 * ROW;
             const int sub = lane / LPR, c = lane % LPR * 4;
 #pragma unroll 1
@@ -652,10 +698,19 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prompt_kernel(const AttendArgs 
                         tmem_ld16_wait(o_at + d + i, *reinterpret_cast<float(*)[16]>(o + i));
                 }
 #pragma unroll
-                for (int i = 0; i < COLS; i += 4)
-                    *reinterpret_cast<float4*>(stage + lane * ROW + i * 4) =
-                        u.steps > 0 ? make_float4(o[i] * inv, o[i + 1] * inv, o[i + 2] * inv, o[i + 3] * inv)
-                                    : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                for (int i = 0; i < COLS; i += 4) {
+                    float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                    if (u.steps > 0) {
+                        v = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+                        if (!two && u.steps > 1) {
+                            const float4 y = joined[(d + i) / 4 * 2 * TILE];
+                            v = make_float4(f_own * v.x + f_other * y.x, f_own * v.y + f_other * y.y,
+                                            f_own * v.z + f_other * y.z, f_own * v.w + f_other * y.w);
+                        }
+                        v = make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv);
+                    }
+                    *reinterpret_cast<float4*>(stage + lane * ROW + i * 4) = v;
+                }
                 __syncwarp();
 #pragma unroll
                 for (int i = 0; i < LPR; ++i) {
