@@ -23,6 +23,7 @@ namespace mmq {
 constexpr int KV_PAGE = MMQ_KV_PAGE;   // tokens per page
 constexpr int KV_GROUP = 32;           // values per scale
 constexpr int KV_PROMPT_ROWS = 256;    // rows of a kv_prompt.cu CTA
+constexpr int KV_MAX_CLUSTER = 8;      // CTAs of a kv_step.cu cluster
 
 // Byte offsets inside a piece of head size D; the documented layout is in mmq.h.
 template <int D>
@@ -269,6 +270,7 @@ struct AttendArgs {
     int row_tiles;         // kv_step.cu: row tiles per (sequence, kv head); kv_prompt.cu: of the whole batch
     int nsplit;            // parts of the visible pages,
     int part_pages;        // each of so many
+    int cluster;           // kv_step.cu: CTAs that share a part
     bool wide;
     float* part;           // nsplit > 1: [nsplit][ntok * heads][D] unnormalised sums
     float2* part_ml;       //             [nsplit][ntok * heads] {reference, sum}
@@ -278,7 +280,7 @@ struct AttendArgs {
 struct AttendPlan {
     int kernel;      // 0: kv_step.cu, 1: kv_prompt.cu
     int tile_rows, row_tiles;
-    int nsplit, part_pages;
+    int nsplit, part_pages, cluster;
     size_t part_bytes, ml_bytes;
 };
 AttendPlan plan_attend(int dtype, int heads, int kv_heads, int dim, int batch, int ntok, int max_q, int max_kv,

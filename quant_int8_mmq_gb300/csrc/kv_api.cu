@@ -29,13 +29,15 @@ AttendPlan plan_attend(int dtype, int heads, int kv_heads, int dim, int batch, i
     // 24 rows 42 / 48, 32 rows 58 / 49; 16-bit ones 32 rows 34 / 45, 48 rows 45 / 45.
     const int few = dtype == KV_F32 ? (dim == 128 ? 32 : 24) : (dim == 128 ? 16 : 48);
     p.kernel = rows > few ? 1 : 0;
-    // units: independent CTAs without parts; least, most: pages of a part
-    long long units, parts, least, most;
+    // units: independent CTAs without parts; slots: CTAs that the chip holds at once; least, most:
+    // pages of a part
+    long long units, slots = SMS, parts, least, most;
     if (p.kernel == 0) {
         p.tile_rows = dtype == KV_F32 || rows <= 8 ? 8 : 16;
         p.row_tiles = static_cast<int>((rows + p.tile_rows - 1) / p.tile_rows);
         units = static_cast<long long>(batch) * kv_heads * p.row_tiles;
-        parts = (p.tile_rows == 16 ? 3 : 4) * SMS / units;   // CTAs that the chip holds at once
+        slots = (p.tile_rows == 16 ? 3 : 4) * SMS;
+        parts = slots / units;
         parts = parts < 1 ? 1 : parts;
         least = 4;      // a page a warp
         most = 64;      // sequences of uneven length: parts even the load out
@@ -48,7 +50,7 @@ AttendPlan plan_attend(int dtype, int heads, int kv_heads, int dim, int batch, i
         // Where the tiles do not fill the chip, parts do, and cost the trip of their sums through
         // memory: the least of the expected times in us (GB300: a CTA's start and end 8; 128 keys
         // of 256 rows 3.0 for f32 rows of 128 values, 1.8 for 16-bit ones, half of it for 64
-        // values; the join 3 and its bytes at 6 TB/s).  More tiles than SMs are left whole: two
+        // values; the join 8, most of it the host's, and its bytes at 6 TB/s).  More tiles than SMs are left whole: two
         // parts against the uneven last round took 821 us for 747 (2048 and 1944 tokens on 16384
         // and 13563, 32 heads on 8).
         const double step = (dtype == KV_F32 ? 3.0 : 1.8) * dim / 128;
@@ -57,7 +59,7 @@ AttendPlan plan_attend(int dtype, int heads, int kv_heads, int dim, int batch, i
         double least_us = 0;
         for (long long n = 1; n == 1 || (units < SMS && n <= 64 && pages >= 8 * n); ++n) {
             const double us = static_cast<double>((units * n + SMS - 1) / SMS) * (8 + step * pages / 2 / n) +
-                              (n == 1 ? 0 : 3 + n * bytes / 6e6);
+                              (n == 1 ? 0 : 8 + n * bytes / 6e6);
             if (n == 1 || us < least_us) {
                 best = n;
                 least_us = us;
@@ -70,8 +72,23 @@ AttendPlan plan_attend(int dtype, int heads, int kv_heads, int dim, int batch, i
     long long part = (pages + parts - 1) / parts;
     part = part < least ? least : part > most ? most : part;
     part = (part + 3) / 4 * 4;
-    p.part_pages = static_cast<int>(part);
-    p.nsplit = static_cast<int>((pages + part - 1) / part);
+    long long cut = (pages + part - 1) / part;
+    p.cluster = 1;
+    if (p.kernel == 0) {
+        // Parts of half the chip or less become one cluster: no second kernel and no workspace (17
+        // us for 22 for a call on 4 sequences of 1000 keys, most of it the host's), for up to 16
+        // pieces at twice the pages.  A fuller chip has no room for clusters to fall into place
+        // (64 clusters of 7 took 49 us where 448 CTAs took 30), and takes the join.
+        const long long eighth = (pages + KV_MAX_CLUSTER - 1) / KV_MAX_CLUSTER;
+        if (cut > KV_MAX_CLUSTER && cut <= 2 * KV_MAX_CLUSTER && units * KV_MAX_CLUSTER <= slots / 2) {
+            part = (eighth + 3) / 4 * 4;
+            cut = (pages + part - 1) / part;
+        }
+        if (cut <= KV_MAX_CLUSTER && units * cut <= slots / 2)
+            p.cluster = static_cast<int>(cut);
+    }
+    p.part_pages = static_cast<int>(part * p.cluster);
+    p.nsplit = static_cast<int>((pages + p.part_pages - 1) / p.part_pages);
     if (p.nsplit > 1) {
         const size_t flat = static_cast<size_t>(p.nsplit) * ntok * heads;
         p.part_bytes = flat * dim * sizeof(float);
@@ -256,7 +273,8 @@ mmq_status mmq_kv_attend(const mmq_kv_cache* c, const mmq_rows* q, const mmq_row
         if (!aligned(workspace, 16))
             return MMQ_ERR_ALIGN;
     }
-    if (static_cast<long long>(p.nsplit) * p.row_tiles * c->kv_heads * (p.kernel == 0 ? c->batch : 1) > 0x7fffffffll ||
+    if (static_cast<long long>(p.nsplit) * p.cluster * p.row_tiles * c->kv_heads * (p.kernel == 0 ? c->batch : 1) >
+            0x7fffffffll ||
         static_cast<long long>(ntok) * heads > 0x7fffffffll)
         return MMQ_ERR_SHAPE;
     if ((st = mmq::check_device()) != MMQ_OK)
@@ -278,6 +296,7 @@ mmq_status mmq_kv_attend(const mmq_kv_cache* c, const mmq_rows* q, const mmq_row
     a.row_tiles = p.row_tiles;
     a.nsplit = p.nsplit;
     a.part_pages = p.part_pages;
+    a.cluster = p.cluster;
     const int four = q->dtype == MMQ_F32 ? 16 : 8;   // bytes of four elements
     a.wide = wide(q, four) && wide(out, four);
     a.part = static_cast<float*>(workspace);

@@ -24,8 +24,9 @@
 // A CTA is 4 warps; each takes every fourth of the CTA's pages through its own ring of
 // bulk copies, with its own running reference and sums, and the four are joined in shared
 // memory.  When there are few tiles, or sequences of uneven length, the visible pages are
-// cut into parts of bounded length, whose sums go to the workspace and are joined by a
-// second kernel.
+// cut into parts.  A part goes to a cluster of up to 8 CTAs, which share its pages evenly
+// whatever their number turns out to be and join their sums through distributed shared
+// memory; only what takes more parts than one goes by the workspace and a second kernel.
 #include <atomic>
 
 #include "kv.cuh"
@@ -82,8 +83,9 @@ __global__ void __launch_bounds__(WARPS * 32, MODE == WIDE ? 3 : D == 128 ? 4 : 
     const int n = lane / 4, t = lane % 4;
 
     grid_dep_wait();
-    // the unit: a split of the pages for one row tile of one sequence's kv head
-    int id = blockIdx.x;
+    // the unit: a part of the pages for one row tile of one sequence's kv head
+    int id = blockIdx.x / g.cluster;
+    const int rank = blockIdx.x % g.cluster;
     const int split = id % g.nsplit;
     id /= g.nsplit;
     const int head = id % g.c.kv_heads;
@@ -112,18 +114,20 @@ __global__ void __launch_bounds__(WARPS * 32, MODE == WIDE ? 3 : D == 128 ? 4 : 
     const int npage = nsink + (kend + KV_PAGE - 1) / KV_PAGE - page_lo;
     // the last part takes what the caller's max_kv did not foresee
     const long long part0 = static_cast<long long>(split) * g.part_pages;
-    const int i_end = split == g.nsplit - 1 ? npage : static_cast<int>(min(part0 + g.part_pages, static_cast<long long>(npage)));
+    const int part1 = split == g.nsplit - 1 ? npage : static_cast<int>(min(part0 + g.part_pages, static_cast<long long>(npage)));
     const int flat_rows = g.ntok * g.heads;
     if (g.nsplit > 1 && part0 >= npage) {   // nothing here: say so and leave
-        if (threadIdx.x < nrow) {
+        if (rank == 0 && threadIdx.x < nrow) {
             const int row = row0 + threadIdx.x;
             g.part_ml[static_cast<size_t>(split) * flat_rows + static_cast<size_t>(first + row / g.group) * g.heads +
                       head * g.group + row % g.group] = make_float2(-INFINITY, 0.0f);
         }
         return;
     }
-
-    const int i0 = static_cast<int>(part0) + warp;
+    // this CTA's share: a page a warp at least
+    const int share = max((part1 - static_cast<int>(part0) + g.cluster - 1) / g.cluster, WARPS);
+    const int i0 = static_cast<int>(part0) + rank * share + warp;
+    const int i_end = min(static_cast<int>(part0) + (rank + 1) * share, part1);
     const uint32_t sbase = smem_u32(smem);
     const uint32_t ring = sbase + S::RING + warp * STAGES * S::HALF;
     const uint32_t bar = sbase + S::BAR + warp * STAGES * 8;
@@ -441,9 +445,8 @@ __global__ void __launch_bounds__(WARPS * 32, MODE == WIDE ? 3 : D == 128 ? 4 : 
     __syncthreads();
 
     constexpr int LANES = WARPS * 32 / ROWS;   // threads a row
+    constexpr int GROUPS = D / (4 * LANES);    // of four values a thread
     const int r = threadIdx.x / LANES, l = threadIdx.x % LANES;
-    if (r >= nrow)
-        return;
     float top = -INFINITY, total = 0.0f, f[WARPS];
 #pragma unroll
     for (int w = 0; w < WARPS; ++w)
@@ -454,32 +457,69 @@ __global__ void __launch_bounds__(WARPS * 32, MODE == WIDE ? 3 : D == 128 ? 4 : 
         f[w] = v.x == -INFINITY ? 0.0f : kv_ex2(v.x - top);
         total += f[w] * v.y;
     }
+    float4 v[GROUPS];
+    auto add = [](float4& a, float k, float4 b) {
+        a.x += k * b.x;
+        a.y += k * b.y;
+        a.z += k * b.z;
+        a.w += k * b.w;
+    };
+#pragma unroll
+    for (int j = 0; j < GROUPS; ++j) {
+        v[j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+        for (int w = 0; w < WARPS; ++w)
+            add(v[j], f[w], *reinterpret_cast<const float4*>(os + (w * ROWS + r) * S::OROW + 4 * (LANES * j + l)));
+    }
+    if (g.cluster > 1) {
+        __syncthreads();   // everyone has read the warps' sums, the CTA's go over them
+        if (l == 0)
+            ml[r] = make_float2(top, total);
+#pragma unroll
+        for (int j = 0; j < GROUPS; ++j)
+            *reinterpret_cast<float4*>(os + r * S::OROW + 4 * (LANES * j + l)) = v[j];
+        cluster_sync();
+        if (rank == 0) {
+            const uint32_t ml_at = smem_u32(ml + r), os_at = smem_u32(os + r * S::OROW + 4 * l);
+            float all = top;
+            for (int c = 1; c < g.cluster; ++c)
+                all = fmaxf(all, ld_cluster_f32(cluster_map(ml_at, c)));
+            const float own = top == -INFINITY ? 0.0f : kv_ex2(top - all);
+            total *= own;
+#pragma unroll
+            for (int j = 0; j < GROUPS; ++j)
+                v[j] = make_float4(own * v[j].x, own * v[j].y, own * v[j].z, own * v[j].w);
+            for (int c = 1; c < g.cluster; ++c) {
+                const float ref_c = ld_cluster_f32(cluster_map(ml_at, c));
+                const float k = ref_c == -INFINITY ? 0.0f : kv_ex2(ref_c - all);
+                total += k * ld_cluster_f32(cluster_map(ml_at + 4, c));
+#pragma unroll
+                for (int j = 0; j < GROUPS; ++j)
+                    add(v[j], k, ld_cluster_f32x4(cluster_map(os_at + 16 * LANES * j, c)));
+            }
+            top = all;
+        }
+        cluster_sync();    // the first CTA has read the others' sums
+        if (rank != 0)
+            return;
+    }
+    if (r >= nrow)
+        return;
     const int row = row0 + r;
     const long long token = first + row / g.group;
     const int h = head * g.group + row % g.group;
+    const size_t at = static_cast<size_t>(split) * flat_rows + static_cast<size_t>(token) * g.heads + h;
+    if (g.nsplit > 1 && l == 0)
+        g.part_ml[at] = make_float2(top, total);
+    const float inv = total == 0.0f ? 0.0f : 1.0f / total;   // a row that sees no key is zero
 #pragma unroll
-    for (int j = 0; j < D / (4 * LANES); ++j) {
+    for (int j = 0; j < GROUPS; ++j) {
         const int d = 4 * (LANES * j + l);
-        float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll
-        for (int w = 0; w < WARPS; ++w) {
-            const float4 p = *reinterpret_cast<const float4*>(os + (w * ROWS + r) * S::OROW + d);
-            v.x += f[w] * p.x;
-            v.y += f[w] * p.y;
-            v.z += f[w] * p.z;
-            v.w += f[w] * p.w;
-        }
-        const size_t flat = static_cast<size_t>(token) * g.heads + h;
-        if (g.nsplit == 1) {
-            const float inv = total == 0.0f ? 0.0f : 1.0f / total;   // a row that sees no key is zero
-            v = make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv);
-            store4(static_cast<T*>(g.out.data) + token * g.out.tok + h * g.out.head + d, v, g.wide);
-        } else {
-            const size_t at = static_cast<size_t>(split) * flat_rows + flat;
-            *reinterpret_cast<float4*>(g.part + at * D + d) = v;
-            if (l == 0 && j == 0)
-                g.part_ml[at] = make_float2(top, total);
-        }
+        if (g.nsplit > 1)
+            *reinterpret_cast<float4*>(g.part + at * D + d) = v[j];
+        else
+            store4(static_cast<T*>(g.out.data) + token * g.out.tok + h * g.out.head + d,
+                   make_float4(v[j].x * inv, v[j].y * inv, v[j].z * inv, v[j].w * inv), g.wide);
     }
 }
 
@@ -557,10 +597,23 @@ cudaError_t launch_step(const AttendArgs& a, cudaStream_t s)
     const cudaError_t e = kv_allow_smem(kv_step_kernel<D, T, MODE>, BYTES, &done);
     if (e != cudaSuccess)
         return e;
-    const unsigned int grid = static_cast<unsigned int>(static_cast<long long>(a.nsplit) * a.c.kv_heads * a.row_tiles *
-                                                        a.c.batch);
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = static_cast<unsigned int>(a.cluster);
+    at[1].val.clusterDim.y = 1;
+    at[1].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned int>(static_cast<long long>(a.cluster) * a.nsplit * a.c.kv_heads *
+                                                 a.row_tiles * a.c.batch));
+    cfg.blockDim = dim3(WARPS * 32);
+    cfg.dynamicSmemBytes = BYTES;
+    cfg.stream = s;
+    cfg.attrs = at;
+    cfg.numAttrs = a.cluster > 1 ? 2 : 1;
     count_launch();
-    return launch_dependent_smem(kv_step_kernel<D, T, MODE>, dim3(grid), dim3(WARPS * 32), BYTES, s, a);
+    return cudaLaunchKernelEx(&cfg, kv_step_kernel<D, T, MODE>, a);
 }
 
 template <int D>
