@@ -243,6 +243,29 @@ def test_attention(new, length, heads, kv_heads, dim, dtype):
     b.check(q, mmq.kv_attend(q, *b.cache, max_q=max(new)))
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("length", [63, 64, 65, 127, 128, 129, 193, 256, 257, 385, 700])
+def test_every_number_of_pages(length, dim, dtype):
+    """Rows of one tile (both tiles take every other step), of two, and of two and a rest, with
+    odd and even numbers of pages and steps."""
+    for rows in (min(length, 40), min(length, 100), min(length, 190)):
+        b = Batch([rows], [length], 1, dim, dtype, seed=length)
+        q = b.q(2)
+        b.check(q, mmq.kv_attend(q, *b.cache, max_q=rows))
+
+
+@pytest.mark.parametrize("dtype", [F32, F16])
+@pytest.mark.parametrize("new,heads,kv_heads", [(1, 4, 1), (2, 12, 1), (1, 32, 4), (40, 2, 1), (300, 1, 1)])
+@pytest.mark.parametrize("length", [257, 700, 1500, 3000, 6000, 20000])
+def test_parts_of_any_number(length, new, heads, kv_heads, dtype):
+    """Few rows on caches that are cut into one part, one cluster, or many parts and a join."""
+    new = min(new, length)
+    b = Batch([new], [length], kv_heads, 128, dtype, seed=length)
+    q = b.q(heads)
+    b.check(q, mmq.kv_attend(q, *b.cache, max_q=new, max_kv=length))
+
+
 @pytest.mark.parametrize("dtype", [F32, F16])
 @pytest.mark.parametrize("window,sinks", [(1, 0), (1, 1), (64, 4), (65, 0), (100, 64), (100, 65), (700, 4),
                                           (333, 200), (1 << 30, 3), (50, 1 << 30)])
