@@ -137,7 +137,7 @@ __device__ __forceinline__ float4 load4(const T* p, bool wide)
 // The same in two halves: the load, and the values once they are used.
 template <typename T>
 struct Raw4 {
-    T e[4];
+    alignas(4 * sizeof(T)) T e[4];
     __device__ __forceinline__ void load(const T* p, bool wide)
     {
         if (wide) {

@@ -36,7 +36,7 @@ AttendPlan plan_attend(int dtype, int heads, int kv_heads, int dim, int batch, i
         p.tile_rows = dtype == KV_F32 || rows <= 8 ? 8 : 16;
         p.row_tiles = static_cast<int>((rows + p.tile_rows - 1) / p.tile_rows);
         units = static_cast<long long>(batch) * kv_heads * p.row_tiles;
-        slots = (p.tile_rows == 16 ? 3 : 4) * SMS;
+        slots = (p.tile_rows == 16 ? 3 : dim == 128 ? 4 : 6) * SMS;
         parts = slots / units;
         parts = parts < 1 ? 1 : parts;
         least = 4;      // a page a warp

@@ -7,9 +7,10 @@
 // head) as two tiles of 128 TMEM lanes, and walks the visible pages 128 keys at a time.
 // The cached values are widened to f16, exactly, by one warpgroup for both tiles: K as
 // [key][value] and V transposed as [value][key], the K-major operand tiles of the two
-// products.  Q is scaled per row by a power of two and split q = hi + lo in f16, P
-// likewise: f32 rows use both parts (four products a tile, 22-bit operands), 16-bit rows
-// are exact in hi (bf16 to 2^-24 of the row's largest) and round P to f16.
+// products.  Q is scaled per row by a power of two (f16 rows are operands as they are) and
+// split q = hi + lo in f16, P likewise: f32 rows use both parts (four products a tile,
+// 22-bit operands), 16-bit rows are exact in hi (bf16 to 2^-24 of the row's largest) and
+// round P to f16.
 //
 // TMEM: S of each tile in 128 columns, its P over the S that it came from (per 32 keys 16
 // columns of hi and 16 of lo), O in D columns.  The tiles alternate on the tensor pipe, P V and the next Q K^T of one
@@ -507,28 +508,36 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prompt_kernel(const AttendArgs 
 #pragma unroll
                 for (int k = 0; k < BATCH; ++k) {
                     const int r32 = warp % 4 * 32 + i0 + 4 * k + sub;
-                    float a = 0.0f;
+                    int e = 0;
+                    float f = 1.0f;
+                    if constexpr (!std::is_same<T, __half>::value) {   // f16 is an operand as it is
+                        float a = 0.0f;
 #pragma unroll
-                    for (int i = 0; i < LOADS; ++i) {
-                        const float4 v = x[k][i].get();
-                        a = fmaxf(a, fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w))));
+                        for (int i = 0; i < LOADS; ++i) {
+                            const float4 v = x[k][i].get();
+                            a = fmaxf(a, fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w))));
+                        }
+#pragma unroll
+                        for (int s = 1; s < 8; s <<= 1)
+                            a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, s));
+                        e = kv_exponent(a);
+                        f = kv_pow2(-e);
                     }
-#pragma unroll
-                    for (int s = 1; s < 8; s <<= 1)
-                        a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, s));
-                    const int e = kv_exponent(a);
-                    const float f = kv_pow2(-e);
 #pragma unroll
                     for (int i = 0; i < LOADS; ++i) {
                         const int d = 32 * i + c;
-                        const float4 v = x[k][i].get();
-                        uint2 hi, lo;
-                        kv_split2(v.x * f, v.y * f, hi.x, lo.x);
-                        kv_split2(v.z * f, v.w * f, hi.y, lo.y);
                         uint8_t* at = dst + d / 64 * C::BLOCK + r32 * 128 + ((d / 8 % 8 ^ (r32 & 7)) << 4) + d % 8 * 2;
-                        *reinterpret_cast<uint2*>(at) = hi;
-                        if (HL)
-                            *reinterpret_cast<uint2*>(at + C::KB * C::BLOCK) = lo;
+                        if constexpr (std::is_same<T, __half>::value) {
+                            *reinterpret_cast<uint2*>(at) = *reinterpret_cast<const uint2*>(x[k][i].e);
+                        } else {
+                            const float4 v = x[k][i].get();
+                            uint2 hi, lo;
+                            kv_split2(v.x * f, v.y * f, hi.x, lo.x);
+                            kv_split2(v.z * f, v.w * f, hi.y, lo.y);
+                            *reinterpret_cast<uint2*>(at) = hi;
+                            if (HL)
+                                *reinterpret_cast<uint2*>(at + C::KB * C::BLOCK) = lo;
+                        }
                     }
                     if (c == 0)
                         red[r32 - l] = fminf(fmaxf(g.scale_log2 * kv_pow2(e), 1e-38f), 1e38f);
@@ -689,7 +698,15 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prompt_kernel(const AttendArgs 
             constexpr int COLS = C::COLS, ROW = C::STAGED, LPR = COLS / 4;
             uint8_t* stage = smem + C::Q + (warp - SOFT_WARP) * 32 * ROW;
             const int sub = lane / LPR, c = lane % LPR * 4;
-#pragma unroll 1
+            long long to[LPR];   // of the rows whose values c .. c + 3 this lane writes
+            uint32_t there = 0;
+#pragma unroll
+            for (int i = 0; i < LPR; ++i) {
+                const int src = 32 / LPR * i + sub;
+                to[i] = __shfl_sync(0xffffffffu, out_at, src) + c + D / 2 * h;
+                there |= (__shfl_sync(0xffffffffu, mine, src) ? 1u : 0u) << i;
+            }
+#pragma unroll
             for (int d = 0; d < D / 2; d += COLS) {
                 float o[COLS];
                 if (u.steps > 0) {
@@ -697,6 +714,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prompt_kernel(const AttendArgs 
                     for (int i = 0; i < COLS; i += 16)
                         tmem_ld16_wait(o_at + d + i, *reinterpret_cast<float(*)[16]>(o + i));
                 }
+                __syncwarp();
 #pragma unroll
                 for (int i = 0; i < COLS; i += 4) {
                     float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
@@ -714,17 +732,14 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prompt_kernel(const AttendArgs 
                 __syncwarp();
 #pragma unroll
                 for (int i = 0; i < LPR; ++i) {
-                    const int src = 32 / LPR * i + sub;
-                    const long long at = __shfl_sync(0xffffffffu, out_at, src) + c + D / 2 * h + d;
-                    const float4 v = *reinterpret_cast<const float4*>(stage + src * ROW + c * 4);
-                    if (__shfl_sync(0xffffffffu, mine, src)) {
+                    const float4 v = *reinterpret_cast<const float4*>(stage + (32 / LPR * i + sub) * ROW + c * 4);
+                    if (there >> i & 1u) {
                         if (g.nsplit > 1)
-                            *reinterpret_cast<float4*>(g.part + at) = v;
+                            *reinterpret_cast<float4*>(g.part + to[i] + d) = v;
                         else
-                            store4(static_cast<T*>(g.out.data) + at, v, g.wide);
+                            store4(static_cast<T*>(g.out.data) + to[i] + d, v, g.wide);
                     }
                 }
-                __syncwarp();
             }
         }
     }

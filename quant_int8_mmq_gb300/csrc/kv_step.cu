@@ -43,11 +43,10 @@ enum Mode { HI_LO = 0, ONE_PART = 1, WIDE = 2 };
 template <int D, int MODE>
 struct StepSmem {
     static constexpr int ROWS = MODE == WIDE ? 16 : 8;
-    static constexpr int QROW = D * 2 + 16;                         // padded row of f16
     static constexpr int HALF = Piece<D>::V_CODES;                  // bytes of a piece's K or V
     static constexpr int RING = 0;                                  // [WARPS][STAGES] halves
     static constexpr int Q = RING + WARPS * STAGES * HALF;
-    static constexpr int COEF = Q + 16 * QROW;                      // f32 per row
+    static constexpr int COEF = Q + 16 * D * 2;                     // f32 per row
     static constexpr int ML = COEF + ROWS * 4;                      // float2 [WARPS][ROWS]
     static constexpr int BAR = ML + WARPS * ROWS * 8;
     static constexpr int BYTES = BAR + WARPS * STAGES * 8;
@@ -73,7 +72,7 @@ __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1
 }
 
 template <int D, typename T, int MODE>
-__global__ void __launch_bounds__(WARPS * 32, MODE == WIDE ? 3 : D == 128 ? 4 : 5) kv_step_kernel(const AttendArgs g)
+__global__ void __launch_bounds__(WARPS * 32, MODE == WIDE ? 3 : D == 128 ? 4 : 6) kv_step_kernel(const AttendArgs g)
 {
     using P = Piece<D>;
     using S = StepSmem<D, MODE>;
@@ -194,26 +193,24 @@ __global__ void __launch_bounds__(WARPS * 32, MODE == WIDE ? 3 : D == 128 ? 4 : 
             uint2 hi, lo;
             kv_split2(x.x * f, x.y * f, hi.x, lo.x);
             kv_split2(x.z * f, x.w * f, hi.y, lo.y);
-            *reinterpret_cast<uint2*>(smem + S::Q + r * S::QROW + lane * 8) = hi;
-            if (MODE != WIDE)
-                *reinterpret_cast<uint2*>(smem + S::Q + (8 + r) * S::QROW + lane * 8) = lo;
+            // as the operand's lanes read it: values D/4 t .. of row n (and n + 8), four a step
+            const int step = 4 * lane % (D / 4) / 4, owner = r % 8 * 4 + 4 * lane / (D / 4);
+            uint32_t* at = reinterpret_cast<uint32_t*>(smem + S::Q + (step * 32 + owner) * 16);
+            if constexpr (MODE == WIDE) {
+                at[r / 8] = hi.x;
+                at[2 + r / 8] = hi.y;
+            } else {
+                *reinterpret_cast<uint4*>(at) = make_uint4(hi.x, lo.x, hi.y, lo.y);
+            }
         }
         if (lane == 0)
             *reinterpret_cast<float*>(smem + S::COEF + 4 * r) = fminf(fmaxf(g.scale_log2 * kv_pow2(e), 1e-38f), 1e38f);
     }
     __syncthreads();
 
-    // operand rows n and n + 8: lane t holds values D/4 t .. D/4 t + D/4 - 1
-    uint32_t qf[D / 16][4];
-#pragma unroll
-    for (int j = 0; j < D / 16; ++j) {
-        const uint2 up = *reinterpret_cast<const uint2*>(smem + S::Q + n * S::QROW + (D / 4 * t + 4 * j) * 2);
-        const uint2 low = *reinterpret_cast<const uint2*>(smem + S::Q + (8 + n) * S::QROW + (D / 4 * t + 4 * j) * 2);
-        qf[j][0] = up.x;
-        qf[j][1] = low.x;
-        qf[j][2] = up.y;
-        qf[j][3] = low.y;
-    }
+    // the operand Q, read again for every two octets of keys: kept in registers (32 of them) it
+    // left the rest too few to run ahead (524288 keys, 32 heads on 8: 158 us for 154)
+    const uint4* qf = reinterpret_cast<const uint4*>(smem + S::Q) + lane;   // step j at 32 j
     float coef[SETS], ref[SETS], sum[SETS];
     int pos[SETS];   // the row sees keys up to here, -1: no row
 #pragma unroll
@@ -282,17 +279,19 @@ __global__ void __launch_bounds__(WARPS * 32, MODE == WIDE ? 3 : D == 128 ? 4 : 
                 sb[h] = kv_addend(s[h]);
             }
 #pragma unroll
-            for (int j = 0; j < D / 16; ++j)
+            for (int j = 0; j < D / 16; ++j) {
+                const uint4 q = qf[32 * j];
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     const uint32_t v = w[h][j / 2];
                     const uint32_t b0 = kv_h2u(j % 2 ? kv_widen<2>(v, s[h], sb[h]) : kv_widen<0>(v, s[h], sb[h]));
                     const uint32_t b1 = kv_h2u(j % 2 ? kv_widen<3>(v, s[h], sb[h]) : kv_widen<1>(v, s[h], sb[h]));
                     if (j < SUMS)
-                        mma16816_first(c[h][j % SUMS], qf[j][0], qf[j][1], qf[j][2], qf[j][3], b0, b1);
+                        mma16816_first(c[h][j % SUMS], q.x, q.y, q.z, q.w, b0, b1);
                     else
-                        mma16816(c[h][j % SUMS], qf[j][0], qf[j][1], qf[j][2], qf[j][3], b0, b1);
+                        mma16816(c[h][j % SUMS], q.x, q.y, q.z, q.w, b0, b1);
                 }
+            }
 #pragma unroll
             for (int h = 0; h < 2; ++h)
 #pragma unroll
