@@ -80,7 +80,7 @@ __device__ __forceinline__ __half2 kv_u2h(uint32_t v) { return *reinterpret_cast
 // at most 11 significant bits; the former takes an add and a multiply, as 1032 s would
 // be rounded.  Nothing is inexact.  Each mask and exponent is one three-input logic
 // operation (written as such: as an expression it compiled to two, and the step kernel
-// executed 1571 instructions a page for 1315), and only pairs 2 and 3 share a shift, which
+// executed 555 of them a page for 314), and only pairs 2 and 3 share a shift, which
 // keeps half of the work off the integer pipe.
 __device__ __forceinline__ uint32_t kv_field(uint32_t x, uint32_t mask, uint32_t exponent)
 {

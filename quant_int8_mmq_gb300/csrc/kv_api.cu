@@ -50,9 +50,9 @@ AttendPlan plan_attend(int dtype, int heads, int kv_heads, int dim, int batch, i
         // Where the tiles do not fill the chip, parts do, and cost the trip of their sums through
         // memory: the least of the expected times in us (GB300: a CTA's start and end 8; 128 keys
         // of 256 rows 3.0 for f32 rows of 128 values, 1.8 for 16-bit ones, half of it for 64
-        // values; the join 8, most of it the host's, and its bytes at 6 TB/s).  More tiles than SMs are left whole: two
-        // parts against the uneven last round took 821 us for 747 (2048 and 1944 tokens on 16384
-        // and 13563, 32 heads on 8).
+        // values; the join 8, most of it the host's, and its bytes at 6 TB/s).  More tiles than
+        // SMs are left whole: two parts against the uneven last round took 821 us for 747 (2048
+        // and 1944 tokens on 16384 and 13563, 32 heads on 8).
         const double step = (dtype == KV_F32 ? 3.0 : 1.8) * dim / 128;
         const double bytes = 8.0 * ntok * heads * dim;
         long long best = 1;

@@ -13,11 +13,11 @@
 // round P to f16.
 //
 // TMEM: S of each tile in 128 columns, its P over the S that it came from (per 32 keys 16
-// columns of hi and 16 of lo), O in D columns.  The tiles alternate on the tensor pipe, P V and the next Q K^T of one
-// while the other's softmax runs: two threads a row read S, keep the row's reference and
-// sums, and write P.  A row's O is rescaled only when its reference moves, which the
-// lag of kv.cuh makes rare, by the softmax thread itself: its S arrived behind the last
-// P V of the tile, so O is at rest.
+// columns of hi and 16 of lo), O in D columns.  The tiles alternate on the tensor pipe, P V
+// and the next Q K^T of one while the other's softmax runs: two threads a row read S, keep
+// the row's reference and sums, and write P.  A row's O is rescaled only when its reference
+// moves, which the lag of kv.cuh makes rare, by the softmax thread itself: its S arrived
+// behind the last P V of the tile, so O is at rest.
 //
 // Where a CTA has 128 rows or fewer, both tiles hold them and take every other step, and
 // their sums are joined at the end.
@@ -25,9 +25,16 @@
 // 24 warps: warp 0 issues the MMAs, warp 1 copies the pages' bytes into a ring, warps 4-7
 // widen, warps 8-15 and 16-23 are the softmax of tiles 0 and 1: two threads a row, one for
 // each page of the step, which tell each other their largest x (with one thread a row the
-// softmax took 2000 of a step's 3500 cycles, the products waiting for it).  Every wait is bounded; on
-// expiry the roles leave their loops, copies and MMAs in flight are waited for, TMEM is
-// freed and the CTA ends.
+// softmax took 2000 of a step's 3500 cycles, the products waiting for it).  Every wait is
+// bounded; on expiry the roles leave their loops, copies and MMAs in flight are waited for,
+// TMEM is freed and the CTA ends.
+//
+// What bounds it: a tile's chain of softmax, P V and Q K^T, which the other tile covers only
+// in part; the tensor pipe is active in 60 % of the cycles.  On GB300: chunks of 2048 and 1944
+// bf16 tokens on 16384 and 13563, 32 heads of 128 on 8, 748 us, 1224 TFLOP/s of the two
+// products (a large library product reaches 1913); a prompt of 3314 f32 tokens, 32 heads of
+// 128, 148 us, 1.2 PFLOP/s of the four.  Sums in TMEM are f32, cut toward zero by every
+// product: 3.7e-6 of the result on that prompt.
 #include <type_traits>
 
 #include "kv.cuh"
@@ -474,7 +481,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prompt_kernel(const AttendArgs 
             }
         }
     } else {
-        // ------------------------------------------------------------ softmax: a thread per row
+        // ------------------------------------------------------------ softmax: two threads a row
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(SOFT_REGS));
         const int w = (warp - SOFT_WARP) / 8, h = (warp - SOFT_WARP) / 4 % 2;   // tile, page of a step
         const int l = warp % 4 * 32 + lane;                                      // TMEM lane

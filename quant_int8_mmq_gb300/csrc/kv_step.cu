@@ -27,6 +27,11 @@
 // cut into parts.  A part goes to a cluster of up to 8 CTAs, which share its pages evenly
 // whatever their number turns out to be and join their sums through distributed shared
 // memory; only what takes more parts than one goes by the workspace and a second kernel.
+//
+// What bounds it: the instructions of the widening, some 1500 a page with the products, at
+// the 16 warps that the registers hold.  On GB300: one token on 131071 keys, 32 f32 heads of
+// 128 on 8, 46 us (3.3 TB/s), on 524288 keys 154 us (3.9 TB/s); 64 sequences of 95 to 8192
+// keys, bf16, 91 us (3.4 TB/s).  A copy reaches 6.8 TB/s.
 #include <atomic>
 
 #include "kv.cuh"
