@@ -406,15 +406,17 @@ mmq_status mmq_kv_read(const mmq_kv_cache* c, const mmq_rows* k, const mmq_rows*
  * j > p - window or j < sinks (the first tokens that stay visible).  Head h reads kv
  * head h / (heads / kv_heads).  A row that sees no key is 0.  q and out have one dtype;
  * sums, the softmax and both products' accumulators are f32.  For f32 rows the queries
- * and the weights enter the products as pairs of f16 (22 bits); as the tensor
- * cores cut their sums toward zero, up to 4e-6 of the result (2-norm) was lost on prompts
- * of 3314 tokens, where f32 arithmetic loses 1e-6.  For 16-bit rows the weights are rounded
- * to f16.  q must be finite: a row that is not has no
+ * and the weights enter the products as pairs of f16 (22 bits); the tensor
+ * cores cut their sums toward zero, which f32 rows keep below 1e-5 of the result for values
+ * of one sign (2.3e-6 on a prompt of 3314 tokens, where f32 arithmetic loses 1.0e-6).  For
+ * 16-bit rows the weights are rounded to f16.  q must be finite: a row that is not has no
  * number for a result and touches no other row.
  * scale > 0, a normal number up to 1e38.
  *   max_q   at least the largest start[b + 1] - start[b] (else rows past it may be left
  *           out, and mmq_get_device_error then returns MMQ_ERR_ARG)
  *   max_kv  about the largest length[b]; it guides how the work is cut, any value is right
+ *           (one far too low costs time and, for a few f32 rows, digits: their sums are cut
+ *           by the parts alone)
  * The work is cut into parts whose sums meet in the workspace (of
  * mmq_kv_attend_workspace_bytes for the same arguments, 16-byte aligned; may be NULL when
  * that is 0) in a fixed order, so results do not vary from call to call.  out may not

@@ -25,8 +25,8 @@ AttendPlan plan_attend(int dtype, int heads, int kv_heads, int dim, int batch, i
     // The step kernel reads and widens the cache once per tile of 8 or 16 rows, the prompt kernel
     // once per 256, at a cost that hardly depends on how many there are.  Measured, us, step /
     // prompt kernel, 16 sequences of 8192 keys and 4 kv heads: f32 rows of 128 values, 32 rows
-    // 91 / 90, 48 rows 134 / 92; 16-bit ones 16 rows 30 / 50, 24 rows 54 / 50; f32 rows of 64,
-    // 24 rows 42 / 48, 32 rows 58 / 49; 16-bit ones 32 rows 34 / 45, 48 rows 45 / 45.
+    // 86 / 95, 36 rows 113 / 96; 16-bit ones 16 rows 30 / 50, 24 rows 54 / 50; f32 rows of 64,
+    // 24 rows 45 / 50, 32 rows 58 / 51; 16-bit ones 32 rows 34 / 45, 48 rows 45 / 45.
     const int few = dtype == KV_F32 ? (dim == 128 ? 32 : 24) : (dim == 128 ? 16 : 48);
     p.kernel = rows > few ? 1 : 0;
     // units: independent CTAs without parts; slots: CTAs that the chip holds at once; least, most:
@@ -67,7 +67,9 @@ AttendPlan plan_attend(int dtype, int heads, int kv_heads, int dim, int batch, i
         }
         parts = best;
         least = 8;
-        most = 1ll << 30;
+        // 16-bit rows: a sum of 65536 keys in tensor memory, cut toward zero by every product, is
+        // off by no more than their own rounding (2e-4); f32 rows move such sums out.
+        most = dtype != KV_F32 ? 1024 : 1ll << 30;
     }
     long long part = (pages + parts - 1) / parts;
     part = part < least ? least : part > most ? most : part;

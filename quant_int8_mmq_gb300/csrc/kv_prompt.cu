@@ -33,8 +33,16 @@
 // in part; the tensor pipe is active in 60 % of the cycles.  On GB300: chunks of 2048 and 1944
 // bf16 tokens on 16384 and 13563, 32 heads of 128 on 8, 748 us, 1224 TFLOP/s of the two
 // products (a large library product reaches 1913); a prompt of 3314 f32 tokens, 32 heads of
-// 128, 148 us, 1.2 PFLOP/s of the four.  Sums in TMEM are f32, cut toward zero by every
-// product: 3.7e-6 of the result on that prompt.
+// 128, 158 us, 1.1 PFLOP/s of the four.
+//
+// Sums in TMEM are f32, but cut toward zero by every product: 16 a step for f32 rows, which
+// cost values of one sign 1.4e-4 of the result after 20000 keys.  So f32 rows move O out every
+// RUN steps and add it, rounded, to sums that lie in the rows of the result (or of their part),
+// which belong to the CTA; L2 holds them.  What is left is the cut of RUN steps, below
+// 1e-5 for such values (12 steps: 1.0e-5, 16: 1.3e-5).  2048 tokens on 16384, 32 heads on 8, take 751 us for 648
+// without: the moves' bytes, as they took 666 with everything but the loads and stores, and more
+// when the CTAs moved at different steps (818 for 770 at 8 steps).  16-bit rows do without: their
+// own rounding is larger up to the 65536 keys that a part has at most.
 #include <type_traits>
 
 #include "kv.cuh"
@@ -54,6 +62,8 @@ static_assert(CTRL_REGS + WIDEN_REGS + 4 * SOFT_REGS == 6 * LAUNCH_REGS, "regist
 // .dec may only lower a warp's count and .inc only raise it (the other way is no instruction)
 static_assert(CTRL_REGS < LAUNCH_REGS && WIDEN_REGS < LAUNCH_REGS && SOFT_REGS > LAUNCH_REGS, "register split");
 constexpr int JOIN_BAR = 9;   // named barrier of all softmax warps (1-8: pairs)
+constexpr int TILE_BAR = 10;  // of tile 1's
+constexpr int RUN = 10;       // steps of a tile that O sums up before f32 rows move its sums out
 constexpr int META = 8;   // steps whose page descriptions are kept: more than any role runs ahead
 
 // HL: hi and lo parts of Q and P.
@@ -267,7 +277,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prompt_kernel(const AttendArgs 
 #pragma unroll                                                 // by less while they are small
                     for (int kb = 0; kb < C::KB; ++kb) {
                         const uint64_t a =
-                            sdesc_k_sw128(sbase + C::Q + ((w * C::PARTS + part) * C::KB + kb) * C::BLOCK);
+                            sdesc_k_sw128(sbase + C::Q + ((two || !HL ? w * C::PARTS : 0) + part) * C::KB * C::BLOCK + kb * C::BLOCK);
                         const uint64_t b = sdesc_k_sw128(sbase + C::K + buf * C::K_BYTES + kb * C::BLOCK);
 #pragma unroll
                         for (int kk = 0; kk < 4; ++kk)
@@ -319,7 +329,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prompt_kernel(const AttendArgs 
                     if (!ok)
                         break;
                     tc_fence_after();
-                    product_pv(w, buf, j >= stride);
+                    product_pv(w, buf, HL ? j / stride % RUN != 0 : j >= stride);
                     if (w == 1 || !two)
                         umma_commit_by(lead, bar(C::VEMPTY + buf));
                     if (jn >= u.steps) {
@@ -570,10 +580,96 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prompt_kernel(const AttendArgs 
         float ref = -INFINITY, sum = 0.0f;
         bool ok = true;
         int k = 0;   // steps of this tile so far
+
+        // of the row's sums among the parts'; of its result
+        auto part_row = [&] { return static_cast<long long>(u.split) * g.ntok * g.heads + token * g.heads + head; };
+        auto result = [&] { return g.nsplit > 1 ? part_row() * D : token * g.out.tok + head * g.out.head; };
+        // Sums moved out lie where the result will: in the warp's rows, its half of their values,
+        // but four values of one lane after four of the next, so that a warp moves whole lines.
+        // Tile 1, when it has tile 0's rows, keeps them in place of its own Q.
+        constexpr int FOURS = D / 8;   // of four values a thread has
+        float moved = 1.0f;            // what the moved sums' reference has come to since
+        [[maybe_unused]] const bool inside = !two && w == 1;
+        [[maybe_unused]] float4* const slots = reinterpret_cast<float4*>(smem + C::Q + C::Q_BYTES / 2) + h * TILE + l;
+        [[maybe_unused]] const int valid = min(max(u.nrow - tile0 - (l & ~31), 0), 32);   // the warp's rows
+        [[maybe_unused]] const bool wide = g.nsplit > 1 || g.wide;
+        [[maybe_unused]] auto moved_to = [&](long long out_at, int i) {
+            const int at = i * valid + lane;
+            float* rows = g.nsplit > 1 ? g.part : static_cast<float*>(g.out.data);
+            return rows + __shfl_sync(0xffffffffu, out_at, at / FOURS & 31) + D / 2 * h + at % FOURS * 4;
+        };
+        [[maybe_unused]] auto moved_load = [&](float4 (&x)[FOURS]) {
+            const long long out_at = result();
+#pragma unroll
+            for (int i = 0; i < FOURS; ++i) {
+                x[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                if (inside) {
+                    x[i] = slots[i * 2 * TILE];
+                } else {
+                    const float* p = moved_to(out_at, i);
+                    if (lane < valid) {
+                        Raw4<float> v;
+                        v.load(p, wide);
+                        x[i] = v.get();
+                    }
+                }
+            }
+        };
+        // O added to the moved sums x
+        [[maybe_unused]] auto move_out = [&](const float4 (&x)[FOURS]) {
+            const long long out_at = result();
+#pragma unroll
+            for (int d = 0; d < D / 2; d += 16) {
+                float o[16];
+                tmem_ld16_wait(o_at + d, o);
+#pragma unroll
+                for (int c = 0; c < 16; c += 4) {
+                    const int i = (d + c) / 4;
+                    const float4 v = make_float4(fmaf(x[i].x, moved, o[c]), fmaf(x[i].y, moved, o[c + 1]),
+                                                 fmaf(x[i].z, moved, o[c + 2]), fmaf(x[i].w, moved, o[c + 3]));
+                    if (inside) {
+                        slots[i * 2 * TILE] = v;
+                    } else {
+                        float* p = moved_to(out_at, i);
+                        if (lane < valid)
+                            store4(p, v, wide);
+                    }
+                }
+            }
+            moved = 1.0f;
+        };
+        // the moved sums x added to O
+        [[maybe_unused]] auto move_in = [&](const float4 (&x)[FOURS]) {
+#pragma unroll
+            for (int d = 0; d < D / 2; d += 16) {
+                float o[16];
+                uint32_t v[16];
+                tmem_ld16_wait(o_at + d, o);
+#pragma unroll
+                for (int c = 0; c < 16; c += 4) {
+                    const float4 y = x[(d + c) / 4];
+                    v[c] = __float_as_uint(fmaf(y.x, moved, o[c]));
+                    v[c + 1] = __float_as_uint(fmaf(y.y, moved, o[c + 1]));
+                    v[c + 2] = __float_as_uint(fmaf(y.z, moved, o[c + 2]));
+                    v[c + 3] = __float_as_uint(fmaf(y.w, moved, o[c + 3]));
+                }
+                tmem_store16(o_at + d, v);
+            }
+            tmem_wait_st();
+        };
         {
             for (int j = two ? 0 : w; j < u.steps; j += stride, ++k) {
-                ok = warp_wait(g, bar(C::SFULL + w), k & 1);
-                tc_fence_after();
+                if (HL && k > 0 && k % RUN == 0) {
+                    float4 x[FOURS] = {};
+                    if (k > RUN)
+                        moved_load(x);   // on its way while S is waited for
+                    ok = warp_wait(g, bar(C::SFULL + w), k & 1);
+                    tc_fence_after();
+                    move_out(x);
+                } else {
+                    ok = warp_wait(g, bar(C::SFULL + w), k & 1);
+                    tc_fence_after();
+                }
                 const int2 held = reinterpret_cast<const int2*>(smem + C::META_AT)[j % META];
                 const int kbase = page_of(u, u.i0 + 2 * j + h) * KV_PAGE;
                 const bool there = (h ? held.y : held.x) >= 0;
@@ -610,7 +706,8 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prompt_kernel(const AttendArgs 
                         const float f = raise ? kv_ex2(ref - next) : 1.0f;
                         ref = next;
                         sum *= f;
-                        if (k > 0) {
+                        moved *= f;
+                        if (HL ? k % RUN != 0 : k > 0) {
 #pragma unroll 1
                             for (int d = 0; d < D / 2; d += 16) {
                                 float o[16];
@@ -658,8 +755,16 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prompt_kernel(const AttendArgs 
                     mbar_arrive(bar(C::PFULL + w));
             }
             if (ok && k > 0) {
-                warp_wait(g, bar(C::OFULL + w), 0);
-                tc_fence_after();
+                if (HL && k > RUN) {
+                    float4 x[FOURS];
+                    moved_load(x);
+                    warp_wait(g, bar(C::OFULL + w), 0);
+                    tc_fence_after();
+                    move_in(x);
+                } else {
+                    warp_wait(g, bar(C::OFULL + w), 0);
+                    tc_fence_after();
+                }
             }
         }
         red[2 * ROWS * (k & 1) + h * ROWS] = sum;
@@ -673,6 +778,8 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prompt_kernel(const AttendArgs 
         if (!two && u.steps > 1) {
             float2* other = reinterpret_cast<float2*>(smem + C::JOIN) + l;
             if (w == 1) {
+                if (HL && u.steps > 2 * RUN)   // what was moved lies there too: every thread has its own back
+                    named_bar_sync(TILE_BAR, SOFT_WARPS * 16);
 #pragma unroll 1
                 for (int d = 0; d < D / 2; d += 16) {
                     float o[16];
@@ -697,11 +804,9 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prompt_kernel(const AttendArgs 
             // with): the warp writes four rows' 32 values at a time, whole lines for the strided 16
             // bytes a thread that its own row would take
             const float inv = g.nsplit > 1 ? 1.0f : sum == 0.0f ? 0.0f : 1.0f / sum;
-            const long long flat = token * g.heads + head;
-            const long long part_at = static_cast<long long>(u.split) * g.ntok * g.heads + flat;
-            const long long out_at = g.nsplit > 1 ? part_at * D : token * g.out.tok + head * g.out.head;
+            const long long out_at = result();
             if (g.nsplit > 1 && mine && h == 0)
-                g.part_ml[part_at] = make_float2(ref, sum);
+                g.part_ml[part_row()] = make_float2(ref, sum);
             constexpr int COLS = C::COLS, ROW = C::STAGED, LPR = COLS / 4;
             uint8_t* stage = smem + C::Q + (warp - SOFT_WARP) * 32 * ROW;
             const int sub = lane / LPR, c = lane % LPR * 4;

@@ -425,3 +425,30 @@ def test_example_block(kv_heads, dim, hidden):
     worst = attention_block.main(["--hidden", str(hidden), "--heads", str(hidden // dim), "--kv-heads", str(kv_heads),
                                   "--dim", str(dim), "--prompt", "150", "--steps", "3"])
     assert worst < 1e-3
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("new,heads,kv_heads", [(300, 2, 1), (100, 1, 1), (70, 6, 2)])
+@pytest.mark.parametrize("length,hint", [(20000, 64), (20000, 20000), (4300, 64), (2050, 64)])
+@pytest.mark.parametrize("shift", [0, 1])
+def test_sums_over_long_caches_keep_32_bits(length, hint, new, heads, kv_heads, dim, shift):
+    """Values of one sign, whose sums lose the most to a sum that is cut toward zero: 1e-5 of every
+    element, which a single such sum over 20000 keys exceeds (2500 products, each cutting half of
+    2^-23 of what is there, half of the whole on average: 4e-5 and more).  Scores of small
+    queries add at most 2^-19 * 1.7.  A low hint leaves the keys in one part.  Results in place
+    of rows of another stride and alignment too."""
+    b = Batch([new], [length], kv_heads, dim, F32, seed=length)
+    g = torch.Generator().manual_seed(3)
+    b.v = [(1.0 + 0.25 * torch.randn(length, kv_heads, dim, generator=g)).to(DEV)]
+    whole = torch.tensor([0, length], dtype=torch.int32, device=DEV)
+    mmq.kv_write(b.k[0], b.v[0], b.pages, b.table, whole, b.length)
+    q = b.q(heads, factor=0.1)
+    room = torch.full((new, heads, dim + 4 * shift + shift), 7.0, device=DEV)
+    out = room[..., shift:shift + dim]
+    mmq.kv_attend(q, *b.cache, max_q=new, max_kv=hint, out=out)
+    k, v = b.held(0)
+    want, _ = ref.attend(q.double(), k, v, torch.arange(length - new, length, device=DEV), dim ** -0.5)
+    err = ((out.double() - want).abs() / want.abs()).max().item()
+    assert err <= 1e-5, err
+    assert (room[..., :shift] == 7).all() and (room[..., shift + dim:] == 7).all()
+    assert status() == 0
