@@ -14,7 +14,7 @@
 // the search for the token's place.  The 8 warps of a CTA hold consecutive tokens, whose
 // value codes share their sectors.
 //
-// On GB300: reading 105537 tokens of 8 heads of 128 as bf16 takes 111 us (5.8 TB/s, a copy
+// On GB300: reading 121318 tokens of 8 heads of 128 as bf16 takes 111 us (5.8 TB/s, a copy
 // reaches 6.8); writing 3314 f32 tokens of 32 heads of 128 and reading them back 56 us
 // (4.4 TB/s), of which the write is a little under half and bound by its instructions.
 #include "kv.cuh"
