@@ -67,9 +67,10 @@ AttendPlan plan_attend(int dtype, int heads, int kv_heads, int dim, int batch, i
         }
         parts = best;
         least = 8;
-        // 16-bit rows: a sum of 65536 keys in tensor memory, cut toward zero by every product, is
-        // off by no more than their own rounding (2e-4); f32 rows move such sums out.
-        most = dtype != KV_F32 ? 1024 : 1ll << 30;
+        // 16-bit rows: a sum in tensor memory, cut toward zero by every product, lost 3.9e-4 of
+        // values of one sign after 65536 keys.  32768 keys stay below half a unit of f16's last
+        // place, 131072 of bf16's; f32 rows move such sums out.
+        most = dtype == KV_F16 ? 512 : dtype == KV_BF16 ? 2048 : 1ll << 30;
     }
     long long part = (pages + parts - 1) / parts;
     part = part < least ? least : part > most ? most : part;

@@ -42,8 +42,8 @@
 // steps, below 1e-5 for such values (12 steps: 1.0e-5, 16: 1.3e-5).  2048 tokens on 16384,
 // 32 heads on 8, take 751 us for 648 without.  What costs is the moves' bytes: moving every
 // 8 steps took 770, without its loads and stores 666, and 818 when each CTA moved at steps
-// of its own.  16-bit rows do without: their own rounding is larger up to the 65536 keys
-// that a part has at most.
+// of its own.  16-bit rows do without: their parts end before the cut passes their own
+// rounding.
 #include <type_traits>
 
 #include "kv.cuh"

@@ -452,3 +452,23 @@ def test_sums_over_long_caches_keep_32_bits(length, hint, new, heads, kv_heads, 
     assert err <= 1e-5, err
     assert (room[..., :shift] == 7).all() and (room[..., shift + dim:] == 7).all()
     assert status() == 0
+
+
+def test_long_sums_of_f16_rows_lose_less_than_their_rounding():
+    """160 sequences on the same 65536 tokens, values of one sign: enough tiles to fill the chip, so
+    that nothing but the sums' length cuts them.  Rounding the results averages out over the
+    elements, sums cut toward zero do not: less than half a unit of f16's last place, 2^-12."""
+    batch, new, length, dim = 160, 200, 65536, 64   # more than 128 rows: each tile sums up all keys
+    b = Batch([new], [length], 1, dim, F16, seed=1)
+    g = torch.Generator().manual_seed(3)
+    b.v = [(1.0 + 0.25 * torch.randn(length, 1, dim, generator=g)).to(F16).to(DEV)]
+    mmq.kv_write(b.k[0], b.v[0], b.pages, b.table, torch.tensor([0, length], dtype=torch.int32, device=DEV), b.length)
+    q = b.q(1, factor=0.1)
+    out = mmq.kv_attend(q.repeat(batch, 1, 1), b.pages, b.table.repeat(batch, 1),
+                        torch.arange(batch + 1, dtype=torch.int32, device=DEV) * new, b.length.repeat(batch),
+                        max_q=new, max_kv=length)
+    k, v = b.held(0)
+    want, _ = ref.attend(q.double(), k, v, torch.arange(length - new, length, device=DEV), dim ** -0.5)
+    off = ((out.double().view(batch, new, 1, dim) - want) / want).mean().item()
+    assert abs(off) < 2.0 ** -12, off
+    assert status() == 0
