@@ -284,7 +284,7 @@ struct AttendPlan {
     size_t part_bytes, ml_bytes;
 };
 AttendPlan plan_attend(int dtype, int heads, int kv_heads, int dim, int batch, int ntok, int max_q, int max_kv,
-                       int window, int sinks);
+                       int max_pages, int window, int sinks);
 cudaError_t launch_kv_step(const AttendArgs& a, int dim, int dtype, cudaStream_t s);
 cudaError_t launch_kv_prompt(const AttendArgs& a, int dim, int dtype, cudaStream_t s);
 cudaError_t launch_kv_join(const AttendArgs& a, int dim, int dtype, cudaStream_t s);

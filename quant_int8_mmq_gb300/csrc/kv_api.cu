@@ -10,13 +10,16 @@ namespace mmq {
 // How an attention call is cut up: rows to row tiles and, where those are few, the visible
 // pages to parts.  Depends on the arguments alone (the chip has 152 SMs).
 AttendPlan plan_attend(int dtype, int heads, int kv_heads, int dim, int batch, int ntok, int max_q, int max_kv,
-                       int window, int sinks)
+                       int max_pages, int window, int sinks)
 {
     constexpr int SMS = 152;
     AttendPlan p = {};
     const int group = heads / kv_heads;
     max_q = max_q < ntok ? max_q : ntok;
+    // no sequence has more pages than its row of the table, whatever max_kv says: parts past
+    // them would only fill the workspace
     long long pages = (static_cast<long long>(max_kv) + KV_PAGE - 1) / KV_PAGE;
+    pages = pages < max_pages ? pages : max_pages;
     if (window > 0) {
         const long long seen = (static_cast<long long>(window) + max_q + sinks) / KV_PAGE + 3;
         pages = pages < seen ? pages : seen;
@@ -200,7 +203,8 @@ mmq_status check_attend(const mmq_kv_cache* c, int dtype, int heads, int ntok, i
     if (c->head_dim != 64 && c->head_dim != 128)
         return MMQ_ERR_SHAPE;
     if (c->kv_heads < 1 || c->kv_heads > MMQ_KV_MAX_HEADS || c->batch < 1 || c->batch > MMQ_KV_MAX_BATCH ||
-        heads < 1 || heads > MMQ_KV_MAX_HEADS || heads % c->kv_heads != 0 || ntok < 0 || ntok > MMQ_MAX_M)
+        c->max_pages < 1 || c->max_pages > MMQ_KV_MAX_PAGES || heads < 1 || heads > MMQ_KV_MAX_HEADS ||
+        heads % c->kv_heads != 0 || ntok < 0 || ntok > MMQ_MAX_M)
         return MMQ_ERR_SHAPE;
     return MMQ_OK;
 }
@@ -208,7 +212,7 @@ mmq_status check_attend(const mmq_kv_cache* c, int dtype, int heads, int ntok, i
 AttendPlan plan(const mmq_kv_cache* c, int dtype, int heads, int ntok, int max_q, int max_kv, int window, int sinks)
 {
     return mmq::plan_attend(dtype, heads, c->kv_heads, c->head_dim, c->batch, ntok, max_q < 1 ? 1 : max_q,
-                            max_kv < 1 ? 1 : max_kv, window, sinks);
+                            max_kv < 1 ? 1 : max_kv, c->max_pages, window, sinks);
 }
 
 }  // namespace

@@ -133,3 +133,26 @@ def test_tensor_helpers_refuse(mmq_lib):
         for call in (lambda c: mmq.kv_write(x, x, *c), lambda c: mmq.kv_read(*c, 3), lambda c: mmq.kv_attend(x, *c, 3)):
             with pytest.raises(ValueError, match=what):
                 call(bad)
+
+
+@pytest.mark.parametrize("heads,kv_heads,dim,batch,new,dtype", [(32, 8, 128, 64, 1, 2), (4, 2, 128, 2, 2, 0),
+                                                                (32, 8, 128, 1, 16384, 1), (1, 1, 64, 1, 1, 0)])
+@pytest.mark.parametrize("max_pages", [1, 79, 2048])
+def test_a_length_hint_past_the_table_counts_as_the_table(mmq_lib, heads, kv_heads, dim, batch, new, dtype, max_pages):
+    """No sequence has more keys than its row of the table has pages for, so a larger max_kv cuts
+    the work no finer and asks for no more workspace."""
+    c = cache(kv_heads=kv_heads, head_dim=dim, batch=batch, max_pages=max_pages)
+
+    def need(max_kv):
+        return mmq.mmq_kv_attend_workspace_bytes(c, dtype, heads, batch * new, new, max_kv)
+
+    assert need(1 << 30) == need((1 << 31) - 1) == need(64 * max_pages)
+    # a part holds 4 pages or more: sums, reference and weight of each row for so many parts at most
+    assert need(1 << 30) <= (max_pages // 4 + 1) * batch * new * heads * (4 * dim + 8) + 16
+
+
+def test_the_size_query_checks_the_tables_width(mmq_lib):
+    for max_pages in (0, -1, (1 << 24) + 1):
+        with pytest.raises(mmq.MMQError) as e:
+            mmq.mmq_kv_attend_workspace_bytes(cache(max_pages=max_pages), 0, 2, 4, 4, 256)
+        assert e.value.status == SHAPE
