@@ -353,7 +353,9 @@ mmq_status mmq_debug_inject_wait_timeout(int fill, unsigned long long limit_ns);
  * position length[b] - start[b + 1] + r.  table, start and length are read on the
  * device.  A page id outside [0, num_pages) or a position outside [0, 64 max_pages) is
  * not followed: such a token is not written and reads as zeros, such keys are not
- * there for the attention, and mmq_get_device_error then returns MMQ_ERR_ARG.
+ * there for the attention, and mmq_get_device_error then returns MMQ_ERR_ARG.  So it does
+ * for packed rows outside start[0] .. start[batch], or of a sequence whose start leads outside
+ * [0, ntok]: they are not written, read as zeros, and are zeros as results of the attention.
  * -------------------------------------------------------------------------- */
 #define MMQ_KV_PAGE 64
 #define MMQ_KV_MAX_HEADS 1024
@@ -413,7 +415,7 @@ mmq_status mmq_kv_read(const mmq_kv_cache* c, const mmq_rows* k, const mmq_rows*
  * number for a result and touches no other row.
  * scale > 0, a normal number up to 1e38.
  *   max_q   at least the largest start[b + 1] - start[b] (else rows past it may be left
- *           out, and mmq_get_device_error then returns MMQ_ERR_ARG)
+ *           out as zeros, and mmq_get_device_error then returns MMQ_ERR_ARG)
  *   max_kv  about the largest length[b]; it guides how the work is cut, any value is right
  *           (one past 64 * max_pages counts as that; one far too low costs time and, where
  *           it leaves long sums whole, digits: 3e-5 of values of one sign for one f32 row

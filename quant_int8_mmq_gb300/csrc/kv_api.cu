@@ -280,7 +280,8 @@ mmq_status mmq_kv_attend(const mmq_kv_cache* c, const mmq_rows* q, const mmq_row
         if (!aligned(workspace, 16))
             return MMQ_ERR_ALIGN;
     }
-    if (static_cast<long long>(p.nsplit) * p.cluster * p.row_tiles * c->kv_heads * (p.kernel == 0 ? c->batch : 1) >
+    // the grid: the units and a block (a cluster) for the rows of none
+    if ((static_cast<long long>(p.nsplit) * p.row_tiles * c->kv_heads * (p.kernel == 0 ? c->batch : 1) + 1) * p.cluster >
             0x7fffffffll ||
         static_cast<long long>(ntok) * heads > 0x7fffffffll)
         return MMQ_ERR_SHAPE;

@@ -168,6 +168,10 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prompt_kernel(const AttendArgs 
     auto bar = [&](int i) -> uint32_t { return sbase + C::BAR + 8u * static_cast<uint32_t>(i); };
 
     grid_dep_wait();
+    if (blockIdx.x == gridDim.x - 1) {
+        kv_clear_others<D, T>(g, 1ll << 60);   // the tiles take any number of new tokens
+        return;
+    }
     // ---------------------------------------------------------------- the unit
     // blocks run from the last row tile of the batch to the first (a sequence's later tiles
     // see more keys), all heads and splits of a tile together
@@ -884,7 +888,7 @@ cudaError_t launch_prompt(const AttendArgs& a, cudaStream_t s)
     if (regs.load() != LAUNCH_REGS)
         return cudaErrorInvalidConfiguration;
     const unsigned int grid =
-        static_cast<unsigned int>(static_cast<long long>(a.nsplit) * a.c.kv_heads * a.row_tiles);
+        static_cast<unsigned int>(static_cast<long long>(a.nsplit) * a.c.kv_heads * a.row_tiles + 1);
     count_launch();
     return launch_dependent_smem(kv_prompt_kernel<D, T>, dim3(grid), dim3(THREADS), C::BYTES, s, a);
 }

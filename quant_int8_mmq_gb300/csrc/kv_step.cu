@@ -90,6 +90,11 @@ __global__ void __launch_bounds__(WARPS * 32, MODE == WIDE ? 3 : D == 128 ? 4 : 
     // the unit: a part of the pages for one row tile of one sequence's kv head
     int id = blockIdx.x / g.cluster;
     const int rank = blockIdx.x % g.cluster;
+    if (id == static_cast<int>(gridDim.x) / g.cluster - 1) {
+        if (rank == 0)
+            kv_clear_others<D, T>(g, static_cast<long long>(g.row_tiles) * ROWS);
+        return;
+    }
     const int split = id % g.nsplit;
     id /= g.nsplit;
     const int head = id % g.c.kv_heads;
@@ -101,8 +106,6 @@ __global__ void __launch_bounds__(WARPS * 32, MODE == WIDE ? 3 : D == 128 ? 4 : 
     const int rows_b = (last - first) * g.group, row0 = tile * ROWS;
     if (row0 >= rows_b)
         return;
-    if (threadIdx.x == 0 && tile == 0 && (rows_b + ROWS - 1) / ROWS > g.row_tiles)
-        *g.c.bad = 1u;   // more new tokens than the caller's max_q: rows past it are not computed
     const int nrow = min(ROWS, rows_b - row0);
     const int pos0 = max(g.c.length[b], 0) - rows_b / g.group;
     const int room = g.c.max_pages * KV_PAGE;
@@ -609,8 +612,8 @@ cudaError_t launch_step(const AttendArgs& a, cudaStream_t s)
     at[1].val.clusterDim.y = 1;
     at[1].val.clusterDim.z = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned int>(static_cast<long long>(a.cluster) * a.nsplit * a.c.kv_heads *
-                                                 a.row_tiles * a.c.batch));
+    cfg.gridDim = dim3(static_cast<unsigned int>(
+        a.cluster * (static_cast<long long>(a.nsplit) * a.c.kv_heads * a.row_tiles * a.c.batch + 1)));
     cfg.blockDim = dim3(WARPS * 32);
     cfg.dynamicSmemBytes = BYTES;
     cfg.stream = s;

@@ -472,3 +472,57 @@ def test_long_sums_of_f16_rows_lose_less_than_their_rounding():
     off = ((out.double().view(batch, new, 1, dim) - want) / want).mean().item()
     assert abs(off) < 2.0 ** -12, off
     assert status() == 0
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("new,length,heads", [([1, 2], [200, 90], 4), ([1, 1], [3000, 90], 4),      # a CTA, a cluster a part,
+                                              ([1, 1], [20000, 90], 4), ([1] * 70, [90] * 70, 2),   # many parts;
+                                              ([150, 3], [300, 90], 2), ([60, 3], [20000, 90], 2)])  # prompts
+def test_rows_of_no_sequence_are_zero_and_reported(new, length, heads, dtype):
+    """Packed rows before the first sequence's and past the last's, as a padded batch has them."""
+    b = Batch(new, length, 2, 64, dtype)
+    front, back = 3, 5
+    q = b.q(heads)
+    wide = torch.cat([torch.ones(front, heads, 64, device=DEV).to(dtype), q, torch.ones(back, heads, 64, device=DEV).to(dtype)])
+    for lo, hi in ((front, back), (0, back), (front, 0)):
+        part = wide[front - lo:wide.shape[0] - back + hi]
+        out = torch.full_like(part, 7.0)
+        mmq.kv_attend(part, b.pages, b.table, b.start + lo, b.length, max_q=max(new), max_kv=max(length), out=out)
+        assert status() == 1 and status() == 0
+        assert (out[:lo] == 0).all() and (out[lo + b.rows:] == 0).all()
+        b.check(q, out[lo:lo + b.rows])
+
+
+@pytest.mark.parametrize("dtype", [F32, F16])
+@pytest.mark.parametrize("new,length", [([2, 3], [200, 90]), ([1, 2], [20000, 90]), ([300, 40], [300, 90])])
+def test_sequences_that_lead_outside_the_rows_are_zero_and_reported(new, length, dtype):
+    b = Batch(new, length, 2, 64, dtype)
+    q = b.q(4)
+    right = mmq.kv_attend(q, *b.cache, max_q=max(new), max_kv=max(length))
+    b.check(q, right)
+    n = new[0]
+    for start, lo, hi in (([-1, n, b.rows], 0, n), ([0, n, b.rows + 2], n, b.rows), ([-5, -5, -5], 0, b.rows)):
+        out = torch.full_like(q, 7.0)
+        mmq.kv_attend(q, b.pages, b.table, torch.tensor(start, dtype=torch.int32, device=DEV), b.length, max_q=max(new),
+                      max_kv=max(length), out=out)
+        assert status() == 1 and status() == 0
+        assert (out[lo:hi] == 0).all()
+        assert torch.equal(out[:lo], right[:lo]) and torch.equal(out[hi:], right[hi:])
+    out = mmq.kv_attend(q, b.pages, b.table, torch.tensor([0, n, n - 1], dtype=torch.int32, device=DEV), b.length,
+                        max_q=max(new), max_kv=max(length), out=torch.full_like(q, 7.0))
+    assert status() == 1
+    assert torch.equal(out[:n - 1], right[:n - 1]) and (out[n:] == 0).all()
+
+
+@pytest.mark.parametrize("length", [128, 20000])
+def test_rows_past_max_q_are_zero_and_reported(length):
+    b = Batch([40, 2], [length, 70], 1, 64)
+    q = b.q(1)
+    out = torch.full_like(q, 7.0)
+    mmq.kv_attend(q, *b.cache, max_q=2, max_kv=length, out=out)
+    assert status() == 1 and status() == 0
+    left = (out[:40] == 0).flatten(1).all(1)
+    assert left.any() and not left[0]
+    want = mmq.kv_attend(q, *b.cache, max_q=40, max_kv=length)
+    out[:40][left] = want[:40][left]
+    b.check(q, out)
