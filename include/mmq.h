@@ -417,9 +417,9 @@ mmq_status mmq_kv_read(const mmq_kv_cache* c, const mmq_rows* k, const mmq_rows*
  *   max_q   at least the largest start[b + 1] - start[b] (else rows past it may be left
  *           out as zeros, and mmq_get_device_error then returns MMQ_ERR_ARG)
  *   max_kv  about the largest length[b]; it guides how the work is cut, any value is right
- *           (one past 64 * max_pages counts as that; one far too low costs time and, where
- *           it leaves long sums whole, digits: 3e-5 of values of one sign for one f32 row
- *           on 20000 keys under a hint of 64)
+ *           (one past 64 * max_pages counts as that; one far too low costs time and, for
+ *           16-bit rows, digits, as their sums over the keys past it stay whole: f16 rows
+ *           lose 4.3e-4 of values of one sign over 65536 such keys)
  * The work is cut into parts whose sums meet in the workspace (of
  * mmq_kv_attend_workspace_bytes for the same arguments, 16-byte aligned; may be NULL when
  * that is 0) in a fixed order, so results do not vary from call to call.  out may not

@@ -28,6 +28,12 @@
 // whatever their number turns out to be and join their sums through distributed shared
 // memory; only what takes more parts than one goes by the workspace and a second kernel.
 //
+// The tensor cores cut sums toward zero at every product, 8 a page for f32 rows.  Those set
+// their sums aside every RUN pages of a warp and go on from zero: what is left is the cut of
+// 128 products, 6e-6 of values of one sign whatever the length (one sum over 20000 keys lost
+// 3.2e-5, over 131072 keys 2.2e-4).  A part is that long a warp only where a cluster takes up
+// to 128 pages a CTA or where max_kv is far too low, so the other calls pay nothing.
+//
 // What bounds it: the instructions of the widening, some 1500 a page with the products, at
 // the 16 warps that the registers hold.  On GB300: one token on 131071 keys, 32 f32 heads of
 // 128 on 8, 46 us (3.3 TB/s), on 524288 keys 154 us (3.9 TB/s); 64 sequences of 95 to 8192
@@ -41,6 +47,7 @@ namespace {
 
 constexpr int WARPS = 4;
 constexpr int STAGES = 2;   // half pieces (K or V) a warp's ring holds
+constexpr int RUN = 16;     // pages that a warp's accumulators sum up before f32 rows set them aside
 
 // Row tiles (see above).
 enum Mode { HI_LO = 0, ONE_PART = 1, WIDE = 2 };
@@ -254,7 +261,25 @@ __global__ void __launch_bounds__(WARPS * 32, MODE == WIDE ? 3 : D == 128 ? 4 : 
         flying &= ~(1u << stage);
         return smem + S::RING + (warp * STAGES + stage) * S::HALF;
     };
+    // Long parts of f32 rows (see above): sums set aside, in local memory, so that the loop's
+    // registers are not needed for them.  `ahead` tells the pages so far.
+    [[maybe_unused]] volatile float aside[MODE == HI_LO ? D / 4 + 1 : 1];
+    auto any_aside = [&] { return MODE == HI_LO && ahead > 2 * RUN + STAGES - 1; };
+    auto set_aside = [&] {
+        const bool any = any_aside();
+#pragma unroll
+        for (int j = 0; j < D / 4; ++j) {
+            aside[j] = any ? aside[j] + o[0][j / 4][j % 4] : o[0][j / 4][j % 4];
+            o[0][j / 4][j % 4] = 0.0f;
+        }
+        aside[D / 4] = any ? aside[D / 4] + sum[0] : sum[0];
+        sum[0] = 0.0f;
+    };
     for (int i = i0; i < i_end; i += WARPS) {
+        if constexpr (MODE == HI_LO) {
+            if (ahead % (2 * RUN) == STAGES - 1 && ahead > 2 * RUN)
+                set_aside();
+        }
         const uint8_t* page = next_half();
         if (page == nullptr) {
             if (!ok)
@@ -360,6 +385,14 @@ __global__ void __launch_bounds__(WARPS * 32, MODE == WIDE ? 3 : D == 128 ? 4 : 
                     o[i][j][2] *= f0;
                     o[i][j][3] *= f1;
                 }
+                if constexpr (MODE == HI_LO) {
+                    if (any_aside()) {
+#pragma unroll
+                        for (int j = 0; j < D / 4; ++j)
+                            aside[j] = aside[j] * (j % 2 ? f1 : f0);
+                        aside[D / 4] = aside[D / 4] * f;
+                    }
+                }
             }
         }
 #pragma unroll
@@ -423,6 +456,12 @@ __global__ void __launch_bounds__(WARPS * 32, MODE == WIDE ? 3 : D == 128 ? 4 : 
                     step(o[0][2 * j], o[0][2 * j + 1], a, b, lo[0], lo[1]);
             }
         }
+    }
+    if (any_aside()) {
+#pragma unroll
+        for (int j = 0; j < D / 4; ++j)
+            o[0][j / 4][j % 4] += aside[j];
+        sum[0] += aside[D / 4];
     }
     if (!ok) {   // a wait ran out: the copies in flight still have to land before the CTA ends
 #pragma unroll

@@ -526,3 +526,26 @@ def test_rows_past_max_q_are_zero_and_reported(length):
     want = mmq.kv_attend(q, *b.cache, max_q=40, max_kv=length)
     out[:40][left] = want[:40][left]
     b.check(q, out)
+
+
+@pytest.mark.parametrize("batch,new,length,heads,kv_heads,dim,hint", [
+    (9, 1, 65536, 4, 4, 128, 65536), (7, 1, 65536, 8, 8, 64, 65536),             # clusters of twice the pages
+    (1, 1, 20000, 1, 1, 128, 64), (1, 3, 70000, 8, 2, 64, 64), (1, 1, 131072, 4, 1, 128, 64)])   # all keys in one CTA
+def test_sums_of_few_rows_over_long_caches_keep_32_bits(batch, new, length, heads, kv_heads, dim, hint):
+    """Values of one sign under few rows, as above for many: 1e-5 of every element.  Where a CTA has
+    128 pages a warp sums up 256 products, each cutting up to 2^-23 of what is there, half of it
+    on average; sequences share their pages, so that a batch costs one sequence's memory."""
+    b = Batch([new], [length], kv_heads, dim, F32, seed=length)
+    g = torch.Generator().manual_seed(3)
+    b.v = [(1.0 + 0.25 * torch.randn(length, kv_heads, dim, generator=g)).to(DEV)]
+    whole = torch.tensor([0, length], dtype=torch.int32, device=DEV)
+    mmq.kv_write(b.k[0], b.v[0], b.pages, b.table, whole, b.length)
+    q = b.q(heads, factor=0.1)
+    out = mmq.kv_attend(q.repeat(batch, 1, 1), b.pages, b.table.repeat(batch, 1),
+                        torch.arange(batch + 1, dtype=torch.int32, device=DEV) * new, b.length.repeat(batch),
+                        max_q=new, max_kv=hint)
+    k, v = b.held(0)
+    want, _ = ref.attend(q.double(), k, v, torch.arange(length - new, length, device=DEV), dim ** -0.5)
+    err = ((out.double().view(batch, new, heads, dim) - want).abs() / want.abs()).max().item()
+    assert err <= 1e-5, err
+    assert status() == 0
