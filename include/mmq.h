@@ -408,11 +408,16 @@ mmq_status mmq_kv_read(const mmq_kv_cache* c, const mmq_rows* k, const mmq_rows*
  * j > p - window or j < sinks (the first tokens that stay visible).  Head h reads kv
  * head h / (heads / kv_heads).  A row that sees no key is 0.  q and out have one dtype;
  * sums, the softmax and both products' accumulators are f32.  For f32 rows the queries
- * and the weights enter the products as pairs of f16 (22 bits); the tensor
- * cores cut their sums toward zero, which f32 rows keep below 1e-5 of the result for values
- * of one sign (2.3e-6 on a prompt of 3314 tokens, where f32 arithmetic loses 1.0e-6).  For
- * 16-bit rows the weights are rounded to f16.  q must be finite: a row that is not has no
- * number for a result and touches no other row.
+ * and the weights enter the products as pairs of f16 (22 bits, a weight no finer than 2^-38 of
+ * the row's largest).  The tensor cores cut their sums toward zero, by up to 2^-23 at each
+ * product; f32 rows add up at most 160 products before they move such a sum to one that is
+ * rounded.  For values of one sign that is below 1e-5 of the result where no key outweighs
+ * the others (2.3e-6 on a prompt of 3314 tokens, where f32 arithmetic loses 1.0e-6) and up to
+ * 2.5e-5 where one outweighs a long tail.  For 16-bit rows the weights are rounded to f16 and no
+ * finer than 2^-32 of the row's largest.  Such errors are relative to the largest values that
+ * have weight: where the key that outweighs the others has a value near zero, they are more of
+ * the result.  q must be finite: a row that is not has no number for a result and touches no
+ * other row.
  * scale > 0, a normal number up to 1e38.
  *   max_q   at least the largest start[b + 1] - start[b] (else rows past it may be left
  *           out as zeros, and mmq_get_device_error then returns MMQ_ERR_ARG)

@@ -196,10 +196,17 @@ __device__ __forceinline__ void kv_split2(float x, float y, uint32_t& hi, uint32
     lo = kv_h2u(__floats2half2_rn(x - f.x, y - f.y));
 }
 
-// Softmax weights p = 2^(x - ref) are kept in f16 halves.  A fresh reference is 7 below the
-// row's largest x and stands until some x is 15 above it, so p is at most 2^15, rows are
-// rescaled rarely, and what 2^7 is to the largest p, f16's least step 2^-24 is to the least.
-constexpr float KV_REF_BELOW = 7.0f;
+// Softmax weights p = 2^(x - ref) are kept in f16 halves.  A fresh reference is `below` less
+// than the row's largest x and stands until some x is 15 above it, so p is at most 2^15.  f16's
+// least step is 2^-24: a weight may be off by 2^-25, which n keys together make n 2^-(25 + below)
+// of the largest.  16-bit rows: 7, so that rows are rescaled rarely (by a factor of 2^8 or
+// more); 131072 keys lose up to 3e-5, below the rounding of P.  f32 rows: 13, a factor of 4;
+// 2^20 keys lose up to 4e-6 (with 7 a far tail of 131072 keys lost 6e-5).
+template <typename T>
+__host__ __device__ constexpr float kv_ref_below()
+{
+    return sizeof(T) == 4 ? 13.0f : 7.0f;
+}
 constexpr float KV_REF_LIMIT = 15.0f;
 
 // Which keys of a page (64 from kbase on) a row at position pos sees, one bit each.

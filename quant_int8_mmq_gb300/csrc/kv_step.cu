@@ -368,7 +368,7 @@ __global__ void __launch_bounds__(WARPS * 32, MODE == WIDE ? 3 : D == 128 ? 4 : 
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2)) * coef[i];
             const bool up = top > ref[i] + KV_REF_LIMIT;   // also the first visible key: ref is -inf until then
-            next[i] = up ? top - KV_REF_BELOW : ref[i];
+            next[i] = up ? top - kv_ref_below<T>() : ref[i];
             raise |= up;
         }
         if (__any_sync(0xffffffffu, raise)) {
@@ -404,6 +404,7 @@ __global__ void __launch_bounds__(WARPS * 32, MODE == WIDE ? 3 : D == 128 ? 4 : 
             break;
         page -= P::V_CODES;
         const int held = min(kend - kbase, KV_PAGE);
+        float page_sum = 0.0f;   // f32 rows: a page's weights together do not vanish beside a large sum
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk) {   // keys 16 kk .. 16 kk + 15
             uint32_t hi[SETS][2], lo[2];
@@ -413,7 +414,7 @@ __global__ void __launch_bounds__(WARPS * 32, MODE == WIDE ? 3 : D == 128 ? 4 : 
                 for (int h = 0; h < 2; ++h) {
                     const float p0 = kv_ex2(fmaf(x[2 * kk + h][i][0], coef[i], -base[i]));
                     const float p1 = kv_ex2(fmaf(x[2 * kk + h][i][1], coef[i], -base[i]));
-                    sum[i] += p0 + p1;
+                    (MODE == HI_LO ? page_sum : sum[i]) += p0 + p1;
                     if constexpr (MODE == HI_LO)
                         kv_split2(p0, p1, hi[i][h], lo[h]);
                     else
@@ -456,6 +457,8 @@ __global__ void __launch_bounds__(WARPS * 32, MODE == WIDE ? 3 : D == 128 ? 4 : 
                     step(o[0][2 * j], o[0][2 * j + 1], a, b, lo[0], lo[1]);
             }
         }
+        if constexpr (MODE == HI_LO)
+            sum[0] += page_sum;
     }
     if (any_aside()) {
 #pragma unroll

@@ -549,3 +549,33 @@ def test_sums_of_few_rows_over_long_caches_keep_32_bits(batch, new, length, head
     err = ((out.double().view(batch, new, heads, dim) - want).abs() / want.abs()).max().item()
     assert err <= 1e-5, err
     assert status() == 0
+
+
+@pytest.mark.parametrize("new,heads,length,dim,products,run", [(1, 4, 400000, 64, 128, 4 * 1024),
+                                                               (70, 1, 131072, 64, 160, 1280),
+                                                               (300, 1, 131072, 128, 160, 1280)])
+def test_one_loud_key_before_a_long_tail(new, heads, length, dim, products, run):
+    """f32 rows whose first key outweighs each of the others by 2^28 .. 2^40, all keys in one part.
+    The tail must not be lost key by key: each may be off by 2^-38 of the largest weight, and its
+    value is up to 8 times that of the first; the products that meet in one tensor-core sum cut 2^-23 of
+    it each; products and weights so far are added up in f32 once a run of keys (of four warps under
+    few rows), the weights of a run in up to 16 steps."""
+    b = Batch([new], [length], 1, dim, F32, seed=length, fill=False)
+    g = torch.Generator().manual_seed(3)
+    b.k = [torch.zeros(length, 1, dim, device=DEV)]
+    b.k[0][0] = 1.0
+    b.v = [(1.0 + 0.25 * torch.randn(length, 1, dim, generator=g)).clamp(min=0.5).to(DEV)]
+    b.v[0][0] = 0.25
+    whole = torch.tensor([0, length], dtype=torch.int32, device=DEV)
+    mmq.kv_write(b.k[0], b.v[0], b.pages, b.table, whole, b.length)
+    k, v = b.held(0)
+    below = torch.linspace(28, 40, new * heads, device=DEV).view(new, heads, 1)
+    below[-1, -1] = 32.05
+    q = (below / k[0].sum()).float().expand(new, heads, dim).contiguous()
+    scale = float(np.float32(np.log(2.0)))
+    out = mmq.kv_attend(q, *b.cache, max_q=new, max_kv=64, scale=scale)
+    want, _ = ref.attend(q.double(), k, v, torch.arange(length - new, length, device=DEV), scale)
+    err = ((out.double() - want).abs() / want.abs()).max().item()
+    # the scores' own errors change what the tail adds, which is little
+    assert err <= products * 2.0 ** -23 + 8 * length * 2.0 ** -38 + 2 * (length / run + 16) * 2.0 ** -24 + 2.0 ** -19, err
+    assert status() == 0
