@@ -431,7 +431,7 @@ def _kv_cache(pages, table, start, length):
             (nstart,), (nlength,) = start.shape, length.shape
         except ValueError:
             piece = 1
-        if piece % 72 == 0 and nstart == batch + 1 and nlength == batch:
+        if piece % 72 == 0 and nstart == batch + 1 and nlength == batch and dev == torch._C._cuda_getDevice():
             return KVCache(pages.data_ptr(), table.data_ptr(), start.data_ptr(), length.data_ptr(), num_pages,
                            kv_heads, piece // 72, batch, max_pages), dev
     if pages.dtype != torch.uint8 or pages.dim() != 3 or not pages.is_contiguous() or pages.shape[2] % 72:
@@ -441,7 +441,10 @@ def _kv_cache(pages, table, start, length):
     for x, n, name in ((start, table.shape[0] + 1, "start"), (length, table.shape[0], "length")):
         if x.dtype != i32 or x.shape != (n,) or not x.is_contiguous():
             raise ValueError(f"{name} must be a contiguous int32 [{n}] tensor")
-    raise ValueError("pages, table, start and length must be CUDA tensors on one device")
+    if dev < 0 or not dev == table.get_device() == start.get_device() == length.get_device():
+        raise ValueError("pages, table, start and length must be CUDA tensors on one device")
+    # the library launches on the current device, and takes its error words from there
+    raise ValueError(f"the cache is on cuda:{dev}, which is not the current device: call under torch.cuda.device({dev})")
 
 
 def _kv_rows(x, rows, heads, dim, dev, name):
@@ -460,7 +463,11 @@ def _kv_rows(x, rows, heads, dim, dev, name):
 
 def _kv_stream(stream, dev):
     """Handle of the given or the device's current stream."""
-    return _torch_module._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+    if stream is None:
+        return _torch_module._C._cuda_getCurrentRawStream(dev)
+    if stream.device_index != dev:
+        raise ValueError(f"the stream is of cuda:{stream.device_index}, the cache on cuda:{dev}")
+    return stream.cuda_stream
 
 
 def _kv_empty(shape, dtype, device, stream):

@@ -156,3 +156,49 @@ def test_the_size_query_checks_the_tables_width(mmq_lib):
         with pytest.raises(mmq.MMQError) as e:
             mmq.mmq_kv_attend_workspace_bytes(cache(max_pages=max_pages), 0, 2, 4, 4, 256)
         assert e.value.status == SHAPE
+
+
+def test_tensors_of_another_device_than_the_current_are_refused(mmq_lib, monkeypatch):
+    """The library launches on the current device.  The tensors here are host memory that claims to
+    be on cuda:1; the library is replaced too, so that nothing can reach a GPU."""
+    import torch
+
+    class OnOne(torch.Tensor):
+        def get_device(self):
+            return 1
+
+    def at(*shape, dtype=torch.int32):
+        return torch.zeros(*shape, dtype=dtype).as_subclass(OnOne)
+
+    class Stream:
+        def __init__(self, device):
+            self.device_index, self.cuda_stream = device, 0
+
+    calls = []
+
+    class Library:
+        def __getattr__(self, name):
+            return lambda *a: calls.append(name) or 0
+
+    monkeypatch.setattr(mmq, "_lib", Library())
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda dev: 0, raising=False)
+    x = at(3, 2, 64, dtype=torch.float32)
+    cache = at(4, 2, 72 * 64, dtype=torch.uint8), at(1, 4), at(2), at(1)
+
+    def everything(stream):
+        yield lambda: mmq.kv_write(x, x, *cache, stream=stream)
+        yield lambda: mmq.kv_read(*cache, 3, k=x, v=x, stream=stream)
+        yield lambda: mmq.kv_attend(x, *cache, 3, out=x, stream=stream)
+
+    for current, stream, what in ((0, None, "current device"), (0, Stream(0), "current device"),
+                                  (0, Stream(1), "current device"), (1, Stream(0), "stream")):
+        monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: current, raising=False)
+        for call in everything(stream):
+            with pytest.raises(ValueError, match=what):
+                call()
+    assert calls == []
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 1, raising=False)
+    for stream in (None, Stream(1)):
+        for call in everything(stream):
+            call()
+    assert calls == ["mmq_kv_write", "mmq_kv_read", "mmq_kv_attend"] * 2
