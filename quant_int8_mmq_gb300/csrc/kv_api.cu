@@ -130,10 +130,10 @@ mmq_status check_cache(const mmq_kv_cache* c)
 
 bool known_type(int t) { return t == MMQ_F32 || t == MMQ_F16 || t == MMQ_BF16; }
 
-// [ntok][heads][dim] rows; those that are written may not overlap.
+// [ntok][heads][dim] rows (no rows have no address); those that are written may not overlap.
 mmq_status check_rows(const mmq_rows* r, int ntok, int heads, int dim, bool written)
 {
-    if (!r || !r->data || !known_type(r->dtype) || r->token_stride < 0 || r->head_stride < 0)
+    if (!r || (!r->data && ntok > 0) || !known_type(r->dtype) || r->token_stride < 0 || r->head_stride < 0)
         return MMQ_ERR_ARG;
     constexpr long long MOST = 1ll << 40;
     if (r->token_stride > MOST || r->head_stride > MOST)

@@ -202,3 +202,13 @@ def test_tensors_of_another_device_than_the_current_are_refused(mmq_lib, monkeyp
         for call in everything(stream):
             call()
     assert calls == ["mmq_kv_write", "mmq_kv_read", "mmq_kv_attend"] * 2
+
+
+def test_rows_without_an_address_are_no_rows(mmq_lib):
+    """An empty tensor's data pointer is null; a call on it is as little work as on any other."""
+    before = mmq.mmq_launch_count()
+    none = rows(data=None)
+    assert write(k=none, v=none, n=0) == OK and read(k=none, v=none, n=0) == OK
+    assert attend(q=none, out=none, n=0, ws=None, size=0) == OK
+    assert mmq.mmq_launch_count() == before
+    assert write(k=none, n=1) == ARG and read(v=none, n=1) == ARG and attend(out=none, n=1) == ARG

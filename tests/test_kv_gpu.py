@@ -579,3 +579,14 @@ def test_one_loud_key_before_a_long_tail(new, heads, length, dim, products, run)
     # the scores' own errors change what the tail adds, which is little
     assert err <= products * 2.0 ** -23 + 8 * length * 2.0 ** -38 + 2 * (length / run + 16) * 2.0 ** -24 + 2.0 ** -19, err
     assert status() == 0
+
+
+def test_calls_on_empty_tensors_do_nothing():
+    b = Batch([0, 0], [70, 5], 2, 64)
+    before = b.pages.clone()
+    x, q = torch.empty(0, 2, 64, device=DEV), torch.empty(0, 4, 64, device=DEV)
+    mmq.kv_write(x, x, *b.cache)
+    k, v = mmq.kv_read(*b.cache, 0)
+    out = mmq.kv_attend(q, *b.cache, max_q=0)
+    assert k.shape == v.shape == (0, 2, 64) and out.shape == q.shape
+    assert torch.equal(b.pages, before) and status() == 0
