@@ -272,6 +272,7 @@ def mmq_version() -> str:
 # ----------------------------------------------------------------------------
 # Tensor helpers: PyTorch provides device memory and the current stream only.
 # ----------------------------------------------------------------------------
+_INT_MAX = 0x7fffffff
 _torch_module = None
 _ROW_TYPES = {}      # torch dtype -> mmq_dtype
 
@@ -449,7 +450,7 @@ def _kv_cache(pages, table, start, length):
 
 def _kv_rows(x, rows, heads, dim, dev, name):
     t = _ROW_TYPES.get(x.dtype)
-    if t is not None and x.shape == (rows, heads, dim) and x.get_device() == dev:
+    if t is not None and x.shape == (rows, heads, dim) and x.get_device() == dev and rows <= _INT_MAX:
         st, sh, sd = x.stride()
         if sd == 1:
             return Rows(x.data_ptr(), t, st, sh)
@@ -457,6 +458,8 @@ def _kv_rows(x, rows, heads, dim, dev, name):
         raise ValueError(f"{name} must be float32, float16 or bfloat16, got {x.dtype}")
     if x.get_device() != dev:
         raise ValueError(f"{name} must be on the cache's device")
+    if rows > _INT_MAX:
+        raise ValueError(f"{name} has too many rows: {rows}")
     raise ValueError(f"{name} must be {[rows, heads, dim]} with unit stride in its last dimension, got {list(x.shape)} "
                      f"with strides {list(x.stride())}")
 
@@ -518,6 +521,9 @@ def kv_attend(q, pages, table, start, length, max_q, max_kv=None, scale=None, wi
         max_kv = c.max_pages * KV_PAGE
     if scale is None:
         scale = dim ** -0.5
+    if (max_q | max_kv | window | sinks) > _INT_MAX:
+        # ctypes would drop the high bits; larger numbers mean no more than the largest the library takes
+        max_q, max_kv, window, sinks = (min(n, _INT_MAX) for n in (max_q, max_kv, window, sinks))
     rq = _kv_rows(q, rows, heads, dim, dev, "q")
     if out is None:
         out = _torch_module.empty_like(q) if stream is None and q.is_contiguous() else _kv_empty(

@@ -212,3 +212,39 @@ def test_rows_without_an_address_are_no_rows(mmq_lib):
     assert attend(q=none, out=none, n=0, ws=None, size=0) == OK
     assert mmq.mmq_launch_count() == before
     assert write(k=none, n=1) == ARG and read(v=none, n=1) == ARG and attend(out=none, n=1) == ARG
+
+
+def test_numbers_past_32_bits_are_not_cut_off(mmq_lib, monkeypatch):
+    """A window of 2^32 is a wide one, not none.  Host memory that claims to be on a device, and no
+    library behind it."""
+    import torch
+
+    class OnZero(torch.Tensor):
+        def get_device(self):
+            return 0
+
+    def at(*shape, dtype=torch.int32):
+        return torch.zeros(*shape, dtype=dtype).as_subclass(OnZero)
+
+    seen = []
+
+    class Library:
+        def __getattr__(self, name):
+            return lambda *a: seen.append(a) or 0
+
+    monkeypatch.setattr(mmq, "_lib", Library())
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda dev: 0, raising=False)
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0, raising=False)
+    x = at(3, 2, 64, dtype=torch.float32)
+    cache = at(4, 2, 72 * 64, dtype=torch.uint8), at(1, 4), at(2), at(1)
+    big = (1 << 31) - 1
+    for given, taken in (((3, 70, 5, 1), (3, 70, 5, 1)), ((1 << 32, 70, 0, 1 << 33), (big, 70, 0, big)),
+                         ((3, (1 << 40) + 1, (1 << 32) + 7, 1 << 31), (3, big, big, big)), ((3, 70, -1, 0), (3, 70, -1, 0))):
+        max_q, max_kv, window, sinks = given
+        mmq.kv_attend(x, *cache, max_q, max_kv, window=window, sinks=sinks, out=x)
+        a = seen.pop()
+        assert (a[5], a[6], a[8], a[9]) == taken
+    many = x[:1].expand((1 << 32) + 1, 2, 64).as_subclass(OnZero)
+    with pytest.raises(ValueError, match="rows"):
+        mmq.kv_write(many, many, *cache)
+    assert seen == []
