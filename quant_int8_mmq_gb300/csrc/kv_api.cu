@@ -310,6 +310,9 @@ mmq_status mmq_kv_attend(const mmq_kv_cache* c, const mmq_rows* q, const mmq_row
     a.part = static_cast<float*>(workspace);
     a.part_ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(workspace) + p.part_bytes);
     a.wc = {a.c.bad - 1, mmq::WAIT_LIMIT_NS, -1};
+    bool injected = false;
+    if (p.cluster == 1 && mmq::take_wait_ctl(&a.wc, &injected) != cudaSuccess)   // a cluster barrier has no time limit
+        return MMQ_ERR_CUDA;
     const auto launch = p.kernel == 0 ? mmq::launch_kv_step : mmq::launch_kv_prompt;
     cudaError_t e = launch(a, c->head_dim, q->dtype, reinterpret_cast<cudaStream_t>(s));
     if (e == cudaSuccess && p.nsplit > 1)

@@ -156,6 +156,10 @@ __global__ void __launch_bounds__(WARPS * 32, MODE == WIDE ? 3 : D == 128 ? 4 : 
     // the warp's pages are i0, i0 + WARPS, ...; ids of 32 of them at a time, one per lane
     const int* table = g.c.table + static_cast<size_t>(b) * g.c.max_pages;
     int ids = -1, ahead = 0;   // halves asked for so far: K, V of the first page, K, ...
+    // verification only: the first CTA's first page is left out (never armed, never copied), so
+    // that the wait for it runs out
+    constexpr int WITHHELD = 0x7fffffff;
+    const bool withhold = g.wc.withhold_fill >= 0 && blockIdx.x == 0 && warp == 0;
     int fill = 0;              // their next stage
     uint32_t flying = 0;       // bit s: stage s holds or awaits a half
     auto fetch = [&] {
@@ -168,13 +172,15 @@ __global__ void __launch_bounds__(WARPS * 32, MODE == WIDE ? 3 : D == 128 ? 4 : 
                 if (ids < 0 || ids >= g.c.num_pages) {
                     *g.c.bad = 1u;
                     ids = -1;
+                } else if (withhold && k + lane == 0) {
+                    ids = WITHHELD;
                 }
             }
         }
         const int pid = __shfl_sync(0xffffffffu, ids, k % 32);
         if (pid >= 0) {
             flying |= 1u << fill;
-            if (lane == 0) {
+            if (lane == 0 && pid != WITHHELD) {
                 fence_proxy_async_smem();   // the stage's last half was read with ordinary loads
                 mbar_arrive_expect_tx(bar + 8 * fill, S::HALF);
                 bulk_g2s(ring + fill * S::HALF,
@@ -469,7 +475,7 @@ __global__ void __launch_bounds__(WARPS * 32, MODE == WIDE ? 3 : D == 128 ? 4 : 
     if (!ok) {   // a wait ran out: the copies in flight still have to land before the CTA ends
 #pragma unroll
         for (int s = 0; s < STAGES; ++s)
-            if (flying >> s & 1u)
+            if (flying >> s & 1u && !withhold)   // that warp never gets past its first page
                 mbar_drain_wait(bar + 8 * s, parity >> s & 1u, WAIT_LIMIT_NS, g.wc.err);
     }
 

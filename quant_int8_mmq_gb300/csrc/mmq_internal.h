@@ -166,7 +166,7 @@ void count_launch();
 cudaError_t device_error_word(unsigned int** word);
 cudaError_t read_and_clear_device_error(cudaStream_t s, unsigned int (&value)[2]);
 
-// What a tile-GEMM launch's bounded waits use: the error word, the time limit of
+// What a tile-GEMM or attention launch's bounded waits use: the error word, the time limit of
 // each wait, and (verification only) one operand-ring fill that CTA 0's producer
 // leaves out, so that the wait for it runs out (-1: none).
 constexpr unsigned long long WAIT_LIMIT_NS = 2000000000ull;
@@ -175,7 +175,7 @@ struct WaitCtl {
     unsigned long long limit_ns;
     int withhold_fill;
 };
-// The WaitCtl of the next tile-GEMM launch: the default limit and no withheld fill,
+// The WaitCtl of the next tile-GEMM or attention launch: the default limit and no withheld fill,
 // unless mmq_debug_inject_wait_timeout armed a one-shot injection, which this call
 // consumes.  *injected tells which.
 cudaError_t take_wait_ctl(WaitCtl* wc, bool* injected);

@@ -590,3 +590,31 @@ def test_calls_on_empty_tensors_do_nothing():
     out = mmq.kv_attend(q, *b.cache, max_q=0)
     assert k.shape == v.shape == (0, 2, 64) and out.shape == q.shape
     assert torch.equal(b.pages, before) and status() == 0
+
+
+@pytest.mark.parametrize("dtype,new,length,heads,kv_heads,dim,batch,fill", [
+    (F32, 1, 200, 4, 4, 128, 1, 0), (F16, 4, 250, 16, 4, 128, 1, 0), (BF16, 1, 9000, 16, 8, 64, 40, 0),   # few rows
+    (F32, 1, 9000, 8, 8, 128, 40, 3),
+    (F32, 100, 900, 2, 1, 128, 1, 0), (F32, 400, 2000, 1, 1, 64, 1, 3), (BF16, 100, 900, 2, 1, 128, 1, 1),
+    (F16, 400, 2000, 1, 1, 64, 1, 5), (F16, 400, 500, 2, 2, 128, 30, 2)])
+def test_expired_wait_is_reported_then_cleared(dtype, new, length, heads, kv_heads, dim, batch, fill):
+    """One copy of the first CTA is left out and every wait of the launch gives up after 1 ms (launches
+    without clusters of CTAs): the launch ends, the report says why and clears, the next is right."""
+    b = Batch([new], [length], kv_heads, dim, dtype)
+    q = b.q(heads)
+    call = dict(max_q=new, max_kv=length)
+    many = (b.pages, b.table.repeat(batch, 1), torch.arange(batch + 1, dtype=torch.int32, device=DEV) * new,
+            b.length.repeat(batch))
+    torch.cuda.synchronize()
+    assert status() == 0
+    try:
+        mmq.mmq_debug_inject_wait_timeout(fill, 1_000_000)
+        mmq.kv_attend(q.repeat(batch, 1, 1), *many, **call)
+        assert status() == 5
+        assert status() == 0
+        out = mmq.kv_attend(q.repeat(batch, 1, 1), *many, **call)
+        assert status() == 0
+    finally:
+        mmq.mmq_debug_inject_wait_timeout(-1)
+    b.check(q, out[:new])
+    b.check(q, out[-new:])
