@@ -317,9 +317,10 @@ mmq_status mmq_debug_select_large_m_kernel(int which);
  * result: [r56] §3.1).  Arms a one-shot injection for the next GEMM launch that
  * runs a tile kernel (M > MMQ_SMALL_M), or attention launch whose CTAs form no
  * clusters: its waits give up after limit_ns (1 us .. 2 s) instead of about two
- * seconds, and the producer of its first CTA leaves operand fill number `fill` (0-based, counted over that CTA's k-blocks; attention:
- * over the K and V halves of a prompt's first rows' page pairs, or the first page of a step
- * whatever `fill` is) out, so the wait for it runs out, the launch exits early and
+ * seconds, and the producer of its first CTA leaves operand fill number `fill` out
+ * (0-based, counted over that CTA's k-blocks; over the K and V halves of a prompt's
+ * pairs of pages, for its first rows of kv head 0; a few rows' attention leaves its first
+ * page out whatever `fill` is), so the wait for it runs out, the launch exits early and
  * mmq_get_device_error() then returns MMQ_ERR_TIMEOUT (and clears the word).
  * That launch takes no CTA-cluster split.  Its result is undefined.  fill < 0
  * disarms a pending injection.  MMQ_ERR_ARG for a limit outside the range.

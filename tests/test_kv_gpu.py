@@ -618,3 +618,15 @@ def test_expired_wait_is_reported_then_cleared(dtype, new, length, heads, kv_hea
         mmq.mmq_debug_inject_wait_timeout(-1)
     b.check(q, out[:new])
     b.check(q, out[-new:])
+
+
+@pytest.mark.parametrize("dtype", [F32, F16])
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("new,window,sinks", [(1, 0, 0), (1, 19000, 70), (3, 0, 0), (3, 12000, 4)])
+def test_many_pages_of_one_warp(new, window, sinks, dim, dtype):
+    """A hint far too low leaves 20000 keys, 79 pages a warp, in one CTA of the step kernel, which
+    fetches page ids 32 at a time."""
+    b = Batch([new], [20000], 2, dim, dtype, seed=dim)
+    q = b.q(6)
+    out = mmq.kv_attend(q, *b.cache, max_q=new, max_kv=64, window=window, sinks=sinks)
+    b.check(q, out, window=window, sinks=sinks)
