@@ -30,17 +30,20 @@
 // TMEM is freed and the CTA ends.
 //
 // What bounds it: a tile's chain of softmax, P V and Q K^T, which the other tile covers only
-// in part; the tensor pipe is active in 60 % of the cycles (f32 rows: 52 %).  On GB300:
+// in part; the tensor pipe is active in 60 % of the cycles (f32 rows: 52 %).  The f32 builds spill
+// (0.6 % of the instructions executed), the others a word of 128-value heads at most.  On GB300:
 // chunks of 2048 and 1944 bf16 tokens on 16384 and 13563, 32 heads of 128 on 8, 748 us, 1224
 // TFLOP/s of the two products (a large library product reaches 1913); a prompt of 3314 f32
-// tokens, 32 heads of 128, 158 us, 1.1 PFLOP/s of the four.
+// tokens, 32 heads of 128, 161 us, 1.1 PFLOP/s of the four.
 //
 // Sums in TMEM are f32, but cut toward zero by every product: 16 a step for f32 rows, which
 // cost values of one sign 1.4e-4 of the result after 20000 keys.  So f32 rows move O out
 // every RUN steps and add it, rounded, to sums that lie in the rows of the result (or of
 // their part), which belong to the CTA; L2 holds them.  What is left is the cut of RUN
-// steps, below 1e-5 for such values (12 steps: 1.0e-5, 16: 1.3e-5).  2048 tokens on 16384,
-// 32 heads on 8, take 751 us for 648 without.  What costs is the moves' bytes: moving every
+// steps, below 1e-5 for such values (12 steps: 1.0e-5, 16: 1.3e-5) and up to 2e-5 where a first
+// key outweighs the others, as each of its 160 products may cut 2^-23.  A step's weights are
+// summed up over those steps too before they are added to the rest.  2048 tokens on 16384,
+// 32 heads on 8, took 751 us for 648 without, and take 757 now.  What costs is the moves' bytes: moving every
 // 8 steps took 770, without its loads and stores 666, and 818 when each CTA moved at steps
 // of its own.  16-bit rows do without: their parts end before the cut passes their own
 // rounding.

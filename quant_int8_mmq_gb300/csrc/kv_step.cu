@@ -34,10 +34,14 @@
 // 3.2e-5, over 131072 keys 2.2e-4).  A part is that long a warp only where a cluster takes up
 // to 128 pages a CTA or where max_kv is far too low, so the other calls pay nothing.
 //
-// What bounds it: the instructions of the widening, some 1500 a page with the products, at
-// the 16 warps that the registers hold.  On GB300: one token on 131071 keys, 32 f32 heads of
-// 128 on 8, 46 us (3.3 TB/s), on 524288 keys 154 us (3.9 TB/s); 64 sequences of 95 to 8192
-// keys, bf16, 91 us (3.4 TB/s).  A copy reaches 6.8 TB/s.
+// What bounds it: chains of dependent instructions, some 1500 a page for widening and products,
+// at the 4 warps a scheduler that the registers hold: an instruction issues in 57 % of the
+// cycles, and no pipe is over 45 % busy.  On GB300: one token on 131071 keys, 32 f32 heads of
+// 128 on 8, 47 us (3.2 TB/s), on 524288 keys 158 us (3.8 TB/s); 64 sequences of 95 to 8192
+// keys, bf16, 92 us (3.4 TB/s).  A copy reaches 6.8 TB/s.
+//
+// The 16-row tiles of 128 values spill: 20 of a page's instructions are loads and stores of
+// spilled registers (1.3 %).  The other builds spill a few words outside the loop or none.
 #include <atomic>
 
 #include "kv.cuh"
@@ -230,7 +234,8 @@ __global__ void __launch_bounds__(WARPS * 32, MODE == WIDE ? 3 : D == 128 ? 4 : 
     __syncthreads();
 
     // the operand Q, read again for every two octets of keys: kept in registers (32 of them) it
-    // left the rest too few to run ahead (524288 keys, 32 heads on 8: 158 us for 154)
+    // left the rest too few to run ahead (524288 keys, 32 heads on 8: 158 us for 154, before f32 rows
+    // set sums aside)
     const uint4* qf = reinterpret_cast<const uint4*>(smem + S::Q) + lane;   // step j at 32 j
     float coef[SETS], ref[SETS], sum[SETS];
     int pos[SETS];   // the row sees keys up to here, -1: no row
