@@ -32,16 +32,17 @@
 // their sums aside every RUN pages of a warp and go on from zero: what is left is the cut of
 // 128 products, 6e-6 of values of one sign whatever the length (one sum over 20000 keys lost
 // 3.2e-5, over 131072 keys 2.2e-4).  A part is that long a warp only where a cluster takes up
-// to 128 pages a CTA or where max_kv is far too low, so the other calls pay nothing.
+// to 128 pages a CTA or where max_kv is far too low; the others pay for the test (one token on
+// 131071 keys, 47.8 us for 46.0).
 //
 // What bounds it: chains of dependent instructions, some 1500 a page for widening and products,
 // at the 4 warps a scheduler that the registers hold: an instruction issues in 57 % of the
 // cycles, and no pipe is over 45 % busy.  On GB300: one token on 131071 keys, 32 f32 heads of
-// 128 on 8, 47 us (3.2 TB/s), on 524288 keys 158 us (3.8 TB/s); 64 sequences of 95 to 8192
+// 128 on 8, 48 us (3.2 TB/s), on 524288 keys 158 us (3.8 TB/s); 64 sequences of 95 to 8192
 // keys, bf16, 92 us (3.4 TB/s).  A copy reaches 6.8 TB/s.
 //
 // The 16-row tiles of 128 values spill: 20 of a page's instructions are loads and stores of
-// spilled registers (1.3 %).  The other builds spill a few words outside the loop or none.
+// spilled registers (1.3 %); the other builds have 3 or none.
 #include <atomic>
 
 #include "kv.cuh"
@@ -163,7 +164,6 @@ __global__ void __launch_bounds__(WARPS * 32, MODE == WIDE ? 3 : D == 128 ? 4 : 
     // verification only: the first CTA's first page is left out (never armed, never copied), so
     // that the wait for it runs out
     constexpr int WITHHELD = 0x7fffffff;
-    const bool withhold = g.wc.withhold_fill >= 0 && blockIdx.x == 0 && warp == 0;
     int fill = 0;              // their next stage
     uint32_t flying = 0;       // bit s: stage s holds or awaits a half
     auto fetch = [&] {
@@ -176,7 +176,7 @@ __global__ void __launch_bounds__(WARPS * 32, MODE == WIDE ? 3 : D == 128 ? 4 : 
                 if (ids < 0 || ids >= g.c.num_pages) {
                     *g.c.bad = 1u;
                     ids = -1;
-                } else if (withhold && k + lane == 0) {
+                } else if (g.wc.withhold_fill >= 0 && blockIdx.x == 0 && warp == 0 && k + lane == 0) {
                     ids = WITHHELD;
                 }
             }
@@ -274,7 +274,7 @@ __global__ void __launch_bounds__(WARPS * 32, MODE == WIDE ? 3 : D == 128 ? 4 : 
     };
     // Long parts of f32 rows (see above): sums set aside, in local memory, so that the loop's
     // registers are not needed for them.  `ahead` tells the pages so far.
-    [[maybe_unused]] volatile float aside[MODE == HI_LO ? D / 4 + 1 : 1];
+    [[maybe_unused]] volatile float aside[D / 4 + 1];
     auto any_aside = [&] { return MODE == HI_LO && ahead > 2 * RUN + STAGES - 1; };
     auto set_aside = [&] {
         const bool any = any_aside();
@@ -478,9 +478,10 @@ __global__ void __launch_bounds__(WARPS * 32, MODE == WIDE ? 3 : D == 128 ? 4 : 
         sum[0] += aside[D / 4];
     }
     if (!ok) {   // a wait ran out: the copies in flight still have to land before the CTA ends
+        const bool withheld = __shfl_sync(0xffffffffu, ids, 0) == WITHHELD;   // both halves of it, nothing else
 #pragma unroll
         for (int s = 0; s < STAGES; ++s)
-            if (flying >> s & 1u && !withhold)   // that warp never gets past its first page
+            if (flying >> s & 1u && !withheld)
                 mbar_drain_wait(bar + 8 * s, parity >> s & 1u, WAIT_LIMIT_NS, g.wc.err);
     }
 
