@@ -437,6 +437,99 @@ mmq_status mmq_kv_attend(const mmq_kv_cache* c, const mmq_rows* q, const mmq_row
                          int max_kv, float scale, int window, int sinks, void* workspace, size_t workspace_bytes,
                          mmq_stream_t s);
 
+/* --------------------------------------------------------------------------
+ * A cache held to a budget of tokens.
+ *
+ * weights: f32 [num_pages][kv_heads][MMQ_KV_PAGE], what each cached token's key of each kv head
+ * has received of the softmax so far, beside the pages of the cache (16-byte aligned).
+ * -------------------------------------------------------------------------- */
+
+/* mmq_kv_attend (same arguments, same result), and the weight that each key received, added to
+ * what it had: for kv head h and every token j of every sequence with new tokens,
+ *   new_weights[h][j] = (j < length - new ? decay * weights[h][j] : 0) + sum over the sequence's new
+ *   rows and the heads that read h of w_j / sum_i w_i
+ * (w as above; 0 for keys that a row does not see; new = start[b + 1] - start[b], whose tokens start
+ * from 0, so nothing has to be cleared).  decay in [0, 1].  new_weights may be weights; a buffer of
+ * its own keeps the old ones, for a step that may be taken back.  Slots past the last token, and
+ * pages of no sequence with new tokens, are left as they were.  A page that two sequences of the call
+ * share gets one of their sums.  A row that is not finite, or past max_q (see there), adds nothing.
+ * The sums are f32, in a fixed order.
+ * Workspace: mmq_kv_attend_weights_workspace_bytes, more than 0 where ntok is. */
+mmq_status mmq_kv_attend_weights_workspace_bytes(const mmq_kv_cache* c, int dtype, int heads, int ntok, int max_q,
+                                                 int max_kv, int window, int sinks, size_t* bytes);
+mmq_status mmq_kv_attend_weights(const mmq_kv_cache* c, const mmq_rows* q, const mmq_rows* out, int heads, int ntok,
+                                 int max_q, int max_kv, float scale, int window, int sinks, const float* weights,
+                                 float* new_weights, float decay, void* workspace, size_t workspace_bytes,
+                                 mmq_stream_t s);
+
+/* Eviction: of each sequence min(length, keep) tokens go to the pages of new_table ([batch][new_pages]
+ * page ids, new_pages * MMQ_KV_PAGE >= keep), in their order, with their weights.  Where length >
+ * keep those are, per kv head, the first `first` tokens, the last `last` (first + last <= keep), and the
+ * keep - first - last of the rest with the largest weights; of equal ones the earlier stays, and a
+ * weight that is no number counts as the least.  So a slot may hold different tokens in different
+ * heads.  Codes and scales are moved, not computed anew.
+ *   new_length  [batch]: min(length, keep); may be c->length
+ *   kept        [batch][kv_heads][keep]: the old place of the token in each new one, -1 past new_length
+ *   max_kv      about the longest length, as for mmq_kv_attend
+ * c->start is not read.  The old pages are only read, so other sequences may share them; the new ones
+ * may not be among them or be named twice (what they then hold is undefined).  Slots past
+ * new_length are left as they were.  A token whose old page is no page of the pool counts as the
+ * least weight and moves as zeros, one whose new page is none does not move, and mmq_get_device_error
+ * then returns MMQ_ERR_ARG.
+ * A window of mmq_kv_attend counts slots: after an eviction it reaches further back than before.
+ * Keys keep the rotation they were written with; new ones go on with the positions of the text. */
+mmq_status mmq_kv_evict(const mmq_kv_cache* c, float* weights, const int32_t* new_table, int new_pages, int keep,
+                        int first, int last, int max_kv, int32_t* new_length, int32_t* kept, mmq_stream_t s);
+
+/* --------------------------------------------------------------------------
+ * Rotary positions.  With f_i the angle per position of pair i, the values (a, b) of the pair in a
+ * row at position p become (a c - b s, a s + b c), c = m cos(p f_i), s = m sin(p f_i).  Pair i is values
+ * i and i + rot_dim / 2 of the head, or 2 i and 2 i + 1 interleaved; values from rot_dim on stay.
+ * cos and sin are f32 numbers next to the true ones however far the position; products and sums are
+ * f32, rounded one by one, and the result is rounded once to the rows' type.
+ * -------------------------------------------------------------------------- */
+#define MMQ_ROPE_MAX_DIM 1024
+
+typedef struct {
+    const uint64_t* turns;    /* device, rot_dim / 2, 8-byte aligned: f_i / (2 pi) * 2^64 modulo 2^64 */
+    int rot_dim;              /* even, 2 .. head_dim */
+    int interleaved;          /* 0 or 1 */
+    float magnitude;          /* m, finite; 1 where nothing asks for another */
+} mmq_rope_plan;
+
+typedef enum {
+    MMQ_ROPE_PLAIN = 0,       /* f_i = base^(-2 i / rot_dim) */
+    MMQ_ROPE_LINEAR = 1,      /* f_i / factor: positions interpolated */
+    MMQ_ROPE_NTK = 2,         /* base * factor^(rot_dim / (rot_dim - 2)) for base: the slowest pair is
+                                 factor times slower, the fastest as it was */
+    MMQ_ROPE_YARN = 3,        /* (1 - r_i) f_i + r_i f_i / factor, r_i = (i - lo) / (hi - lo) within [0, 1], lo
+                                 and hi the (real) pairs, rounded down and up, that make 32 turns and 1
+                                 turn over `original` positions; magnitude 0.1 ln(factor) + 1 (B. Peng et
+                                 al., YaRN, 2023) */
+    MMQ_ROPE_BANDS = 4        /* n_i f_i + (1 - n_i) f_i / factor, n_i = (t_i - 1) / 3 within [0, 1], t_i the
+                                 turns of the pair over `original` positions */
+} mmq_rope_scaling;
+
+/* Host only: the f_i (freq, rot_dim / 2 doubles) and the magnitude of a scaling.  base > 1, factor >= 1
+ * (not looked at by PLAIN), original >= 1 (looked at by YARN and BANDS). */
+mmq_status mmq_rope_frequencies(mmq_rope_scaling scaling, int rot_dim, double base, double factor, double original,
+                                double* freq, float* magnitude);
+/* Host only: the turns of n frequencies (magnitudes up to 1e6), to copy to the device. */
+mmq_status mmq_rope_turns(const double* freq, int n, uint64_t* turns);
+
+/* out = x turned, rows of `heads` heads of head_dim values (up to MMQ_ROPE_MAX_DIM) of one dtype, row r
+ * at position pos[r] (device, any int32).  out may be x (same data and strides); other overlaps are
+ * undefined.  A value that is not finite touches its pair alone. */
+mmq_status mmq_rope(const mmq_rope_plan* p, const mmq_rows* x, const mmq_rows* out, const int32_t* pos, int heads,
+                    int head_dim, int ntok, mmq_stream_t s);
+
+/* mmq_rope of q into q_out (which may be q), and mmq_kv_write of k, turned, and v, in one launch.  All
+ * rows have one dtype; the turned k is quantised as it is in f32, not rounded to that type before.  pos
+ * is the rotation's position and need not be the place in the cache (after an eviction it is not). */
+mmq_status mmq_kv_write_rope(const mmq_kv_cache* c, const mmq_rope_plan* p, const mmq_rows* q, const mmq_rows* q_out,
+                             int heads, const mmq_rows* k, const mmq_rows* v, const int32_t* pos, int ntok,
+                             mmq_stream_t s);
+
 /* Synchronizes `s`, then reports and clears the sticky device error words:
  * MMQ_ERR_TIMEOUT if a bounded wait expired since the last call, else MMQ_ERR_ARG if a
  * cache call met a page, a position or a row count outside what it was given,
@@ -453,7 +546,8 @@ const char* mmq_last_path(void);
 /* Number of kernel launches the library has made in this process (every entry
  * point that launches adds the kernels it launched: prepass 1, repack 4 or 5,
  * GEMM 1, or 2 when K-half tiles are first zeroed; cache write and read 1, attention 1,
- * or 2 when parts are joined through the workspace). */
+ * or 2 when parts are joined through the workspace, and 1 more for the weights; eviction 2;
+ * rotary positions 1). */
 unsigned long long mmq_launch_count(void);
 
 /* Library version string. */

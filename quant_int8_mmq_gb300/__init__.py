@@ -28,6 +28,9 @@ __all__ = [
     "quantize_act", "pack_weights", "pack_weights_fused", "gemm", "gemm_dots", "TYPES",
     "mmq_kv_page_bytes", "mmq_kv_write", "mmq_kv_read", "mmq_kv_attend_workspace_bytes", "mmq_kv_attend",
     "KVCache", "Rows", "DTYPES", "KV_PAGE", "kv_pages", "kv_write", "kv_read", "kv_attend",
+    "mmq_kv_attend_weights_workspace_bytes", "mmq_kv_attend_weights", "mmq_kv_evict",
+    "mmq_rope_frequencies", "mmq_rope_turns", "mmq_rope", "mmq_kv_write_rope",
+    "RopePlan", "ROPE_SCALINGS", "rope_plan", "rope", "kv_write_rope", "kv_weights", "kv_attend_weights", "kv_evict",
 ]
 
 MMQ_Q4_K = 12
@@ -36,6 +39,7 @@ MMQ_ERR_ARG = 1
 TYPES = {"q4_K": MMQ_Q4_K, "q6_K": MMQ_Q6_K}
 DTYPES = {"float32": 0, "float16": 1, "bfloat16": 2}     # mmq_dtype by torch's name
 KV_PAGE = 64                                             # tokens per page of the 4-bit key/value cache
+ROPE_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3, "bands": 4}    # mmq_rope_scaling
 BLOCK_BYTES = {MMQ_Q4_K: 144, MMQ_Q6_K: 210}
 
 STATUS = {0: "MMQ_OK", 1: "MMQ_ERR_ARG", 2: "MMQ_ERR_SHAPE", 3: "MMQ_ERR_ALIGN", 4: "MMQ_ERR_CUDA",
@@ -56,6 +60,13 @@ class Rows(ctypes.Structure):
     """mmq_rows of the C ABI."""
     _fields_ = [("data", ctypes.c_void_p), ("dtype", ctypes.c_int), ("token_stride", ctypes.c_longlong),
                 ("head_stride", ctypes.c_longlong)]
+
+
+class RopePlan(ctypes.Structure):
+    """mmq_rope_plan of the C ABI; one made by rope_plan keeps its device memory alive as ``held``."""
+    _fields_ = [("turns", ctypes.c_void_p), ("rot_dim", ctypes.c_int), ("interleaved", ctypes.c_int),
+                ("magnitude", ctypes.c_float)]
+    held = None
 
 
 class MMQError(RuntimeError):
@@ -81,7 +92,8 @@ def load():
                                "(or __graft_entry__.build())")
         lib = ctypes.CDLL(LIB_PATH)
         P, I, S = ctypes.c_void_p, ctypes.c_int, ctypes.POINTER(ctypes.c_size_t)
-        C, R = ctypes.POINTER(KVCache), ctypes.POINTER(Rows)
+        C, R, RP = ctypes.POINTER(KVCache), ctypes.POINTER(Rows), ctypes.POINTER(RopePlan)
+        D, F = ctypes.c_double, ctypes.c_float
         sig = {
             "mmq_act_plane_bytes": [I, I, S, S],
             "mmq_quantize_act": [P, I, I, I, P, P, P],
@@ -104,6 +116,13 @@ def load():
             "mmq_kv_read": [C, R, R, I, P],
             "mmq_kv_attend_workspace_bytes": [C, I, I, I, I, I, I, I, S],
             "mmq_kv_attend": [C, R, R, I, I, I, I, ctypes.c_float, I, I, P, ctypes.c_size_t, P],
+            "mmq_kv_attend_weights_workspace_bytes": [C, I, I, I, I, I, I, I, S],
+            "mmq_kv_attend_weights": [C, R, R, I, I, I, I, F, I, I, P, P, F, P, ctypes.c_size_t, P],
+            "mmq_kv_evict": [C, P, P, I, I, I, I, I, P, P, P],
+            "mmq_rope_frequencies": [I, I, D, D, D, ctypes.POINTER(D), ctypes.POINTER(F)],
+            "mmq_rope_turns": [ctypes.POINTER(D), I, ctypes.POINTER(ctypes.c_uint64)],
+            "mmq_rope": [RP, R, R, P, I, I, I, P],
+            "mmq_kv_write_rope": [C, RP, R, R, I, R, R, P, I, P],
         }
         for name, args in sig.items():
             fn = getattr(lib, name)
@@ -243,6 +262,48 @@ def mmq_kv_attend(cache, q, out, heads, ntok, max_q, max_kv, scale, window=0, si
                   workspace_bytes=0, stream=0):
     _check(load().mmq_kv_attend(cache, q, out, heads, ntok, max_q, max_kv, scale, window, sinks, workspace or None,
                                 workspace_bytes, stream or None), "mmq_kv_attend")
+
+
+def mmq_kv_attend_weights_workspace_bytes(cache, dtype, heads, ntok, max_q, max_kv, window=0, sinks=0) -> int:
+    b = ctypes.c_size_t()
+    _check(load().mmq_kv_attend_weights_workspace_bytes(cache, dtype, heads, ntok, max_q, max_kv, window, sinks,
+                                                        ctypes.byref(b)), "mmq_kv_attend_weights_workspace_bytes")
+    return b.value
+
+
+def mmq_kv_attend_weights(cache, q, out, heads, ntok, max_q, max_kv, scale, weights, new_weights, decay=1.0, window=0,
+                          sinks=0, workspace=0, workspace_bytes=0, stream=0):
+    _check(load().mmq_kv_attend_weights(cache, q, out, heads, ntok, max_q, max_kv, scale, window, sinks, weights,
+                                        new_weights, decay, workspace or None, workspace_bytes, stream or None),
+           "mmq_kv_attend_weights")
+
+
+def mmq_kv_evict(cache, weights, new_table, new_pages, keep, first, last, max_kv, new_length, kept, stream=0):
+    _check(load().mmq_kv_evict(cache, weights, new_table, new_pages, keep, first, last, max_kv, new_length, kept,
+                               stream or None), "mmq_kv_evict")
+
+
+def mmq_rope_frequencies(scaling, rot_dim: int, base=10000.0, factor=1.0, original=0.0):
+    """(frequencies in radians per position, magnitude) of a scaling; host only."""
+    freq, m = (ctypes.c_double * max(rot_dim // 2, 1))(), ctypes.c_float()
+    _check(load().mmq_rope_frequencies(ROPE_SCALINGS.get(scaling, scaling), rot_dim, base, factor, original, freq,
+                                       ctypes.byref(m)), "mmq_rope_frequencies")
+    return list(freq), m.value
+
+
+def mmq_rope_turns(freq):
+    """Turns per position of each frequency, as 64-bit fractions; host only."""
+    turns = (ctypes.c_uint64 * max(len(freq), 1))()
+    _check(load().mmq_rope_turns((ctypes.c_double * max(len(freq), 1))(*freq), len(freq), turns), "mmq_rope_turns")
+    return list(turns)[:len(freq)]
+
+
+def mmq_rope(plan, x, out, pos, heads, head_dim, ntok, stream=0):
+    _check(load().mmq_rope(plan, x, out, pos, heads, head_dim, ntok, stream or None), "mmq_rope")
+
+
+def mmq_kv_write_rope(cache, plan, q, q_out, heads, k, v, pos, ntok, stream=0):
+    _check(load().mmq_kv_write_rope(cache, plan, q, q_out, heads, k, v, pos, ntok, stream or None), "mmq_kv_write_rope")
 
 
 def mmq_get_device_error(stream=0) -> int:
@@ -544,3 +605,160 @@ def kv_attend(q, pages, table, start, length, max_q, max_kv=None, scale=None, wi
     if st:
         raise MMQError(st, "kv_attend")
     return out
+
+
+# ----------------------------------------------------------------------------
+# Rotary positions, and a cache held to a budget of tokens.
+# ----------------------------------------------------------------------------
+def rope_plan(rot_dim, base=10000.0, interleaved=False, scaling="none", factor=1.0, original=0, freq=None,
+              magnitude=None, device="cuda"):
+    """What rope and kv_write_rope need to know, made once.  scaling stretches contexts of
+    `original` positions by `factor`: none, linear, ntk, yarn or bands (see include/mmq.h); freq
+    (radians per position of each of rot_dim / 2 pairs) and magnitude take the place of its."""
+    torch = _torch()
+    _require(scaling in ROPE_SCALINGS, f"scaling must be one of {', '.join(ROPE_SCALINGS)}, got {scaling!r}")
+    own, m = mmq_rope_frequencies(scaling, rot_dim, base, factor, original)
+    if freq is not None:
+        freq = [float(f) for f in freq]
+        _require(len(freq) == len(own), f"freq must have {len(own)} entries, got {len(freq)}")
+    turns = mmq_rope_turns(own if freq is None else freq)
+    held = torch.tensor([t - (1 << 64) if t >> 63 else t for t in turns], dtype=torch.int64).to(device)
+    plan = RopePlan(held.data_ptr(), rot_dim, int(bool(interleaved)), m if magnitude is None else magnitude)
+    plan.held = held
+    return plan
+
+
+def _rope_args(plan, pos, rows, dev):
+    """One chain of checks for a right call, as _kv_cache."""
+    if plan.held is not None and plan.held.get_device() != dev:
+        raise ValueError("the plan must be on the rows' device")
+    if (pos.dtype is not _torch_module.int32 or pos.shape != (rows,) or not pos.is_contiguous()
+            or pos.get_device() != dev):
+        raise ValueError(f"pos must be a contiguous int32 [{rows}] CUDA tensor on the rows' device")
+    return pos.data_ptr()
+
+
+def rope(x, pos, plan, out=None, stream=None):
+    """x [rows, heads, head_dim] (any strides with a contiguous last dimension) at positions pos
+    (int32 [rows]), turned; out may be x."""
+    torch = _torch_module or _torch()
+    if x.dim() != 3:
+        raise ValueError(f"x must be [rows, heads, head_dim], got {list(x.shape)}")
+    rows, heads, dim = x.shape
+    dev = x.get_device()
+    if dev < 0:
+        raise ValueError("x must be a CUDA tensor")
+    if dev != torch._C._cuda_getDevice():
+        raise ValueError(f"x is on cuda:{dev}, which is not the current device: call under torch.cuda.device({dev})")
+    at = _rope_args(plan, pos, rows, dev)
+    if out is None:
+        out = _kv_empty((rows, heads, dim), x.dtype, x.device, stream)
+    st = (_lib or load()).mmq_rope(plan, _kv_rows(x, rows, heads, dim, dev, "x"), _kv_rows(out, rows, heads, dim, dev, "out"),
+                                   at, heads, dim, rows, _kv_stream(stream, dev) or None)
+    if st:
+        raise MMQError(st, "rope")
+    return out
+
+
+def kv_write_rope(q, k, v, pos, plan, pages, table, start, length, out=None, stream=None):
+    """q [rows, heads, head_dim] turned (returned; out may be q), and k, turned, and v into the cache
+    as kv_write does."""
+    c, dev = _kv_cache(pages, table, start, length)
+    if q.dim() != 3:
+        raise ValueError(f"q must be [rows, heads, head_dim], got {list(q.shape)}")
+    rows, heads = q.shape[:2]
+    hk, dim = c.kv_heads, c.head_dim
+    at = _rope_args(plan, pos, rows, dev)
+    if out is None:
+        out = _kv_empty((rows, heads, dim), q.dtype, q.device, stream)
+    st = (_lib or load()).mmq_kv_write_rope(c, plan, _kv_rows(q, rows, heads, dim, dev, "q"),
+                                            _kv_rows(out, rows, heads, dim, dev, "out"), heads,
+                                            _kv_rows(k, rows, hk, dim, dev, "k"), _kv_rows(v, rows, hk, dim, dev, "v"), at,
+                                            rows, _kv_stream(stream, dev) or None)
+    if st:
+        raise MMQError(st, "kv_write_rope")
+    return out
+
+
+def kv_weights(num_pages, kv_heads, device="cuda"):
+    """What each cached token has received so far: float32 [num_pages, kv_heads, 64], beside the pages.
+    It need not be cleared, a token's weight starts from 0 in the call that it is new in."""
+    return _torch().empty((num_pages, kv_heads, KV_PAGE), dtype=_torch().float32, device=device)
+
+
+def _kv_weights(w, c, dev, name):
+    if (w.dtype is not _torch_module.float32 or w.shape != (c.num_pages, c.kv_heads, KV_PAGE) or not w.is_contiguous()
+            or w.get_device() != dev):
+        raise ValueError(f"{name} must be a contiguous float32 {[c.num_pages, c.kv_heads, KV_PAGE]} tensor on the "
+                         "cache's device")
+    return w.data_ptr()
+
+
+def kv_attend_weights(q, weights, pages, table, start, length, max_q, max_kv=None, scale=None, window=0, sinks=0,
+                      decay=1.0, out=None, into=None, workspace=None, stream=None):
+    """(kv_attend's result, weights): the softmax weight that each key received, summed over the new
+    rows and the heads of its kv head, is added to decay times what weights (from kv_weights) holds;
+    in place, or into another such tensor."""
+    c, dev = _kv_cache(pages, table, start, length)
+    if q.dim() != 3:
+        raise ValueError(f"q must be [rows, heads, head_dim], got {list(q.shape)}")
+    rows, heads = q.shape[:2]
+    dim = c.head_dim
+    if max_kv is None:
+        max_kv = c.max_pages * KV_PAGE
+    if scale is None:
+        scale = dim ** -0.5
+    # ctypes would drop high bits; larger numbers mean no more than the largest the library takes
+    max_q, max_kv, window, sinks = (min(n, _INT_MAX) for n in (max_q, max_kv, window, sinks))
+    if into is None:
+        into = weights
+    at, to = _kv_weights(weights, c, dev, "weights"), _kv_weights(into, c, dev, "into")
+    rq = _kv_rows(q, rows, heads, dim, dev, "q")
+    if out is None:
+        out = _kv_empty((rows, heads, dim), q.dtype, q.device, stream)
+    ro = _kv_rows(out, rows, heads, dim, dev, "out")
+    need = mmq_kv_attend_weights_workspace_bytes(c, rq.dtype, heads, rows, max_q, max_kv, window, sinks)
+    if workspace is None:
+        workspace = _kv_empty((need,), _torch_module.uint8, q.device, stream)
+    elif workspace.get_device() != dev or not workspace.is_contiguous() or _nbytes(workspace) < need:
+        raise ValueError(f"workspace must be a contiguous CUDA buffer of at least {need} bytes")
+    st = (_lib or load()).mmq_kv_attend_weights(c, rq, ro, heads, rows, max_q, max_kv, scale, window, sinks, at, to, decay,
+                                                workspace.data_ptr(), need, _kv_stream(stream, dev) or None)
+    if st:
+        raise MMQError(st, "kv_attend_weights")
+    return out, into
+
+
+def kv_evict(weights, pages, table, start, length, new_table, keep, first=4, last=64, max_kv=None, new_length=None,
+             kept=None, stream=None):
+    """Moves min(length, keep) tokens of each sequence to the pages of new_table (int32 [batch, new_pages],
+    pages that no sequence uses): per kv head the first and last ones and those with the most weight
+    between them.  Returns (new_length int32 [batch], kept int32 [batch, kv_heads, keep]): kept is the old
+    place of each token, -1 past new_length.  new_length may be length."""
+    c, dev = _kv_cache(pages, table, start, length)
+    torch = _torch_module
+    at = _kv_weights(weights, c, dev, "weights")
+    if (new_table.dtype is not torch.int32 or new_table.dim() != 2 or new_table.shape[0] != c.batch
+            or not new_table.is_contiguous() or new_table.get_device() != dev):
+        raise ValueError(f"new_table must be a contiguous int32 [{c.batch}, new_pages] tensor on the cache's device")
+    if max_kv is None:
+        max_kv = c.max_pages * KV_PAGE
+    max_kv = min(max_kv, _INT_MAX)
+    for n, name in ((keep, "keep"), (first, "first"), (last, "last")):
+        if not 0 <= n <= _INT_MAX:
+            raise ValueError(f"{name} must be a number of tokens, got {n}")
+    if keep < 1 or first + last > keep or keep > new_table.shape[1] * KV_PAGE:
+        raise ValueError(f"of keep = {keep} tokens, first + last = {first + last} are taken, and new_table has room for "
+                         f"{new_table.shape[1] * KV_PAGE}")
+    if new_length is None:
+        new_length = _kv_empty((c.batch,), torch.int32, pages.device, stream)
+    if kept is None:
+        kept = _kv_empty((c.batch, c.kv_heads, keep), torch.int32, pages.device, stream)
+    for x, shape, name in ((new_length, (c.batch,), "new_length"), (kept, (c.batch, c.kv_heads, keep), "kept")):
+        if x.dtype is not torch.int32 or x.shape != shape or not x.is_contiguous() or x.get_device() != dev:
+            raise ValueError(f"{name} must be a contiguous int32 {list(shape)} tensor on the cache's device")
+    st = (_lib or load()).mmq_kv_evict(c, at, new_table.data_ptr(), new_table.shape[1], keep, first, last, max_kv,
+                                       new_length.data_ptr(), kept.data_ptr(), _kv_stream(stream, dev) or None)
+    if st:
+        raise MMQError(st, "kv_evict")
+    return new_length, kept

@@ -281,8 +281,16 @@ struct AttendArgs {
     bool wide;
     float* part;           // nsplit > 1: [nsplit][ntok * heads][D] unnormalised sums
     float2* part_ml;       //             [nsplit][ntok * heads] {reference, sum}
+    float2* stats;         // null, or [ntok * heads] {reference, 1 / sum}, {0, 0} of a row without keys
     WaitCtl wc;
 };
+// What kv_weigh.cu needs of a row to compute its weights again; a row whose sum is no positive
+// number has none.
+__device__ __forceinline__ float2 kv_row_stats(float ref, float sum)
+{
+    const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+    return inv > 0.0f ? make_float2(ref, inv) : make_float2(0.0f, 0.0f);
+}
 
 // The attention's last block (the others have a unit of work each): packed rows that no unit
 // computes become zero, and are reported.  They are those before the first sequence's and past
@@ -304,6 +312,10 @@ __device__ __forceinline__ void kv_clear_others(const AttendArgs& g, long long m
                     for (long long i = lo + threadIdx.x; i < hi; i += blockDim.x)
                         g.part_ml[(split * n + i / g.group) * g.heads + head + i % g.group] = make_float2(-INFINITY, 0.0f);
                 continue;
+            }
+            if (g.stats) {
+                for (long long i = lo + threadIdx.x; i < hi; i += blockDim.x)
+                    g.stats[i / g.group * g.heads + head + i % g.group] = make_float2(0.0f, 0.0f);
             }
             for (long long i = lo * FOURS + threadIdx.x; i < hi * FOURS; i += blockDim.x) {
                 const long long row = i / FOURS;
@@ -351,5 +363,34 @@ AttendPlan plan_attend(int dtype, int heads, int kv_heads, int dim, int batch, i
 cudaError_t launch_kv_step(const AttendArgs& a, int dim, int dtype, cudaStream_t s);
 cudaError_t launch_kv_prompt(const AttendArgs& a, int dim, int dtype, cudaStream_t s);
 cudaError_t launch_kv_join(const AttendArgs& a, int dim, int dtype, cudaStream_t s);
+
+// The weight that each key receives: [page][kv head][slot].
+struct WeighArgs {
+    AttendArgs a;          // stats written
+    const float* in;
+    float* out;
+    float decay;
+    int parts;             // CTAs that share a sequence's kv head
+};
+cudaError_t launch_kv_weigh(const WeighArgs& a, int dim, int dtype, int max_kv, cudaStream_t s);
+
+struct RopeView;
+cudaError_t launch_rope(const KvRows& x, const KvRows& out, const int* pos, const RopeView& r, int dtype, int heads,
+                        int dim, int ntok, bool wide, cudaStream_t s);
+cudaError_t launch_kv_write_rope(const KvView& c, int dim, int dtype, const KvRows& q, const KvRows& q_out, int heads,
+                                 const KvRows& k, const KvRows& v, const int* pos, const RopeView& r, bool wide_q,
+                                 bool wide_kv, int ntok, cudaStream_t s);
+
+struct EvictArgs {
+    KvView c;
+    float* weights;        // [page][kv head][slot]
+    const int* new_table;  // [batch][new_pages]
+    int* new_length;
+    int* kept;             // [batch][kv head][keep]
+    int new_pages, keep, first, last;
+    int cluster;           // CTAs of a sequence's kv head in the choice
+    int held;              // tokens that each keeps in shared memory
+};
+cudaError_t launch_kv_evict(const EvictArgs& a, int dim, int max_kv, cudaStream_t s);
 
 }  // namespace mmq

@@ -1,9 +1,13 @@
-// kv_api.cu -- entry points of the 4-bit key/value cache and the attention over it.
+// kv_api.cu -- entry points of the 4-bit key/value cache, of the attention over it and the
+// weights it gives, of eviction by them, and of rotary positions.
 //
 // As in api.cu, arguments are checked on the host before any CUDA call; what only the
 // device knows (page ids, lengths) is checked by the kernels.
+#include <cmath>
+
 #include "api.h"
 #include "kv.cuh"
+#include "rope.cuh"
 
 namespace mmq {
 
@@ -215,6 +219,101 @@ AttendPlan plan(const mmq_kv_cache* c, int dtype, int heads, int ntok, int max_q
                             max_kv < 1 ? 1 : max_kv, c->max_pages, window, sinks);
 }
 
+// {reference, 1 / sum} of each row of an attention whose weights are wanted.
+size_t stats_bytes(int ntok, int heads)
+{
+    return (static_cast<size_t>(ntok) * static_cast<size_t>(heads) * sizeof(float2) + 15) / 16 * 16;
+}
+
+struct Weights {
+    const float* in;
+    float* out;
+    float decay;
+};
+
+mmq_status attend(const mmq_kv_cache* c, const mmq_rows* q, const mmq_rows* out, int heads, int ntok, int max_q,
+                  int max_kv, float scale, int window, int sinks, const Weights* weights,
+                  void* workspace, size_t workspace_bytes, mmq_stream_t s)
+{
+    mmq_status st = check_cache(c);
+    if (st != MMQ_OK)
+        return st;
+    if (!q || !out)
+        return MMQ_ERR_ARG;
+    if ((st = check_attend(c, q->dtype, heads, ntok, max_q, max_kv, window, sinks)) != MMQ_OK ||
+        (st = check_rows(q, ntok, heads, c->head_dim, false)) != MMQ_OK ||
+        (st = check_rows(out, ntok, heads, c->head_dim, true)) != MMQ_OK)
+        return st;
+    // a positive normal number whose log2(e) multiple is finite
+    if (q->dtype != out->dtype || !(scale >= 1.17549435e-38f && scale <= 1e38f))
+        return MMQ_ERR_ARG;
+    if (ntok == 0)
+        return MMQ_OK;
+    const AttendPlan p = plan(c, q->dtype, heads, ntok, max_q, max_kv, window, sinks);
+    const size_t need = p.part_bytes + p.ml_bytes + (weights ? stats_bytes(ntok, heads) : 0);
+    if (need > 0) {
+        if (!workspace || workspace_bytes < need)
+            return MMQ_ERR_ARG;
+        if (!aligned(workspace, 16))
+            return MMQ_ERR_ALIGN;
+    }
+    // the grid: the units and a block (a cluster) for the rows of none
+    if ((static_cast<long long>(p.nsplit) * p.row_tiles * c->kv_heads * (p.kernel == 0 ? c->batch : 1) + 1) * p.cluster >
+            0x7fffffffll ||
+        static_cast<long long>(ntok) * heads > 0x7fffffffll)
+        return MMQ_ERR_SHAPE;
+    if ((st = mmq::check_device()) != MMQ_OK)
+        return st;
+    mmq::AttendArgs a = {};
+    if ((st = view(c, &a.c)) != MMQ_OK)
+        return st;
+    a.q = rows(q);
+    a.out = rows(out);
+    a.heads = heads;
+    a.group = heads / c->kv_heads;
+    a.ntok = ntok;
+    a.scale_log2 = scale * 1.4426950408889634f;
+    // positions are below 64 MMQ_KV_MAX_PAGES = 2^30, where larger windows and sinks change nothing
+    constexpr int FAR = 1 << 30;
+    a.window = window < FAR ? window : FAR;
+    a.sinks = window == 0 ? 0 : sinks < FAR ? sinks : FAR;
+    a.tile_rows = p.tile_rows;
+    a.row_tiles = p.row_tiles;
+    a.nsplit = p.nsplit;
+    a.part_pages = p.part_pages;
+    a.cluster = p.cluster;
+    const int four = q->dtype == MMQ_F32 ? 16 : 8;   // bytes of four elements
+    a.wide = wide(q, four) && wide(out, four);
+    a.part = static_cast<float*>(workspace);
+    a.part_ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(workspace) + p.part_bytes);
+    if (weights)
+        a.stats = reinterpret_cast<float2*>(static_cast<uint8_t*>(workspace) + p.part_bytes + p.ml_bytes);
+    a.wc = {a.c.bad - 1, mmq::WAIT_LIMIT_NS, -1};
+    bool injected = false;
+    if (p.cluster == 1 && mmq::take_wait_ctl(&a.wc, &injected) != cudaSuccess)   // a cluster barrier has no time limit
+        return MMQ_ERR_CUDA;
+    const auto launch = p.kernel == 0 ? mmq::launch_kv_step : mmq::launch_kv_prompt;
+    cudaError_t e = launch(a, c->head_dim, q->dtype, reinterpret_cast<cudaStream_t>(s));
+    if (e == cudaSuccess && p.nsplit > 1)
+        e = mmq::launch_kv_join(a, c->head_dim, q->dtype, reinterpret_cast<cudaStream_t>(s));
+    if (e == cudaSuccess && weights)
+        e = mmq::launch_kv_weigh({a, weights->in, weights->out, weights->decay, 1}, c->head_dim, q->dtype, max_kv,
+                                 reinterpret_cast<cudaStream_t>(s));
+    return mmq::from_cuda(e);
+}
+
+mmq_status check_plan(const mmq_rope_plan* p, int head_dim, mmq::RopeView* r)
+{
+    if (!p || !p->turns || (p->interleaved != 0 && p->interleaved != 1) || !std::isfinite(p->magnitude))
+        return MMQ_ERR_ARG;
+    if (p->rot_dim < 2 || p->rot_dim % 2 != 0 || p->rot_dim > head_dim)
+        return MMQ_ERR_SHAPE;
+    if (!aligned(p->turns, 8))
+        return MMQ_ERR_ALIGN;
+    *r = {reinterpret_cast<const unsigned long long*>(p->turns), p->rot_dim, p->interleaved != 0, p->magnitude};
+    return MMQ_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -259,65 +358,197 @@ mmq_status mmq_kv_attend(const mmq_kv_cache* c, const mmq_rows* q, const mmq_row
                          int max_kv, float scale, int window, int sinks, void* workspace, size_t workspace_bytes,
                          mmq_stream_t s)
 {
+    return attend(c, q, out, heads, ntok, max_q, max_kv, scale, window, sinks, nullptr, workspace, workspace_bytes, s);
+}
+
+mmq_status mmq_kv_attend_weights_workspace_bytes(const mmq_kv_cache* c, int dtype, int heads, int ntok, int max_q,
+                                                 int max_kv, int window, int sinks, size_t* bytes)
+{
+    const mmq_status st = mmq_kv_attend_workspace_bytes(c, dtype, heads, ntok, max_q, max_kv, window, sinks, bytes);
+    if (st == MMQ_OK)
+        *bytes += stats_bytes(ntok, heads);
+    return st;
+}
+
+mmq_status mmq_kv_attend_weights(const mmq_kv_cache* c, const mmq_rows* q, const mmq_rows* out, int heads, int ntok,
+                                 int max_q, int max_kv, float scale, int window, int sinks, const float* weights,
+                                 float* new_weights, float decay, void* workspace, size_t workspace_bytes,
+                                 mmq_stream_t s)
+{
+    if (!weights || !new_weights || !(decay >= 0.0f && decay <= 1.0f))
+        return MMQ_ERR_ARG;
+    if (!aligned(weights, 16) || !aligned(new_weights, 16))
+        return MMQ_ERR_ALIGN;
+    const Weights w = {weights, new_weights, decay};
+    return attend(c, q, out, heads, ntok, max_q, max_kv, scale, window, sinks, &w, workspace, workspace_bytes, s);
+}
+
+mmq_status mmq_kv_evict(const mmq_kv_cache* c, float* weights, const int32_t* new_table, int new_pages, int keep,
+                        int first, int last, int max_kv, int32_t* new_length, int32_t* kept, mmq_stream_t s)
+{
     mmq_status st = check_cache(c);
     if (st != MMQ_OK)
         return st;
-    if (!q || !out)
+    if (!weights || !new_table || !new_length || !kept || first < 0 || last < 0 || max_kv < 0)
         return MMQ_ERR_ARG;
-    if ((st = check_attend(c, q->dtype, heads, ntok, max_q, max_kv, window, sinks)) != MMQ_OK ||
-        (st = check_rows(q, ntok, heads, c->head_dim, false)) != MMQ_OK ||
-        (st = check_rows(out, ntok, heads, c->head_dim, true)) != MMQ_OK)
-        return st;
-    // a positive normal number whose log2(e) multiple is finite
-    if (q->dtype != out->dtype || !(scale >= 1.17549435e-38f && scale <= 1e38f))
-        return MMQ_ERR_ARG;
-    if (ntok == 0)
-        return MMQ_OK;
-    const AttendPlan p = plan(c, q->dtype, heads, ntok, max_q, max_kv, window, sinks);
-    if (p.part_bytes + p.ml_bytes > 0) {
-        if (!workspace || workspace_bytes < p.part_bytes + p.ml_bytes)
-            return MMQ_ERR_ARG;
-        if (!aligned(workspace, 16))
-            return MMQ_ERR_ALIGN;
-    }
-    // the grid: the units and a block (a cluster) for the rows of none
-    if ((static_cast<long long>(p.nsplit) * p.row_tiles * c->kv_heads * (p.kernel == 0 ? c->batch : 1) + 1) * p.cluster >
-            0x7fffffffll ||
-        static_cast<long long>(ntok) * heads > 0x7fffffffll)
+    if (keep < 1 || new_pages < 1 || new_pages > MMQ_KV_MAX_PAGES ||
+        static_cast<long long>(new_pages) * mmq::KV_PAGE < keep || static_cast<long long>(first) + last > keep)
+        return MMQ_ERR_SHAPE;
+    if (!aligned(weights, 16) || !aligned(new_table, 4) || !aligned(new_length, 4) || !aligned(kept, 4))
+        return MMQ_ERR_ALIGN;
+    // grids: CTAs of the choice, new pages of the move
+    const long long units = static_cast<long long>(c->batch) * c->kv_heads;
+    if (units * ((keep + mmq::KV_PAGE - 1) / mmq::KV_PAGE) > 0x7fffffffll)
         return MMQ_ERR_SHAPE;
     if ((st = mmq::check_device()) != MMQ_OK)
         return st;
-    mmq::AttendArgs a = {};
+    mmq::EvictArgs a = {};
     if ((st = view(c, &a.c)) != MMQ_OK)
         return st;
-    a.q = rows(q);
-    a.out = rows(out);
-    a.heads = heads;
-    a.group = heads / c->kv_heads;
-    a.ntok = ntok;
-    a.scale_log2 = scale * 1.4426950408889634f;
-    // positions are below 64 MMQ_KV_MAX_PAGES = 2^30, where larger windows and sinks change nothing
-    constexpr int FAR = 1 << 30;
-    a.window = window < FAR ? window : FAR;
-    a.sinks = window == 0 ? 0 : sinks < FAR ? sinks : FAR;
-    a.tile_rows = p.tile_rows;
-    a.row_tiles = p.row_tiles;
-    a.nsplit = p.nsplit;
-    a.part_pages = p.part_pages;
-    a.cluster = p.cluster;
-    const int four = q->dtype == MMQ_F32 ? 16 : 8;   // bytes of four elements
-    a.wide = wide(q, four) && wide(out, four);
-    a.part = static_cast<float*>(workspace);
-    a.part_ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(workspace) + p.part_bytes);
-    a.wc = {a.c.bad - 1, mmq::WAIT_LIMIT_NS, -1};
-    bool injected = false;
-    if (p.cluster == 1 && mmq::take_wait_ctl(&a.wc, &injected) != cudaSuccess)   // a cluster barrier has no time limit
-        return MMQ_ERR_CUDA;
-    const auto launch = p.kernel == 0 ? mmq::launch_kv_step : mmq::launch_kv_prompt;
-    cudaError_t e = launch(a, c->head_dim, q->dtype, reinterpret_cast<cudaStream_t>(s));
-    if (e == cudaSuccess && p.nsplit > 1)
-        e = mmq::launch_kv_join(a, c->head_dim, q->dtype, reinterpret_cast<cudaStream_t>(s));
-    return mmq::from_cuda(e);
+    a.weights = weights;
+    a.new_table = new_table;
+    a.new_length = new_length;
+    a.kept = kept;
+    a.new_pages = new_pages;
+    a.keep = keep;
+    a.first = first;
+    a.last = last;
+    return mmq::from_cuda(mmq::launch_kv_evict(a, c->head_dim, max_kv, reinterpret_cast<cudaStream_t>(s)));
+}
+
+mmq_status mmq_rope_frequencies(mmq_rope_scaling scaling, int rot_dim, double base, double factor, double original,
+                                double* freq, float* magnitude)
+{
+    if (!freq || !magnitude || !(base > 1.0 && std::isfinite(base)))
+        return MMQ_ERR_ARG;
+    if (rot_dim < 2 || rot_dim > MMQ_ROPE_MAX_DIM || rot_dim % 2 != 0)
+        return MMQ_ERR_SHAPE;
+    if (scaling < MMQ_ROPE_PLAIN || scaling > MMQ_ROPE_BANDS)
+        return MMQ_ERR_ARG;
+    if (scaling != MMQ_ROPE_PLAIN && !(factor >= 1.0 && std::isfinite(factor)))
+        return MMQ_ERR_ARG;
+    if (scaling >= MMQ_ROPE_YARN && !(original >= 1.0 && std::isfinite(original)))
+        return MMQ_ERR_ARG;
+    constexpr double PI = 3.14159265358979323846;
+    const int half = rot_dim / 2;
+    *magnitude = 1.0f;
+    if (scaling == MMQ_ROPE_NTK && rot_dim > 2) {
+        base *= std::pow(factor, rot_dim / (rot_dim - 2.0));
+        if (!std::isfinite(base))
+            return MMQ_ERR_ARG;
+    }
+    // YaRN's ramp between the pairs that make 32 turns and 1 turn in the original context
+    double lo = 0.0, hi = 0.0;
+    if (scaling == MMQ_ROPE_YARN) {
+        const auto pair = [&](double turns) {
+            return rot_dim * std::log(original / (turns * 2.0 * PI)) / (2.0 * std::log(base));
+        };
+        const auto limit = [&](double d) { return d < 0.0 ? 0.0 : d > rot_dim - 1.0 ? rot_dim - 1.0 : d; };
+        lo = limit(std::floor(pair(32.0)));
+        hi = limit(std::ceil(pair(1.0)));
+        *magnitude = static_cast<float>(0.1 * std::log(factor) + 1.0);
+    }
+    for (int i = 0; i < half; ++i) {
+        double f = std::pow(base, -2.0 * i / rot_dim);
+        if (scaling == MMQ_ROPE_LINEAR) {
+            f /= factor;
+        } else if (scaling == MMQ_ROPE_YARN) {
+            const double width = hi - lo > 0.001 ? hi - lo : 0.001;
+            double ramp = (i - lo) / width;
+            ramp = ramp < 0.0 ? 0.0 : ramp > 1.0 ? 1.0 : ramp;
+            f = f / factor * ramp + f * (1.0 - ramp);
+        } else if (scaling == MMQ_ROPE_BANDS) {
+            double near = (original * f / (2.0 * PI) - 1.0) / 3.0;
+            near = near < 0.0 ? 0.0 : near > 1.0 ? 1.0 : near;
+            f = (1.0 - near) * f / factor + near * f;
+        }
+        freq[i] = f;
+    }
+    return MMQ_OK;
+}
+
+mmq_status mmq_rope_turns(const double* freq, int n, uint64_t* turns)
+{
+    if (!freq || !turns)
+        return MMQ_ERR_ARG;
+    if (n < 1 || n > MMQ_ROPE_MAX_DIM / 2)
+        return MMQ_ERR_SHAPE;
+    for (int i = 0; i < n; ++i)
+        if (!(std::fabs(freq[i]) <= 1e6))
+            return MMQ_ERR_ARG;
+    // 1 / (2 pi) in two parts; a product's two parts are below 2^18, its error below 2^-88
+    constexpr double HI = 0.15915494309189535, LO = -9.839338337591243e-18;
+    for (int i = 0; i < n; ++i) {
+        const double f = std::fabs(freq[i]), p = f * HI, q = std::fma(f, HI, -p) + f * LO;
+        const double whole = std::ldexp(p - std::floor(p), 64);   // below 2^64; cut to a whole number
+        const double rest = whole - std::floor(whole) + std::ldexp(q, 64);
+        const uint64_t w = static_cast<uint64_t>(whole) + static_cast<uint64_t>(static_cast<int64_t>(std::nearbyint(rest)));
+        turns[i] = freq[i] < 0.0 ? ~w + 1u : w;
+    }
+    return MMQ_OK;
+}
+
+mmq_status mmq_rope(const mmq_rope_plan* p, const mmq_rows* x, const mmq_rows* out, const int32_t* pos, int heads,
+                    int head_dim, int ntok, mmq_stream_t s)
+{
+    mmq::RopeView r;
+    mmq_status st = check_plan(p, head_dim, &r);
+    if (st != MMQ_OK)
+        return st;
+    if (!pos && ntok > 0)
+        return MMQ_ERR_ARG;
+    if (heads < 1 || heads > MMQ_KV_MAX_HEADS || head_dim > MMQ_ROPE_MAX_DIM || ntok < 0 || ntok > MMQ_MAX_M)
+        return MMQ_ERR_SHAPE;
+    if ((st = check_rows(x, ntok, heads, head_dim, false)) != MMQ_OK ||
+        (st = check_rows(out, ntok, heads, head_dim, true)) != MMQ_OK)
+        return st;
+    if (x->dtype != out->dtype)
+        return MMQ_ERR_ARG;
+    if (!aligned(pos, 4))
+        return MMQ_ERR_ALIGN;
+    if (ntok == 0)
+        return MMQ_OK;
+    if ((st = mmq::check_device()) != MMQ_OK)
+        return st;
+    return mmq::from_cuda(mmq::launch_rope(rows(x), rows(out), pos, r, x->dtype, heads, head_dim, ntok,
+                                           wide(x, 16) && wide(out, 16), reinterpret_cast<cudaStream_t>(s)));
+}
+
+mmq_status mmq_kv_write_rope(const mmq_kv_cache* c, const mmq_rope_plan* p, const mmq_rows* q, const mmq_rows* q_out,
+                             int heads, const mmq_rows* k, const mmq_rows* v, const int32_t* pos, int ntok,
+                             mmq_stream_t s)
+{
+    mmq_status st = check_cache(c);
+    if (st != MMQ_OK)
+        return st;
+    mmq::RopeView r;
+    if ((st = check_plan(p, c->head_dim, &r)) != MMQ_OK)
+        return st;
+    if (!pos && ntok > 0)
+        return MMQ_ERR_ARG;
+    if (heads < 1 || heads > MMQ_KV_MAX_HEADS || ntok < 0 || ntok > MMQ_MAX_M)
+        return MMQ_ERR_SHAPE;
+    if ((st = check_rows(q, ntok, heads, c->head_dim, false)) != MMQ_OK ||
+        (st = check_rows(q_out, ntok, heads, c->head_dim, true)) != MMQ_OK)
+        return st;
+    for (const mmq_rows* x : {k, v})
+        if ((st = check_rows(x, ntok, c->kv_heads, c->head_dim, false)) != MMQ_OK)
+            return st;
+    if (q->dtype != q_out->dtype || q->dtype != k->dtype || k->dtype != v->dtype)
+        return MMQ_ERR_ARG;
+    if (!aligned(pos, 4))
+        return MMQ_ERR_ALIGN;
+    if (ntok == 0)
+        return MMQ_OK;
+    if ((st = mmq::check_device()) != MMQ_OK)
+        return st;
+    mmq::KvView cv;
+    if ((st = view(c, &cv)) != MMQ_OK)
+        return st;
+    return mmq::from_cuda(mmq::launch_kv_write_rope(cv, c->head_dim, q->dtype, rows(q), rows(q_out), heads, rows(k),
+                                                    rows(v), pos, r, wide(q, 16) && wide(q_out, 16),
+                                                    wide(k, 16) && wide(v, 16), ntok,
+                                                    reinterpret_cast<cudaStream_t>(s)));
 }
 
 }  // extern "C"

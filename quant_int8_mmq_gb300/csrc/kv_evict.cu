@@ -1,0 +1,343 @@
+// kv_evict.cu -- fewer tokens in the 4-bit cache: which stay, and their way to other pages.
+//
+// Of a sequence of n > keep tokens stay, per kv head, the first ones, the last ones, and of
+// the rest the m with the largest weights (ties: the lower position).  The m-th largest weight
+// T is found by a radix search: weights as unsigned numbers of the same order, three
+// histograms (11, 11 and 10 bits) of those that agree with T in the bits known so far.  A token
+// then stays if its weight is above T, or equal and among the first of those that equal it, and
+// its new place is the number of tokens before it that stay.
+//
+// kv_choose_kernel: a CTA, or a cluster of them for few long sequences, per (sequence, kv
+// head), its weights in shared memory.  kv_move_kernel: a CTA per new page and kv head gathers
+// its 64 tokens' codes and scales, 16 bytes a thread; nothing is decoded, the two tokens that
+// share a word of value codes are put together from the halves of theirs.
+#include <type_traits>
+
+#include "kv.cuh"
+
+namespace mmq {
+namespace {
+
+constexpr int CHOOSE_WARPS = 16, CHOOSE = CHOOSE_WARPS * 32;
+constexpr int BINS = 2048;
+constexpr int ROUNDS = 3;
+
+// Unsigned numbers in the order of f32 ones; -0 as 0, no number below all others.
+__device__ __forceinline__ uint32_t order_of(float w)
+{
+    const uint32_t u = __float_as_uint(w + 0.0f);
+    return w != w ? 0u : u >> 31 ? ~u : u | 0x80000000u;
+}
+
+__global__ void __launch_bounds__(CHOOSE) kv_choose_kernel(const EvictArgs g)
+{
+    extern __shared__ uint32_t keys[];                 // [g.held] of this CTA's tokens
+    __shared__ uint32_t hist[BINS];
+    __shared__ uint32_t warp_sum[CHOOSE_WARPS];
+    __shared__ uint2 counts[CHOOSE_WARPS];             // tokens above T, and equal to it
+    __shared__ uint2 mine;                             // of the CTA
+    __shared__ uint32_t found[2];                      // bin, tokens above it
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    grid_dep_wait();
+    grid_dep_launch();
+    const int unit = blockIdx.x / g.cluster, rank = blockIdx.x % g.cluster;
+    const int b = unit / g.c.kv_heads, head = unit % g.c.kv_heads;
+    const int room = g.c.max_pages * KV_PAGE;
+    const int n = min(max(g.c.length[b], 0), room);
+    if (threadIdx.x == 0 && n != g.c.length[b])
+        *g.c.bad = 1u;
+    int* kept = g.kept + (static_cast<size_t>(b) * g.c.kv_heads + head) * g.keep;
+    const int stay = min(n, g.keep);
+    for (int i = stay + rank * CHOOSE + static_cast<int>(threadIdx.x); i < g.keep; i += g.cluster * CHOOSE)
+        kept[i] = -1;
+    if (n <= g.keep) {
+        for (int i = rank * CHOOSE + threadIdx.x; i < n; i += g.cluster * CHOOSE)
+            kept[i] = i;
+        return;
+    }
+
+    // this CTA's tokens: whole pages, those past what it holds are read again each time
+    const int pages = (n + KV_PAGE - 1) / KV_PAGE, share = (pages + g.cluster - 1) / g.cluster;
+    const int lo = min(rank * share * KV_PAGE, n), hi = min(lo + share * KV_PAGE, n), size = hi - lo;
+    const int* table = g.c.table + static_cast<size_t>(b) * g.c.max_pages;
+    auto read = [&](int j) {   // the order of token lo + j
+        const int page = table[(lo + j) / KV_PAGE];
+        if (page < 0 || page >= g.c.num_pages) {
+            *g.c.bad = 1u;
+            return 0u;
+        }
+        return order_of(g.weights[(static_cast<size_t>(page) * g.c.kv_heads + head) * KV_PAGE + (lo + j) % KV_PAGE]);
+    };
+#pragma unroll 8
+    for (int j = threadIdx.x; j < min(size, g.held); j += CHOOSE)
+        keys[j] = read(j);
+    __syncthreads();
+    auto key = [&](int j) { return j < g.held ? keys[j] : read(j); };
+    // tokens [from, to) compete for `need` places
+    const int from = g.first, to = n - g.last;
+    uint32_t need = static_cast<uint32_t>(g.keep - g.first - g.last);
+    uint32_t prefix = 0, known = 0;
+    for (int round = 0; need > 0 && round < ROUNDS; ++round) {
+        const int shift = round == 0 ? 21 : round == 1 ? 10 : 0;
+        const uint32_t low = round == 2 ? 1023u : 2047u;
+        for (int i = threadIdx.x; i < BINS; i += CHOOSE)
+            hist[i] = 0;
+        __syncthreads();
+        for (int j0 = 0; j0 < size; j0 += CHOOSE) {
+            const int j = j0 + threadIdx.x;
+            uint32_t bin = BINS;
+            if (j < size && lo + j >= from && lo + j < to) {
+                const uint32_t k = key(j);
+                if ((k & known) == prefix)
+                    bin = k >> shift & low;
+            }
+            // equal weights are common: a warp adds them up first
+            const uint32_t same = __match_any_sync(0xffffffffu, bin);
+            if (bin < BINS && (same & ((1u << lane) - 1)) == 0)
+                atomicAdd(hist + bin, __popc(same));
+        }
+        if (g.cluster > 1)
+            cluster_sync();
+        else
+            __syncthreads();
+        // the bin that holds the need-th largest: thread i has the i-th four bins from the top
+        constexpr int EACH = BINS / CHOOSE;
+        uint32_t c[EACH], sum = 0;
+#pragma unroll
+        for (int i = 0; i < EACH; ++i) {
+            const int bin = BINS - 1 - (EACH * static_cast<int>(threadIdx.x) + i);
+            c[i] = hist[bin];
+            if (g.cluster > 1) {
+                c[i] = 0;
+                const uint32_t at = smem_u32(hist + bin);
+                for (int r = 0; r < g.cluster; ++r)
+                    c[i] += ld_cluster_u32(cluster_map(at, r));
+            }
+            sum += c[i];
+        }
+        uint32_t before = sum;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const uint32_t v = __shfl_up_sync(0xffffffffu, before, d);
+            before += lane >= d ? v : 0;
+        }
+        if (lane == 31)
+            warp_sum[warp] = before;
+        __syncthreads();
+        before -= sum;
+        for (int w = 0; w < warp; ++w)
+            before += warp_sum[w];
+#pragma unroll
+        for (int i = 0; i < EACH; ++i) {
+            if (before < need && need <= before + c[i]) {
+                found[0] = BINS - 1 - (EACH * threadIdx.x + i);
+                found[1] = before;
+            }
+            before += c[i];
+        }
+        if (g.cluster > 1)
+            cluster_sync();   // everyone has read this CTA's histogram
+        else
+            __syncthreads();
+        prefix |= found[0] << shift;
+        known |= low << shift;
+        need -= found[1];
+        __syncthreads();
+    }
+
+    // `need` of the tokens that equal T = prefix stay (none where nobody competes)
+    const bool compete = g.keep > g.first + g.last;
+    const int part = ((size + CHOOSE_WARPS - 1) / CHOOSE_WARPS + 31) / 32 * 32;
+    const int j0 = min(warp * part, size), j1 = min(j0 + part, size);
+    auto look = [&](int j, uint32_t& above, uint32_t& equal) {
+        bool a = false, e = false;
+        if (j < j1) {
+            const int i = lo + j;
+            if (i < from || i >= to) {
+                a = true;
+            } else if (compete) {
+                const uint32_t k = key(j);
+                a = k > prefix;
+                e = k == prefix;
+            }
+        }
+        above = __ballot_sync(0xffffffffu, a);
+        equal = __ballot_sync(0xffffffffu, e);
+    };
+    uint2 sum = make_uint2(0, 0);
+    for (int j = j0; j < j1; j += 32) {
+        uint32_t a, e;
+        look(j + lane, a, e);
+        sum.x += __popc(a);
+        sum.y += __popc(e);
+    }
+    if (lane == 0)
+        counts[warp] = sum;
+    __syncthreads();
+    uint2 before = make_uint2(0, 0);
+    for (int w = 0; w < CHOOSE_WARPS; ++w) {
+        if (w == warp)
+            sum = before;
+        before.x += counts[w].x;
+        before.y += counts[w].y;
+    }
+    if (g.cluster > 1) {
+        if (threadIdx.x == 0)
+            mine = before;
+        cluster_sync();
+        const uint32_t at = smem_u32(&mine);
+        for (int r = 0; r < rank; ++r) {
+            sum.x += ld_cluster_u32(cluster_map(at, r));
+            sum.y += ld_cluster_u32(cluster_map(at + 4, r));
+        }
+    }
+    const uint32_t below = (1u << lane) - 1;
+    for (int j = j0; j < j1; j += 32) {
+        uint32_t a, e;
+        look(j + lane, a, e);
+        const uint32_t na = sum.x + __popc(a & below), ne = sum.y + __popc(e & below);
+        if ((a >> lane & 1u) || ((e >> lane & 1u) && ne < need))
+            kept[na + min(ne, need)] = lo + j + lane;
+        sum.x += __popc(a);
+        sum.y += __popc(e);
+    }
+    if (g.cluster > 1)
+        cluster_sync();   // the others have read this CTA's counts
+}
+
+template <int D>
+__global__ void __launch_bounds__(2 * D) kv_move_kernel(const EvictArgs g)
+{
+    using P = Piece<D>;
+    __shared__ const uint8_t* from[KV_PAGE];   // pieces of the tokens, null: none
+    __shared__ uint8_t slots[KV_PAGE];
+    grid_dep_wait();
+    const int new_pages = (g.keep + KV_PAGE - 1) / KV_PAGE;
+    int id = blockIdx.x;
+    const int page = id % new_pages;
+    id /= new_pages;
+    const int head = id % g.c.kv_heads, b = id / g.c.kv_heads;
+    const int tid = threadIdx.x;
+    if (page == 0 && head == 0 && tid == 0)
+        g.new_length[b] = min(min(max(g.c.length[b], 0), g.c.max_pages * KV_PAGE), g.keep);
+    const int i = page * KV_PAGE + tid;
+    int old = -1;
+    if (tid < KV_PAGE && i < g.keep)
+        old = g.kept[(static_cast<size_t>(b) * g.c.kv_heads + head) * g.keep + i];
+    const int count = __syncthreads_count(old >= 0);
+    if (count == 0)
+        return;
+    const int to = g.new_table[static_cast<size_t>(b) * g.new_pages + page];
+    const bool there = to >= 0 && to < g.c.num_pages;
+    if (!there && tid == 0)
+        *g.c.bad = 1u;
+    const size_t to_piece = (static_cast<size_t>(there ? to : 0) * g.c.kv_heads + head);
+    if (old >= 0) {
+        const int p = g.c.table[static_cast<size_t>(b) * g.c.max_pages + old / KV_PAGE];
+        const bool held = p >= 0 && p < g.c.num_pages;
+        const size_t piece = static_cast<size_t>(held ? p : 0) * g.c.kv_heads + head;
+        from[tid] = held ? g.c.pages + piece * P::BYTES : nullptr;
+        slots[tid] = static_cast<uint8_t>(old % KV_PAGE);
+        if (!held)
+            *g.c.bad = 1u;
+        if (there)
+            g.weights[to_piece * KV_PAGE + tid] = held ? g.weights[piece * KV_PAGE + old % KV_PAGE] : 0.0f;
+    } else if (tid < KV_PAGE) {
+        from[tid] = nullptr;
+        slots[tid] = 0;
+    }
+    __syncthreads();
+    if (!there)
+        return;
+    uint8_t* dst = g.c.pages + to_piece * P::BYTES;
+    const uint4 none = make_uint4(0, 0, 0, 0);
+    {   // a key's group
+        const int t = tid / P::NG, gr = tid % P::NG;
+        if (t < count)
+            *reinterpret_cast<uint4*>(dst + P::k_chunk(t, gr)) =
+                from[t] ? *reinterpret_cast<const uint4*>(from[t] + P::k_chunk(slots[t], gr)) : none;
+    }
+    {   // 16 values of two tokens
+        const int p = tid / (D / 16), a = tid % (D / 16);
+        const int s0 = slots[2 * p], s1 = slots[2 * p + 1];
+        const uint8_t *f0 = from[2 * p], *f1 = from[2 * p + 1];
+        const uint4 x = f0 ? *reinterpret_cast<const uint4*>(f0 + P::v_chunk(s0 / 2, a)) : none;
+        const uint4 y = f1 ? *reinterpret_cast<const uint4*>(f1 + P::v_chunk(s1 / 2, a)) : none;
+        const uint32_t pick = (s0 & 1 ? 0x32u : 0x10u) | (s1 & 1 ? 0x7600u : 0x5400u);
+        const uint4 z = make_uint4(__byte_perm(x.x, y.x, pick), __byte_perm(x.y, y.y, pick), __byte_perm(x.z, y.z, pick),
+                                   __byte_perm(x.w, y.w, pick));
+        uint8_t* at = dst + P::v_chunk(p, a);
+        // the pair's scales, one word of the two tokens' per group
+        const bool scales = a % 2 == 0;
+        const int gr = a / 2;
+        uint32_t sx = 0, sy = 0;
+        if (scales) {
+            sx = f0 ? *reinterpret_cast<const uint32_t*>(f0 + P::v_scale(s0 / 2, gr)) : 0u;
+            sy = f1 ? *reinterpret_cast<const uint32_t*>(f1 + P::v_scale(s1 / 2, gr)) : 0u;
+        }
+        const uint32_t sz = __byte_perm(sx, sy, pick);
+        if (2 * p + 1 < count) {
+            *reinterpret_cast<uint4*>(at) = z;
+            if (scales)
+                *reinterpret_cast<uint32_t*>(dst + P::v_scale(p, gr)) = sz;
+        } else if (2 * p < count) {   // the other token's halves stay as they are
+            const uint32_t w[4] = {z.x, z.y, z.z, z.w};
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+                *reinterpret_cast<uint16_t*>(at + 4 * u) = static_cast<uint16_t>(w[u]);
+            if (scales)
+                *reinterpret_cast<uint16_t*>(dst + P::v_scale(p, gr)) = static_cast<uint16_t>(sz);
+        }
+    }
+    if (tid < count) {   // a key's scales
+        using W = typename std::conditional<D == 128, uint2, uint32_t>::type;
+        W s = {};
+        if (from[tid])
+            s = *reinterpret_cast<const W*>(from[tid] + P::k_scale(slots[tid], 0));
+        *reinterpret_cast<W*>(dst + P::k_scale(tid, 0)) = s;
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_kv_evict(const EvictArgs& args, int dim, int max_kv, cudaStream_t s)
+{
+    EvictArgs a = args;
+    const long long room = static_cast<long long>(a.c.max_pages) * KV_PAGE;
+    const long long most = max_kv < room ? max_kv : room;
+    const long long units = static_cast<long long>(a.c.batch) * a.c.kv_heads;
+    // a cluster while the chip is not full and a CTA keeps 2048 tokens
+    a.cluster = 1;
+    while (a.cluster < KV_MAX_CLUSTER && units * a.cluster * 2 <= 2 * 152 && most > 2048ll * a.cluster)
+        a.cluster *= 2;
+    constexpr int MOST = 48 * 1024;   // tokens in shared memory
+    const long long share = (most / KV_PAGE / a.cluster + 2) * KV_PAGE;
+    a.held = static_cast<int>(share < MOST ? share : MOST);
+    static std::atomic<uint64_t> done{0};
+    cudaError_t e = kv_allow_smem(kv_choose_kernel, MOST * 4, &done);
+    if (e != cudaSuccess)
+        return e;
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = static_cast<unsigned int>(a.cluster);
+    at[1].val.clusterDim.y = 1;
+    at[1].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned int>(units * a.cluster));
+    cfg.blockDim = dim3(CHOOSE);
+    cfg.dynamicSmemBytes = static_cast<size_t>(a.held) * 4;
+    cfg.stream = s;
+    cfg.attrs = at;
+    cfg.numAttrs = a.cluster > 1 ? 2 : 1;
+    count_launch();
+    if ((e = cudaLaunchKernelEx(&cfg, kv_choose_kernel, a)) != cudaSuccess)
+        return e;
+    const dim3 grid(static_cast<unsigned int>(units * ((a.keep + KV_PAGE - 1) / KV_PAGE)));
+    count_launch();
+    return dim == 128 ? launch_dependent(kv_move_kernel<128>, grid, dim3(256), s, a)
+                      : launch_dependent(kv_move_kernel<64>, grid, dim3(128), s, a);
+}
+
+}  // namespace mmq

@@ -835,6 +835,8 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prompt_kernel(const AttendArgs 
             const long long out_at = result();
             if (g.nsplit > 1 && mine && h == 0)
                 g.part_ml[part_row()] = make_float2(ref, sum);
+            if (g.nsplit == 1 && g.stats && mine && h == 0)
+                g.stats[part_row()] = kv_row_stats(ref, sum);
             constexpr int COLS = C::COLS, ROW = C::STAGED, LPR = COLS / 4;
             uint8_t* stage = smem + C::Q + (warp - SOFT_WARP) * 32 * ROW;
             const int sub = lane / LPR, c = lane % LPR * 4;

@@ -572,6 +572,8 @@ __global__ void __launch_bounds__(WARPS * 32, MODE == WIDE ? 3 : D == 128 ? 4 : 
     const size_t at = static_cast<size_t>(split) * flat_rows + static_cast<size_t>(token) * g.heads + h;
     if (g.nsplit > 1 && l == 0)
         g.part_ml[at] = make_float2(top, total);
+    if (g.nsplit == 1 && g.stats && l == 0)
+        g.stats[at] = kv_row_stats(top, total);
     const float inv = total == 0.0f ? 0.0f : 1.0f / total;   // a row that sees no key is zero
 #pragma unroll
     for (int j = 0; j < GROUPS; ++j) {
@@ -643,6 +645,8 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) kv_join_kernel(const AttendAr
             v.w += p.w;
         }
     }
+    if (g.stats && threadIdx.x == 0)
+        g.stats[flat] = kv_row_stats(top, total);
     const float inv = total == 0.0f ? 0.0f : 1.0f / total;
     v = make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv);
     store4(static_cast<T*>(g.out.data) + static_cast<long long>(flat / g.heads) * g.out.tok +
