@@ -219,10 +219,20 @@ AttendPlan plan(const mmq_kv_cache* c, int dtype, int heads, int ntok, int max_q
                             max_kv < 1 ? 1 : max_kv, c->max_pages, window, sinks);
 }
 
-// {reference, 1 / sum} of each row of an attention whose weights are wanted.
-size_t stats_bytes(int ntok, int heads)
+// What the weights need in the workspace beside the attention's: {reference, 1 / sum} of each row,
+// then the rows as operands.
+struct WeighPlan {
+    size_t stats_bytes, operand_bytes;
+    int cols;
+    long long tiles;
+};
+WeighPlan weigh_plan(const mmq_kv_cache* c, int dtype, int heads, int ntok, int max_q)
 {
-    return (static_cast<size_t>(ntok) * static_cast<size_t>(heads) * sizeof(float2) + 15) / 16 * 16;
+    WeighPlan p;
+    p.stats_bytes = (static_cast<size_t>(ntok) * static_cast<size_t>(heads) * sizeof(float2) + 15) / 16 * 16;
+    p.operand_bytes = mmq::weigh_bytes(dtype, heads, c->kv_heads, c->head_dim, c->batch, ntok, max_q < 1 ? 1 : max_q,
+                                       &p.cols, &p.tiles);
+    return p;
 }
 
 struct Weights {
@@ -250,7 +260,8 @@ mmq_status attend(const mmq_kv_cache* c, const mmq_rows* q, const mmq_rows* out,
     if (ntok == 0)
         return MMQ_OK;
     const AttendPlan p = plan(c, q->dtype, heads, ntok, max_q, max_kv, window, sinks);
-    const size_t need = p.part_bytes + p.ml_bytes + (weights ? stats_bytes(ntok, heads) : 0);
+    const WeighPlan wp = weights ? weigh_plan(c, q->dtype, heads, ntok, max_q) : WeighPlan{};
+    const size_t need = p.part_bytes + p.ml_bytes + wp.stats_bytes + wp.operand_bytes;
     if (need > 0) {
         if (!workspace || workspace_bytes < need)
             return MMQ_ERR_ARG;
@@ -296,9 +307,12 @@ mmq_status attend(const mmq_kv_cache* c, const mmq_rows* q, const mmq_rows* out,
     cudaError_t e = launch(a, c->head_dim, q->dtype, reinterpret_cast<cudaStream_t>(s));
     if (e == cudaSuccess && p.nsplit > 1)
         e = mmq::launch_kv_join(a, c->head_dim, q->dtype, reinterpret_cast<cudaStream_t>(s));
-    if (e == cudaSuccess && weights)
-        e = mmq::launch_kv_weigh({a, weights->in, weights->out, weights->decay, 1}, c->head_dim, q->dtype, max_kv,
-                                 reinterpret_cast<cudaStream_t>(s));
+    if (e == cudaSuccess && weights) {
+        a.wc = {a.c.bad - 1, mmq::WAIT_LIMIT_NS, -1};
+        const mmq::WeighArgs w = {a, weights->in, weights->out, weights->decay, max_q < 1 ? 1 : max_q, wp.cols, wp.tiles,
+                                  reinterpret_cast<uint8_t*>(a.stats) + wp.stats_bytes, 1};
+        e = mmq::launch_kv_weigh(w, c->head_dim, q->dtype, max_kv, reinterpret_cast<cudaStream_t>(s));
+    }
     return mmq::from_cuda(e);
 }
 
@@ -365,8 +379,10 @@ mmq_status mmq_kv_attend_weights_workspace_bytes(const mmq_kv_cache* c, int dtyp
                                                  int max_kv, int window, int sinks, size_t* bytes)
 {
     const mmq_status st = mmq_kv_attend_workspace_bytes(c, dtype, heads, ntok, max_q, max_kv, window, sinks, bytes);
-    if (st == MMQ_OK)
-        *bytes += stats_bytes(ntok, heads);
+    if (st == MMQ_OK && ntok > 0) {
+        const WeighPlan p = weigh_plan(c, dtype, heads, ntok, max_q);
+        *bytes += p.stats_bytes + p.operand_bytes;
+    }
     return st;
 }
 
