@@ -11,9 +11,8 @@
 // they are f32, split in two f16 parts.
 //
 // kv_weigh_few_kernel, up to 128 rows per sequence and kv head: the rows stay in shared memory
-// and the keys stream by, 128 a step, two steps in flight.  One warpgroup widens (a thread a
-// key; the next step's codes are on their way meanwhile) and issues the products, two take
-// every other step's S each.
+// and the keys stream by, 128 a step, their codes through a ring of bulk copies.  One warpgroup
+// widens (a thread a key) and issues the products, two take every other step's S each.
 //
 // kv_weigh_many_kernel: 256 keys stay in shared memory and the rows stream by, 128 a step, as
 // operands that kv_weigh_rows_kernel has laid out in the workspace.  Four warpgroups, one for each
@@ -87,16 +86,16 @@ template <int D>
 struct KeyCodes {
     uint4 code[D / 32];
     uint2 scale;
-    __device__ __forceinline__ void load(const WeighArgs& w, int page, int head, int slot)
+    // of slot `slot` of a piece; one that is not there gives zeros: any code times the scale 0
+    __device__ __forceinline__ void get(const uint8_t* src, int slot, bool there)
     {
         using P = Piece<D>;
-        scale = make_uint2(0, 0);   // a page that is not there gives zeros
+        scale = make_uint2(0, 0);
 #pragma unroll
         for (int i = 0; i < D / 32; ++i)
             code[i] = make_uint4(0, 0, 0, 0);
-        if (page < 0 || page >= w.a.c.num_pages)
+        if (!there)
             return;
-        const uint8_t* src = w.a.c.pages + (static_cast<size_t>(page) * w.a.c.kv_heads + head) * P::BYTES;
 #pragma unroll
         for (int i = 0; i < D / 32; ++i)
             code[i] = *reinterpret_cast<const uint4*>(src + P::k_chunk(slot, i));
@@ -122,11 +121,11 @@ struct KeyCodes {
     }
 };
 
-// One row as operand row r of [part][64-value block][n rows] tiles, by a warp; what its column
-// needs.  A row whose statistics are {0, 0} becomes zeros.
+// One row as operand row r of [64-value block][n rows] tiles, by a warp, an f32 row's low part as
+// row r + low; what its column needs.  A row whose statistics are {0, 0} becomes zeros.
 template <int D, typename T>
 __device__ __forceinline__ void put_row(const AttendArgs& g, const T* q, float2 stats, int pos, uint8_t* dst, int n, int r,
-                                        Columns* cols, int lane)
+                                        int low, Columns* cols, int lane)
 {
     float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     if (q && stats.y > 0.0f && lane < D / 4)
@@ -145,7 +144,7 @@ __device__ __forceinline__ void put_row(const AttendArgs& g, const T* q, float2 
         uint8_t* at = dst + d / 64 * n * 128 + r * 128 + ((d / 8 % 8 ^ (r & 7)) << 4) + d % 8 * 2;
         *reinterpret_cast<uint2*>(at) = hi;
         if constexpr (sizeof(T) == 4)
-            *reinterpret_cast<uint2*>(at + D / 64 * n * 128) = lo;
+            *reinterpret_cast<uint2*>(at + low * 128) = lo;   // a multiple of 8 rows: the same turn
     }
     if (lane == 0) {
         cols->coef[r] = fminf(fmaxf(g.scale_log2 * kv_pow2(e), 1e-38f), 1e38f);
@@ -202,23 +201,36 @@ __device__ __forceinline__ void add_columns(const AttendArgs& g, const float (&x
 }
 
 // ------------------------------------------------------------------ few rows
-constexpr int FEW_THREADS = 384;    // widening, two of sums
+constexpr int FEW_WARPS = 14;               // widening, two of sums, one that copies, one that issues products
+constexpr int COPY_WARP = 12, MMA_WARP = 13;
 
+// f32 rows: the low parts are n more columns, so that K is read once for both.
 template <int D, typename T>
 struct Few {
     static constexpr int PARTS = sizeof(T) == 4 ? 2 : 1, KB = D / 64;
     static constexpr int K_BYTES = KB * KEYS * 128;
-    static constexpr int COLS = 2 * K_BYTES, BAR = COLS + static_cast<int>(sizeof(Columns));
-    static constexpr int Q = (BAR + 64 + 1023) / 1024 * 1024;
-    enum { SFULL, SEMPTY = SFULL + 2, DRAIN = SEMPTY + 2, NBAR };
-    static_assert(NBAR * 8 + 4 <= 64, "barriers");
+    static constexpr int HALF = Piece<D>::V_CODES;                 // a page's keys
+    static constexpr int STAGES = 4, STAGE = 2 * HALF;             // codes on their way
+    static constexpr int RING = 2 * K_BYTES, COLS = RING + STAGES * STAGE;
+    static constexpr int META = COLS + static_cast<int>(sizeof(Columns));   // int2 [STAGES]: whether its pages are there
+    static constexpr int BAR = META + STAGES * 8;
+    enum { QFULL, RFULL, REMPTY = RFULL + STAGES, KFULL = REMPTY + STAGES, KEMPTY = KFULL + 2, SFULL = KEMPTY + 2,
+           SEMPTY = SFULL + 2, DRAIN = SEMPTY + 2, NBAR };
+    static constexpr int TMEM_AT = BAR + NBAR * 8;
+    static constexpr int Q = (TMEM_AT + 4 + 1023) / 1024 * 1024;
+    static_assert(RING % 16 == 0 && COLS % 16 == 0 && BAR % 8 == 0, "alignment");
     static constexpr int bytes(int n) { return Q + PARTS * KB * n * 128 + 1024; }   // and the alignment
+    __host__ __device__ static constexpr int columns(int n)        // of one S in tensor memory
+    {
+        return n * PARTS <= 32 ? 32 : n * PARTS <= 64 ? 64 : n * PARTS <= 128 ? 128 : 256;
+    }
 };
 
 template <int D, typename T>
-__global__ void __launch_bounds__(FEW_THREADS) kv_weigh_few_kernel(const WeighArgs w)
+__global__ void __launch_bounds__(FEW_WARPS * 32) kv_weigh_few_kernel(const WeighArgs w)
 {
     using C = Few<D, T>;
+    using P = Piece<D>;
     const AttendArgs& g = w.a;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw), pad = (1024u - (raw & 1023u)) & 1023u;
@@ -226,8 +238,9 @@ __global__ void __launch_bounds__(FEW_THREADS) kv_weigh_few_kernel(const WeighAr
     const uint32_t sbase = raw + pad;
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x / 32, 0), lane = threadIdx.x % 32;
     auto bar = [&](int i) -> uint32_t { return sbase + C::BAR + 8u * static_cast<uint32_t>(i); };
-    uint32_t* tmem_at = reinterpret_cast<uint32_t*>(smem + C::BAR + 8 * C::NBAR);
+    uint32_t* tmem_at = reinterpret_cast<uint32_t*>(smem + C::TMEM_AT);
     Columns* cols = reinterpret_cast<Columns*>(smem + C::COLS);
+    int2* meta = reinterpret_cast<int2*>(smem + C::META);
 
     grid_dep_wait();
     const int part = blockIdx.x % w.parts;
@@ -240,117 +253,184 @@ __global__ void __launch_bounds__(FEW_THREADS) kv_weigh_few_kernel(const WeighAr
     const int tiles = (u.length + KEYS - 1) / KEYS;
     if (part >= tiles)
         return;
-    const uint32_t columns = n <= 32 ? 32 : n <= 64 ? 64 : 128;   // of one S
+    const uint32_t columns = C::columns(n);
     if (threadIdx.x == 0) {
+        mbar_init(bar(C::QFULL), COPY_WARP);
+        for (int i = 0; i < C::STAGES; ++i) {
+            mbar_init(bar(C::RFULL + i), 1);
+            mbar_init(bar(C::REMPTY + i), 4);
+        }
         for (int i = 0; i < 2; ++i) {
+            mbar_init(bar(C::KFULL + i), 4);
+            mbar_init(bar(C::KEMPTY + i), 1);
             mbar_init(bar(C::SFULL + i), 1);
             mbar_init(bar(C::SEMPTY + i), 4);
         }
         mbar_init(bar(C::DRAIN), 1);
         fence_barrier_init();
     }
-    if (warp == 0) {
+    if (warp == MMA_WARP) {
         tmem_alloc(smem_u32(tmem_at), 2 * columns);
         tmem_relinquish();
     }
-    for (int r = warp; r < n; r += FEW_THREADS / 32) {
-        const bool there = r < rows;
-        const long long token = u.first + r / g.group;
-        const int h = u.head * g.group + r % g.group;
-        put_row<D, T>(g, there ? static_cast<const T*>(g.q.data) + token * g.q.tok + h * g.q.head : nullptr,
-                      there ? g.stats[token * g.heads + h] : make_float2(0.0f, 0.0f), there ? u.pos0 + r / g.group : -1,
-                      smem + C::Q, n, r, cols, lane);
-    }
-    fence_proxy_async_smem();
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_at;
 
+    if (warp < COPY_WARP) {   // the rows, while the first codes are on their way
+        for (int r = warp; r < n; r += COPY_WARP) {
+            const bool there = r < rows;
+            const long long token = u.first + r / g.group;
+            const int h = u.head * g.group + r % g.group;
+            put_row<D, T>(g, there ? static_cast<const T*>(g.q.data) + token * g.q.tok + h * g.q.head : nullptr,
+                          there ? g.stats[token * g.heads + h] : make_float2(0.0f, 0.0f), there ? u.pos0 + r / g.group : -1,
+                          smem + C::Q, C::PARTS * n, r, n, cols, lane);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0)
+            mbar_arrive(bar(C::QFULL));
+    }
+
+    // the CTA's tiles are part, part + parts, ...; those of which no key is seen are passed over
     auto seen = [&](int tile) { return any_seen(g, u.plo, u.phi, tile * KEYS, KEYS); };
     bool ok = true;
     int step = 0;   // tiles so far of which a key is seen
     if (warp < 4) {
+        // ------------------------------------------------------------ widening
         const int t = threadIdx.x;
-        const uint32_t lead = elect_one(), idesc = idesc_f16_f32(KEYS, n);
-        auto next = [&](int tile) {
-            do
-                tile += w.parts;
-            while (tile < tiles && !seen(tile));
-            return tile;
-        };
-        auto page = [&](int tile) {
-            const int i = 2 * tile + t / KV_PAGE;
+        for (int tile = part; ok && tile < tiles; tile += w.parts) {
+            if (!seen(tile))
+                continue;
+            const int buf = step % 2, stage = step % C::STAGES;
+            ok = warp_wait(w, bar(C::RFULL + stage), step / C::STAGES & 1) &&
+                 warp_wait(w, bar(C::KEMPTY + buf), (step / 2 & 1) ^ 1);
+            if (!ok)
+                break;
+            const int2 there = meta[stage];
+            KeyCodes<D> codes;
+            codes.get(smem + C::RING + stage * C::STAGE + t / KV_PAGE * C::HALF, t % KV_PAGE, t < KV_PAGE ? there.x : there.y);
+            codes.widen(smem + buf * C::K_BYTES, t);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(bar(C::KFULL + buf));
+                mbar_arrive(bar(C::REMPTY + stage));
+            }
+            ++step;
+        }
+    } else if (warp == MMA_WARP) {
+        // ------------------------------------------------------------ products
+        const uint32_t lead = elect_one(), idesc = idesc_f16_f32(KEYS, C::PARTS * n);
+        ok = warp_wait(w, bar(C::QFULL), 0);
+        for (int tile = part; ok && tile < tiles; tile += w.parts) {
+            if (!seen(tile))
+                continue;
+            const int buf = step % 2;
+            ok = warp_wait(w, bar(C::KFULL + buf), step / 2 & 1) && warp_wait(w, bar(C::SEMPTY + buf), (step / 2 & 1) ^ 1);
+            if (!ok)
+                break;
+            tc_fence_after();
+            product<D, 1>(lead, tmem + buf * columns, sbase + buf * C::K_BYTES, sbase + C::Q, C::PARTS * n * 128, idesc);
+            umma_commit_by(lead, bar(C::SFULL + buf));
+            umma_commit_by(lead, bar(C::KEMPTY + buf));
+            ++step;
+        }
+        umma_commit_by(lead, bar(C::DRAIN));
+        if (lead)
+            mbar_drain_wait(bar(C::DRAIN), 0, WAIT_LIMIT_NS, g.wc.err);
+        __syncwarp();
+    } else if (warp == COPY_WARP) {
+        // ------------------------------------------------------------ codes: the keys of two pages a step
+        // ids of 16 tiles at a time, two lanes each, and those of the next 16 on their way
+        auto ids_of = [&](long long k) {
+            const long long tile = part + (k + lane / 2) * w.parts, i = 2 * tile + lane % 2;
             return tile < tiles && i * KV_PAGE < u.length ? u.table[i] : -1;
         };
-        int tile = part;
-        if (!seen(tile))
-            tile = next(tile);
-        int after = tile < tiles ? next(tile) : tiles;
-        KeyCodes<D> codes;
-        codes.load(w, page(tile), u.head, t % KV_PAGE);
-        int ahead = page(after);
-        for (; tile < tiles; ++step) {
-            const KeyCodes<D> now = codes;
-            codes.load(w, ahead, u.head, t % KV_PAGE);
-            tile = after;
-            after = tile < tiles ? next(tile) : tiles;
-            ahead = page(after);
-            const int buf = step % 2;
-            if (step >= 2)   // the products that read this K are done
-                ok = ok && warp_wait(w, bar(C::SFULL + buf), step / 2 - 1 & 1);
-            if (ok)
-                now.widen(smem + buf * C::K_BYTES, t);
-            fence_proxy_async_smem();
-            if (!named_bar_and(1, 128, ok)) {
-                ok = false;
+        int ids = -1, later = ids_of(0);
+        for (int k = 0, tile = part; tile < tiles; ++k, tile += w.parts) {
+            if (k % 16 == 0) {
+                ids = later < g.c.num_pages ? later : -1;
+                later = ids_of(k + 16);
+            }
+            if (!seen(tile))
+                continue;
+            const int p0 = __shfl_sync(0xffffffffu, ids, k % 16 * 2), p1 = __shfl_sync(0xffffffffu, ids, k % 16 * 2 + 1);
+            const int stage = step % C::STAGES;
+            ok = warp_wait(w, bar(C::REMPTY + stage), (step / C::STAGES & 1) ^ 1);
+            if (!ok)
                 break;
+            if (lane == 0) {
+                meta[stage] = make_int2(p0 >= 0, p1 >= 0);
+                fence_proxy_async_smem();   // the stage was read with ordinary loads
+                mbar_arrive_expect_tx(bar(C::RFULL + stage), ((p0 >= 0) + (p1 >= 0)) * C::HALF);
+                const uint32_t dst = sbase + C::RING + stage * C::STAGE;
+                const size_t piece = static_cast<size_t>(g.c.kv_heads) * P::BYTES;
+                const uint8_t* src = g.c.pages + static_cast<size_t>(u.head) * P::BYTES;
+                if (p0 >= 0)
+                    bulk_g2s(dst, src + p0 * piece, C::HALF, bar(C::RFULL + stage));
+                if (p1 >= 0)
+                    bulk_g2s(dst + C::HALF, src + p1 * piece, C::HALF, bar(C::RFULL + stage));
             }
-            if (warp == 0) {
-                if (step >= 2)
-                    ok = warp_wait(w, bar(C::SEMPTY + buf), step / 2 - 1 & 1);
-                if (ok) {
-                    tc_fence_after();
-                    product<D, C::PARTS>(lead, tmem + buf * columns, sbase + buf * C::K_BYTES, sbase + C::Q, n * 128, idesc);
-                    umma_commit_by(lead, bar(C::SFULL + buf));
-                }
-            }
+            ++step;
         }
-        if (warp == 0) {
-            umma_commit_by(lead, bar(C::DRAIN));
-            if (lead)
-                mbar_drain_wait(bar(C::DRAIN), 0, WAIT_LIMIT_NS, g.wc.err);
-        }
+        if (lane == 0)   // the last fill of each stage lands before the CTA ends
+            for (int i = max(0, step - C::STAGES); i < step; ++i)
+                mbar_drain_wait(bar(C::RFULL + i % C::STAGES), i / C::STAGES & 1, WAIT_LIMIT_NS, g.wc.err);
         __syncwarp();
     } else {
+        // ------------------------------------------------------------ sums: a thread a key
         const int buf = warp / 4 - 1, t = threadIdx.x % KEYS;
         const uint32_t s_at = tmem + buf * columns + (static_cast<uint32_t>(t & ~31) << 16);
-        int count = 0;
-        for (int tile = part; tile < tiles; tile += w.parts, ++count) {
-            const int key = tile * KEYS + t;
-            const bool used = seen(tile);
-            if ((used ? step++ : count) % 2 != buf)
-                continue;
-            if (!used && w.in == w.out && w.decay == 1.0f && tile * KEYS + KEYS <= u.pos0)
-                continue;   // nothing changes
-            int page = key < u.length ? u.table[key / KV_PAGE] : -1;
-            if (page >= g.c.num_pages || (page < 0 && key < u.length)) {
-                *g.c.bad = 1u;
-                page = -1;
+        int unseen = 0;   // tiles so far of which no key is seen; they go to the warpgroups in turn too
+        // the warpgroup's next tile from `tile` on, and whether S has it
+        auto next = [&](int tile, bool& used) {
+            for (; tile < tiles; tile += w.parts) {
+                used = seen(tile);
+                if ((used ? step++ : unseen++) % 2 != buf)
+                    continue;
+                if (used || w.in != w.out || w.decay != 1.0f || tile * KEYS + KEYS > u.pos0)
+                    return tile;   // else nothing changes
             }
-            const size_t at = (static_cast<size_t>(max(page, 0)) * g.c.kv_heads + u.head) * KV_PAGE + key % KV_PAGE;
-            const float old = page >= 0 && key < u.pos0 ? w.decay * w.in[at] : 0.0f;
+            return tile;
+        };
+        auto page_of = [&](int tile) { return tile < tiles && tile * KEYS + t < u.length ? u.table[(tile * KEYS + t) / KV_PAGE] : -1; };
+        auto place = [&](int page, int tile) {
+            return (static_cast<size_t>(page) * g.c.kv_heads + u.head) * KV_PAGE + (tile * KEYS + t) % KV_PAGE;
+        };
+        auto had = [&](int page, int tile) {
+            return page >= 0 && page < g.c.num_pages && tile * KEYS + t < u.pos0 ? w.in[place(page, tile)] : 0.0f;
+        };
+        // what the next tile had is on its way while this one's weights are added up, and the page of
+        // the one after that
+        bool used = false, used1 = false, used2 = false;
+        int tile = next(part, used), tile1 = tile < tiles ? next(tile + w.parts, used1) : tile;
+        int page = page_of(tile), page1 = page_of(tile1), turn = 0;
+        float old = had(page, tile);
+        ok = warp_wait(w, bar(C::QFULL), 0);
+        while (ok && tile < tiles) {
+            const int tile2 = tile1 < tiles ? next(tile1 + w.parts, used2) : tile1, page2 = page_of(tile2);
+            const float old1 = had(page1, tile1);
             float2 sum = make_float2(0.0f, 0.0f);
             if (used) {
-                const int turn = (step - 1) / 2;
                 ok = warp_wait(w, bar(C::SFULL + buf), turn & 1);
                 if (!ok)
                     break;
+                ++turn;
                 tc_fence_after();
                 const bool plain = rows % 4 == 0 && all_seen(g, u.plo, u.phi, tile * KEYS, KEYS);
                 for (int c = 0; c < rows; c += 16) {
                     float x[16];
-                    tmem_ld16_wait(s_at + c, x);
+                    if constexpr (C::PARTS == 2) {
+                        float lo[16];
+                        tmem_ld16x2_wait(s_at + c, s_at + n + c, x, lo);
+#pragma unroll
+                        for (int i = 0; i < 16; ++i)
+                            x[i] += lo[i];
+                    } else {
+                        tmem_ld16_wait(s_at + c, x);
+                    }
                     if (c + 16 >= rows) {
                         tc_fence_before();
                         __syncwarp();
@@ -358,19 +438,28 @@ __global__ void __launch_bounds__(FEW_THREADS) kv_weigh_few_kernel(const WeighAr
                             mbar_arrive(bar(C::SEMPTY + buf));
                     }
                     if (plain)
-                        add_columns<false>(g, x, cols, c, rows, key, sum);
+                        add_columns<false>(g, x, cols, c, rows, tile * KEYS + t, sum);
                     else
-                        add_columns<true>(g, x, cols, c, rows, key, sum);
+                        add_columns<true>(g, x, cols, c, rows, tile * KEYS + t, sum);
                 }
             }
-            if (page >= 0)
-                w.out[at] = old + (sum.x + sum.y);
+            if (page >= 0 && page < g.c.num_pages)
+                w.out[place(page, tile)] = w.decay * old + (sum.x + sum.y);
+            else if (tile * KEYS + t < u.length)
+                *g.c.bad = 1u;
+            tile = tile1;
+            page = page1;
+            used = used1;
+            old = old1;
+            tile1 = tile2;
+            page1 = page2;
+            used1 = used2;
         }
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == 0)
+    if (warp == MMA_WARP)
         tmem_dealloc(tmem, 2 * columns);
 }
 
@@ -419,7 +508,7 @@ __global__ void __launch_bounds__(256) kv_weigh_rows_kernel(const WeighArgs w)
         uint8_t* record = w.operands +
                           (h / g.group * w.tiles + first_tile(g, first, b) + row / MOST_ROWS) * static_cast<long long>(C::RECORD);
         put_row<D, T>(g, static_cast<const T*>(g.q.data) + r * g.q.tok + h * g.q.head, g.stats[static_cast<size_t>(r) * g.heads + h],
-                      pos, record, MOST_ROWS, row % MOST_ROWS, reinterpret_cast<Columns*>(record + C::Q_BYTES), lane);
+                      pos, record, MOST_ROWS, row % MOST_ROWS, C::KB * MOST_ROWS, reinterpret_cast<Columns*>(record + C::Q_BYTES), lane);
     }
 }
 
@@ -562,7 +651,10 @@ __global__ void __launch_bounds__(MANY_THREADS, 1) kv_weigh_many_kernel(const We
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
                 const int i = (group * GROUP + k * KEYS + t) / KV_PAGE;
-                codes[k].load(w, i * KV_PAGE < u.length ? u.table[i] : -1, u.head, t % KV_PAGE);
+                const int page = i * KV_PAGE < u.length ? u.table[i] : -1;
+                const bool there = page >= 0 && page < g.c.num_pages;
+                codes[k].get(g.c.pages + (static_cast<size_t>(there ? page : 0) * g.c.kv_heads + u.head) * Piece<D>::BYTES,
+                             t % KV_PAGE, there);
             }
             ok = warp_wait(w, bar(C::KEMPTY), (visit & 1) ^ 1);
             if (!ok)
@@ -652,11 +744,11 @@ cudaError_t launch_weigh(WeighArgs a, long long keys, cudaStream_t s)
     if (a.tiles == 0) {
         using C = Few<D, T>;
         static std::atomic<uint64_t> done{0};
-        cudaError_t e = kv_allow_smem(kv_weigh_few_kernel<D, T>, C::bytes(MOST_ROWS) > 112 * 1024 ? C::bytes(MOST_ROWS) : 112 * 1024, &done);
+        cudaError_t e = kv_allow_smem(kv_weigh_few_kernel<D, T>, C::bytes(MOST_ROWS) > 116 * 1024 ? C::bytes(MOST_ROWS) : 116 * 1024, &done);
         if (e != cudaSuccess)
             return e;
         // no more CTAs to an SM than its 512 columns of tensor memory are enough for
-        const int resident = a.cols <= 32 ? 4 : a.cols <= 64 ? 4 : 2;
+        const int resident = 512 / (2 * C::columns(a.cols));
         int bytes = C::bytes(a.cols);
         const int least = 227 * 1024 / (resident + 1);
         bytes = bytes > least ? bytes : least;
@@ -666,7 +758,7 @@ cudaError_t launch_weigh(WeighArgs a, long long keys, cudaStream_t s)
         a.parts = parts(tiles, even > uneven ? even : uneven);
         count_launch();
         return launch_dependent_smem(kv_weigh_few_kernel<D, T>, dim3(static_cast<unsigned int>(units * a.parts)),
-                                     dim3(FEW_THREADS), static_cast<size_t>(bytes), s, a);
+                                     dim3(FEW_WARPS * 32), static_cast<size_t>(bytes), s, a);
     }
     using C = Many<D, T>;
     static std::atomic<uint64_t> done{0};
