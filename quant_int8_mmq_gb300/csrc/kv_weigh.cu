@@ -37,6 +37,9 @@ __device__ __forceinline__ bool wait(const WeighArgs& w, uint32_t bar, uint32_t 
 {
     return mbar_wait_asleep(bar, parity, w.a.wc.limit_ns, w.a.wc.err);
 }
+// All lanes ask the same barrier in one instruction, so the warp stays together: with lanes that
+// waited for different barriers, or one for all, it came apart, and tcgen05's .aligned
+// instructions after that faulted.
 __device__ __forceinline__ bool warp_wait(const WeighArgs& w, uint32_t bar, uint32_t parity)
 {
     return __all_sync(0xffffffffu, wait(w, bar, parity));
@@ -50,17 +53,17 @@ struct Unit {
     int plo, phi;           // positions of the first and last row
     const int* table;
 };
-__device__ __forceinline__ bool unit_of(const WeighArgs& w, int id, Unit& u)
+__device__ __forceinline__ bool unit_of(const WeighArgs& w, int b, int head, Unit& u)
 {
     const AttendArgs& g = w.a;
-    u.head = id % g.c.kv_heads;
-    u.b = id / g.c.kv_heads;
+    u.head = head;
+    u.b = b;
     u.first = g.c.start[u.b];
     const int last = g.c.start[u.b + 1];
     if (u.first < 0 || last <= u.first || last > g.ntok)
         return false;
     const int new_tokens = last - u.first, counted = min(new_tokens, w.max_q);
-    if (new_tokens > counted && threadIdx.x == 0)
+    if (new_tokens > counted)
         *g.c.bad = 1u;
     u.rows = counted * g.group;
     u.length = min(max(g.c.length[u.b], 0), g.c.max_pages * KV_PAGE);
@@ -68,7 +71,7 @@ __device__ __forceinline__ bool unit_of(const WeighArgs& w, int id, Unit& u)
     u.plo = u.pos0;
     u.phi = u.pos0 + counted - 1;
     u.table = g.c.table + static_cast<size_t>(u.b) * g.c.max_pages;
-    return u.rows > 0;
+    return true;
 }
 
 // Whether a row sees any of the keys [k0, k0 + n), and whether all see all.
@@ -104,32 +107,42 @@ struct KeyCodes {
         else
             scale.x = *reinterpret_cast<const uint32_t*>(src + P::k_scale(slot, 0));
     }
+    // the 32 values of a group as 16 pairs
+    __device__ __forceinline__ void widen(int gr, uint32_t (&o)[16]) const
+    {
+        const uint32_t both = gr < 2 ? scale.x : scale.y;
+        const __half2 s = kv_u2h(__byte_perm(both, 0, gr % 2 ? 0x3232 : 0x1010)), sb = kv_addend(s);
+        const uint32_t v[4] = {code[gr].x, code[gr].y, code[gr].z, code[gr].w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            o[4 * i] = kv_h2u(kv_widen<0>(v[i], s, sb));
+            o[4 * i + 1] = kv_h2u(kv_widen<1>(v[i], s, sb));
+            o[4 * i + 2] = kv_h2u(kv_widen<2>(v[i], s, sb));
+            o[4 * i + 3] = kv_h2u(kv_widen<3>(v[i], s, sb));
+        }
+    }
     // row t of [64-value block][128 keys] tiles, 128-byte swizzle
     __device__ __forceinline__ void widen(uint8_t* dst, int t) const
     {
 #pragma unroll
         for (int gr = 0; gr < D / 32; ++gr) {
-            const uint32_t both = gr < 2 ? scale.x : scale.y;
-            const __half2 s = kv_u2h(__byte_perm(both, 0, gr % 2 ? 0x3232 : 0x1010)), sb = kv_addend(s);
-            const uint32_t v[4] = {code[gr].x, code[gr].y, code[gr].z, code[gr].w};
+            uint32_t o[16];
+            widen(gr, o);
 #pragma unroll
             for (int i = 0; i < 4; ++i)
                 *reinterpret_cast<uint4*>(dst + gr / 2 * KEYS * 128 + t * 128 + ((gr % 2 * 4 + i) ^ (t & 7)) * 16) =
-                    make_uint4(kv_h2u(kv_widen<0>(v[i], s, sb)), kv_h2u(kv_widen<1>(v[i], s, sb)),
-                               kv_h2u(kv_widen<2>(v[i], s, sb)), kv_h2u(kv_widen<3>(v[i], s, sb)));
+                    make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
         }
     }
 };
 
-// One row as operand row r of [64-value block][n rows] tiles, by a warp, an f32 row's low part as
-// row r + low; what its column needs.  A row whose statistics are {0, 0} becomes zeros.
+// One row, four values a lane, as operand row r of [64-value block][n rows] tiles, by a warp, an
+// f32 row's low part as row r + low; what its column needs.  A row whose statistics are {0, 0} is
+// given as zeros.
 template <int D, typename T>
-__device__ __forceinline__ void put_row(const AttendArgs& g, const T* q, float2 stats, int pos, uint8_t* dst, int n, int r,
+__device__ __forceinline__ void put_row(const AttendArgs& g, float4 x, float2 stats, int pos, uint8_t* dst, int n, int r,
                                         int low, Columns* cols, int lane)
 {
-    float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    if (q && stats.y > 0.0f && lane < D / 4)
-        x = load4(q + 4 * lane, g.wide);
     float a = fmaxf(fmaxf(fabsf(x.x), fabsf(x.y)), fmaxf(fabsf(x.z), fabsf(x.w)));
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1)
@@ -154,6 +167,40 @@ __device__ __forceinline__ void put_row(const AttendArgs& g, const T* q, float2 
     }
 }
 
+// The rows of a unit, warp `warp` of `warps` taking every warps-th, four loads on their way at once.
+template <int D, typename T>
+__device__ __forceinline__ void put_rows(const AttendArgs& g, const Unit& u, int n, int warp, int warps, uint8_t* dst,
+                                         Columns* cols, int lane)
+{
+    constexpr int BATCH = 4;
+    const int rows = min(u.rows, n);
+    for (int r0 = warp; r0 < n; r0 += BATCH * warps) {
+        Raw4<T> x[BATCH];
+        float2 stats[BATCH];
+#pragma unroll
+        for (int i = 0; i < BATCH; ++i) {
+            const int r = r0 + i * warps;
+            stats[i] = make_float2(0.0f, 0.0f);
+            if (r < rows) {
+                const long long token = u.first + r / g.group;
+                const int h = u.head * g.group + r % g.group;
+                stats[i] = g.stats[token * g.heads + h];
+                if (lane < D / 4)
+                    x[i].load(static_cast<const T*>(g.q.data) + token * g.q.tok + h * g.q.head + 4 * lane, g.wide);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < BATCH; ++i) {
+            const int r = r0 + i * warps;
+            if (r >= n)
+                break;
+            const bool there = stats[i].y > 0.0f && lane < D / 4;
+            put_row<D, T>(g, there ? x[i].get() : make_float4(0.0f, 0.0f, 0.0f, 0.0f), stats[i],
+                          r < rows ? u.pos0 + r / g.group : -1, dst, (sizeof(T) == 4 ? 2 : 1) * n, r, n, cols, lane);
+        }
+    }
+}
+
 // K Q^T of one step: 128 keys by n rows.
 template <int D, int PARTS>
 __device__ __forceinline__ void product(uint32_t lead, uint32_t to, uint32_t k, uint32_t q, int q_block, uint32_t idesc)
@@ -171,13 +218,22 @@ __device__ __forceinline__ void product(uint32_t lead, uint32_t to, uint32_t k, 
         }
 }
 
-// The weights of 16 columns of a key.
-template <bool MASKED>
-__device__ __forceinline__ void add_columns(const AttendArgs& g, const float (&x)[16], const Columns* cols, int c0, int n,
+// A warp has what it wants of S.
+__device__ __forceinline__ void release(uint32_t bar, int lane)
+{
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0)
+        mbar_arrive(bar);
+}
+
+// The weights of some columns of a key.
+template <bool MASKED, int N>
+__device__ __forceinline__ void add_columns(const AttendArgs& g, const float (&x)[N], const Columns* cols, int c0, int n,
                                             int key, float2& sum)
 {
 #pragma unroll
-    for (int c = 0; c < 16; c += 4) {
+    for (int c = 0; c < N; c += 4) {
         if (c0 + c >= n)
             break;
         const float4 f = *reinterpret_cast<const float4*>(cols->coef + c0 + c);
@@ -201,266 +257,488 @@ __device__ __forceinline__ void add_columns(const AttendArgs& g, const float (&x
 }
 
 // ------------------------------------------------------------------ few rows
-constexpr int FEW_WARPS = 14;               // widening, two of sums, one that copies, one that issues products
-constexpr int COPY_WARP = 12, MMA_WARP = 13;
+// One CTA an SM; all tiles of 128 keys, sequence by sequence and head by head, are cut into even
+// shares, so that lengths may differ as they like and a CTA's pipeline runs on from one head to
+// the next.  What a tile costs its warps is a chain of dependent instructions, waits among them,
+// of 500 cycles (products) to 1200 (widening, sums), and its bytes arrive in 400: so each role is
+// several warpgroups' or warps', which take the tiles in turn.
+constexpr int GROUPS = 3, ROW_WARPS = 4, COPY_WARPS = 2;
+constexpr int SUM_WARP = 4 * GROUPS, ROW_WARP = SUM_WARP + 4 * GROUPS, COPY_WARP = ROW_WARP + ROW_WARPS,
+              MMA_WARP = COPY_WARP + COPY_WARPS, FEW_WARPS = MMA_WARP + 1, FEW_THREADS = FEW_WARPS * 32;
+constexpr int BATCH = 4;               // tiles a copying warp asks for at once
 
-// f32 rows: the low parts are n more columns, so that K is read once for both.
-template <int D, typename T>
-struct Few {
-    static constexpr int PARTS = sizeof(T) == 4 ? 2 : 1, KB = D / 64;
-    static constexpr int K_BYTES = KB * KEYS * 128;
-    static constexpr int HALF = Piece<D>::V_CODES;                 // a page's keys
-    static constexpr int STAGES = 4, STAGE = 2 * HALF;             // codes on their way
-    static constexpr int RING = 2 * K_BYTES, COLS = RING + STAGES * STAGE;
-    static constexpr int META = COLS + static_cast<int>(sizeof(Columns));   // int2 [STAGES]: whether its pages are there
-    static constexpr int BAR = META + STAGES * 8;
-    enum { QFULL, RFULL, REMPTY = RFULL + STAGES, KFULL = REMPTY + STAGES, KEMPTY = KFULL + 2, SFULL = KEMPTY + 2,
-           SEMPTY = SFULL + 2, DRAIN = SEMPTY + 2, NBAR };
-    static constexpr int TMEM_AT = BAR + NBAR * 8;
-    static constexpr int Q = (TMEM_AT + 4 + 1023) / 1024 * 1024;
-    static_assert(RING % 16 == 0 && COLS % 16 == 0 && BAR % 8 == 0, "alignment");
-    static constexpr int bytes(int n) { return Q + PARTS * KB * n * 128 + 1024; }   // and the alignment
-    __host__ __device__ static constexpr int columns(int n)        // of one S in tensor memory
-    {
-        return n * PARTS <= 32 ? 32 : n * PARTS <= 64 ? 64 : n * PARTS <= 128 ? 128 : 256;
-    }
+// K as an operand lies in tensor memory: widened codes go there from registers, and neither they
+// nor the products' reading of them take shared memory's bandwidth (in shared memory a tile
+// took 1000 cycles, most of them that).
+//
+// Waits tell one round of a barrier from the next by its parity, so nobody may wait for a round
+// while the one before it is open.  Each warpgroup has a buffer of its own (S, and K unless two
+// have to do), and one warp issues all products in order: a group that has its buffer back
+// from step i knows that all steps before i are done with, and the stages of codes are more than
+// the steps that can be open.
+constexpr int MAX_Q = 2, MAX_STAGES = 16;
+static_assert(MAX_STAGES % (BATCH * COPY_WARPS) == 0, "stages");
+enum { F_RFULL = 0, F_REMPTY = F_RFULL + MAX_STAGES, F_KFULL = F_REMPTY + MAX_STAGES, F_KEMPTY = F_KFULL + GROUPS,
+       F_SFULL = F_KEMPTY + GROUPS, F_SEMPTY = F_SFULL + GROUPS, F_QFULL = F_SEMPTY + GROUPS, F_QEMPTY = F_QFULL + MAX_Q,
+       F_DRAIN = F_QEMPTY + MAX_Q, F_BARS };
+
+// Where everything is in shared memory, and how many buffers of each there are.
+struct FewLayout {
+    int qbufs, kbufs, stages, stage_bits, columns;   // operands Q and K, codes on their way (a power of two: a
+                                                     // division took as long as the rest of a step), columns of S
+    int ring, cols, ids, bars, bytes;
 };
 
 template <int D, typename T>
-__global__ void __launch_bounds__(FEW_WARPS * 32) kv_weigh_few_kernel(const WeighArgs w)
+struct Few {
+    static constexpr int PARTS = sizeof(T) == 4 ? 2 : 1, KB = D / 64;
+    static constexpr int K_COLUMNS = D / 2;
+    static constexpr int HALF = Piece<D>::V_CODES, STAGE = 2 * HALF;    // a page's keys, a step's
+    static constexpr int q_bytes(int n) { return PARTS * KB * n * 128; }
+    // low parts of f32 rows: n more columns of S, or, where that is too many, a second product
+    __host__ __device__ static constexpr bool side_by_side(int n) { return PARTS * n <= 128; }
+    static FewLayout layout(int n)
+    {
+        FewLayout l = {};
+        const int wide = side_by_side(n) ? PARTS * n : n;
+        l.columns = wide <= 32 ? 32 : wide <= 64 ? 64 : 128;
+        l.kbufs = GROUPS * (l.columns + K_COLUMNS) <= 512 ? GROUPS : 2;
+        for (l.qbufs = MAX_Q;; --l.qbufs) {
+            l.cols = l.qbufs * q_bytes(n);
+            l.ids = l.cols + l.qbufs * static_cast<int>(sizeof(Columns));
+            l.bars = l.ids + MAX_STAGES * 8;
+            l.ring = (l.bars + F_BARS * 8 + 15) / 16 * 16;
+            // a multiple of the copying warps' turns, so that a stage is always filled by the same lanes
+            constexpr int TURN = BATCH * COPY_WARPS;
+            const int left = (225 * 1024 - l.ring) / STAGE / TURN * TURN;
+            l.stages = left < MAX_STAGES ? left : MAX_STAGES;
+            l.bytes = l.ring + l.stages * STAGE + 1024;   // and the alignment
+            l.stage_bits = l.stages == 16 ? 4 : 3;
+            if (l.stages > 0 || l.qbufs == 1)
+                return l;
+        }
+    }
+};
+static_assert(GROUPS * MOST_ROWS + 2 * Few<128, float>::K_COLUMNS <= 512, "tensor memory");
+
+// A run of one head's tiles [t0, t1); the n of them of which some row sees a key are the first n1
+// (before the window) and those from `second` on.
+struct Run {
+    int t0, t1, n1, n, second;
+    __device__ __forceinline__ int tile(int i) const { return i < n1 ? t0 + i : second + i - n1; }
+};
+
+// The tiles [c, end) of all sequences' and heads' as runs, each role on its own.
+struct Walk {
+    const WeighArgs& w;
+    Unit u;
+    int b, head, tiles, tile;   // of the current sequence; first tile of the next run
+    long long left;
+    __device__ __forceinline__ Walk(const WeighArgs& args, int b0, long long skip, long long count) : w(args), b(b0), left(count)
+    {
+        open();
+        head = tiles ? static_cast<int>(skip / tiles) : 0;
+        tile = tiles ? static_cast<int>(skip % tiles) : 0;
+    }
+    static __device__ __forceinline__ int tiles_of(const WeighArgs& w, int b)
+    {
+        const int first = w.a.c.start[b], last = w.a.c.start[b + 1];
+        const int length = min(max(w.a.c.length[b], 0), w.a.c.max_pages * KV_PAGE);
+        return first < 0 || last <= first || last > w.a.ntok ? 0 : (length + KEYS - 1) / KEYS;
+    }
+    __device__ __forceinline__ void open()
+    {
+        tiles = 0;
+        while (left > 0 && (tiles = tiles_of(w, b)) == 0)
+            ++b;
+        if (tiles)
+            unit_of(w, b, 0, u);
+    }
+    // false at the end
+    __device__ __forceinline__ bool next(Run& r)
+    {
+        if (left <= 0)
+            return false;
+        if (tile == tiles) {
+            tile = 0;
+            if (++head == w.a.c.kv_heads) {
+                head = 0;
+                ++b;
+                open();
+            }
+        }
+        u.head = head;
+        r.t0 = tile;
+        r.t1 = static_cast<int>(min(static_cast<long long>(tiles), tile + left));
+        left -= r.t1 - r.t0;
+        tile = r.t1;
+        // tile t is seen if t KEYS <= phi and, with a window, t KEYS + KEYS - 1 > plo - window or t KEYS < sinks
+        const AttendArgs& g = w.a;
+        const int end = min(r.t1, u.phi < 0 ? 0 : u.phi / KEYS + 1);
+        const int from = g.window > 0 ? max(u.plo - g.window + 1, 0) / KEYS : 0;
+        const int sinks = min((g.sinks + KEYS - 1) / KEYS, from);
+        r.n1 = max(min(end, sinks) - r.t0, 0);
+        r.second = max(r.t0, from);
+        r.n = r.n1 + max(end - r.second, 0);
+        return true;
+    }
+};
+
+// A ring's place and the parity of its round.
+struct Turn {
+    int i = 0;
+    uint32_t round = 0;
+    __device__ __forceinline__ void next(int n)
+    {
+        if (++i == n) {
+            i = 0;
+            round ^= 1u;
+        }
+    }
+};
+
+__device__ __forceinline__ void tmem_store16(uint32_t taddr, const uint32_t (&v)[16])
+{
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+        "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+        : "memory");
+}
+
+template <int D, typename T>
+__global__ void __launch_bounds__(FEW_THREADS, 1) kv_weigh_few_kernel(const WeighArgs w, const FewLayout l)
 {
     using C = Few<D, T>;
     using P = Piece<D>;
     const AttendArgs& g = w.a;
     extern __shared__ uint8_t smem_raw[];
+    __shared__ long long total, skip;
+    __shared__ long long warp_sum[FEW_WARPS];
+    __shared__ int first_b;
+    __shared__ uint32_t tmem_at;
     const uint32_t raw = smem_u32(smem_raw), pad = (1024u - (raw & 1023u)) & 1023u;
     uint8_t* smem = smem_raw + pad;
     const uint32_t sbase = raw + pad;
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x / 32, 0), lane = threadIdx.x % 32;
-    auto bar = [&](int i) -> uint32_t { return sbase + C::BAR + 8u * static_cast<uint32_t>(i); };
-    uint32_t* tmem_at = reinterpret_cast<uint32_t*>(smem + C::TMEM_AT);
-    Columns* cols = reinterpret_cast<Columns*>(smem + C::COLS);
-    int2* meta = reinterpret_cast<int2*>(smem + C::META);
+    auto bar = [&](int i) -> uint32_t { return sbase + static_cast<uint32_t>(l.bars) + 8u * static_cast<uint32_t>(i); };
+    Columns* cols = reinterpret_cast<Columns*>(smem + l.cols);
+    int2* ids = reinterpret_cast<int2*>(smem + l.ids);
 
-    grid_dep_wait();
-    const int part = blockIdx.x % w.parts;
-    Unit u;
-    if (!unit_of(w, blockIdx.x / w.parts, u))
-        return;
-    const int n = w.cols, rows = min(u.rows, n);
-    if (u.rows > n && threadIdx.x == 0)
-        *g.c.bad = 1u;
-    const int tiles = (u.length + KEYS - 1) / KEYS;
-    if (part >= tiles)
-        return;
-    const uint32_t columns = C::columns(n);
     if (threadIdx.x == 0) {
-        mbar_init(bar(C::QFULL), COPY_WARP);
-        for (int i = 0; i < C::STAGES; ++i) {
-            mbar_init(bar(C::RFULL + i), 1);
-            mbar_init(bar(C::REMPTY + i), 4);
+        for (int i = 0; i < MAX_STAGES; ++i) {
+            mbar_init(bar(F_RFULL + i), 1);
+            mbar_init(bar(F_REMPTY + i), 4);
         }
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(bar(C::KFULL + i), 4);
-            mbar_init(bar(C::KEMPTY + i), 1);
-            mbar_init(bar(C::SFULL + i), 1);
-            mbar_init(bar(C::SEMPTY + i), 4);
+        for (int i = 0; i < GROUPS; ++i) {
+            mbar_init(bar(F_KFULL + i), 4);
+            mbar_init(bar(F_KEMPTY + i), 1);
+            mbar_init(bar(F_SFULL + i), 1);
+            mbar_init(bar(F_SEMPTY + i), 4);
         }
-        mbar_init(bar(C::DRAIN), 1);
+        for (int i = 0; i < MAX_Q; ++i) {
+            mbar_init(bar(F_QFULL + i), ROW_WARPS);
+            mbar_init(bar(F_QEMPTY + i), 1 + 4 * GROUPS);
+        }
+        mbar_init(bar(F_DRAIN), 1);
         fence_barrier_init();
+        total = 0;
+    }
+    grid_dep_wait();
+    // this CTA's share of all tiles: where it begins
+    long long sum = 0;
+    for (int b = threadIdx.x; b < g.c.batch; b += FEW_THREADS)
+        sum += Walk::tiles_of(w, b);
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1)
+        sum += __shfl_xor_sync(0xffffffffu, sum, d);
+    if (lane == 0)
+        warp_sum[warp] = sum;
+    __syncthreads();
+    long long all = 0;
+    for (int i = 0; i < FEW_WARPS; ++i)
+        all += warp_sum[i];
+    all *= g.c.kv_heads;
+    const long long c0 = all * blockIdx.x / gridDim.x, c1 = all * (blockIdx.x + 1) / gridDim.x;
+    if (c0 == c1)
+        return;
+    for (int b0 = 0; b0 < g.c.batch; b0 += FEW_THREADS) {
+        const int b = b0 + threadIdx.x;
+        const long long mine = b < g.c.batch ? static_cast<long long>(Walk::tiles_of(w, b)) * g.c.kv_heads : 0;
+        long long to = mine;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const long long v = __shfl_up_sync(0xffffffffu, to, d);
+            to += lane >= d ? v : 0;
+        }
+        __syncthreads();   // the sums of the round before are read
+        if (lane == 31)
+            warp_sum[warp] = to;
+        __syncthreads();
+        to += total;
+        for (int i = 0; i < warp; ++i)
+            to += warp_sum[i];
+        if (to - mine <= c0 && c0 < to) {
+            first_b = b;
+            skip = c0 - (to - mine);
+        }
+        __syncthreads();
+        if (threadIdx.x == FEW_THREADS - 1)
+            total = to;
     }
     if (warp == MMA_WARP) {
-        tmem_alloc(smem_u32(tmem_at), 2 * columns);
+        tmem_alloc(smem_u32(&tmem_at), 512);
         tmem_relinquish();
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = *tmem_at;
-
-    if (warp < COPY_WARP) {   // the rows, while the first codes are on their way
-        for (int r = warp; r < n; r += COPY_WARP) {
-            const bool there = r < rows;
-            const long long token = u.first + r / g.group;
-            const int h = u.head * g.group + r % g.group;
-            put_row<D, T>(g, there ? static_cast<const T*>(g.q.data) + token * g.q.tok + h * g.q.head : nullptr,
-                          there ? g.stats[token * g.heads + h] : make_float2(0.0f, 0.0f), there ? u.pos0 + r / g.group : -1,
-                          smem + C::Q, C::PARTS * n, r, n, cols, lane);
-        }
+    const uint32_t tmem = tmem_at;
+    const int n = w.cols, q_bytes = C::PARTS * C::KB * n * 128;
+    Walk walk(w, first_b, skip, c1 - c0);
+    const Unit& u = walk.u;
+    Run run;
+    bool ok = true;
+    // the first run's rows: by all, but the warps that copy, which have begun
+    if (warp < COPY_WARP) {
+        walk.u.head = walk.head;
+        put_rows<D, T>(g, u, n, warp, COPY_WARP, smem, cols, lane);
         fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0)
-            mbar_arrive(bar(C::QFULL));
+        named_bar_sync(1, COPY_WARP * 32);
     }
 
-    // the CTA's tiles are part, part + parts, ...; those of which no key is seen are passed over
-    auto seen = [&](int tile) { return any_seen(g, u.plo, u.phi, tile * KEYS, KEYS); };
-    bool ok = true;
-    int step = 0;   // tiles so far of which a key is seen
-    if (warp < 4) {
+    if (warp < SUM_WARP) {
         // ------------------------------------------------------------ widening
-        const int t = threadIdx.x;
-        for (int tile = part; ok && tile < tiles; tile += w.parts) {
-            if (!seen(tile))
-                continue;
-            const int buf = step % 2, stage = step % C::STAGES;
-            ok = warp_wait(w, bar(C::RFULL + stage), step / C::STAGES & 1) &&
-                 warp_wait(w, bar(C::KEMPTY + buf), (step / 2 & 1) ^ 1);
-            if (!ok)
-                break;
-            const int2 there = meta[stage];
-            KeyCodes<D> codes;
-            codes.get(smem + C::RING + stage * C::STAGE + t / KV_PAGE * C::HALF, t % KV_PAGE, t < KV_PAGE ? there.x : there.y);
-            codes.widen(smem + buf * C::K_BYTES, t);
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) {
-                mbar_arrive(bar(C::KFULL + buf));
-                mbar_arrive(bar(C::REMPTY + stage));
-            }
-            ++step;
-        }
-    } else if (warp == MMA_WARP) {
-        // ------------------------------------------------------------ products
-        const uint32_t lead = elect_one(), idesc = idesc_f16_f32(KEYS, C::PARTS * n);
-        ok = warp_wait(w, bar(C::QFULL), 0);
-        for (int tile = part; ok && tile < tiles; tile += w.parts) {
-            if (!seen(tile))
-                continue;
-            const int buf = step % 2;
-            ok = warp_wait(w, bar(C::KFULL + buf), step / 2 & 1) && warp_wait(w, bar(C::SEMPTY + buf), (step / 2 & 1) ^ 1);
-            if (!ok)
-                break;
-            tc_fence_after();
-            product<D, 1>(lead, tmem + buf * columns, sbase + buf * C::K_BYTES, sbase + C::Q, C::PARTS * n * 128, idesc);
-            umma_commit_by(lead, bar(C::SFULL + buf));
-            umma_commit_by(lead, bar(C::KEMPTY + buf));
-            ++step;
-        }
-        umma_commit_by(lead, bar(C::DRAIN));
-        if (lead)
-            mbar_drain_wait(bar(C::DRAIN), 0, WAIT_LIMIT_NS, g.wc.err);
-        __syncwarp();
-    } else if (warp == COPY_WARP) {
-        // ------------------------------------------------------------ codes: the keys of two pages a step
-        // ids of 16 tiles at a time, two lanes each, and those of the next 16 on their way
-        auto ids_of = [&](long long k) {
-            const long long tile = part + (k + lane / 2) * w.parts, i = 2 * tile + lane % 2;
-            return tile < tiles && i * KV_PAGE < u.length ? u.table[i] : -1;
-        };
-        int ids = -1, later = ids_of(0);
-        for (int k = 0, tile = part; tile < tiles; ++k, tile += w.parts) {
-            if (k % 16 == 0) {
-                ids = later < g.c.num_pages ? later : -1;
-                later = ids_of(k + 16);
-            }
-            if (!seen(tile))
-                continue;
-            const int p0 = __shfl_sync(0xffffffffu, ids, k % 16 * 2), p1 = __shfl_sync(0xffffffffu, ids, k % 16 * 2 + 1);
-            const int stage = step % C::STAGES;
-            ok = warp_wait(w, bar(C::REMPTY + stage), (step / C::STAGES & 1) ^ 1);
-            if (!ok)
-                break;
-            if (lane == 0) {
-                meta[stage] = make_int2(p0 >= 0, p1 >= 0);
-                fence_proxy_async_smem();   // the stage was read with ordinary loads
-                mbar_arrive_expect_tx(bar(C::RFULL + stage), ((p0 >= 0) + (p1 >= 0)) * C::HALF);
-                const uint32_t dst = sbase + C::RING + stage * C::STAGE;
-                const size_t piece = static_cast<size_t>(g.c.kv_heads) * P::BYTES;
-                const uint8_t* src = g.c.pages + static_cast<size_t>(u.head) * P::BYTES;
-                if (p0 >= 0)
-                    bulk_g2s(dst, src + p0 * piece, C::HALF, bar(C::RFULL + stage));
-                if (p1 >= 0)
-                    bulk_g2s(dst + C::HALF, src + p1 * piece, C::HALF, bar(C::RFULL + stage));
-            }
-            ++step;
-        }
-        if (lane == 0)   // the last fill of each stage lands before the CTA ends
-            for (int i = max(0, step - C::STAGES); i < step; ++i)
-                mbar_drain_wait(bar(C::RFULL + i % C::STAGES), i / C::STAGES & 1, WAIT_LIMIT_NS, g.wc.err);
-        __syncwarp();
-    } else {
-        // ------------------------------------------------------------ sums: a thread a key
-        const int buf = warp / 4 - 1, t = threadIdx.x % KEYS;
-        const uint32_t s_at = tmem + buf * columns + (static_cast<uint32_t>(t & ~31) << 16);
-        int unseen = 0;   // tiles so far of which no key is seen; they go to the warpgroups in turn too
-        // the warpgroup's next tile from `tile` on, and whether S has it
-        auto next = [&](int tile, bool& used) {
-            for (; tile < tiles; tile += w.parts) {
-                used = seen(tile);
-                if ((used ? step++ : unseen++) % 2 != buf)
-                    continue;
-                if (used || w.in != w.out || w.decay != 1.0f || tile * KEYS + KEYS > u.pos0)
-                    return tile;   // else nothing changes
-            }
-            return tile;
-        };
-        auto page_of = [&](int tile) { return tile < tiles && tile * KEYS + t < u.length ? u.table[(tile * KEYS + t) / KV_PAGE] : -1; };
-        auto place = [&](int page, int tile) {
-            return (static_cast<size_t>(page) * g.c.kv_heads + u.head) * KV_PAGE + (tile * KEYS + t) % KV_PAGE;
-        };
-        auto had = [&](int page, int tile) {
-            return page >= 0 && page < g.c.num_pages && tile * KEYS + t < u.pos0 ? w.in[place(page, tile)] : 0.0f;
-        };
-        // what the next tile had is on its way while this one's weights are added up, and the page of
-        // the one after that
-        bool used = false, used1 = false, used2 = false;
-        int tile = next(part, used), tile1 = tile < tiles ? next(tile + w.parts, used1) : tile;
-        int page = page_of(tile), page1 = page_of(tile1), turn = 0;
-        float old = had(page, tile);
-        ok = warp_wait(w, bar(C::QFULL), 0);
-        while (ok && tile < tiles) {
-            const int tile2 = tile1 < tiles ? next(tile1 + w.parts, used2) : tile1, page2 = page_of(tile2);
-            const float old1 = had(page1, tile1);
-            float2 sum = make_float2(0.0f, 0.0f);
-            if (used) {
-                ok = warp_wait(w, bar(C::SFULL + buf), turn & 1);
+        const int t = threadIdx.x % KEYS, group = warp / 4;
+        const uint32_t k_at = tmem + GROUPS * l.columns + group * C::K_COLUMNS + (static_cast<uint32_t>(t & ~31) << 16);
+        int step = 0, turn = group, visit = 0;   // of the run's first seen tile; steps until the group's next; its steps
+        if (group >= l.kbufs)
+            ok = false;   // two groups have to do
+        while (ok && walk.next(run)) {
+            for (; turn < run.n; turn += l.kbufs, ++visit) {
+                const int at = step + turn, stage = at & (l.stages - 1);
+                ok = warp_wait(w, bar(F_KEMPTY + group), (visit & 1) ^ 1) && warp_wait(w, bar(F_RFULL + stage), at >> l.stage_bits & 1);
                 if (!ok)
                     break;
-                ++turn;
+                tc_fence_after();
+                const int2 page = ids[stage];
+                KeyCodes<D> codes;
+                codes.get(smem + l.ring + stage * C::STAGE + t / KV_PAGE * C::HALF, t % KV_PAGE,
+                          (t < KV_PAGE ? page.x : page.y) >= 0);
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(bar(F_REMPTY + stage));
+#pragma unroll
+                for (int gr = 0; gr < D / 32; ++gr) {
+                    uint32_t v[16];
+                    codes.widen(gr, v);
+                    tmem_store16(k_at + 16 * gr, v);
+                }
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(bar(F_KFULL + group));
+            }
+            turn -= run.n;
+            step += run.n;
+        }
+    } else if (warp < ROW_WARP) {
+        // ------------------------------------------------------------ sums: a thread a key
+        const int group = (warp - SUM_WARP) / 4, t = threadIdx.x % KEYS;
+        const uint32_t s_at = tmem + group * l.columns + (static_cast<uint32_t>(t & ~31) << 16);
+        const bool still = w.in == w.out && w.decay == 1.0f, both = C::PARTS == 2 && C::side_by_side(n);
+        const size_t page_floats = static_cast<size_t>(g.c.kv_heads) * KV_PAGE;
+        int turn = group, visit = 0;   // steps until the group's next; its steps
+        Turn q;
+        while (ok && walk.next(run)) {
+            const int rows = min(u.rows, n);
+            const float* in = w.in + u.head * KV_PAGE + t % KV_PAGE;
+            float* out = w.out + u.head * KV_PAGE + t % KV_PAGE;
+            // the page of this thread's key of a tile, if the pool has it
+            auto page_of = [&](int tile) {
+                const int key = tile * KEYS + t;
+                const int page = key < u.length ? u.table[key / KV_PAGE] : -1;
+                return page < g.c.num_pages ? page : -1;
+            };
+            auto had = [&](int page, int tile) { return page >= 0 && tile * KEYS + t < u.pos0 ? in[page * page_floats] : 0.0f; };
+            // tiles without a key that is seen; with decay 1 in place nothing changes but for new tokens
+            for (int tile = still ? max(run.t0, max(u.pos0, 0) / KEYS) : run.t0; tile < run.t1; ++tile) {
+                if (tile < run.t0 + run.n1 || (tile >= run.second && tile < run.second + run.n - run.n1) || tile % GROUPS != group)
+                    continue;
+                const int page = page_of(tile);
+                if (page >= 0)
+                    out[page * page_floats] = w.decay * had(page, tile);
+                else if (tile * KEYS + t < u.length)
+                    *g.c.bad = 1u;
+            }
+            // what a key had, and the page of the one after, are on their way while a tile is added up
+            int i = turn, page = -1, page1 = -1;
+            float old = 0.0f;
+            if (i < run.n) {
+                page = page_of(run.tile(i));
+                if (i + GROUPS < run.n)
+                    page1 = page_of(run.tile(i + GROUPS));
+                old = had(page, run.tile(i));
+            }
+            ok = warp_wait(w, bar(F_QFULL + q.i), q.round);
+            for (; ok && i < run.n; i += GROUPS, ++visit) {
+                const int tile = run.tile(i), key = tile * KEYS + t;
+                const bool more = i + GROUPS < run.n;
+                const float old1 = more ? had(page1, run.tile(i + GROUPS)) : 0.0f;
+                const int page2 = i + 2 * GROUPS < run.n ? page_of(run.tile(i + 2 * GROUPS)) : -1;
+                ok = warp_wait(w, bar(F_SFULL + group), visit & 1);
+                if (!ok)
+                    break;
                 tc_fence_after();
                 const bool plain = rows % 4 == 0 && all_seen(g, u.plo, u.phi, tile * KEYS, KEYS);
-                for (int c = 0; c < rows; c += 16) {
-                    float x[16];
-                    if constexpr (C::PARTS == 2) {
-                        float lo[16];
-                        tmem_ld16x2_wait(s_at + c, s_at + n + c, x, lo);
-#pragma unroll
-                        for (int i = 0; i < 16; ++i)
-                            x[i] += lo[i];
-                    } else {
-                        tmem_ld16_wait(s_at + c, x);
-                    }
-                    if (c + 16 >= rows) {
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0)
-                            mbar_arrive(bar(C::SEMPTY + buf));
-                    }
+                float2 got = make_float2(0.0f, 0.0f);
+                auto add = [&](const float (&x)[8], int c) {
                     if (plain)
-                        add_columns<false>(g, x, cols, c, rows, tile * KEYS + t, sum);
+                        add_columns<false>(g, x, cols + q.i, c, rows, key, got);
                     else
-                        add_columns<true>(g, x, cols, c, rows, tile * KEYS + t, sum);
+                        add_columns<true>(g, x, cols + q.i, c, rows, key, got);
+                };
+                for (int c = 0; c < rows; c += both ? 8 : 16) {
+                    float x[8], y[8];   // 8 columns and their low parts, or the 8 after them
+                    tmem_ld8x2_wait(s_at + c, s_at + c + (both ? n : 8), x, y);
+                    if (c + (both ? 8 : 16) >= rows)
+                        release(bar(F_SEMPTY + group), lane);
+                    if (both) {
+#pragma unroll
+                        for (int j = 0; j < 8; ++j)
+                            x[j] += y[j];
+                    }
+                    add(x, c);
+                    if (!both)
+                        add(y, c + 8);
                 }
+                if (page >= 0)
+                    out[page * page_floats] = (key < u.pos0 ? w.decay * old : 0.0f) + (got.x + got.y);
+                page = page1;
+                page1 = page2;
+                old = old1;
             }
-            if (page >= 0 && page < g.c.num_pages)
-                w.out[place(page, tile)] = w.decay * old + (sum.x + sum.y);
-            else if (tile * KEYS + t < u.length)
-                *g.c.bad = 1u;
-            tile = tile1;
-            page = page1;
-            used = used1;
-            old = old1;
-            tile1 = tile2;
-            page1 = page2;
-            used1 = used2;
+            turn = i - run.n;
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(bar(F_QEMPTY + q.i));
+            q.next(l.qbufs);
         }
+    } else if (warp < COPY_WARP) {
+        // ------------------------------------------------------------ rows
+        Turn q;
+        for (bool first = true; ok && walk.next(run); first = false) {
+            if (!first) {
+                ok = warp_wait(w, bar(F_QEMPTY + q.i), q.round ^ 1u);
+                if (!ok)
+                    break;
+                put_rows<D, T>(g, u, n, warp - ROW_WARP, ROW_WARPS, smem + q.i * q_bytes, cols + q.i, lane);
+                fence_proxy_async_smem();
+            }
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(bar(F_QFULL + q.i));
+            q.next(l.qbufs);
+        }
+    } else if (warp < MMA_WARP) {
+        // ------------------------------------------------------------ codes
+        // two lanes a tile, one for each of its pages
+        const int mine = lane / 2 % BATCH, half = lane % 2;
+        const bool act_lane = lane < 2 * BATCH;
+        int step = 0;       // of the run's first seen tile
+        uint32_t asked = 0, odd = 0;    // bit s: this lane has filled stage s; in an odd round last
+        while (ok && walk.next(run)) {
+            auto id_of = [&](int i) {
+                const int p = 2 * run.tile(i) + half;
+                return act_lane && i < run.n && p * KV_PAGE < u.length ? u.table[p] : -1;
+            };
+            // batches are counted over all runs, so that the warps take turns
+            const int from = step / BATCH;
+            auto base_of = [&](int batch) { return (from + batch) * BATCH - step; };   // the batch's first tile in the run
+            int batch = (from % COPY_WARPS == warp - COPY_WARP) ? 0 : 1;
+            int page = base_of(batch) + mine >= 0 ? id_of(base_of(batch) + mine) : -1;
+            for (; base_of(batch) < run.n; batch += COPY_WARPS) {
+                const int i = base_of(batch) + mine;
+                const int page_next = id_of(base_of(batch + COPY_WARPS) + mine);
+                const bool act = act_lane && i >= 0 && i < run.n;
+                if (page >= g.c.num_pages || (page < 0 && act && (2 * run.tile(i) + half) * KV_PAGE < u.length)) {
+                    *g.c.bad = 1u;
+                    page = -1;
+                }
+                const int at = (step + max(i, 0)) & (l.stages - 1);
+                const uint32_t round = (step + max(i, 0)) >> l.stage_bits & 1;
+                ok = __all_sync(0xffffffffu, !act || wait(w, bar(F_REMPTY + at), round ^ 1u));
+                if (!ok)
+                    break;
+                const int other = __shfl_xor_sync(0xffffffffu, page, 1);
+                if (act && half == 0) {
+                    ids[at] = make_int2(page, other);
+                    mbar_arrive_expect_tx(bar(F_RFULL + at), ((page >= 0) + (other >= 0)) * C::HALF);
+                    asked |= 1u << at;
+                    odd = (odd & ~(1u << at)) | round << at;
+                }
+                __syncwarp();
+                if (act && page >= 0) {
+                    fence_proxy_async_smem();   // the stage was read with ordinary loads
+                    bulk_g2s(sbase + l.ring + at * C::STAGE + half * C::HALF,
+                             g.c.pages + (static_cast<size_t>(page) * g.c.kv_heads + u.head) * P::BYTES, C::HALF,
+                             bar(F_RFULL + at));
+                }
+                page = page_next;
+            }
+            step += run.n;
+        }
+        // the last fill of each stage lands before the CTA ends
+        for (int s = 0; s < l.stages; ++s)
+            if (asked >> s & 1u)
+                mbar_drain_wait(bar(F_RFULL + s), odd >> s & 1u, WAIT_LIMIT_NS, g.wc.err);
+        __syncwarp();
+    } else {
+        // ------------------------------------------------------------ products
+        const uint32_t lead = elect_one();
+        const bool both = C::PARTS == 2 && C::side_by_side(n);
+        const uint32_t idesc = idesc_f16_f32(KEYS, both ? 2 * n : n);
+        const int block = C::PARTS * n * 128;
+        Turn q, k, s;
+        while (ok && walk.next(run)) {
+            ok = warp_wait(w, bar(F_QFULL + q.i), q.round);
+            const uint32_t rows = sbase + q.i * q_bytes;
+            for (int i = 0; ok && i < run.n; ++i) {
+                ok = warp_wait(w, bar(F_KFULL + k.i), k.round) && warp_wait(w, bar(F_SEMPTY + s.i), s.round ^ 1u);
+                if (!ok)
+                    break;
+                tc_fence_after();
+                // lo first, while the sums, cut toward zero, are small
+                for (int part = C::PARTS == 1 || both ? 0 : 1; part >= 0; --part)
+#pragma unroll
+                    for (int kb = 0; kb < C::KB; ++kb) {
+                        const uint64_t b = sdesc_k_sw128(rows + kb * block + part * n * 128);
+#pragma unroll
+                        for (int kk = 0; kk < 4; ++kk)
+                            umma_f16_ts_by(lead, tmem + s.i * l.columns,
+                                           tmem + GROUPS * l.columns + k.i * C::K_COLUMNS + 32 * kb + 8 * kk,
+                                           b + 2u * kk, idesc, (kb || kk || (C::PARTS == 2 && !both && part == 0)) ? 1u : 0u);
+                    }
+                umma_commit_by(lead, bar(F_SFULL + s.i));
+                umma_commit_by(lead, bar(F_KEMPTY + k.i));
+                k.next(l.kbufs);
+                s.next(GROUPS);
+            }
+            if (ok)
+                umma_commit_by(lead, bar(F_QEMPTY + q.i));
+            q.next(l.qbufs);
+        }
+        umma_commit_by(lead, bar(F_DRAIN));
+        if (lead)
+            mbar_drain_wait(bar(F_DRAIN), 0, WAIT_LIMIT_NS, g.wc.err);
+        __syncwarp();
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     if (warp == MMA_WARP)
-        tmem_dealloc(tmem, 2 * columns);
+        tmem_dealloc(tmem, 512);
 }
 
 // ------------------------------------------------------------------ many rows
@@ -507,8 +785,11 @@ __global__ void __launch_bounds__(256) kv_weigh_rows_kernel(const WeighArgs w)
         const int row = (r - first) * g.group + h % g.group;
         uint8_t* record = w.operands +
                           (h / g.group * w.tiles + first_tile(g, first, b) + row / MOST_ROWS) * static_cast<long long>(C::RECORD);
-        put_row<D, T>(g, static_cast<const T*>(g.q.data) + r * g.q.tok + h * g.q.head, g.stats[static_cast<size_t>(r) * g.heads + h],
-                      pos, record, MOST_ROWS, row % MOST_ROWS, C::KB * MOST_ROWS, reinterpret_cast<Columns*>(record + C::Q_BYTES), lane);
+        const float2 stats = g.stats[static_cast<size_t>(r) * g.heads + h];
+        float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (stats.y > 0.0f && lane < D / 4)
+            x = load4(static_cast<const T*>(g.q.data) + r * g.q.tok + h * g.q.head + 4 * lane, g.wide);
+        put_row<D, T>(g, x, stats, pos, record, MOST_ROWS, row % MOST_ROWS, C::KB * MOST_ROWS, reinterpret_cast<Columns*>(record + C::Q_BYTES), lane);
     }
 }
 
@@ -530,7 +811,8 @@ __global__ void __launch_bounds__(MANY_THREADS, 1) kv_weigh_many_kernel(const We
     // early keys are seen by the most rows: their CTAs come first
     const int units = g.c.batch * g.c.kv_heads, part = blockIdx.x / units;
     Unit u;
-    if (!unit_of(w, blockIdx.x % units, u))
+    const int unit = blockIdx.x % units;
+    if (!unit_of(w, unit / g.c.kv_heads, unit % g.c.kv_heads, u))
         return;
     const int groups = (u.length + GROUP - 1) / GROUP;
     if (part >= groups)
@@ -742,23 +1024,13 @@ cudaError_t launch_weigh(WeighArgs a, long long keys, cudaStream_t s)
         return static_cast<int>(want < 1 ? 1 : want);
     };
     if (a.tiles == 0) {
-        using C = Few<D, T>;
         static std::atomic<uint64_t> done{0};
-        cudaError_t e = kv_allow_smem(kv_weigh_few_kernel<D, T>, C::bytes(MOST_ROWS) > 116 * 1024 ? C::bytes(MOST_ROWS) : 116 * 1024, &done);
+        cudaError_t e = kv_allow_smem(kv_weigh_few_kernel<D, T>, 226 * 1024, &done);
         if (e != cudaSuccess)
             return e;
-        // no more CTAs to an SM than its 512 columns of tensor memory are enough for
-        const int resident = 512 / (2 * C::columns(a.cols));
-        int bytes = C::bytes(a.cols);
-        const int least = 227 * 1024 / (resident + 1);
-        bytes = bytes > least ? bytes : least;
-        const long long tiles = (keys + KEYS - 1) / KEYS, slots = 152ll * (227 * 1024 / (bytes + 1024));
-        // the chip once over, or CTAs of 16 steps where lengths are uneven
-        const long long even = slots / units, uneven = tiles / 16;
-        a.parts = parts(tiles, even > uneven ? even : uneven);
+        const FewLayout l = Few<D, T>::layout(a.cols);
         count_launch();
-        return launch_dependent_smem(kv_weigh_few_kernel<D, T>, dim3(static_cast<unsigned int>(units * a.parts)),
-                                     dim3(FEW_WARPS * 32), static_cast<size_t>(bytes), s, a);
+        return launch_dependent_smem(kv_weigh_few_kernel<D, T>, dim3(152), dim3(FEW_THREADS), static_cast<size_t>(l.bytes), s, a, l);
     }
     using C = Many<D, T>;
     static std::atomic<uint64_t> done{0};
