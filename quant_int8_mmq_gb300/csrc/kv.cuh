@@ -282,6 +282,10 @@ struct AttendArgs {
     float* part;           // nsplit > 1: [nsplit][ntok * heads][D] unnormalised sums
     float2* part_ml;       //             [nsplit][ntok * heads] {reference, sum}
     float2* stats;         // null, or [ntok * heads] {reference, 1 / sum}, {0, 0} of a row without keys
+    float* scores;         // kv_step.cu: null, or the scores of each key that a row looks at, -inf where it sees
+                           // none: [sequence][kv head][score_pages][score_rows][64], in units of `coef`
+    float* coef;           // with scores: [sequence][kv head][score_rows], what makes them powers of two
+    int score_pages, score_rows;
     WaitCtl wc;
 };
 // What kv_weigh.cu needs of a row to compute its weights again; a row whose sum is no positive
@@ -371,6 +375,7 @@ struct WeighArgs {
     float* out;
     float decay;
     int max_q;             // new tokens of a sequence that count
+    int tile_rows;         // kv_finish_weights_kernel: rows of the attention's tiles
     int cols;              // kv_weigh_few_kernel: rows as a column count, a multiple of 16 up to 128
     long long tiles;       // kv_weigh_many_kernel: operand tiles of a kv head in the workspace; 0: few rows
     uint8_t* operands;
@@ -380,6 +385,8 @@ struct WeighArgs {
 size_t weigh_bytes(int dtype, int heads, int kv_heads, int dim, int batch, int ntok, int max_q, int* cols,
                    long long* tiles);
 cudaError_t launch_kv_weigh(const WeighArgs& a, int dim, int dtype, int max_kv, cudaStream_t s);
+// The same from the scores that kv_step.cu has left.
+cudaError_t launch_kv_finish_weights(const WeighArgs& a, int dim, int dtype, int max_kv, cudaStream_t s);
 
 struct RopeView;
 cudaError_t launch_rope(const KvRows& x, const KvRows& out, const int* pos, const RopeView& r, int dtype, int heads,

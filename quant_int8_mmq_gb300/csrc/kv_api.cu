@@ -222,16 +222,31 @@ AttendPlan plan(const mmq_kv_cache* c, int dtype, int heads, int ntok, int max_q
 // What the weights need in the workspace beside the attention's: {reference, 1 / sum} of each row,
 // then the rows as operands.
 struct WeighPlan {
-    size_t stats_bytes, operand_bytes;
-    int cols;
+    size_t stats_bytes, operand_bytes, score_bytes, coef_bytes;   // scores: of the step kernel
+    int cols, score_pages, score_rows;
     long long tiles;
 };
-WeighPlan weigh_plan(const mmq_kv_cache* c, int dtype, int heads, int ntok, int max_q)
+WeighPlan weigh_plan(const mmq_kv_cache* c, const AttendPlan& attend, int dtype, int heads, int ntok, int max_q,
+                     int max_kv)
 {
-    WeighPlan p;
+    WeighPlan p = {};
     p.stats_bytes = (static_cast<size_t>(ntok) * static_cast<size_t>(heads) * sizeof(float2) + 15) / 16 * 16;
     p.operand_bytes = mmq::weigh_bytes(dtype, heads, c->kv_heads, c->head_dim, c->batch, ntok, max_q < 1 ? 1 : max_q,
                                        &p.cols, &p.tiles);
+    // A few rows' scores are kept, unless they are more than a gigabyte (a batch of long tables without a
+    // max_kv); the keys are then read again.
+    if (attend.kernel == 0) {
+        const long long pages = (static_cast<long long>(max_kv < 1 ? 1 : max_kv) + mmq::KV_PAGE - 1) / mmq::KV_PAGE;
+        p.score_pages = static_cast<int>(pages < c->max_pages ? pages : c->max_pages);
+        p.score_rows = (max_q < 1 ? 1 : max_q < ntok ? max_q : ntok) * (heads / c->kv_heads);
+        const size_t rows = static_cast<size_t>(c->batch) * c->kv_heads * p.score_rows;
+        p.score_bytes = rows * p.score_pages * mmq::KV_PAGE * sizeof(float);
+        p.coef_bytes = (rows * sizeof(float) + 15) / 16 * 16;
+        if (p.score_bytes > size_t{1} << 30)
+            p.score_bytes = p.coef_bytes = 0;
+        else
+            p.operand_bytes = 0;
+    }
     return p;
 }
 
@@ -260,8 +275,8 @@ mmq_status attend(const mmq_kv_cache* c, const mmq_rows* q, const mmq_rows* out,
     if (ntok == 0)
         return MMQ_OK;
     const AttendPlan p = plan(c, q->dtype, heads, ntok, max_q, max_kv, window, sinks);
-    const WeighPlan wp = weights ? weigh_plan(c, q->dtype, heads, ntok, max_q) : WeighPlan{};
-    const size_t need = p.part_bytes + p.ml_bytes + wp.stats_bytes + wp.operand_bytes;
+    const WeighPlan wp = weights ? weigh_plan(c, p, q->dtype, heads, ntok, max_q, max_kv) : WeighPlan{};
+    const size_t need = p.part_bytes + p.ml_bytes + wp.stats_bytes + wp.operand_bytes + wp.coef_bytes + wp.score_bytes;
     if (need > 0) {
         if (!workspace || workspace_bytes < need)
             return MMQ_ERR_ARG;
@@ -297,8 +312,15 @@ mmq_status attend(const mmq_kv_cache* c, const mmq_rows* q, const mmq_rows* out,
     a.wide = wide(q, four) && wide(out, four);
     a.part = static_cast<float*>(workspace);
     a.part_ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(workspace) + p.part_bytes);
+    uint8_t* rest = static_cast<uint8_t*>(workspace) + p.part_bytes + p.ml_bytes + wp.stats_bytes;
     if (weights)
-        a.stats = reinterpret_cast<float2*>(static_cast<uint8_t*>(workspace) + p.part_bytes + p.ml_bytes);
+        a.stats = reinterpret_cast<float2*>(rest - wp.stats_bytes);
+    if (wp.score_bytes > 0) {
+        a.coef = reinterpret_cast<float*>(rest);
+        a.scores = reinterpret_cast<float*>(rest + wp.coef_bytes);
+        a.score_pages = wp.score_pages;
+        a.score_rows = wp.score_rows;
+    }
     a.wc = {a.c.bad - 1, mmq::WAIT_LIMIT_NS, -1};
     bool injected = false;
     if (p.cluster == 1 && mmq::take_wait_ctl(&a.wc, &injected) != cudaSuccess)   // a cluster barrier has no time limit
@@ -309,9 +331,10 @@ mmq_status attend(const mmq_kv_cache* c, const mmq_rows* q, const mmq_rows* out,
         e = mmq::launch_kv_join(a, c->head_dim, q->dtype, reinterpret_cast<cudaStream_t>(s));
     if (e == cudaSuccess && weights) {
         a.wc = {a.c.bad - 1, mmq::WAIT_LIMIT_NS, -1};
-        const mmq::WeighArgs w = {a, weights->in, weights->out, weights->decay, max_q < 1 ? 1 : max_q, wp.cols, wp.tiles,
-                                  reinterpret_cast<uint8_t*>(a.stats) + wp.stats_bytes, 1};
-        e = mmq::launch_kv_weigh(w, c->head_dim, q->dtype, max_kv, reinterpret_cast<cudaStream_t>(s));
+        const mmq::WeighArgs w = {a, weights->in, weights->out, weights->decay, max_q < 1 ? 1 : max_q, p.tile_rows, wp.cols,
+                                  wp.tiles, rest, 1};
+        const auto weigh = a.scores ? mmq::launch_kv_finish_weights : mmq::launch_kv_weigh;
+        e = weigh(w, c->head_dim, q->dtype, max_kv, reinterpret_cast<cudaStream_t>(s));
     }
     return mmq::from_cuda(e);
 }
@@ -380,8 +403,9 @@ mmq_status mmq_kv_attend_weights_workspace_bytes(const mmq_kv_cache* c, int dtyp
 {
     const mmq_status st = mmq_kv_attend_workspace_bytes(c, dtype, heads, ntok, max_q, max_kv, window, sinks, bytes);
     if (st == MMQ_OK && ntok > 0) {
-        const WeighPlan p = weigh_plan(c, dtype, heads, ntok, max_q);
-        *bytes += p.stats_bytes + p.operand_bytes;
+        const WeighPlan p = weigh_plan(c, plan(c, dtype, heads, ntok, max_q, max_kv, window, sinks), dtype, heads, ntok, max_q,
+                                       max_kv);
+        *bytes += p.stats_bytes + p.operand_bytes + p.coef_bytes + p.score_bytes;
     }
     return st;
 }

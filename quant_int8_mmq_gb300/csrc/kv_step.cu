@@ -88,7 +88,9 @@ __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-template <int D, typename T, int MODE>
+// SCORES: the scores of the keys are left for kv_weigh.cu (a build of its own, so that the others
+// stay as they are).
+template <int D, typename T, int MODE, bool SCORES>
 __global__ void __launch_bounds__(WARPS * 32, MODE == WIDE ? 3 : D == 128 ? 4 : 6) kv_step_kernel(const AttendArgs g)
 {
     using P = Piece<D>;
@@ -228,8 +230,12 @@ __global__ void __launch_bounds__(WARPS * 32, MODE == WIDE ? 3 : D == 128 ? 4 : 
                 *reinterpret_cast<uint4*>(at) = make_uint4(hi.x, lo.x, hi.y, lo.y);
             }
         }
-        if (lane == 0)
-            *reinterpret_cast<float*>(smem + S::COEF + 4 * r) = fminf(fmaxf(g.scale_log2 * kv_pow2(e), 1e-38f), 1e38f);
+        if (lane == 0) {
+            const float coef = fminf(fmaxf(g.scale_log2 * kv_pow2(e), 1e-38f), 1e38f);
+            *reinterpret_cast<float*>(smem + S::COEF + 4 * r) = coef;
+            if (SCORES && r < nrow && row0 + r < g.score_rows)   // every part's CTAs write the same
+                g.coef[(static_cast<size_t>(b) * g.c.kv_heads + head) * g.score_rows + row0 + r] = coef;
+        }
     }
     __syncthreads();
 
@@ -364,6 +370,24 @@ __global__ void __launch_bounds__(WARPS * 32, MODE == WIDE ? 3 : D == 128 ? 4 : 
                     for (int e = 0; e < 2; ++e)
                         if ((m >> (8 * oct + e) & 1u) == 0)
                             x[oct][i][e] = -INFINITY;
+            }
+        }
+
+        if constexpr (SCORES) {
+            const int at = kbase / KV_PAGE;
+            if (at < g.score_pages) {
+                float* to = g.scores +
+                            ((static_cast<size_t>(b) * g.c.kv_heads + head) * g.score_pages + at) * g.score_rows * KV_PAGE + 2 * t;
+#pragma unroll
+                for (int i = 0; i < SETS; ++i) {
+                    const int row = n + 8 * i;
+                    if (row < nrow && row0 + row < g.score_rows) {
+#pragma unroll
+                        for (int oct = 0; oct < 8; ++oct)
+                            *reinterpret_cast<float2*>(to + (row0 + row) * KV_PAGE + 8 * oct) =
+                                make_float2(x[oct][i][0], x[oct][i][1]);
+                    }
+                }
             }
         }
 
@@ -654,12 +678,12 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) kv_join_kernel(const AttendAr
            v, g.wide);
 }
 
-template <int D, typename T, int MODE>
+template <int D, typename T, int MODE, bool SCORES>
 cudaError_t launch_step(const AttendArgs& a, cudaStream_t s)
 {
     constexpr int BYTES = StepSmem<D, MODE>::BYTES;
     static std::atomic<uint64_t> done{0};
-    const cudaError_t e = kv_allow_smem(kv_step_kernel<D, T, MODE>, BYTES, &done);
+    const cudaError_t e = kv_allow_smem(kv_step_kernel<D, T, MODE, SCORES>, BYTES, &done);
     if (e != cudaSuccess)
         return e;
     cudaLaunchAttribute at[2];
@@ -678,7 +702,12 @@ cudaError_t launch_step(const AttendArgs& a, cudaStream_t s)
     cfg.attrs = at;
     cfg.numAttrs = a.cluster > 1 ? 2 : 1;
     count_launch();
-    return cudaLaunchKernelEx(&cfg, kv_step_kernel<D, T, MODE>, a);
+    return cudaLaunchKernelEx(&cfg, kv_step_kernel<D, T, MODE, SCORES>, a);
+}
+template <int D, typename T, int MODE>
+cudaError_t launch_step(const AttendArgs& a, cudaStream_t s)
+{
+    return a.scores ? launch_step<D, T, MODE, true>(a, s) : launch_step<D, T, MODE, false>(a, s);
 }
 
 template <int D>

@@ -286,6 +286,31 @@ def test_a_whole_prompt_and_a_long_cache():
     weigh_and_check(Batch([700, 1], [2000, 900], 1, 128, BF16), 3, window=300, sinks=5)
 
 
+@pytest.mark.parametrize("dtype", [F32, F16, BF16])
+@pytest.mark.parametrize("dim,window,sinks", [(64, 0, 0), (128, 0, 0), (64, 200, 3), (128, 130, 70)])
+def test_more_scores_than_are_kept(dtype, dim, window, sinks):
+    """A table so wide that scores for all of it would be over a gigabyte: the keys are read again."""
+    lens = [1, 64, 129, 300, 5, 1000, 128, 2500]
+    b = Batch([1, 2, 1, 2, 1, 1, 1, 2], lens, 2, dim, dtype, max_pages=(1 << 30) // (256 * 8 * 2 * 8) + 1)
+    weigh_and_check(b, 8, window=window, sinks=sinks, decay=0.5)
+    q = b.q(8)
+    w = [weights_for(b) for _ in range(2)]
+    for x, most in zip(w, (2500, None)):                                # kept, and not
+        mmq.kv_attend_weights(q, x, *b.cache, 2, most, window=window, sinks=sinks)
+    assert not torch.equal(*w) and (w[0] - w[1]).abs().max() < 1e-4
+
+
+@pytest.mark.parametrize("dtype", [F32, F16, BF16])
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("hint", [1, 100, 130])
+def test_a_length_hint_that_is_too_low(dtype, dim, hint):
+    b = Batch([1, 2, 3], [200, 700, 90], 2, dim, dtype)
+    weigh_and_check(b, 6, max_kv=hint, decay=0.5)
+    weigh_and_check(b, 6, max_kv=hint, window=100, sinks=2)
+    weigh_and_check(Batch([40, 90], [300, 700], 2, dim, dtype), 4, max_kv=hint)
+    weigh_and_check(Batch([400], [900], 1, dim, dtype), 4, max_kv=hint)
+
+
 def test_every_row_gives_one_and_heads_add_up():
     b = Batch([9], [500], 2, 64)
     w = weights_for(b).zero_()
