@@ -1016,51 +1016,57 @@ __global__ void __launch_bounds__(MANY_THREADS, 1) kv_weigh_many_kernel(const We
 
 // ------------------------------------------------------------------ from scores
 // The attention for few rows has left its scores, so that K is not read again: 4 bytes a row and key
-// for the 72 of a key.  A warp has a page, a lane two keys.  Pages past the ones there was room
-// for (a max_kv that is too low) are computed here, value by value.
-constexpr int FINISH_WARPS = 4;
+// for the 72 of a key.  Half a warp has a page, a lane four keys.  Pages past the ones there was
+// room for (a max_kv that is too low) are computed here, value by value.
+constexpr int FINISH_WARPS = 4, FINISH_PAGES = 2 * FINISH_WARPS;   // of a CTA at once
 
 template <int D, typename T>
-__device__ __noinline__ float2 scores_again(const WeighArgs& w, const Unit& u, const uint8_t* piece, int row, int slot)
+__device__ __noinline__ float4 scores_again(const WeighArgs& w, const Unit& u, const uint8_t* piece, int row, int slot)
 {
     const AttendArgs& g = w.a;
     const T* q = static_cast<const T*>(g.q.data) + (u.first + row / g.group) * g.q.tok + (u.head * g.group + row % g.group) * g.q.head;
-    float2 x = make_float2(0.0f, 0.0f);
-    for (int h = 0; h < 2; ++h) {
-        float sum = 0.0f;
+    float x[4];
+#pragma unroll 1
+    for (int h = 0; h < 4; ++h) {
+        x[h] = 0.0f;
+#pragma unroll 1
         for (int gr = 0; gr < D / 32; ++gr) {
             const uint32_t* code = reinterpret_cast<const uint32_t*>(piece + Piece<D>::k_chunk(slot + h, gr));
             const float s = __half2float(*reinterpret_cast<const __half*>(piece + Piece<D>::k_scale(slot + h, gr)));
+#pragma unroll 1
             for (int i = 0; i < 32; ++i) {
                 const int n = code[i / 8] >> (4 * (i / 2 % 4) + 16 * (i % 2)) & 15;
-                sum = fmaf(Elt<T>::to(q[32 * gr + i]), s * static_cast<float>(n - 8), sum);
+                x[h] = fmaf(Elt<T>::to(q[32 * gr + i]), s * static_cast<float>(n - 8), x[h]);
             }
         }
-        (h ? x.y : x.x) = sum * g.scale_log2;
+        x[h] *= g.scale_log2;
     }
-    return x;
+    return make_float4(x[0], x[1], x[2], x[3]);
 }
 
 template <int D, typename T>
-__global__ void __launch_bounds__(FINISH_WARPS * 32) kv_finish_weights_kernel(const WeighArgs w)
+__global__ void __launch_bounds__(FINISH_WARPS * 32, 10) kv_finish_weights_kernel(const WeighArgs w)
 {
     const AttendArgs& g = w.a;
-    __shared__ float3 rows[MOST_ROWS];   // coefficient, reference, 1 / sum
-    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    __shared__ float4 rows[MOST_ROWS];   // coefficient, reference, 1 / sum
     grid_dep_wait();
     const int part = blockIdx.x % w.parts, unit = blockIdx.x / w.parts;
     Unit u;
     if (!unit_of(w, unit / g.c.kv_heads, unit % g.c.kv_heads, u))
         return;
     const int n = min(u.rows, g.score_rows), pages = (u.length + KV_PAGE - 1) / KV_PAGE;
+    if (part * FINISH_PAGES >= pages)
+        return;
     for (int r = threadIdx.x; r < n; r += FINISH_WARPS * 32) {
         const float2 stats = g.stats[(u.first + r / g.group) * static_cast<size_t>(g.heads) + u.head * g.group + r % g.group];
-        rows[r] = make_float3(g.coef[static_cast<size_t>(unit) * g.score_rows + r], stats.x, stats.y);
+        // a row that is no number adds nothing
+        rows[r] = make_float4(g.coef[static_cast<size_t>(unit) * g.score_rows + r], stats.x, stats.y, 0.0f);
     }
     __syncthreads();
     const bool still = w.in == w.out && w.decay == 1.0f;
-    for (int i = part * FINISH_WARPS + warp; i < pages; i += w.parts * FINISH_WARPS) {
-        const int kbase = i * KV_PAGE, key = kbase + 2 * lane;
+    const int slot = threadIdx.x % 16 * 4;
+    for (int i = part * FINISH_PAGES + threadIdx.x / 16; i < pages; i += w.parts * FINISH_PAGES) {
+        const int kbase = i * KV_PAGE, key = kbase + slot;
         const int page = u.table[i];
         if (page < 0 || page >= g.c.num_pages) {
             *g.c.bad = 1u;
@@ -1069,46 +1075,63 @@ __global__ void __launch_bounds__(FINISH_WARPS * 32) kv_finish_weights_kernel(co
         const bool used = any_seen(g, u.plo, u.phi, kbase, KV_PAGE);
         if (!used && still && kbase + KV_PAGE <= u.pos0)
             continue;   // nothing changes
-        const size_t piece = static_cast<size_t>(page) * g.c.kv_heads + u.head, at = piece * KV_PAGE + 2 * lane;
-        const float2 old = key < u.pos0 ? *reinterpret_cast<const float2*>(w.in + at) : make_float2(0.0f, 0.0f);
-        float2 sum = make_float2(0.0f, 0.0f);
+        const size_t piece = static_cast<size_t>(page) * g.c.kv_heads + u.head, at = piece * KV_PAGE + slot;
+        const float4 old = key < u.pos0 ? *reinterpret_cast<const float4*>(w.in + at) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         if (used) {
-            const float* scores = g.scores + (static_cast<size_t>(unit) * g.score_pages + i) * g.score_rows * KV_PAGE + 2 * lane;
-            const bool stored = i < g.score_pages;
+            const float* scores = g.scores + (static_cast<size_t>(unit) * g.score_pages + i) * g.score_rows * KV_PAGE + slot;
+            auto add = [&](float4 x, float coef, float4 c) {
+                if (c.z > 0.0f) {
+                    sum.x = fmaf(kv_ex2(fmaf(x.x, coef, -c.y)), c.z, sum.x);
+                    sum.y = fmaf(kv_ex2(fmaf(x.y, coef, -c.y)), c.z, sum.y);
+                    sum.z = fmaf(kv_ex2(fmaf(x.z, coef, -c.y)), c.z, sum.z);
+                    sum.w = fmaf(kv_ex2(fmaf(x.w, coef, -c.y)), c.z, sum.w);
+                }
+            };
             for (int r0 = 0; r0 < n; r0 += w.tile_rows) {
                 // a tile of the attention has looked at the pages that one of its rows sees
                 const int r1 = min(r0 + w.tile_rows, n);
                 const int plo = u.pos0 + r0 / g.group, phi = u.pos0 + (r1 - 1) / g.group;
-                if (kbase > phi)
+                if (kbase > phi || (g.window > 0 && i < max(plo - g.window + 1, 0) / KV_PAGE && kbase >= g.sinks))
                     continue;
-                if (g.window > 0 && i < max(plo - g.window + 1, 0) / KV_PAGE && kbase >= g.sinks)
+                if (i < g.score_pages) {
+                    for (int r = r0; r < r1; r += 4) {
+                        float4 x[4];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            x[k] = *reinterpret_cast<const float4*>(scores + min(r + k, r1 - 1) * KV_PAGE);
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            if (r + k < r1)
+                                add(x[k], rows[r + k].x, rows[r + k]);
+                    }
                     continue;
-#pragma unroll 4
+                }
                 for (int r = r0; r < r1; ++r) {
-                    const float3 c = rows[r];
-                    float2 x;
-                    float coef = c.x;
-                    if (stored) {
-                        x = *reinterpret_cast<const float2*>(scores + r * KV_PAGE);
-                    } else {
-                        x = scores_again<D, T>(w, u, g.c.pages + piece * Piece<D>::BYTES, r, 2 * lane);
-                        coef = 1.0f;
-                        const uint64_t m = kv_seen_bits(u.pos0 + r / g.group, kbase, g.window, g.sinks) >> (2 * lane);
-                        x.x = m & 1u ? x.x : -INFINITY;
-                        x.y = m & 2u ? x.y : -INFINITY;
-                    }
-                    if (c.z > 0.0f) {   // a row that is no number adds nothing
-                        sum.x = fmaf(kv_ex2(fmaf(x.x, coef, -c.y)), c.z, sum.x);
-                        sum.y = fmaf(kv_ex2(fmaf(x.y, coef, -c.y)), c.z, sum.y);
-                    }
+                    float4 x = scores_again<D, T>(w, u, g.c.pages + piece * Piece<D>::BYTES, r, slot);
+                    const uint64_t m = kv_seen_bits(u.pos0 + r / g.group, kbase, g.window, g.sinks) >> slot;
+                    x.x = m & 1u ? x.x : -INFINITY;
+                    x.y = m & 2u ? x.y : -INFINITY;
+                    x.z = m & 4u ? x.z : -INFINITY;
+                    x.w = m & 8u ? x.w : -INFINITY;
+                    add(x, 1.0f, rows[r]);
                 }
             }
         }
-        if (key + 1 < u.length)
-            *reinterpret_cast<float2*>(w.out + at) = make_float2((key < u.pos0 ? w.decay * old.x : 0.0f) + sum.x,
-                                                                 (key + 1 < u.pos0 ? w.decay * old.y : 0.0f) + sum.y);
-        else if (key < u.length)
-            w.out[at] = (key < u.pos0 ? w.decay * old.x : 0.0f) + sum.x;
+        const float4 got = make_float4((key < u.pos0 ? w.decay * old.x : 0.0f) + sum.x,
+                                       (key + 1 < u.pos0 ? w.decay * old.y : 0.0f) + sum.y,
+                                       (key + 2 < u.pos0 ? w.decay * old.z : 0.0f) + sum.z,
+                                       (key + 3 < u.pos0 ? w.decay * old.w : 0.0f) + sum.w);
+        if (key + 3 < u.length) {
+            *reinterpret_cast<float4*>(w.out + at) = got;
+        } else {
+            if (key < u.length)
+                w.out[at] = got.x;
+            if (key + 1 < u.length)
+                w.out[at + 1] = got.y;
+            if (key + 2 < u.length)
+                w.out[at + 2] = got.z;
+        }
     }
 }
 
@@ -1116,9 +1139,10 @@ template <int D, typename T>
 cudaError_t launch_finish(WeighArgs a, long long keys, cudaStream_t s)
 {
     const long long units = static_cast<long long>(a.a.c.batch) * a.a.c.kv_heads, pages = (keys + KV_PAGE - 1) / KV_PAGE;
-    // the chip's 16 CTAs an SM, or 8 pages a warp where lengths are uneven
-    long long parts = 16 * 152 / units > pages / 32 ? 16 * 152 / units : pages / 32;
-    parts = parts < (pages + FINISH_WARPS - 1) / FINISH_WARPS ? parts : (pages + FINISH_WARPS - 1) / FINISH_WARPS;
+    // the chip's 10 CTAs an SM, or 4 pages a half warp where lengths are uneven
+    const long long whole = (pages + FINISH_PAGES - 1) / FINISH_PAGES;
+    long long parts = 10 * 152 / units > whole / 4 ? 10 * 152 / units : whole / 4;
+    parts = parts < whole ? parts : whole;
     parts = parts < 0x7fffffffll / units ? parts : 0x7fffffffll / units;
     a.parts = static_cast<int>(parts < 1 ? 1 : parts);
     count_launch();
