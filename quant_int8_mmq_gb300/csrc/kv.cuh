@@ -404,6 +404,7 @@ struct EvictArgs {
     int new_pages, keep, first, last;
     int cluster;           // CTAs of a sequence's kv head in the choice
     int held;              // tokens that each keeps in shared memory
+    int parts;             // CTAs of a sequence's kv head in the move
 };
 cudaError_t launch_kv_evict(const EvictArgs& a, int dim, int max_kv, cudaStream_t s);
 

@@ -31,8 +31,8 @@ __device__ __forceinline__ uint32_t order_of(float w)
 
 __global__ void __launch_bounds__(CHOOSE) kv_choose_kernel(const EvictArgs g)
 {
-    extern __shared__ uint32_t keys[];                 // [g.held] of this CTA's tokens
-    __shared__ uint32_t hist[BINS];
+    extern __shared__ __align__(16) uint32_t keys[];   // [g.held] of this CTA's tokens
+    __shared__ __align__(16) uint32_t hist[BINS];
     __shared__ uint32_t warp_sum[CHOOSE_WARPS];
     __shared__ uint2 counts[CHOOSE_WARPS];             // tokens above T, and equal to it
     __shared__ uint2 mine;                             // of the CTA
@@ -68,9 +68,33 @@ __global__ void __launch_bounds__(CHOOSE) kv_choose_kernel(const EvictArgs g)
         }
         return order_of(g.weights[(static_cast<size_t>(page) * g.c.kv_heads + head) * KV_PAGE + (lo + j) % KV_PAGE]);
     };
-#pragma unroll 8
-    for (int j = threadIdx.x; j < min(size, g.held); j += CHOOSE)
-        keys[j] = read(j);
+    const int inside = min(size, g.held), quads = (inside + 3) / 4;
+    for (int q0 = threadIdx.x; q0 < quads; q0 += 8 * CHOOSE) {   // four weights a thread and load, eight on their way
+        int page[8];
+        float4 v[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int q = q0 + i * CHOOSE;
+            page[i] = q < quads ? table[lo / KV_PAGE + q / 16] : -1;
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int q = q0 + i * CHOOSE;
+            v[i] = make_float4(NAN, NAN, NAN, NAN);
+            if (page[i] >= 0 && page[i] < g.c.num_pages)
+                v[i] = *reinterpret_cast<const float4*>(
+                    g.weights + (static_cast<size_t>(page[i]) * g.c.kv_heads + head) * KV_PAGE + q % 16 * 4);
+            else if (q < quads)
+                *g.c.bad = 1u;
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int q = q0 + i * CHOOSE;
+            if (q < quads)
+                *reinterpret_cast<uint4*>(keys + 4 * q) =
+                    make_uint4(order_of(v[i].x), order_of(v[i].y), order_of(v[i].z), order_of(v[i].w));
+        }
+    }
     __syncthreads();
     auto key = [&](int j) { return j < g.held ? keys[j] : read(j); };
     // tokens [from, to) compete for `need` places
@@ -83,18 +107,33 @@ __global__ void __launch_bounds__(CHOOSE) kv_choose_kernel(const EvictArgs g)
         for (int i = threadIdx.x; i < BINS; i += CHOOSE)
             hist[i] = 0;
         __syncthreads();
-        for (int j0 = 0; j0 < size; j0 += CHOOSE) {
-            const int j = j0 + threadIdx.x;
-            uint32_t bin = BINS;
-            if (j < size && lo + j >= from && lo + j < to) {
-                const uint32_t k = key(j);
-                if ((k & known) == prefix)
-                    bin = k >> shift & low;
-            }
-            // equal weights are common: a warp adds them up first
-            const uint32_t same = __match_any_sync(0xffffffffu, bin);
-            if (bin < BINS && (same & ((1u << lane) - 1)) == 0)
-                atomicAdd(hist + bin, __popc(same));
+        // all lanes of a warp together; one bin (equal weights are common, none above all) is counted by
+        // a vote, the others by themselves
+        auto count = [&](uint32_t k, int j) {
+            const bool counts = j < size && lo + j >= from && lo + j < to && (k & known) == prefix;
+            const uint32_t bin = k >> shift & low, active = __ballot_sync(0xffffffffu, counts);
+            if (active == 0)
+                return;
+            const int first = __ffs(active) - 1;
+            const uint32_t one = __shfl_sync(0xffffffffu, bin, first);
+            const uint32_t same = __ballot_sync(0xffffffffu, counts && bin == one);
+            if (lane == first)
+                atomicAdd(hist + one, __popc(same));
+            else if (counts && bin != one)
+                atomicAdd(hist + bin, 1u);
+        };
+        for (int q0 = 0; q0 < quads; q0 += CHOOSE) {
+            const int q = q0 + threadIdx.x;
+            const uint4 k = q < quads ? *reinterpret_cast<const uint4*>(keys + 4 * q) : make_uint4(0, 0, 0, 0);
+            const int j = q < quads ? 4 * q : size;
+            count(k.x, j);
+            count(k.y, j + 1);
+            count(k.z, j + 2);
+            count(k.w, j + 3);
+        }
+        for (int j0 = g.held; j0 < size; j0 += CHOOSE) {
+            const int j = j0 + static_cast<int>(threadIdx.x);
+            count(j < size ? read(j) : 0u, j);
         }
         if (g.cluster > 1)
             cluster_sync();
@@ -102,19 +141,26 @@ __global__ void __launch_bounds__(CHOOSE) kv_choose_kernel(const EvictArgs g)
             __syncthreads();
         // the bin that holds the need-th largest: thread i has the i-th four bins from the top
         constexpr int EACH = BINS / CHOOSE;
-        uint32_t c[EACH], sum = 0;
+        static_assert(EACH == 4, "a thread's bins are 16 bytes");
+        const uint32_t at = smem_u32(hist + BINS - EACH - EACH * static_cast<int>(threadIdx.x));
+        uint4 v[KV_MAX_CLUSTER];
 #pragma unroll
-        for (int i = 0; i < EACH; ++i) {
-            const int bin = BINS - 1 - (EACH * static_cast<int>(threadIdx.x) + i);
-            c[i] = hist[bin];
-            if (g.cluster > 1) {
-                c[i] = 0;
-                const uint32_t at = smem_u32(hist + bin);
-                for (int r = 0; r < g.cluster; ++r)
-                    c[i] += ld_cluster_u32(cluster_map(at, r));
+        for (int r = 0; r < KV_MAX_CLUSTER; ++r) {
+            v[r] = make_uint4(0, 0, 0, 0);
+            if (r < g.cluster) {
+                const float4 x = ld_cluster_f32x4(cluster_map(at, r));
+                v[r] = make_uint4(__float_as_uint(x.x), __float_as_uint(x.y), __float_as_uint(x.z), __float_as_uint(x.w));
             }
-            sum += c[i];
         }
+        uint32_t c[EACH] = {0, 0, 0, 0};
+#pragma unroll
+        for (int r = 0; r < KV_MAX_CLUSTER; ++r) {
+            c[0] += v[r].w;
+            c[1] += v[r].z;
+            c[2] += v[r].y;
+            c[3] += v[r].x;
+        }
+        const uint32_t sum = c[0] + c[1] + c[2] + c[3];
         uint32_t before = sum;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
@@ -205,96 +251,113 @@ __global__ void __launch_bounds__(CHOOSE) kv_choose_kernel(const EvictArgs g)
         cluster_sync();   // the others have read this CTA's counts
 }
 
+// A CTA takes every parts-th new page of one sequence's kv head.  A page's tokens are looked up
+// (kept, page table: two dependent loads, and the weight behind them) while the one before is moved.
 template <int D>
 __global__ void __launch_bounds__(2 * D) kv_move_kernel(const EvictArgs g)
 {
     using P = Piece<D>;
-    __shared__ const uint8_t* from[KV_PAGE];   // pieces of the tokens, null: none
-    __shared__ uint8_t slots[KV_PAGE];
+    struct Source {
+        const uint8_t* from[KV_PAGE];   // pieces of the tokens, null: none
+        uint8_t slot[KV_PAGE];
+    };
+    __shared__ Source sources[2];
     grid_dep_wait();
     const int new_pages = (g.keep + KV_PAGE - 1) / KV_PAGE;
-    int id = blockIdx.x;
-    const int page = id % new_pages;
-    id /= new_pages;
-    const int head = id % g.c.kv_heads, b = id / g.c.kv_heads;
+    const int part = blockIdx.x % g.parts, unit = blockIdx.x / g.parts;
+    const int head = unit % g.c.kv_heads, b = unit / g.c.kv_heads;
     const int tid = threadIdx.x;
-    if (page == 0 && head == 0 && tid == 0)
-        g.new_length[b] = min(min(max(g.c.length[b], 0), g.c.max_pages * KV_PAGE), g.keep);
-    const int i = page * KV_PAGE + tid;
-    int old = -1;
-    if (tid < KV_PAGE && i < g.keep)
-        old = g.kept[(static_cast<size_t>(b) * g.c.kv_heads + head) * g.keep + i];
-    const int count = __syncthreads_count(old >= 0);
-    if (count == 0)
-        return;
-    const int to = g.new_table[static_cast<size_t>(b) * g.new_pages + page];
-    const bool there = to >= 0 && to < g.c.num_pages;
-    if (!there && tid == 0)
-        *g.c.bad = 1u;
-    const size_t to_piece = (static_cast<size_t>(there ? to : 0) * g.c.kv_heads + head);
-    if (old >= 0) {
-        const int p = g.c.table[static_cast<size_t>(b) * g.c.max_pages + old / KV_PAGE];
-        const bool held = p >= 0 && p < g.c.num_pages;
-        const size_t piece = static_cast<size_t>(held ? p : 0) * g.c.kv_heads + head;
-        from[tid] = held ? g.c.pages + piece * P::BYTES : nullptr;
-        slots[tid] = static_cast<uint8_t>(old % KV_PAGE);
-        if (!held)
+    const int stay = min(min(max(g.c.length[b], 0), g.c.max_pages * KV_PAGE), g.keep);
+    if (part == 0 && head == 0 && tid == 0)
+        g.new_length[b] = stay;   // may be length[b] itself: of the new value the others make the same
+    const int* kept = g.kept + static_cast<size_t>(unit) * g.keep;
+    const int* table = g.c.table + static_cast<size_t>(b) * g.c.max_pages;
+    const int* new_table = g.new_table + static_cast<size_t>(b) * g.new_pages;
+    auto old_of = [&](int page) {
+        const int i = page * KV_PAGE + tid;
+        return tid < KV_PAGE && page < new_pages && i < stay ? kept[i] : -1;
+    };
+    auto page_of = [&](int old) { return old >= 0 ? table[old / KV_PAGE] : -1; };
+    auto to_of = [&](int page) { return page * KV_PAGE < stay ? new_table[page] : -1; };
+    // piece of the page of token `old`; its weight
+    auto tell = [&](Source& s, int old, int page, float& weight) {
+        if (tid >= KV_PAGE)
+            return;
+        const bool held = page >= 0 && page < g.c.num_pages;
+        const size_t piece = static_cast<size_t>(held ? page : 0) * g.c.kv_heads + head;
+        s.from[tid] = held ? g.c.pages + piece * P::BYTES : nullptr;
+        s.slot[tid] = static_cast<uint8_t>(old % KV_PAGE);
+        weight = held ? g.weights[piece * KV_PAGE + old % KV_PAGE] : 0.0f;
+        if (old >= 0 && !held)
             *g.c.bad = 1u;
-        if (there)
-            g.weights[to_piece * KV_PAGE + tid] = held ? g.weights[piece * KV_PAGE + old % KV_PAGE] : 0.0f;
-    } else if (tid < KV_PAGE) {
-        from[tid] = nullptr;
-        slots[tid] = 0;
-    }
+    };
+    int page = part, old = old_of(page), old1 = old_of(page + g.parts), to = to_of(page);
+    float weight = 0.0f, weight1 = 0.0f;
+    tell(sources[0], old, page_of(old), weight);
     __syncthreads();
-    if (!there)
-        return;
-    uint8_t* dst = g.c.pages + to_piece * P::BYTES;
-    const uint4 none = make_uint4(0, 0, 0, 0);
-    {   // a key's group
-        const int t = tid / P::NG, gr = tid % P::NG;
-        if (t < count)
-            *reinterpret_cast<uint4*>(dst + P::k_chunk(t, gr)) =
-                from[t] ? *reinterpret_cast<const uint4*>(from[t] + P::k_chunk(slots[t], gr)) : none;
-    }
-    {   // 16 values of two tokens
-        const int p = tid / (D / 16), a = tid % (D / 16);
-        const int s0 = slots[2 * p], s1 = slots[2 * p + 1];
-        const uint8_t *f0 = from[2 * p], *f1 = from[2 * p + 1];
-        const uint4 x = f0 ? *reinterpret_cast<const uint4*>(f0 + P::v_chunk(s0 / 2, a)) : none;
-        const uint4 y = f1 ? *reinterpret_cast<const uint4*>(f1 + P::v_chunk(s1 / 2, a)) : none;
-        const uint32_t pick = (s0 & 1 ? 0x32u : 0x10u) | (s1 & 1 ? 0x7600u : 0x5400u);
-        const uint4 z = make_uint4(__byte_perm(x.x, y.x, pick), __byte_perm(x.y, y.y, pick), __byte_perm(x.z, y.z, pick),
-                                   __byte_perm(x.w, y.w, pick));
-        uint8_t* at = dst + P::v_chunk(p, a);
-        // the pair's scales, one word of the two tokens' per group
-        const bool scales = a % 2 == 0;
-        const int gr = a / 2;
-        uint32_t sx = 0, sy = 0;
-        if (scales) {
-            sx = f0 ? *reinterpret_cast<const uint32_t*>(f0 + P::v_scale(s0 / 2, gr)) : 0u;
-            sy = f1 ? *reinterpret_cast<const uint32_t*>(f1 + P::v_scale(s1 / 2, gr)) : 0u;
-        }
-        const uint32_t sz = __byte_perm(sx, sy, pick);
-        if (2 * p + 1 < count) {
-            *reinterpret_cast<uint4*>(at) = z;
-            if (scales)
-                *reinterpret_cast<uint32_t*>(dst + P::v_scale(p, gr)) = sz;
-        } else if (2 * p < count) {   // the other token's halves stay as they are
-            const uint32_t w[4] = {z.x, z.y, z.z, z.w};
+    for (int turn = 0; page * KV_PAGE < stay; ++turn, page += g.parts) {
+        const Source& s = sources[turn % 2];
+        // on their way for the next page, and the one after it
+        const int id1 = page_of(old1), old2 = old_of(page + 2 * g.parts), to1 = to_of(page + g.parts);
+        const int count = min(stay - page * KV_PAGE, KV_PAGE);
+        const bool there = to >= 0 && to < g.c.num_pages;
+        if (there) {
+            const size_t piece = static_cast<size_t>(to) * g.c.kv_heads + head;
+            uint8_t* dst = g.c.pages + piece * P::BYTES;
+            const uint4 none = make_uint4(0, 0, 0, 0);
+            // a key's group
+            const int t = tid / P::NG, gr = tid % P::NG;
+            const uint8_t* f = t < count ? s.from[t] : nullptr;
+            const uint4 key = f ? *reinterpret_cast<const uint4*>(f + P::k_chunk(s.slot[t], gr)) : none;
+            // 16 values of two tokens
+            const int p = tid / (D / 16), a = tid % (D / 16);
+            const int s0 = s.slot[2 * p], s1 = s.slot[2 * p + 1];
+            const uint8_t* f0 = 2 * p < count ? s.from[2 * p] : nullptr;
+            const uint8_t* f1 = 2 * p + 1 < count ? s.from[2 * p + 1] : nullptr;
+            const uint4 x = f0 ? *reinterpret_cast<const uint4*>(f0 + P::v_chunk(s0 / 2, a)) : none;
+            const uint4 y = f1 ? *reinterpret_cast<const uint4*>(f1 + P::v_chunk(s1 / 2, a)) : none;
+            // the pair's scales, one word of the two tokens' per group, and a key's scales
+            const bool scales = a % 2 == 0;
+            uint32_t sx = 0, sy = 0;
+            if (scales) {
+                sx = f0 ? *reinterpret_cast<const uint32_t*>(f0 + P::v_scale(s0 / 2, a / 2)) : 0u;
+                sy = f1 ? *reinterpret_cast<const uint32_t*>(f1 + P::v_scale(s1 / 2, a / 2)) : 0u;
+            }
+            using W = typename std::conditional<D == 128, uint2, uint32_t>::type;
+            W ks = {};
+            if (tid < count && s.from[tid])
+                ks = *reinterpret_cast<const W*>(s.from[tid] + P::k_scale(s.slot[tid], 0));
+
+            const uint32_t pick = (s0 & 1 ? 0x32u : 0x10u) | (s1 & 1 ? 0x7600u : 0x5400u);
+            const uint32_t z[4] = {__byte_perm(x.x, y.x, pick), __byte_perm(x.y, y.y, pick), __byte_perm(x.z, y.z, pick),
+                                   __byte_perm(x.w, y.w, pick)};
+            const uint32_t sz = __byte_perm(sx, sy, pick);
+            if (t < count)
+                *reinterpret_cast<uint4*>(dst + P::k_chunk(t, gr)) = key;
+            uint8_t* at = dst + P::v_chunk(p, a);
+            if (2 * p + 1 < count) {
+                *reinterpret_cast<uint4*>(at) = make_uint4(z[0], z[1], z[2], z[3]);
+                if (scales)
+                    *reinterpret_cast<uint32_t*>(dst + P::v_scale(p, a / 2)) = sz;
+            } else if (2 * p < count) {   // the other token's halves stay as they are
 #pragma unroll
-            for (int u = 0; u < 4; ++u)
-                *reinterpret_cast<uint16_t*>(at + 4 * u) = static_cast<uint16_t>(w[u]);
-            if (scales)
-                *reinterpret_cast<uint16_t*>(dst + P::v_scale(p, gr)) = static_cast<uint16_t>(sz);
+                for (int u = 0; u < 4; ++u)
+                    *reinterpret_cast<uint16_t*>(at + 4 * u) = static_cast<uint16_t>(z[u]);
+                if (scales)
+                    *reinterpret_cast<uint16_t*>(dst + P::v_scale(p, a / 2)) = static_cast<uint16_t>(sz);
+            }
+            if (tid < count) {
+                *reinterpret_cast<W*>(dst + P::k_scale(tid, 0)) = ks;
+                g.weights[piece * KV_PAGE + tid] = weight;
+            }
+        } else if (tid == 0) {
+            *g.c.bad = 1u;
         }
-    }
-    if (tid < count) {   // a key's scales
-        using W = typename std::conditional<D == 128, uint2, uint32_t>::type;
-        W s = {};
-        if (from[tid])
-            s = *reinterpret_cast<const W*>(from[tid] + P::k_scale(slots[tid], 0));
-        *reinterpret_cast<W*>(dst + P::k_scale(tid, 0)) = s;
+        tell(sources[(turn + 1) % 2], old1, id1, weight1);
+        __syncthreads();
+        old1 = old2;
+        to = to1;
+        weight = weight1;
     }
 }
 
@@ -334,7 +397,11 @@ cudaError_t launch_kv_evict(const EvictArgs& args, int dim, int max_kv, cudaStre
     count_launch();
     if ((e = cudaLaunchKernelEx(&cfg, kv_choose_kernel, a)) != cudaSuccess)
         return e;
-    const dim3 grid(static_cast<unsigned int>(units * ((a.keep + KV_PAGE - 1) / KV_PAGE)));
+    // the chip's CTAs, or 8 pages a CTA where sequences are few or of uneven length
+    const long long pages = (a.keep + KV_PAGE - 1) / KV_PAGE, fill = 152 * (dim == 128 ? 8 : 16) / units;
+    const long long parts = fill > pages / 8 ? fill : pages / 8;
+    a.parts = static_cast<int>(parts < 1 ? 1 : parts < pages ? parts : pages);
+    const dim3 grid(static_cast<unsigned int>(units * a.parts));
     count_launch();
     return dim == 128 ? launch_dependent(kv_move_kernel<128>, grid, dim3(256), s, a)
                       : launch_dependent(kv_move_kernel<64>, grid, dim3(128), s, a);
