@@ -37,6 +37,8 @@ __global__ void __launch_bounds__(CHOOSE) kv_choose_kernel(const EvictArgs g)
     __shared__ uint2 counts[CHOOSE_WARPS];             // tokens above T, and equal to it
     __shared__ uint2 mine;                             // of the CTA
     __shared__ uint32_t found[2];                      // bin, tokens above it
+    __shared__ __align__(16) uint32_t merged[BINS / 2];   // a cluster: this CTA's slice of the bins, of all CTAs
+    __shared__ uint32_t slice_sum[ROUNDS];
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     grid_dep_wait();
     grid_dep_launch();
@@ -95,6 +97,8 @@ __global__ void __launch_bounds__(CHOOSE) kv_choose_kernel(const EvictArgs g)
                     make_uint4(order_of(v[i].x), order_of(v[i].y), order_of(v[i].z), order_of(v[i].w));
         }
     }
+    if (threadIdx.x < ROUNDS)
+        slice_sum[threadIdx.x] = 0;
     __syncthreads();
     auto key = [&](int j) { return j < g.held ? keys[j] : read(j); };
     // tokens [from, to) compete for `need` places
@@ -107,20 +111,9 @@ __global__ void __launch_bounds__(CHOOSE) kv_choose_kernel(const EvictArgs g)
         for (int i = threadIdx.x; i < BINS; i += CHOOSE)
             hist[i] = 0;
         __syncthreads();
-        // all lanes of a warp together; one bin (equal weights are common, none above all) is counted by
-        // a vote, the others by themselves
         auto count = [&](uint32_t k, int j) {
-            const bool counts = j < size && lo + j >= from && lo + j < to && (k & known) == prefix;
-            const uint32_t bin = k >> shift & low, active = __ballot_sync(0xffffffffu, counts);
-            if (active == 0)
-                return;
-            const int first = __ffs(active) - 1;
-            const uint32_t one = __shfl_sync(0xffffffffu, bin, first);
-            const uint32_t same = __ballot_sync(0xffffffffu, counts && bin == one);
-            if (lane == first)
-                atomicAdd(hist + one, __popc(same));
-            else if (counts && bin != one)
-                atomicAdd(hist + bin, 1u);
+            if (j < size && lo + j >= from && lo + j < to && (k & known) == prefix)
+                atomicAdd(hist + (k >> shift & low), 1u);
         };
         for (int q0 = 0; q0 < quads; q0 += CHOOSE) {
             const int q = q0 + threadIdx.x;
@@ -135,30 +128,63 @@ __global__ void __launch_bounds__(CHOOSE) kv_choose_kernel(const EvictArgs g)
             const int j = j0 + static_cast<int>(threadIdx.x);
             count(j < size ? read(j) : 0u, j);
         }
-        if (g.cluster > 1)
-            cluster_sync();
-        else
-            __syncthreads();
-        // the bin that holds the need-th largest: thread i has the i-th four bins from the top
-        constexpr int EACH = BINS / CHOOSE;
+        // A cluster's CTAs add up a slice of the bins each, and look into the one slice that holds the
+        // need-th largest (all bins from all CTAs were 64 KB each and took 5000 cycles).
+        constexpr int EACH = BINS / CHOOSE;   // bins of a thread, the i-th four from the top
         static_assert(EACH == 4, "a thread's bins are 16 bytes");
-        const uint32_t at = smem_u32(hist + BINS - EACH - EACH * static_cast<int>(threadIdx.x));
-        uint4 v[KV_MAX_CLUSTER];
+        int slice = 0, slices = 1;
+        uint32_t over = 0;                    // tokens above the slice
+        uint32_t* bins = hist;
+        if (g.cluster > 1) {
+            cluster_sync();
+            slices = g.cluster;
+            const int width = BINS / slices;  // at least BINS / KV_MAX_CLUSTER, of 4 a thread
+            if (threadIdx.x < width / 4) {
+                const uint32_t at = smem_u32(hist + rank * width + 4 * threadIdx.x);
+                uint4 v = make_uint4(0, 0, 0, 0);
 #pragma unroll
-        for (int r = 0; r < KV_MAX_CLUSTER; ++r) {
-            v[r] = make_uint4(0, 0, 0, 0);
-            if (r < g.cluster) {
-                const float4 x = ld_cluster_f32x4(cluster_map(at, r));
-                v[r] = make_uint4(__float_as_uint(x.x), __float_as_uint(x.y), __float_as_uint(x.z), __float_as_uint(x.w));
+                for (int r = 0; r < KV_MAX_CLUSTER; ++r)
+                    if (r < slices) {
+                        const float4 x = ld_cluster_f32x4(cluster_map(at, r));
+                        v.x += __float_as_uint(x.x), v.y += __float_as_uint(x.y);
+                        v.z += __float_as_uint(x.z), v.w += __float_as_uint(x.w);
+                    }
+                *reinterpret_cast<uint4*>(merged + 4 * threadIdx.x) = v;
+                uint32_t sum = v.x + v.y + v.z + v.w;
+#pragma unroll
+                for (int d = 16; d > 0; d >>= 1)
+                    sum += __shfl_xor_sync(0xffffffffu, sum, d);
+                if (lane == 0)
+                    atomicAdd(&slice_sum[round], sum);
+            }
+            cluster_sync();
+            uint32_t sums[KV_MAX_CLUSTER];
+#pragma unroll
+            for (int r = 0; r < KV_MAX_CLUSTER; ++r)
+                sums[r] = r < slices ? ld_cluster_u32(cluster_map(smem_u32(&slice_sum[round]), r)) : 0u;
+            uint32_t above = 0;
+#pragma unroll
+            for (int r = KV_MAX_CLUSTER - 1; r >= 0; --r) {
+                if (above < need && need <= above + sums[r]) {
+                    slice = r;
+                    over = above;
+                }
+                above += sums[r];
+            }
+            const uint32_t at = smem_u32(merged + 4 * threadIdx.x);
+            if (threadIdx.x < width / 4) {
+                const float4 x = ld_cluster_f32x4(cluster_map(at, slice));
+                *reinterpret_cast<uint4*>(hist + 4 * threadIdx.x) =
+                    make_uint4(__float_as_uint(x.x), __float_as_uint(x.y), __float_as_uint(x.z), __float_as_uint(x.w));
             }
         }
+        __syncthreads();
+        const int width = BINS / slices;
         uint32_t c[EACH] = {0, 0, 0, 0};
-#pragma unroll
-        for (int r = 0; r < KV_MAX_CLUSTER; ++r) {
-            c[0] += v[r].w;
-            c[1] += v[r].z;
-            c[2] += v[r].y;
-            c[3] += v[r].x;
+        const int top = width - 1 - EACH * static_cast<int>(threadIdx.x);   // the thread's first bin of the slice
+        if (top > 0) {
+            const uint4 v = *reinterpret_cast<const uint4*>(bins + top - 3);
+            c[0] = v.w, c[1] = v.z, c[2] = v.y, c[3] = v.x;
         }
         const uint32_t sum = c[0] + c[1] + c[2] + c[3];
         uint32_t before = sum;
@@ -170,19 +196,19 @@ __global__ void __launch_bounds__(CHOOSE) kv_choose_kernel(const EvictArgs g)
         if (lane == 31)
             warp_sum[warp] = before;
         __syncthreads();
-        before -= sum;
+        before += over - sum;
         for (int w = 0; w < warp; ++w)
             before += warp_sum[w];
 #pragma unroll
         for (int i = 0; i < EACH; ++i) {
             if (before < need && need <= before + c[i]) {
-                found[0] = BINS - 1 - (EACH * threadIdx.x + i);
+                found[0] = static_cast<uint32_t>(slice * width + top - i);
                 found[1] = before;
             }
             before += c[i];
         }
         if (g.cluster > 1)
-            cluster_sync();   // everyone has read this CTA's histogram
+            cluster_sync();   // everyone has read this CTA's slice
         else
             __syncthreads();
         prefix |= found[0] << shift;
@@ -193,29 +219,40 @@ __global__ void __launch_bounds__(CHOOSE) kv_choose_kernel(const EvictArgs g)
 
     // `need` of the tokens that equal T = prefix stay (none where nobody competes)
     const bool compete = g.keep > g.first + g.last;
-    const int part = ((size + CHOOSE_WARPS - 1) / CHOOSE_WARPS + 31) / 32 * 32;
+    // each warp looks at a part of the tokens, four a lane: bits 0-3 tell which of them are above T (or
+    // stay anyhow), bits 4-7 which equal it
+    const int part = ((size + CHOOSE_WARPS - 1) / CHOOSE_WARPS + 127) / 128 * 128;
     const int j0 = min(warp * part, size), j1 = min(j0 + part, size);
-    auto look = [&](int j, uint32_t& above, uint32_t& equal) {
-        bool a = false, e = false;
-        if (j < j1) {
-            const int i = lo + j;
-            if (i < from || i >= to) {
-                a = true;
-            } else if (compete) {
-                const uint32_t k = key(j);
-                a = k > prefix;
-                e = k == prefix;
-            }
+    auto look = [&](int j) {
+        uint32_t k[4];
+        if (j + 3 < g.held) {
+            const uint4 v = *reinterpret_cast<const uint4*>(keys + j);
+            k[0] = v.x, k[1] = v.y, k[2] = v.z, k[3] = v.w;
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                k[i] = j + i < j1 ? key(j + i) : 0u;
         }
-        above = __ballot_sync(0xffffffffu, a);
-        equal = __ballot_sync(0xffffffffu, e);
+        uint32_t m = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int at = lo + j + i;
+            const bool mine = j + i < j1, free = at >= from && at < to;
+            m |= mine && (!free || (compete && k[i] > prefix)) ? 1u << i : 0u;
+            m |= mine && free && compete && k[i] == prefix ? 16u << i : 0u;
+        }
+        return m;
     };
     uint2 sum = make_uint2(0, 0);
-    for (int j = j0; j < j1; j += 32) {
-        uint32_t a, e;
-        look(j + lane, a, e);
-        sum.x += __popc(a);
-        sum.y += __popc(e);
+    for (int j = j0; j < j1; j += 128) {
+        const uint32_t m = look(j + 4 * lane);
+        sum.x += __popc(m & 15u);
+        sum.y += __popc(m & 0xf0u);
+    }
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) {
+        sum.x += __shfl_xor_sync(0xffffffffu, sum.x, d);
+        sum.y += __shfl_xor_sync(0xffffffffu, sum.y, d);
     }
     if (lane == 0)
         counts[warp] = sum;
@@ -237,15 +274,26 @@ __global__ void __launch_bounds__(CHOOSE) kv_choose_kernel(const EvictArgs g)
             sum.y += ld_cluster_u32(cluster_map(at + 4, r));
         }
     }
-    const uint32_t below = (1u << lane) - 1;
-    for (int j = j0; j < j1; j += 32) {
-        uint32_t a, e;
-        look(j + lane, a, e);
-        const uint32_t na = sum.x + __popc(a & below), ne = sum.y + __popc(e & below);
-        if ((a >> lane & 1u) || ((e >> lane & 1u) && ne < need))
-            kept[na + min(ne, need)] = lo + j + lane;
-        sum.x += __popc(a);
-        sum.y += __popc(e);
+    for (int j = j0; j < j1; j += 128) {
+        const uint32_t m = look(j + 4 * lane), own = __popc(m & 15u) | __popc(m & 0xf0u) << 16;
+        uint32_t to_here = own;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const uint32_t v = __shfl_up_sync(0xffffffffu, to_here, d);
+            to_here += lane >= d ? v : 0;
+        }
+        uint32_t na = sum.x + ((to_here - own) & 0xffffu), ne = sum.y + ((to_here - own) >> 16);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const bool a = m >> i & 1u, e = m >> (4 + i) & 1u;
+            if (a || (e && ne < need))
+                kept[na + min(ne, need)] = lo + j + 4 * lane + i;
+            na += a;
+            ne += e;
+        }
+        const uint32_t all = __shfl_sync(0xffffffffu, to_here, 31);
+        sum.x += all & 0xffffu;
+        sum.y += all >> 16;
     }
     if (g.cluster > 1)
         cluster_sync();   // the others have read this CTA's counts
