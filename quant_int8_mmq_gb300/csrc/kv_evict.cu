@@ -2,8 +2,8 @@
 //
 // Of a sequence of n > keep tokens stay, per kv head, the first ones, the last ones, and of
 // the rest the m with the largest weights (ties: the lower position).  The m-th largest weight
-// T is found by a radix search: weights as unsigned numbers of the same order, three
-// histograms (11, 11 and 10 bits) of those that agree with T in the bits known so far.  A token
+// T is found by a radix search: weights as unsigned numbers of the same order, four
+// histograms of 8 bits of those that agree with T in the bits known so far.  A token
 // then stays if its weight is above T, or equal and among the first of those that equal it, and
 // its new place is the number of tokens before it that stay.
 //
@@ -19,8 +19,7 @@ namespace mmq {
 namespace {
 
 constexpr int CHOOSE_WARPS = 16, CHOOSE = CHOOSE_WARPS * 32;
-constexpr int BINS = 2048;
-constexpr int ROUNDS = 3;
+constexpr int BINS = 256, ROUNDS = 4;
 
 // Unsigned numbers in the order of f32 ones; -0 as 0, no number below all others.
 __device__ __forceinline__ uint32_t order_of(float w)
@@ -29,16 +28,13 @@ __device__ __forceinline__ uint32_t order_of(float w)
     return w != w ? 0u : u >> 31 ? ~u : u | 0x80000000u;
 }
 
-__global__ void __launch_bounds__(CHOOSE) kv_choose_kernel(const EvictArgs g)
+__global__ void __launch_bounds__(CHOOSE, 3) kv_choose_kernel(const EvictArgs g)
 {
     extern __shared__ __align__(16) uint32_t keys[];   // [g.held] of this CTA's tokens
-    __shared__ __align__(16) uint32_t hist[BINS];
-    __shared__ uint32_t warp_sum[CHOOSE_WARPS];
+    __shared__ __align__(16) uint32_t hist[ROUNDS][BINS];
     __shared__ uint2 counts[CHOOSE_WARPS];             // tokens above T, and equal to it
     __shared__ uint2 mine;                             // of the CTA
-    __shared__ uint32_t found[2];                      // bin, tokens above it
-    __shared__ __align__(16) uint32_t merged[BINS / 2];   // a cluster: this CTA's slice of the bins, of all CTAs
-    __shared__ uint32_t slice_sum[ROUNDS];
+    __shared__ uint2 found[ROUNDS];                    // bin, tokens above it
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     grid_dep_wait();
     grid_dep_launch();
@@ -71,16 +67,17 @@ __global__ void __launch_bounds__(CHOOSE) kv_choose_kernel(const EvictArgs g)
         return order_of(g.weights[(static_cast<size_t>(page) * g.c.kv_heads + head) * KV_PAGE + (lo + j) % KV_PAGE]);
     };
     const int inside = min(size, g.held), quads = (inside + 3) / 4;
-    for (int q0 = threadIdx.x; q0 < quads; q0 += 8 * CHOOSE) {   // four weights a thread and load, eight on their way
-        int page[8];
-        float4 v[8];
+    constexpr int BATCH = 4;
+    for (int q0 = threadIdx.x; q0 < quads; q0 += BATCH * CHOOSE) {   // four weights a thread and load
+        int page[BATCH];
+        float4 v[BATCH];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
+        for (int i = 0; i < BATCH; ++i) {
             const int q = q0 + i * CHOOSE;
             page[i] = q < quads ? table[lo / KV_PAGE + q / 16] : -1;
         }
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
+        for (int i = 0; i < BATCH; ++i) {
             const int q = q0 + i * CHOOSE;
             v[i] = make_float4(NAN, NAN, NAN, NAN);
             if (page[i] >= 0 && page[i] < g.c.num_pages)
@@ -90,15 +87,15 @@ __global__ void __launch_bounds__(CHOOSE) kv_choose_kernel(const EvictArgs g)
                 *g.c.bad = 1u;
         }
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
+        for (int i = 0; i < BATCH; ++i) {
             const int q = q0 + i * CHOOSE;
             if (q < quads)
                 *reinterpret_cast<uint4*>(keys + 4 * q) =
                     make_uint4(order_of(v[i].x), order_of(v[i].y), order_of(v[i].z), order_of(v[i].w));
         }
     }
-    if (threadIdx.x < ROUNDS)
-        slice_sum[threadIdx.x] = 0;
+    for (int i = threadIdx.x; i < ROUNDS * BINS; i += CHOOSE)
+        hist[i / BINS][i % BINS] = 0;
     __syncthreads();
     auto key = [&](int j) { return j < g.held ? keys[j] : read(j); };
     // tokens [from, to) compete for `need` places
@@ -106,14 +103,10 @@ __global__ void __launch_bounds__(CHOOSE) kv_choose_kernel(const EvictArgs g)
     uint32_t need = static_cast<uint32_t>(g.keep - g.first - g.last);
     uint32_t prefix = 0, known = 0;
     for (int round = 0; need > 0 && round < ROUNDS; ++round) {
-        const int shift = round == 0 ? 21 : round == 1 ? 10 : 0;
-        const uint32_t low = round == 2 ? 1023u : 2047u;
-        for (int i = threadIdx.x; i < BINS; i += CHOOSE)
-            hist[i] = 0;
-        __syncthreads();
+        const int shift = 24 - 8 * round;
         auto count = [&](uint32_t k, int j) {
             if (j < size && lo + j >= from && lo + j < to && (k & known) == prefix)
-                atomicAdd(hist + (k >> shift & low), 1u);
+                atomicAdd(&hist[round][k >> shift & (BINS - 1)], 1u);
         };
         for (int q0 = 0; q0 < quads; q0 += CHOOSE) {
             const int q = q0 + threadIdx.x;
@@ -128,93 +121,55 @@ __global__ void __launch_bounds__(CHOOSE) kv_choose_kernel(const EvictArgs g)
             const int j = j0 + static_cast<int>(threadIdx.x);
             count(j < size ? read(j) : 0u, j);
         }
-        // A cluster's CTAs add up a slice of the bins each, and look into the one slice that holds the
-        // need-th largest (all bins from all CTAs were 64 KB each and took 5000 cycles).
-        constexpr int EACH = BINS / CHOOSE;   // bins of a thread, the i-th four from the top
-        static_assert(EACH == 4, "a thread's bins are 16 bytes");
-        int slice = 0, slices = 1;
-        uint32_t over = 0;                    // tokens above the slice
-        uint32_t* bins = hist;
-        if (g.cluster > 1) {
-            cluster_sync();
-            slices = g.cluster;
-            const int width = BINS / slices;  // at least BINS / KV_MAX_CLUSTER, of 4 a thread
-            if (threadIdx.x < width / 4) {
-                const uint32_t at = smem_u32(hist + rank * width + 4 * threadIdx.x);
-                uint4 v = make_uint4(0, 0, 0, 0);
-#pragma unroll
-                for (int r = 0; r < KV_MAX_CLUSTER; ++r)
-                    if (r < slices) {
-                        const float4 x = ld_cluster_f32x4(cluster_map(at, r));
-                        v.x += __float_as_uint(x.x), v.y += __float_as_uint(x.y);
-                        v.z += __float_as_uint(x.z), v.w += __float_as_uint(x.w);
-                    }
-                *reinterpret_cast<uint4*>(merged + 4 * threadIdx.x) = v;
-                uint32_t sum = v.x + v.y + v.z + v.w;
-#pragma unroll
-                for (int d = 16; d > 0; d >>= 1)
-                    sum += __shfl_xor_sync(0xffffffffu, sum, d);
-                if (lane == 0)
-                    atomicAdd(&slice_sum[round], sum);
-            }
-            cluster_sync();
-            uint32_t sums[KV_MAX_CLUSTER];
-#pragma unroll
-            for (int r = 0; r < KV_MAX_CLUSTER; ++r)
-                sums[r] = r < slices ? ld_cluster_u32(cluster_map(smem_u32(&slice_sum[round]), r)) : 0u;
-            uint32_t above = 0;
-#pragma unroll
-            for (int r = KV_MAX_CLUSTER - 1; r >= 0; --r) {
-                if (above < need && need <= above + sums[r]) {
-                    slice = r;
-                    over = above;
-                }
-                above += sums[r];
-            }
-            const uint32_t at = smem_u32(merged + 4 * threadIdx.x);
-            if (threadIdx.x < width / 4) {
-                const float4 x = ld_cluster_f32x4(cluster_map(at, slice));
-                *reinterpret_cast<uint4*>(hist + 4 * threadIdx.x) =
-                    make_uint4(__float_as_uint(x.x), __float_as_uint(x.y), __float_as_uint(x.z), __float_as_uint(x.w));
-            }
-        }
-        __syncthreads();
-        const int width = BINS / slices;
-        uint32_t c[EACH] = {0, 0, 0, 0};
-        const int top = width - 1 - EACH * static_cast<int>(threadIdx.x);   // the thread's first bin of the slice
-        if (top > 0) {
-            const uint4 v = *reinterpret_cast<const uint4*>(bins + top - 3);
-            c[0] = v.w, c[1] = v.z, c[2] = v.y, c[3] = v.x;
-        }
-        const uint32_t sum = c[0] + c[1] + c[2] + c[3];
-        uint32_t before = sum;
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-            const uint32_t v = __shfl_up_sync(0xffffffffu, before, d);
-            before += lane >= d ? v : 0;
-        }
-        if (lane == 31)
-            warp_sum[warp] = before;
-        __syncthreads();
-        before += over - sum;
-        for (int w = 0; w < warp; ++w)
-            before += warp_sum[w];
-#pragma unroll
-        for (int i = 0; i < EACH; ++i) {
-            if (before < need && need <= before + c[i]) {
-                found[0] = static_cast<uint32_t>(slice * width + top - i);
-                found[1] = before;
-            }
-            before += c[i];
-        }
         if (g.cluster > 1)
-            cluster_sync();   // everyone has read this CTA's slice
+            cluster_sync();
         else
             __syncthreads();
-        prefix |= found[0] << shift;
-        known |= low << shift;
-        need -= found[1];
+        // the bin that holds the need-th largest: a lane has 8 bins, the first one those at the top
+        if (warp == 0) {
+            constexpr int EACH = BINS / 32;
+            const uint32_t at = smem_u32(&hist[round][BINS - EACH * (lane + 1)]);
+            uint32_t c[EACH] = {};
+            auto add = [&](int half, float4 x) {
+                c[4 * half] += __float_as_uint(x.x), c[4 * half + 1] += __float_as_uint(x.y);
+                c[4 * half + 2] += __float_as_uint(x.z), c[4 * half + 3] += __float_as_uint(x.w);
+            };
+            for (int r = 0; r < g.cluster; r += 2) {   // of one CTA, or of all of the cluster, two at a time
+                float4 x[2][2] = {};
+#pragma unroll
+                for (int k = 0; k < 2; ++k)
+#pragma unroll
+                    for (int half = 0; half < 2; ++half)
+                        if (r + k < g.cluster)
+                            x[k][half] = ld_cluster_f32x4(cluster_map(at + 16 * half, r + k));
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    add(0, x[k][0]);
+                    add(1, x[k][1]);
+                }
+            }
+            uint32_t sum = 0;
+#pragma unroll
+            for (int i = 0; i < EACH; ++i)
+                sum += c[i];
+            uint32_t before = sum;
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const uint32_t v = __shfl_up_sync(0xffffffffu, before, d);
+                before += lane >= d ? v : 0;
+            }
+            before -= sum;
+#pragma unroll
+            for (int i = EACH - 1; i >= 0; --i) {
+                if (before < need && need <= before + c[i])
+                    found[round] = make_uint2(BINS - EACH * (lane + 1) + i, before);
+                before += c[i];
+            }
+        }
         __syncthreads();
+        prefix |= found[round].x << shift;
+        known |= static_cast<uint32_t>(BINS - 1) << shift;
+        need -= found[round].y;
     }
 
     // `need` of the tokens that equal T = prefix stay (none where nobody competes)
@@ -234,6 +189,12 @@ __global__ void __launch_bounds__(CHOOSE) kv_choose_kernel(const EvictArgs g)
                 k[i] = j + i < j1 ? key(j + i) : 0u;
         }
         uint32_t m = 0;
+        if (compete && j + 3 < j1 && lo + j >= from && lo + j + 3 < to) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                m |= (k[i] > prefix ? 1u << i : 0u) | (k[i] == prefix ? 16u << i : 0u);
+            return m;
+        }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int at = lo + j + i;
@@ -283,13 +244,15 @@ __global__ void __launch_bounds__(CHOOSE) kv_choose_kernel(const EvictArgs g)
             to_here += lane >= d ? v : 0;
         }
         uint32_t na = sum.x + ((to_here - own) & 0xffffu), ne = sum.y + ((to_here - own) >> 16);
+        if (own) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const bool a = m >> i & 1u, e = m >> (4 + i) & 1u;
-            if (a || (e && ne < need))
-                kept[na + min(ne, need)] = lo + j + 4 * lane + i;
-            na += a;
-            ne += e;
+            for (int i = 0; i < 4; ++i) {
+                const bool a = m >> i & 1u, e = m >> (4 + i) & 1u;
+                if (a || (e && ne < need))
+                    kept[na + min(ne, need)] = lo + j + 4 * lane + i;
+                na += a;
+                ne += e;
+            }
         }
         const uint32_t all = __shfl_sync(0xffffffffu, to_here, 31);
         sum.x += all & 0xffffu;
