@@ -34,6 +34,7 @@ __global__ void __launch_bounds__(CHOOSE, 3) kv_choose_kernel(const EvictArgs g)
     __shared__ __align__(16) uint32_t hist[ROUNDS][BINS];
     __shared__ uint2 counts[CHOOSE_WARPS];             // tokens above T, and equal to it
     __shared__ uint2 mine;                             // of the CTA
+    __shared__ __align__(16) uint32_t all[KV_MAX_CLUSTER][BINS];
     __shared__ uint2 found[ROUNDS];                    // bin, tokens above it
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     grid_dep_wait();
@@ -112,40 +113,45 @@ __global__ void __launch_bounds__(CHOOSE, 3) kv_choose_kernel(const EvictArgs g)
             const int q = q0 + threadIdx.x;
             const uint4 k = q < quads ? *reinterpret_cast<const uint4*>(keys + 4 * q) : make_uint4(0, 0, 0, 0);
             const int j = q < quads ? 4 * q : size;
-            count(k.x, j);
-            count(k.y, j + 1);
-            count(k.z, j + 2);
-            count(k.w, j + 3);
+            if (j + 3 < size && lo + j >= from && lo + j + 3 < to) {
+                const uint32_t e[4] = {k.x, k.y, k.z, k.w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if ((e[i] & known) == prefix)
+                        atomicAdd(&hist[round][e[i] >> shift & (BINS - 1)], 1u);
+            } else {
+                count(k.x, j);
+                count(k.y, j + 1);
+                count(k.z, j + 2);
+                count(k.w, j + 3);
+            }
         }
         for (int j0 = g.held; j0 < size; j0 += CHOOSE) {
             const int j = j0 + static_cast<int>(threadIdx.x);
             count(j < size ? read(j) : 0u, j);
         }
-        if (g.cluster > 1)
+        if (g.cluster > 1) {
+            // a load from another CTA takes 1000 cycles: each CTA's bins are fetched by a warp of their own
             cluster_sync();
-        else
-            __syncthreads();
+            if (warp < g.cluster) {
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    const float4 x = ld_cluster_f32x4(cluster_map(smem_u32(&hist[round][8 * lane + 4 * half]), warp));
+                    *reinterpret_cast<float4*>(&all[warp][8 * lane + 4 * half]) = x;
+                }
+            }
+        }
+        __syncthreads();
         // the bin that holds the need-th largest: a lane has 8 bins, the first one those at the top
         if (warp == 0) {
             constexpr int EACH = BINS / 32;
-            const uint32_t at = smem_u32(&hist[round][BINS - EACH * (lane + 1)]);
             uint32_t c[EACH] = {};
-            auto add = [&](int half, float4 x) {
-                c[4 * half] += __float_as_uint(x.x), c[4 * half + 1] += __float_as_uint(x.y);
-                c[4 * half + 2] += __float_as_uint(x.z), c[4 * half + 3] += __float_as_uint(x.w);
-            };
-            for (int r = 0; r < g.cluster; r += 2) {   // of one CTA, or of all of the cluster, two at a time
-                float4 x[2][2] = {};
+            for (int r = 0; r < g.cluster; ++r) {
+                const uint32_t* bins = g.cluster > 1 ? all[r] : hist[round];
 #pragma unroll
-                for (int k = 0; k < 2; ++k)
-#pragma unroll
-                    for (int half = 0; half < 2; ++half)
-                        if (r + k < g.cluster)
-                            x[k][half] = ld_cluster_f32x4(cluster_map(at + 16 * half, r + k));
-#pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    add(0, x[k][0]);
-                    add(1, x[k][1]);
+                for (int half = 0; half < 2; ++half) {
+                    const uint4 x = *reinterpret_cast<const uint4*>(bins + BINS - EACH * (lane + 1) + 4 * half);
+                    c[4 * half] += x.x, c[4 * half + 1] += x.y, c[4 * half + 2] += x.z, c[4 * half + 3] += x.w;
                 }
             }
             uint32_t sum = 0;
@@ -174,41 +180,46 @@ __global__ void __launch_bounds__(CHOOSE, 3) kv_choose_kernel(const EvictArgs g)
 
     // `need` of the tokens that equal T = prefix stay (none where nobody competes)
     const bool compete = g.keep > g.first + g.last;
-    // each warp looks at a part of the tokens, four a lane: bits 0-3 tell which of them are above T (or
-    // stay anyhow), bits 4-7 which equal it
-    const int part = ((size + CHOOSE_WARPS - 1) / CHOOSE_WARPS + 127) / 128 * 128;
+    // each warp looks at a part of the tokens, eight a lane: the low bits tell which of them are above T
+    // (or stay anyhow), the high ones which equal it
+    constexpr int EACH = 8, STEP = 32 * EACH;
+    const int part = ((size + CHOOSE_WARPS - 1) / CHOOSE_WARPS + EACH - 1) / EACH * EACH;
     const int j0 = min(warp * part, size), j1 = min(j0 + part, size);
     auto look = [&](int j) {
-        uint32_t k[4];
-        if (j + 3 < g.held) {
-            const uint4 v = *reinterpret_cast<const uint4*>(keys + j);
-            k[0] = v.x, k[1] = v.y, k[2] = v.z, k[3] = v.w;
+        uint32_t k[EACH];
+        if (j + EACH <= g.held) {
+#pragma unroll
+            for (int i = 0; i < EACH; i += 4) {
+                const uint4 v = *reinterpret_cast<const uint4*>(keys + j + i);
+                k[i] = v.x, k[i + 1] = v.y, k[i + 2] = v.z, k[i + 3] = v.w;
+            }
         } else {
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+            for (int i = 0; i < EACH; ++i)
                 k[i] = j + i < j1 ? key(j + i) : 0u;
         }
         uint32_t m = 0;
-        if (compete && j + 3 < j1 && lo + j >= from && lo + j + 3 < to) {
+        if (compete && j + EACH <= j1 && lo + j >= from && lo + j + EACH <= to) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                m |= (k[i] > prefix ? 1u << i : 0u) | (k[i] == prefix ? 16u << i : 0u);
+            for (int i = 0; i < EACH; ++i)
+                m |= (k[i] > prefix ? 1u << i : 0u) | (k[i] == prefix ? 1u << (EACH + i) : 0u);
             return m;
         }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < EACH; ++i) {
             const int at = lo + j + i;
             const bool mine = j + i < j1, free = at >= from && at < to;
             m |= mine && (!free || (compete && k[i] > prefix)) ? 1u << i : 0u;
-            m |= mine && free && compete && k[i] == prefix ? 16u << i : 0u;
+            m |= mine && free && compete && k[i] == prefix ? 1u << (EACH + i) : 0u;
         }
         return m;
     };
+    constexpr uint32_t ABOVE = (1u << EACH) - 1, EQUAL = ABOVE << EACH;
     uint2 sum = make_uint2(0, 0);
-    for (int j = j0; j < j1; j += 128) {
-        const uint32_t m = look(j + 4 * lane);
-        sum.x += __popc(m & 15u);
-        sum.y += __popc(m & 0xf0u);
+    for (int j = j0; j < j1; j += STEP) {
+        const uint32_t m = look(j + EACH * lane);
+        sum.x += __popc(m & ABOVE);
+        sum.y += __popc(m & EQUAL);
     }
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) {
@@ -235,8 +246,8 @@ __global__ void __launch_bounds__(CHOOSE, 3) kv_choose_kernel(const EvictArgs g)
             sum.y += ld_cluster_u32(cluster_map(at + 4, r));
         }
     }
-    for (int j = j0; j < j1; j += 128) {
-        const uint32_t m = look(j + 4 * lane), own = __popc(m & 15u) | __popc(m & 0xf0u) << 16;
+    for (int j = j0; j < j1; j += STEP) {
+        const uint32_t m = look(j + EACH * lane), own = __popc(m & ABOVE) | __popc(m & EQUAL) << 16;
         uint32_t to_here = own;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
@@ -246,17 +257,17 @@ __global__ void __launch_bounds__(CHOOSE, 3) kv_choose_kernel(const EvictArgs g)
         uint32_t na = sum.x + ((to_here - own) & 0xffffu), ne = sum.y + ((to_here - own) >> 16);
         if (own) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const bool a = m >> i & 1u, e = m >> (4 + i) & 1u;
+            for (int i = 0; i < EACH; ++i) {
+                const bool a = m >> i & 1u, e = m >> (EACH + i) & 1u;
                 if (a || (e && ne < need))
-                    kept[na + min(ne, need)] = lo + j + 4 * lane + i;
+                    kept[na + min(ne, need)] = lo + j + EACH * lane + i;
                 na += a;
                 ne += e;
             }
         }
-        const uint32_t all = __shfl_sync(0xffffffffu, to_here, 31);
-        sum.x += all & 0xffffu;
-        sum.y += all >> 16;
+        const uint32_t last = __shfl_sync(0xffffffffu, to_here, 31);
+        sum.x += last & 0xffffu;
+        sum.y += last >> 16;
     }
     if (g.cluster > 1)
         cluster_sync();   // the others have read this CTA's counts
