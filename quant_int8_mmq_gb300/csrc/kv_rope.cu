@@ -16,7 +16,7 @@ namespace {
 constexpr int THREADS = 256;
 
 // ------------------------------------------------------------------ rows
-// A thread takes V pairs of a row (16 bytes of first and 16 of second values, or of the pairs
+// A thread takes V pairs of a row (16 bytes of first and 16 of second values, or 32 of the pairs
 // themselves), which is all that a pair needs, so rows may be turned in place; where there are
 // values that stay, further threads of the row copy 2 V of them each.
 template <typename T>
@@ -25,49 +25,44 @@ struct Pairs {
     alignas(16) T a[V];
     alignas(16) T b[V];
 };
-constexpr int BATCH = 4;          // rows of a thread on their way at once
+constexpr int BATCH = 2;          // rows of a thread on their way at once
 constexpr int TABLE = 2048;       // angles of a CTA's tokens, at most
 
-// `wide`: every chunk is whole and aligned to 16 bytes.  Else element by element: na and nb
-// of a and b, the b's `apart` after the a's, elements of a `step` apart.
+// a: na values from x on, b: nb values from x + apart on.  `wide`: all V or none, aligned to 16 bytes.
 template <typename T>
-__device__ __forceinline__ void load_pairs(Pairs<T>& p, const T* x, bool wide, int na, int nb, int step, int apart)
+__device__ __forceinline__ void load_pairs(Pairs<T>& p, const T* x, bool wide, int na, int nb, int apart)
 {
-    constexpr int V = Pairs<T>::V;
     if (wide) {
-        const int second = step == 1 ? apart : V;
         if (na > 0)
             *reinterpret_cast<uint4*>(p.a) = *reinterpret_cast<const uint4*>(x);
         if (nb > 0)
-            *reinterpret_cast<uint4*>(p.b) = *reinterpret_cast<const uint4*>(x + second);
+            *reinterpret_cast<uint4*>(p.b) = *reinterpret_cast<const uint4*>(x + apart);
         return;
     }
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
+    for (int i = 0; i < Pairs<T>::V; ++i) {
         if (i < na)
-            p.a[i] = x[i * step];
+            p.a[i] = x[i];
         if (i < nb)
-            p.b[i] = x[i * step + apart];
+            p.b[i] = x[i + apart];
     }
 }
 template <typename T>
-__device__ __forceinline__ void store_pairs(const Pairs<T>& p, T* x, bool wide, int na, int nb, int step, int apart)
+__device__ __forceinline__ void store_pairs(const Pairs<T>& p, T* x, bool wide, int na, int nb, int apart)
 {
-    constexpr int V = Pairs<T>::V;
     if (wide) {
-        const int second = step == 1 ? apart : V;
         if (na > 0)
             *reinterpret_cast<uint4*>(x) = *reinterpret_cast<const uint4*>(p.a);
         if (nb > 0)
-            *reinterpret_cast<uint4*>(x + second) = *reinterpret_cast<const uint4*>(p.b);
+            *reinterpret_cast<uint4*>(x + apart) = *reinterpret_cast<const uint4*>(p.b);
         return;
     }
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
+    for (int i = 0; i < Pairs<T>::V; ++i) {
         if (i < na)
-            x[i * step] = p.a[i];
+            x[i] = p.a[i];
         if (i < nb)
-            x[i * step + apart] = p.b[i];
+            x[i + apart] = p.b[i];
     }
 }
 
@@ -76,53 +71,60 @@ struct RopeArgs {
     const int* pos;
     RopeView r;
     int heads, dim, ntok;
-    int toks;              // tokens of a CTA
-    int chunks, copies;    // threads of a row that turn pairs, and that copy what stays
+    unsigned int heads_inv;   // 2^32 / heads, rounded up
+    int toks;                 // tokens of a CTA
+    int chunks, copies;       // threads of a row that turn pairs, and that copy what stays
     bool wide;
 };
 
 template <typename T, bool INTERLEAVED>
-__global__ void __launch_bounds__(THREADS) rope_kernel(const RopeArgs g)
+__global__ void __launch_bounds__(THREADS, 5) rope_kernel(const RopeArgs g)
 {
     constexpr int V = Pairs<T>::V;
-    __shared__ float2 table[TABLE];
+    __shared__ __align__(16) float2 table[TABLE];
     const int half = g.r.rot / 2, first = blockIdx.x * g.toks, toks = min(g.toks, g.ntok - first);
     grid_dep_wait();
     grid_dep_launch();
 
-    // the thread's chunk, the same in all its rows: rows[0], rows[0] + step, ... of the CTA's
+    // the thread's chunk, the same in all its rows: `row`, `row` + step, ... of the CTA's
     const int width = g.chunks + g.copies, step = THREADS / width, chunk = threadIdx.x % width;
     const int nrow = toks * g.heads;
     int row = threadIdx.x / width;
     if (row >= step)
         row = nrow;   // more threads than rows at once
     const bool turns = chunk < g.chunks;
-    int at, na, nb, apart, stride;
-    if (turns) {
-        at = INTERLEAVED ? 2 * V * chunk : V * chunk;
-        na = nb = min(V, half - V * chunk);
-        apart = INTERLEAVED ? 1 : half;
-        stride = INTERLEAVED ? 2 : 1;
-    } else {
+    int at, na, nb, apart = V;
+    if (!turns) {
         at = g.r.rot + 2 * V * (chunk - g.chunks);
         na = min(V, g.dim - at);
         nb = max(0, min(V, g.dim - at - V));
-        apart = V;
-        stride = 1;
+    } else if (INTERLEAVED) {   // 2 V values, a then b
+        at = 2 * V * chunk;
+        na = min(V, g.r.rot - at);
+        nb = max(0, min(V, g.r.rot - at - V));
+    } else {
+        at = V * chunk;
+        na = nb = min(V, half - at);
+        apart = half;
     }
+    // token of row i; i heads < 2^32
+    auto token = [&](int i) { return g.heads == 1 ? i : static_cast<int>(__umulhi(static_cast<unsigned int>(i), g.heads_inv)); };
     auto where = [&](const KvRows& r, int i) {
-        return static_cast<T*>(r.data) + (first + i / g.heads) * r.tok + i % g.heads * r.head + at;
+        const int t = token(i);
+        return static_cast<T*>(r.data) + (first + t) * r.tok + (i - t * g.heads) * r.head + at;
     };
     Pairs<T> p[BATCH];
     auto load = [&](int i) {
 #pragma unroll
         for (int k = 0; k < BATCH; ++k)
             if (i + k * step < nrow)
-                load_pairs<T>(p[k], where(g.x, i + k * step), g.wide, na, nb, stride, apart);
+                load_pairs<T>(p[k], where(g.x, i + k * step), g.wide, na, nb, apart);
     };
     load(row);
-    for (int i = threadIdx.x; i < toks * half; i += THREADS)
-        table[i] = rope_turn(g.r, i % half, g.pos[first + i / half]);
+    for (int i = threadIdx.x; i < toks * half; i += THREADS) {
+        const int t = i / half;
+        table[i] = rope_turn(g.r, i - t * half, g.pos[first + t]);
+    }
     __syncthreads();
     for (; row < nrow; row += BATCH * step) {
 #pragma unroll
@@ -131,31 +133,44 @@ __global__ void __launch_bounds__(THREADS) rope_kernel(const RopeArgs g)
             if (i >= nrow)
                 break;
             if (turns) {
-                const float2* cs = table + i / g.heads * half + V * chunk;
+                const float2* cs = table + token(i) * half + V * chunk;
+                if constexpr (INTERLEAVED) {
 #pragma unroll
-                for (int j = 0; j < V; ++j) {
-                    if (j >= na)
-                        break;
-                    T& u = INTERLEAVED && g.wide ? (2 * j < V ? p[k].a[2 * j % V] : p[k].b[2 * j % V]) : p[k].a[j];
-                    T& v = INTERLEAVED && g.wide ? (2 * j < V ? p[k].a[2 * j % V + 1] : p[k].b[2 * j % V + 1]) : p[k].b[j];
-                    const float a = Elt<T>::to(u), b = Elt<T>::to(v);
-                    u = Elt<T>::from(rope_first(a, b, cs[j]));
-                    v = Elt<T>::from(rope_second(a, b, cs[j]));
+                    for (int j = 0; j < V; ++j) {
+                        T* pair = 2 * j < V ? p[k].a + 2 * j : p[k].b + (2 * j - V);
+                        if (2 * j < V ? 2 * j < na : 2 * j - V < nb) {
+                            const float a = Elt<T>::to(pair[0]), b = Elt<T>::to(pair[1]);
+                            pair[0] = Elt<T>::from(rope_first(a, b, cs[j]));
+                            pair[1] = Elt<T>::from(rope_second(a, b, cs[j]));
+                        }
+                    }
+                } else {
+#pragma unroll
+                    for (int j = 0; j < V; ++j)
+                        if (j < na) {
+                            const float a = Elt<T>::to(p[k].a[j]), b = Elt<T>::to(p[k].b[j]);
+                            p[k].a[j] = Elt<T>::from(rope_first(a, b, cs[j]));
+                            p[k].b[j] = Elt<T>::from(rope_second(a, b, cs[j]));
+                        }
                 }
             }
-            store_pairs<T>(p[k], where(g.out, i), g.wide, na, nb, stride, apart);
+            store_pairs<T>(p[k], where(g.out, i), g.wide, na, nb, apart);
         }
         load(row + BATCH * step);
     }
 }
 
 // ------------------------------------------------------------------ into the cache
-// The lanes of kv_rows.cuh: 8 values a lane, D / 8 lanes a row, 2 rows of 128 values (4 of 64)
-// a warp at once.  A token's keys and values come first, then its queries; one pass's rows are
-// loaded while the last one's are turned.
+// A lane has 8 values of a row, D / 8 lanes a row, 2 rows of 128 values (4 of 64) a warp at once.  A
+// token's keys and values come first, then its queries; one pass's rows are loaded while the last
+// one's are turned.
 constexpr int WARPS = THREADS / 32;
 
-enum RopePairs { BY_LANES = 0, INSIDE = 1, ANYWHERE = 2 };   // where a value's partner is
+// Where a value's partner is.  HALVES: a lane has four values of one half of what turns and the four
+// they pair with (and, of what stays, four of each half), which takes 32-value groups to lie in
+// one or the other.  INSIDE: 8 consecutive values, pairs among them.  ANYWHERE: 8 consecutive values,
+// partners read from memory.
+enum RopePairs { HALVES = 0, INSIDE = 1, ANYWHERE = 2 };
 
 struct EnterArgs {
     KvView c;
@@ -167,11 +182,45 @@ struct EnterArgs {
     bool wide_q, wide_kv;
 };
 
-template <int D, int PAIRS, typename T>
-__device__ __forceinline__ void turn8(float (&x)[8], const T* row, int l, const RopeView& r, const float2* cs)
+// The two fours of values of lane l: from first and from second on (8 consecutive ones in the other
+// layouts).
+struct Fours {
+    int first, second;
+    bool turns;
+    int pair;              // of the first value
+};
+template <int PAIRS>
+__device__ __forceinline__ Fours fours_of(int l, int dim, int rot)
+{
+    if constexpr (PAIRS != HALVES)
+        return {8 * l, 8 * l + 4, true, 0};
+    const int half = rot / 2, stay = dim - rot;
+    return 4 * l < half ? Fours{4 * l, half + 4 * l, true, 4 * l}
+                        : Fours{half + 4 * l, half + 4 * l + stay / 2, false, 0};
+}
+template <typename T>
+__device__ __forceinline__ void load_fours(const T* row, const Fours& f, bool wide, float (&x)[8])
+{
+    const float4 a = load4(row + f.first, wide), b = load4(row + f.second, wide);
+    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w;
+    x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+}
+
+template <int PAIRS, typename T>
+__device__ __forceinline__ void turn8(float (&x)[8], const T* row, int l, const Fours& f, const RopeView& r, const float2* cs)
 {
     const int half = r.rot / 2;
-    if constexpr (PAIRS == INSIDE) {
+    if constexpr (PAIRS == HALVES) {
+        if (f.turns) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float2 c = cs[f.pair + j];
+                const float a = x[j], b = x[4 + j];
+                x[j] = rope_first(a, b, c);
+                x[4 + j] = rope_second(a, b, c);
+            }
+        }
+    } else if constexpr (PAIRS == INSIDE) {
 #pragma unroll
         for (int j = 0; j < 4; ++j)
             if (4 * l + j < half) {
@@ -180,21 +229,8 @@ __device__ __forceinline__ void turn8(float (&x)[8], const T* row, int l, const 
                 x[2 * j] = rope_first(a, b, c);
                 x[2 * j + 1] = rope_second(a, b, c);
             }
-    } else if constexpr (PAIRS == BY_LANES) {   // half is a multiple of 8
-        const int lanes = half / 8;
-        const bool lower = l < lanes, turns = l < 2 * lanes;
-        const int lane = threadIdx.x % 32, from = turns ? lower ? lane + lanes : lane - lanes : lane;
-        float y[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-            y[j] = __shfl_sync(0xffffffffu, x[j], from);
-        if (turns) {
-            const float2* c = cs + 8 * (lower ? l : l - lanes);
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                x[j] = lower ? rope_first(x[j], y[j], c[j]) : rope_second(y[j], x[j], c[j]);
-        }
     } else {
+        row += 8 * l;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             const int d = 8 * l + j;
@@ -209,12 +245,47 @@ __device__ __forceinline__ void turn8(float (&x)[8], const T* row, int l, const 
     }
 }
 
+// A key row whose lanes have two fours each: the largest of a group among 8 lanes, and words of
+// codes put together by two lanes, the even one of its first group's, the odd one of its second's.
+template <int D>
+__device__ __forceinline__ void put_key_fours(const float (&x)[8], const Fours& f, int l, int slot, uint8_t* piece, bool store)
+{
+    using P = Piece<D>;
+    uint32_t word[2];
+    float s[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        float y[4], a = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            y[i] = x[4 * h + i] == x[4 * h + i] ? x[4 * h + i] : 0.0f;   // no number is 0
+            a = fmaxf(a, fabsf(y[i]));
+        }
+#pragma unroll
+        for (int d = 1; d < 8; d <<= 1)
+            a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, d));
+        s[h] = kv_scale(a);
+        uint32_t n[4];
+        kv_codes(y, s[h], n);
+        word[h] = (n[0] & 15u) | (n[2] & 15u) << 4 | (n[1] & 15u) << 16 | (n[3] & 15u) << 20;
+    }
+    const bool odd = l & 1;
+    const uint32_t other = __shfl_xor_sync(0xffffffffu, odd ? word[0] : word[1], 1);
+    const uint32_t own = odd ? other | word[1] << 8 : word[0] | other << 8;
+    const int from = odd ? f.second : f.first, group = from / 32;
+    if (!store)
+        return;
+    *reinterpret_cast<uint32_t*>(piece + P::k_chunk(slot, group) + from % 32 / 8 * 4) = own;
+    if (l % 8 < 2)
+        *reinterpret_cast<__half*>(piece + P::k_scale(slot, group)) = __float2half_rn(odd ? s[1] : s[0]);   // exact
+}
+
 template <int D, typename T, int PAIRS>
-__global__ void __launch_bounds__(THREADS) kv_write_rope_kernel(const EnterArgs g)
+__global__ void __launch_bounds__(THREADS, 4) kv_write_rope_kernel(const EnterArgs g)
 {
     using P = Piece<D>;
     constexpr int LANES = D / 8, AT_ONCE = 32 / LANES;
-    __shared__ float2 table[WARPS * D / 2];
+    __shared__ __align__(16) float2 table[WARPS * D / 2];
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
     const int half = g.r.rot / 2, first = blockIdx.x * g.toks, toks = min(g.toks, g.ntok - first);
     grid_dep_wait();
@@ -225,24 +296,19 @@ __global__ void __launch_bounds__(THREADS) kv_write_rope_kernel(const EnterArgs 
     const bool spare = warp / warps >= toks;
     const int t = first + tok, hk = g.c.kv_heads;
     const int l = lane % LANES, sub = warp % warps * AT_ONCE + lane / LANES, step = warps * AT_ONCE;
-    // passes over the rows: keys and values, then queries
-    const int enters = (2 * hk + step - 1) / step, passes = enters + (g.heads + step - 1) / step;
+    const Fours mine = fours_of<PAIRS>(l, D, g.r.rot), plain = {8 * l, 8 * l + 4, false, 0};
+    // passes over the rows: keys, values, queries
+    const int each = (hk + step - 1) / step, passes = 2 * each + (g.heads + step - 1) / step;
     auto row_of = [&](int pass) -> const T* {
-        const KvRows* in;
-        int h;
-        if (pass < enters) {
-            const int i = min(pass * step + sub, 2 * hk - 1);
-            in = i < hk ? &g.k : &g.v;
-            h = i < hk ? i : i - hk;
-        } else {
-            in = &g.q;
-            h = min((pass - enters) * step + sub, g.heads - 1);
-        }
-        return static_cast<const T*>(in->data) + t * in->tok + h * in->head + 8 * l;
+        const KvRows& in = pass < each ? g.k : pass < 2 * each ? g.v : g.q;
+        const int h = pass < each ? min(pass * step + sub, hk - 1)
+                      : pass < 2 * each ? min((pass - each) * step + sub, hk - 1)
+                                        : min((pass - 2 * each) * step + sub, g.heads - 1);
+        return static_cast<const T*>(in.data) + t * in.tok + h * in.head;
     };
     const T* row = row_of(0);
     float ahead[8];
-    load8(row, g.wide_kv, ahead);
+    load_fours(row, mine, g.wide_kv, ahead);
     for (int i = threadIdx.x; i < toks * half; i += THREADS)
         table[i] = rope_turn(g.r, i % half, g.pos[first + i / half]);
     int slot;
@@ -258,30 +324,34 @@ __global__ void __launch_bounds__(THREADS) kv_write_rope_kernel(const EnterArgs 
         const T* here = row;
         if (pass + 1 < passes) {
             row = row_of(pass + 1);
-            load8(row, pass + 1 < enters ? g.wide_kv : g.wide_q, ahead);
+            load_fours(row, pass + 1 >= each && pass + 1 < 2 * each ? plain : mine, pass + 1 < 2 * each ? g.wide_kv : g.wide_q, ahead);
         }
-        if (pass < enters) {
-            const int i = pass * step + sub;
-            const bool key = i < hk;
-            if (__any_sync(0xffffffffu, key)) {
-                float y[8];
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    y[j] = x[j];
-                turn8<D, PAIRS>(y, here, l, g.r, cs);
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    x[j] = key ? y[j] : x[j];
+        if (pass < each) {
+            const int h = pass * step + sub;
+            const bool store = h < hk && page >= 0 && !spare;
+            uint8_t* piece = g.c.pages + page + h * P::BYTES;
+            turn8<PAIRS>(x, here, l, mine, g.r, cs);
+            if constexpr (PAIRS == HALVES) {
+                put_key_fours<D>(x, mine, l, slot, piece, store);
+            } else {
+                const Codes8 codes = kv_quantise8(x, true);
+                if (store)
+                    Place8<D>(slot, l, true).put(piece, codes, l, true);
             }
-            const Codes8 codes = kv_quantise8(x, key);
-            if (i < 2 * hk && page >= 0 && !spare)
-                Place8<D>(slot, l, key).put(g.c.pages + page + (key ? i : i - hk) * P::BYTES, codes, l, key);
+        } else if (pass < 2 * each) {
+            const int h = (pass - each) * step + sub;
+            const Codes8 codes = kv_quantise8(x, false);
+            if (h < hk && page >= 0 && !spare)
+                Place8<D>(slot, l, false).put(g.c.pages + page + h * P::BYTES, codes, l, false);
         } else {
-            const int h = (pass - enters) * step + sub;
-            turn8<D, PAIRS>(x, here, l, g.r, cs);
+            const int h = (pass - 2 * each) * step + sub;
+            turn8<PAIRS>(x, here, l, mine, g.r, cs);
             __syncwarp();   // in place: every lane has what it needs of the row
-            if (h < g.heads && !spare)
-                store8(static_cast<T*>(g.q_out.data) + t * g.q_out.tok + h * g.q_out.head + 8 * l, g.wide_q, x);
+            if (h < g.heads && !spare) {
+                T* out = static_cast<T*>(g.q_out.data) + t * g.q_out.tok + h * g.q_out.head;
+                store4(out + mine.first, make_float4(x[0], x[1], x[2], x[3]), g.wide_q);
+                store4(out + mine.second, make_float4(x[4], x[5], x[6], x[7]), g.wide_q);
+            }
         }
     }
 }
@@ -293,8 +363,8 @@ cudaError_t launch_enter(const EnterArgs& a, cudaStream_t s)
     count_launch();
     if (a.r.interleaved)
         return launch_dependent(kv_write_rope_kernel<D, T, INSIDE>, grid, block, s, a);
-    if (a.r.rot % 16 == 0)
-        return launch_dependent(kv_write_rope_kernel<D, T, BY_LANES>, grid, block, s, a);
+    if (a.r.rot % 64 == 0 && (D - a.r.rot) % 64 == 0)
+        return launch_dependent(kv_write_rope_kernel<D, T, HALVES>, grid, block, s, a);
     return launch_dependent(kv_write_rope_kernel<D, T, ANYWHERE>, grid, block, s, a);
 }
 
@@ -304,14 +374,20 @@ cudaError_t launch_rope(const KvRows& x, const KvRows& out, const int* pos, cons
                         int dim, int ntok, bool wide, cudaStream_t s)
 {
     const int v = dtype == KV_F32 ? 4 : 8, half = r.rot / 2;
-    RopeArgs a = {x, out, pos, r, heads, dim, ntok, 1, (half + v - 1) / v, 0, wide && half % v == 0 && dim % v == 0};
+    RopeArgs a = {x, out, pos, r, heads, dim, ntok, 0, 1, (half + v - 1) / v, 0, wide && half % v == 0 && dim % v == 0};
     if (x.data != out.data || x.tok != out.tok || x.head != out.head)   // in place nothing is copied
         a.copies = (dim - r.rot + 2 * v - 1) / (2 * v);
-    // tokens of a CTA: rows enough for its threads
+    a.heads_inv = static_cast<unsigned int>(((1ull << 32) + heads - 1) / heads);
+    // tokens of a CTA: up to four rows a thread while the chip stays full, one at least
     const int step = THREADS / (a.chunks + a.copies);
-    int toks = step / heads;
-    toks = toks < 1 ? 1 : toks;
-    toks = toks < TABLE / half ? toks : TABLE / half;
+    int toks = 1;
+    for (int rows = 4; rows >= 1; rows /= 2) {
+        toks = rows * step / heads;
+        toks = toks < TABLE / half ? toks : TABLE / half;
+        toks = toks < 1 ? 1 : toks;
+        if ((ntok + toks - 1) / toks >= 152 * 6)
+            break;
+    }
     a.toks = toks;
     const dim3 grid(static_cast<unsigned int>((ntok + toks - 1) / toks)), block(THREADS);
     count_launch();

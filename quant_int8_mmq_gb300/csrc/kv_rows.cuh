@@ -80,6 +80,24 @@ __device__ __forceinline__ float quotient(float x, float y, float r)
     return fmaf(fmaf(-q, y, x), r, q);
 }
 
+// The scale of a group whose largest magnitude is a.
+__device__ __forceinline__ float kv_scale(float a)
+{
+    const float amax = fminf(a, 1e30f);   // the scale's limit is far below
+    const uint32_t up = (__float_as_uint(quotient(amax, 7.5f, 1.0f / 7.5f)) + 0x1FFFFu) & ~0x1FFFFu;
+    return fminf(fmaxf(__uint_as_float(up), KV_SCALE_MIN), KV_SCALE_MAX);
+}
+// code = rint(x / s) + 8 in the low bits of 1.5 * 2^23 + 8 + x / s; limiting x to [-8 s, 7 s]
+// limits the rounded quotient to [-8, 7]
+template <int N>
+__device__ __forceinline__ void kv_codes(const float (&x)[N], float s, uint32_t (&n)[N])
+{
+    const float inv = __frcp_rn(s);
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        n[i] = __float_as_uint(quotient(fminf(fmaxf(x[i], -8.0f * s), 7.0f * s), s, inv) + 12582920.0f);
+}
+
 // The codes of a lane's 8 values of a key or a value row: two 16-bit halves, and the group's scale.
 // The four lanes of a group call it together.
 struct Codes8 {
@@ -102,16 +120,9 @@ __device__ __forceinline__ Codes8 kv_quantise8(float (&x)[8], bool key)
     }
     a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 1));
     a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 2));
-    const float amax = fminf(a, 1e30f);   // the scale's limit is far below
-    const uint32_t up = (__float_as_uint(quotient(amax, 7.5f, 1.0f / 7.5f)) + 0x1FFFFu) & ~0x1FFFFu;
-    const float s = fminf(fmaxf(__uint_as_float(up), KV_SCALE_MIN), KV_SCALE_MAX);
-    const float inv = __frcp_rn(s);
-    // code = rint(x / s) + 8 in the low bits of 1.5 * 2^23 + 8 + x / s; limiting x to [-8 s, 7 s]
-    // limits the rounded quotient to [-8, 7]
+    const float s = kv_scale(a);
     uint32_t n[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-        n[i] = __float_as_uint(quotient(fminf(fmaxf(x[i], -8.0f * s), 7.0f * s), s, inv) + 12582920.0f);
+    kv_codes(x, s, n);
     // 16-bit halves of four codes: key values 0 2 4 6 | 1 3 5 7, value values 0 1 2 3 | 4 5 6 7
     const uint32_t lo = n[0] + ((key ? n[2] : n[1]) << 4) + ((key ? n[4] : n[2]) << 8) + ((key ? n[6] : n[3]) << 12);
     const uint32_t hi = (key ? n[1] : n[4]) + ((key ? n[3] : n[5]) << 4) + ((key ? n[5] : n[6]) << 8) + (n[7] << 12);
