@@ -452,9 +452,12 @@ mmq_status mmq_kv_attend(const mmq_kv_cache* c, const mmq_rows* q, const mmq_row
  * from 0, so nothing has to be cleared).  decay in [0, 1].  new_weights may be weights; a buffer of
  * its own keeps the old ones, for a step that may be taken back.  Slots past the last token, and
  * pages of no sequence with new tokens, are left as they were.  A page that two sequences of the call
- * share gets one of their sums.  A row that is not finite, or past max_q (see there), adds nothing.
- * The sums are f32, in a fixed order.
- * Workspace: mmq_kv_attend_weights_workspace_bytes, more than 0 where ntok is. */
+ * share gets one of their sums where new_weights is a buffer of its own, and in place may get one of
+ * them added to the other.  A row that is not finite, or past max_q (see there), adds nothing.  The
+ * sums are f32, in a fixed order.
+ * Workspace: mmq_kv_attend_weights_workspace_bytes, more than 0 where ntok is.  For few new tokens it
+ * has room for the scores of max_kv keys, up to a gigabyte, so that K is read once: a max_kv near
+ * the longest length keeps it small.  What it holds before does not matter. */
 mmq_status mmq_kv_attend_weights_workspace_bytes(const mmq_kv_cache* c, int dtype, int heads, int ntok, int max_q,
                                                  int max_kv, int window, int sinks, size_t* bytes);
 mmq_status mmq_kv_attend_weights(const mmq_kv_cache* c, const mmq_rows* q, const mmq_rows* out, int heads, int ntok,
@@ -546,8 +549,9 @@ const char* mmq_last_path(void);
 /* Number of kernel launches the library has made in this process (every entry
  * point that launches adds the kernels it launched: prepass 1, repack 4 or 5,
  * GEMM 1, or 2 when K-half tiles are first zeroed; cache write and read 1, attention 1,
- * or 2 when parts are joined through the workspace, and 1 more for the weights; eviction 2;
- * rotary positions 1). */
+ * or 2 when parts are joined through the workspace, and for the weights 1 more, or 2 when a
+ * sequence's kv head has more than 128 rows; eviction 2; rotary positions 1, with the cache write or
+ * without). */
 unsigned long long mmq_launch_count(void);
 
 /* Library version string. */

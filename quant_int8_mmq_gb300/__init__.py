@@ -285,6 +285,7 @@ def mmq_kv_evict(cache, weights, new_table, new_pages, keep, first, last, max_kv
 
 def mmq_rope_frequencies(scaling, rot_dim: int, base=10000.0, factor=1.0, original=0.0):
     """(frequencies in radians per position, magnitude) of a scaling; host only."""
+    rot_dim = max(-1, min(rot_dim, 1 << 16))    # ctypes would drop high bits; what is out of range stays so
     freq, m = (ctypes.c_double * max(rot_dim // 2, 1))(), ctypes.c_float()
     _check(load().mmq_rope_frequencies(ROPE_SCALINGS.get(scaling, scaling), rot_dim, base, factor, original, freq,
                                        ctypes.byref(m)), "mmq_rope_frequencies")

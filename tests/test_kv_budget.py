@@ -256,3 +256,9 @@ def test_helpers_check_shapes_types_and_devices(mmq_lib, monkeypatch):
         with pytest.raises(ValueError, match=what):
             call()
     assert [c for c in calls if not c.endswith("bytes")] == []
+
+
+def test_numbers_past_32_bits_are_not_cut(mmq_lib):
+    for rot in (2 ** 32 + 64, 2 ** 40, -2 ** 40):
+        with pytest.raises(mmq.MMQError):
+            mmq.mmq_rope_frequencies("none", rot)

@@ -15,7 +15,7 @@ import torch
 
 import quant_int8_mmq_gb300 as mmq
 from tests import budget_reference as ref
-from tests.test_kv_gpu import BF16, DEV, F16, F32, HALF_ULP, Batch, status
+from tests.test_kv_gpu import BF16, DEV, F16, F32, HALF_ULP, Batch, hard_rows, status
 
 pytestmark = pytest.mark.gpu
 
@@ -622,3 +622,130 @@ def test_a_conversation_within_a_budget():
             held = weights[cache[1][0, j // 64].long(), h, j % 64]
             assert (held.double() - sums[h]).abs().max() < 1e-4 * sums[h].max()
     assert status() == 0
+
+
+# ------------------------------------------------------------------------------------ as programs use them
+@pytest.mark.parametrize("dtype", [F32, F16])
+@pytest.mark.parametrize("new,lens,window,sinks,wide", [
+    ([1, 2, 1], [5000, 90, 700], 0, 0, 0), ([1, 2, 1], [5000, 90, 700], 130, 70, 0), ([2, 1], [9000, 20000], 0, 0, 0),
+    ([1, 2, 1, 1, 1, 1, 2, 1], [500, 90, 700, 1, 64, 65, 128, 40], 100, 0, 1), ([9, 20], [300, 1000], 200, 1, 0),
+    ([150, 1, 70], [1000, 30, 70], 0, 0, 0), ([300, 40], [2000, 555], 333, 7, 0)])
+def test_a_workspace_may_hold_anything(dtype, new, lens, window, sinks, wide):
+    """Scores, statistics and operands of other calls, or no numbers, change nothing."""
+    b = Batch(new, lens, 2, 128, dtype, max_pages=(1 << 30) // (256 * 8 * 2 * 8) + 1 if wide else None)
+    q, most = b.q(8), b.max_pages * 64
+    need = mmq.mmq_kv_attend_weights_workspace_bytes(mmq._kv_cache(*b.cache)[0], mmq.DTYPES[str(dtype)[6:]], 8, b.rows,
+                                                     max(new), most, window, sinks)
+    got = []
+    for byte in (0, 0xFF, 0x43):                                        # 0x43434343 is 195.26
+        w = weights_for(b)
+        out, _ = mmq.kv_attend_weights(q, w, *b.cache, max(new), window=window, sinks=sinks,
+                                       workspace=torch.full((need,), byte, dtype=torch.uint8, device=DEV))
+        got.append((out, w))
+    assert status() == 0
+    for out, w in got[1:]:
+        assert torch.equal(out, got[0][0]) and torch.equal(w, got[0][1])
+
+
+@pytest.mark.parametrize("dtype", [F32, F16, BF16])
+@pytest.mark.parametrize("dim,rot,interleaved", [(128, 128, False), (128, 64, False), (128, 34, False), (128, 128, True),
+                                                 (64, 64, False), (64, 20, True)])
+def test_keys_of_any_kind_enter_turned(dtype, dim, rot, interleaved):
+    """Ties, zeros, huge, tiny and infinite values and no numbers, byte for byte as turning and writing."""
+    plan = mmq.rope_plan(rot, interleaved=interleaved)
+    b = Batch([120], [150], 2, dim, dtype, fill=False)
+    k, v = (hard_rows(120, 2, dim, dtype, s).to(DEV) for s in (5, 6))
+    pos = torch.randint(0, 5, (120,), dtype=torch.int32, device=DEV)    # many rows at 0, where ties stay ties
+    q, other = rand(120, 3, dim, dtype=dtype), b.pages.clone()
+    mmq.kv_write_rope(q, k, v, pos, plan, *b.cache)
+    mmq.kv_write(mmq.rope(k.float(), pos, plan), v.float(), other, *b.cache[1:])
+    assert status() == 0 and torch.equal(b.pages, other)
+
+
+def turn_weigh_evict(b, q, k, v, pos, plan, table, w, keep, stream=None):
+    turned = mmq.kv_write_rope(q, k, v, pos, plan, *b.cache, stream=stream)
+    out, _ = mmq.kv_attend_weights(turned, w, *b.cache, max(b.new), decay=0.5, stream=stream)
+    length, kept = mmq.kv_evict(w, b.pages, b.table, b.start, b.length, table, keep, stream=stream)
+    return turned, out, length, kept
+
+
+def budget_case(seed, new, lens, keep, heads, hk, dim, dtype):
+    n = -(-keep // 64)
+    b = Batch(new, lens, hk, dim, dtype, seed=seed, spare=n * len(lens) + 1)
+    used = set(b.table.flatten().tolist())
+    free = [i for i in range(b.pages.shape[0]) if i not in used][:n * len(lens)]
+    table = torch.tensor(free, dtype=torch.int32, device=DEV).view(len(lens), n)
+    q, k, v = (rand(b.rows, h, dim, dtype=dtype, seed=seed + i) for i, h in enumerate((heads, hk, hk)))
+    pos = torch.randint(0, 5000, (b.rows,), generator=torch.Generator().manual_seed(seed), dtype=torch.int32).to(DEV)
+    return b, q, k, v, pos, mmq.rope_plan(dim), table, weights_for(b), keep
+
+
+def test_calls_on_two_streams_at_once():
+    shapes = [(1, [1, 1, 2], [700, 3000, 90], 200, 8, 2, 128, F16), (2, [150, 40], [900, 4000], 300, 4, 2, 64, F32)]
+    want = []
+    for s in shapes:
+        case = budget_case(*s)
+        want.append((turn_weigh_evict(*case), case))
+    torch.cuda.synchronize()
+    cases, streams = [budget_case(*s) for s in shapes], [torch.cuda.Stream() for _ in shapes]
+    torch.cuda.synchronize()
+    got = [turn_weigh_evict(*c, stream=s) for c, s in zip(cases, streams)]
+    torch.cuda.synchronize()
+    assert status() == 0
+    for (w, wc), g, gc in zip(want, got, cases):
+        for x, y in zip(w, g):
+            assert torch.equal(x, y)
+        assert torch.equal(wc[0].pages, gc[0].pages) and torch.equal(wc[7], gc[7])
+
+
+def test_a_whole_step_replays():
+    b, q, k, v, pos, plan, table, w, keep = budget_case(3, [1, 2, 1], [700, 300, 65], 128, 8, 2, 128, BF16)
+    pages0, w0 = b.pages.clone(), w.clone()
+    want = turn_weigh_evict(b, q, k, v, pos, plan, table, w, keep)
+    pages1, w1 = b.pages.clone(), w.clone()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = turn_weigh_evict(b, q, k, v, pos, plan, table, w, keep)
+    for _ in range(2):
+        b.pages.copy_(pages0)
+        w.copy_(w0)
+        graph.replay()
+        assert torch.equal(b.pages, pages1) and torch.equal(w, w1)
+        assert all(torch.equal(x, y) for x, y in zip(got, want))
+    assert status() == 0
+
+
+def test_pools_past_32_bits():
+    """Page ids whose bytes are past 2^32, against the same tokens in a small pool."""
+    b, q, k, v, pos, plan, table, w, keep = budget_case(4, [1, 20], [300, 200], 128, 16, 8, 64, F16)
+    far = 2 ** 32 // (8 * 64 * 72) + 1
+    n = b.pages.shape[0]
+    big = mmq.kv_pages(far + n, 8, 64)
+    wide = mmq.kv_weights(far + n, 8)
+    big[far:] = b.pages
+    wide[far:] = w
+    other = Batch([1, 20], [300, 200], 8, 64, F16, fill=False)
+    other.pages, other.table = big, torch.where(b.table >= 0, b.table + far, -1)
+    got = turn_weigh_evict(other, q, k, v, pos, plan, table + far, wide, keep)
+    want = turn_weigh_evict(b, q, k, v, pos, plan, table, w, keep)
+    assert status() == 0 and all(torch.equal(x, y) for x, y in zip(got, want))
+    assert torch.equal(big[far:], b.pages) and torch.equal(wide[far:], w)
+
+
+@pytest.mark.parametrize("dtype", [F32, F16])
+@pytest.mark.parametrize("new", [2, 40, 150])
+def test_lengths_that_are_no_lengths(dtype, new):
+    """Below zero nobody has a key; past the table its pages are all there are.  The other sequence is as ever."""
+    b = Batch([new, new], [200, 200], 1, 128, dtype)
+    q, before = b.q(2), weights_for(b)
+    alone = before.clone()
+    mmq.kv_attend_weights(q, alone, *b.cache, new)
+    second, first = b.table[1].long(), b.table[0].long()
+    for m in (-7, 0):
+        w = before.clone()
+        length = torch.tensor([m, 200], dtype=torch.int32, device=DEV)
+        out, _ = mmq.kv_attend_weights(q, w, b.pages, b.table, b.start, length, new)
+        status()
+        assert torch.equal(w[second], alone[second]) and torch.equal(w[first], before[first])
+        assert (out[:new] == 0).all()
