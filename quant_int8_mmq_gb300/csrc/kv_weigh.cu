@@ -227,10 +227,10 @@ __device__ __forceinline__ void release(uint32_t bar, int lane)
         mbar_arrive(bar);
 }
 
-// The weights of some columns of a key.
-template <bool MASKED, int N>
-__device__ __forceinline__ void add_columns(const AttendArgs& g, const float (&x)[N], const Columns* cols, int c0, int n,
-                                            int key, float2& sum)
+// The weights of some columns, c0 on, of KS keys (key, key + KEYS, ...).
+template <bool MASKED, int N, int KS>
+__device__ __forceinline__ void add_columns(const AttendArgs& g, const float (&x)[KS][N], const Columns* cols, int c0, int n,
+                                            int key, float2 (&sum)[KS])
 {
 #pragma unroll
     for (int c = 0; c < N; c += 4) {
@@ -239,20 +239,24 @@ __device__ __forceinline__ void add_columns(const AttendArgs& g, const float (&x
         const float4 f = *reinterpret_cast<const float4*>(cols->coef + c0 + c);
         const float4 r = *reinterpret_cast<const float4*>(cols->ref + c0 + c);
         const float4 v = *reinterpret_cast<const float4*>(cols->inv + c0 + c);
-        float4 p = make_float4(kv_ex2(fmaf(x[c], f.x, -r.x)), kv_ex2(fmaf(x[c + 1], f.y, -r.y)),
-                               kv_ex2(fmaf(x[c + 2], f.z, -r.z)), kv_ex2(fmaf(x[c + 3], f.w, -r.w)));
-        if constexpr (MASKED) {
-            const int4 pos = *reinterpret_cast<const int4*>(cols->pos + c0 + c);
-            auto seen = [&](int i, int at) {
-                return c0 + c + i < n && key <= at && (g.window == 0 || key > at - g.window || key < g.sinks);
-            };
-            p.x = seen(0, pos.x) ? p.x : 0.0f;
-            p.y = seen(1, pos.y) ? p.y : 0.0f;
-            p.z = seen(2, pos.z) ? p.z : 0.0f;
-            p.w = seen(3, pos.w) ? p.w : 0.0f;
+        const int4 pos = MASKED ? *reinterpret_cast<const int4*>(cols->pos + c0 + c) : make_int4(0, 0, 0, 0);
+#pragma unroll
+        for (int k = 0; k < KS; ++k) {
+            float4 p = make_float4(kv_ex2(fmaf(x[k][c], f.x, -r.x)), kv_ex2(fmaf(x[k][c + 1], f.y, -r.y)),
+                                   kv_ex2(fmaf(x[k][c + 2], f.z, -r.z)), kv_ex2(fmaf(x[k][c + 3], f.w, -r.w)));
+            if constexpr (MASKED) {
+                const int j = key + k * KEYS;
+                auto seen = [&](int i, int at) {
+                    return c0 + c + i < n && j <= at && (g.window == 0 || j > at - g.window || j < g.sinks);
+                };
+                p.x = seen(0, pos.x) ? p.x : 0.0f;
+                p.y = seen(1, pos.y) ? p.y : 0.0f;
+                p.z = seen(2, pos.z) ? p.z : 0.0f;
+                p.w = seen(3, pos.w) ? p.w : 0.0f;
+            }
+            sum[k] = ffma2(make_float2(p.x, p.y), make_float2(v.x, v.y), sum[k]);
+            sum[k] = ffma2(make_float2(p.z, p.w), make_float2(v.z, v.w), sum[k]);
         }
-        sum = ffma2(make_float2(p.x, p.y), make_float2(v.x, v.y), sum);
-        sum = ffma2(make_float2(p.z, p.w), make_float2(v.z, v.w), sum);
     }
 }
 
@@ -592,29 +596,29 @@ __global__ void __launch_bounds__(FEW_THREADS, 1) kv_weigh_few_kernel(const Weig
                     break;
                 tc_fence_after();
                 const bool plain = rows % 4 == 0 && all_seen(g, u.plo, u.phi, tile * KEYS, KEYS);
-                float2 got = make_float2(0.0f, 0.0f);
-                auto add = [&](const float (&x)[8], int c) {
+                float2 got[1] = {make_float2(0.0f, 0.0f)};
+                auto add = [&](const float (&x)[1][8], int c) {
                     if (plain)
                         add_columns<false>(g, x, cols + q.i, c, rows, key, got);
                     else
                         add_columns<true>(g, x, cols + q.i, c, rows, key, got);
                 };
                 for (int c = 0; c < rows; c += both ? 8 : 16) {
-                    float x[8], y[8];   // 8 columns and their low parts, or the 8 after them
-                    tmem_ld8x2_wait(s_at + c, s_at + c + (both ? n : 8), x, y);
+                    float x[1][8], y[1][8];   // 8 columns and their low parts, or the 8 after them
+                    tmem_ld8x2_wait(s_at + c, s_at + c + (both ? n : 8), x[0], y[0]);
                     if (c + (both ? 8 : 16) >= rows)
                         release(bar(F_SEMPTY + group), lane);
                     if (both) {
 #pragma unroll
                         for (int j = 0; j < 8; ++j)
-                            x[j] += y[j];
+                            x[0][j] += y[0][j];
                     }
                     add(x, c);
                     if (!both)
                         add(y, c + 8);
                 }
                 if (page >= 0)
-                    out[page * page_floats] = (key < u.pos0 ? w.decay * old : 0.0f) + (got.x + got.y);
+                    out[page * page_floats] = (key < u.pos0 ? w.decay * old : 0.0f) + (got[0].x + got[0].y);
                 page = page1;
                 page1 = page2;
                 old = old1;
@@ -754,10 +758,10 @@ struct Many {
     static constexpr int K_BYTES = KB * KEYS * 128;        // of 128 keys
     static constexpr int STAGES = 2, CSTAGES = 4;          // operands, columns on their way or in use
     static constexpr int K = 0, Q = K + 2 * K_BYTES, COLS = Q + STAGES * Q_BYTES;
-    static constexpr int RED = COLS + CSTAGES * static_cast<int>(sizeof(Columns));   // f32 [2][KEYS]
-    static constexpr int BAR = RED + 2 * KEYS * 4;
+    static constexpr int RED = COLS + CSTAGES * static_cast<int>(sizeof(Columns));   // f32 [4][2 KEYS]
+    static constexpr int BAR = RED + 4 * 2 * KEYS * 4;
     enum { KFULL, KEMPTY, QFULL, QEMPTY = QFULL + STAGES, CFULL = QEMPTY + STAGES, CEMPTY = CFULL + CSTAGES,
-           SFULL = CEMPTY + CSTAGES, SEMPTY = SFULL + 4, DRAIN = SEMPTY + 4, NBAR };
+           SFULL = CEMPTY + CSTAGES, SEMPTY = SFULL + 2, DRAIN = SEMPTY + 2, NBAR };
     static constexpr int TMEM_AT = BAR + NBAR * 8, BYTES = TMEM_AT + 16 + 1024;
     static_assert(BYTES <= 227 * 1024 && Q % 1024 == 0 && COLS % 16 == 0 && BAR % 8 == 0, "shared memory");
 };
@@ -828,9 +832,9 @@ __global__ void __launch_bounds__(MANY_THREADS, 1) kv_weigh_many_kernel(const We
             mbar_init(bar(C::CFULL + i), 1);
             mbar_init(bar(C::CEMPTY + i), 8);
         }
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < 2; ++i) {
             mbar_init(bar(C::SFULL + i), 1);
-            mbar_init(bar(C::SEMPTY + i), 4);
+            mbar_init(bar(C::SEMPTY + i), 8);
         }
         mbar_init(bar(C::DRAIN), 1);
         fence_barrier_init();
@@ -870,19 +874,17 @@ __global__ void __launch_bounds__(MANY_THREADS, 1) kv_weigh_many_kernel(const We
                 const int stage = step % C::STAGES;
                 const int n = min(MOST_ROWS, u.rows - tile * MOST_ROWS);
                 const uint32_t idesc = idesc_f16_f32(KEYS, (n + 15) / 16 * 16);
-                ok = warp_wait(w, bar(C::QFULL + stage), step / C::STAGES & 1);
-                for (int k = 0; ok && k < 2; ++k) {
-                    const int s = 2 * k + step % 2;
-                    ok = warp_wait(w, bar(C::SEMPTY + s), (step / 2 & 1) ^ 1);
-                    if (!ok)
-                        break;
-                    tc_fence_after();
-                    product<D, C::PARTS>(lead, tmem + s * MOST_ROWS, sbase + C::K + k * C::K_BYTES,
+                ok = warp_wait(w, bar(C::QFULL + stage), step / C::STAGES & 1) &&
+                     warp_wait(w, bar(C::SEMPTY + step % 2), (step / 2 & 1) ^ 1);
+                if (!ok)
+                    break;
+                tc_fence_after();
+#pragma unroll
+                for (int k = 0; k < 2; ++k)
+                    product<D, C::PARTS>(lead, tmem + (2 * (step % 2) + k) * MOST_ROWS, sbase + C::K + k * C::K_BYTES,
                                          sbase + C::Q + stage * C::Q_BYTES, C::BLOCK, idesc);
-                    umma_commit_by(lead, bar(C::SFULL + s));
-                }
-                if (ok)
-                    umma_commit_by(lead, bar(C::QEMPTY + stage));
+                umma_commit_by(lead, bar(C::SFULL + step % 2));
+                umma_commit_by(lead, bar(C::QEMPTY + stage));
             }
             if (ok)
                 umma_commit_by(lead, bar(C::KEMPTY));
@@ -951,60 +953,59 @@ __global__ void __launch_bounds__(MANY_THREADS, 1) kv_weigh_many_kernel(const We
             ++visit;
         }
     } else if (warp >= 8) {
-        const int s = warp / 4 - 2, k = s / 2, odd = s % 2, t = threadIdx.x % KEYS;   // half of the keys, parity of the steps
-        const uint32_t s_at = tmem + s * MOST_ROWS + (static_cast<uint32_t>(t & ~31) << 16);
-        float* red = reinterpret_cast<float*>(smem + C::RED) + k * KEYS + t;
+        // Of every other step a warpgroup takes half of the rows, with both halves of the keys: what it reads of
+        // a row then serves two keys of a thread.
+        const int s = warp / 4 - 2, part_of = s / 2, odd = s % 2, t = threadIdx.x % KEYS;
+        const uint32_t s_at = tmem + 2 * odd * MOST_ROWS + (static_cast<uint32_t>(t & ~31) << 16);
+        float* red = reinterpret_cast<float*>(smem + C::RED);   // [4][GROUP]
         for (int group = part; group < groups; group += w.parts) {
             int lo, hi;
             range(group, lo, hi);
-            const int k0 = group * GROUP + k * KEYS, key = k0 + t;
-            float2 sum = make_float2(0.0f, 0.0f);
+            const int k0 = group * GROUP;
+            float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
             for (int tile = lo; ok && tile < hi; ++tile, ++step) {
                 if (step % 2 != odd)
                     continue;
                 const int cstage = step % C::CSTAGES;
                 const Columns* cols = reinterpret_cast<const Columns*>(smem + C::COLS) + cstage;
                 const int row0 = tile * MOST_ROWS, n = min(MOST_ROWS, u.rows - row0);
-                ok = warp_wait(w, bar(C::CFULL + cstage), step / C::CSTAGES & 1) && warp_wait(w, bar(C::SFULL + s), step / 2 & 1);
+                const int c0 = part_of * (MOST_ROWS / 2), c1 = min(n, c0 + MOST_ROWS / 2);
+                ok = warp_wait(w, bar(C::CFULL + cstage), step / C::CSTAGES & 1) && warp_wait(w, bar(C::SFULL + odd), step / 2 & 1);
                 if (!ok)
                     break;
                 tc_fence_after();
-                const bool plain = n % 4 == 0 && all_seen(g, u.pos0 + row0 / g.group, u.pos0 + (row0 + n - 1) / g.group, k0, KEYS);
-                for (int c = 0; c < n; c += 16) {
-                    float x[16];
-                    tmem_ld16_wait(s_at + c, x);
-                    if (c + 16 >= n) {
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0)
-                            mbar_arrive(bar(C::SEMPTY + s));
-                    }
+                const bool plain = n % 4 == 0 && all_seen(g, u.pos0 + row0 / g.group, u.pos0 + (row0 + n - 1) / g.group, k0, GROUP);
+                for (int c = c0; c < c1; c += 16) {
+                    float x[2][16];
+                    tmem_ld16x2_wait(s_at + c, s_at + MOST_ROWS + c, x[0], x[1]);
                     if (plain)
-                        add_columns<false>(g, x, cols, c, n, key, sum);
+                        add_columns<false>(g, x, cols, c, c1, k0 + t, sum);
                     else
-                        add_columns<true>(g, x, cols, c, n, key, sum);
+                        add_columns<true>(g, x, cols, c, c1, k0 + t, sum);
                 }
-                __syncwarp();
+                release(bar(C::SEMPTY + odd), lane);
                 if (lane == 0)
                     mbar_arrive(bar(C::CEMPTY + cstage));
             }
-            // the sums of odd steps to those of even ones
-            if (odd)
-                *red = sum.x + sum.y;
-            ok = named_bar_and(2 + k, 256, ok);
+            // the four warpgroups' sums, two of them a half of the keys each
+            red[s * GROUP + t] = sum[0].x + sum[0].y;
+            red[s * GROUP + KEYS + t] = sum[1].x + sum[1].y;
+            ok = named_bar_and(2, 512, ok);
             if (!ok)
                 break;
-            if (!odd && key < u.length) {
+            const int j = s * KEYS + t, key = k0 + j;
+            if (s < 2 && key < u.length) {
                 const int page = u.table[key / KV_PAGE];
                 if (page >= 0 && page < g.c.num_pages) {
                     const size_t at = (static_cast<size_t>(page) * g.c.kv_heads + u.head) * KV_PAGE + key % KV_PAGE;
-                    w.out[at] = (key < u.pos0 ? w.decay * w.in[at] : 0.0f) + ((sum.x + sum.y) + *red);
+                    const float got = (red[j] + red[GROUP + j]) + (red[2 * GROUP + j] + red[3 * GROUP + j]);
+                    w.out[at] = (key < u.pos0 ? w.decay * w.in[at] : 0.0f) + got;
                 } else {
                     *g.c.bad = 1u;
                 }
             }
             if (group + w.parts < groups)
-                named_bar_sync(2 + k, 256);   // both have what they need of this group's
+                named_bar_sync(2, 512);   // what the next group overwrites is read
         }
     }
     tc_fence_before();
