@@ -179,6 +179,8 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prompt_kernel(const AttendArgs 
     auto bar = [&](int i) -> uint32_t { return sbase + C::BAR + 8u * static_cast<uint32_t>(i); };
 
     grid_dep_wait();
+    if (g.stats && g.nsplit == 1)
+        grid_dep_launch();   // the weights' rows are laid out beside the last CTAs
     if (blockIdx.x == gridDim.x - 1) {
         if constexpr (HL)
             clear_others_apart<D, T>(g);

@@ -17,6 +17,7 @@
 // kv_weigh_many_kernel: 256 keys stay in shared memory and the rows stream by, 128 a step, as
 // operands that kv_weigh_rows_kernel has laid out in the workspace.  Four warpgroups, one for each
 // half of the keys and every other step.
+#include <cfloat>
 #include <type_traits>
 
 #include "kv.cuh"
@@ -137,11 +138,9 @@ struct KeyCodes {
 };
 
 // One row, four values a lane, as operand row r of [64-value block][n rows] tiles, by a warp, an
-// f32 row's low part as row r + low; what its column needs.  A row whose statistics are {0, 0} is
-// given as zeros.
+// f32 row's low part as row r + low; the coefficient that makes its products powers of two.
 template <int D, typename T>
-__device__ __forceinline__ void put_row(const AttendArgs& g, float4 x, float2 stats, int pos, uint8_t* dst, int n, int r,
-                                        int low, Columns* cols, int lane)
+__device__ __forceinline__ float put_row(const AttendArgs& g, float4 x, uint8_t* dst, int n, int r, int low, int lane)
 {
     float a = fmaxf(fmaxf(fabsf(x.x), fabsf(x.y)), fmaxf(fabsf(x.z), fabsf(x.w)));
 #pragma unroll
@@ -159,12 +158,7 @@ __device__ __forceinline__ void put_row(const AttendArgs& g, float4 x, float2 st
         if constexpr (sizeof(T) == 4)
             *reinterpret_cast<uint2*>(at + low * 128) = lo;   // a multiple of 8 rows: the same turn
     }
-    if (lane == 0) {
-        cols->coef[r] = fminf(fmaxf(g.scale_log2 * kv_pow2(e), 1e-38f), 1e38f);
-        cols->ref[r] = stats.x;
-        cols->inv[r] = stats.y;
-        cols->pos[r] = pos;
-    }
+    return fminf(fmaxf(g.scale_log2 * kv_pow2(e), 1e-38f), 1e38f);
 }
 
 // The rows of a unit, warp `warp` of `warps` taking every warps-th, four loads on their way at once.
@@ -194,9 +188,15 @@ __device__ __forceinline__ void put_rows(const AttendArgs& g, const Unit& u, int
             const int r = r0 + i * warps;
             if (r >= n)
                 break;
-            const bool there = stats[i].y > 0.0f && lane < D / 4;
-            put_row<D, T>(g, there ? x[i].get() : make_float4(0.0f, 0.0f, 0.0f, 0.0f), stats[i],
-                          r < rows ? u.pos0 + r / g.group : -1, dst, (sizeof(T) == 4 ? 2 : 1) * n, r, n, cols, lane);
+            const bool there = stats[i].y > 0.0f && lane < D / 4;   // a row without weights is given as zeros
+            const float coef = put_row<D, T>(g, there ? x[i].get() : make_float4(0.0f, 0.0f, 0.0f, 0.0f), dst,
+                                             (sizeof(T) == 4 ? 2 : 1) * n, r, n, lane);
+            if (lane == 0) {
+                cols->coef[r] = coef;
+                cols->ref[r] = stats[i].x;
+                cols->inv[r] = stats[i].y;
+                cols->pos[r] = r < rows ? u.pos0 + r / g.group : -1;
+            }
         }
     }
 }
@@ -754,7 +754,7 @@ struct Many {
     static constexpr int PARTS = sizeof(T) == 4 ? 2 : 1, KB = D / 64;
     static constexpr int BLOCK = MOST_ROWS * 128;
     static constexpr int Q_BYTES = PARTS * KB * BLOCK;
-    static constexpr int RECORD = Q_BYTES + static_cast<int>(sizeof(Columns));
+    static constexpr int RECORD = Q_BYTES + MOST_ROWS * 4;   // operands, coefficients
     static constexpr int K_BYTES = KB * KEYS * 128;        // of 128 keys
     static constexpr int STAGES = 2, CSTAGES = 4;          // operands, columns on their way or in use
     static constexpr int K = 0, Q = K + 2 * K_BYTES, COLS = Q + STAGES * Q_BYTES;
@@ -772,28 +772,39 @@ __device__ __forceinline__ long long first_tile(const AttendArgs& g, int start, 
     return static_cast<long long>(start) * g.group / MOST_ROWS + b;
 }
 
+// The operands do not need the attention's results, so this kernel runs beside its last CTAs; one CTA
+// waits for them, so that it ends after the attention and the kernel behind it need wait for this one
+// alone.  (The attention's CTAs let it begin when they have waited themselves: what an earlier call reads
+// of the workspace is then read.)
 template <int D, typename T>
-__global__ void __launch_bounds__(256) kv_weigh_rows_kernel(const WeighArgs w)
+__global__ void __launch_bounds__(256, 8) kv_weigh_rows_kernel(const WeighArgs w)
 {
     using C = Many<D, T>;
     const AttendArgs& g = w.a;
     const int lane = threadIdx.x % 32, r = blockIdx.x;
-    grid_dep_wait();
     grid_dep_launch();
+    if (r == g.ntok) {
+        grid_dep_wait();
+        return;
+    }
     const int b = kv_sequence_of(g.c.start, g.c.batch, r, lane);
     const int first = g.c.start[b], last = g.c.start[b + 1];
     if (r < first || r >= last || first < 0 || last > g.ntok)
         return;
-    const int pos = max(g.c.length[b], 0) - last + r;
     for (int h = threadIdx.x / 32; h < g.heads; h += 8) {
         const int row = (r - first) * g.group + h % g.group;
         uint8_t* record = w.operands +
                           (h / g.group * w.tiles + first_tile(g, first, b) + row / MOST_ROWS) * static_cast<long long>(C::RECORD);
-        const float2 stats = g.stats[static_cast<size_t>(r) * g.heads + h];
         float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        if (stats.y > 0.0f && lane < D / 4)
+        if (lane < D / 4)
             x = load4(static_cast<const T*>(g.q.data) + r * g.q.tok + h * g.q.head + 4 * lane, g.wide);
-        put_row<D, T>(g, x, stats, pos, record, MOST_ROWS, row % MOST_ROWS, C::KB * MOST_ROWS, reinterpret_cast<Columns*>(record + C::Q_BYTES), lane);
+        // a row that is not finite has no weights
+        const bool finite = fabsf(x.x) <= FLT_MAX && fabsf(x.y) <= FLT_MAX && fabsf(x.z) <= FLT_MAX && fabsf(x.w) <= FLT_MAX;
+        if (!__all_sync(0xffffffffu, finite))
+            x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        const float coef = put_row<D, T>(g, x, record, MOST_ROWS, row % MOST_ROWS, C::KB * MOST_ROWS, lane);
+        if (lane == 0)
+            reinterpret_cast<float*>(record + C::Q_BYTES)[row % MOST_ROWS] = coef;
     }
 }
 
@@ -862,6 +873,7 @@ __global__ void __launch_bounds__(MANY_THREADS, 1) kv_weigh_many_kernel(const We
     };
     bool ok = true;
     int step = 0, visit = 0;    // steps, and groups with any, so far
+    const uint8_t* records = w.operands + (static_cast<long long>(u.head) * w.tiles + first_tile(g, u.first, u.b)) * C::RECORD;
     if (warp == 0) {
         const uint32_t lead = elect_one();
         for (int group = part; ok && group < groups; group += w.parts) {
@@ -895,35 +907,61 @@ __global__ void __launch_bounds__(MANY_THREADS, 1) kv_weigh_many_kernel(const We
             mbar_drain_wait(bar(C::DRAIN), 0, WAIT_LIMIT_NS, g.wc.err);
         __syncwarp();
     } else if (warp == 1) {
-        const uint8_t* records = w.operands + (static_cast<long long>(u.head) * w.tiles + first_tile(g, u.first, u.b)) * C::RECORD;
         for (int group = part; ok && group < groups; group += w.parts) {
             int lo, hi;
             range(group, lo, hi);
             for (int tile = lo; tile < hi; ++tile, ++step) {
-                const int stage = step % C::STAGES, cstage = step % C::CSTAGES;
-                ok = warp_wait(w, bar(C::QEMPTY + stage), (step / C::STAGES & 1) ^ 1) &&
-                     warp_wait(w, bar(C::CEMPTY + cstage), (step / C::CSTAGES & 1) ^ 1);
+                const int stage = step % C::STAGES;
+                ok = warp_wait(w, bar(C::QEMPTY + stage), (step / C::STAGES & 1) ^ 1);
                 if (!ok)
                     break;
                 if (lane == 0) {
                     const uint8_t* src = records + static_cast<long long>(tile) * C::RECORD;
-                    fence_proxy_async_smem();   // the columns were read with ordinary loads
                     mbar_arrive_expect_tx(bar(C::QFULL + stage), C::Q_BYTES);
 #pragma unroll
                     for (int i = 0; i < C::Q_BYTES; i += C::BLOCK)
                         bulk_g2s(sbase + C::Q + stage * C::Q_BYTES + i, src + i, C::BLOCK, bar(C::QFULL + stage));
-                    mbar_arrive_expect_tx(bar(C::CFULL + cstage), sizeof(Columns));
-                    bulk_g2s(sbase + C::COLS + cstage * sizeof(Columns), src + C::Q_BYTES, sizeof(Columns), bar(C::CFULL + cstage));
                 }
             }
         }
         if (lane == 0) {   // the last fill of each stage lands before the CTA ends
             for (int i = max(0, step - C::STAGES); i < step; ++i)
                 mbar_drain_wait(bar(C::QFULL + i % C::STAGES), i / C::STAGES & 1, WAIT_LIMIT_NS, g.wc.err);
-            for (int i = max(0, step - C::CSTAGES); i < step; ++i)
-                mbar_drain_wait(bar(C::CFULL + i % C::CSTAGES), i / C::CSTAGES & 1, WAIT_LIMIT_NS, g.wc.err);
         }
         __syncwarp();
+    } else if (warp == 2) {
+        // four rows a lane, on their way while the place is not free
+        for (int group = part; ok && group < groups; group += w.parts) {
+            int lo, hi;
+            range(group, lo, hi);
+            for (int tile = lo; tile < hi; ++tile, ++step) {
+                const int cstage = step % C::CSTAGES;
+                const float4 coef = *reinterpret_cast<const float4*>(records + static_cast<long long>(tile) * C::RECORD + C::Q_BYTES + 16 * lane);
+                float f[4] = {coef.x, coef.y, coef.z, coef.w};
+                float2 stats[4];
+                int pos[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int row = tile * MOST_ROWS + 4 * lane + i, token = row / g.group;
+                    const bool there = row < u.rows;
+                    pos[i] = there ? u.pos0 + token : -1;
+                    stats[i] = there ? g.stats[(u.first + token) * static_cast<size_t>(g.heads) + u.head * g.group + row % g.group]
+                                     : make_float2(0.0f, 0.0f);
+                    f[i] = stats[i].y > 0.0f ? f[i] : 0.0f;   // none: 2^0, times 0
+                }
+                ok = warp_wait(w, bar(C::CEMPTY + cstage), (step / C::CSTAGES & 1) ^ 1);
+                if (!ok)
+                    break;
+                Columns* cols = reinterpret_cast<Columns*>(smem + C::COLS) + cstage;
+                *reinterpret_cast<float4*>(cols->coef + 4 * lane) = make_float4(f[0], f[1], f[2], f[3]);
+                *reinterpret_cast<float4*>(cols->ref + 4 * lane) = make_float4(stats[0].x, stats[1].x, stats[2].x, stats[3].x);
+                *reinterpret_cast<float4*>(cols->inv + 4 * lane) = make_float4(stats[0].y, stats[1].y, stats[2].y, stats[3].y);
+                *reinterpret_cast<int4*>(cols->pos + 4 * lane) = make_int4(pos[0], pos[1], pos[2], pos[3]);
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(bar(C::CFULL + cstage));
+            }
+        }
     } else if (warp >= 4 && warp < 8) {
         const int t = threadIdx.x - 128;
         for (int group = part; ok && group < groups; group += w.parts) {
@@ -1175,7 +1213,8 @@ cudaError_t launch_weigh(WeighArgs a, long long keys, cudaStream_t s)
     if (e != cudaSuccess)
         return e;
     count_launch();
-    if ((e = launch_dependent(kv_weigh_rows_kernel<D, T>, dim3(static_cast<unsigned int>(a.a.ntok)), dim3(256), s, a)) != cudaSuccess)
+    if ((e = launch_dependent(kv_weigh_rows_kernel<D, T>, dim3(static_cast<unsigned int>(a.a.ntok) + 1), dim3(256), s, a)) !=
+        cudaSuccess)
         return e;
     const long long groups = (keys + 2 * KEYS - 1) / (2 * KEYS);
     a.parts = parts(groups, groups);
@@ -1191,7 +1230,7 @@ size_t weigh_bytes(int dtype, int heads, int kv_heads, int dim, int batch, int n
     const long long group = heads / kv_heads, rows = (max_q < ntok ? max_q : ntok) * group;
     *cols = static_cast<int>(rows < 16 ? 16 : rows > MOST_ROWS ? MOST_ROWS : (rows + 15) / 16 * 16);
     *tiles = rows <= MOST_ROWS ? 0 : static_cast<long long>(ntok) * group / MOST_ROWS + batch + 1;
-    const size_t record = static_cast<size_t>(dtype == KV_F32 ? 2 : 1) * MOST_ROWS * dim * 2 + sizeof(Columns);
+    const size_t record = static_cast<size_t>(dtype == KV_F32 ? 2 : 1) * MOST_ROWS * dim * 2 + MOST_ROWS * 4;
     return static_cast<size_t>(*tiles) * kv_heads * record;
 }
 
