@@ -75,16 +75,14 @@ struct RopeArgs {
     int toks;                 // tokens of a CTA
     int chunks, copies;       // threads of a row that turn pairs, and that copy what stays
     bool wide;
+    int ctas() const { return (ntok + toks - 1) / toks; }
 };
 
 template <typename T, bool INTERLEAVED>
-__global__ void __launch_bounds__(THREADS, 5) rope_kernel(const RopeArgs g)
+__device__ __forceinline__ void rope_rows(const RopeArgs& g, int cta, float2* table)
 {
     constexpr int V = Pairs<T>::V;
-    __shared__ __align__(16) float2 table[TABLE];
-    const int half = g.r.rot / 2, first = blockIdx.x * g.toks, toks = min(g.toks, g.ntok - first);
-    grid_dep_wait();
-    grid_dep_launch();
+    const int half = g.r.rot / 2, first = cta * g.toks, toks = min(g.toks, g.ntok - first);
 
     // the thread's chunk, the same in all its rows: `row`, `row` + step, ... of the CTA's
     const int width = g.chunks + g.copies, step = THREADS / width, chunk = threadIdx.x % width;
@@ -160,10 +158,40 @@ __global__ void __launch_bounds__(THREADS, 5) rope_kernel(const RopeArgs g)
     }
 }
 
+template <typename T, bool INTERLEAVED>
+__global__ void __launch_bounds__(THREADS, 5) rope_kernel(const RopeArgs g)
+{
+    __shared__ __align__(16) float2 table[TABLE];
+    grid_dep_wait();
+    grid_dep_launch();
+    rope_rows<T, INTERLEAVED>(g, blockIdx.x, table);
+}
+
+template <typename T>
+RopeArgs rope_args(const KvRows& x, const KvRows& out, const int* pos, const RopeView& r, int heads, int dim, int ntok, bool wide)
+{
+    constexpr int V = Pairs<T>::V;
+    const int half = r.rot / 2;
+    RopeArgs a = {x, out, pos, r, heads, dim, ntok, 0, 1, (half + V - 1) / V, 0, wide && half % V == 0 && dim % V == 0};
+    if (x.data != out.data || x.tok != out.tok || x.head != out.head)   // in place nothing is copied
+        a.copies = (dim - r.rot + 2 * V - 1) / (2 * V);
+    a.heads_inv = static_cast<unsigned int>(((1ull << 32) + heads - 1) / heads);
+    // tokens of a CTA: up to four rows a thread while the chip stays full, one at least
+    const int step = THREADS / (a.chunks + a.copies);
+    for (int rows = 4; rows >= 1; rows /= 2) {
+        a.toks = rows * step / heads;
+        a.toks = a.toks < TABLE / half ? a.toks : TABLE / half;
+        a.toks = a.toks < 1 ? 1 : a.toks;
+        if (a.ctas() >= 152 * 6)
+            break;
+    }
+    return a;
+}
+
 // ------------------------------------------------------------------ into the cache
-// A lane has 8 values of a row, D / 8 lanes a row, 2 rows of 128 values (4 of 64) a warp at once.  A
-// token's keys and values come first, then its queries; one pass's rows are loaded while the last
-// one's are turned.
+// The first CTAs have keys and values, the others queries, which are rows as above.  A lane has 8
+// values of a key or value, D / 8 lanes a row, 2 rows of 128 values (4 of 64) a warp at once; one pass's
+// rows are loaded while the last one's are turned.
 constexpr int WARPS = THREADS / 32;
 
 // Where a value's partner is.  HALVES: a lane has four values of one half of what turns and the four
@@ -174,12 +202,11 @@ enum RopePairs { HALVES = 0, INSIDE = 1, ANYWHERE = 2 };
 
 struct EnterArgs {
     KvView c;
-    KvRows q, q_out, k, v;
-    const int* pos;
-    RopeView r;
-    int heads, ntok;
-    int toks;              // tokens of a CTA: 1, 2, 4 or 8
-    bool wide_q, wide_kv;
+    KvRows k, v;
+    RopeArgs q;            // and positions, the plan and the number of tokens
+    int toks;              // tokens of a CTA of keys and values: 1, 2, 4 or 8
+    int ctas;              // of keys and values: the longer ones, and the first
+    bool wide;             // keys and values
 };
 
 // The two fours of values of lane l: from first and from second on (8 consecutive ones in the other
@@ -285,32 +312,34 @@ __global__ void __launch_bounds__(THREADS, 4) kv_write_rope_kernel(const EnterAr
 {
     using P = Piece<D>;
     constexpr int LANES = D / 8, AT_ONCE = 32 / LANES;
-    __shared__ __align__(16) float2 table[WARPS * D / 2];
+    __shared__ __align__(16) float2 table[TABLE];
+    static_assert(WARPS * D / 2 <= TABLE, "table");
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
-    const int half = g.r.rot / 2, first = blockIdx.x * g.toks, toks = min(g.toks, g.ntok - first);
     grid_dep_wait();
     grid_dep_launch();
+    if (static_cast<int>(blockIdx.x) >= g.ctas)
+        return rope_rows<T, PAIRS == INSIDE>(g.q, blockIdx.x - g.ctas, table);
+    const RopeView& r = g.q.r;
+    const int half = r.rot / 2, first = blockIdx.x * g.toks, toks = min(g.toks, g.q.ntok - first);
 
     const int warps = WARPS / g.toks;                    // of a token
     const int tok = min(warp / warps, toks - 1);         // a last CTA's spare warps compute and store nothing
     const bool spare = warp / warps >= toks;
     const int t = first + tok, hk = g.c.kv_heads;
     const int l = lane % LANES, sub = warp % warps * AT_ONCE + lane / LANES, step = warps * AT_ONCE;
-    const Fours mine = fours_of<PAIRS>(l, D, g.r.rot), plain = {8 * l, 8 * l + 4, false, 0};
-    // passes over the rows: keys, values, queries
-    const int each = (hk + step - 1) / step, passes = 2 * each + (g.heads + step - 1) / step;
+    const Fours mine = fours_of<PAIRS>(l, D, r.rot), plain = {8 * l, 8 * l + 4, false, 0};
+    // passes over the rows: keys, values
+    const int each = (hk + step - 1) / step, passes = 2 * each;
     auto row_of = [&](int pass) -> const T* {
-        const KvRows& in = pass < each ? g.k : pass < 2 * each ? g.v : g.q;
-        const int h = pass < each ? min(pass * step + sub, hk - 1)
-                      : pass < 2 * each ? min((pass - each) * step + sub, hk - 1)
-                                        : min((pass - 2 * each) * step + sub, g.heads - 1);
+        const KvRows& in = pass < each ? g.k : g.v;
+        const int h = min((pass < each ? pass : pass - each) * step + sub, hk - 1);
         return static_cast<const T*>(in.data) + t * in.tok + h * in.head;
     };
     const T* row = row_of(0);
     float ahead[8];
-    load_fours(row, mine, g.wide_kv, ahead);
+    load_fours(row, mine, g.wide, ahead);
     for (int i = threadIdx.x; i < toks * half; i += THREADS)
-        table[i] = rope_turn(g.r, i % half, g.pos[first + i / half]);
+        table[i] = rope_turn(r, i % half, g.q.pos[first + i / half]);
     int slot;
     const long long page = kv_page_of(g.c, t, static_cast<long long>(hk) * P::BYTES, lane, &slot);
     const float2* cs = table + tok * half;
@@ -324,13 +353,13 @@ __global__ void __launch_bounds__(THREADS, 4) kv_write_rope_kernel(const EnterAr
         const T* here = row;
         if (pass + 1 < passes) {
             row = row_of(pass + 1);
-            load_fours(row, pass + 1 >= each && pass + 1 < 2 * each ? plain : mine, pass + 1 < 2 * each ? g.wide_kv : g.wide_q, ahead);
+            load_fours(row, pass + 1 >= each ? plain : mine, g.wide, ahead);
         }
+        const int h = (pass < each ? pass : pass - each) * step + sub;
+        const bool store = h < hk && page >= 0 && !spare;
+        uint8_t* piece = g.c.pages + page + h * P::BYTES;
         if (pass < each) {
-            const int h = pass * step + sub;
-            const bool store = h < hk && page >= 0 && !spare;
-            uint8_t* piece = g.c.pages + page + h * P::BYTES;
-            turn8<PAIRS>(x, here, l, mine, g.r, cs);
+            turn8<PAIRS>(x, here, l, mine, r, cs);
             if constexpr (PAIRS == HALVES) {
                 put_key_fours<D>(x, mine, l, slot, piece, store);
             } else {
@@ -338,34 +367,46 @@ __global__ void __launch_bounds__(THREADS, 4) kv_write_rope_kernel(const EnterAr
                 if (store)
                     Place8<D>(slot, l, true).put(piece, codes, l, true);
             }
-        } else if (pass < 2 * each) {
-            const int h = (pass - each) * step + sub;
-            const Codes8 codes = kv_quantise8(x, false);
-            if (h < hk && page >= 0 && !spare)
-                Place8<D>(slot, l, false).put(g.c.pages + page + h * P::BYTES, codes, l, false);
         } else {
-            const int h = (pass - 2 * each) * step + sub;
-            turn8<PAIRS>(x, here, l, mine, g.r, cs);
-            __syncwarp();   // in place: every lane has what it needs of the row
-            if (h < g.heads && !spare) {
-                T* out = static_cast<T*>(g.q_out.data) + t * g.q_out.tok + h * g.q_out.head;
-                store4(out + mine.first, make_float4(x[0], x[1], x[2], x[3]), g.wide_q);
-                store4(out + mine.second, make_float4(x[4], x[5], x[6], x[7]), g.wide_q);
-            }
+            const Codes8 codes = kv_quantise8(x, false);
+            if (store)
+                Place8<D>(slot, l, false).put(piece, codes, l, false);
         }
     }
 }
 
 template <int D, typename T>
-cudaError_t launch_enter(const EnterArgs& a, cudaStream_t s)
+cudaError_t launch_enter(EnterArgs a, const KvRows& q, const KvRows& q_out, const int* pos, const RopeView& r, int heads, int ntok,
+                         bool wide_q, cudaStream_t s)
 {
-    const dim3 grid(static_cast<unsigned int>((a.ntok + a.toks - 1) / a.toks)), block(THREADS);
+    a.q = rope_args<T>(q, q_out, pos, r, heads, D, ntok, wide_q);
+    // More tokens a CTA fill its warps with few heads and share the wait for the first rows; fewer end
+    // together.  A CTA's time goes with its passes.  Measured, us, 1 / 2 / 4 / 8 tokens: 700 tokens of 8 kv
+    // heads 8.0 / 6.2 / 5.9 / 9.0 (f16, 128 values), of 32 10.6 / 13.0 / 14.9 / 26.3; 10000 tokens of 8
+    // 91.7 / 64.6 / 59.4 / 57.1, of 32 136 / 126 / 120 / 117, of one of 64 values 55.9 / 31.3 / 19.0 / 13.0.
+    for (a.toks = 8; a.toks > 1; a.toks /= 2) {
+        const int at_once = WARPS / a.toks * (256 / D);
+        if (3ll * ((ntok + a.toks - 1) / a.toks) >= 2ll * 152 * ((a.c.kv_heads + at_once - 1) / at_once))
+            break;
+    }
+    a.ctas = (ntok + a.toks - 1) / a.toks;
+    const dim3 grid(static_cast<unsigned int>(a.ctas + a.q.ctas())), block(THREADS);
     count_launch();
-    if (a.r.interleaved)
+    if (r.interleaved)
         return launch_dependent(kv_write_rope_kernel<D, T, INSIDE>, grid, block, s, a);
-    if (a.r.rot % 64 == 0 && (D - a.r.rot) % 64 == 0)
+    if (r.rot % 64 == 0 && (D - r.rot) % 64 == 0)
         return launch_dependent(kv_write_rope_kernel<D, T, HALVES>, grid, block, s, a);
     return launch_dependent(kv_write_rope_kernel<D, T, ANYWHERE>, grid, block, s, a);
+}
+
+template <typename T>
+cudaError_t launch_rows(const KvRows& x, const KvRows& out, const int* pos, const RopeView& r, int heads, int dim, int ntok,
+                        bool wide, cudaStream_t s)
+{
+    const RopeArgs a = rope_args<T>(x, out, pos, r, heads, dim, ntok, wide);
+    count_launch();
+    return launch_dependent(r.interleaved ? rope_kernel<T, true> : rope_kernel<T, false>, dim3(static_cast<unsigned int>(a.ctas())),
+                            dim3(THREADS), s, a);
 }
 
 }  // namespace
@@ -373,47 +414,26 @@ cudaError_t launch_enter(const EnterArgs& a, cudaStream_t s)
 cudaError_t launch_rope(const KvRows& x, const KvRows& out, const int* pos, const RopeView& r, int dtype, int heads,
                         int dim, int ntok, bool wide, cudaStream_t s)
 {
-    const int v = dtype == KV_F32 ? 4 : 8, half = r.rot / 2;
-    RopeArgs a = {x, out, pos, r, heads, dim, ntok, 0, 1, (half + v - 1) / v, 0, wide && half % v == 0 && dim % v == 0};
-    if (x.data != out.data || x.tok != out.tok || x.head != out.head)   // in place nothing is copied
-        a.copies = (dim - r.rot + 2 * v - 1) / (2 * v);
-    a.heads_inv = static_cast<unsigned int>(((1ull << 32) + heads - 1) / heads);
-    // tokens of a CTA: up to four rows a thread while the chip stays full, one at least
-    const int step = THREADS / (a.chunks + a.copies);
-    int toks = 1;
-    for (int rows = 4; rows >= 1; rows /= 2) {
-        toks = rows * step / heads;
-        toks = toks < TABLE / half ? toks : TABLE / half;
-        toks = toks < 1 ? 1 : toks;
-        if ((ntok + toks - 1) / toks >= 152 * 6)
-            break;
-    }
-    a.toks = toks;
-    const dim3 grid(static_cast<unsigned int>((ntok + toks - 1) / toks)), block(THREADS);
-    count_launch();
-    auto launch = [&](auto kernel) { return launch_dependent(kernel, grid, block, s, a); };
-    if (r.interleaved)
-        return dtype == KV_F32   ? launch(rope_kernel<float, true>)
-               : dtype == KV_F16 ? launch(rope_kernel<__half, true>)
-                                 : launch(rope_kernel<__nv_bfloat16, true>);
-    return dtype == KV_F32   ? launch(rope_kernel<float, false>)
-           : dtype == KV_F16 ? launch(rope_kernel<__half, false>)
-                             : launch(rope_kernel<__nv_bfloat16, false>);
+    const auto launch = dtype == KV_F32 ? launch_rows<float> : dtype == KV_F16 ? launch_rows<__half> : launch_rows<__nv_bfloat16>;
+    return launch(x, out, pos, r, heads, dim, ntok, wide, s);
 }
 
 cudaError_t launch_kv_write_rope(const KvView& c, int dim, int dtype, const KvRows& q, const KvRows& q_out, int heads,
                                  const KvRows& k, const KvRows& v, const int* pos, const RopeView& r, bool wide_q,
                                  bool wide_kv, int ntok, cudaStream_t s)
 {
-    EnterArgs a = {c, q, q_out, k, v, pos, r, heads, ntok, 1, wide_q, wide_kv};
-    a.toks = ntok >= 8 * 152 * 8 ? 8 : ntok >= 4 * 152 * 8 ? 4 : ntok >= 2 * 152 * 8 ? 2 : 1;
-    if (dim == 128)
-        return dtype == KV_F32   ? launch_enter<128, float>(a, s)
-               : dtype == KV_F16 ? launch_enter<128, __half>(a, s)
-                                 : launch_enter<128, __nv_bfloat16>(a, s);
-    return dtype == KV_F32   ? launch_enter<64, float>(a, s)
-           : dtype == KV_F16 ? launch_enter<64, __half>(a, s)
-                             : launch_enter<64, __nv_bfloat16>(a, s);
+    EnterArgs a = {};
+    a.c = c;
+    a.k = k;
+    a.v = v;
+    a.wide = wide_kv;
+    const auto launch = dim == 128 ? (dtype == KV_F32   ? launch_enter<128, float>
+                                      : dtype == KV_F16 ? launch_enter<128, __half>
+                                                        : launch_enter<128, __nv_bfloat16>)
+                                   : (dtype == KV_F32   ? launch_enter<64, float>
+                                      : dtype == KV_F16 ? launch_enter<64, __half>
+                                                        : launch_enter<64, __nv_bfloat16>);
+    return launch(a, q, q_out, pos, r, heads, ntok, wide_q, s);
 }
 
 }  // namespace mmq

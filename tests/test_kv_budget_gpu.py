@@ -199,6 +199,20 @@ def test_many_tokens_enter(rows, interleaved, rot):
     assert status() == 0 and torch.equal(b.pages, other) and torch.equal(out, mmq.rope(q, pos, plan))
 
 
+@pytest.mark.parametrize("rows", [205, 403, 811])
+@pytest.mark.parametrize("kv_heads,dim", [(1, 64), (3, 128)])
+def test_some_tokens_enter(rows, kv_heads, dim):
+    """Two, four and eight tokens a CTA, the last one not full, queries of other CTAs."""
+    plan = mmq.rope_plan(dim)
+    b = Batch([rows // 3, rows - rows // 3], [rows // 3 + 10, rows], kv_heads, dim, F16, fill=False)
+    other = b.pages.clone()
+    q, k, v = (rand(rows, h, dim, dtype=F16, seed=s) for s, h in ((1, 3), (2, kv_heads), (3, kv_heads)))
+    pos = torch.arange(rows, dtype=torch.int32, device=DEV)
+    out = mmq.kv_write_rope(q, k, v, pos, plan, *b.cache)
+    mmq.kv_write(mmq.rope(k.float(), pos, plan), v.float(), other, *b.cache[1:])
+    assert status() == 0 and torch.equal(b.pages, other) and torch.equal(out, mmq.rope(q, pos, plan))
+
+
 def test_rows_of_any_stride_enter_and_those_without_a_place_turn():
     plan = mmq.rope_plan(128)
     b = Batch([3, 70], [2, 70], 2, 128, max_pages=2, fill=False)         # the first row is before its sequence
