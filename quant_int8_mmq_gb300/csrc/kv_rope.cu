@@ -6,7 +6,11 @@
 // Both kernels move bytes; what they compute is little beside that as long as an angle, some
 // 90 instructions, is computed once for all heads of its token: a CTA fills a table of its
 // tokens' cosines and sines in shared memory while its first rows are on their way, and then
-// walks over the rows.
+// walks over the rows.  On GB300: 3314 tokens of 32 heads of 128, f32, 20 us, 5.4 TB/s (0.80 of a plain
+// copy's rate), 8191 of 16 heads of 80 of which 32 turn, f16, 8.8 us, 4.8 TB/s; 64 tokens 2.2 us, a
+// launch.  Into the cache 10000 tokens of 32 heads on 8 of 128: f32 73 us, 5.7 TB/s; f16 57 us, 3.7 TB/s,
+// bound by issue slots (the rotation and the codes of a key, its values' and the halves of words that
+// they are written in): queries alone take 31 us, keys and values 30, and 17 unturned.
 #include "kv_rows.cuh"
 #include "rope.cuh"
 
@@ -25,7 +29,8 @@ struct Pairs {
     alignas(16) T a[V];
     alignas(16) T b[V];
 };
-constexpr int BATCH = 2;          // rows of a thread on their way at once
+constexpr int BATCH = 2;          // rows of a thread on their way at once (8191 f16 rows of 16 heads of 80:
+                                  // 8.9 us, one 9.2, four 13.8)
 constexpr int TABLE = 2048;       // angles of a CTA's tokens, at most
 
 // a: na values from x on, b: nb values from x + apart on.  `wide`: all V or none, aligned to 16 bytes.
@@ -176,7 +181,8 @@ RopeArgs rope_args(const KvRows& x, const KvRows& out, const int* pos, const Rop
     if (x.data != out.data || x.tok != out.tok || x.head != out.head)   // in place nothing is copied
         a.copies = (dim - r.rot + 2 * V - 1) / (2 * V);
     a.heads_inv = static_cast<unsigned int>(((1ull << 32) + heads - 1) / heads);
-    // tokens of a CTA: up to four rows a thread while the chip stays full, one at least
+    // tokens of a CTA: up to four rows a thread while the chip stays full, one at least (8191 tokens of
+    // 16 heads of 80, f16, four rows 8.9 us, one 10.9; 64 tokens of 32 heads 2.2 with one)
     const int step = THREADS / (a.chunks + a.copies);
     for (int rows = 4; rows >= 1; rows /= 2) {
         a.toks = rows * step / heads;
@@ -394,6 +400,8 @@ cudaError_t launch_enter(EnterArgs a, const KvRows& q, const KvRows& q_out, cons
     count_launch();
     if (r.interleaved)
         return launch_dependent(kv_write_rope_kernel<D, T, INSIDE>, grid, block, s, a);
+    // the partners that come with a lane's own values, 62 us, and those read from memory, 103 (3 prompts of
+    // up to 3314 tokens, 32 heads on 8 of 128, f32, with the cache read back)
     if (r.rot % 64 == 0 && (D - r.rot) % 64 == 0)
         return launch_dependent(kv_write_rope_kernel<D, T, HALVES>, grid, block, s, a);
     return launch_dependent(kv_write_rope_kernel<D, T, ANYWHERE>, grid, block, s, a);

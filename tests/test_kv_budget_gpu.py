@@ -763,3 +763,10 @@ def test_lengths_that_are_no_lengths(dtype, new):
         status()
         assert torch.equal(w[second], alone[second]) and torch.equal(w[first], before[first])
         assert (out[:new] == 0).all()
+
+
+@pytest.mark.parametrize("length", [8191, 8192, 8193, 16385, 32769])
+def test_clusters_begin(length):
+    """One CTA and clusters of two, four and eight, whose last has hardly a token."""
+    b = Batch([1], [length], 1, 64, fill=False)
+    evict_and_check(b, weights_for(b), 4000, 3, 100, bytes_too=False)
