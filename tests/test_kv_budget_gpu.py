@@ -770,3 +770,15 @@ def test_clusters_begin(length):
     """One CTA and clusters of two, four and eight, whose last has hardly a token."""
     b = Batch([1], [length], 1, 64, fill=False)
     evict_and_check(b, weights_for(b), 4000, 3, 100, bytes_too=False)
+
+
+@pytest.mark.parametrize("budget", [1, 100, 400])
+def test_the_example_keeps_a_budget(budget):
+    """It runs; a budget that all of the prompt fits in changes nothing that the cache's own rounding does not."""
+    from examples import attention_block
+    args = ["--hidden", "512", "--heads", "4", "--kv-heads", "2", "--dim", "128", "--prompt", "300", "--steps", "3",
+            "--batch", "2"]
+    worst = attention_block.main(args + ["--budget", str(budget)])
+    assert math.isfinite(worst)
+    if budget == 400:
+        assert worst == pytest.approx(attention_block.main(args), abs=1e-5)
