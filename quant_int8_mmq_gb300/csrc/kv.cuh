@@ -281,11 +281,13 @@ struct AttendArgs {
     bool wide;
     float* part;           // nsplit > 1: [nsplit][ntok * heads][D] unnormalised sums
     float2* part_ml;       //             [nsplit][ntok * heads] {reference, sum}
+    // For kv_weigh.cu, by builds of the attention kernels of their own (WEIGH), so that the others stay as they
+    // are: as branches of theirs they cost single tokens 1 % and prompts 1.7 %.
     float2* stats;         // null, or [ntok * heads] {reference, 1 / sum}, {0, 0} of a row without keys
-    float* scores;         // kv_step.cu: null, or the scores of each key that a row looks at, -inf where it sees
+    float* scores;         // kv_step.cu, with stats: the scores of each key that a row looks at, -inf where it sees
                            // none: [sequence][kv head][score_pages][score_rows][64], in units of `coef`
     float* coef;           // with scores: [sequence][kv head][score_rows], what makes them powers of two
-    int score_pages, score_rows;
+    int score_pages, score_rows;   // 0: no scores
     WaitCtl wc;
 };
 // What kv_weigh.cu needs of a row to compute its weights again; a row whose sum is no positive
@@ -301,7 +303,7 @@ __device__ __forceinline__ float2 kv_row_stats(float ref, float sum)
 // the last's, those of a sequence whose rows lead outside the packed ones, and those past the
 // first `most` (new tokens times the group) of a sequence.  A block of its own keeps this off
 // the others' time: as a branch of theirs it cost 64 single tokens and short prompts 1.3 %.
-template <int D, typename T>
+template <int D, typename T, bool WEIGH>
 __device__ __forceinline__ void kv_clear_others(const AttendArgs& g, long long most)
 {
     const long long n = g.ntok;
@@ -317,7 +319,7 @@ __device__ __forceinline__ void kv_clear_others(const AttendArgs& g, long long m
                         g.part_ml[(split * n + i / g.group) * g.heads + head + i % g.group] = make_float2(-INFINITY, 0.0f);
                 continue;
             }
-            if (g.stats) {
+            if constexpr (WEIGH) {
                 for (long long i = lo + threadIdx.x; i < hi; i += blockDim.x)
                     g.stats[i / g.group * g.heads + head + i % g.group] = make_float2(0.0f, 0.0f);
             }

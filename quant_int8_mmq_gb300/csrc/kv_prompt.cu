@@ -158,13 +158,13 @@ __device__ __forceinline__ bool warp_wait(const AttendArgs& g, uint32_t bar, uin
 
 // For f32 rows a function of its own: inlined, more of the softmax was spilled (165 us for 161 on
 // the prompt of 3314 tokens).
-template <int D, typename T>
+template <int D, typename T, bool WEIGH>
 __device__ __noinline__ void clear_others_apart(const AttendArgs g)
 {
-    kv_clear_others<D, T>(g, 1ll << 60);
+    kv_clear_others<D, T, WEIGH>(g, 1ll << 60);
 }
 
-template <int D, typename T>
+template <int D, typename T, bool WEIGH>
 __global__ void __launch_bounds__(THREADS, 1) kv_prompt_kernel(const AttendArgs g)
 {
     constexpr bool HL = sizeof(T) == 4;
@@ -179,13 +179,13 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prompt_kernel(const AttendArgs 
     auto bar = [&](int i) -> uint32_t { return sbase + C::BAR + 8u * static_cast<uint32_t>(i); };
 
     grid_dep_wait();
-    if (g.stats && g.nsplit == 1)
+    if (WEIGH && g.nsplit == 1)
         grid_dep_launch();   // the weights' rows are laid out beside the last CTAs
     if (blockIdx.x == gridDim.x - 1) {
         if constexpr (HL)
-            clear_others_apart<D, T>(g);
+            clear_others_apart<D, T, WEIGH>(g);
         else
-            kv_clear_others<D, T>(g, 1ll << 60);   // the tiles take any number of new tokens
+            kv_clear_others<D, T, WEIGH>(g, 1ll << 60);   // the tiles take any number of new tokens
         return;
     }
     // ---------------------------------------------------------------- the unit
@@ -837,7 +837,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prompt_kernel(const AttendArgs 
             const long long out_at = result();
             if (g.nsplit > 1 && mine && h == 0)
                 g.part_ml[part_row()] = make_float2(ref, sum);
-            if (g.nsplit == 1 && g.stats && mine && h == 0)
+            if (WEIGH && g.nsplit == 1 && mine && h == 0)
                 g.stats[part_row()] = kv_row_stats(ref, sum);
             constexpr int COLS = C::COLS, ROW = C::STAGED, LPR = COLS / 4;
             uint8_t* stage = smem + C::Q + (warp - SOFT_WARP) * 32 * ROW;
@@ -895,12 +895,12 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prompt_kernel(const AttendArgs 
         tmem_dealloc(tmem, 512);
 }
 
-template <int D, typename T>
+template <int D, typename T, bool WEIGH>
 cudaError_t launch_prompt(const AttendArgs& a, cudaStream_t s)
 {
     using C = Cfg<D, sizeof(T) == 4>;
     static std::atomic<uint64_t> done{0};
-    cudaError_t e = kv_allow_smem(kv_prompt_kernel<D, T>, C::BYTES, &done);
+    cudaError_t e = kv_allow_smem(kv_prompt_kernel<D, T, WEIGH>, C::BYTES, &done);
     if (e != cudaSuccess)
         return e;
     // the register split draws on what the launch reserves: with fewer the softmax would
@@ -908,7 +908,7 @@ cudaError_t launch_prompt(const AttendArgs& a, cudaStream_t s)
     static std::atomic<int> regs{0};
     if (regs.load() == 0) {
         cudaFuncAttributes fa;
-        if ((e = cudaFuncGetAttributes(&fa, kv_prompt_kernel<D, T>)) != cudaSuccess)
+        if ((e = cudaFuncGetAttributes(&fa, kv_prompt_kernel<D, T, WEIGH>)) != cudaSuccess)
             return e;
         regs.store(fa.numRegs);
     }
@@ -917,7 +917,13 @@ cudaError_t launch_prompt(const AttendArgs& a, cudaStream_t s)
     const unsigned int grid =
         static_cast<unsigned int>(static_cast<long long>(a.nsplit) * a.c.kv_heads * a.row_tiles + 1);
     count_launch();
-    return launch_dependent_smem(kv_prompt_kernel<D, T>, dim3(grid), dim3(THREADS), C::BYTES, s, a);
+    return launch_dependent_smem(kv_prompt_kernel<D, T, WEIGH>, dim3(grid), dim3(THREADS), C::BYTES, s, a);
+}
+
+template <int D, typename T>
+cudaError_t launch_prompt(const AttendArgs& a, cudaStream_t s)
+{
+    return a.stats ? launch_prompt<D, T, true>(a, s) : launch_prompt<D, T, false>(a, s);
 }
 
 }  // namespace

@@ -88,9 +88,9 @@ __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// SCORES: the scores of the keys are left for kv_weigh.cu (a build of its own, so that the others
-// stay as they are): 48.5 us for 47.2 on 131071 keys, 32 heads on 8, f32.
-template <int D, typename T, int MODE, bool SCORES>
+// WEIGH: the scores of the keys, if there is room for them, and the rows' statistics are left for
+// kv_weigh.cu: 48.5 us for 47.2 on 131071 keys, 32 heads on 8, f32.
+template <int D, typename T, int MODE, bool WEIGH>
 __global__ void __launch_bounds__(WARPS * 32, MODE == WIDE ? 3 : D == 128 ? 4 : 6) kv_step_kernel(const AttendArgs g)
 {
     using P = Piece<D>;
@@ -106,7 +106,7 @@ __global__ void __launch_bounds__(WARPS * 32, MODE == WIDE ? 3 : D == 128 ? 4 : 
     const int rank = blockIdx.x % g.cluster;
     if (id == static_cast<int>(gridDim.x) / g.cluster - 1) {
         if (rank == 0)
-            kv_clear_others<D, T>(g, static_cast<long long>(g.row_tiles) * ROWS);
+            kv_clear_others<D, T, WEIGH>(g, static_cast<long long>(g.row_tiles) * ROWS);
         return;
     }
     const int split = id % g.nsplit;
@@ -233,7 +233,7 @@ __global__ void __launch_bounds__(WARPS * 32, MODE == WIDE ? 3 : D == 128 ? 4 : 
         if (lane == 0) {
             const float coef = fminf(fmaxf(g.scale_log2 * kv_pow2(e), 1e-38f), 1e38f);
             *reinterpret_cast<float*>(smem + S::COEF + 4 * r) = coef;
-            if (SCORES && r < nrow && row0 + r < g.score_rows)   // every part's CTAs write the same
+            if (WEIGH && r < nrow && row0 + r < g.score_rows)   // every part's CTAs write the same
                 g.coef[(static_cast<size_t>(b) * g.c.kv_heads + head) * g.score_rows + row0 + r] = coef;
         }
     }
@@ -373,7 +373,7 @@ __global__ void __launch_bounds__(WARPS * 32, MODE == WIDE ? 3 : D == 128 ? 4 : 
             }
         }
 
-        if constexpr (SCORES) {
+        if constexpr (WEIGH) {
             const int at = kbase / KV_PAGE;
             if (at < g.score_pages) {
                 float* to = g.scores +
@@ -596,7 +596,7 @@ __global__ void __launch_bounds__(WARPS * 32, MODE == WIDE ? 3 : D == 128 ? 4 : 
     const size_t at = static_cast<size_t>(split) * flat_rows + static_cast<size_t>(token) * g.heads + h;
     if (g.nsplit > 1 && l == 0)
         g.part_ml[at] = make_float2(top, total);
-    if (g.nsplit == 1 && g.stats && l == 0)
+    if (WEIGH && g.nsplit == 1 && l == 0)
         g.stats[at] = kv_row_stats(top, total);
     const float inv = total == 0.0f ? 0.0f : 1.0f / total;   // a row that sees no key is zero
 #pragma unroll
@@ -612,7 +612,7 @@ __global__ void __launch_bounds__(WARPS * 32, MODE == WIDE ? 3 : D == 128 ? 4 : 
 
 // Joins the nsplit sums of each row: a CTA per row, its warps taking the splits in turn.
 constexpr int JOIN_WARPS = 4;
-template <int D, typename T>
+template <int D, typename T, bool WEIGH>
 __global__ void __launch_bounds__(JOIN_WARPS * 32) kv_join_kernel(const AttendArgs g)
 {
     __shared__ float4 part[JOIN_WARPS][32];
@@ -669,7 +669,7 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) kv_join_kernel(const AttendAr
             v.w += p.w;
         }
     }
-    if (g.stats && threadIdx.x == 0)
+    if (WEIGH && threadIdx.x == 0)
         g.stats[flat] = kv_row_stats(top, total);
     const float inv = total == 0.0f ? 0.0f : 1.0f / total;
     v = make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv);
@@ -678,12 +678,12 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) kv_join_kernel(const AttendAr
            v, g.wide);
 }
 
-template <int D, typename T, int MODE, bool SCORES>
+template <int D, typename T, int MODE, bool WEIGH>
 cudaError_t launch_step(const AttendArgs& a, cudaStream_t s)
 {
     constexpr int BYTES = StepSmem<D, MODE>::BYTES;
     static std::atomic<uint64_t> done{0};
-    const cudaError_t e = kv_allow_smem(kv_step_kernel<D, T, MODE, SCORES>, BYTES, &done);
+    const cudaError_t e = kv_allow_smem(kv_step_kernel<D, T, MODE, WEIGH>, BYTES, &done);
     if (e != cudaSuccess)
         return e;
     cudaLaunchAttribute at[2];
@@ -702,12 +702,12 @@ cudaError_t launch_step(const AttendArgs& a, cudaStream_t s)
     cfg.attrs = at;
     cfg.numAttrs = a.cluster > 1 ? 2 : 1;
     count_launch();
-    return cudaLaunchKernelEx(&cfg, kv_step_kernel<D, T, MODE, SCORES>, a);
+    return cudaLaunchKernelEx(&cfg, kv_step_kernel<D, T, MODE, WEIGH>, a);
 }
 template <int D, typename T, int MODE>
 cudaError_t launch_step(const AttendArgs& a, cudaStream_t s)
 {
-    return a.scores ? launch_step<D, T, MODE, true>(a, s) : launch_step<D, T, MODE, false>(a, s);
+    return a.stats ? launch_step<D, T, MODE, true>(a, s) : launch_step<D, T, MODE, false>(a, s);
 }
 
 template <int D>
@@ -724,7 +724,7 @@ template <int D, typename T>
 cudaError_t launch_join(const AttendArgs& a, cudaStream_t s)
 {
     count_launch();
-    return launch_dependent(kv_join_kernel<D, T>, dim3(static_cast<unsigned int>(a.ntok) * a.heads),
+    return launch_dependent(a.stats ? kv_join_kernel<D, T, true> : kv_join_kernel<D, T, false>, dim3(static_cast<unsigned int>(a.ntok) * a.heads),
                             dim3(JOIN_WARPS * 32), s, a);
 }
 
