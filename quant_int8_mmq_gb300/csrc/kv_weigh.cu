@@ -41,7 +41,7 @@ constexpr int MOST_ROWS = 128;  // columns of a step
 
 // What a row's column needs, in shared memory and (many rows) in the workspace.
 struct alignas(16) Columns {
-    float coef[MOST_ROWS], ref[MOST_ROWS], inv[MOST_ROWS];
+    float coef[MOST_ROWS], minus[MOST_ROWS], inv[MOST_ROWS];   // minus the reference
     int pos[MOST_ROWS];
 };
 
@@ -204,7 +204,7 @@ __device__ __forceinline__ void put_rows(const AttendArgs& g, const Unit& u, int
                                              (sizeof(T) == 4 ? 2 : 1) * n, r, n, lane);
             if (lane == 0) {
                 cols->coef[r] = coef;
-                cols->ref[r] = stats[i].x;
+                cols->minus[r] = -stats[i].x;
                 cols->inv[r] = stats[i].y;
                 cols->pos[r] = r < rows ? u.pos0 + r / g.group : -1;
             }
@@ -238,23 +238,45 @@ __device__ __forceinline__ void release(uint32_t bar, int lane)
         mbar_arrive(bar);
 }
 
-// The weights of some columns, c0 on, of KS keys (key, key + KEYS, ...).
+// What four columns need.  Asked for before a load from tensor memory is waited for: behind the wait it
+// would be another latency.
+struct Four {
+    float4 coef, minus, inv;
+    __device__ __forceinline__ void load(const Columns* cols, int c)
+    {
+        coef = *reinterpret_cast<const float4*>(cols->coef + c);
+        minus = *reinterpret_cast<const float4*>(cols->minus + c);
+        inv = *reinterpret_cast<const float4*>(cols->inv + c);
+    }
+};
+template <int N>
+struct Constants {
+    Four four[N / 4];
+    __device__ __forceinline__ Constants(const Columns* cols, int c)
+    {
+#pragma unroll
+        for (int i = 0; i < N / 4; ++i)
+            four[i].load(cols, c + 4 * i);
+    }
+};
+
+// The weights of some columns, c0 on, of KS keys (key, key + KEYS, ...).  MASKED: those from n on and those
+// that do not see the key count nothing.
 template <bool MASKED, int N, int KS>
-__device__ __forceinline__ void add_columns(const AttendArgs& g, const float (&x)[KS][N], const Columns* cols, int c0, int n,
-                                            int key, float2 (&sum)[KS])
+__device__ __forceinline__ void add_columns(const AttendArgs& g, const float (&x)[KS][N], const Constants<N>& at, const Columns* cols,
+                                            int c0, int n, int key, float2 (&sum)[KS])
 {
 #pragma unroll
     for (int c = 0; c < N; c += 4) {
-        if (c0 + c >= n)
+        if (MASKED && c0 + c >= n)
             break;
-        const float4 f = *reinterpret_cast<const float4*>(cols->coef + c0 + c);
-        const float4 r = *reinterpret_cast<const float4*>(cols->ref + c0 + c);
-        const float4 v = *reinterpret_cast<const float4*>(cols->inv + c0 + c);
+        const float4 f = at.four[c / 4].coef, r = at.four[c / 4].minus, v = at.four[c / 4].inv;
         const int4 pos = MASKED ? *reinterpret_cast<const int4*>(cols->pos + c0 + c) : make_int4(0, 0, 0, 0);
 #pragma unroll
         for (int k = 0; k < KS; ++k) {
-            float4 p = make_float4(kv_ex2(fmaf(x[k][c], f.x, -r.x)), kv_ex2(fmaf(x[k][c + 1], f.y, -r.y)),
-                                   kv_ex2(fmaf(x[k][c + 2], f.z, -r.z)), kv_ex2(fmaf(x[k][c + 3], f.w, -r.w)));
+            const float2 a = ffma2(make_float2(x[k][c], x[k][c + 1]), make_float2(f.x, f.y), make_float2(r.x, r.y));
+            const float2 b = ffma2(make_float2(x[k][c + 2], x[k][c + 3]), make_float2(f.z, f.w), make_float2(r.z, r.w));
+            float4 p = make_float4(kv_ex2(a.x), kv_ex2(a.y), kv_ex2(b.x), kv_ex2(b.y));
             if constexpr (MASKED) {
                 const int j = key + k * KEYS;
                 auto seen = [&](int i, int at) {
@@ -606,15 +628,16 @@ __global__ void __launch_bounds__(FEW_THREADS, 1) kv_weigh_few_kernel(const Weig
                 if (!ok)
                     break;
                 tc_fence_after();
-                const bool plain = rows % 4 == 0 && all_seen(g, u.plo, u.phi, tile * KEYS, KEYS);
+                const bool plain = all_seen(g, u.plo, u.phi, tile * KEYS, KEYS);   // columns past the rows are zeros
                 float2 got[1] = {make_float2(0.0f, 0.0f)};
-                auto add = [&](const float (&x)[1][8], int c) {
+                auto add = [&](const float (&x)[1][8], const Constants<8>& at, int c) {
                     if (plain)
-                        add_columns<false>(g, x, cols + q.i, c, rows, key, got);
+                        add_columns<false>(g, x, at, cols + q.i, c, rows, key, got);
                     else
-                        add_columns<true>(g, x, cols + q.i, c, rows, key, got);
+                        add_columns<true>(g, x, at, cols + q.i, c, rows, key, got);
                 };
                 for (int c = 0; c < rows; c += both ? 8 : 16) {
+                    const Constants<8> at(cols + q.i, c);
                     float x[1][8], y[1][8];   // 8 columns and their low parts, or the 8 after them
                     tmem_ld8x2_wait(s_at + c, s_at + c + (both ? n : 8), x[0], y[0]);
                     if (c + (both ? 8 : 16) >= rows)
@@ -624,9 +647,9 @@ __global__ void __launch_bounds__(FEW_THREADS, 1) kv_weigh_few_kernel(const Weig
                         for (int j = 0; j < 8; ++j)
                             x[0][j] += y[0][j];
                     }
-                    add(x, c);
+                    add(x, at, c);
                     if (!both)
-                        add(y, c + 8);
+                        add(y, Constants<8>(cols + q.i, c + 8), c + 8);
                 }
                 if (page >= 0)
                     out[page * page_floats] = (key < u.pos0 ? w.decay * old : 0.0f) + (got[0].x + got[0].y);
@@ -971,7 +994,7 @@ __global__ void __launch_bounds__(MANY_THREADS, 1) kv_weigh_many_kernel(const We
                     break;
                 Columns* cols = reinterpret_cast<Columns*>(smem + C::COLS) + cstage;
                 *reinterpret_cast<float4*>(cols->coef + 4 * lane) = make_float4(f[0], f[1], f[2], f[3]);
-                *reinterpret_cast<float4*>(cols->ref + 4 * lane) = make_float4(stats[0].x, stats[1].x, stats[2].x, stats[3].x);
+                *reinterpret_cast<float4*>(cols->minus + 4 * lane) = make_float4(-stats[0].x, -stats[1].x, -stats[2].x, -stats[3].x);
                 *reinterpret_cast<float4*>(cols->inv + 4 * lane) = make_float4(stats[0].y, stats[1].y, stats[2].y, stats[3].y);
                 *reinterpret_cast<int4*>(cols->pos + 4 * lane) = make_int4(pos[0], pos[1], pos[2], pos[3]);
                 __syncwarp();
@@ -1029,14 +1052,15 @@ __global__ void __launch_bounds__(MANY_THREADS, 1) kv_weigh_many_kernel(const We
                 if (!ok)
                     break;
                 tc_fence_after();
-                const bool plain = n % 4 == 0 && all_seen(g, u.pos0 + row0 / g.group, u.pos0 + (row0 + n - 1) / g.group, k0, GROUP);
+                const bool plain = n % 16 == 0 && all_seen(g, u.pos0 + row0 / g.group, u.pos0 + (row0 + n - 1) / g.group, k0, GROUP);
                 for (int c = c0; c < c1; c += 16) {
                     float x[2][16];
                     tmem_ld16x2_wait(s_at + c, s_at + MOST_ROWS + c, x[0], x[1]);
+                    const Constants<16> at(cols, c);
                     if (plain)
-                        add_columns<false>(g, x, cols, c, c1, k0 + t, sum);
+                        add_columns<false>(g, x, at, cols, c, c1, k0 + t, sum);
                     else
-                        add_columns<true>(g, x, cols, c, c1, k0 + t, sum);
+                        add_columns<true>(g, x, at, cols, c, c1, k0 + t, sum);
                 }
                 release(bar(C::SEMPTY + odd), lane);
                 if (lane == 0)
