@@ -18,8 +18,9 @@
 // thread; nothing is decoded, the two tokens that share a word of value codes are put together from the
 // halves of theirs.  Bound by its gathers: three dependent loads (old place, page id, codes), of which two
 // are on their way while the page before is moved; and words of values are two tokens', so that one that
-// stays without its neighbour has twice its bytes read.  64 sequences of up to 8192 tokens to 4096, 8 heads of 128:
-// 145 us for both kernels, 0.59 of a plain copy's rate on the bytes that stay.
+// stays without its neighbour has twice its bytes read.  So as many warps as an SM has room for, at 32
+// registers (at 57, half of them, 147 us for 125).  64 sequences of up to 8192 tokens to 4096, 8 heads of 128:
+// 122 us for both kernels, 0.70 of a plain copy's rate on the bytes that stay.
 #include <type_traits>
 
 #include "kv.cuh"
@@ -27,7 +28,6 @@
 namespace mmq {
 namespace {
 
-constexpr int CHOOSE_WARPS = 16, CHOOSE = CHOOSE_WARPS * 32;
 constexpr int BINS = 256, ROUNDS = 4;
 
 // Unsigned numbers in the order of f32 ones; -0 as 0, no number below all others.
@@ -37,11 +37,14 @@ __device__ __forceinline__ uint32_t order_of(float w)
     return w != w ? 0u : u >> 31 ? ~u : u | 0x80000000u;
 }
 
-__global__ void __launch_bounds__(CHOOSE, 3) kv_choose_kernel(const EvictArgs g)
+template <int WARPS>
+__global__ void __launch_bounds__(WARPS * 32, 3) kv_choose_kernel(const EvictArgs g)
 {
+    constexpr int CHOOSE = WARPS * 32;
+    static_assert(WARPS >= KV_MAX_CLUSTER, "a warp fetches a CTA's bins");
     extern __shared__ __align__(16) uint32_t keys[];   // [g.held] of this CTA's tokens
     __shared__ __align__(16) uint32_t hist[ROUNDS][BINS];
-    __shared__ uint2 counts[CHOOSE_WARPS];             // tokens above T, and equal to it
+    __shared__ uint2 counts[WARPS];             // tokens above T, and equal to it
     __shared__ uint2 mine;                             // of the CTA
     __shared__ __align__(16) uint32_t all[KV_MAX_CLUSTER][BINS];
     __shared__ uint2 found[ROUNDS];                    // bin, tokens above it
@@ -192,7 +195,7 @@ __global__ void __launch_bounds__(CHOOSE, 3) kv_choose_kernel(const EvictArgs g)
     // each warp looks at a part of the tokens, eight a lane: the low bits tell which of them are above T
     // (or stay anyhow), the high ones which equal it
     constexpr int EACH = 8, STEP = 32 * EACH;
-    const int part = ((size + CHOOSE_WARPS - 1) / CHOOSE_WARPS + EACH - 1) / EACH * EACH;
+    const int part = ((size + WARPS - 1) / WARPS + EACH - 1) / EACH * EACH;
     const int j0 = min(warp * part, size), j1 = min(j0 + part, size);
     auto look = [&](int j) {
         uint32_t k[EACH];
@@ -239,7 +242,7 @@ __global__ void __launch_bounds__(CHOOSE, 3) kv_choose_kernel(const EvictArgs g)
         counts[warp] = sum;
     __syncthreads();
     uint2 before = make_uint2(0, 0);
-    for (int w = 0; w < CHOOSE_WARPS; ++w) {
+    for (int w = 0; w < WARPS; ++w) {
         if (w == warp)
             sum = before;
         before.x += counts[w].x;
@@ -285,7 +288,7 @@ __global__ void __launch_bounds__(CHOOSE, 3) kv_choose_kernel(const EvictArgs g)
 // A CTA takes every parts-th new page of one sequence's kv head.  A page's tokens are looked up
 // (kept, page table: two dependent loads, and the weight behind them) while the one before is moved.
 template <int D>
-__global__ void __launch_bounds__(2 * D) kv_move_kernel(const EvictArgs g)
+__global__ void __launch_bounds__(2 * D, 1024 / D) kv_move_kernel(const EvictArgs g)
 {
     using P = Piece<D>;
     struct Source {
@@ -409,8 +412,13 @@ cudaError_t launch_kv_evict(const EvictArgs& args, int dim, int max_kv, cudaStre
     constexpr int MOST = 48 * 1024;   // tokens in shared memory: what one CTA an SM has room for; others are read again
     const long long share = (most / KV_PAGE / a.cluster + 2) * KV_PAGE;
     a.held = static_cast<int>(share < MOST ? share : MOST);
-    static std::atomic<uint64_t> done{0};
-    cudaError_t e = kv_allow_smem(kv_choose_kernel, MOST * 4, &done);
+    // Few tokens a CTA, or more CTAs than the chip holds: 8 warps, else 16.  8 / 16 warps, us: 2000 tokens 8.5 /
+    // 9.8, 5000 12.6 / 12.4, 8000 15.3 / 13.7, 30000 by 8 CTAs 18.0 / 18.7, 131071 43.2 / 37.5; 64
+    // sequences of up to 8192 144.3 / 146.3.
+    const bool small = share <= 4096 + 2 * KV_PAGE || units > 2 * 152;
+    static std::atomic<uint64_t> done[2];
+    const auto choose = small ? kv_choose_kernel<8> : kv_choose_kernel<16>;
+    cudaError_t e = kv_allow_smem(choose, MOST * 4, &done[small]);
     if (e != cudaSuccess)
         return e;
     cudaLaunchAttribute at[2];
@@ -422,18 +430,18 @@ cudaError_t launch_kv_evict(const EvictArgs& args, int dim, int max_kv, cudaStre
     at[1].val.clusterDim.z = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned int>(units * a.cluster));
-    cfg.blockDim = dim3(CHOOSE);
+    cfg.blockDim = dim3(small ? 256 : 512);
     cfg.dynamicSmemBytes = static_cast<size_t>(a.held) * 4;
     cfg.stream = s;
     cfg.attrs = at;
     cfg.numAttrs = a.cluster > 1 ? 2 : 1;
     count_launch();
-    if ((e = cudaLaunchKernelEx(&cfg, kv_choose_kernel, a)) != cudaSuccess)
+    if ((e = cudaLaunchKernelEx(&cfg, choose, a)) != cudaSuccess)
         return e;
-    // The chip's CTAs, or more of 8 pages each for sequences of uneven length: 64 of 2000 to 8192 tokens
-    // 147 us, with the chip's alone 158, with a CTA for every page 182.
+    // The chip's CTAs, or more of 4 pages each for sequences of uneven length: 64 of 2000 to 8192 tokens
+    // 122 us, with 8 pages 125, with the chip's alone 129, with a CTA for every page 133.
     const long long pages = (a.keep + KV_PAGE - 1) / KV_PAGE, fill = 152 * (dim == 128 ? 8 : 16) / units;
-    const long long parts = fill > pages / 8 ? fill : pages / 8;
+    const long long parts = fill > pages / 4 ? fill : pages / 4;
     a.parts = static_cast<int>(parts < 1 ? 1 : parts < pages ? parts : pages);
     const dim3 grid(static_cast<unsigned int>(units * a.parts));
     count_launch();
