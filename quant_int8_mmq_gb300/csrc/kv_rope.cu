@@ -8,7 +8,7 @@
 // tokens' cosines and sines in shared memory while its first rows are on their way, and then
 // walks over the rows.  On GB300: 3314 tokens of 32 heads of 128, f32, 20 us, 5.4 TB/s (0.80 of a plain
 // copy's rate), 8191 of 16 heads of 80 of which 32 turn, f16, 8.8 us, 4.8 TB/s; 64 tokens 2.2 us, a
-// launch.  Into the cache 10000 tokens of 32 heads on 8 of 128: f32 73 us, 5.7 TB/s; f16 57 us, 3.7 TB/s,
+// launch.  Into the cache 10000 tokens of 32 heads on 8 of 128: f32 69 us, 6.1 TB/s; f16 54 us, 4.0 TB/s,
 // bound by issue slots (the rotation and the codes of a key, its values' and the halves of words that
 // they are written in): queries alone take 31 us, keys and values 30, and 17 unturned.
 #include "kv_rows.cuh"
@@ -29,8 +29,7 @@ struct Pairs {
     alignas(16) T a[V];
     alignas(16) T b[V];
 };
-constexpr int BATCH = 2;          // rows of a thread on their way at once (8191 f16 rows of 16 heads of 80:
-                                  // 8.9 us, one 9.2, four 13.8)
+constexpr int BATCH = 2;          // rows of a thread on their way at once
 constexpr int TABLE = 2048;       // angles of a CTA's tokens, at most
 
 // a: na values from x on, b: nb values from x + apart on.  `wide`: all V or none, aligned to 16 bytes.
@@ -163,6 +162,7 @@ __device__ __forceinline__ void rope_rows(const RopeArgs& g, int cta, float2* ta
     }
 }
 
+// Two rows a thread, five CTAs an SM: 8191 f16 rows of 16 heads of 80 8.8 us, one row 9.2, four 13.8 (spills).
 template <typename T, bool INTERLEAVED>
 __global__ void __launch_bounds__(THREADS, 5) rope_kernel(const RopeArgs g)
 {
@@ -313,8 +313,10 @@ __device__ __forceinline__ void put_key_fours(const float (&x)[8], const Fours& 
         *reinterpret_cast<__half*>(piece + P::k_scale(slot, group)) = __float2half_rn(odd ? s[1] : s[0]);   // exact
 }
 
+// Five CTAs an SM: 10000 f16 tokens of 32 heads on 8 54 us, with four 57, with six (28 bytes spilled) and one
+// row a thread 52, but 2500 of 8 on one of 64 values 7.4 for 6.5.
 template <int D, typename T, int PAIRS>
-__global__ void __launch_bounds__(THREADS, 4) kv_write_rope_kernel(const EnterArgs g)
+__global__ void __launch_bounds__(THREADS, 5) kv_write_rope_kernel(const EnterArgs g)
 {
     using P = Piece<D>;
     constexpr int LANES = D / 8, AT_ONCE = 32 / LANES;
@@ -389,7 +391,7 @@ cudaError_t launch_enter(EnterArgs a, const KvRows& q, const KvRows& q_out, cons
     // More tokens a CTA fill its warps with few heads and share the wait for the first rows; fewer end
     // together.  A CTA's time goes with its passes.  Measured, us, 1 / 2 / 4 / 8 tokens: 700 tokens of 8 kv
     // heads 8.0 / 6.2 / 5.9 / 9.0 (f16, 128 values), of 32 10.6 / 13.0 / 14.9 / 26.3; 10000 tokens of 8
-    // 91.7 / 64.6 / 59.4 / 57.1, of 32 136 / 126 / 120 / 117, of one of 64 values 55.9 / 31.3 / 19.0 / 13.0.
+    // 92 / 65 / 59 / 57, of 32 136 / 126 / 120 / 117, of one of 64 values 56 / 31 / 19 / 13 (four CTAs an SM).
     for (a.toks = 8; a.toks > 1; a.toks /= 2) {
         const int at_once = WARPS / a.toks * (256 / D);
         if (3ll * ((ntok + a.toks - 1) / a.toks) >= 2ll * 152 * ((a.c.kv_heads + at_once - 1) / at_once))
