@@ -235,7 +235,7 @@ WeighPlan weigh_plan(const mmq_kv_cache* c, const AttendPlan& attend, int dtype,
                                        &p.cols, &p.tiles);
     // A few rows' scores are kept, unless they are more than a gigabyte (a batch of long tables without a
     // max_kv); the keys are then read again.  Kept / read again, us, attention included: a token on 131071
-    // keys, 32 heads on 8, f32, 57 / 80; 64 sequences of 95 to 8192, bf16, 114 / 160.
+    // keys, 32 heads on 8, f32, 57 / 81; 64 sequences of 95 to 8192, bf16, 114 / 165.
     if (attend.kernel == 0) {
         const long long pages = (static_cast<long long>(max_kv < 1 ? 1 : max_kv) + mmq::KV_PAGE - 1) / mmq::KV_PAGE;
         p.score_pages = static_cast<int>(pages < c->max_pages ? pages : c->max_pages);

@@ -10,7 +10,7 @@
 //
 // kv_finish_weights_kernel (few rows: the step kernel ran).  The attention has left its scores, 4 bytes
 // a row and key, so that K is not read and widened again: for a token on 131071 keys, 32 heads on 8,
-// 57 us with the attention (47) for 80 with the next kernel; 64 sequences of up to 8192, 114 for 160.
+// 57 us with the attention (47) for 81 with the next kernel; 64 sequences of up to 8192, 114 for 165.
 // Where scores would take more than a gigabyte the next kernel runs.
 //
 // kv_weigh_few_kernel (up to 128 rows per sequence and kv head) and kv_weigh_many_kernel (more):
@@ -22,12 +22,12 @@
 // stay and the rows stream by.
 //
 // What bounds them: few rows a step's chain (widening 700 cycles, products, sums 1100), shared by
-// three warpgroups in turn; 32 f16 rows on 131072 keys, 8 kv heads, 80 us (0.95 TB/s of K).  Many rows
+// three warpgroups in turn; 32 f16 tokens on 131072 keys, 32 heads on 8, 74 us (1.0 TB/s of K).  Many rows
 // the sums: an exponential and two fma an element, and three reads of a column's constants for every four
-// elements of two keys.  2 x 2048 rows of 32 heads on 8 on 16384 keys 589 us beside 820 for the
-// attention: 875 TFLOP/s of the one product.  Without its exponentials the kernel took 13 % less,
-// without the constants' reads 20 %; those could go into the product (three more values of every row),
-// but an argument that is far from 0 costs weights three bits, and rows of a tile need one factor.
+// elements of two keys.  2 x 2048 tokens of 32 heads on 8 on 16384 keys 577 us beside 820 for the
+// attention: 890 TFLOP/s of the one product.  Without its exponentials an earlier form of the kernel took
+// 13 % less, without the constants' reads 20 %; those could go into the product (three more values of every
+// row), but an argument that is far from 0 costs weights three bits, and rows of a tile need one factor.
 #include <cfloat>
 #include <type_traits>
 
