@@ -1098,7 +1098,7 @@ __global__ void __launch_bounds__(MANY_THREADS, 1) kv_weigh_many_kernel(const We
 // The attention for few rows has left its scores, so that K is not read again: 4 bytes a row and key
 // for the 72 of a key.  Half a warp has a page, a lane four keys: 9 us for a token on 131071 keys, 32
 // heads on 8 (16.8 MB of scores and 8.4 of weights, from L2 for the most part; a warp a page, two keys a
-// lane, took 16), 22 us for 64 sequences of up to 8192 (40 MB).  Pages past the ones there was room for
+// lane, took 16), 22 us for 64 sequences of up to 8192 (50 MB).  Pages past the ones there was room for
 // (a max_kv that is too low) are computed here, value by value.
 constexpr int FINISH_WARPS = 4, FINISH_PAGES = 2 * FINISH_WARPS;   // of a CTA at once
 
