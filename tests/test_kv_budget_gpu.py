@@ -782,3 +782,27 @@ def test_the_example_keeps_a_budget(budget):
     assert math.isfinite(worst)
     if budget == 400:
         assert worst == pytest.approx(attention_block.main(args), abs=1e-5)
+
+
+@pytest.mark.parametrize("dtype", [F32, F16])
+@pytest.mark.parametrize("new,length,batch", [(1, 9000, 40), (40, 700, 4), (300, 900, 2)])
+def test_a_wait_that_runs_out_ends_every_kernel_of_the_call(dtype, new, length, batch):
+    """A fill that the attention's first CTA leaves out: the kernels behind it see the error and end, and the
+    next call is right."""
+    b = Batch([new] * batch, [length] * batch, 2, 128, dtype)
+    q, before = b.q(4), weights_for(b)
+    want = before.clone()
+    mmq.kv_attend_weights(q, want, *b.cache, new, length, decay=0.5)
+    torch.cuda.synchronize()
+    assert status() == 0
+    try:
+        mmq.mmq_debug_inject_wait_timeout(0, 1_000_000)
+        mmq.kv_attend_weights(q, before.clone(), *b.cache, new, length, decay=0.5)
+        assert status() == 5
+        assert status() == 0
+        got = before.clone()
+        mmq.kv_attend_weights(q, got, *b.cache, new, length, decay=0.5)
+        assert status() == 0
+    finally:
+        mmq.mmq_debug_inject_wait_timeout(-1)
+    assert torch.equal(got, want)
