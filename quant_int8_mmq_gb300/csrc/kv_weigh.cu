@@ -15,8 +15,8 @@
 //
 // kv_weigh_few_kernel (up to 128 rows per sequence and kv head) and kv_weigh_many_kernel (more):
 // S^T = K Q^T on the tensor cores.  Keys are the 128 lanes of tensor memory and rows its columns, so a
-// key's sum over the rows stays in one thread's registers and nothing is added up across CTAs; what a
-// column needs (coefficient, reference, 1 / sum) is read by whole warps at once.  K is widened to f16,
+// key's sum over the rows stays in a thread's registers (many rows: four threads') and nothing is added
+// up across CTAs; what a column needs (coefficient, reference, 1 / sum) is read by whole warps at once.  K is widened to f16,
 // exactly, from the codes; rows are scaled by a power of two and, where they are f32, split in two f16
 // parts.  With few rows these stay in shared memory and the keys stream by; with many, 256 keys
 // stay and the rows stream by.
