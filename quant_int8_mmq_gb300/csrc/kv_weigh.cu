@@ -812,21 +812,17 @@ __device__ __forceinline__ long long first_tile(const AttendArgs& g, int start, 
     return static_cast<long long>(start) * g.group / MOST_ROWS + b;
 }
 
-// The operands do not need the attention's results, so this kernel runs beside its last CTAs; one CTA
-// waits for them, so that it ends after the attention and the kernel behind it need wait for this one
-// alone.  (The attention's CTAs let it begin when they have waited themselves: what an earlier call reads
-// of the workspace is then read.)
+// A CTA a row.  It needs none of the attention's results, but what was written before the attention (q, start) is
+// visible to the CTAs that wait themselves, not to those that one of them waits for.  (With one that
+// waited, the others beside the attention's last CTAs, a prompt of 3314 tokens took 1.5 % less.)
 template <int D, typename T>
 __global__ void __launch_bounds__(256, 8) kv_weigh_rows_kernel(const WeighArgs w)
 {
     using C = Many<D, T>;
     const AttendArgs& g = w.a;
     const int lane = threadIdx.x % 32, r = blockIdx.x;
+    grid_dep_wait();
     grid_dep_launch();
-    if (r == g.ntok) {
-        grid_dep_wait();
-        return;
-    }
     const int b = kv_sequence_of(g.c.start, g.c.batch, r, lane);
     const int first = g.c.start[b], last = g.c.start[b + 1];
     if (r < first || r >= last || first < 0 || last > g.ntok)
@@ -1256,7 +1252,7 @@ cudaError_t launch_weigh(WeighArgs a, long long keys, cudaStream_t s)
     if (e != cudaSuccess)
         return e;
     count_launch();
-    if ((e = launch_dependent(kv_weigh_rows_kernel<D, T>, dim3(static_cast<unsigned int>(a.a.ntok) + 1), dim3(256), s, a)) !=
+    if ((e = launch_dependent(kv_weigh_rows_kernel<D, T>, dim3(static_cast<unsigned int>(a.a.ntok)), dim3(256), s, a)) !=
         cudaSuccess)
         return e;
     const long long groups = (keys + 2 * KEYS - 1) / (2 * KEYS);

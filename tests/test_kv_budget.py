@@ -262,3 +262,30 @@ def test_numbers_past_32_bits_are_not_cut(mmq_lib):
     for rot in (2 ** 32 + 64, 2 ** 40, -2 ** 40):
         with pytest.raises(mmq.MMQError):
             mmq.mmq_rope_frequencies("none", rot)
+
+
+def test_every_cta_waits_for_the_kernel_before_it(mmq_lib):
+    """Kernels of the cache start while the one ahead of them runs, and what that one wrote is only visible to a CTA
+    that has waited itself: the wait stands in no branch, and nothing that may have been written is touched before it."""
+    import glob
+    import os
+    import re
+    csrc = os.path.join(os.path.dirname(mmq.__file__), "csrc")
+    seen = []
+    for path in sorted(glob.glob(os.path.join(csrc, "kv_*.cu"))):
+        text = re.sub(r"//[^\n]*", "", open(path).read())
+        for found in re.finditer(r"__global__[^{;]*?(kv_\w+_kernel|rope_kernel)\(", text):
+            body = text[text.index("{", found.end()) + 1:]
+            depth, flat = 1, ""                                         # inner blocks as empty statements
+            for c in body:
+                depth += (c == "{") - (c == "}")
+                if depth == 0:
+                    break
+                flat += ";" if c == "}" else c if depth == 1 else ""
+            seen.append(found[1])
+            assert "grid_dep_wait();" in flat, (path, found[1])
+            before = flat[:flat.index("grid_dep_wait();")]
+            for memory in (r"c\.(start|length|table|pages)\[", r"\bstats\[", r"kv_sequence_of", r"unit_of", r"\.data\)"):
+                assert not re.search(memory, before), (path, found[1], memory)
+            assert not re.search(r"\b(if|else|for|while)\b[^;]*$", before.rstrip()), (path, found[1])
+    assert len(seen) == 13 and "kv_weigh_rows_kernel" in seen
