@@ -1098,11 +1098,26 @@ __global__ void __launch_bounds__(MANY_THREADS, 1) kv_weigh_many_kernel(const We
 // (a max_kv that is too low) are computed here, value by value.
 constexpr int FINISH_WARPS = 4, FINISH_PAGES = 2 * FINISH_WARPS;   // of a CTA at once
 
-template <int D, typename T>
-__device__ __noinline__ float4 scores_again(const WeighArgs& w, const Unit& u, const uint8_t* piece, int row, int slot)
+template <typename T>
+__device__ __forceinline__ const T* query_of(const AttendArgs& g, const Unit& u, int row)
 {
-    const AttendArgs& g = w.a;
-    const T* q = static_cast<const T*>(g.q.data) + (u.first + row / g.group) * g.q.tok + (u.head * g.group + row % g.group) * g.q.head;
+    return static_cast<const T*>(g.q.data) + (u.first + row / g.group) * g.q.tok + (u.head * g.group + row % g.group) * g.q.head;
+}
+// The attention's 2^-e of a row, by which the row is in units of its coefficient: q . k itself may pass f32.
+template <int D, typename T>
+__device__ __noinline__ float row_scale(const WeighArgs& w, const Unit& u, int row)
+{
+    const T* q = query_of<T>(w.a, u, row);
+    float a = 0.0f;
+#pragma unroll 1
+    for (int d = 0; d < D; ++d)
+        a = fmaxf(a, fabsf(Elt<T>::to(q[d])));
+    return kv_pow2(-kv_exponent(a));
+}
+template <int D, typename T>
+__device__ __noinline__ float4 scores_again(const WeighArgs& w, const Unit& u, const uint8_t* piece, int row, float scale, int slot)
+{
+    const T* q = query_of<T>(w.a, u, row);
     float x[4];
 #pragma unroll 1
     for (int h = 0; h < 4; ++h) {
@@ -1114,10 +1129,9 @@ __device__ __noinline__ float4 scores_again(const WeighArgs& w, const Unit& u, c
 #pragma unroll 1
             for (int i = 0; i < 32; ++i) {
                 const int n = code[i / 8] >> (4 * (i / 2 % 4) + 16 * (i % 2)) & 15;
-                x[h] = fmaf(Elt<T>::to(q[32 * gr + i]), s * static_cast<float>(n - 8), x[h]);
+                x[h] = fmaf(Elt<T>::to(q[32 * gr + i]) * scale, s * static_cast<float>(n - 8), x[h]);
             }
         }
-        x[h] *= g.scale_log2;
     }
     return make_float4(x[0], x[1], x[2], x[3]);
 }
@@ -1126,7 +1140,7 @@ template <int D, typename T>
 __global__ void __launch_bounds__(FINISH_WARPS * 32, 10) kv_finish_weights_kernel(const WeighArgs w)
 {
     const AttendArgs& g = w.a;
-    __shared__ float4 rows[MOST_ROWS];   // coefficient, reference, 1 / sum
+    __shared__ float4 rows[MOST_ROWS];   // coefficient, reference, 1 / sum; 2^-e where scores are computed here
     grid_dep_wait();
     const int part = blockIdx.x % w.parts, unit = blockIdx.x / w.parts;
     Unit u;
@@ -1138,7 +1152,8 @@ __global__ void __launch_bounds__(FINISH_WARPS * 32, 10) kv_finish_weights_kerne
     for (int r = threadIdx.x; r < n; r += FINISH_WARPS * 32) {
         const float2 stats = g.stats[(u.first + r / g.group) * static_cast<size_t>(g.heads) + u.head * g.group + r % g.group];
         // a row that is no number adds nothing
-        rows[r] = make_float4(g.coef[static_cast<size_t>(unit) * g.score_rows + r], stats.x, stats.y, 0.0f);
+        rows[r] = make_float4(g.coef[static_cast<size_t>(unit) * g.score_rows + r], stats.x, stats.y,
+                              pages > g.score_pages ? row_scale<D, T>(w, u, r) : 0.0f);
     }
     __syncthreads();
     const bool still = w.in == w.out && w.decay == 1.0f;
@@ -1158,12 +1173,12 @@ __global__ void __launch_bounds__(FINISH_WARPS * 32, 10) kv_finish_weights_kerne
         float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         if (used) {
             const float* scores = g.scores + (static_cast<size_t>(unit) * g.score_pages + i) * g.score_rows * KV_PAGE + slot;
-            auto add = [&](float4 x, float coef, float4 c) {
+            auto add = [&](float4 x, float4 c) {
                 if (c.z > 0.0f) {
-                    sum.x = fmaf(kv_ex2(fmaf(x.x, coef, -c.y)), c.z, sum.x);
-                    sum.y = fmaf(kv_ex2(fmaf(x.y, coef, -c.y)), c.z, sum.y);
-                    sum.z = fmaf(kv_ex2(fmaf(x.z, coef, -c.y)), c.z, sum.z);
-                    sum.w = fmaf(kv_ex2(fmaf(x.w, coef, -c.y)), c.z, sum.w);
+                    sum.x = fmaf(kv_ex2(fmaf(x.x, c.x, -c.y)), c.z, sum.x);
+                    sum.y = fmaf(kv_ex2(fmaf(x.y, c.x, -c.y)), c.z, sum.y);
+                    sum.z = fmaf(kv_ex2(fmaf(x.z, c.x, -c.y)), c.z, sum.z);
+                    sum.w = fmaf(kv_ex2(fmaf(x.w, c.x, -c.y)), c.z, sum.w);
                 }
             };
             for (int r0 = 0; r0 < n; r0 += w.tile_rows) {
@@ -1181,18 +1196,18 @@ __global__ void __launch_bounds__(FINISH_WARPS * 32, 10) kv_finish_weights_kerne
 #pragma unroll
                         for (int k = 0; k < 4; ++k)
                             if (r + k < r1)
-                                add(x[k], rows[r + k].x, rows[r + k]);
+                                add(x[k], rows[r + k]);
                     }
                     continue;
                 }
                 for (int r = r0; r < r1; ++r) {
-                    float4 x = scores_again<D, T>(w, u, g.c.pages + piece * Piece<D>::BYTES, r, slot);
+                    float4 x = scores_again<D, T>(w, u, g.c.pages + piece * Piece<D>::BYTES, r, rows[r].w, slot);
                     const uint64_t m = kv_seen_bits(u.pos0 + r / g.group, kbase, g.window, g.sinks) >> slot;
                     x.x = m & 1u ? x.x : -INFINITY;
                     x.y = m & 2u ? x.y : -INFINITY;
                     x.z = m & 4u ? x.z : -INFINITY;
                     x.w = m & 8u ? x.w : -INFINITY;
-                    add(x, 1.0f, rows[r]);
+                    add(x, rows[r]);
                 }
             }
         }

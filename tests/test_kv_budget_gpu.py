@@ -806,3 +806,13 @@ def test_a_wait_that_runs_out_ends_every_kernel_of_the_call(dtype, new, length, 
     finally:
         mmq.mmq_debug_inject_wait_timeout(-1)
     assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("factor,scale", [(4e37, 1.2e-38), (1e-38, 2e37), (1e-30, 1.5e29)])
+@pytest.mark.parametrize("new,length,hint", [([1, 2], [700, 300], None), ([1, 2], [700, 300], 100), ([40], [700], None),
+                                             ([200], [700], None)])
+def test_rows_of_any_size_weigh(dtype, factor, scale, new, length, hint):
+    """q . k alone passes f32 where its product with the scale is an ordinary number, as does a row's size."""
+    b = Batch(new, length, 2, 128, dtype)
+    weigh_and_check(b, 6, factor=factor, scale=scale, max_kv=hint, decay=0.5)
