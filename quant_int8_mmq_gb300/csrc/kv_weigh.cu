@@ -782,7 +782,8 @@ __global__ void __launch_bounds__(FEW_THREADS, 1) kv_weigh_few_kernel(const Weig
 // ------------------------------------------------------------------ many rows
 // Operand tiles in the workspace: 128 rows of one sequence and kv head, [part][64-value block][row],
 // and their coefficients.  Those of sequence b are first_tile(b), first_tile(b) + 1, ...; tiles of a kv
-// head lie together.
+// head lie together.  From one sequence that has rows to the next both its slot and its first row grow by
+// one at least, so the lesser of them tells their tiles apart, and slots without rows take no room.
 //
 // A step: 128 rows by both halves of the keys, into one of two pairs of buffers.  The columns of the rows,
 // of which a warp makes what the sums need out of the attention's results, are kept four steps, as the
@@ -809,7 +810,7 @@ constexpr int MANY_THREADS = 768;   // products, row operands, columns and an id
 
 __device__ __forceinline__ long long first_tile(const AttendArgs& g, int start, int b)
 {
-    return static_cast<long long>(start) * g.group / MOST_ROWS + b;
+    return static_cast<long long>(start) * g.group / MOST_ROWS + min(b, start);
 }
 
 // A CTA a row.  It needs none of the attention's results, but what was written before the attention (q, start) is
@@ -1283,7 +1284,7 @@ size_t weigh_bytes(int dtype, int heads, int kv_heads, int dim, int batch, int n
 {
     const long long group = heads / kv_heads, rows = (max_q < ntok ? max_q : ntok) * group;
     *cols = static_cast<int>(rows < 16 ? 16 : rows > MOST_ROWS ? MOST_ROWS : (rows + 15) / 16 * 16);
-    *tiles = rows <= MOST_ROWS ? 0 : static_cast<long long>(ntok) * group / MOST_ROWS + batch + 1;
+    *tiles = rows <= MOST_ROWS ? 0 : static_cast<long long>(ntok) * group / MOST_ROWS + (batch < ntok ? batch : ntok);
     const size_t record = static_cast<size_t>(dtype == KV_F32 ? 2 : 1) * MOST_ROWS * dim * 2 + MOST_ROWS * 4;
     return static_cast<size_t>(*tiles) * kv_heads * record;
 }

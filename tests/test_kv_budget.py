@@ -289,3 +289,17 @@ def test_every_cta_waits_for_the_kernel_before_it(mmq_lib):
                 assert not re.search(memory, before), (path, found[1], memory)
             assert not re.search(r"\b(if|else|for|while)\b[^;]*$", before.rstrip()), (path, found[1])
     assert len(seen) == 13 and "kv_weigh_rows_kernel" in seen
+
+
+def test_slots_without_new_tokens_need_no_operands(mmq_lib):
+    """Rows as operands: a tile of 128 of them more for each sequence that has any, not for each slot of the batch."""
+    def need(batch, ntok=2048, dtype=0):
+        c = cache(kv_heads=32, batch=batch, max_pages=64)
+        return (mmq.mmq_kv_attend_weights_workspace_bytes(c, dtype, 32, ntok, 2048, 4096)
+                - mmq.mmq_kv_attend_workspace_bytes(c, dtype, 32, ntok, 2048, 4096))
+    for dtype, tile in ((0, 2 * 128 * 128 * 2 + 128 * 4), (1, 128 * 128 * 2 + 128 * 4)):
+        for ntok in (2048, 200, 300):
+            stats = ntok * 32 * 8
+            for batch in (1, 16, 1024, 1 << 20):
+                assert need(batch, ntok, dtype) <= stats + (ntok // 128 + min(batch, ntok) + 1) * 32 * tile
+        assert need(1 << 20, 2048, dtype) == need(2048, 2048, dtype)

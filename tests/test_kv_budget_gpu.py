@@ -816,3 +816,12 @@ def test_rows_of_any_size_weigh(dtype, factor, scale, new, length, hint):
     """q . k alone passes f32 where its product with the scale is an ordinary number, as does a row's size."""
     b = Batch(new, length, 2, 128, dtype)
     weigh_and_check(b, 6, factor=factor, scale=scale, max_kv=hint, decay=0.5)
+
+
+@pytest.mark.parametrize("dtype", [F32, F16])
+@pytest.mark.parametrize("new", [[0] * 90 + [300] + [0] * 200 + [1, 0, 1, 129, 0, 2] + [0] * 40 + [128],
+                                 [1] * 140 + [0] * 300 + [200], [1, 200] + [0] * 50 + [1] * 20 + [0, 255, 1]])
+def test_many_slots_and_few_with_new_tokens(dtype, new):
+    """Operand tiles of sequences lie side by side however many slots without rows are between them."""
+    b = Batch(new, [n + (i * 37) % 150 for i, n in enumerate(new)], 2, 64, dtype)
+    weigh_and_check(b, 6, decay=0.5)
