@@ -241,12 +241,12 @@ WeighPlan weigh_plan(const mmq_kv_cache* c, const AttendPlan& attend, int dtype,
         p.score_pages = static_cast<int>(pages < c->max_pages ? pages : c->max_pages);
         p.score_rows = (max_q < 1 ? 1 : max_q < ntok ? max_q : ntok) * (heads / c->kv_heads);
         const size_t rows = static_cast<size_t>(c->batch) * c->kv_heads * p.score_rows;
-        p.score_bytes = rows * p.score_pages * mmq::KV_PAGE * sizeof(float);
-        p.coef_bytes = (rows * sizeof(float) + 15) / 16 * 16;
-        if (p.score_bytes > size_t{1} << 30)
-            p.score_bytes = p.coef_bytes = 0;
-        else
+        const size_t row = static_cast<size_t>(p.score_pages) * mmq::KV_PAGE * sizeof(float);
+        if (rows <= (size_t{1} << 30) / row) {   // the product itself may pass 64 bits
+            p.score_bytes = rows * row;
+            p.coef_bytes = (rows * sizeof(float) + 15) / 16 * 16;
             p.operand_bytes = 0;
+        }
     }
     return p;
 }

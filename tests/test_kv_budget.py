@@ -303,3 +303,13 @@ def test_slots_without_new_tokens_need_no_operands(mmq_lib):
             for batch in (1, 16, 1024, 1 << 20):
                 assert need(batch, ntok, dtype) <= stats + (ntok // 128 + min(batch, ntok) + 1) * 32 * tile
         assert need(1 << 20, 2048, dtype) == need(2048, 2048, dtype)
+
+
+def test_sizes_past_64_bits_are_not_small_ones(mmq_lib):
+    """Scores of the largest batch that the checks let through are no room for a few."""
+    for heads in (1020, 1021, 1023, 1024):
+        for q in (1, 3, 4, 16, 32):
+            c = cache(kv_heads=heads, batch=1 << 20, max_pages=1 << 24)
+            size = mmq.mmq_kv_attend_weights_workspace_bytes(c, 0, heads, q, q, (1 << 31) - 1)
+            few = mmq.mmq_kv_attend_workspace_bytes(c, 0, heads, q, q, (1 << 31) - 1) + q * heads * 8 + 16
+            assert size <= few, (heads, q)                              # the keys are read again
