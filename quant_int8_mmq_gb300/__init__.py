@@ -544,6 +544,12 @@ def _kv_empty(shape, dtype, device, stream):
         return torch.empty(shape, dtype=dtype, device=device)
 
 
+def _c_int(n):
+    """ctypes would drop the high bits; larger numbers mean no more than the largest the library takes, and it
+    refuses any below zero."""
+    return max(-1, min(n, _INT_MAX))
+
+
 def kv_write(k, v, pages, table, start, length, stream=None):
     """Quantise the new tokens' k and v ([rows, kv_heads, head_dim], any token and head strides)
     into the cache."""
@@ -583,9 +589,8 @@ def kv_attend(q, pages, table, start, length, max_q, max_kv=None, scale=None, wi
         max_kv = c.max_pages * KV_PAGE
     if scale is None:
         scale = dim ** -0.5
-    if (max_q | max_kv | window | sinks) > _INT_MAX:
-        # ctypes would drop the high bits; larger numbers mean no more than the largest the library takes
-        max_q, max_kv, window, sinks = (min(n, _INT_MAX) for n in (max_q, max_kv, window, sinks))
+    if not 0 <= (max_q | max_kv | window | sinks) <= _INT_MAX:
+        max_q, max_kv, window, sinks = (_c_int(n) for n in (max_q, max_kv, window, sinks))
     rq = _kv_rows(q, rows, heads, dim, dev, "q")
     if out is None:
         out = _torch_module.empty_like(q) if stream is None and q.is_contiguous() else _kv_empty(
@@ -709,8 +714,7 @@ def kv_attend_weights(q, weights, pages, table, start, length, max_q, max_kv=Non
         max_kv = c.max_pages * KV_PAGE
     if scale is None:
         scale = dim ** -0.5
-    # ctypes would drop high bits; larger numbers mean no more than the largest the library takes
-    max_q, max_kv, window, sinks = (min(n, _INT_MAX) for n in (max_q, max_kv, window, sinks))
+    max_q, max_kv, window, sinks = (_c_int(n) for n in (max_q, max_kv, window, sinks))
     if into is None:
         into = weights
     at, to = _kv_weights(weights, c, dev, "weights"), _kv_weights(into, c, dev, "into")
@@ -744,7 +748,7 @@ def kv_evict(weights, pages, table, start, length, new_table, keep, first=4, las
         raise ValueError(f"new_table must be a contiguous int32 [{c.batch}, new_pages] tensor on the cache's device")
     if max_kv is None:
         max_kv = c.max_pages * KV_PAGE
-    max_kv = min(max_kv, _INT_MAX)
+    max_kv = _c_int(max_kv)
     for n, name in ((keep, "keep"), (first, "first"), (last, "last")):
         if not 0 <= n <= _INT_MAX:
             raise ValueError(f"{name} must be a number of tokens, got {n}")

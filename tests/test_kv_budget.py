@@ -305,6 +305,43 @@ def test_slots_without_new_tokens_need_no_operands(mmq_lib):
         assert need(1 << 20, 2048, dtype) == need(2048, 2048, dtype)
 
 
+def test_numbers_far_below_zero_stay_below(mmq_lib, monkeypatch):
+    """Their low 32 bits may be none, but they are not taken for 0: the library is given negative ones, which it
+    refuses."""
+    import torch
+
+    class OnZero(torch.Tensor):
+        def get_device(self):
+            return 0
+
+    def at(*shape, dtype=torch.int32):
+        return torch.zeros(*shape, dtype=dtype).as_subclass(OnZero)
+
+    calls = {}
+
+    class Library:
+        def __getattr__(self, name):
+            return lambda *a: calls.update({name: a}) or 0
+
+    monkeypatch.setattr(mmq, "_lib", Library())
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda dev: 0, raising=False)
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0, raising=False)
+    q, kv = at(3, 2, 64, dtype=torch.float32), (at(4, 2, 72 * 64, dtype=torch.uint8), at(1, 4), at(2), at(1))
+    w, ws = at(4, 2, 64, dtype=torch.float32), at(1 << 16, dtype=torch.uint8)
+    place = dict(max_q=5, max_kv=6, window=8, sinks=9)
+    for name, i in place.items():
+        for more in ({}, {"max_kv": 1 << 40}, {"max_q": 1 << 40}):
+            args = {**dict(max_q=3, max_kv=64, window=0, sinks=0), **more, name: -(1 << 40)}
+            mmq.kv_attend(q, *kv, out=q, workspace=ws, **args)
+            mmq.kv_attend_weights(q, w, *kv, out=q, workspace=ws, **args)
+            for call in ("mmq_kv_attend", "mmq_kv_attend_weights"):
+                assert -(1 << 31) <= calls[call][i] < 0, (call, args)
+                assert all(calls[call][k] < 1 << 31 for k in place.values())
+            assert -(1 << 31) <= calls["mmq_kv_attend_weights_workspace_bytes"][{5: 4, 6: 5, 8: 6, 9: 7}[i]] < 0
+    mmq.kv_evict(w, *kv, at(1, 1), 8, 1, 2, max_kv=-(1 << 40), new_length=at(1), kept=at(1, 2, 8))
+    assert -(1 << 31) <= calls["mmq_kv_evict"][7] < 0
+
+
 def test_sizes_past_64_bits_are_not_small_ones(mmq_lib):
     """Scores of the largest batch that the checks let through are no room for a few."""
     for heads in (1020, 1021, 1023, 1024):
