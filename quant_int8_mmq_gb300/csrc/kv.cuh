@@ -379,13 +379,13 @@ struct WeighArgs {
     int max_q;             // new tokens of a sequence that count
     int tile_rows;         // kv_finish_weights_kernel: rows of the attention's tiles
     int cols;              // kv_weigh_few_kernel: rows as a column count, a multiple of 16 up to 128
-    long long tiles;       // kv_weigh_many_kernel: operand tiles of a kv head in the workspace; 0: few rows
+    long long operand_rows;   // kv_weigh_many_kernel: room for rows of a kv head in the workspace; 0: few rows
     uint8_t* operands;
     int parts;             // CTAs that share a sequence's kv head
 };
 // Bytes of the row operands that a call needs in the workspace, and the numbers above.
 size_t weigh_bytes(int dtype, int heads, int kv_heads, int dim, int batch, int ntok, int max_q, int* cols,
-                   long long* tiles);
+                   long long* operand_rows);
 cudaError_t launch_kv_weigh(const WeighArgs& a, int dim, int dtype, int max_kv, cudaStream_t s);
 // The same from the scores that kv_step.cu has left.
 cudaError_t launch_kv_finish_weights(const WeighArgs& a, int dim, int dtype, int max_kv, cudaStream_t s);

@@ -224,7 +224,7 @@ AttendPlan plan(const mmq_kv_cache* c, int dtype, int heads, int ntok, int max_q
 struct WeighPlan {
     size_t stats_bytes, operand_bytes, score_bytes, coef_bytes;
     int cols, score_pages, score_rows;
-    long long tiles;
+    long long operand_rows;
 };
 WeighPlan weigh_plan(const mmq_kv_cache* c, const AttendPlan& attend, int dtype, int heads, int ntok, int max_q,
                      int max_kv)
@@ -232,7 +232,7 @@ WeighPlan weigh_plan(const mmq_kv_cache* c, const AttendPlan& attend, int dtype,
     WeighPlan p = {};
     p.stats_bytes = (static_cast<size_t>(ntok) * static_cast<size_t>(heads) * sizeof(float2) + 15) / 16 * 16;
     p.operand_bytes = mmq::weigh_bytes(dtype, heads, c->kv_heads, c->head_dim, c->batch, ntok, max_q < 1 ? 1 : max_q,
-                                       &p.cols, &p.tiles);
+                                       &p.cols, &p.operand_rows);
     // A few rows' scores are kept, unless they are more than a gigabyte (a batch of long tables without a
     // max_kv); the keys are then read again.  Kept / read again, us, attention included: a token on 131071
     // keys, 32 heads on 8, f32, 57 / 81; 64 sequences of 95 to 8192, bf16, 114 / 165.
@@ -333,7 +333,7 @@ mmq_status attend(const mmq_kv_cache* c, const mmq_rows* q, const mmq_rows* out,
     if (e == cudaSuccess && weights) {
         a.wc = {a.c.bad - 1, mmq::WAIT_LIMIT_NS, -1};
         const mmq::WeighArgs w = {a, weights->in, weights->out, weights->decay, max_q < 1 ? 1 : max_q, p.tile_rows, wp.cols,
-                                  wp.tiles, rest, 1};
+                                  wp.operand_rows, rest, 1};
         const auto weigh = a.scores ? mmq::launch_kv_finish_weights : mmq::launch_kv_weigh;
         e = weigh(w, c->head_dim, q->dtype, max_kv, reinterpret_cast<cudaStream_t>(s));
     }

@@ -148,10 +148,10 @@ struct KeyCodes {
     }
 };
 
-// One row, four values a lane, as operand row r of [64-value block][n rows] tiles, by a warp, an
-// f32 row's low part as row r + low; the coefficient that makes its products powers of two.
+// One row, four values a lane, as operand row r (modulo 8) at dst, its 64-value blocks `block` bytes
+// apart, by a warp, an f32 row's low part `low` bytes on; the coefficient that makes its products powers of two.
 template <int D, typename T>
-__device__ __forceinline__ float put_row(const AttendArgs& g, float4 x, uint8_t* dst, int n, int r, int low, int lane)
+__device__ __forceinline__ float put_row(const AttendArgs& g, float4 x, uint8_t* dst, size_t block, int r, size_t low, int lane)
 {
     float a = fmaxf(fmaxf(fabsf(x.x), fabsf(x.y)), fmaxf(fabsf(x.z), fabsf(x.w)));
 #pragma unroll
@@ -164,10 +164,10 @@ __device__ __forceinline__ float put_row(const AttendArgs& g, float4 x, uint8_t*
         kv_split2(x.x * f, x.y * f, hi.x, lo.x);
         kv_split2(x.z * f, x.w * f, hi.y, lo.y);
         const int d = 4 * lane;
-        uint8_t* at = dst + d / 64 * n * 128 + r * 128 + ((d / 8 % 8 ^ (r & 7)) << 4) + d % 8 * 2;
+        uint8_t* at = dst + d / 64 * block + ((d / 8 % 8 ^ (r & 7)) << 4) + d % 8 * 2;
         *reinterpret_cast<uint2*>(at) = hi;
         if constexpr (sizeof(T) == 4)
-            *reinterpret_cast<uint2*>(at + low * 128) = lo;   // a multiple of 8 rows: the same turn
+            *reinterpret_cast<uint2*>(at + low) = lo;   // a multiple of 8 rows: the same turn
     }
     return fminf(fmaxf(g.scale_log2 * kv_pow2(e), 1e-38f), 1e38f);
 }
@@ -200,8 +200,8 @@ __device__ __forceinline__ void put_rows(const AttendArgs& g, const Unit& u, int
             if (r >= n)
                 break;
             const bool there = stats[i].y > 0.0f && lane < D / 4;   // a row without weights is given as zeros
-            const float coef = put_row<D, T>(g, there ? x[i].get() : make_float4(0.0f, 0.0f, 0.0f, 0.0f), dst,
-                                             (sizeof(T) == 4 ? 2 : 1) * n, r, n, lane);
+            const float coef = put_row<D, T>(g, there ? x[i].get() : make_float4(0.0f, 0.0f, 0.0f, 0.0f), dst + r * 128,
+                                             (sizeof(T) == 4 ? 2 : 1) * n * 128, r, n * 128, lane);
             if (lane == 0) {
                 cols->coef[r] = coef;
                 cols->minus[r] = -stats[i].x;
@@ -780,10 +780,11 @@ __global__ void __launch_bounds__(FEW_THREADS, 1) kv_weigh_few_kernel(const Weig
 }
 
 // ------------------------------------------------------------------ many rows
-// Operand tiles in the workspace: 128 rows of one sequence and kv head, [part][64-value block][row],
-// and their coefficients.  Those of sequence b are first_tile(b), first_tile(b) + 1, ...; tiles of a kv
-// head lie together.  From one sequence that has rows to the next both its slot and its first row grow by
-// one at least, so the lesser of them tells their tiles apart, and slots without rows take no room.
+// Rows as operands in the workspace: [kv head][part][64-value block][row], and [kv head][row] coefficients.
+// Those of sequence b begin at first_row(b), on a multiple of 8, where the swizzle's turn begins, so that a
+// step's 128 rows are one copy a block from wherever it begins.  From one sequence that has rows to the
+// next both its slot and its first token grow by one at least, so the lesser of them tells their rows
+// apart.  (In tiles of 128 rows a sequence, a batch of single tokens and one long prompt took up to 16 times the room.)
 //
 // A step: 128 rows by both halves of the keys, into one of two pairs of buffers.  The columns of the rows,
 // of which a warp makes what the sums need out of the attention's results, are kept four steps, as the
@@ -795,7 +796,6 @@ struct Many {
     static constexpr int PARTS = sizeof(T) == 4 ? 2 : 1, KB = D / 64;
     static constexpr int BLOCK = MOST_ROWS * 128;
     static constexpr int Q_BYTES = PARTS * KB * BLOCK;
-    static constexpr int RECORD = Q_BYTES + MOST_ROWS * 4;   // operands, coefficients
     static constexpr int K_BYTES = KB * KEYS * 128;        // of 128 keys
     static constexpr int STAGES = 2, CSTAGES = 4;          // operands, columns on their way or in use
     static constexpr int K = 0, Q = K + 2 * K_BYTES, COLS = Q + STAGES * Q_BYTES;
@@ -808,9 +808,16 @@ struct Many {
 };
 constexpr int MANY_THREADS = 768;   // products, row operands, columns and an idle warp; widening; 4 x 4 of sums
 
-__device__ __forceinline__ long long first_tile(const AttendArgs& g, int start, int b)
+constexpr int TURN_ROWS = 8;
+__device__ __forceinline__ long long first_row(const AttendArgs& g, int start, int b)
 {
-    return static_cast<long long>(start) * g.group / MOST_ROWS + min(b, start);
+    return (static_cast<long long>(start) * g.group / TURN_ROWS + min(b, start)) * TURN_ROWS;
+}
+// The coefficients of a kv head.
+template <typename C>
+__device__ __forceinline__ float* coefficients(const WeighArgs& w, int head)
+{
+    return reinterpret_cast<float*>(w.operands + w.a.c.kv_heads * w.operand_rows * (C::PARTS * C::KB * 128)) + head * w.operand_rows;
 }
 
 // A CTA a row.  It needs none of the attention's results, but what was written before the attention (q, start) is
@@ -830,8 +837,7 @@ __global__ void __launch_bounds__(256, 8) kv_weigh_rows_kernel(const WeighArgs w
         return;
     for (int h = threadIdx.x / 32; h < g.heads; h += 8) {
         const int row = (r - first) * g.group + h % g.group;
-        uint8_t* record = w.operands +
-                          (h / g.group * w.tiles + first_tile(g, first, b) + row / MOST_ROWS) * static_cast<long long>(C::RECORD);
+        const long long at = first_row(g, first, b) + row;
         float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         if (lane < D / 4)
             x = load4(static_cast<const T*>(g.q.data) + r * g.q.tok + h * g.q.head + 4 * lane, g.wide);
@@ -839,9 +845,11 @@ __global__ void __launch_bounds__(256, 8) kv_weigh_rows_kernel(const WeighArgs w
         const bool finite = fabsf(x.x) <= FLT_MAX && fabsf(x.y) <= FLT_MAX && fabsf(x.z) <= FLT_MAX && fabsf(x.w) <= FLT_MAX;
         if (!__all_sync(0xffffffffu, finite))
             x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        const float coef = put_row<D, T>(g, x, record, MOST_ROWS, row % MOST_ROWS, C::KB * MOST_ROWS, lane);
+        const size_t block = w.operand_rows * 128;
+        const float coef = put_row<D, T>(g, x, w.operands + h / g.group * (C::PARTS * C::KB) * block + at * 128, block, row,
+                                         C::KB * block, lane);
         if (lane == 0)
-            reinterpret_cast<float*>(record + C::Q_BYTES)[row % MOST_ROWS] = coef;
+            coefficients<C>(w, h / g.group)[at] = coef;
     }
 }
 
@@ -910,7 +918,6 @@ __global__ void __launch_bounds__(MANY_THREADS, 1) kv_weigh_many_kernel(const We
     };
     bool ok = true;
     int step = 0, visit = 0;    // steps, and groups with any, so far
-    const uint8_t* records = w.operands + (static_cast<long long>(u.head) * w.tiles + first_tile(g, u.first, u.b)) * C::RECORD;
     if (warp == 0) {
         const uint32_t lead = elect_one();
         for (int group = part; ok && group < groups; group += w.parts) {
@@ -944,6 +951,8 @@ __global__ void __launch_bounds__(MANY_THREADS, 1) kv_weigh_many_kernel(const We
             mbar_drain_wait(bar(C::DRAIN), 0, WAIT_LIMIT_NS, g.wc.err);
         __syncwarp();
     } else if (warp == 1) {
+        const size_t block = w.operand_rows * 128;
+        const uint8_t* operands = w.operands + u.head * (C::PARTS * C::KB) * block + first_row(g, u.first, u.b) * 128;
         for (int group = part; ok && group < groups; group += w.parts) {
             int lo, hi;
             range(group, lo, hi);
@@ -953,11 +962,11 @@ __global__ void __launch_bounds__(MANY_THREADS, 1) kv_weigh_many_kernel(const We
                 if (!ok)
                     break;
                 if (lane == 0) {
-                    const uint8_t* src = records + static_cast<long long>(tile) * C::RECORD;
+                    const uint8_t* src = operands + static_cast<long long>(tile) * C::BLOCK;
                     mbar_arrive_expect_tx(bar(C::QFULL + stage), C::Q_BYTES);
 #pragma unroll
-                    for (int i = 0; i < C::Q_BYTES; i += C::BLOCK)
-                        bulk_g2s(sbase + C::Q + stage * C::Q_BYTES + i, src + i, C::BLOCK, bar(C::QFULL + stage));
+                    for (int i = 0; i < C::PARTS * C::KB; ++i)
+                        bulk_g2s(sbase + C::Q + stage * C::Q_BYTES + i * C::BLOCK, src + i * block, C::BLOCK, bar(C::QFULL + stage));
                 }
             }
         }
@@ -968,12 +977,13 @@ __global__ void __launch_bounds__(MANY_THREADS, 1) kv_weigh_many_kernel(const We
         __syncwarp();
     } else if (warp == 2) {
         // four rows a lane, on their way while the place is not free
+        const float* coefs = coefficients<C>(w, u.head) + first_row(g, u.first, u.b);
         for (int group = part; ok && group < groups; group += w.parts) {
             int lo, hi;
             range(group, lo, hi);
             for (int tile = lo; tile < hi; ++tile, ++step) {
                 const int cstage = step % C::CSTAGES;
-                const float4 coef = *reinterpret_cast<const float4*>(records + static_cast<long long>(tile) * C::RECORD + C::Q_BYTES + 16 * lane);
+                const float4 coef = *reinterpret_cast<const float4*>(coefs + static_cast<long long>(tile) * MOST_ROWS + 4 * lane);
                 float f[4] = {coef.x, coef.y, coef.z, coef.w};
                 float2 stats[4];
                 int pos[4];
@@ -1253,7 +1263,7 @@ cudaError_t launch_weigh(WeighArgs a, long long keys, cudaStream_t s)
         want = want < 0x7fffffffll / units ? want : 0x7fffffffll / units;
         return static_cast<int>(want < 1 ? 1 : want);
     };
-    if (a.tiles == 0) {
+    if (a.operand_rows == 0) {
         static std::atomic<uint64_t> done{0};
         cudaError_t e = kv_allow_smem(kv_weigh_few_kernel<D, T>, 226 * 1024, &done);
         if (e != cudaSuccess)
@@ -1280,13 +1290,17 @@ cudaError_t launch_weigh(WeighArgs a, long long keys, cudaStream_t s)
 
 }  // namespace
 
-size_t weigh_bytes(int dtype, int heads, int kv_heads, int dim, int batch, int ntok, int max_q, int* cols, long long* tiles)
+size_t weigh_bytes(int dtype, int heads, int kv_heads, int dim, int batch, int ntok, int max_q, int* cols,
+                   long long* operand_rows)
 {
     const long long group = heads / kv_heads, rows = (max_q < ntok ? max_q : ntok) * group;
     *cols = static_cast<int>(rows < 16 ? 16 : rows > MOST_ROWS ? MOST_ROWS : (rows + 15) / 16 * 16);
-    *tiles = rows <= MOST_ROWS ? 0 : static_cast<long long>(ntok) * group / MOST_ROWS + (batch < ntok ? batch : ntok);
-    const size_t record = static_cast<size_t>(dtype == KV_F32 ? 2 : 1) * MOST_ROWS * dim * 2 + MOST_ROWS * 4;
-    return static_cast<size_t>(*tiles) * kv_heads * record;
+    // up to 7 rows between two sequences, and the last step's copies past the last row
+    *operand_rows = rows <= MOST_ROWS ? 0
+                                      : (static_cast<long long>(ntok) * group / TURN_ROWS + (batch < ntok ? batch : ntok)) * TURN_ROWS +
+                                            MOST_ROWS;
+    const size_t row = static_cast<size_t>(dtype == KV_F32 ? 2 : 1) * dim * 2 + 4;
+    return static_cast<size_t>(*operand_rows) * kv_heads * row;
 }
 
 cudaError_t launch_kv_weigh(const WeighArgs& a, int dim, int dtype, int max_kv, cudaStream_t s)

@@ -350,3 +350,35 @@ def test_sizes_past_64_bits_are_not_small_ones(mmq_lib):
             size = mmq.mmq_kv_attend_weights_workspace_bytes(c, 0, heads, q, q, (1 << 31) - 1)
             few = mmq.mmq_kv_attend_workspace_bytes(c, 0, heads, q, q, (1 << 31) - 1) + q * heads * 8 + 16
             assert size <= few, (heads, q)                              # the keys are read again
+
+
+def test_operands_take_the_room_of_their_rows(mmq_lib):
+    """Rows, up to 7 more for each sequence, and 128: a long prompt in a batch of many slots is not a tile of 128 a slot."""
+    for dtype, row in ((0, 2 * 128 * 2 + 4), (1, 128 * 2 + 4)):
+        for heads in (8, 32):
+            for ntok in (200, 2048, 4000):
+                for batch in (1, 16, 1024, 1 << 20):
+                    c = cache(kv_heads=8, batch=batch, max_pages=64)
+                    size = (mmq.mmq_kv_attend_weights_workspace_bytes(c, dtype, heads, ntok, ntok, 4096)
+                            - mmq.mmq_kv_attend_workspace_bytes(c, dtype, heads, ntok, ntok, 4096))
+                    rows = ntok * heads // 8
+                    assert 8 * rows * row <= size <= ntok * heads * 8 + 8 * row * (rows + 8 * min(batch, ntok) + 128)
+
+
+def test_rows_of_sequences_do_not_meet():
+    """first_row of kv_weigh.cu: from the first row of a sequence on there is room for all of its rows before the next
+    one's, and for 128 past the last, whatever sequences without rows lie between."""
+    import random
+    rng = random.Random(1)
+    for _ in range(2000):
+        group, batch = rng.choice([1, 2, 3, 4, 5, 7, 8, 16, 129]), rng.randint(1, 40)
+        new = [rng.choice([0, 0, 1, 1, 2, 7, 8, 9, 127, 128, 300]) for _ in range(batch)]
+        ntok = sum(new) + rng.choice([0, 0, 5])
+        start, end = rng.choice([0, ntok - sum(new)]), 0
+        for b, n in enumerate(new):
+            if n:
+                at = (start * group // 8 + min(b, start)) * 8
+                assert at >= end
+                end = at + n * group
+            start += n
+        assert end + 127 <= (ntok * group // 8 + min(batch, ntok)) * 8 + 128
