@@ -451,13 +451,21 @@ mmq_status mmq_kv_attend(const mmq_kv_cache* c, const mmq_rows* q, const mmq_row
  * (w as above; 0 for keys that a row does not see; new = start[b + 1] - start[b], whose tokens start
  * from 0, so nothing has to be cleared).  decay in [0, 1].  new_weights may be weights; a buffer of
  * its own keeps the old ones, for a step that may be taken back.  Slots past the last token, and
- * pages of no sequence with new tokens, are left as they were.  A page that two sequences of the call
- * share gets one of their sums where new_weights is a buffer of its own, and in place may get one of
- * them added to the other.  A row that is not finite, or past max_q (see there), adds nothing.  The
- * sums are f32, in a fixed order.
- * Workspace: mmq_kv_attend_weights_workspace_bytes, more than 0 where ntok is.  For few new tokens it
- * has room for the scores of max_kv keys, up to a gigabyte, so that K is read once: a max_kv near
- * the longest length keeps it small.  What it holds before does not matter. */
+ * pages of no sequence with new tokens, are left as they were.  A row that is not finite, or past
+ * max_q (see there), adds nothing.  The sums are f32, in a fixed order: the same call gives the same bits.
+ * No two sequences of a call that have new tokens may share a page (a prefix, say): what its weights then
+ * are is not defined and varies from call to call (one's sum, or, in place, one added to the other with
+ * the decay applied twice), and nothing reports it.  A call for each of them is defined: each adds to
+ * what the one before left.
+ * Tokens that came in by another call (mmq_kv_attend) hold what the memory held; clear that first.
+ * Workspace: mmq_kv_attend_weights_workspace_bytes, more than 0 where ntok is, and what it holds before
+ * does not matter.  Up to 16 to 48 rows (new tokens times the heads that read a kv head, by type and
+ * head_dim) it has room for the scores of max_kv keys, up to a gigabyte, so that K is read once.  Above
+ * 128 rows it has the rows of all heads in 16 bits, twice that for f32 ones, and up to 8 more rows of
+ * each kv head for each sequence that may have new tokens.
+ * max_kv: with scores kept, keys past it are computed again value by value, and at once cost much more than
+ * their reading (one token on 131071 keys, 32 heads on 8: 56 us; with max_kv 130000 0.27 ms, with 65536 1.2 ms,
+ * with 1 41 ms).  Where lengths grow while a captured call is replayed, give the length they may reach. */
 mmq_status mmq_kv_attend_weights_workspace_bytes(const mmq_kv_cache* c, int dtype, int heads, int ntok, int max_q,
                                                  int max_kv, int window, int sinks, size_t* bytes);
 mmq_status mmq_kv_attend_weights(const mmq_kv_cache* c, const mmq_rows* q, const mmq_rows* out, int heads, int ntok,
@@ -474,9 +482,9 @@ mmq_status mmq_kv_attend_weights(const mmq_kv_cache* c, const mmq_rows* q, const
  *   new_length  [batch]: min(length, keep); may be c->length
  *   kept        [batch][kv_heads][keep]: the old place of the token in each new one, -1 past new_length
  *   max_kv      about the longest length, as for mmq_kv_attend
- * c->start is not read.  The old pages are only read, so other sequences may share them; the new ones
- * may not be among them or be named twice (what they then hold is undefined).  Slots past
- * new_length are left as they were.  A token whose old page is no page of the pool counts as the
+ * c->start is not read.  The old pages are only read, so other sequences may share them (for their
+ * weights see mmq_kv_attend_weights); the new ones may not be among them or be named twice (what they
+ * then hold is undefined).  Slots past new_length are left as they were.  A token whose old page is no page of the pool counts as the
  * least weight and moves as zeros, one whose new page is none does not move, and mmq_get_device_error
  * then returns MMQ_ERR_ARG.
  * A window of mmq_kv_attend counts slots: after an eviction it reaches further back than before.

@@ -688,7 +688,8 @@ def kv_write_rope(q, k, v, pos, plan, pages, table, start, length, out=None, str
 
 def kv_weights(num_pages, kv_heads, device="cuda"):
     """What each cached token has received so far: float32 [num_pages, kv_heads, 64], beside the pages.
-    It need not be cleared, a token's weight starts from 0 in the call that it is new in."""
+    It need not be cleared, a token's weight starts from 0 in the kv_attend_weights call that it is new in; one
+    that came in by kv_attend alone has what the memory held."""
     return _torch().empty((num_pages, kv_heads, KV_PAGE), dtype=_torch().float32, device=device)
 
 
@@ -704,7 +705,9 @@ def kv_attend_weights(q, weights, pages, table, start, length, max_q, max_kv=Non
                       decay=1.0, out=None, into=None, workspace=None, stream=None):
     """(kv_attend's result, weights): the softmax weight that each key received, summed over the new
     rows and the heads of its kv head, is added to decay times what weights (from kv_weights) holds;
-    in place, or into another such tensor."""
+    in place, or into another such tensor.  Sequences of one call may not share pages.  For few new tokens
+    the workspace has room for the scores of max_kv keys: all of the table unless given, up to a gigabyte a
+    call.  Keys past max_kv cost far more than the others: give the length that sequences may reach."""
     c, dev = _kv_cache(pages, table, start, length)
     if q.dim() != 3:
         raise ValueError(f"q must be [rows, heads, head_dim], got {list(q.shape)}")

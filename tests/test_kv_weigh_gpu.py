@@ -2,6 +2,8 @@
 where lengths are none, and eviction by clusters of every size: on the GPU, against the definitions of
 tests/budget_reference.py in 64 bits, with the tolerances of tests/test_kv_budget_gpu.py.
 """
+from types import SimpleNamespace
+
 import pytest
 import torch
 
@@ -226,6 +228,23 @@ def test_rows_past_max_q_of_many(dtype, new, max_q):
     mmq.kv_attend_weights(q, w, *b.cache, max_q, decay=0.5)
     assert status() == (1 if max_q < max(new) else 0)
     check_weights(b, q, before, w, decay=0.5, max_q=max_q)
+
+
+@pytest.mark.parametrize("dtype", [F32, F16])
+@pytest.mark.parametrize("new", [2, 40, 150])
+def test_sequences_that_share_pages_weigh_one_by_one(dtype, new):
+    """Not in one call; in a call each, both add to what the pages of the prefix hold."""
+    b = Batch([new, new], [400, 360], 2, 64, dtype)
+    b.table[1, :3] = b.table[0, :3]
+    b.k[1][:192], b.v[1][:192] = b.k[0][:192], b.v[0][:192]
+    q, w = b.q(8), weights_for(b)
+    start = torch.tensor([0, new], dtype=torch.int32, device=DEV)
+    for s in range(2):
+        one, rows, before = slice(s, s + 1), slice(s * new, (s + 1) * new), w.clone()
+        mmq.kv_attend_weights(q[rows], w, b.pages, b.table[one], start, b.length[one], new, decay=0.5)
+        assert status() == 0
+        alone = SimpleNamespace(new=[new], len=b.len[one], hk=b.hk, dim=b.dim, table=b.table[one], k=b.k[one], v=b.v[one])
+        check_weights(alone, q[rows], before, w, decay=0.5)
 
 
 # ------------------------------------------------------------------------------------ eviction
