@@ -234,8 +234,11 @@ WeighPlan weigh_plan(const mmq_kv_cache* c, const AttendPlan& attend, int dtype,
     p.operand_bytes = mmq::weigh_bytes(dtype, heads, c->kv_heads, c->head_dim, c->batch, ntok, max_q < 1 ? 1 : max_q,
                                        &p.cols, &p.operand_rows);
     // A few rows' scores are kept, unless they are more than a gigabyte (a batch of long tables without a
-    // max_kv); the keys are then read again.  Kept / read again, us, attention included: a token on 131071
-    // keys, 32 heads on 8, f32, 57 / 81; 64 sequences of 95 to 8192, bf16, 114 / 165.
+    // max_kv); the keys are then read again.  Kept / read again, us, attention included, 131071 keys of 8 kv
+    // heads by rows a kv head: f32 rows of 128 values, 4 rows 56 / 78, 8 59 / 78, 16 99 / 114, 32 187 / 190; of 64, 4
+    // 42 / 58, 8 47 / 59, 16 71 / 79, 24 103 / 104; f16 rows of 128, 4 52 / 73, 8 55 / 73, 16 67 / 77; of 64, 4 39 / 55, 8
+    // 43 / 56, 16 54 / 56, 32 114 / 102, 48 150 / 123: from there on reading again would be the faster way.
+    // 16 x 8191 keys give the same picture; 64 sequences of 95 to 8192, 4 bf16 rows of 128, 113 / 165.
     if (attend.kernel == 0) {
         const long long pages = (static_cast<long long>(max_kv < 1 ? 1 : max_kv) + mmq::KV_PAGE - 1) / mmq::KV_PAGE;
         p.score_pages = static_cast<int>(pages < c->max_pages ? pages : c->max_pages);

@@ -10,8 +10,8 @@
 //
 // kv_finish_weights_kernel (few rows: the step kernel ran).  The attention has left its scores, 4 bytes
 // a row and key, so that K is not read and widened again: for a token on 131071 keys, 32 heads on 8,
-// 57 us with the attention (47) for 81 with the next kernel; 64 sequences of up to 8192, 114 for 165.
-// Where scores would take more than a gigabyte the next kernel runs.
+// 56 us with the attention (47.5 alone) for 78 with the next kernel; 64 sequences of up to 8192, 113 for 165.
+// Where scores would take more than a gigabyte the next kernel runs (more sizes at weigh_plan).
 //
 // kv_weigh_few_kernel (up to 128 rows per sequence and kv head) and kv_weigh_many_kernel (more):
 // S^T = K Q^T on the tensor cores.  Keys are the 128 lanes of tensor memory and rows its columns, so a
@@ -21,11 +21,11 @@
 // parts.  With few rows these stay in shared memory and the keys stream by; with many, 256 keys
 // stay and the rows stream by.
 //
-// What bounds them: few rows a step's chain (widening 700 cycles, products, sums 1100), shared by
-// three warpgroups in turn; 32 f16 tokens on 131072 keys, 32 heads on 8, 74 us (1.0 TB/s of K).  Many rows
-// the sums: an exponential and two fma an element, and three reads of a column's constants for every four
-// elements of two keys.  2 x 2048 tokens of 32 heads on 8 on 16384 keys 577 us beside 820 for the
-// attention: 890 TFLOP/s of the one product.  Without its exponentials an earlier form of the kernel took
+// What bounds them: the sums.  Few rows: a warpgroup's loop of load from tensor memory, wait, constants and
+// exponentials (cycles below); 32 f16 tokens on 131072 keys, 32 heads on 8, 67 us of 147 (1.1 TB/s of K).
+// Many rows: an exponential and two fma an element, and three reads of a column's constants for every four
+// elements of two keys.  2 x 2048 f16 tokens of 32 heads on 8 on 16384 keys 640 us, with the rows' laying
+// out, beside 816 for the attention.  Without its exponentials an earlier form of the kernel took
 // 13 % less, without the constants' reads 20 %; those could go into the product (three more values of every
 // row), but an argument that is far from 0 costs weights three bits, and rows of a tile need one factor.
 #include <cfloat>
@@ -297,8 +297,13 @@ __device__ __forceinline__ void add_columns(const AttendArgs& g, const float (&x
 // One CTA an SM; all tiles of 128 keys, sequence by sequence and head by head, are cut into even
 // shares, so that lengths may differ as they like and a CTA's pipeline runs on from one head to
 // the next.  What a tile costs its warps is a chain of dependent instructions, waits among them,
-// of 500 cycles (products) to 1200 (widening, sums), and its bytes arrive in 400: so each role is
-// several warpgroups' or warps', which take the tiles in turn.
+// longer than the 400 cycles that its bytes take: so each role is several warpgroups' or warps', which
+// take the tiles in turn.  Clock stamps of one CTA, 131072 keys, means of 40 tiles, 128 / 64 / 32 columns of
+// f16 rows: codes widened 810 / 850 / 860 cycles; product issued to S seen 1400 / 1500 / 1610; sums 4270 / 2430 /
+// 1550, of which S is free again after 3650 / 1830 / 970; a tile every 1890 / 1280 / 1000.  With 128
+// columns that is one group's S: awaited, read and given back in 5600 cycles, a third of which is a
+// tile's share; the widening groups and the issuing warp wait for it.  With fewer columns no role is
+// busy all the time: what is left are the handoffs between them.
 constexpr int GROUPS = 3, ROW_WARPS = 4, COPY_WARPS = 2;
 constexpr int SUM_WARP = 4 * GROUPS, ROW_WARP = SUM_WARP + 4 * GROUPS, COPY_WARP = ROW_WARP + ROW_WARPS,
               MMA_WARP = COPY_WARP + COPY_WARPS, FEW_WARPS = MMA_WARP + 1, FEW_THREADS = FEW_WARPS * 32;
